@@ -411,6 +411,177 @@ ssd_status_t ssd_prefill_block(const ssd_params_t* p, const void* xbc, const flo
                                const void* initial_state, void* out, void* final_state,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/* ====================================================================================
+ * The selective state space scan and its short causal convolution, for prompts, training
+ * and single tokens, and an 8-bit cache for the states of this library.
+ *
+ * The conventions at the top of this header hold (device pointers owned by the caller,
+ * asynchronous on `stream`, host-only argument checks before any HIP call, no allocation,
+ * no synchronisation, no abort), with one addition: inputs marked "rows" may be views whose
+ * rows (one per token, in [B][L] order) lie a constant number of elements apart, given by a
+ * *_stride field (0: contiguous); the elements of a row are always contiguous.
+ *
+ * Sequences and states.  Without seq_idx, each batch row is one sequence and its state is
+ * number b.  With seq_idx [B, L] int32 (packed input, as in ssd_prefill_varlen_states), a sequence
+ * starts at t = 0 of every row and wherever seq_idx changes, and seq_idx[b,t] is the number of
+ * the sequence holding token t; states are indexed by that number, in [0, nseq), and each number
+ * labels one run of tokens.  Tokens whose number lies outside [0, nseq) (padding) run from a
+ * zero state and write none.  Entries of state outputs that no sequence uses are left as they
+ * were.  Below, S is batch without seq_idx and nseq with it.
+ *
+ * The single-token forms work in place on a pool of nseq states: row b uses the state
+ * slots[b] (int32; NULL: slot b, with nseq = batch).  Each slot in use appears once.  A row
+ * whose slot lies outside [0, nseq) (a padded batch) touches no state and gets a zero output row.
+ * ==================================================================================== */
+
+/* ---- causal depthwise convolution -----------------------------------------------------
+ *     pre[b,t,c] = bias[c] + sum_k w[c,k] * x[b, t - (W-1) + k, c],   out = pre or silu(pre)
+ * where the W-1 inputs before a sequence's first token come from its initial state. */
+typedef struct {
+    size_t struct_size; /* sizeof(ssd_conv_params_t) */
+    int batch;          /* B >= 1 */
+    int seqlen;         /* L >= 1 (1 for ssd_causal_conv_step) */
+    int channels;       /* Ch >= 1 */
+    int width;          /* W in {2, 3, 4} */
+    int in_dtype;       /* ssd_dtype_t of x, out, the states and their gradients */
+    int silu;           /* 1: out = silu(pre); 0: out = pre */
+    int nseq;           /* with seq_idx (or for the step): the number of states; else ignored */
+    int split_a;        /* 0 <= split_a <= split_b <= Ch: channels [0, split_a) go to out0, */
+    int split_b;        /* [split_a, split_b) to out1, the rest to out2 (each [B, L, its channels]); */
+                        /* split_a = Ch: everything to out0 */
+    int64_t x_stride;   /* elements between rows of x; 0: Ch */
+} ssd_conv_params_t;
+
+/*   x             [B, L, Ch]   in_dtype  required, rows
+ *   w             [Ch, W]      fp32      required
+ *   bias          [Ch]         fp32      NULL means 0
+ *   seq_idx       [B, L]       int32     NULL: every batch row is one sequence
+ *   initial_state [S, Ch, W-1] in_dtype  NULL means 0; column j holds the input at place
+ *                                        j - (W-1) from the sequence's start
+ *   out0..2                    in_dtype  required where they have channels
+ *   final_state   [S, Ch, W-1] in_dtype  NULL: not wanted; the last W-1 inputs of each sequence
+ *                                        (of its initial state where it is shorter)
+ * Every pointer has its element's alignment.  initial_state and final_state must not overlap. */
+ssd_status_t ssd_causal_conv(const ssd_conv_params_t* p, const void* x, const float* w, const float* bias,
+                             const int32_t* seq_idx, const void* initial_state,
+                             void* out0, void* out1, void* out2, void* final_state, void* stream);
+
+/* The gradients of ssd_causal_conv from dout0..2 (contiguous, laid out like out0..2) and, if not
+ * NULL, dfinal_state [S, Ch, W-1]:
+ *   dx             [B, L, Ch]   in_dtype  required, contiguous
+ *   dw             [Ch, W]      fp32      required
+ *   dbias          [Ch]         fp32      NULL: not wanted
+ *   dinitial_state [S, Ch, W-1] in_dtype  NULL: not wanted
+ * The sums over tokens run in fp32 in a fixed order (two calls give the same bits). */
+size_t ssd_causal_conv_backward_workspace_size(const ssd_conv_params_t* p);
+ssd_status_t ssd_causal_conv_backward(const ssd_conv_params_t* p, const void* dout0, const void* dout1,
+                                      const void* dout2, const void* dfinal_state, const void* x, const float* w,
+                                      const float* bias, const int32_t* seq_idx, const void* initial_state,
+                                      void* dx, float* dw, float* dbias, void* dinitial_state,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token per batch row: x [B, Ch] (rows) -> out0..2 [B, their channels], and state
+ * [nseq, Ch, W-1] moves on by one input in place. */
+ssd_status_t ssd_causal_conv_step(const ssd_conv_params_t* p, const void* x, const float* w, const float* bias,
+                                  void* state, const int32_t* slots, void* out0, void* out1, void* out2,
+                                  void* stream);
+
+/* ---- selective state space scan -------------------------------------------------------
+ * One decay per (channel, state) pair.  For every batch row b and channel c (B/C group
+ * g = c / (D / G)), over t = 0 .. L-1:
+ *     d = softplus(dt_raw[b,t,c] + dt_bias[c])                    (dt_softplus = 1)
+ *     h[n] = exp(d * A[c,n]) * h[n] + d * x[b,t,c] * B[b,t,g,n]
+ *     y = sum_n h[n] * C[b,t,g,n] + D[c] * x[b,t,c],    out[b,t,c] = y * silu(z[b,t,c])  (or y) */
+typedef struct {
+    size_t struct_size; /* sizeof(ssd_scan_params_t) */
+    int batch;          /* B >= 1 */
+    int seqlen;         /* L >= 1 (1 for ssd_selective_scan_step) */
+    int channels;       /* D >= 1 */
+    int dstate;         /* N in {8, 16, 32, 64} */
+    int ngroups;        /* G >= 1, D % G == 0 */
+    int in_dtype;       /* ssd_dtype_t of x, dt, B, C, z, out and their gradients */
+    int state_dtype;    /* ssd_dtype_t of the states and their gradients (the scan itself runs in fp32) */
+    int dt_softplus;    /* 1: d = softplus(dt_raw + dt_bias); 0: d = dt_raw + dt_bias */
+    int nseq;           /* with seq_idx (or for the step): the number of states; else ignored */
+    int64_t x_stride, dt_stride, z_stride; /* elements between rows; 0: D */
+    int64_t B_stride, C_stride;            /* elements between rows; 0: G*N (even for 16-bit types) */
+} ssd_scan_params_t;
+
+/*   x, dt         [B, L, D]     in_dtype    required, rows
+ *   A             [D, N]        fp32        required, 16-byte aligned; A <= 0 is a precondition (not checked)
+ *   B, C          [B, L, G, N]  in_dtype    required, rows, 4-byte aligned
+ *   D, dt_bias    [D]           fp32        NULL means 0
+ *   z             [B, L, D]     in_dtype    rows; NULL: no gate
+ *   seq_idx       [B, L]        int32       NULL: every batch row is one sequence
+ *   initial_state [S, D, N]     state_dtype NULL means 0; 16-byte aligned
+ *   out           [B, L, D]     in_dtype    required, contiguous
+ *   final_state   [S, D, N]     state_dtype NULL: not wanted; 16-byte aligned
+ *   saved         bytes         -           NULL, or ssd_selective_scan_saved_size() bytes, 16-byte aligned:
+ *                                           states kept for the backward pass (fp32, one every 16 tokens;
+ *                                           8 for N = 64)
+ *   workspace     bytes         -           required, 256-byte aligned,
+ *                                           ssd_selective_scan_workspace_size() bytes
+ * initial_state and final_state must not overlap. */
+size_t ssd_selective_scan_workspace_size(const ssd_scan_params_t* p);
+size_t ssd_selective_scan_saved_size(const ssd_scan_params_t* p);
+ssd_status_t ssd_selective_scan(const ssd_scan_params_t* p, const void* x, const void* dt, const float* A,
+                                const void* B, const void* C, const float* D, const float* dt_bias, const void* z,
+                                const int32_t* seq_idx, const void* initial_state, void* out, void* final_state,
+                                void* saved, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradients of ssd_selective_scan from dout [B, L, D] (contiguous), dfinal_state [S, D, N]
+ * (NULL means 0), the same inputs and the `saved` states of the forward call:
+ *   dx, ddt, dz [B, L, D], dB, dC [B, L, G, N] in_dtype contiguous (16-byte aligned dB, dC; ddt is the
+ *   gradient of dt_raw; dz required exactly when z is given); dA [D, N] fp32 required; dD and ddt_bias
+ *   [D] fp32 and dinitial_state [S, D, N] state_dtype, NULL: not wanted.
+ * The sums over tokens and channels run in fp32 in a fixed order (two calls give the same bits). */
+size_t ssd_selective_scan_backward_workspace_size(const ssd_scan_params_t* p);
+ssd_status_t ssd_selective_scan_backward(const ssd_scan_params_t* p, const void* dout, const void* dfinal_state,
+                                         const void* x, const void* dt, const float* A, const void* B, const void* C,
+                                         const float* D, const float* dt_bias, const void* z,
+                                         const int32_t* seq_idx, const void* initial_state, const void* saved,
+                                         void* dx, void* ddt, float* dA, void* dB, void* dC, float* dD,
+                                         float* ddt_bias, void* dz, void* dinitial_state,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token per batch row: x, dt, z [B, D] and B, C [B, G, N] (rows) -> out [B, D]; state
+ * [nseq, D, N] state_dtype is updated in place (fp32 arithmetic, rounded to state_dtype once). */
+ssd_status_t ssd_selective_scan_step(const ssd_scan_params_t* p, const void* x, const void* dt, const float* A,
+                                     const void* B, const void* C, const float* D, const float* dt_bias,
+                                     const void* z, void* state, const int32_t* slots, void* out, void* stream);
+
+/* ---- 8-bit state cache -------------------------------------------------------------------
+ * A pool of states (of ssd_prefill, ssd_decode_step or the scan: any layout, `elems` values each)
+ * held as one byte a value and one fp32 scale for each run of `group` consecutive values:
+ *     scale = max|v| / 127 (int8) or max|v| / 448 (e4m3), rounded to fp32
+ *     code  = v / scale rounded to the nearest code, ties to even (the exact quotient is rounded once)
+ *     v'    = code * scale, rounded to state_dtype once
+ * A group that holds an infinity or a NaN gets a NaN scale (and reads back as NaN); one whose scale
+ * would be below 2^-80 gets scale 0 and reads back as 0.  e4m3: 4 exponent bits (bias 7), 3 mantissa
+ * bits, largest value 448, no infinities. */
+typedef enum { SSD_CACHE_INT8 = 0, SSD_CACHE_E4M3 = 1 } ssd_cache_format_t;
+
+typedef struct {
+    size_t struct_size; /* sizeof(ssd_cache_params_t) */
+    int batch;          /* states read or written, >= 1 */
+    int nslots;         /* states in the pool, >= 1 */
+    int64_t elems;      /* values of a state, a multiple of group */
+    int group;          /* 16, 32, 64 or 128 */
+    int format;         /* ssd_cache_format_t */
+    int state_dtype;    /* ssd_dtype_t of `state` */
+} ssd_cache_params_t;
+
+/*   state  [batch, elems]         state_dtype  16-byte aligned
+ *   codes  [nslots, elems]        bytes        16-byte aligned
+ *   scales [nslots, elems/group]  fp32
+ *   slots  [batch]                int32        NULL: slot b.  A row whose slot lies outside [0, nslots) is
+ *                                              padding: a write stores nothing, a read gives a zero state.
+ *                                              A write names each slot once. */
+ssd_status_t ssd_state_cache_write(const ssd_cache_params_t* p, const void* state, const int32_t* slots,
+                                   void* codes, float* scales, void* stream);
+ssd_status_t ssd_state_cache_read(const ssd_cache_params_t* p, const void* codes, const float* scales,
+                                  const int32_t* slots, void* state, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,6 +7,8 @@ built, every call raises: there is no fallback path.
 
     y, final_state = ssd_prefill(x, dt, A, B, C, D, dt_bias, initial_state,
                                  chunk_size=128, impl="fused")
+
+The selective scan, its causal convolution and the 8-bit state cache are in selective.py.
 """
 import ctypes
 import os
@@ -117,6 +119,8 @@ def load_library():
     for f in ("ssd_step_chunk_cumsum", "ssd_step_bmm", "ssd_step_chunk_state", "ssd_step_state_passing",
               "ssd_step_chunk_scan", "ssd_decode_step", "ssd_conv_silu", "ssd_gated_norm", "ssd_prefill_block"):
         getattr(lib, f).restype = ctypes.c_int
+    from . import selective
+    selective.declare(lib)
     _lib = lib
     return lib
 
@@ -472,3 +476,11 @@ def ssd_decode_step(x, dt, A, B, C, D=None, dt_bias=None, state=None, state_dtyp
                                           _ptr(dt_bias), _ptr(state), _ptr(out_state), _ptr(y), _stream(dev)),
            "ssd_decode_step")
     return y, out_state
+
+
+# ---- selective scan, causal convolution, 8-bit state cache (selective.py) ------------------------
+from . import selective  # noqa: E402
+from .selective import *  # noqa: E402,F401,F403
+
+__all__ += selective.__all__
+EXPORTED_SYMBOLS += selective.EXPORTED_SYMBOLS

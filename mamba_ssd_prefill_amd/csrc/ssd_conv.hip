@@ -1,0 +1,407 @@
+// ssd_conv.hip -- the causal depthwise convolution of width W in {2, 3, 4} with an optional SiLU: prompts,
+// their gradients, and one token on a pool of states (ssd_causal_conv* in include/mamba_ssd.h).
+//
+//     pre[t] = bias + sum_k w[k] in[t - (W-1) + k],     out = silu(pre) or pre
+//     dpre[t] = dout[t] silu'(pre[t]),   dx[s] = sum_i w[W-1-i] dpre[s+i],   dw[k] = sum_t dpre[t] in[t-(W-1)+k]
+//
+// All three are HBM-bound streams.  A lane owns CW neighbouring channels of a run of tokens and slides a
+// window of W-1 inputs down them, so each input is read once a run plus a halo of W-1 rows;
+// consecutive lanes take consecutive channels.
+#include "ssd_device.h"
+#include "ssd_select.h"
+
+namespace ssd {
+
+// CW elements at p (4: one 8- or 16-byte access).
+template <typename T, int CW> __device__ inline void load_cw(const T* p, float (&v)[CW]) {
+    if constexpr (CW == 4) {
+        const typename TT<T>::v4 r = *(const typename TT<T>::v4*)p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)r[e];
+    } else {
+        v[0] = (float)*p;
+    }
+}
+template <typename T, int CW> __device__ inline void store_cw(T* p, const float (&v)[CW]) {
+    if constexpr (CW == 4) {
+        typename TT<T>::v4 r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = (T)v[e];
+        *(typename TT<T>::v4*)p = r;
+    } else {
+        *p = (T)v[0];
+    }
+}
+
+// Row `row` of channel c0 in a tensor split by channel ranges.
+template <typename T> __device__ inline T* split_ptr(void* const* base, int sa, int sb, int ch, int c0, int64_t row) {
+    if (c0 < sa) return (T*)base[0] + row * sa + c0;
+    if (c0 < sb) return (T*)base[1] + row * (sb - sa) + (c0 - sa);
+    return (T*)base[2] + row * (ch - sb) + (c0 - sb);
+}
+
+// The lane's item: piece of CW channels (fastest), segment of a.rows tokens, batch row.
+struct ConvItem {
+    int b, c0, t0, t1;
+};
+template <int CW> __device__ inline bool conv_item(const CausalConvArgs& a, ConvItem* it) {
+    const int npc = a.channels / CW;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)a.batch * a.nseg * npc) return false;
+    it->c0 = (int)(i % npc) * CW;
+    const int64_t r = i / npc;
+    it->t0 = (int)(r % a.nseg) * a.rows;
+    it->b = (int)(r / a.nseg);
+    it->t1 = min(it->t0 + a.rows, a.seqlen);
+    return true;
+}
+
+template <int W, int CW> struct ConvW {
+    float w[W][CW], bias[CW];
+    __device__ inline void load(const CausalConvArgs& a, int c0) {
+#pragma unroll
+        for (int e = 0; e < CW; ++e) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][e] = a.w[(int64_t)(c0 + e) * W + k];
+            bias[e] = a.bias ? a.bias[c0 + e] : 0.f;
+        }
+    }
+};
+
+// Walks one sequence after another down a batch row: the number of the sequence holding the
+// current token, its place in it (counted up to W-1), and the W-1 inputs before it.
+template <typename T, int W, int CW> struct ConvWalk {
+    const CausalConvArgs& a;
+    const int b, c0;
+    const int32_t* seq;
+    int q, place;
+    float win[W - 1][CW];
+
+    __device__ inline ConvWalk(const CausalConvArgs& a_, int b_, int c0_) : a(a_), b(b_), c0(c0_) {
+        seq = a.seq ? a.seq + (int64_t)b * a.seqlen : nullptr;
+    }
+    __device__ inline const T* row(int t) const { return (const T*)a.x + ((int64_t)b * a.seqlen + t) * a.xs + c0; }
+    __device__ inline bool has_state(int n) const { return n >= 0 && n < (seq ? a.nseq : a.batch); }
+    // the window before a sequence's first token, shifted by `done` inputs already taken
+    __device__ inline void load_state(int done) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            if (j + done > W - 2) continue;
+#pragma unroll
+            for (int e = 0; e < CW; ++e)
+                win[j][e] = a.h0 && has_state(q)
+                                ? (float)((const T*)a.h0)[((int64_t)q * a.channels + c0 + e) * (W - 1) + j + done]
+                                : 0.f;
+        }
+    }
+    // stand before token t
+    __device__ inline void start(int t) {
+        q = seq ? seq[t] : b;
+        place = 0;
+        while (place < W - 1 && t - place > 0 && (!seq || seq[t - place - 1] == q)) ++place;
+        load_state(place);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)  // the inputs of this sequence before t
+            if (W - 1 - j <= place) load_cw<T, CW>(row(t - (W - 1) + j), win[j]);
+    }
+    // arrive at token t from t - 1
+    __device__ inline void step_to(int t) {
+        if (seq && seq[t] != q) {
+            q = seq[t];
+            place = 0;
+            load_state(0);
+        }
+    }
+    __device__ inline void taps(const ConvW<W, CW>& k, const float (&cur)[CW], float (&pre)[CW]) const {
+#pragma unroll
+        for (int e = 0; e < CW; ++e) {
+            float s = k.bias[e];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) s += k.w[j][e] * win[j][e];
+            pre[e] = s + k.w[W - 1][e] * cur[e];
+        }
+    }
+    __device__ inline void push(const float (&cur)[CW]) {
+#pragma unroll
+        for (int j = 0; j + 1 < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < CW; ++e) win[j][e] = win[j + 1][e];
+#pragma unroll
+        for (int e = 0; e < CW; ++e) win[W - 2][e] = cur[e];
+        if (place < W) ++place;
+    }
+    __device__ inline bool last(int t) const { return t == a.seqlen - 1 || (seq && seq[t + 1] != q); }
+};
+
+template <typename T, int W, int CW> __global__ __launch_bounds__(256) void k_causal_conv(CausalConvArgs a) {
+    ConvItem it;
+    if (!conv_item<CW>(a, &it)) return;
+    ConvW<W, CW> k;
+    k.load(a, it.c0);
+    ConvWalk<T, W, CW> s(a, it.b, it.c0);
+    s.start(it.t0);
+    T* out = split_ptr<T>(a.out, a.split_a, a.split_b, a.channels, it.c0, (int64_t)it.b * a.seqlen + it.t0);
+    const int os = it.c0 < a.split_a ? a.split_a : it.c0 < a.split_b ? a.split_b - a.split_a : a.channels - a.split_b;
+    for (int t = it.t0; t < it.t1; ++t, out += os) {
+        float cur[CW], pre[CW];
+        load_cw<T, CW>(s.row(t), cur);
+        s.step_to(t);
+        s.taps(k, cur, pre);
+        if (a.silu) {
+#pragma unroll
+            for (int e = 0; e < CW; ++e) pre[e] = silu_f(pre[e]);
+        }
+        store_cw<T, CW>(out, pre);
+        s.push(cur);
+        if (a.fin && s.last(t) && s.has_state(s.q)) {
+            // the window holds inputs (or the initial state) as they were, so this rounds nothing
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int e = 0; e < CW; ++e)
+                    ((T*)a.fin)[((int64_t)s.q * a.channels + it.c0 + e) * (W - 1) + j] = (T)s.win[j][e];
+        }
+    }
+}
+
+// silu'(v) = p (1 + v (1 - p)), p the sigmoid of v
+__device__ inline float dsilu_f(float v) {
+    const float p = __builtin_amdgcn_rcpf(1.f + __expf(-v));
+    return p * (1.f + v * (1.f - p));
+}
+
+// One pass over a run of tokens and the W-1 tokens behind it: dpre of a token completes dx of the token
+// W-1 before it.  A lane's sums of dw and dbias over its own tokens go to `part` (one row per
+// segment), summed by k_conv_sums in a fixed order.
+template <typename T, int W, int CW> __global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) {
+    ConvItem it;
+    if (!conv_item<CW>(a, &it)) return;
+    ConvW<W, CW> k;
+    k.load(a, it.c0);
+    ConvWalk<T, W, CW> s(a, it.b, it.c0);
+    s.start(it.t0);
+    const int64_t row0 = (int64_t)it.b * a.seqlen;
+    const T* dout = split_ptr<T>((void* const*)a.dout, a.split_a, a.split_b, a.channels, it.c0, row0 + it.t0);
+    const int os = it.c0 < a.split_a ? a.split_a : it.c0 < a.split_b ? a.split_b - a.split_a : a.channels - a.split_b;
+    float dw[W][CW] = {}, db[CW] = {};
+    // dx of the W-1 tokens before the current one, still short of later tokens' terms
+    float acc[W - 1][CW] = {};
+    // gradients of the initial state, at a sequence's first tokens
+    float dh[W - 1][CW] = {};
+    const int end = min(it.t1 + W - 1, a.seqlen);
+    for (int t = it.t0; t < it.t1 + W - 1; ++t, dout += os) {
+        float here[CW] = {};
+        if (t < end) {
+            float cur[CW], pre[CW], g[CW];
+            load_cw<T, CW>(s.row(t), cur);
+            load_cw<T, CW>(dout, g);
+            s.step_to(t);
+            s.taps(k, cur, pre);
+            if (a.silu) {
+#pragma unroll
+                for (int e = 0; e < CW; ++e) g[e] *= dsilu_f(pre[e]);
+            }
+            const int place = s.place;  // of t in its sequence, up to W
+            if (t < it.t1) {
+#pragma unroll
+                for (int e = 0; e < CW; ++e) {
+                    db[e] += g[e];
+                    dw[W - 1][e] += g[e] * cur[e];
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) dw[j][e] += g[e] * s.win[j][e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < CW; ++e) here[e] = k.w[W - 1][e] * g[e];
+            // acc[j] belongs to token t - (W-1) + j, which tap j of t reads if it is in t's sequence
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+                if (W - 1 - j <= place) {
+#pragma unroll
+                    for (int e = 0; e < CW; ++e) acc[j][e] += k.w[j][e] * g[e];
+                }
+            s.push(cur);
+            const bool last = s.last(t);
+            // the initial state: tap j of the token at place p reads its column p + j while that is below W-1;
+            // the lane that holds the sequence's first token sums and stores it
+            const bool head = a.dh0 && place <= W - 2 && t - place >= it.t0 && t - place < it.t1 && s.has_state(s.q);
+            if (head) {
+#pragma unroll
+                for (int c = 0; c < W - 1; ++c) {
+#pragma unroll
+                    for (int j = 0; j <= c; ++j) {
+                        if (place + j != c) continue;
+                        // the sequence's first token (place 0) begins every column
+#pragma unroll
+                        for (int e = 0; e < CW; ++e) dh[c][e] = (place ? dh[c][e] : 0.f) + k.w[j][e] * g[e];
+                    }
+                }
+            }
+            if (a.dfin && last && s.has_state(s.q)) {
+                // column j of the final state is the input of token t - (W-2) + j, if it is in the sequence
+                const T* df = (const T*)a.dfin + ((int64_t)s.q * a.channels + it.c0) * (W - 1);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {
+                    if (W - 2 - j > place) continue;
+#pragma unroll
+                    for (int e = 0; e < CW; ++e) {
+                        const float v = (float)df[e * (W - 1) + j];
+                        if (j == W - 2)
+                            here[e] += v;
+                        else
+                            acc[j + 1][e] += v;
+                    }
+                }
+                // a sequence shorter than the state keeps part of its initial state: column place + 1 + j
+                if (head) {
+#pragma unroll
+                    for (int c = 1; c < W - 1; ++c)
+#pragma unroll
+                        for (int j = 0; j < c; ++j) {
+                            if (place + 1 + j != c) continue;
+#pragma unroll
+                            for (int e = 0; e < CW; ++e) dh[c][e] += (float)df[e * (W - 1) + j];
+                        }
+                }
+            }
+            if (head && (last || place == W - 2)) {
+#pragma unroll
+                for (int c = 0; c < W - 1; ++c)
+#pragma unroll
+                    for (int e = 0; e < CW; ++e)
+                        ((T*)a.dh0)[((int64_t)s.q * a.channels + it.c0 + e) * (W - 1) + c] = (T)dh[c][e];
+            }
+        }
+        const int sdone = t - (W - 1);
+        if (sdone >= it.t0) store_cw<T, CW>((T*)a.dx + (row0 + sdone) * a.channels + it.c0, acc[0]);
+#pragma unroll
+        for (int j = 0; j + 1 < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < CW; ++e) acc[j][e] = acc[j + 1][e];
+#pragma unroll
+        for (int e = 0; e < CW; ++e) acc[W - 2][e] = here[e];
+    }
+    float* part = a.part + (((int64_t)it.b * a.nseg + it.t0 / a.rows) * a.channels + it.c0) * (W + 1);
+#pragma unroll
+    for (int e = 0; e < CW; ++e) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) part[e * (W + 1) + j] = dw[j][e];
+        part[e * (W + 1) + W] = db[e];
+    }
+}
+
+// dw [channels][W] and dbias [channels] from the rows of `part`.
+template <int W> __global__ __launch_bounds__(256) void k_conv_sums(const float* part, int nrows, int channels,
+                                                                     float* dw, float* db) {
+    const int64_t n = (int64_t)channels * (W + 1), i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    float s = 0.f;
+    for (int r = 0; r < nrows; ++r) s += part[r * n + i];
+    const int c = (int)(i / (W + 1)), j = (int)(i % (W + 1));
+    if (j < W)
+        dw[(int64_t)c * W + j] = s;
+    else if (db)
+        db[c] = s;
+}
+
+// One token: a lane owns a channel, reads the W-1 inputs of its slot, writes the output and moves the
+// state on by one input.
+template <typename T, int W> __global__ __launch_bounds__(256) void k_causal_conv_step(CausalConvArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)a.batch * a.channels) return;
+    const int c = (int)(i % a.channels), b = (int)(i / a.channels);
+    const int slot = a.slots ? a.slots[b] : b;
+    T* out = split_ptr<T>(a.out, a.split_a, a.split_b, a.channels, c, b);
+    if (slot < 0 || slot >= a.nseq) {
+        *out = (T)0.f;
+        return;
+    }
+    T* st = (T*)a.pool + ((int64_t)slot * a.channels + c) * (W - 1);
+    const T cur = ((const T*)a.x)[b * a.xs + c];
+    float s = a.bias ? a.bias[c] : 0.f;
+    T win[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        win[j] = st[j];
+        s += a.w[(int64_t)c * W + j] * (float)win[j];
+    }
+    s += a.w[(int64_t)c * W + W - 1] * (float)cur;
+    *out = (T)(a.silu ? silu_f(s) : s);
+#pragma unroll
+    for (int j = 0; j + 1 < W - 1; ++j) st[j] = win[j + 1];
+    st[W - 2] = cur;
+}
+
+constexpr int kConvForwardRows = 16;  // tokens per lane of the forward
+
+int conv_backward_rows(int64_t batch, int64_t seqlen, int64_t channels) { return 16; }
+
+// Whether lanes can take four channels with one access: every row they touch starts on a
+// multiple of four elements.
+static bool conv_vec4(const CausalConvArgs& a, size_t es, const void* const* tens, int ntens) {
+    if (a.channels % 4 || a.split_a % 4 || a.split_b % 4 || a.xs % 4) return false;
+    if ((uintptr_t)a.x % (4 * es)) return false;
+    for (int i = 0; i < ntens; ++i)
+        if ((uintptr_t)tens[i] % (4 * es)) return false;
+    return true;
+}
+
+template <typename T, int W> hipError_t launch_conv_tw(CausalConvArgs& a, hipStream_t st) {
+    a.rows = kConvForwardRows;
+    a.nseg = (a.seqlen + a.rows - 1) / a.rows;
+    const bool v4 = conv_vec4(a, sizeof(T), a.out, 3);
+    const int64_t items = (int64_t)a.batch * a.nseg * (a.channels / (v4 ? 4 : 1));
+    void* args[] = {&a};
+    return hipLaunchKernel(v4 ? (const void*)&k_causal_conv<T, W, 4> : (const void*)&k_causal_conv<T, W, 1>,
+                           dim3((unsigned)((items + 255) / 256)), dim3(256), args, 0, st);
+}
+
+template <typename T, int W> hipError_t launch_conv_back_tw(CausalConvArgs& a, float* dw, float* db, hipStream_t st) {
+    a.rows = conv_backward_rows(a.batch, a.seqlen, a.channels);
+    a.nseg = (a.seqlen + a.rows - 1) / a.rows;
+    const void* tens[4] = {a.dout[0], a.dout[1], a.dout[2], a.dx};
+    const bool v4 = conv_vec4(a, sizeof(T), tens, 4);
+    const int64_t items = (int64_t)a.batch * a.nseg * (a.channels / (v4 ? 4 : 1));
+    void* args[] = {&a};
+    hipError_t e = hipLaunchKernel(
+        v4 ? (const void*)&k_causal_conv_backward<T, W, 4> : (const void*)&k_causal_conv_backward<T, W, 1>,
+        dim3((unsigned)((items + 255) / 256)), dim3(256), args, 0, st);
+    if (e != hipSuccess) return e;
+    int nrows = a.batch * a.nseg;
+    const int64_t n = (int64_t)a.channels * (W + 1);
+    void* sargs[] = {&a.part, &nrows, &a.channels, &dw, &db};
+    return hipLaunchKernel((const void*)&k_conv_sums<W>, dim3((unsigned)((n + 255) / 256)), dim3(256), sargs, 0, st);
+}
+
+template <typename T, int W> hipError_t launch_conv_step_tw(CausalConvArgs& a, hipStream_t st) {
+    const int64_t items = (int64_t)a.batch * a.channels;
+    void* args[] = {&a};
+    return hipLaunchKernel((const void*)&k_causal_conv_step<T, W>, dim3((unsigned)((items + 255) / 256)), dim3(256),
+                           args, 0, st);
+}
+
+#define SSD_CONV_BY_TYPE(fn, ...)                                              \
+    switch (in_dtype * 8 + a.width) {                                          \
+    case DT_F32 * 8 + 2: return fn<float, 2>(__VA_ARGS__);                     \
+    case DT_F32 * 8 + 3: return fn<float, 3>(__VA_ARGS__);                     \
+    case DT_F32 * 8 + 4: return fn<float, 4>(__VA_ARGS__);                     \
+    case DT_F16 * 8 + 2: return fn<_Float16, 2>(__VA_ARGS__);                  \
+    case DT_F16 * 8 + 3: return fn<_Float16, 3>(__VA_ARGS__);                  \
+    case DT_F16 * 8 + 4: return fn<_Float16, 4>(__VA_ARGS__);                  \
+    case DT_BF16 * 8 + 2: return fn<__bf16, 2>(__VA_ARGS__);                   \
+    case DT_BF16 * 8 + 3: return fn<__bf16, 3>(__VA_ARGS__);                   \
+    case DT_BF16 * 8 + 4: return fn<__bf16, 4>(__VA_ARGS__);                   \
+    default: return hipErrorNotSupported;                                      \
+    }
+
+hipError_t launch_causal_conv(CausalConvArgs& a, int in_dtype, hipStream_t st) {
+    SSD_CONV_BY_TYPE(launch_conv_tw, a, st)
+}
+hipError_t launch_causal_conv_backward(CausalConvArgs& a, int in_dtype, float* dw, float* db, hipStream_t st) {
+    SSD_CONV_BY_TYPE(launch_conv_back_tw, a, dw, db, st)
+}
+hipError_t launch_causal_conv_step(CausalConvArgs& a, int in_dtype, hipStream_t st) {
+    SSD_CONV_BY_TYPE(launch_conv_step_tw, a, st)
+}
+
+}  // namespace ssd

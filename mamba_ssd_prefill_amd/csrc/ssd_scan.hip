@@ -1,0 +1,200 @@
+// ssd_scan.hip -- the selective scan forward and its single-token step (ssd_selective_scan and
+// ssd_selective_scan_step in include/mamba_ssd.h).
+//
+//     d = softplus(dt + bias),  h[n] = exp(d A[n]) h[n] + d x B[n],  y = sum_n C[n] h[n] + D x,  out = y silu(z)
+//
+// Each (token, channel, n) costs one exponential (a quarter-rate instruction, 4 issue slots) and
+// four multiply-adds, against 8 bytes of 16-bit input and output a (token, channel): the prompt scan is
+// bound by the vector ALU, the step by the state's traffic.
+#include "ssd_scan_common.h"
+
+namespace ssd {
+
+template <typename T, int NW, int NS, bool VL>
+__global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
+    constexpr int TT_ = 16;            // tokens of a tile
+    constexpr int TPW = TT_ / NW;      // tokens a wave prepares and finishes
+    constexpr int PERIOD = 64 / NS;    // tokens between saved states
+    constexpr int N = NW * NS;
+    __shared__ f32x2 s_d[TT_][64];     // (d, d x)
+    __shared__ float s_y[NW][TT_][64];
+    const ScanPlace p = scan_place(a);
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = w * NS;
+
+    float A2[NS], h[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        A2[i] = a.A[(int64_t)p.c * N + n0 + i] * kLog2e;
+        h[i] = 0.f;
+    }
+    const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f, Dc = a.D ? a.D[p.c] : 0.f;
+    const int64_t soff = (int64_t)p.c * N + n0, sstride = (int64_t)a.channels * N;
+    const int tile0 = p.split * a.tiles_per_split, tile1 = min(tile0 + a.tiles_per_split, (a.seqlen + TT_ - 1) / TT_);
+    if (p.split) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) h[i] = a.split_state[((int64_t)p.b * a.nsplit + p.split) * sstride + soff + i];
+    } else if (!VL && a.h0) {
+        load_states<NS>(a.h0, a.state_dtype, p.b * sstride + soff, h);
+    }
+    for (int tile = tile0; tile < tile1; ++tile) {
+        const int t0 = tile * TT_;
+        float xv[TPW], zv[TPW];
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            const int k = w + j * NW, t = t0 + k;
+            const int64_t r = p.row0 + min(t, a.seqlen - 1);
+            xv[j] = f32of(((const T*)a.x)[r * a.xs + p.c]);
+            const float v = f32of(((const T*)a.dt)[r * a.dts + p.c]) + bias;
+            zv[j] = a.z ? f32of(((const T*)a.z)[r * a.zs + p.c]) : 0.f;
+            // tokens past the end take no step: d = 0 leaves the state as it is
+            const float d = t < a.seqlen ? (a.softplus ? softplus_f(v) : v) : 0.f;
+            s_d[k][lane] = f32x2{d, d * xv[j]};
+        }
+        SeqMasks m{0, 0};
+        if (VL) m = seq_masks<TT_>(a, p.row0, t0);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < TT_; ++k) {
+            const int64_t r = p.row0 + min(t0 + k, a.seqlen - 1);
+            float Bv[NS], Cv[NS];
+            scalar_row<T, NS>((const T*)a.B + r * a.Bs + p.g * N + n0, Bv);
+            scalar_row<T, NS>((const T*)a.C + r * a.Cs + p.g * N + n0, Cv);
+            if (k % PERIOD == 0 && a.saved && t0 + k < a.seqlen && p.live) {
+                float* sv = a.saved + ((int64_t)p.b * a.ntiles + (t0 + k) / PERIOD) * sstride + soff;
+                store_states<NS>(sv, DT_F32, 0, h);
+            }
+            if (VL && (m.start >> k & 1)) {
+                const int q = a.seq[r];
+#pragma unroll
+                for (int i = 0; i < NS; ++i) h[i] = 0.f;
+                if (a.h0 && state_number(a, q)) load_states<NS>(a.h0, a.state_dtype, q * sstride + soff, h);
+            }
+            const f32x2 dv = s_d[k][lane];
+            float y = 0.f;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                h[i] = __builtin_amdgcn_exp2f(dv[0] * A2[i]) * h[i] + dv[1] * Bv[i];
+                y += h[i] * Cv[i];
+            }
+            s_y[w][k][lane] = y;
+            if (VL && (m.end >> k & 1) && a.fin && p.live) {
+                const int q = a.seq[r];
+                if (state_number(a, q)) store_states<NS>(a.fin, a.state_dtype, q * sstride + soff, h);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            const int k = w + j * NW, t = t0 + k;
+            float y = Dc * xv[j];
+#pragma unroll
+            for (int i = 0; i < NW; ++i) y += s_y[i][k][lane];
+            if (a.z) y *= silu_f(zv[j]);
+            if (t < a.seqlen && p.live) ((T*)a.out)[(p.row0 + t) * a.channels + p.c] = (T)y;
+        }
+    }
+    if (!VL && a.fin && tile1 * TT_ >= a.seqlen && p.live)
+        store_states<NS>(a.fin, a.state_dtype, p.b * sstride + soff, h);
+}
+
+// One token: N / 4 lanes hold a channel's states, four each, and share the sum over n.
+template <typename T, typename S, int N> __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a) {
+    constexpr int LPC = N / 4;  // lanes per channel
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i / LPC;
+    const int n0 = (int)(i % LPC) * 4;
+    if (row >= (int64_t)a.batch * a.channels) return;  // whole channels: a channel's lanes stay together
+    const int b = (int)(row / a.channels), c = (int)(row % a.channels), g = c / a.dg;
+    const int slot = a.slots ? a.slots[b] : b;
+    T* out = (T*)a.out + (int64_t)b * a.channels + c;
+    if (slot < 0 || slot >= a.nseq) {
+        if (n0 == 0) *out = (T)0.f;
+        return;
+    }
+    S* st = (S*)a.pool + ((int64_t)slot * a.channels + c) * N + n0;
+    float h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = (float)st[j];
+    const float x = f32of(((const T*)a.x)[b * a.xs + c]);
+    const float v = f32of(((const T*)a.dt)[b * a.dts + c]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
+    const float d = a.softplus ? softplus_f(v) : v;
+    const f32x4 A = *(const f32x4*)(a.A + (int64_t)c * N + n0);
+    const T* Bp = (const T*)a.B + b * a.Bs + g * N + n0;
+    const T* Cp = (const T*)a.C + b * a.Cs + g * N + n0;
+    float y = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        h[j] = __builtin_amdgcn_exp2f(d * (A[j] * kLog2e)) * h[j] + d * x * f32of(Bp[j]);
+        y += h[j] * f32of(Cp[j]);
+        st[j] = (S)h[j];
+    }
+#pragma unroll
+    for (int m = LPC / 2; m >= 1; m >>= 1) y += __shfl_xor(y, m, 64);
+    if (n0 == 0) {
+        if (a.D) y += a.D[c] * x;
+        if (a.z) y *= silu_f(f32of(((const T*)a.z)[b * a.zs + c]));
+        *out = (T)y;
+    }
+}
+
+int scan_splits(int64_t batch, int64_t seqlen, int64_t channels, int groups, int dstate, bool backward) { return 1; }
+
+template <typename T, int NW, int NS> hipError_t launch_scan_n(ScanArgs& a, hipStream_t st) {
+    void* args[] = {&a};
+    const void* fn = a.seq ? (const void*)&k_scan<T, NW, NS, true> : (const void*)&k_scan<T, NW, NS, false>;
+    return hipLaunchKernel(fn, dim3((unsigned)(a.batch * a.nsplit * a.groups * a.cblk)), dim3(NW * 64), args, 0, st);
+}
+
+template <typename T> hipError_t launch_scan_t(ScanArgs& a, hipStream_t st) {
+    switch (a.dstate) {
+    case 8: return launch_scan_n<T, 2, 4>(a, st);
+    case 16: return launch_scan_n<T, 4, 4>(a, st);
+    case 32: return launch_scan_n<T, 8, 4>(a, st);
+    case 64: return launch_scan_n<T, 8, 8>(a, st);
+    default: return hipErrorNotSupported;
+    }
+}
+
+hipError_t launch_scan(ScanArgs& a, int in_dtype, hipStream_t st) {
+    switch (in_dtype) {
+    case DT_F32: return launch_scan_t<float>(a, st);
+    case DT_F16: return launch_scan_t<_Float16>(a, st);
+    case DT_BF16: return launch_scan_t<__bf16>(a, st);
+    default: return hipErrorNotSupported;
+    }
+}
+
+template <typename T, typename S> hipError_t launch_scan_step_ts(ScanArgs& a, hipStream_t st) {
+    const void* fn = nullptr;
+    switch (a.dstate) {
+    case 8: fn = (const void*)&k_scan_step<T, S, 8>; break;
+    case 16: fn = (const void*)&k_scan_step<T, S, 16>; break;
+    case 32: fn = (const void*)&k_scan_step<T, S, 32>; break;
+    case 64: fn = (const void*)&k_scan_step<T, S, 64>; break;
+    default: return hipErrorNotSupported;
+    }
+    const int64_t lanes = (int64_t)a.batch * a.channels * (a.dstate / 4);
+    void* args[] = {&a};
+    return hipLaunchKernel(fn, dim3((unsigned)((lanes + 255) / 256)), dim3(256), args, 0, st);
+}
+
+template <typename T> hipError_t launch_scan_step_t(ScanArgs& a, hipStream_t st) {
+    switch (a.state_dtype) {
+    case DT_F32: return launch_scan_step_ts<T, float>(a, st);
+    case DT_F16: return launch_scan_step_ts<T, _Float16>(a, st);
+    case DT_BF16: return launch_scan_step_ts<T, __bf16>(a, st);
+    default: return hipErrorNotSupported;
+    }
+}
+
+hipError_t launch_scan_step(ScanArgs& a, int in_dtype, hipStream_t st) {
+    switch (in_dtype) {
+    case DT_F32: return launch_scan_step_t<float>(a, st);
+    case DT_F16: return launch_scan_step_t<_Float16>(a, st);
+    case DT_BF16: return launch_scan_step_t<__bf16>(a, st);
+    default: return hipErrorNotSupported;
+    }
+}
+
+}  // namespace ssd

@@ -1,0 +1,117 @@
+// ssd_scan_common.h -- device code shared by the forward and the backward of the selective scan.
+//
+// A workgroup holds 64 channels of one batch row, one a lane; its NW waves hold NS states each
+// of the N = NW * NS.  So B and C of a token are the same for a whole wave and are read as scalars, each
+// wave's part of the recurrence needs no other, and only the sums over n (y, and two sums of the
+// backward) cross waves, through LDS.  What a (token, channel) needs once -- the step d, d * x, the gate
+// -- is computed by one of the waves, tokens dealt round robin.
+#pragma once
+
+#include "ssd_device.h"
+#include "ssd_select.h"
+
+namespace ssd {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Wave-uniform reads through the scalar cache (the data is written before the launch).
+typedef const __attribute__((address_space(4))) uint32_t* ScalarPtr;
+__device__ inline ScalarPtr scalar_ptr(const void* p) { return (ScalarPtr)(uintptr_t)p; }
+
+// NS values of type T at a 4-byte aligned address, as fp32.
+template <typename T, int NS> __device__ inline void scalar_row(const T* p, float (&v)[NS]) {
+    ScalarPtr s = scalar_ptr(p);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) v[i] = __builtin_bit_cast(float, s[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS / 2; ++i) {
+            const uint32_t u = s[i];
+            if constexpr (__is_same(T, __bf16)) {
+                v[2 * i] = __builtin_bit_cast(float, u << 16);
+                v[2 * i + 1] = __builtin_bit_cast(float, u & 0xffff0000u);
+            } else {
+                const f16x2 h = __builtin_bit_cast(f16x2, u);
+                v[2 * i] = (float)h[0];
+                v[2 * i + 1] = (float)h[1];
+            }
+        }
+    }
+}
+
+// NS states at element offset `off`.
+template <int NS> __device__ inline void load_states(const void* base, int dtype, int64_t off, float (&h)[NS]) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) {
+        f32x4 v;
+        if (dtype == DT_F32) {
+            v = *(const f32x4*)((const float*)base + off + i);
+        } else if (dtype == DT_F16) {
+            const f16x4 r = *(const f16x4*)((const _Float16*)base + off + i);
+            v = f32x4{(float)r[0], (float)r[1], (float)r[2], (float)r[3]};
+        } else {
+            const bf16x4 r = *(const bf16x4*)((const __bf16*)base + off + i);
+            v = f32x4{(float)r[0], (float)r[1], (float)r[2], (float)r[3]};
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[i + j] = v[j];
+    }
+}
+template <int NS> __device__ inline void store_states(void* base, int dtype, int64_t off, const float (&h)[NS]) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) {
+        const f32x4 v = {h[i], h[i + 1], h[i + 2], h[i + 3]};
+        if (dtype == DT_F32)
+            *(f32x4*)((float*)base + off + i) = v;
+        else if (dtype == DT_F16)
+            *(f16x4*)((_Float16*)base + off + i) = cvt4<_Float16>(v);
+        else
+            *(bf16x4*)((__bf16*)base + off + i) = cvt4<__bf16>(v);
+    }
+}
+
+// softplus'(v)
+__device__ inline float sigmoid_f(float v) { return __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
+
+// Where a workgroup stands.
+struct ScanPlace {
+    int b, split, g, cblk;
+    int c;        // this lane's channel
+    bool live;    // false for lanes behind the group's last channel (they repeat it and store nothing)
+    int64_t row0; // b * seqlen
+};
+__device__ inline ScanPlace scan_place(const ScanArgs& a) {
+    ScanPlace p;
+    int i = blockIdx.x;
+    p.cblk = i % a.cblk;
+    i /= a.cblk;
+    p.g = i % a.groups;
+    i /= a.groups;
+    p.split = i % a.nsplit;
+    p.b = i / a.nsplit;
+    const int k = p.cblk * 64 + (int)(threadIdx.x & 63);
+    p.live = k < a.dg;
+    p.c = p.g * a.dg + (p.live ? k : a.dg - 1);
+    p.row0 = (int64_t)p.b * a.seqlen;
+    return p;
+}
+
+// Sequence starts and ends among the T tokens from t0: bit k for token t0 + k.
+struct SeqMasks {
+    uint32_t start, end;
+};
+template <int T> __device__ inline SeqMasks seq_masks(const ScanArgs& a, int64_t row0, int t0) {
+    const int k = threadIdx.x & 63, t = t0 + k;
+    bool s = false, e = false;
+    if (k < T && t < a.seqlen) {
+        const int32_t q = a.seq[row0 + t];
+        s = t == 0 || a.seq[row0 + t - 1] != q;
+        e = t == a.seqlen - 1 || a.seq[row0 + t + 1] != q;
+    }
+    return SeqMasks{(uint32_t)__ballot(s), (uint32_t)__ballot(e)};
+}
+
+__device__ inline bool state_number(const ScanArgs& a, int q) { return q >= 0 && q < a.nseq; }
+
+}  // namespace ssd

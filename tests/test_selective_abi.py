@@ -1,0 +1,229 @@
+"""Refusals of the causal convolution, the selective scan and the 8-bit state cache, without a GPU: every C call
+here fails exactly one host check (fake aligned addresses), so nothing is launched; and the binding's
+structs have the header's layout."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+import mamba_ssd_prefill_amd as ssd
+from mamba_ssd_prefill_amd import selective
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, NULLP, SHAPE, UNSUP, MISAL, WS_SMALL, HIP, TIMEOUT, BADARG = range(9)
+FAKE = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return ssd.load_library()
+
+
+def conv_prm(**kw):
+    p = dict(batch=2, seqlen=30, channels=64, width=4, in_dtype=2, silu=1, nseq=0, split_a=64, split_b=64, x_stride=0)
+    p.update(kw)
+    return ssd.ConvParams(ctypes.sizeof(ssd.ConvParams), *p.values())
+
+
+def scan_prm(**kw):
+    p = dict(batch=2, seqlen=30, channels=64, dstate=16, ngroups=1, in_dtype=2, state_dtype=0, dt_softplus=1, nseq=0,
+             x_stride=0, dt_stride=0, z_stride=0, B_stride=0, C_stride=0)
+    p.update(kw)
+    return ssd.ScanParams(ctypes.sizeof(ssd.ScanParams), *p.values())
+
+
+def cache_prm(**kw):
+    p = dict(batch=2, nslots=4, elems=1024, group=64, format=0, state_dtype=0)
+    p.update(kw)
+    return ssd.CacheParams(ctypes.sizeof(ssd.CacheParams), *p.values())
+
+
+# the pointer arguments of each entry point, and those that may be NULL in the calls below
+ARGS = {
+    "ssd_causal_conv": ("x w bias seq h0 out0 out1 out2 fin", "bias seq h0 out1 out2 fin"),
+    "ssd_causal_conv_backward": ("dout0 dout1 dout2 dfin x w bias seq h0 dx dw db dh0 ws", "dout1 dout2 dfin bias seq h0 db dh0"),
+    "ssd_causal_conv_step": ("x w bias state slots out0 out1 out2", "bias slots out1 out2"),
+    "ssd_selective_scan": ("x dt A B C D bias z seq h0 out fin saved ws", "D bias z seq h0 fin saved"),
+    "ssd_selective_scan_backward": ("dout dfin x dt A B C D bias z seq h0 saved dx ddt dA dB dC dD db dz dh0 ws",
+                                    "dfin D bias z seq h0 dD db dz dh0"),
+    "ssd_selective_scan_step": ("x dt A B C D bias z state slots out", "D bias z slots"),
+    "ssd_state_cache_write": ("state slots codes scales", "slots"),
+    "ssd_state_cache_read": ("codes scales slots state", "slots"),
+}
+PRM = {"ssd_causal": conv_prm, "ssd_select": scan_prm, "ssd_state_": cache_prm}
+
+
+def params_for(name, **kw):
+    if name.endswith("_step"):
+        kw = dict(dict(seqlen=1, nseq=2), **kw)
+    return PRM[name[:10]](**kw)
+
+
+def call(lib, name, prm, ws_bytes=1 << 40, **over):
+    fields = ARGS[name][0].split()
+    vals = {f: FAKE * (i + 1) for i, f in enumerate(fields)}
+    vals["seq"] = None
+    vals["slots"] = None
+    vals.update(over)
+    a = [vals[f] for f in fields]
+    if "ws" in fields:
+        a.append(ws_bytes)
+    return getattr(lib, name)(ctypes.byref(prm) if prm is not None else None, *a, None)
+
+
+@pytest.mark.parametrize("name", sorted(ARGS))
+def test_null_pointers(lib, name):
+    assert call(lib, name, None) == NULLP
+    fields, free = (s.split() for s in ARGS[name])
+    for f in fields:
+        if f not in free:
+            assert call(lib, name, params_for(name), **{f: None}) == NULLP, f
+    if name == "ssd_selective_scan_backward":
+        assert call(lib, name, params_for(name), dz=None) == NULLP
+        assert call(lib, name, params_for(name), z=None) == BADARG
+
+
+ALIGN = {"h0": 16, "fin": 16, "dfin": 16, "dh0": 16, "saved": 16, "state": 16, "codes": 16, "A": 16, "ws": 256, "B": 4, "C": 4,
+         "dB": 16, "dC": 16}
+
+
+@pytest.mark.parametrize("name", sorted(ARGS))
+def test_misaligned(lib, name):
+    for i, f in enumerate(ARGS[name][0].split()):
+        conv = "conv" in name
+        a = 2 if conv and f in ("h0", "fin", "dfin", "dh0", "state") else ALIGN.get(f, 4 if f in (
+            "w", "bias", "seq", "D", "dw", "db", "dD", "dA", "slots", "scales") else 2)
+        if f in ("out1", "out2", "dout1", "dout2"):
+            continue
+        kw = dict(nseq=2) if f in ("seq", "slots") and "cache" not in name else {}
+        assert call(lib, name, params_for(name, **kw), **{f: FAKE * (i + 1) + a // 2}) == MISAL, (f, a)
+    if "conv" in name:  # a range with channels needs its tensor, aligned
+        prm = params_for(name, split_a=10, split_b=20)
+        pre = "dout" if "backward" in name else "out"
+        for k in (1, 2):
+            assert call(lib, name, prm, **{pre + str(k): None}) == NULLP
+            assert call(lib, name, prm, **{pre + str(k): FAKE + 1}) == MISAL
+
+
+@pytest.mark.parametrize("name", ["ssd_causal_conv", "ssd_causal_conv_backward", "ssd_causal_conv_step"])
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), SHAPE), (dict(channels=0), SHAPE), (dict(seqlen=0), SHAPE), (dict(width=1), UNSUP),
+    (dict(width=5), UNSUP), (dict(in_dtype=3), BADARG), (dict(silu=2), BADARG), (dict(split_a=65), SHAPE),
+    (dict(split_a=-1), SHAPE), (dict(split_a=20, split_b=10), SHAPE), (dict(split_b=65), SHAPE), (dict(x_stride=63), SHAPE),
+    (dict(x_stride=-64), SHAPE), (dict(batch=1 << 20, seqlen=1 << 12), SHAPE)])
+def test_conv_parameters(lib, name, kw, code):
+    if name.endswith("_step") and "seqlen" in kw and kw["seqlen"] != 0:
+        kw = dict(seqlen=2)
+    assert call(lib, name, params_for(name, **kw)) == code
+
+
+@pytest.mark.parametrize("name", ["ssd_selective_scan", "ssd_selective_scan_backward", "ssd_selective_scan_step"])
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), SHAPE), (dict(channels=0), SHAPE), (dict(seqlen=0), SHAPE), (dict(ngroups=0), SHAPE),
+    (dict(ngroups=3), SHAPE), (dict(dstate=0), SHAPE), (dict(dstate=4), UNSUP), (dict(dstate=24), UNSUP),
+    (dict(dstate=128), UNSUP), (dict(in_dtype=-1), BADARG), (dict(state_dtype=3), BADARG), (dict(dt_softplus=2), BADARG),
+    (dict(x_stride=10), SHAPE), (dict(dt_stride=-1), SHAPE), (dict(z_stride=63), SHAPE), (dict(B_stride=15), SHAPE),
+    (dict(C_stride=17), MISAL), (dict(B_stride=19), MISAL), (dict(batch=1 << 20, seqlen=1 << 12), SHAPE),
+    (dict(channels=1 << 28), SHAPE)])
+def test_scan_parameters(lib, name, kw, code):
+    if name.endswith("_step") and "seqlen" in kw and kw["seqlen"] != 0:
+        kw = dict(seqlen=2)
+    assert call(lib, name, params_for(name, **kw)) == code
+
+
+@pytest.mark.parametrize("name", ["ssd_state_cache_write", "ssd_state_cache_read"])
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), SHAPE), (dict(nslots=0), SHAPE), (dict(elems=0), SHAPE), (dict(elems=1000), SHAPE), (dict(group=0), SHAPE),
+    (dict(group=48), UNSUP), (dict(group=256), UNSUP), (dict(format=2), BADARG), (dict(state_dtype=9), BADARG),
+    (dict(batch=5), SHAPE), (dict(elems=1 << 40), SHAPE)])
+def test_cache_parameters(lib, name, kw, code):
+    assert call(lib, name, cache_prm(**kw)) == code
+
+
+@pytest.mark.parametrize("name", sorted(ARGS))
+def test_short_struct(lib, name):
+    p = params_for(name)
+    p.struct_size -= 1
+    assert call(lib, name, p) == BADARG
+
+
+def test_packed_input_and_pools_need_their_number_of_states(lib):
+    for name in ("ssd_causal_conv", "ssd_causal_conv_backward", "ssd_selective_scan", "ssd_selective_scan_backward"):
+        assert call(lib, name, params_for(name, nseq=0), seq=FAKE) == SHAPE
+    for name in ("ssd_causal_conv_step", "ssd_selective_scan_step"):
+        assert call(lib, name, params_for(name, nseq=0), slots=FAKE) == SHAPE
+        assert call(lib, name, params_for(name, nseq=3)) == SHAPE  # without slots: one state per row
+
+
+def test_states_in_place_are_refused_for_prompts(lib):
+    for name in ("ssd_causal_conv", "ssd_selective_scan"):
+        assert call(lib, name, params_for(name), h0=FAKE, fin=FAKE) == BADARG
+
+
+def test_workspaces(lib):
+    for name, size in (("ssd_causal_conv_backward", lib.ssd_causal_conv_backward_workspace_size),
+                       ("ssd_selective_scan", lib.ssd_selective_scan_workspace_size),
+                       ("ssd_selective_scan_backward", lib.ssd_selective_scan_backward_workspace_size)):
+        p = params_for(name)
+        n = size(ctypes.byref(p))
+        assert n > 0 and n % 256 == 0
+        assert call(lib, name, p, ws_bytes=n - 1) == WS_SMALL
+        assert size(ctypes.byref(params_for(name, batch=0))) == 0 and size(None) == 0
+    assert lib.ssd_selective_scan_saved_size(ctypes.byref(scan_prm(seqlen=33))) == 2 * 3 * 64 * 16 * 4
+    assert lib.ssd_selective_scan_saved_size(ctypes.byref(scan_prm(seqlen=33, dstate=64))) == 2 * 5 * 64 * 64 * 4
+    assert lib.ssd_selective_scan_saved_size(ctypes.byref(scan_prm(dstate=24))) == 0
+
+
+def test_struct_layouts(tmp_path):
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("gcc not available")
+    pairs = [("ssd_conv_params_t", ssd.ConvParams), ("ssd_scan_params_t", ssd.ScanParams), ("ssd_cache_params_t", ssd.CacheParams)]
+    src = '#include <stdio.h>\n#include <stddef.h>\n#include "mamba_ssd.h"\nint main(void) {\n'
+    for c, cls in pairs:
+        src += '    printf("%%zu\\n", sizeof(%s));\n' % c
+        for f, _ in cls._fields_:
+            src += '    printf("%%zu\\n", offsetof(%s, %s));\n' % (c, f)
+    (tmp_path / "s.c").write_text(src + "    return 0;\n}\n")
+    subprocess.run([gcc, "-std=c11", "-I", os.path.join(ROOT, "include"), str(tmp_path / "s.c"), "-o", str(tmp_path / "s")], check=True)
+    got = [int(v) for v in subprocess.run([str(tmp_path / "s")], capture_output=True, text=True).stdout.split()]
+    want = []
+    for _, cls in pairs:
+        want += [ctypes.sizeof(cls)] + [getattr(cls, f).offset for f, _ in cls._fields_]
+    assert got == want
+
+
+def test_the_binding_refuses_what_it_cannot_pass():
+    z = torch.zeros
+    with pytest.raises(ValueError, match="device"):
+        ssd.causal_conv(z(1, 4, 8), z(8, 4))
+    with pytest.raises(ValueError, match="device"):
+        ssd.selective_scan(z(1, 4, 8), z(1, 4, 8), z(8, 8), z(1, 4, 1, 8), z(1, 4, 1, 8))
+    with pytest.raises(ValueError, match="device"):
+        ssd.state_cache_write(z(1, 64), *ssd.state_cache(1, (64,), device="cpu"))
+    with pytest.raises(ValueError, match="nseq"):
+        ssd.causal_conv(z(1, 4, 8), z(8, 4), seq_idx=z(1, 4, dtype=torch.int32))
+    with pytest.raises(ValueError, match="nseq"):
+        ssd.selective_scan(z(1, 4, 8), z(1, 4, 8), z(8, 8), z(1, 4, 1, 8), z(1, 4, 1, 8), nseq=3)
+    with pytest.raises(ValueError, match="group"):
+        ssd.state_cache(2, (40,), device="cpu")
+    with pytest.raises(ValueError, match="format"):
+        ssd.state_cache(2, (64,), format="int4", device="cpu")
+    with pytest.raises(ValueError, match="float"):
+        ssd.selective_scan(z(1, 4, 8), z(1, 4, 8), z(8, 8), z(1, 4, 1, 8), z(1, 4, 1, 8), state_dtype=torch.float64)
+
+
+def test_row_views():
+    """The distance between rows that the binding finds in views, and the views it refuses."""
+    rows = lambda t, lead=2: selective._rows("x", t, t.device, t.dtype, t.shape, lead)  # noqa: E731
+    u = torch.zeros(3, 5, 20)
+    assert rows(u) == 0 and rows(u[..., 4:12]) == 20 and rows(u[:1, 1:4, :8]) == 20 and rows(u[:, :1, :8]) == 100
+    assert rows(u[:1, :1, :8]) == 0 and rows(u[:, 2], 1) == 100
+    assert rows(u[..., :12].unflatten(-1, (3, 4))) == 20
+    for bad in (u[:, :, ::2], u[:, 1:4, :8], u.transpose(1, 2), u[..., :1].expand(3, 5, 4), u[:, ::2, :8],
+                torch.zeros(1, 1, 8).expand(3, 5, 8)):
+        with pytest.raises(ValueError):
+            rows(bad)
