@@ -6,18 +6,37 @@
 // Each (token, channel, n) costs one exponential (a quarter-rate instruction, 4 issue slots) and
 // four multiply-adds, against 8 bytes of 16-bit input and output a (token, channel): the prompt scan is
 // bound by the vector ALU, the step by the state's traffic.
+#include <algorithm>
+
 #include "ssd_scan_common.h"
 
 namespace ssd {
 
+constexpr int kTile = 16;  // tokens of a tile
+
+// The tokens of a tile that a wave prepares: raw inputs, loaded a tile ahead.
+template <typename T, int TPW, bool Z> struct ScanTokens {
+    T x[TPW], dt[TPW], z[Z ? TPW : 1];
+    __device__ inline void load(const ScanArgs& a, const ScanPlace& p, int t0, int w, int nw) {
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            const int64_t r = p.row0 + min(t0 + w + j * nw, a.seqlen - 1);
+            x[j] = ((const T*)a.x)[r * a.xs + p.c];
+            dt[j] = ((const T*)a.dt)[r * a.dts + p.c];
+            if (Z) z[j] = a.z ? ((const T*)a.z)[r * a.zs + p.c] : (T)0.f;
+        }
+    }
+};
+
+// A workgroup runs its split's tokens a tile at a time: every wave prepares its tokens' (d, d x) in LDS, runs the
+// recurrence of its NS states through the tile, leaves its share of y in LDS, and finishes its tokens.
 template <typename T, int NW, int NS, bool VL>
 __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
-    constexpr int TT_ = 16;            // tokens of a tile
-    constexpr int TPW = TT_ / NW;      // tokens a wave prepares and finishes
+    constexpr int TPW = kTile / NW;    // tokens a wave prepares and finishes
     constexpr int PERIOD = 64 / NS;    // tokens between saved states
     constexpr int N = NW * NS;
-    __shared__ f32x2 s_d[TT_][64];     // (d, d x)
-    __shared__ float s_y[NW][TT_][64];
+    __shared__ f32x2 s_d[kTile][64];   // (d, d x)
+    __shared__ float s_y[NW][kTile][64];
     const ScanPlace p = scan_place(a);
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = w * NS;
@@ -30,32 +49,30 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
     }
     const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f, Dc = a.D ? a.D[p.c] : 0.f;
     const int64_t soff = (int64_t)p.c * N + n0, sstride = (int64_t)a.channels * N;
-    const int tile0 = p.split * a.tiles_per_split, tile1 = min(tile0 + a.tiles_per_split, (a.seqlen + TT_ - 1) / TT_);
-    if (p.split) {
-#pragma unroll
-        for (int i = 0; i < NS; ++i) h[i] = a.split_state[((int64_t)p.b * a.nsplit + p.split) * sstride + soff + i];
-    } else if (!VL && a.h0) {
+    const int tile0 = p.split * a.tiles_per_split, tile1 = min(tile0 + a.tiles_per_split, (a.seqlen + kTile - 1) / kTile);
+    if (p.split)
+        load_states<NS>(a.split_state, DT_F32, ((int64_t)p.b * a.nsplit + p.split) * sstride + soff, h);
+    else if (!VL && a.h0)
         load_states<NS>(a.h0, a.state_dtype, p.b * sstride + soff, h);
-    }
+    ScanTokens<T, TPW, true> next;
+    next.load(a, p, tile0 * kTile, w, NW);
     for (int tile = tile0; tile < tile1; ++tile) {
-        const int t0 = tile * TT_;
-        float xv[TPW], zv[TPW];
+        const int t0 = tile * kTile;
+        const ScanTokens<T, TPW, true> cur = next;
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            const int k = w + j * NW, t = t0 + k;
-            const int64_t r = p.row0 + min(t, a.seqlen - 1);
-            xv[j] = f32of(((const T*)a.x)[r * a.xs + p.c]);
-            const float v = f32of(((const T*)a.dt)[r * a.dts + p.c]) + bias;
-            zv[j] = a.z ? f32of(((const T*)a.z)[r * a.zs + p.c]) : 0.f;
+            const int k = w + j * NW;
+            const float v = f32of(cur.dt[j]) + bias;
             // tokens past the end take no step: d = 0 leaves the state as it is
-            const float d = t < a.seqlen ? (a.softplus ? softplus_f(v) : v) : 0.f;
-            s_d[k][lane] = f32x2{d, d * xv[j]};
+            const float d = t0 + k < a.seqlen ? (a.softplus ? step_f(v) : v) : 0.f;
+            s_d[k][lane] = f32x2{d, d * f32of(cur.x[j])};
         }
         SeqMasks m{0, 0};
-        if (VL) m = seq_masks<TT_>(a, p.row0, t0);
+        if (VL) m = seq_masks<kTile>(a, p.row0, t0);
         __syncthreads();
+        next.load(a, p, t0 + kTile, w, NW);
 #pragma unroll
-        for (int k = 0; k < TT_; ++k) {
+        for (int k = 0; k < kTile; ++k) {
             const int64_t r = p.row0 + min(t0 + k, a.seqlen - 1);
             float Bv[NS], Cv[NS];
             scalar_row<T, NS>((const T*)a.B + r * a.Bs + p.g * N + n0, Bv);
@@ -87,15 +104,107 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             const int k = w + j * NW, t = t0 + k;
-            float y = Dc * xv[j];
+            float y = Dc * f32of(cur.x[j]);
 #pragma unroll
             for (int i = 0; i < NW; ++i) y += s_y[i][k][lane];
-            if (a.z) y *= silu_f(zv[j]);
+            if (a.z) y *= silu_f(f32of(cur.z[j]));
             if (t < a.seqlen && p.live) ((T*)a.out)[(p.row0 + t) * a.channels + p.c] = (T)y;
         }
     }
-    if (!VL && a.fin && tile1 * TT_ >= a.seqlen && p.live)
+    if (!VL && a.fin && tile1 * kTile >= a.seqlen && p.live)
         store_states<NS>(a.fin, a.state_dtype, p.b * sstride + soff, h);
+}
+
+// First pass over the time splits: the state at the end of each split but the last, from a zero state at
+// its start (into the next split's place), and the sum of its steps, by which the state entering it decays
+// (infinite where a sequence starts inside: nothing passes).
+template <typename T, int NW, int NS, bool VL>
+__global__ __launch_bounds__(NW * 64) void k_scan_carry(ScanArgs a) {
+    constexpr int TPW = kTile / NW;
+    constexpr int N = NW * NS;
+    __shared__ f32x2 s_d[2][kTile][64];  // (d, d x), one tile ahead
+    ScanArgs grid = a;
+    grid.nsplit = a.nsplit - 1;
+    const ScanPlace p = scan_place(grid);
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = w * NS;
+    float A2[NS], h[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        A2[i] = a.A[(int64_t)p.c * N + n0 + i] * kLog2e;
+        h[i] = 0.f;
+    }
+    const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
+    const int64_t soff = (int64_t)p.c * N + n0, sstride = (int64_t)a.channels * N;
+    const int tile0 = p.split * a.tiles_per_split, tile1 = tile0 + a.tiles_per_split;  // never the last split
+    float sum = 0.f;
+    bool fresh = false;
+    ScanTokens<T, TPW, false> next;
+    auto prepare = [&](int buf) {
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            const float v = f32of(next.dt[j]) + bias;
+            const float d = a.softplus ? step_f(v) : v;
+            s_d[buf][w + j * NW][lane] = f32x2{d, d * f32of(next.x[j])};
+        }
+    };
+    next.load(a, p, tile0 * kTile, w, NW);
+    prepare(0);
+    for (int tile = tile0; tile < tile1; ++tile) {
+        const int t0 = tile * kTile, buf = (tile - tile0) & 1;
+        next.load(a, p, t0 + kTile, w, NW);
+        SeqMasks m{0, 0};
+        if (VL) m = seq_masks<kTile>(a, p.row0, t0);
+        __syncthreads();
+        float part = 0.f;
+#pragma unroll
+        for (int k = 0; k < kTile; ++k) {
+            const int64_t r = p.row0 + t0 + k;
+            float Bv[NS];
+            scalar_row<T, NS>((const T*)a.B + r * a.Bs + p.g * N + n0, Bv);
+            if (VL && (m.start >> k & 1)) {
+                const int q = a.seq[r];
+                fresh = true;
+#pragma unroll
+                for (int i = 0; i < NS; ++i) h[i] = 0.f;
+                if (a.h0 && state_number(a, q)) load_states<NS>(a.h0, a.state_dtype, q * sstride + soff, h);
+            }
+            const f32x2 dv = s_d[buf][k][lane];
+            part += dv[0];
+#pragma unroll
+            for (int i = 0; i < NS; ++i) h[i] = __builtin_amdgcn_exp2f(dv[0] * A2[i]) * h[i] + dv[1] * Bv[i];
+        }
+        sum += part;
+        prepare(buf ^ 1);  // the other buffer's readers passed this tile's barrier
+    }
+    if (!p.live) return;
+    store_states<NS>(a.split_state, DT_F32, ((int64_t)p.b * a.nsplit + p.split + 1) * sstride + soff, h);
+    if (w == 0) a.split_sum[((int64_t)p.b * a.nsplit + p.split) * a.channels + p.c] = fresh ? __builtin_inff() : sum;
+}
+
+// Joins the splits: the state entering each, from the states that k_scan_carry left.  A lane owns one (channel, n).
+__global__ __launch_bounds__(256) void k_scan_join(ScanArgs a) {
+    const int64_t per = (int64_t)a.channels * a.dstate, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.batch * per) return;
+    const int b = (int)(i / per);
+    const int64_t cn = i % per;
+    const int c = (int)(cn / a.dstate);
+    const float A2 = a.A[cn] * kLog2e;
+    float h = 0.f;
+    if (!a.seq && a.h0) {
+        const int64_t o = b * per + cn;
+        h = a.state_dtype == DT_F32   ? ((const float*)a.h0)[o]
+            : a.state_dtype == DT_F16 ? (float)((const _Float16*)a.h0)[o]
+                                      : (float)((const __bf16*)a.h0)[o];
+    }
+    float* st = a.split_state + (int64_t)b * a.nsplit * per + cn;
+    const float* sum = a.split_sum + (int64_t)b * a.nsplit * a.channels + c;
+#pragma unroll 8
+    for (int s = 1; s < a.nsplit; ++s) {
+        const float d = sum[(int64_t)(s - 1) * a.channels], own = st[s * per];
+        h = d == __builtin_inff() ? own : __builtin_amdgcn_exp2f(d * A2) * h + own;
+        st[s * per] = h;
+    }
 }
 
 // One token: N / 4 lanes hold a channel's states, four each, and share the sum over n.
@@ -118,7 +227,7 @@ template <typename T, typename S, int N> __global__ __launch_bounds__(256) void 
     for (int j = 0; j < 4; ++j) h[j] = (float)st[j];
     const float x = f32of(((const T*)a.x)[b * a.xs + c]);
     const float v = f32of(((const T*)a.dt)[b * a.dts + c]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
-    const float d = a.softplus ? softplus_f(v) : v;
+    const float d = a.softplus ? step_f(v) : v;
     const f32x4 A = *(const f32x4*)(a.A + (int64_t)c * N + n0);
     const T* Bp = (const T*)a.B + b * a.Bs + g * N + n0;
     const T* Cp = (const T*)a.C + b * a.Cs + g * N + n0;
@@ -138,12 +247,32 @@ template <typename T, typename S, int N> __global__ __launch_bounds__(256) void 
     }
 }
 
-int scan_splits(int64_t batch, int64_t seqlen, int64_t channels, int groups, int dstate, bool backward) { return 1; }
+constexpr int64_t kSplitBlocks = 2048;  // workgroups that fill the chip's 1024 SIMDs
+
+// Time splits.  A split costs a second pass over its tokens (without y) and a launch or two, so there
+// are only as many as it takes to give every SIMD of the chip work, and none shorter than 2 tiles.
+int scan_splits(int64_t batch, int64_t seqlen, int64_t channels, int groups, int dstate, bool backward) {
+    const int64_t dg = channels / groups, blocks = batch * groups * ((dg + 63) / 64);
+    const int64_t tile = backward ? scan_period(dstate) : kTile, tiles = (seqlen + tile - 1) / tile;
+    int64_t s = std::min(kSplitBlocks / blocks, tiles / 2);
+    if (s < 2) return 1;
+    const int64_t per = (tiles + s - 1) / s;
+    return (int)((tiles + per - 1) / per);
+}
 
 template <typename T, int NW, int NS> hipError_t launch_scan_n(ScanArgs& a, hipStream_t st) {
     void* args[] = {&a};
+    const unsigned blocks = (unsigned)(a.batch * a.groups * a.cblk);
+    if (a.nsplit > 1) {
+        const void* fn = a.seq ? (const void*)&k_scan_carry<T, NW, NS, true> : (const void*)&k_scan_carry<T, NW, NS, false>;
+        hipError_t e = hipLaunchKernel(fn, dim3(blocks * (a.nsplit - 1)), dim3(NW * 64), args, 0, st);
+        if (e != hipSuccess) return e;
+        const int64_t lanes = (int64_t)a.batch * a.channels * a.dstate;
+        e = hipLaunchKernel((const void*)&k_scan_join, dim3((unsigned)((lanes + 255) / 256)), dim3(256), args, 0, st);
+        if (e != hipSuccess) return e;
+    }
     const void* fn = a.seq ? (const void*)&k_scan<T, NW, NS, true> : (const void*)&k_scan<T, NW, NS, false>;
-    return hipLaunchKernel(fn, dim3((unsigned)(a.batch * a.nsplit * a.groups * a.cblk)), dim3(NW * 64), args, 0, st);
+    return hipLaunchKernel(fn, dim3(blocks * a.nsplit), dim3(NW * 64), args, 0, st);
 }
 
 template <typename T> hipError_t launch_scan_t(ScanArgs& a, hipStream_t st) {

@@ -14,23 +14,72 @@
 
 namespace ssd {
 
-// Sums v over the wave's 64 lanes, for 64 values v: lane l returns the sum of the value with index l.
-// fn(i) gives value i.
-__device__ inline float wave_sum64(const float (&v)[64]) {
-    const int lane = threadIdx.x & 63;
-    float r = 0.f;
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
-        float s = v[i];
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) s += __shfl_xor(s, m, 64);
-        if (lane == i) r = s;
-    }
-    return r;
+// Sums 64 values over the wave's 64 lanes so that each lane ends with one total.  Two values at a time, a
+// lane keeps the half of the lanes' sum of one and hands its part of the other across: 63 exchanges
+// and additions in all, where 64 sums by themselves would take 384.  Values come in order of their index; at
+// most six sums wait for their partner.  Lane l ends with the value whose index is l's bits in the order
+// 3, 2, 1, 0, 5, 4 (the exchanges within 16 lanes ride on the addition, so they come first).
+template <int CTRL> __device__ inline float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
+struct WaveSum64 {
+    float wait[6];
+    template <int LEVEL> __device__ static inline float join(float x, float y) {
+        const int lane = threadIdx.x & 63;
+        if constexpr (LEVEL < 4) {
+            const bool up = lane & (8 >> LEVEL);
+            const float mine = up ? y : x, other = up ? x : y;
+            // partners: lane ^ 8 (rotate 16 by 8), ^ 7 (mirror 8), ^ 2, ^ 1
+            return mine + (LEVEL == 0 ? dpp<0x128>(other) : LEVEL == 1 ? dpp<0x141>(other)
+                           : LEVEL == 2 ? dpp<0x4e>(other) : dpp<0xb1>(other));
+        } else {
+            // (the pair's elements are named before the casts: a cast of a vector's element takes its first)
+            const uint32_t u = __builtin_bit_cast(uint32_t, x), v = __builtin_bit_cast(uint32_t, y);
+            const auto r = LEVEL == 4 ? __builtin_amdgcn_permlane32_swap(u, v, false, false)
+                                      : __builtin_amdgcn_permlane16_swap(u, v, false, false);
+            const uint32_t r0 = r[0], r1 = r[1];
+            return __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
+        }
+    }
+    // value `i` (a constant after unrolling)
+    __device__ inline void push(int i, float v) {
+        if (!(i & 1)) { wait[0] = v; return; }
+        v = join<0>(wait[0], v);
+        if (!(i & 2)) { wait[1] = v; return; }
+        v = join<1>(wait[1], v);
+        if (!(i & 4)) { wait[2] = v; return; }
+        v = join<2>(wait[2], v);
+        if (!(i & 8)) { wait[3] = v; return; }
+        v = join<3>(wait[3], v);
+        if (!(i & 16)) { wait[4] = v; return; }
+        v = join<4>(wait[4], v);
+        if (!(i & 32)) { wait[5] = v; return; }
+        wait[0] = join<5>(wait[5], v);
+    }
+    __device__ inline float total() const { return wait[0]; }
+    __device__ static inline int index(int lane) {
+        return (lane >> 3 & 1) | (lane >> 2 & 1) << 1 | (lane >> 1 & 1) << 2 | (lane & 1) << 3 | (lane >> 5 & 1) << 4 |
+               (lane >> 4 & 1) << 5;
+    }
+};
+
+// The tokens of a tile that a wave prepares and finishes: raw inputs, loaded a tile ahead.
+template <typename T, int TPW> struct BackTokens {
+    T x[TPW], dt[TPW], z[TPW], g[TPW];
+    __device__ inline void load(const ScanArgs& a, const ScanPlace& p, int t0, int w, int nw) {
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            const int64_t r = p.row0 + max(0, min(t0 + w + j * nw, a.seqlen - 1));
+            x[j] = ((const T*)a.x)[r * a.xs + p.c];
+            dt[j] = ((const T*)a.dt)[r * a.dts + p.c];
+            g[j] = ((const T*)a.dout)[r * a.channels + p.c];
+            z[j] = a.z ? ((const T*)a.z)[r * a.zs + p.c] : (T)0.f;
+        }
+    }
+};
 
 template <typename T, int NW, int NS, bool VL>
-__global__ __launch_bounds__(NW * 64) void k_scan_backward(ScanArgs a) {
+__global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
     constexpr int TB = 64 / NS;   // tokens of a tile
     constexpr int TPW = TB / NW;  // tokens a wave prepares and finishes
     static_assert(TPW >= 1, "every wave has a token of each tile");
@@ -42,48 +91,49 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward(ScanArgs a) {
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = w * NS;
 
-    float A[NS], g[NS], dA[NS];
+    float A2[NS], g[NS], dA[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        A[i] = a.A[(int64_t)p.c * N + n0 + i];
+        A2[i] = a.A[(int64_t)p.c * N + n0 + i] * kLog2e;
         g[i] = dA[i] = 0.f;
     }
     const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f, Dc = a.D ? a.D[p.c] : 0.f;
     float dD = 0.f, db = 0.f;
     const int64_t soff = (int64_t)p.c * N + n0, sstride = (int64_t)a.channels * N;
     const int tile0 = p.split * a.tiles_per_split, tile1 = min(tile0 + a.tiles_per_split, a.ntiles);
-    if (p.split + 1 < a.nsplit) {
-#pragma unroll
-        for (int i = 0; i < NS; ++i) g[i] = a.split_state[((int64_t)p.b * a.nsplit + p.split) * sstride + soff + i];
-    } else if (!VL && a.dfin) {
+    if (p.split + 1 < a.nsplit)
+        load_states<NS>(a.split_state, DT_F32, ((int64_t)p.b * a.nsplit + p.split) * sstride + soff, g);
+    else if (!VL && a.dfin)
         load_states<NS>(a.dfin, a.state_dtype, p.b * sstride + soff, g);
-    }
-    float* part = a.part_bc + (((int64_t)p.b * a.groups + p.g) * a.cblk + p.cblk) * a.seqlen * N;
+    // this wave's sums over the channels, lane l holding token `pk`, state `pi` of a tile
+    const int pidx = WaveSum64::index(lane), pk = TB - 1 - pidx / NS, pi = pidx % NS;
+    float* part = a.part_bc + (((int64_t)p.b * a.groups + p.g) * a.cblk + p.cblk) * a.seqlen * N + n0 + pi;
     const int64_t part_c = (int64_t)a.batch * a.groups * a.cblk * a.seqlen * N;
 
+    BackTokens<T, TPW> next;
+    next.load(a, p, (tile1 - 1) * TB, w, NW);
+    float hnext[NS];
+    load_states<NS>(a.saved, DT_F32, ((int64_t)p.b * a.ntiles + tile1 - 1) * sstride + soff, hnext);
     for (int tile = tile1 - 1; tile >= tile0; --tile) {
         const int t0 = tile * TB;
-        float xv[TPW], zv[TPW], gv[TPW], sg[TPW], dv_[TPW], dyv[TPW];
+        const BackTokens<T, TPW> cur = next;
+        float hin[NS];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) hin[i] = hnext[i];
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            const int k = w + j * NW, t = t0 + k;
-            const bool in = t < a.seqlen && p.live;
-            const int64_t r = p.row0 + min(t, a.seqlen - 1);
-            xv[j] = f32of(((const T*)a.x)[r * a.xs + p.c]);
-            const float v = f32of(((const T*)a.dt)[r * a.dts + p.c]) + bias;
-            gv[j] = in ? f32of(((const T*)a.dout)[r * a.channels + p.c]) : 0.f;
-            zv[j] = a.z ? f32of(((const T*)a.z)[r * a.zs + p.c]) : 0.f;
-            dv_[j] = in ? (a.softplus ? softplus_f(v) : v) : 0.f;
-            sg[j] = a.softplus ? sigmoid_f(v) : 1.f;
-            dyv[j] = a.z ? gv[j] * silu_f(zv[j]) : gv[j];
-            s_d[k][lane] = f32x2{dv_[j], dv_[j] * xv[j]};
-            s_g[k][lane] = dyv[j];
+            const int k = w + j * NW;
+            const bool in = t0 + k < a.seqlen && p.live;
+            const float v = f32of(cur.dt[j]) + bias;
+            const float d = in ? (a.softplus ? step_f(v) : v) : 0.f, go = in ? f32of(cur.g[j]) : 0.f;
+            s_d[k][lane] = f32x2{d, d * f32of(cur.x[j])};
+            s_g[k][lane] = a.z ? go * silu_f(f32of(cur.z[j])) : go;
         }
         SeqMasks m{0, 0};
         if (VL) m = seq_masks<TB>(a, p.row0, t0);
-        float hin[NS];
-        load_states<NS>(a.saved, DT_F32, ((int64_t)p.b * a.ntiles + tile) * sstride + soff, hin);
         __syncthreads();
+        next.load(a, p, t0 - TB, w, NW);
+        load_states<NS>(a.saved, DT_F32, ((int64_t)p.b * a.ntiles + max(tile - 1, 0)) * sstride + soff, hnext);
 
         // the tile's states and decays again
         float h[TB][NS], e[TB][NS];
@@ -106,14 +156,15 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward(ScanArgs a) {
             float y = 0.f;
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
-                e[k][i] = __builtin_amdgcn_exp2f(dv[0] * (A[i] * kLog2e));
+                e[k][i] = __builtin_amdgcn_exp2f(dv[0] * A2[i]);
                 h[k][i] = e[k][i] * prev[i] + dv[1] * Bv[i];
                 y += h[k][i] * Cv[i];
             }
             s_y[w][k][lane] = y;
         }
         // and the gradients back through them
-        float vB[64], vC[64], dAt[NS];
+        WaveSum64 sb, sc;
+        float dAt[NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) dAt[i] = 0.f;
 #pragma unroll
@@ -142,12 +193,12 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward(ScanArgs a) {
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 g[i] += dy * Cv[i];
-                vC[k * NS + i] = dy * h[k][i];
-                vB[k * NS + i] = g[i] * dv[1];
+                sc.push((TB - 1 - k) * NS + i, dy * h[k][i]);
+                sb.push((TB - 1 - k) * NS + i, g[i] * dv[1]);
                 u += g[i] * Bv[i];
                 g[i] *= e[k][i];
                 const float q = g[i] * prev[i];
-                qa += q * A[i];
+                qa += q * A2[i];
                 dAt[i] += q * dv[0];
             }
             s_u[w][k][lane] = u;
@@ -158,40 +209,42 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward(ScanArgs a) {
                     store_states<NS>(a.dh0, a.state_dtype, q * sstride + soff, g);
             }
         }
+        // a tile's sums first, then the tiles': long sums keep their low bits
 #pragma unroll
         for (int i = 0; i < NS; ++i) dA[i] += dAt[i];
-        {
-            const float sb = wave_sum64(vB), sc = wave_sum64(vC);
-            const int k = lane / NS, i = lane % NS;
-            if (t0 + k < a.seqlen) {
-                part[(int64_t)(t0 + k) * N + n0 + i] = sb;
-                part[part_c + (int64_t)(t0 + k) * N + n0 + i] = sc;
-            }
+        if (t0 + pk < a.seqlen) {
+            part[(int64_t)(t0 + pk) * N] = sb.total();
+            part[part_c + (int64_t)(t0 + pk) * N] = sc.total();
         }
         __syncthreads();
+        float dDt = 0.f, dbt = 0.f;
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             const int k = w + j * NW, t = t0 + k;
-            float y = Dc * xv[j], u = 0.f, q = 0.f;
+            const float x = f32of(cur.x[j]), d = s_d[k][lane][0], dy = s_g[k][lane];
+            float y = Dc * x, u = 0.f, q = 0.f;
 #pragma unroll
             for (int i = 0; i < NW; ++i) {
                 y += s_y[i][k][lane];
                 u += s_u[i][k][lane];
                 q += s_q[i][k][lane];
             }
-            const float ddt = (xv[j] * u + q) * sg[j];
+            float ddt = x * u + q * (1.f / kLog2e);
+            if (a.softplus) ddt *= sigmoid_f(f32of(cur.dt[j]) + bias);
             if (t < a.seqlen && p.live) {
                 const int64_t o = (p.row0 + t) * a.channels + p.c;
-                ((T*)a.dx)[o] = (T)(Dc * dyv[j] + dv_[j] * u);
+                ((T*)a.dx)[o] = (T)(Dc * dy + d * u);
                 ((T*)a.ddt)[o] = (T)ddt;
                 if (a.z) {
-                    const float sz = sigmoid_f(zv[j]);
-                    ((T*)a.dz)[o] = (T)(gv[j] * y * (sz * (1.f + zv[j] * (1.f - sz))));
+                    const float z = f32of(cur.z[j]), sz = sigmoid_f(z);
+                    ((T*)a.dz)[o] = (T)(f32of(cur.g[j]) * y * (sz * (1.f + z * (1.f - sz))));
                 }
-                dD += dyv[j] * xv[j];
-                db += ddt;
+                dDt += dy * x;
+                dbt += ddt;
             }
         }
+        dD += dDt;
+        db += dbt;
         __syncthreads();
     }
     if (!VL && a.dh0 && p.split == 0 && p.live) store_states<NS>(a.dh0, a.state_dtype, p.b * sstride + soff, g);
@@ -209,6 +262,101 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward(ScanArgs a) {
         }
         a.part_d[prow * a.channels + p.c] = d;
         a.part_d[((int64_t)a.batch * a.nsplit + prow) * a.channels + p.c] = b;
+    }
+}
+
+// First pass over the time splits, from the last token to the first: the gradient of the state entering each
+// split but the first, from a zero gradient behind it (into the split before's place), and the sum of its steps.
+template <typename T, int NW, int NS, bool VL>
+__global__ __launch_bounds__(NW * 64) void k_scan_backward_carry(ScanArgs a) {
+    constexpr int TB = 64 / NS, TPW = TB / NW, N = NW * NS;
+    __shared__ f32x2 s_d[2][TB][64];  // (d, dy), one tile ahead
+    ScanArgs grid = a;
+    grid.nsplit = a.nsplit - 1;
+    ScanPlace p = scan_place(grid);
+    p.split += 1;
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = w * NS;
+    float A2[NS], g[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        A2[i] = a.A[(int64_t)p.c * N + n0 + i] * kLog2e;
+        g[i] = 0.f;
+    }
+    const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
+    const int64_t soff = (int64_t)p.c * N + n0, sstride = (int64_t)a.channels * N;
+    const int tile0 = p.split * a.tiles_per_split, tile1 = min(tile0 + a.tiles_per_split, a.ntiles);
+    float sum = 0.f;
+    bool fresh = false;
+    if (!VL && a.dfin && p.split == a.nsplit - 1) load_states<NS>(a.dfin, a.state_dtype, p.b * sstride + soff, g);
+    T dt[TPW], z[TPW], go[TPW];
+    auto load = [&](int t0) {
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            const int64_t r = p.row0 + max(0, min(t0 + w + j * NW, a.seqlen - 1));
+            dt[j] = ((const T*)a.dt)[r * a.dts + p.c];
+            go[j] = ((const T*)a.dout)[r * a.channels + p.c];
+            z[j] = a.z ? ((const T*)a.z)[r * a.zs + p.c] : (T)0.f;
+        }
+    };
+    auto prepare = [&](int buf, int t0) {
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            const bool in = t0 + w + j * NW < a.seqlen;
+            const float v = f32of(dt[j]) + bias, o = in ? f32of(go[j]) : 0.f;
+            s_d[buf][w + j * NW][lane] = f32x2{in ? (a.softplus ? step_f(v) : v) : 0.f, a.z ? o * silu_f(f32of(z[j])) : o};
+        }
+    };
+    load((tile1 - 1) * TB);
+    prepare(0, (tile1 - 1) * TB);
+    for (int tile = tile1 - 1; tile >= tile0; --tile) {
+        const int t0 = tile * TB, buf = (tile1 - 1 - tile) & 1;
+        load(t0 - TB);
+        SeqMasks m{0, 0};
+        if (VL) m = seq_masks<TB>(a, p.row0, t0);
+        __syncthreads();
+        float part = 0.f;
+#pragma unroll
+        for (int k = TB - 1; k >= 0; --k) {
+            const int64_t r = p.row0 + min(t0 + k, a.seqlen - 1);
+            float Cv[NS];
+            scalar_row<T, NS>((const T*)a.C + r * a.Cs + p.g * N + n0, Cv);
+            if (VL && (m.end >> k & 1)) {
+                const int q = a.seq[r];
+                fresh = true;
+#pragma unroll
+                for (int i = 0; i < NS; ++i) g[i] = 0.f;
+                if (a.dfin && state_number(a, q)) load_states<NS>(a.dfin, a.state_dtype, q * sstride + soff, g);
+            }
+            const f32x2 dv = s_d[buf][k][lane];
+            part += dv[0];
+#pragma unroll
+            for (int i = 0; i < NS; ++i) g[i] = __builtin_amdgcn_exp2f(dv[0] * A2[i]) * (g[i] + dv[1] * Cv[i]);
+        }
+        sum += part;
+        prepare(buf ^ 1, t0 - TB);  // the other buffer's readers passed this tile's barrier
+    }
+    if (!p.live) return;
+    store_states<NS>(a.split_state, DT_F32, ((int64_t)p.b * a.nsplit + p.split - 1) * sstride + soff, g);
+    if (w == 0) a.split_sum[((int64_t)p.b * a.nsplit + p.split) * a.channels + p.c] = fresh ? __builtin_inff() : sum;
+}
+
+// Joins the splits from the last to the first: the gradient entering each from behind.
+__global__ __launch_bounds__(256) void k_scan_backward_join(ScanArgs a) {
+    const int64_t per = (int64_t)a.channels * a.dstate, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.batch * per) return;
+    const int b = (int)(i / per);
+    const int64_t cn = i % per;
+    const int c = (int)(cn / a.dstate);
+    const float A2 = a.A[cn] * kLog2e;
+    float* st = a.split_state + (int64_t)b * a.nsplit * per + cn;
+    const float* sum = a.split_sum + (int64_t)b * a.nsplit * a.channels + c;
+    float g = st[(a.nsplit - 2) * per];  // the last split's own pass began with the final state's gradient
+#pragma unroll 8
+    for (int s = a.nsplit - 3; s >= 0; --s) {
+        const float d = sum[(int64_t)(s + 1) * a.channels], own = st[s * per];
+        g = d == __builtin_inff() ? own : __builtin_amdgcn_exp2f(d * A2) * g + own;
+        st[s * per] = g;
     }
 }
 
@@ -265,8 +413,19 @@ __global__ __launch_bounds__(256) void k_scan_sum_params(const float* part_a, co
 template <typename T, int NW, int NS>
 hipError_t launch_scan_backward_n(ScanArgs& a, T* dB, T* dC, float* dA, float* dD, float* db, hipStream_t st) {
     void* args[] = {&a};
+    hipError_t e = hipSuccess;
+    const unsigned blocks = (unsigned)(a.batch * a.groups * a.cblk);
+    if (a.nsplit > 1) {
+        const void* fn = a.seq ? (const void*)&k_scan_backward_carry<T, NW, NS, true>
+                               : (const void*)&k_scan_backward_carry<T, NW, NS, false>;
+        e = hipLaunchKernel(fn, dim3(blocks * (a.nsplit - 1)), dim3(NW * 64), args, 0, st);
+        if (e != hipSuccess) return e;
+        const int64_t lanes = (int64_t)a.batch * a.channels * a.dstate;
+        e = hipLaunchKernel((const void*)&k_scan_backward_join, dim3((unsigned)((lanes + 255) / 256)), dim3(256), args, 0, st);
+        if (e != hipSuccess) return e;
+    }
     const void* fn = a.seq ? (const void*)&k_scan_backward<T, NW, NS, true> : (const void*)&k_scan_backward<T, NW, NS, false>;
-    hipError_t e = hipLaunchKernel(fn, dim3((unsigned)(a.batch * a.nsplit * a.groups * a.cblk)), dim3(NW * 64), args, 0, st);
+    e = hipLaunchKernel(fn, dim3(blocks * a.nsplit), dim3(NW * 64), args, 0, st);
     if (e != hipSuccess) return e;
     const int64_t quads = (int64_t)a.batch * a.seqlen * a.groups * a.dstate / 2;  // both tensors, 4 values a lane
     void* bargs[] = {&a.part_bc, &a.batch, &a.seqlen, &a.groups, &a.cblk, &a.dstate, &dB, &dC};

@@ -71,6 +71,15 @@ template <int NS> __device__ inline void store_states(void* base, int dtype, int
     }
 }
 
+// softplus(v) = max(v, 0) + log1p(u), u = exp(-|v|).  log1p(u) = log(s) + (u - (s - 1)) / s to first order in
+// what rounding s = 1 + u loses; s - 1 is exact.  The hardware logarithm is relative to its result near 1
+// too, so small steps keep their relative precision (about 20 slots against 45 of the library's log1pf).
+__device__ inline float step_f(float v) {
+    const float u = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e), s = 1.f + u;
+    const float l = __builtin_amdgcn_logf(s) * 0.693147180559945309417f;
+    return fmaxf(v, 0.f) + (l + (u - (s - 1.f)) * __builtin_amdgcn_rcpf(s));
+}
+
 // softplus'(v)
 __device__ inline float sigmoid_f(float v) { return __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
 
