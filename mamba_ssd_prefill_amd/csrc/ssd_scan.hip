@@ -33,8 +33,9 @@ template <typename T, int TPW, bool Z> struct ScanTokens {
 template <typename T, int NW, int NS, bool VL>
 __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
     constexpr int TPW = kTile / NW;    // tokens a wave prepares and finishes
-    constexpr int PERIOD = 64 / NS;    // tokens between saved states
-    constexpr int N = NW * NS;
+    constexpr int N = NW * NS, PERIOD = scan_period(N);
+    typedef ScalarRows<T, NS> Rows;
+    constexpr int GT = Rows::GROUP;
     __shared__ f32x2 s_d[kTile][64];   // (d, d x)
     __shared__ float s_y[NW][kTile][64];
     const ScanPlace p = scan_place(a);
@@ -71,18 +72,26 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
         if (VL) m = seq_masks<kTile>(a, p.row0, t0);
         __syncthreads();
         next.load(a, p, t0 + kTile, w, NW);
+        const Rows rb((const T*)a.B + p.g * N + n0, a.Bs, p.row0, t0, a.seqlen);
+        const Rows rc((const T*)a.C + p.g * N + n0, a.Cs, p.row0, t0, a.seqlen);
+        typename Rows::Group gb[2], gc[2];
+        gb[0].load(rb, 0);
+        gc[0].load(rc, 0);
 #pragma unroll
         for (int k = 0; k < kTile; ++k) {
-            const int64_t r = p.row0 + min(t0 + k, a.seqlen - 1);
+            if (k % GT == 0 && k + GT < kTile) {
+                gb[(k / GT + 1) & 1].load(rb, k + GT);
+                gc[(k / GT + 1) & 1].load(rc, k + GT);
+            }
             float Bv[NS], Cv[NS];
-            scalar_row<T, NS>((const T*)a.B + r * a.Bs + p.g * N + n0, Bv);
-            scalar_row<T, NS>((const T*)a.C + r * a.Cs + p.g * N + n0, Cv);
+            gb[(k / GT) & 1].values(k % GT, Bv);
+            gc[(k / GT) & 1].values(k % GT, Cv);
             if (k % PERIOD == 0 && a.saved && t0 + k < a.seqlen && p.live) {
                 float* sv = a.saved + ((int64_t)p.b * a.ntiles + (t0 + k) / PERIOD) * sstride + soff;
                 store_states<NS>(sv, DT_F32, 0, h);
             }
             if (VL && (m.start >> k & 1)) {
-                const int q = a.seq[r];
+                const int q = a.seq[p.row0 + t0 + k];
 #pragma unroll
                 for (int i = 0; i < NS; ++i) h[i] = 0.f;
                 if (a.h0 && state_number(a, q)) load_states<NS>(a.h0, a.state_dtype, q * sstride + soff, h);
@@ -96,7 +105,7 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
             }
             s_y[w][k][lane] = y;
             if (VL && (m.end >> k & 1) && a.fin && p.live) {
-                const int q = a.seq[r];
+                const int q = a.seq[p.row0 + t0 + k];
                 if (state_number(a, q)) store_states<NS>(a.fin, a.state_dtype, q * sstride + soff, h);
             }
         }
@@ -120,8 +129,9 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
 // (infinite where a sequence starts inside: nothing passes).
 template <typename T, int NW, int NS, bool VL>
 __global__ __launch_bounds__(NW * 64) void k_scan_carry(ScanArgs a) {
-    constexpr int TPW = kTile / NW;
-    constexpr int N = NW * NS;
+    constexpr int TPW = kTile / NW, N = NW * NS;
+    typedef ScalarRows<T, NS> Rows;
+    constexpr int GT = Rows::GROUP;
     __shared__ f32x2 s_d[2][kTile][64];  // (d, d x), one tile ahead
     ScanArgs grid = a;
     grid.nsplit = a.nsplit - 1;
@@ -156,14 +166,17 @@ __global__ __launch_bounds__(NW * 64) void k_scan_carry(ScanArgs a) {
         SeqMasks m{0, 0};
         if (VL) m = seq_masks<kTile>(a, p.row0, t0);
         __syncthreads();
+        const Rows rb((const T*)a.B + p.g * N + n0, a.Bs, p.row0, t0, a.seqlen);
+        typename Rows::Group gb[2];
+        gb[0].load(rb, 0);
         float part = 0.f;
 #pragma unroll
         for (int k = 0; k < kTile; ++k) {
-            const int64_t r = p.row0 + t0 + k;
+            if (k % GT == 0 && k + GT < kTile) gb[(k / GT + 1) & 1].load(rb, k + GT);
             float Bv[NS];
-            scalar_row<T, NS>((const T*)a.B + r * a.Bs + p.g * N + n0, Bv);
+            gb[(k / GT) & 1].values(k % GT, Bv);
             if (VL && (m.start >> k & 1)) {
-                const int q = a.seq[r];
+                const int q = a.seq[p.row0 + t0 + k];
                 fresh = true;
 #pragma unroll
                 for (int i = 0; i < NS; ++i) h[i] = 0.f;

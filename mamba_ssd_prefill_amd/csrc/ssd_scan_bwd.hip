@@ -84,6 +84,9 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
     constexpr int TPW = TB / NW;  // tokens a wave prepares and finishes
     static_assert(TPW >= 1, "every wave has a token of each tile");
     constexpr int N = NW * NS;
+    static_assert(TB == scan_period(N), "a saved state enters each tile");
+    typedef ScalarRows<T, NS> Rows;
+    constexpr int GT = Rows::GROUP;
     __shared__ f32x2 s_d[TB][64];  // (d, d x)
     __shared__ float s_g[TB][64];  // dy
     __shared__ float s_y[NW][TB][64], s_u[NW][TB][64], s_q[NW][TB][64];
@@ -137,17 +140,25 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
 
         // the tile's states and decays again
         float h[TB][NS], e[TB][NS];
+        const Rows rb((const T*)a.B + p.g * N + n0, a.Bs, p.row0, t0, a.seqlen);
+        const Rows rc((const T*)a.C + p.g * N + n0, a.Cs, p.row0, t0, a.seqlen);
+        typename Rows::Group gb[2], gc[2];
+        gb[0].load(rb, 0);
+        gc[0].load(rc, 0);
 #pragma unroll
         for (int k = 0; k < TB; ++k) {
-            const int64_t r = p.row0 + min(t0 + k, a.seqlen - 1);
+            if (k % GT == 0 && k + GT < TB) {
+                gb[(k / GT + 1) & 1].load(rb, k + GT);
+                gc[(k / GT + 1) & 1].load(rc, k + GT);
+            }
             float Bv[NS], Cv[NS];
-            scalar_row<T, NS>((const T*)a.B + r * a.Bs + p.g * N + n0, Bv);
-            scalar_row<T, NS>((const T*)a.C + r * a.Cs + p.g * N + n0, Cv);
+            gb[(k / GT) & 1].values(k % GT, Bv);
+            gc[(k / GT) & 1].values(k % GT, Cv);
             float prev[NS];
 #pragma unroll
             for (int i = 0; i < NS; ++i) prev[i] = k ? h[k ? k - 1 : 0][i] : hin[i];
             if (VL && (m.start >> k & 1)) {
-                const int q = a.seq[r];
+                const int q = a.seq[p.row0 + t0 + k];
 #pragma unroll
                 for (int i = 0; i < NS; ++i) prev[i] = 0.f;
                 if (a.h0 && state_number(a, q)) load_states<NS>(a.h0, a.state_dtype, q * sstride + soff, prev);
@@ -167,22 +178,27 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
         float dAt[NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) dAt[i] = 0.f;
+        gb[(TB / GT - 1) & 1].load(rb, TB - GT);
+        gc[(TB / GT - 1) & 1].load(rc, TB - GT);
 #pragma unroll
         for (int k = TB - 1; k >= 0; --k) {
-            const int64_t r = p.row0 + min(t0 + k, a.seqlen - 1);
+            if (k % GT == GT - 1 && k >= GT) {
+                gb[(k / GT - 1) & 1].load(rb, k - 2 * GT + 1);
+                gc[(k / GT - 1) & 1].load(rc, k - 2 * GT + 1);
+            }
             float Bv[NS], Cv[NS], prev[NS];
-            scalar_row<T, NS>((const T*)a.B + r * a.Bs + p.g * N + n0, Bv);
-            scalar_row<T, NS>((const T*)a.C + r * a.Cs + p.g * N + n0, Cv);
+            gb[(k / GT) & 1].values(k % GT, Bv);
+            gc[(k / GT) & 1].values(k % GT, Cv);
 #pragma unroll
             for (int i = 0; i < NS; ++i) prev[i] = k ? h[k ? k - 1 : 0][i] : hin[i];
             if (VL && (m.start >> k & 1)) {
-                const int q = a.seq[r];
+                const int q = a.seq[p.row0 + t0 + k];
 #pragma unroll
                 for (int i = 0; i < NS; ++i) prev[i] = 0.f;
                 if (a.h0 && state_number(a, q)) load_states<NS>(a.h0, a.state_dtype, q * sstride + soff, prev);
             }
             if (VL && (m.end >> k & 1)) {
-                const int q = a.seq[r];
+                const int q = a.seq[p.row0 + t0 + k];
 #pragma unroll
                 for (int i = 0; i < NS; ++i) g[i] = 0.f;
                 if (a.dfin && state_number(a, q)) load_states<NS>(a.dfin, a.state_dtype, q * sstride + soff, g);
@@ -204,7 +220,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
             s_u[w][k][lane] = u;
             s_q[w][k][lane] = qa;
             if (VL && (m.start >> k & 1)) {
-                const int q = a.seq[r];
+                const int q = a.seq[p.row0 + t0 + k];
                 if (a.dh0 && state_number(a, q) && p.live)
                     store_states<NS>(a.dh0, a.state_dtype, q * sstride + soff, g);
             }
@@ -270,6 +286,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
 template <typename T, int NW, int NS, bool VL>
 __global__ __launch_bounds__(NW * 64) void k_scan_backward_carry(ScanArgs a) {
     constexpr int TB = 64 / NS, TPW = TB / NW, N = NW * NS;
+    typedef ScalarRows<T, NS> Rows;
+    constexpr int GT = Rows::GROUP;
     __shared__ f32x2 s_d[2][TB][64];  // (d, dy), one tile ahead
     ScanArgs grid = a;
     grid.nsplit = a.nsplit - 1;
@@ -315,14 +333,17 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward_carry(ScanArgs a) {
         SeqMasks m{0, 0};
         if (VL) m = seq_masks<TB>(a, p.row0, t0);
         __syncthreads();
+        const Rows rc((const T*)a.C + p.g * N + n0, a.Cs, p.row0, t0, a.seqlen);
+        typename Rows::Group gc[2];
+        gc[(TB / GT - 1) & 1].load(rc, TB - GT);
         float part = 0.f;
 #pragma unroll
         for (int k = TB - 1; k >= 0; --k) {
-            const int64_t r = p.row0 + min(t0 + k, a.seqlen - 1);
+            if (k % GT == GT - 1 && k >= GT) gc[(k / GT - 1) & 1].load(rc, k - 2 * GT + 1);
             float Cv[NS];
-            scalar_row<T, NS>((const T*)a.C + r * a.Cs + p.g * N + n0, Cv);
+            gc[(k / GT) & 1].values(k % GT, Cv);
             if (VL && (m.end >> k & 1)) {
-                const int q = a.seq[r];
+                const int q = a.seq[p.row0 + t0 + k];
                 fresh = true;
 #pragma unroll
                 for (int i = 0; i < NS; ++i) g[i] = 0.f;

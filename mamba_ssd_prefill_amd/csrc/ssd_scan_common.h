@@ -14,31 +14,55 @@ namespace ssd {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// Wave-uniform reads through the scalar cache (the data is written before the launch).
-typedef const __attribute__((address_space(4))) uint32_t* ScalarPtr;
-__device__ inline ScalarPtr scalar_ptr(const void* p) { return (ScalarPtr)(uintptr_t)p; }
-
-// NS values of type T at a 4-byte aligned address, as fp32.
-template <typename T, int NS> __device__ inline void scalar_row(const T* p, float (&v)[NS]) {
-    ScalarPtr s = scalar_ptr(p);
-    if constexpr (sizeof(T) == 4) {
+// The rows of B (or C) of a tile for one wave, NS values each, read through the scalar cache (the data is written
+// before the launch) a group of GROUP tokens at a time, so that a group can be on its way while the one
+// before is used.  One base address a tile and 32-bit offsets: scalar instructions issue at the rate of vector
+// ones, and 64-bit addresses for every token took more of them than the recurrence itself.
+typedef const __attribute__((address_space(4))) char* ScalarPtr;
+template <typename T, int NS> struct ScalarRows {
+    static constexpr int WORDS = NS * (int)sizeof(T) / 4;  // 4-byte words of a row
+    static constexpr int GROUP = WORDS <= 2 ? 4 : WORDS <= 4 ? 2 : 1;
+    ScalarPtr base;
+    uint32_t stride;
+    int last;  // rows past the end read the last one
+    __device__ inline ScalarRows(const T* rows, int64_t row_stride, int64_t row0, int t0, int seqlen) {
+        base = (ScalarPtr)(uintptr_t)(rows + (row0 + t0) * row_stride);
+        stride = (uint32_t)row_stride * (uint32_t)sizeof(T);
+        last = seqlen - 1 - t0;
+    }
+    struct Group {
+        uint32_t w[GROUP][WORDS];
+        __device__ inline void load(const ScalarRows& r, int k0) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) v[i] = __builtin_bit_cast(float, s[i]);
-    } else {
+            for (int j = 0; j < GROUP; ++j) {
+                const uint32_t off = (uint32_t)min(k0 + j, r.last) * r.stride;
+                typedef const __attribute__((address_space(4))) uint32_t* Words;
 #pragma unroll
-        for (int i = 0; i < NS / 2; ++i) {
-            const uint32_t u = s[i];
-            if constexpr (__is_same(T, __bf16)) {
-                v[2 * i] = __builtin_bit_cast(float, u << 16);
-                v[2 * i + 1] = __builtin_bit_cast(float, u & 0xffff0000u);
-            } else {
-                const f16x2 h = __builtin_bit_cast(f16x2, u);
-                v[2 * i] = (float)h[0];
-                v[2 * i + 1] = (float)h[1];
+                for (int i = 0; i < WORDS; ++i) w[j][i] = ((Words)(r.base + off))[i];
             }
         }
-    }
-}
+        // token k0 + j as fp32
+        __device__ inline void values(int j, float (&v)[NS]) const {
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < NS; ++i) v[i] = __builtin_bit_cast(float, w[j][i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NS / 2; ++i) {
+                    const uint32_t u = w[j][i];
+                    if constexpr (__is_same(T, __bf16)) {
+                        v[2 * i] = __builtin_bit_cast(float, u << 16);
+                        v[2 * i + 1] = __builtin_bit_cast(float, u & 0xffff0000u);
+                    } else {
+                        const f16x2 h = __builtin_bit_cast(f16x2, u);
+                        v[2 * i] = (float)h[0];
+                        v[2 * i + 1] = (float)h[1];
+                    }
+                }
+            }
+        }
+    };
+};
 
 // NS states at element offset `off`.
 template <int NS> __device__ inline void load_states(const void* base, int dtype, int64_t off, float (&h)[NS]) {

@@ -76,7 +76,7 @@ struct ScanArgs {
 };
 
 // Tokens between two saved states.
-inline int scan_period(int dstate) { return dstate == 64 ? 8 : 16; }
+__host__ __device__ constexpr int scan_period(int dstate) { return dstate == 64 ? 8 : 16; }
 
 // Time splits of the forward and the backward: a function of the sizes alone, so that workspaces
 // can be sized without a device.
