@@ -503,7 +503,7 @@ typedef struct {
     int state_dtype;    /* ssd_dtype_t of the states and their gradients (the scan itself runs in fp32) */
     int dt_softplus;    /* 1: d = softplus(dt_raw + dt_bias); 0: d = dt_raw + dt_bias */
     int nseq;           /* with seq_idx (or for the step): the number of states; else ignored */
-    int64_t x_stride, dt_stride, z_stride; /* elements between rows; 0: D */
+    int64_t x_stride, dt_stride, z_stride; /* elements between rows, below 2^24; 0: D (below 2^24) */
     int64_t B_stride, C_stride;            /* elements between rows, below 2^24; 0: G*N (even for 16-bit types) */
 } ssd_scan_params_t;
 

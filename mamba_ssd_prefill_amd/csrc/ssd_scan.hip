@@ -18,12 +18,17 @@ constexpr int kTile = 16;  // tokens of a tile
 template <typename T, int TPW, bool Z> struct ScanTokens {
     T x[TPW], dt[TPW], z[Z ? TPW : 1];
     __device__ inline void load(const ScanArgs& a, const ScanPlace& p, int t0, int w, int nw) {
+        const uint32_t lo = (uint32_t)p.c * (uint32_t)sizeof(T);
+        const TileRows<T> rx(a.x, a.xs, p.row0, t0, a.seqlen), rd(a.dt, a.dts, p.row0, t0, a.seqlen);
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            const int64_t r = p.row0 + min(t0 + w + j * nw, a.seqlen - 1);
-            x[j] = ((const T*)a.x)[r * a.xs + p.c];
-            dt[j] = ((const T*)a.dt)[r * a.dts + p.c];
-            if (Z) z[j] = a.z ? ((const T*)a.z)[r * a.zs + p.c] : (T)0.f;
+            x[j] = rx.load(w + j * nw, lo);
+            dt[j] = rd.load(w + j * nw, lo);
+        }
+        if (Z && a.z) {
+            const TileRows<T> rz(a.z, a.zs, p.row0, t0, a.seqlen);
+#pragma unroll
+            for (int j = 0; j < TPW; ++j) z[j] = rz.load(w + j * nw, lo);
         }
     }
 };
@@ -110,14 +115,16 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
             }
         }
         __syncthreads();
+        const TileRows<T> ro(a.out, a.channels, p.row0, t0, a.seqlen);
+        const uint32_t lo = p.live ? (uint32_t)p.c * (uint32_t)sizeof(T) : kNoLane;
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            const int k = w + j * NW, t = t0 + k;
+            const int k = w + j * NW;
             float y = Dc * f32of(cur.x[j]);
 #pragma unroll
             for (int i = 0; i < NW; ++i) y += s_y[i][k][lane];
             if (a.z) y *= silu_f(f32of(cur.z[j]));
-            if (t < a.seqlen && p.live) ((T*)a.out)[(p.row0 + t) * a.channels + p.c] = (T)y;
+            ro.store(k, lo, y);
         }
     }
     if (!VL && a.fin && tile1 * kTile >= a.seqlen && p.live)

@@ -67,19 +67,26 @@ struct WaveSum64 {
 template <typename T, int TPW> struct BackTokens {
     T x[TPW], dt[TPW], z[TPW], g[TPW];
     __device__ inline void load(const ScanArgs& a, const ScanPlace& p, int t0, int w, int nw) {
+        const uint32_t lo = (uint32_t)p.c * (uint32_t)sizeof(T);
+        const TileRows<T> rx(a.x, a.xs, p.row0, t0, a.seqlen), rd(a.dt, a.dts, p.row0, t0, a.seqlen);
+        const TileRows<T> rg(a.dout, a.channels, p.row0, t0, a.seqlen);
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            const int64_t r = p.row0 + max(0, min(t0 + w + j * nw, a.seqlen - 1));
-            x[j] = ((const T*)a.x)[r * a.xs + p.c];
-            dt[j] = ((const T*)a.dt)[r * a.dts + p.c];
-            g[j] = ((const T*)a.dout)[r * a.channels + p.c];
-            z[j] = a.z ? ((const T*)a.z)[r * a.zs + p.c] : (T)0.f;
+            x[j] = rx.load(w + j * nw, lo);
+            dt[j] = rd.load(w + j * nw, lo);
+            g[j] = rg.load(w + j * nw, lo);
+        }
+        if (a.z) {
+            const TileRows<T> rz(a.z, a.zs, p.row0, t0, a.seqlen);
+#pragma unroll
+            for (int j = 0; j < TPW; ++j) z[j] = rz.load(w + j * nw, lo);
         }
     }
 };
 
 template <typename T, int NW, int NS, bool VL>
-__global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
+__global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs args) {
+    const ScanArgs& a = args;
     constexpr int TB = 64 / NS;   // tokens of a tile
     constexpr int TPW = TB / NW;  // tokens a wave prepares and finishes
     static_assert(TPW >= 1, "every wave has a token of each tile");
@@ -118,6 +125,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
     float hnext[NS];
     load_states<NS>(a.saved, DT_F32, ((int64_t)p.b * a.ntiles + tile1 - 1) * sstride + soff, hnext);
     for (int tile = tile1 - 1; tile >= tile0; --tile) {
+        const ScanArgs& a = args_again();
         const int t0 = tile * TB;
         const BackTokens<T, TPW> cur = next;
         float hin[NS];
@@ -135,8 +143,6 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
         SeqMasks m{0, 0};
         if (VL) m = seq_masks<TB>(a, p.row0, t0);
         __syncthreads();
-        next.load(a, p, t0 - TB, w, NW);
-        load_states<NS>(a.saved, DT_F32, ((int64_t)p.b * a.ntiles + max(tile - 1, 0)) * sstride + soff, hnext);
 
         // the tile's states and decays again
         float h[TB][NS], e[TB][NS];
@@ -182,6 +188,11 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
         gc[(TB / GT - 1) & 1].load(rc, TB - GT);
 #pragma unroll
         for (int k = TB - 1; k >= 0; --k) {
+            if (k == TB / 2 - 1) {  // half of the tile's states and decays are used up: room for the next tile's inputs
+                const ScanArgs& a = args_again();
+                next.load(a, p, t0 - TB, w, NW);
+                load_states<NS>(a.saved, DT_F32, ((int64_t)p.b * a.ntiles + max(tile - 1, 0)) * sstride + soff, hnext);
+            }
             if (k % GT == GT - 1 && k >= GT) {
                 gb[(k / GT - 1) & 1].load(rb, k - 2 * GT + 1);
                 gc[(k / GT - 1) & 1].load(rc, k - 2 * GT + 1);
@@ -234,9 +245,13 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
         }
         __syncthreads();
         float dDt = 0.f, dbt = 0.f;
+        const ScanArgs& a2 = args_again();
+        const TileRows<T> rx(a2.dx, a2.channels, p.row0, t0, a2.seqlen), rd(a2.ddt, a2.channels, p.row0, t0, a2.seqlen);
+        const TileRows<T> rz(a2.dz, a2.channels, p.row0, t0, a2.seqlen);
+        const uint32_t lo = p.live ? (uint32_t)p.c * (uint32_t)sizeof(T) : kNoLane;
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            const int k = w + j * NW, t = t0 + k;
+            const int k = w + j * NW;
             const float x = f32of(cur.x[j]), d = s_d[k][lane][0], dy = s_g[k][lane];
             float y = Dc * x, u = 0.f, q = 0.f;
 #pragma unroll
@@ -246,18 +261,15 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs a) {
                 q += s_q[i][k][lane];
             }
             float ddt = x * u + q * (1.f / kLog2e);
-            if (a.softplus) ddt *= sigmoid_f(f32of(cur.dt[j]) + bias);
-            if (t < a.seqlen && p.live) {
-                const int64_t o = (p.row0 + t) * a.channels + p.c;
-                ((T*)a.dx)[o] = (T)(Dc * dy + d * u);
-                ((T*)a.ddt)[o] = (T)ddt;
-                if (a.z) {
-                    const float z = f32of(cur.z[j]), sz = sigmoid_f(z);
-                    ((T*)a.dz)[o] = (T)(f32of(cur.g[j]) * y * (sz * (1.f + z * (1.f - sz))));
-                }
-                dDt += dy * x;
-                dbt += ddt;
+            if (a2.softplus) ddt *= sigmoid_f(f32of(cur.dt[j]) + bias);
+            rx.store(k, lo, Dc * dy + d * u);
+            rd.store(k, lo, ddt);
+            if (a2.z) {
+                const float z = f32of(cur.z[j]), sz = sigmoid_f(z);
+                rz.store(k, lo, f32of(cur.g[j]) * y * (sz * (1.f + z * (1.f - sz))));
             }
+            dDt += dy * x;  // zero past the end, where x = dy = 0
+            dbt += t0 + k < a2.seqlen ? ddt : 0.f;
         }
         dD += dDt;
         db += dbt;
@@ -309,12 +321,17 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward_carry(ScanArgs a) {
     if (!VL && a.dfin && p.split == a.nsplit - 1) load_states<NS>(a.dfin, a.state_dtype, p.b * sstride + soff, g);
     T dt[TPW], z[TPW], go[TPW];
     auto load = [&](int t0) {
+        const uint32_t lo = (uint32_t)p.c * (uint32_t)sizeof(T);
+        const TileRows<T> rd(a.dt, a.dts, p.row0, t0, a.seqlen), rg(a.dout, a.channels, p.row0, t0, a.seqlen);
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            const int64_t r = p.row0 + max(0, min(t0 + w + j * NW, a.seqlen - 1));
-            dt[j] = ((const T*)a.dt)[r * a.dts + p.c];
-            go[j] = ((const T*)a.dout)[r * a.channels + p.c];
-            z[j] = a.z ? ((const T*)a.z)[r * a.zs + p.c] : (T)0.f;
+            dt[j] = rd.load(w + j * NW, lo);
+            go[j] = rg.load(w + j * NW, lo);
+        }
+        if (a.z) {
+            const TileRows<T> rz(a.z, a.zs, p.row0, t0, a.seqlen);
+#pragma unroll
+            for (int j = 0; j < TPW; ++j) z[j] = rz.load(w + j * NW, lo);
         }
     };
     auto prepare = [&](int buf, int t0) {

@@ -64,6 +64,39 @@ template <typename T, int NS> struct ScalarRows {
     };
 };
 
+// The rows of one tensor for a tile of tokens, as a buffer that ends with the batch row: loads of tokens past
+// the end give zeros, stores to them (and from lanes without a channel) are dropped, and an access
+// takes one 32-bit offset.  Rows are below 2^24 elements apart, so a tile's offsets stay below 2^31.
+template <typename T> struct TileRows {
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t stride;
+    __device__ inline TileRows(const void* base, int64_t row_stride, int64_t row0, int t0, int seqlen) {
+        stride = (uint32_t)row_stride * (uint32_t)sizeof(T);
+        const int64_t left = t0 < 0 ? 0 : (int64_t)(seqlen - t0) * stride;
+        rsrc = make_rsrc((const T*)base + (row0 + t0) * row_stride,
+                         (uint32_t)(left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : left));
+    }
+    __device__ inline T load(int k, uint32_t lane_off) const {
+        const int off = (int)(lane_off + (uint32_t)k * stride);
+        if constexpr (sizeof(T) == 4) {
+            const uint32_t u = __builtin_amdgcn_raw_buffer_load_b32(rsrc, off, 0, 0);
+            return __builtin_bit_cast(T, u);
+        } else {
+            const uint16_t u = __builtin_amdgcn_raw_buffer_load_b16(rsrc, off, 0, 0);
+            return __builtin_bit_cast(T, u);
+        }
+    }
+    __device__ inline void store(int k, uint32_t lane_off, float v) const {
+        const int off = (int)(lane_off + (uint32_t)k * stride);
+        const T o = (T)v;
+        if constexpr (sizeof(T) == 4)
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, o), rsrc, off, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, o), rsrc, off, 0, 0);
+    }
+};
+constexpr uint32_t kNoLane = 0x80000000u;  // a store offset past every buffer
+
 // NS states at element offset `off`.
 template <int NS> __device__ inline void load_states(const void* base, int dtype, int64_t off, float (&h)[NS]) {
 #pragma unroll
@@ -96,16 +129,26 @@ template <int NS> __device__ inline void store_states(void* base, int dtype, int
 }
 
 // softplus(v) = max(v, 0) + log1p(u), u = exp(-|v|).  log1p(u) = log(s) + (u - (s - 1)) / s to first order in
-// what rounding s = 1 + u loses; s - 1 is exact.  The hardware logarithm is relative to its result near 1
-// too, so small steps keep their relative precision (about 20 slots against 45 of the library's log1pf).
+// what rounding s = 1 + u loses; s - 1 is exact, and the division is left out: where s is not next to 1 the
+// term is below a step of the result.  The hardware logarithm is relative to its result near 1 too, so small
+// steps keep their relative precision.
 __device__ inline float step_f(float v) {
     const float u = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e), s = 1.f + u;
-    const float l = __builtin_amdgcn_logf(s) * 0.693147180559945309417f;
-    return fmaxf(v, 0.f) + (l + (u - (s - 1.f)) * __builtin_amdgcn_rcpf(s));
+    return fmaxf(v, 0.f) + (__builtin_amdgcn_logf(s) * 0.693147180559945309417f + (u - (s - 1.f)));
 }
 
 // softplus'(v)
 __device__ inline float sigmoid_f(float v) { return __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
+
+// The kernel's own arguments, read again from the kernarg segment (scalar loads that hit the cache).  Within a
+// tile loop this keeps the two dozen pointers and strides from being held in scalar registers all along, which
+// costs more in spills to vector lanes than the loads do.
+__device__ inline const ScanArgs& args_again() {
+    typedef const __attribute__((address_space(4))) ScanArgs* Ptr;
+    Ptr p = (Ptr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const ScanArgs*)p;
+}
 
 // Where a workgroup stands.
 struct ScanPlace {

@@ -173,7 +173,7 @@ SSD_EXPORT ssd_status_t ssd_causal_conv_step(const ssd_conv_params_t* p, const v
 namespace {
 
 constexpr int kScanTile = 16;  // tokens of a forward tile
-constexpr int64_t kMaxRowBC = (int64_t)1 << 24;  // elements between rows of B and C
+constexpr int64_t kMaxRow = (int64_t)1 << 24;  // elements between rows
 
 ssd_status_t validate_scan(const ssd_scan_params_t* p, bool step) {
     if (!p) return SSD_ERR_NULL_POINTER;
@@ -189,8 +189,10 @@ ssd_status_t validate_scan(const ssd_scan_params_t* p, bool step) {
     if (!stride_ok(p->x_stride, p->channels) || !stride_ok(p->dt_stride, p->channels) ||
         !stride_ok(p->z_stride, p->channels) || !stride_ok(p->B_stride, gn) || !stride_ok(p->C_stride, gn))
         return SSD_ERR_INVALID_SHAPE;
-    // rows of B and C are read four bytes at a time, at 32-bit offsets within a tile
-    if (p->B_stride >= kMaxRowBC || p->C_stride >= kMaxRowBC || gn >= kMaxRowBC) return SSD_ERR_INVALID_SHAPE;
+    // a tile's rows are accessed at 32-bit offsets, those of B and C four bytes at a time
+    if (p->x_stride >= kMaxRow || p->dt_stride >= kMaxRow || p->z_stride >= kMaxRow || p->B_stride >= kMaxRow ||
+        p->C_stride >= kMaxRow || p->channels >= kMaxRow || gn >= kMaxRow)
+        return SSD_ERR_INVALID_SHAPE;
     if (p->in_dtype != SSD_F32 && (p->B_stride % 2 || p->C_stride % 2)) return SSD_ERR_MISALIGNED;
     // rows, channels and workgroups have to fit 32-bit indexes
     if ((int64_t)p->batch * p->seqlen >= kMaxIndex || (int64_t)p->channels * N >= kMaxIndex)
