@@ -517,8 +517,7 @@ typedef struct {
  *   out           [B, L, D]     in_dtype    required, contiguous
  *   final_state   [S, D, N]     state_dtype NULL: not wanted; 16-byte aligned
  *   saved         bytes         -           NULL, or ssd_selective_scan_saved_size() bytes, 16-byte aligned:
- *                                           states kept for the backward pass (fp32, one every 16 tokens;
- *                                           8 for N = 64)
+ *                                           states kept for the backward pass (fp32, one every 8 tokens)
  *   workspace     bytes         -           required, 256-byte aligned,
  *                                           ssd_selective_scan_workspace_size() bytes
  * initial_state and final_state must not overlap. */

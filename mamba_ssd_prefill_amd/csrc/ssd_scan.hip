@@ -19,14 +19,15 @@ template <typename T, int TPW, bool Z> struct ScanTokens {
     T x[TPW], dt[TPW], z[Z ? TPW : 1];
     __device__ inline void load(const ScanArgs& a, const ScanPlace& p, int t0, int w, int nw) {
         const uint32_t lo = (uint32_t)p.c * (uint32_t)sizeof(T);
-        const TileRows<T> rx(a.x, a.xs, p.row0, t0, a.seqlen), rd(a.dt, a.dts, p.row0, t0, a.seqlen);
+        const TileRows<T, kTile> rx(a.x, a.xs, p.row0, t0, a.seqlen);
+        const TileRows<T, kTile> rd(a.dt, a.dts, p.row0, t0, a.seqlen);
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             x[j] = rx.load(w + j * nw, lo);
             dt[j] = rd.load(w + j * nw, lo);
         }
         if (Z && a.z) {
-            const TileRows<T> rz(a.z, a.zs, p.row0, t0, a.seqlen);
+            const TileRows<T, kTile> rz(a.z, a.zs, p.row0, t0, a.seqlen);
 #pragma unroll
             for (int j = 0; j < TPW; ++j) z[j] = rz.load(w + j * nw, lo);
         }
@@ -38,7 +39,7 @@ template <typename T, int TPW, bool Z> struct ScanTokens {
 template <typename T, int NW, int NS, bool VL>
 __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
     constexpr int TPW = kTile / NW;    // tokens a wave prepares and finishes
-    constexpr int N = NW * NS, PERIOD = scan_period(N);
+    constexpr int N = NW * NS, PERIOD = kScanPeriod;
     typedef ScalarRows<T, NS> Rows;
     constexpr int GT = Rows::GROUP;
     __shared__ f32x2 s_d[kTile][64];   // (d, d x)
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
             }
         }
         __syncthreads();
-        const TileRows<T> ro(a.out, a.channels, p.row0, t0, a.seqlen);
+        const TileRows<T, kTile> ro(a.out, a.channels, p.row0, t0, a.seqlen);
         const uint32_t lo = p.live ? (uint32_t)p.c * (uint32_t)sizeof(T) : kNoLane;
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
@@ -273,7 +274,7 @@ constexpr int64_t kSplitBlocks = 2048;  // workgroups that fill the chip's 1024 
 // are only as many as it takes to give every SIMD of the chip work, and none shorter than 2 tiles.
 int scan_splits(int64_t batch, int64_t seqlen, int64_t channels, int groups, int dstate, bool backward) {
     const int64_t dg = channels / groups, blocks = batch * groups * ((dg + 63) / 64);
-    const int64_t tile = backward ? scan_period(dstate) : kTile, tiles = (seqlen + tile - 1) / tile;
+    const int64_t tile = backward ? kScanPeriod : kTile, tiles = (seqlen + tile - 1) / tile;
     int64_t s = std::min(kSplitBlocks / blocks, tiles / 2);
     if (s < 2) return 1;
     const int64_t per = (tiles + s - 1) / s;

@@ -6,23 +6,25 @@
 //     q[n]  = g[n] exp(d A[n]) h[n] of token t-1
 //     dx = D dy + d sum_n g[n] B[n],   dd = x sum_n g[n] B[n] + sum_n A[n] q[n],   dA[n] = sum_t d q[n]
 //
-// A tile of 64 / NS tokens is taken at a time, from the last to the first: the states of the tile are
-// computed again from the saved state that enters it and kept in registers with their decays (64 of each a
-// lane), and then the gradients run back through them.  The tile's dB and dC are 64 values a wave, each
-// a sum over its 64 lanes, so that after the sums lane l holds one value of each.
+// A tile of 8 tokens is taken at a time, from the last to the first: the states of the tile are computed again
+// from the saved state that enters it and kept in registers with their decays, and then the gradients run
+// back through them.  Tiles of 16 tokens (half the saved states) needed twice the registers and LDS, and with
+// two waves a SIMD instead of four the vector ALU waited: 360 us against XXX us at 2 x 2048 x 5120, N = 16.
 #include "ssd_scan_common.h"
 
 namespace ssd {
 
-// Sums 64 values over the wave's 64 lanes so that each lane ends with one total.  Two values at a time, a
-// lane keeps the half of the lanes' sum of one and hands its part of the other across: 63 exchanges
-// and additions in all, where 64 sums by themselves would take 384.  Values come in order of their index; at
+// Sums V values (32 or 64) over the wave's 64 lanes so that each lane ends with one total.  Two values at a time,
+// a lane keeps the half of the lanes' sum of one and hands its part of the other across: V - 1 exchanges
+// and additions in all, where V sums by themselves would take 6 V.  Values come in order of their index; at
 // most six sums wait for their partner.  Lane l ends with the value whose index is l's bits in the order
-// 3, 2, 1, 0, 5, 4 (the exchanges within 16 lanes ride on the addition, so they come first).
+// 3, 2, 1, 0, 5, 4 (the exchanges within 16 lanes ride on the addition, so they come first); of 32
+// values, lanes l and l ^ 16 hold the same.
 template <int CTRL> __device__ inline float dpp(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
-struct WaveSum64 {
+template <int V> struct WaveSum {
+    static_assert(V == 32 || V == 64, "five or six exchanges");
     float wait[6];
     template <int LEVEL> __device__ static inline float join(float x, float y) {
         const int lane = threadIdx.x & 63;
@@ -53,13 +55,13 @@ struct WaveSum64 {
         v = join<3>(wait[3], v);
         if (!(i & 16)) { wait[4] = v; return; }
         v = join<4>(wait[4], v);
-        if (!(i & 32)) { wait[5] = v; return; }
-        wait[0] = join<5>(wait[5], v);
+        if (V == 64 && !(i & 32)) { wait[5] = v; return; }
+        wait[0] = join<5>(V == 64 ? wait[5] : v, v);
     }
     __device__ inline float total() const { return wait[0]; }
     __device__ static inline int index(int lane) {
         return (lane >> 3 & 1) | (lane >> 2 & 1) << 1 | (lane >> 1 & 1) << 2 | (lane & 1) << 3 | (lane >> 5 & 1) << 4 |
-               (lane >> 4 & 1) << 5;
+               (V == 64 ? (lane >> 4 & 1) << 5 : 0);
     }
 };
 
@@ -68,8 +70,9 @@ template <typename T, int TPW> struct BackTokens {
     T x[TPW], dt[TPW], z[TPW], g[TPW];
     __device__ inline void load(const ScanArgs& a, const ScanPlace& p, int t0, int w, int nw) {
         const uint32_t lo = (uint32_t)p.c * (uint32_t)sizeof(T);
-        const TileRows<T> rx(a.x, a.xs, p.row0, t0, a.seqlen), rd(a.dt, a.dts, p.row0, t0, a.seqlen);
-        const TileRows<T> rg(a.dout, a.channels, p.row0, t0, a.seqlen);
+        const TileRows<T, kScanPeriod> rx(a.x, a.xs, p.row0, t0, a.seqlen);
+        const TileRows<T, kScanPeriod> rd(a.dt, a.dts, p.row0, t0, a.seqlen);
+        const TileRows<T, kScanPeriod> rg(a.dout, a.channels, p.row0, t0, a.seqlen);
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             x[j] = rx.load(w + j * nw, lo);
@@ -77,7 +80,7 @@ template <typename T, int TPW> struct BackTokens {
             g[j] = rg.load(w + j * nw, lo);
         }
         if (a.z) {
-            const TileRows<T> rz(a.z, a.zs, p.row0, t0, a.seqlen);
+            const TileRows<T, kScanPeriod> rz(a.z, a.zs, p.row0, t0, a.seqlen);
 #pragma unroll
             for (int j = 0; j < TPW; ++j) z[j] = rz.load(w + j * nw, lo);
         }
@@ -85,13 +88,12 @@ template <typename T, int TPW> struct BackTokens {
 };
 
 template <typename T, int NW, int NS, bool VL>
-__global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs args) {
+__global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(ScanArgs args) {
     const ScanArgs& a = args;
-    constexpr int TB = 64 / NS;   // tokens of a tile
+    constexpr int TB = kScanPeriod;  // tokens of a tile: a saved state enters each
     constexpr int TPW = TB / NW;  // tokens a wave prepares and finishes
     static_assert(TPW >= 1, "every wave has a token of each tile");
     constexpr int N = NW * NS;
-    static_assert(TB == scan_period(N), "a saved state enters each tile");
     typedef ScalarRows<T, NS> Rows;
     constexpr int GT = Rows::GROUP;
     __shared__ f32x2 s_d[TB][64];  // (d, d x)
@@ -115,8 +117,9 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs args) {
         load_states<NS>(a.split_state, DT_F32, ((int64_t)p.b * a.nsplit + p.split) * sstride + soff, g);
     else if (!VL && a.dfin)
         load_states<NS>(a.dfin, a.state_dtype, p.b * sstride + soff, g);
-    // this wave's sums over the channels, lane l holding token `pk`, state `pi` of a tile
-    const int pidx = WaveSum64::index(lane), pk = TB - 1 - pidx / NS, pi = pidx % NS;
+    // this wave's sums over the channels: lane l holds that of token `pk`, state `pi` of a tile
+    typedef WaveSum<TB * NS> Sum;
+    const int pidx = Sum::index(lane), pk = TB - 1 - pidx / NS, pi = pidx % NS;
     float* part = a.part_bc + (((int64_t)p.b * a.groups + p.g) * a.cblk + p.cblk) * a.seqlen * N + n0 + pi;
     const int64_t part_c = (int64_t)a.batch * a.groups * a.cblk * a.seqlen * N;
 
@@ -180,7 +183,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs args) {
             s_y[w][k][lane] = y;
         }
         // and the gradients back through them
-        WaveSum64 sb, sc;
+        Sum sb, sc;
         float dAt[NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) dAt[i] = 0.f;
@@ -239,15 +242,16 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs args) {
         // a tile's sums first, then the tiles': long sums keep their low bits
 #pragma unroll
         for (int i = 0; i < NS; ++i) dA[i] += dAt[i];
-        if (t0 + pk < a.seqlen) {
+        if (t0 + pk < a.seqlen && (TB * NS == 64 || !(lane & 16))) {
             part[(int64_t)(t0 + pk) * N] = sb.total();
             part[part_c + (int64_t)(t0 + pk) * N] = sc.total();
         }
         __syncthreads();
         float dDt = 0.f, dbt = 0.f;
         const ScanArgs& a2 = args_again();
-        const TileRows<T> rx(a2.dx, a2.channels, p.row0, t0, a2.seqlen), rd(a2.ddt, a2.channels, p.row0, t0, a2.seqlen);
-        const TileRows<T> rz(a2.dz, a2.channels, p.row0, t0, a2.seqlen);
+        const TileRows<T, kScanPeriod> rx(a2.dx, a2.channels, p.row0, t0, a2.seqlen);
+        const TileRows<T, kScanPeriod> rd(a2.ddt, a2.channels, p.row0, t0, a2.seqlen);
+        const TileRows<T, kScanPeriod> rz(a2.dz, a2.channels, p.row0, t0, a2.seqlen);
         const uint32_t lo = p.live ? (uint32_t)p.c * (uint32_t)sizeof(T) : kNoLane;
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
@@ -297,7 +301,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_scan_backward(ScanArgs args) {
 // split but the first, from a zero gradient behind it (into the split before's place), and the sum of its steps.
 template <typename T, int NW, int NS, bool VL>
 __global__ __launch_bounds__(NW * 64) void k_scan_backward_carry(ScanArgs a) {
-    constexpr int TB = 64 / NS, TPW = TB / NW, N = NW * NS;
+    constexpr int TB = kScanPeriod, TPW = TB / NW, N = NW * NS;
     typedef ScalarRows<T, NS> Rows;
     constexpr int GT = Rows::GROUP;
     __shared__ f32x2 s_d[2][TB][64];  // (d, dy), one tile ahead
@@ -322,14 +326,15 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward_carry(ScanArgs a) {
     T dt[TPW], z[TPW], go[TPW];
     auto load = [&](int t0) {
         const uint32_t lo = (uint32_t)p.c * (uint32_t)sizeof(T);
-        const TileRows<T> rd(a.dt, a.dts, p.row0, t0, a.seqlen), rg(a.dout, a.channels, p.row0, t0, a.seqlen);
+        const TileRows<T, kScanPeriod> rd(a.dt, a.dts, p.row0, t0, a.seqlen);
+        const TileRows<T, kScanPeriod> rg(a.dout, a.channels, p.row0, t0, a.seqlen);
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             dt[j] = rd.load(w + j * NW, lo);
             go[j] = rg.load(w + j * NW, lo);
         }
         if (a.z) {
-            const TileRows<T> rz(a.z, a.zs, p.row0, t0, a.seqlen);
+            const TileRows<T, kScanPeriod> rz(a.z, a.zs, p.row0, t0, a.seqlen);
 #pragma unroll
             for (int j = 0; j < TPW; ++j) z[j] = rz.load(w + j * NW, lo);
         }

@@ -26,8 +26,8 @@ template <typename T, int NS> struct ScalarRows {
     uint32_t stride;
     int last;  // rows past the end read the last one
     __device__ inline ScalarRows(const T* rows, int64_t row_stride, int64_t row0, int t0, int seqlen) {
-        base = (ScalarPtr)(uintptr_t)(rows + (row0 + t0) * row_stride);
         stride = (uint32_t)row_stride * (uint32_t)sizeof(T);
+        base = (ScalarPtr)((uintptr_t)rows + (uint64_t)(uint32_t)(row0 + t0) * stride);
         last = seqlen - 1 - t0;
     }
     struct Group {
@@ -66,15 +66,16 @@ template <typename T, int NS> struct ScalarRows {
 
 // The rows of one tensor for a tile of tokens, as a buffer that ends with the batch row: loads of tokens past
 // the end give zeros, stores to them (and from lanes without a channel) are dropped, and an access
-// takes one 32-bit offset.  Rows are below 2^24 elements apart, so a tile's offsets stay below 2^31.
-template <typename T> struct TileRows {
+// takes one 32-bit offset.  Rows are below 2^24 elements apart and there are below 2^31 of them, so a tile's
+// offsets stay below 2^31 and its start is one 32 x 32 bit product.
+template <typename T, int TOKENS> struct TileRows {
     __amdgpu_buffer_rsrc_t rsrc;
     uint32_t stride;
+    // TOKENS rows from token t0 of a batch row (t0 < 0: none)
     __device__ inline TileRows(const void* base, int64_t row_stride, int64_t row0, int t0, int seqlen) {
         stride = (uint32_t)row_stride * (uint32_t)sizeof(T);
-        const int64_t left = t0 < 0 ? 0 : (int64_t)(seqlen - t0) * stride;
-        rsrc = make_rsrc((const T*)base + (row0 + t0) * row_stride,
-                         (uint32_t)(left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : left));
+        const int n = t0 < 0 ? 0 : max(0, min(seqlen - t0, TOKENS));
+        rsrc = make_rsrc((const char*)base + (uint64_t)(uint32_t)(row0 + max(t0, 0)) * stride, (uint32_t)n * stride);
     }
     __device__ inline T load(int k, uint32_t lane_off) const {
         const int off = (int)(lane_off + (uint32_t)k * stride);

@@ -53,7 +53,7 @@ struct ScanArgs {
     const void* h0;
     void* out;
     void* fin;
-    float* saved;  // [batch][tiles][channels][dstate]: the state entering each tile of scan_period() tokens
+    float* saved;  // [batch][tiles][channels][dstate]: the state entering each tile of kScanPeriod tokens
     // backward
     const void* dout;
     const void* dfin;
@@ -76,7 +76,7 @@ struct ScanArgs {
 };
 
 // Tokens between two saved states.
-__host__ __device__ constexpr int scan_period(int dstate) { return dstate == 64 ? 8 : 16; }
+constexpr int kScanPeriod = 8;
 
 // Time splits of the forward and the backward: a function of the sizes alone, so that workspaces
 // can be sized without a device.

@@ -231,8 +231,7 @@ ssd::ScanArgs scan_args(const ssd_scan_params_t* p, const void* x, const void* d
     a.zs = p->z_stride ? p->z_stride : D_;
     a.Bs = p->B_stride ? p->B_stride : gn;
     a.Cs = p->C_stride ? p->C_stride : gn;
-    const int period = ssd::scan_period(p->dstate);
-    a.ntiles = (p->seqlen + period - 1) / period;
+    a.ntiles = (p->seqlen + ssd::kScanPeriod - 1) / ssd::kScanPeriod;
     return a;
 }
 
@@ -289,8 +288,7 @@ SSD_EXPORT size_t ssd_selective_scan_backward_workspace_size(const ssd_scan_para
 
 SSD_EXPORT size_t ssd_selective_scan_saved_size(const ssd_scan_params_t* p) {
     if (validate_scan(p, false) != SSD_OK) return 0;
-    const int period = ssd::scan_period(p->dstate);
-    return (size_t)p->batch * ((p->seqlen + period - 1) / period) * p->channels * p->dstate * 4;
+    return (size_t)p->batch * ((p->seqlen + ssd::kScanPeriod - 1) / ssd::kScanPeriod) * p->channels * p->dstate * 4;
 }
 
 SSD_EXPORT ssd_status_t ssd_selective_scan(const ssd_scan_params_t* p, const void* x, const void* dt, const float* A,

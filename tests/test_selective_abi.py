@@ -172,7 +172,7 @@ def test_workspaces(lib):
         assert n > 0 and n % 256 == 0
         assert call(lib, name, p, ws_bytes=n - 1) == WS_SMALL
         assert size(ctypes.byref(params_for(name, batch=0))) == 0 and size(None) == 0
-    assert lib.ssd_selective_scan_saved_size(ctypes.byref(scan_prm(seqlen=33))) == 2 * 3 * 64 * 16 * 4
+    assert lib.ssd_selective_scan_saved_size(ctypes.byref(scan_prm(seqlen=33))) == 2 * 5 * 64 * 16 * 4
     assert lib.ssd_selective_scan_saved_size(ctypes.byref(scan_prm(seqlen=33, dstate=64))) == 2 * 5 * 64 * 64 * 4
     assert lib.ssd_selective_scan_saved_size(ctypes.byref(scan_prm(dstate=24))) == 0
 
