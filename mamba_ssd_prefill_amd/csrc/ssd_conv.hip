@@ -9,6 +9,7 @@
 // consecutive lanes take consecutive channels.
 #include "ssd_device.h"
 #include "ssd_select.h"
+#include "ssd_sum_rows.h"
 
 namespace ssd {
 
@@ -70,7 +71,7 @@ template <int W, int CW> struct ConvW {
 
 // Walks one sequence after another down a batch row: the number of the sequence holding the
 // current token, its place in it (counted up to W-1), and the W-1 inputs before it.
-template <typename T, int W, int CW> struct ConvWalk {
+template <typename T, int W, int CW, bool VL> struct ConvWalk {
     const CausalConvArgs& a;
     const int b, c0;
     const int32_t* seq;
@@ -78,10 +79,10 @@ template <typename T, int W, int CW> struct ConvWalk {
     float win[W - 1][CW];
 
     __device__ inline ConvWalk(const CausalConvArgs& a_, int b_, int c0_) : a(a_), b(b_), c0(c0_) {
-        seq = a.seq ? a.seq + (int64_t)b * a.seqlen : nullptr;
+        seq = VL ? a.seq + (int64_t)b * a.seqlen : nullptr;
     }
     __device__ inline const T* row(int t) const { return (const T*)a.x + ((int64_t)b * a.seqlen + t) * a.xs + c0; }
-    __device__ inline bool has_state(int n) const { return n >= 0 && n < (seq ? a.nseq : a.batch); }
+    __device__ inline bool has_state(int n) const { return n >= 0 && n < (VL ? a.nseq : a.batch); }
     // the window before a sequence's first token, shifted by `done` inputs already taken
     __device__ inline void load_state(int done) {
 #pragma unroll
@@ -96,9 +97,9 @@ template <typename T, int W, int CW> struct ConvWalk {
     }
     // stand before token t
     __device__ inline void start(int t) {
-        q = seq ? seq[t] : b;
+        q = VL ? seq[t] : b;
         place = 0;
-        while (place < W - 1 && t - place > 0 && (!seq || seq[t - place - 1] == q)) ++place;
+        while (place < W - 1 && t - place > 0 && (!VL || seq[t - place - 1] == q)) ++place;
         load_state(place);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)  // the inputs of this sequence before t
@@ -106,7 +107,7 @@ template <typename T, int W, int CW> struct ConvWalk {
     }
     // arrive at token t from t - 1
     __device__ inline void step_to(int t) {
-        if (seq && seq[t] != q) {
+        if (VL && seq[t] != q) {
             q = seq[t];
             place = 0;
             load_state(0);
@@ -130,21 +131,25 @@ template <typename T, int W, int CW> struct ConvWalk {
         for (int e = 0; e < CW; ++e) win[W - 2][e] = cur[e];
         if (place < W) ++place;
     }
-    __device__ inline bool last(int t) const { return t == a.seqlen - 1 || (seq && seq[t + 1] != q); }
+    __device__ inline bool last(int t) const { return t == a.seqlen - 1 || (VL && seq[t + 1] != q); }
 };
 
-template <typename T, int W, int CW> __global__ __launch_bounds__(256) void k_causal_conv(CausalConvArgs a) {
+template <typename T, int W, int CW, bool VL> __global__ __launch_bounds__(256) void k_causal_conv(CausalConvArgs a) {
     ConvItem it;
     if (!conv_item<CW>(a, &it)) return;
     ConvW<W, CW> k;
     k.load(a, it.c0);
-    ConvWalk<T, W, CW> s(a, it.b, it.c0);
+    ConvWalk<T, W, CW, VL> s(a, it.b, it.c0);
     s.start(it.t0);
     T* out = split_ptr<T>(a.out, a.split_a, a.split_b, a.channels, it.c0, (int64_t)it.b * a.seqlen + it.t0);
     const int os = it.c0 < a.split_a ? a.split_a : it.c0 < a.split_b ? a.split_b - a.split_a : a.channels - a.split_b;
+    float next[CW];
+    load_cw<T, CW>(s.row(it.t0), next);
     for (int t = it.t0; t < it.t1; ++t, out += os) {
         float cur[CW], pre[CW];
-        load_cw<T, CW>(s.row(t), cur);
+#pragma unroll
+        for (int e = 0; e < CW; ++e) cur[e] = next[e];
+        load_cw<T, CW>(s.row(min(t + 1, it.t1 - 1)), next);  // a row ahead
         s.step_to(t);
         s.taps(k, cur, pre);
         if (a.silu) {
@@ -173,12 +178,13 @@ __device__ inline float dsilu_f(float v) {
 // One pass over a run of tokens and the W-1 tokens behind it: dpre of a token completes dx of the token
 // W-1 before it.  A lane's sums of dw and dbias over its own tokens go to `part` (one row per
 // segment), summed by k_conv_sums in a fixed order.
-template <typename T, int W, int CW> __global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) {
+template <typename T, int W, int CW, bool VL>
+__global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) {
     ConvItem it;
     if (!conv_item<CW>(a, &it)) return;
     ConvW<W, CW> k;
     k.load(a, it.c0);
-    ConvWalk<T, W, CW> s(a, it.b, it.c0);
+    ConvWalk<T, W, CW, VL> s(a, it.b, it.c0);
     s.start(it.t0);
     const int64_t row0 = (int64_t)it.b * a.seqlen;
     const T* dout = split_ptr<T>((void* const*)a.dout, a.split_a, a.split_b, a.channels, it.c0, row0 + it.t0);
@@ -189,12 +195,23 @@ template <typename T, int W, int CW> __global__ __launch_bounds__(256) void k_ca
     // gradients of the initial state, at a sequence's first tokens
     float dh[W - 1][CW] = {};
     const int end = min(it.t1 + W - 1, a.seqlen);
-    for (int t = it.t0; t < it.t1 + W - 1; ++t, dout += os) {
+    float xnext[CW], gnext[CW];
+    load_cw<T, CW>(s.row(it.t0), xnext);
+    load_cw<T, CW>(dout, gnext);
+    for (int t = it.t0; t < it.t1 + W - 1; ++t) {
         float here[CW] = {};
         if (t < end) {
             float cur[CW], pre[CW], g[CW];
-            load_cw<T, CW>(s.row(t), cur);
-            load_cw<T, CW>(dout, g);
+#pragma unroll
+            for (int e = 0; e < CW; ++e) {
+                cur[e] = xnext[e];
+                g[e] = gnext[e];
+            }
+            if (t + 1 < end) {  // a row ahead
+                dout += os;
+                load_cw<T, CW>(s.row(t + 1), xnext);
+                load_cw<T, CW>(dout, gnext);
+            }
             s.step_to(t);
             s.taps(k, cur, pre);
             if (a.silu) {
@@ -216,7 +233,7 @@ template <typename T, int W, int CW> __global__ __launch_bounds__(256) void k_ca
             // acc[j] belongs to token t - (W-1) + j, which tap j of t reads if it is in t's sequence
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
-                if (W - 1 - j <= place) {
+                if (!VL || W - 1 - j <= place) {
 #pragma unroll
                     for (int e = 0; e < CW; ++e) acc[j][e] += k.w[j][e] * g[e];
                 }
@@ -290,13 +307,13 @@ template <typename T, int W, int CW> __global__ __launch_bounds__(256) void k_ca
     }
 }
 
-// dw [channels][W] and dbias [channels] from the rows of `part`.
+// dw [channels][W] and dbias [channels] from the rows of `part`, 64 values a workgroup.
 template <int W> __global__ __launch_bounds__(256) void k_conv_sums(const float* part, int nrows, int channels,
                                                                      float* dw, float* db) {
-    const int64_t n = (int64_t)channels * (W + 1), i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    float s = 0.f;
-    for (int r = 0; r < nrows; ++r) s += part[r * n + i];
+    __shared__ float lds[256];
+    const int64_t n = (int64_t)channels * (W + 1), i = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    const float s = sum_rows<float>(part + i, n, nrows, lds, i < n);
+    if (i >= n || threadIdx.x >= 64) return;
     const int c = (int)(i / (W + 1)), j = (int)(i % (W + 1));
     if (j < W)
         dw[(int64_t)c * W + j] = s;
@@ -334,7 +351,7 @@ template <typename T, int W> __global__ __launch_bounds__(256) void k_causal_con
 
 constexpr int kConvForwardRows = 16;  // tokens per lane of the forward
 
-int conv_backward_rows(int64_t batch, int64_t seqlen, int64_t channels) { return 16; }
+int conv_backward_rows(int64_t batch, int64_t seqlen, int64_t channels) { return 32; }
 
 // Whether lanes can take four channels with one access: every row they touch starts on a
 // multiple of four elements.
@@ -352,8 +369,9 @@ template <typename T, int W> hipError_t launch_conv_tw(CausalConvArgs& a, hipStr
     const bool v4 = conv_vec4(a, sizeof(T), a.out, 3);
     const int64_t items = (int64_t)a.batch * a.nseg * (a.channels / (v4 ? 4 : 1));
     void* args[] = {&a};
-    return hipLaunchKernel(v4 ? (const void*)&k_causal_conv<T, W, 4> : (const void*)&k_causal_conv<T, W, 1>,
-                           dim3((unsigned)((items + 255) / 256)), dim3(256), args, 0, st);
+    const void* fn = a.seq ? (v4 ? (const void*)&k_causal_conv<T, W, 4, true> : (const void*)&k_causal_conv<T, W, 1, true>)
+                           : (v4 ? (const void*)&k_causal_conv<T, W, 4, false> : (const void*)&k_causal_conv<T, W, 1, false>);
+    return hipLaunchKernel(fn, dim3((unsigned)((items + 255) / 256)), dim3(256), args, 0, st);
 }
 
 template <typename T, int W> hipError_t launch_conv_back_tw(CausalConvArgs& a, float* dw, float* db, hipStream_t st) {
@@ -363,14 +381,16 @@ template <typename T, int W> hipError_t launch_conv_back_tw(CausalConvArgs& a, f
     const bool v4 = conv_vec4(a, sizeof(T), tens, 4);
     const int64_t items = (int64_t)a.batch * a.nseg * (a.channels / (v4 ? 4 : 1));
     void* args[] = {&a};
-    hipError_t e = hipLaunchKernel(
-        v4 ? (const void*)&k_causal_conv_backward<T, W, 4> : (const void*)&k_causal_conv_backward<T, W, 1>,
-        dim3((unsigned)((items + 255) / 256)), dim3(256), args, 0, st);
+    const void* fn = a.seq ? (v4 ? (const void*)&k_causal_conv_backward<T, W, 4, true>
+                                 : (const void*)&k_causal_conv_backward<T, W, 1, true>)
+                           : (v4 ? (const void*)&k_causal_conv_backward<T, W, 4, false>
+                                 : (const void*)&k_causal_conv_backward<T, W, 1, false>);
+    hipError_t e = hipLaunchKernel(fn, dim3((unsigned)((items + 255) / 256)), dim3(256), args, 0, st);
     if (e != hipSuccess) return e;
     int nrows = a.batch * a.nseg;
     const int64_t n = (int64_t)a.channels * (W + 1);
     void* sargs[] = {&a.part, &nrows, &a.channels, &dw, &db};
-    return hipLaunchKernel((const void*)&k_conv_sums<W>, dim3((unsigned)((n + 255) / 256)), dim3(256), sargs, 0, st);
+    return hipLaunchKernel((const void*)&k_conv_sums<W>, dim3((unsigned)((n + 63) / 64)), dim3(256), sargs, 0, st);
 }
 
 template <typename T, int W> hipError_t launch_conv_step_tw(CausalConvArgs& a, hipStream_t st) {

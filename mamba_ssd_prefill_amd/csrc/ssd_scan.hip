@@ -220,12 +220,8 @@ __global__ __launch_bounds__(256) void k_scan_join(ScanArgs a) {
     }
     float* st = a.split_state + (int64_t)b * a.nsplit * per + cn;
     const float* sum = a.split_sum + (int64_t)b * a.nsplit * a.channels + c;
-#pragma unroll 8
-    for (int s = 1; s < a.nsplit; ++s) {
-        const float d = sum[(int64_t)(s - 1) * a.channels], own = st[s * per];
-        h = d == __builtin_inff() ? own : __builtin_amdgcn_exp2f(d * A2) * h + own;
-        st[s * per] = h;
-    }
+    join_splits(A2, h, a.nsplit - 1, [&](int k) { return sum[(int64_t)k * a.channels]; },
+                [&](int k) { return st + (k + 1) * per; });
 }
 
 // One token: N / 4 lanes hold a channel's states, four each, and share the sum over n.

@@ -11,6 +11,7 @@
 // back through them.  Tiles of 16 tokens (half the saved states) needed twice the registers and LDS, and with
 // two waves a SIMD instead of four the vector ALU waited: 360 us against XXX us at 2 x 2048 x 5120, N = 16.
 #include "ssd_scan_common.h"
+#include "ssd_sum_rows.h"
 
 namespace ssd {
 
@@ -391,66 +392,52 @@ __global__ __launch_bounds__(256) void k_scan_backward_join(ScanArgs a) {
     const int b = (int)(i / per);
     const int64_t cn = i % per;
     const int c = (int)(cn / a.dstate);
-    const float A2 = a.A[cn] * kLog2e;
     float* st = a.split_state + (int64_t)b * a.nsplit * per + cn;
     const float* sum = a.split_sum + (int64_t)b * a.nsplit * a.channels + c;
-    float g = st[(a.nsplit - 2) * per];  // the last split's own pass began with the final state's gradient
-#pragma unroll 8
-    for (int s = a.nsplit - 3; s >= 0; --s) {
-        const float d = sum[(int64_t)(s + 1) * a.channels], own = st[s * per];
-        g = d == __builtin_inff() ? own : __builtin_amdgcn_exp2f(d * A2) * g + own;
-        st[s * per] = g;
-    }
+    // the last split's own pass began with the final state's gradient
+    join_splits(a.A[cn] * kLog2e, st[(a.nsplit - 2) * per], a.nsplit - 2,
+                [&](int k) { return sum[(int64_t)(a.nsplit - 2 - k) * a.channels]; },
+                [&](int k) { return st + (a.nsplit - 3 - k) * per; });
 }
 
-// dB and dC from the channel blocks' sums: out[b][t][g][n] = sum over cblk blocks.
+// The results from the partial sums.  The first `nbc` workgroups: dB and dC from the channel blocks' sums
+// (out[b][t][g][n] = sum over cblk blocks), 64 runs of 4 values each; the others: dA, dD and ddt_bias from the rows
+// of (batch row, split).
 template <typename T>
-__global__ __launch_bounds__(256) void k_scan_sum_bc(const float* part, int batch, int seqlen, int groups, int cblk, int N,
-                                                     T* dB, T* dC) {
-    const int64_t total = (int64_t)batch * seqlen * groups * N;
-    int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= 2 * total) return;
-    const bool c = i >= total;
-    if (c) i -= total;
-    const int n = (int)(i % N);
-    const int64_t r = i / N;
-    const int g = (int)(r % groups);
-    const int64_t row = r / groups;
-    const int t = (int)(row % seqlen);
-    const int64_t b = row / seqlen;
-    const int64_t stride = (int64_t)seqlen * N;
-    const float* src = part + (c ? (int64_t)batch * groups * cblk * stride : 0) + (b * groups + g) * cblk * stride +
-                       (int64_t)t * N + n;
-    f32x4 s = *(const f32x4*)src;
-    for (int k = 1; k < cblk; ++k) s += *(const f32x4*)(src + k * stride);
-    *(typename TT<T>::v4*)((c ? dC : dB) + i) = cvt4<T>(s);
-}
-
-// dA, dD and ddt_bias from the rows of the partial sums.
-__global__ __launch_bounds__(256) void k_scan_sum_params(const float* part_a, const float* part_d, int rows, int channels,
-                                                         int N, float* dA, float* dD, float* db) {
-    const int64_t na = (int64_t)channels * N, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const float* src;
-    float* dst;
-    int64_t stride;
-    if (i < na) {
-        src = part_a + i;
-        dst = dA + i;
-        stride = na;
-    } else {
-        const int64_t j = i - na;
-        if (j >= 2 * (int64_t)channels) return;
-        const bool second = j >= channels;
-        const int64_t c = second ? j - channels : j;
-        float* out = second ? db : dD;
-        if (!out) return;
-        src = part_d + (second ? (int64_t)rows * channels : 0) + c;
-        dst = out + c;
-        stride = channels;
+__global__ __launch_bounds__(256) void k_scan_sums(ScanArgs a, int nbc, T* dB, T* dC, float* dA, float* dD, float* db) {
+    __shared__ f32x4 lds[256];
+    const int lane = threadIdx.x & 63;
+    const int N = a.dstate;
+    if ((int)blockIdx.x < nbc) {
+        const int64_t total = (int64_t)a.batch * a.seqlen * a.groups * N;
+        int64_t i = ((int64_t)blockIdx.x * 64 + lane) * 4;
+        const bool live = i < 2 * total, second = i >= total;
+        if (second) i -= total;
+        if (!live) i = 0;
+        const int n = (int)(i % N);
+        const int64_t r = i / N, row = r / a.groups, b = row / a.seqlen;
+        const int g = (int)(r % a.groups), t = (int)(row % a.seqlen);
+        const int64_t stride = (int64_t)a.seqlen * N;
+        const float* src = a.part_bc + (second ? (int64_t)a.batch * a.groups * a.cblk * stride : 0) +
+                           (b * a.groups + g) * a.cblk * stride + (int64_t)t * N + n;
+        const f32x4 s = sum_rows<f32x4>(src, stride, a.cblk, lds, live);
+        if (live && threadIdx.x < 64) *(typename TT<T>::v4*)((second ? dC : dB) + i) = cvt4<T>(s);
+        return;
     }
-    float s = 0.f;
-    for (int r = 0; r < rows; ++r) s += src[r * stride];
-    *dst = s;
+    const int64_t na = (int64_t)a.channels * N, i = (int64_t)(blockIdx.x - nbc) * 64 + lane;
+    const int rows = a.batch * a.nsplit;
+    const bool live = i < na + 2 * a.channels, second = i >= na + a.channels;
+    const float* src = a.part_a + i;
+    float* dst = dA + i;
+    int64_t stride = na;
+    if (i >= na) {
+        const int64_t c = i - na - (second ? a.channels : 0);
+        src = a.part_d + (second ? (int64_t)rows * a.channels : 0) + c;
+        dst = (second ? db : dD) ? (second ? db : dD) + c : nullptr;
+        stride = a.channels;
+    }
+    const float s = sum_rows<float>(src, stride, rows, (float*)lds, live);
+    if (live && dst && threadIdx.x < 64) *dst = s;
 }
 
 template <typename T, int NW, int NS>
@@ -470,14 +457,11 @@ hipError_t launch_scan_backward_n(ScanArgs& a, T* dB, T* dC, float* dA, float* d
     const void* fn = a.seq ? (const void*)&k_scan_backward<T, NW, NS, true> : (const void*)&k_scan_backward<T, NW, NS, false>;
     e = hipLaunchKernel(fn, dim3(blocks * a.nsplit), dim3(NW * 64), args, 0, st);
     if (e != hipSuccess) return e;
-    const int64_t quads = (int64_t)a.batch * a.seqlen * a.groups * a.dstate / 2;  // both tensors, 4 values a lane
-    void* bargs[] = {&a.part_bc, &a.batch, &a.seqlen, &a.groups, &a.cblk, &a.dstate, &dB, &dC};
-    e = hipLaunchKernel((const void*)&k_scan_sum_bc<T>, dim3((unsigned)((quads + 255) / 256)), dim3(256), bargs, 0, st);
-    if (e != hipSuccess) return e;
-    int rows = a.batch * a.nsplit;
-    const int64_t items = (int64_t)a.channels * (a.dstate + 2);
-    void* pargs[] = {&a.part_a, &a.part_d, &rows, &a.channels, &a.dstate, &dA, &dD, &db};
-    return hipLaunchKernel((const void*)&k_scan_sum_params, dim3((unsigned)((items + 255) / 256)), dim3(256), pargs, 0, st);
+    // both tensors, 64 runs of 4 values a workgroup; 64 parameters a workgroup
+    int nbc = (int)(((int64_t)a.batch * a.seqlen * a.groups * a.dstate / 2 + 63) / 64);
+    const int np = (int)(((int64_t)a.channels * (a.dstate + 2) + 63) / 64);
+    void* sargs[] = {&a, &nbc, &dB, &dC, &dA, &dD, &db};
+    return hipLaunchKernel((const void*)&k_scan_sums<T>, dim3((unsigned)(nbc + np)), dim3(256), sargs, 0, st);
 }
 
 template <typename T>

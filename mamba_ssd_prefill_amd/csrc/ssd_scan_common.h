@@ -189,6 +189,28 @@ template <int T> __device__ inline SeqMasks seq_masks(const ScanArgs& a, int64_t
     return SeqMasks{(uint32_t)__ballot(s), (uint32_t)__ballot(e)};
 }
 
+// Carries v through `n` time splits in order, v = decay(k) v + *place(k), and leaves it in their places.  step(k) is
+// the sum of steps that v decays by on the way (infinite: nothing passes).  Eight splits' values are
+// loaded together, so that the chain waits for one load in eight.
+template <typename Step, typename Place>
+__device__ inline void join_splits(float A2, float v, int n, Step step, Place place) {
+    for (int k0 = 0; k0 < n; k0 += 8) {
+        float own[8], d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int k = min(k0 + j, n - 1);
+            own[j] = *place(k);
+            d[j] = step(k);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (k0 + j >= n) break;
+            v = d[j] == __builtin_inff() ? own[j] : __builtin_amdgcn_exp2f(d[j] * A2) * v + own[j];
+            *place(k0 + j) = v;
+        }
+    }
+}
+
 __device__ inline bool state_number(const ScanArgs& a, int q) { return q >= 0 && q < a.nseq; }
 
 }  // namespace ssd

@@ -199,7 +199,7 @@ ssd_status_t validate_scan(const ssd_scan_params_t* p, bool step) {
         return SSD_ERR_INVALID_SHAPE;
     const int64_t blocks = (int64_t)p->batch * p->ngroups * ((p->channels / p->ngroups + 63) / 64);
     if (blocks >= kMaxIndex / 256 || (int64_t)p->batch * p->channels * (N / 4) / 256 >= kMaxIndex / 2 ||
-        (int64_t)p->batch * p->seqlen * gn >= kMaxIndex * 128)
+        (int64_t)p->batch * p->seqlen * gn >= kMaxIndex * 64)
         return SSD_ERR_INVALID_SHAPE;
     return SSD_OK;
 }
