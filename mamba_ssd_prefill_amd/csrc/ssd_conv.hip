@@ -13,12 +13,16 @@
 
 namespace ssd {
 
-// CW elements at p (4: one 8- or 16-byte access).
+// CW elements at p, in one access.
 template <typename T, int CW> __device__ inline void load_cw(const T* p, float (&v)[CW]) {
     if constexpr (CW == 4) {
         const typename TT<T>::v4 r = *(const typename TT<T>::v4*)p;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = (float)r[e];
+    } else if constexpr (CW == 2) {
+        const typename TT<T>::v2 r = *(const typename TT<T>::v2*)p;
+        v[0] = (float)r[0];
+        v[1] = (float)r[1];
     } else {
         v[0] = (float)*p;
     }
@@ -29,6 +33,8 @@ template <typename T, int CW> __device__ inline void store_cw(T* p, const float 
 #pragma unroll
         for (int e = 0; e < 4; ++e) r[e] = (T)v[e];
         *(typename TT<T>::v4*)p = r;
+    } else if constexpr (CW == 2) {
+        *(typename TT<T>::v2*)p = typename TT<T>::v2{(T)v[0], (T)v[1]};
     } else {
         *p = (T)v[0];
     }
@@ -75,7 +81,7 @@ template <typename T, int W, int CW, bool VL> struct ConvWalk {
     const CausalConvArgs& a;
     const int b, c0;
     const int32_t* seq;
-    int q, place;
+    int q, place, qn, qnn;  // qn, qnn: the numbers of the next token and of the one after it
     float win[W - 1][CW];
 
     __device__ inline ConvWalk(const CausalConvArgs& a_, int b_, int c0_) : a(a_), b(b_), c0(c0_) {
@@ -98,6 +104,10 @@ template <typename T, int W, int CW, bool VL> struct ConvWalk {
     // stand before token t
     __device__ inline void start(int t) {
         q = VL ? seq[t] : b;
+        if (VL) {
+            qn = q;
+            qnn = seq[min(t + 1, a.seqlen - 1)];
+        }
         place = 0;
         while (place < W - 1 && t - place > 0 && (!VL || seq[t - place - 1] == q)) ++place;
         load_state(place);
@@ -105,12 +115,16 @@ template <typename T, int W, int CW, bool VL> struct ConvWalk {
         for (int j = 0; j < W - 1; ++j)  // the inputs of this sequence before t
             if (W - 1 - j <= place) load_cw<T, CW>(row(t - (W - 1) + j), win[j]);
     }
-    // arrive at token t from t - 1
+    // begin with token t, coming from t - 1 (or from start(t))
     __device__ inline void step_to(int t) {
-        if (VL && seq[t] != q) {
-            q = seq[t];
-            place = 0;
-            load_state(0);
+        if constexpr (VL) {
+            if (qn != q) {
+                q = qn;
+                place = 0;
+                load_state(0);
+            }
+            qn = qnn;
+            qnn = seq[min(t + 2, a.seqlen - 1)];  // loaded two tokens ahead, like the inputs
         }
     }
     __device__ inline void taps(const ConvW<W, CW>& k, const float (&cur)[CW], float (&pre)[CW]) const {
@@ -131,8 +145,10 @@ template <typename T, int W, int CW, bool VL> struct ConvWalk {
         for (int e = 0; e < CW; ++e) win[W - 2][e] = cur[e];
         if (place < W) ++place;
     }
-    __device__ inline bool last(int t) const { return t == a.seqlen - 1 || (VL && seq[t + 1] != q); }
+    __device__ inline bool last(int t) const { return t == a.seqlen - 1 || (VL && qn != q); }
 };
+
+constexpr int kConvAhead = 4;
 
 template <typename T, int W, int CW, bool VL> __global__ __launch_bounds__(256) void k_causal_conv(CausalConvArgs a) {
     ConvItem it;
@@ -143,13 +159,20 @@ template <typename T, int W, int CW, bool VL> __global__ __launch_bounds__(256) 
     s.start(it.t0);
     T* out = split_ptr<T>(a.out, a.split_a, a.split_b, a.channels, it.c0, (int64_t)it.b * a.seqlen + it.t0);
     const int os = it.c0 < a.split_a ? a.split_a : it.c0 < a.split_b ? a.split_b - a.split_a : a.channels - a.split_b;
-    float next[CW];
-    load_cw<T, CW>(s.row(it.t0), next);
+    // kConvAhead rows on their way while one is used
+    float next[kConvAhead][CW];
+#pragma unroll
+    for (int i = 0; i < kConvAhead; ++i) load_cw<T, CW>(s.row(min(it.t0 + i, it.t1 - 1)), next[i]);
+#pragma unroll 4
     for (int t = it.t0; t < it.t1; ++t, out += os) {
         float cur[CW], pre[CW];
 #pragma unroll
-        for (int e = 0; e < CW; ++e) cur[e] = next[e];
-        load_cw<T, CW>(s.row(min(t + 1, it.t1 - 1)), next);  // a row ahead
+        for (int e = 0; e < CW; ++e) {
+            cur[e] = next[0][e];
+#pragma unroll
+            for (int i = 0; i + 1 < kConvAhead; ++i) next[i][e] = next[i + 1][e];
+        }
+        load_cw<T, CW>(s.row(min(t + kConvAhead, it.t1 - 1)), next[kConvAhead - 1]);
         s.step_to(t);
         s.taps(k, cur, pre);
         if (a.silu) {
@@ -178,7 +201,7 @@ __device__ inline float dsilu_f(float v) {
 // One pass over a run of tokens and the W-1 tokens behind it: dpre of a token completes dx of the token
 // W-1 before it.  A lane's sums of dw and dbias over its own tokens go to `part` (one row per
 // segment), summed by k_conv_sums in a fixed order.
-template <typename T, int W, int CW, bool VL>
+template <typename T, int W, int CW, bool VL, bool ST>
 __global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) {
     ConvItem it;
     if (!conv_item<CW>(a, &it)) return;
@@ -241,7 +264,7 @@ __global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) 
             const bool last = s.last(t);
             // the initial state: tap j of the token at place p reads its column p + j while that is below W-1;
             // the lane that holds the sequence's first token sums and stores it
-            const bool head = a.dh0 && place <= W - 2 && t - place >= it.t0 && t - place < it.t1 && s.has_state(s.q);
+            const bool head = ST && a.dh0 && place <= W - 2 && t - place >= it.t0 && t - place < it.t1 && s.has_state(s.q);
             if (head) {
 #pragma unroll
                 for (int c = 0; c < W - 1; ++c) {
@@ -254,7 +277,7 @@ __global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) 
                     }
                 }
             }
-            if (a.dfin && last && s.has_state(s.q)) {
+            if (ST && a.dfin && last && s.has_state(s.q)) {
                 // column j of the final state is the input of token t - (W-2) + j, if it is in the sequence
                 const T* df = (const T*)a.dfin + ((int64_t)s.q * a.channels + it.c0) * (W - 1);
 #pragma unroll
@@ -374,17 +397,25 @@ template <typename T, int W> hipError_t launch_conv_tw(CausalConvArgs& a, hipStr
     return hipLaunchKernel(fn, dim3((unsigned)((items + 255) / 256)), dim3(256), args, 0, st);
 }
 
+// Channels a lane of the backward takes where rows allow it.
+constexpr int kConvBackwardWide = 2;
+
+template <typename T, int W, int CW> const void* conv_backward_kernel(bool packed, bool states) {
+    if (packed) return (const void*)&k_causal_conv_backward<T, W, CW, true, true>;
+    return states ? (const void*)&k_causal_conv_backward<T, W, CW, false, true>
+                  : (const void*)&k_causal_conv_backward<T, W, CW, false, false>;
+}
+
 template <typename T, int W> hipError_t launch_conv_back_tw(CausalConvArgs& a, float* dw, float* db, hipStream_t st) {
     a.rows = conv_backward_rows(a.batch, a.seqlen, a.channels);
     a.nseg = (a.seqlen + a.rows - 1) / a.rows;
     const void* tens[4] = {a.dout[0], a.dout[1], a.dout[2], a.dx};
     const bool v4 = conv_vec4(a, sizeof(T), tens, 4);
-    const int64_t items = (int64_t)a.batch * a.nseg * (a.channels / (v4 ? 4 : 1));
+    const int64_t items = (int64_t)a.batch * a.nseg * (a.channels / (v4 ? kConvBackwardWide : 1));
     void* args[] = {&a};
-    const void* fn = a.seq ? (v4 ? (const void*)&k_causal_conv_backward<T, W, 4, true>
-                                 : (const void*)&k_causal_conv_backward<T, W, 1, true>)
-                           : (v4 ? (const void*)&k_causal_conv_backward<T, W, 4, false>
-                                 : (const void*)&k_causal_conv_backward<T, W, 1, false>);
+    const bool states = a.dh0 || a.dfin;
+    const void* fn = v4 ? conv_backward_kernel<T, W, kConvBackwardWide>(a.seq, states)
+                        : conv_backward_kernel<T, W, 1>(a.seq, states);
     hipError_t e = hipLaunchKernel(fn, dim3((unsigned)((items + 255) / 256)), dim3(256), args, 0, st);
     if (e != hipSuccess) return e;
     int nrows = a.batch * a.nseg;

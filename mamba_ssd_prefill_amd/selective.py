@@ -80,21 +80,69 @@ def declare(lib):
 
 
 # ---- helpers -------------------------------------------------------------------------------------
+# A call's checks depend on its arguments' shapes, strides, types and devices alone, so their outcome -- a plan: the
+# parameter block, the output shapes, the workspace size -- is kept under those and found again in a few
+# microseconds.  Nothing is kept about a tensor's identity or contents.
+_PLANS = {}
+_MAX_PLANS = 512
+
+
+class _Plan:
+    __slots__ = ("prm", "ref", "fn", "name", "dev", "index", "dtype", "state_dtype", "shape", "parts", "state", "sizes")
+
+    def __init__(self, name, prm, dev, dtype, state_dtype=None, shape=None, parts=None, state=None, sizes=()):
+        self.prm, self.ref, self.name, self.dev = prm, ctypes.byref(prm), name, dev
+        self.fn, self.index = getattr(load_library(), name), dev.index
+        self.dtype, self.state_dtype, self.shape, self.parts, self.state = dtype, state_dtype, shape, parts, state
+        self.sizes = [_size(s, prm) for s in sizes]
+
+    def call(self, *args):
+        """One C call on the current stream of the tensors' device, with that device current."""
+        import torch
+        if self.index is None or self.index == torch.cuda.current_device():
+            rc = self.fn(self.ref, *args, _stream(self.dev))
+        else:
+            with torch.cuda.device(self.dev):
+                rc = self.fn(self.ref, *args, _stream(self.dev))
+        if rc:
+            raise SSDError(rc, self.name)
+
+
+def _stream(dev):
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same handle without a Stream object
+    return raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _new(shape, dtype, dev):
+    """A new contiguous tensor (torch.empty by the shorter way)."""
+    import torch
+    strides, n = [], 1
+    for d in reversed(shape):
+        strides.append(n)
+        n *= d
+    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=dev)
+
+
+def _keep(key, plan):
+    if len(_PLANS) >= _MAX_PLANS:
+        _PLANS.clear()
+    _PLANS[key] = plan
+    return plan
+
+
+def _m(t):
+    """What a plan depends on of a tensor that has to be contiguous."""
+    return None if t is None else (t.shape, t.dtype, t.device, t.is_contiguous())
+
+
+def _mr(t):
+    """What a plan depends on of a tensor whose rows may be views."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
-
-
-def _call(name, prm, dev, *args):
-    """One C call on the current stream of `dev`, with that device current."""
-    import torch
-    fn = getattr(load_library(), name)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        rc = fn(ctypes.byref(prm), *args, torch.cuda.current_stream(dev).cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(ctypes.byref(prm), *args, torch.cuda.current_stream(dev).cuda_stream)
-    if rc:
-        raise SSDError(rc, name)
 
 
 def _size(name, prm):
@@ -185,13 +233,20 @@ def _seq(seq_idx, nseq, lead, dev):
     return int(nseq)
 
 
-def _workspace(workspace, n, dev):
+def _space(workspace, n, dev):
+    """The workspace given (the library checks its size), or n new bytes."""
     import torch
     if workspace is None:
-        return torch.empty(n, dtype=torch.uint8, device=dev)
+        return _new((n,), torch.uint8, dev)
     if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on %s" % dev)
     return workspace
+
+
+def _states(packed, shape, dtype, dev):
+    """A new state output; entries of numbers that no sequence uses stay zero."""
+    import torch
+    return torch.zeros(shape, dtype=dtype, device=dev) if packed else _new(shape, dtype, dev)
 
 
 # ---- causal convolution ----------------------------------------------------------------------------
@@ -222,24 +277,45 @@ def _three(ts):
     return [_p(t) for t in ts] + [None] * (3 - len(ts))
 
 
+def _conv_plan(name, sizes, x, weight, bias, activation, seq_idx, nseq, splits, states, douts=()):
+    lead = tuple(x.shape[:2])
+    S = _seq(seq_idx, nseq, lead, x.device)
+    prm, dev, parts = _conv_params(x, weight, bias, activation, splits, S, lead)
+    state = (S, prm.channels, prm.width - 1)
+    for n, t in states.items():
+        _same(dev, x.dtype, **{n: (t, state)})
+    if douts and len(douts) != len(parts):
+        raise ValueError("dout must have one tensor per split")
+    for d, n in zip(douts, parts):
+        _same(dev, x.dtype, dout=(d, lead + (n,)))
+    return _Plan(name, prm, dev, x.dtype, shape=tuple(x.shape), parts=[lead + (n,) for n in parts], state=state, sizes=sizes)
+
+
+def _outs(plan):
+    """New outputs, one per split, and the three pointers the library takes."""
+    if len(plan.parts) == 1:
+        o = _new(plan.parts[0], plan.dtype, plan.dev)
+        return (o,), (o.data_ptr(), None, None)
+    outs = tuple([_new(s, plan.dtype, plan.dev) for s in plan.parts])
+    return outs, _three(outs)
+
+
 def causal_conv(x, weight, bias=None, *, activation="silu", seq_idx=None, nseq=None, initial_state=None, splits=None,
                 with_final_state=True, final_state=None):
     """ssd_causal_conv: the causal depthwise convolution of x [B, L, Ch] with weight [Ch, W] float32 (W = 2, 3
     or 4), bias [Ch] and an optional SiLU (``activation`` None or "silu").  Returns (out, final_state);
     ``splits`` (up to three channel counts) makes ``out`` a tuple of contiguous tensors, e.g. the x, B and C
     of an SSD block.  States [B or nseq, Ch, W-1] hold the inputs before (after) a sequence, oldest first."""
-    import torch
-    lead = tuple(x.shape[:2])
-    S = _seq(seq_idx, nseq, lead, x.device)
-    prm, dev, parts = _conv_params(x, weight, bias, activation, splits, S, lead)
-    shape = (S, prm.channels, prm.width - 1)
-    _same(dev, x.dtype, initial_state=(initial_state, shape), final_state=(final_state, shape))
-    outs = tuple(torch.empty(lead + (n,), dtype=x.dtype, device=dev) for n in parts)
+    splits = splits if splits is None else tuple(splits)
+    key = ("conv", _mr(x), _m(weight), _m(bias), _m(seq_idx), _m(initial_state), _m(final_state), activation, nseq, splits)
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _keep(key, _conv_plan("ssd_causal_conv", (), x, weight, bias, activation, seq_idx, nseq, splits,
+                                     dict(initial_state=initial_state, final_state=final_state)))
+    outs, ptrs = _outs(plan)
     if final_state is None and with_final_state:
-        # numbers that no sequence uses keep their entry
-        final_state = (torch.empty if seq_idx is None else torch.zeros)(shape, dtype=x.dtype, device=dev)
-    _call("ssd_causal_conv", prm, dev, _p(x), _p(weight), _p(bias), _p(seq_idx), _p(initial_state), *_three(outs),
-          _p(final_state))
+        final_state = _states(seq_idx is not None, plan.state, plan.dtype, plan.dev)
+    plan.call(x.data_ptr(), weight.data_ptr(), _p(bias), _p(seq_idx), _p(initial_state), *ptrs, _p(final_state))
     return (outs[0] if splits is None else outs), final_state
 
 
@@ -249,32 +325,26 @@ def causal_conv_backward(dout, x, weight, bias=None, *, activation="silu", seq_i
     its output (a tuple with ``splits``) and, if given, of its final state.  dbias and dinitial_state are None
     where bias and initial_state are."""
     import torch
-    lead = tuple(x.shape[:2])
-    S = _seq(seq_idx, nseq, lead, x.device)
-    prm, dev, parts = _conv_params(x, weight, bias, activation, splits, S, lead)
-    shape = (S, prm.channels, prm.width - 1)
+    splits = splits if splits is None else tuple(splits)
     douts = (dout,) if splits is None else tuple(dout)
-    if len(douts) != len(parts):
-        raise ValueError("dout must have one tensor per split")
-    for d, n in zip(douts, parts):
-        _same(dev, x.dtype, dout=(d, lead + (n,)))
-    _same(dev, x.dtype, initial_state=(initial_state, shape), dfinal_state=(dfinal_state, shape))
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    key = ("conv backward", _mr(x), _m(weight), _m(bias), _m(seq_idx), _m(initial_state), _m(dfinal_state), activation,
+           nseq, splits, *[_m(d) for d in douts])
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _keep(key, _conv_plan("ssd_causal_conv_backward", ("ssd_causal_conv_backward_workspace_size",), x, weight,
+                                     bias, activation, seq_idx, nseq, splits,
+                                     dict(initial_state=initial_state, dfinal_state=dfinal_state), douts))
+    dx = _new(plan.shape, plan.dtype, plan.dev)
     dw = torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
-    dh = None
-    if initial_state is not None:
-        dh = (torch.empty if seq_idx is None else torch.zeros)(shape, dtype=x.dtype, device=dev)
-    workspace = _workspace(workspace, _size("ssd_causal_conv_backward_workspace_size", prm), dev)
-    _call("ssd_causal_conv_backward", prm, dev, *_three(douts), _p(dfinal_state), _p(x), _p(weight), _p(bias),
-          _p(seq_idx), _p(initial_state), _p(dx), _p(dw), _p(db), _p(dh), _p(workspace), workspace.numel())
+    dh = None if initial_state is None else _states(seq_idx is not None, plan.state, plan.dtype, plan.dev)
+    workspace = _space(workspace, plan.sizes[0], plan.dev)
+    plan.call(*_three(douts), _p(dfinal_state), x.data_ptr(), weight.data_ptr(), _p(bias), _p(seq_idx), _p(initial_state),
+              dx.data_ptr(), dw.data_ptr(), _p(db), _p(dh), workspace.data_ptr(), workspace.numel())
     return ConvGrads(dx, dw, db, dh)
 
 
-def causal_conv_step(x, weight, bias=None, *, state, activation="silu", slots=None, splits=None):
-    """ssd_causal_conv_step: one token x [B, Ch] per row.  ``state`` [nslots, Ch, W-1] moves on in place; row b
-    uses state ``slots[b]`` (int32; None: state b).  A row whose slot is not in [0, nslots) touches no
-    state and returns zeros.  Returns out (a tuple with ``splits``)."""
+def _conv_step_plan(x, weight, bias, activation, splits, state, slots):
     import torch
     lead = tuple(x.shape[:1])
     if state.dim() != 3:
@@ -282,8 +352,20 @@ def causal_conv_step(x, weight, bias=None, *, state, activation="silu", slots=No
     prm, dev, parts = _conv_params(x, weight, bias, activation, splits, state.shape[0], lead)
     _same(dev, x.dtype, state=(state, (state.shape[0], prm.channels, prm.width - 1)))
     _same(dev, torch.int32, slots=(slots, lead))
-    outs = tuple(torch.empty(lead + (n,), dtype=x.dtype, device=dev) for n in parts)
-    _call("ssd_causal_conv_step", prm, dev, _p(x), _p(weight), _p(bias), _p(state), _p(slots), *_three(outs))
+    return _Plan("ssd_causal_conv_step", prm, dev, x.dtype, parts=[lead + (n,) for n in parts])
+
+
+def causal_conv_step(x, weight, bias=None, *, state, activation="silu", slots=None, splits=None):
+    """ssd_causal_conv_step: one token x [B, Ch] per row.  ``state`` [nslots, Ch, W-1] moves on in place; row b
+    uses state ``slots[b]`` (int32; None: state b).  A row whose slot is not in [0, nslots) touches no
+    state and returns zeros.  Returns out (a tuple with ``splits``)."""
+    splits = splits if splits is None else tuple(splits)
+    key = ("conv step", _mr(x), _m(weight), _m(bias), _m(state), _m(slots), activation, splits)
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _keep(key, _conv_step_plan(x, weight, bias, activation, splits, state, slots))
+    outs, ptrs = _outs(plan)
+    plan.call(x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(), _p(slots), *ptrs)
     return outs[0] if splits is None else outs
 
 
@@ -304,6 +386,22 @@ def _scan_params(x, dt, A, B, C, D, dt_bias, z, dt_softplus, state_code, nseq, l
                       rows("B", B, (G, N)), rows("C", C, (G, N))), dev
 
 
+def _scan_plan(name, sizes, x, dt, A, B, C, D, dt_bias, z, dt_softplus, seq_idx, nseq, state_dtype, states, like_x):
+    lead = tuple(x.shape[:2])
+    S = _seq(seq_idx, nseq, lead, x.device)
+    if state_dtype is None:
+        import torch
+        given = [t for t in states.values() if t is not None]
+        state_dtype = given[0].dtype if given else torch.float32
+    prm, dev = _scan_params(x, dt, A, B, C, D, dt_bias, z, dt_softplus, _state_code(state_dtype), S, lead)
+    state = (S, prm.channels, prm.dstate)
+    for n, t in states.items():
+        _same(dev, state_dtype, **{n: (t, state)})
+    for n, t in like_x.items():
+        _same(dev, x.dtype, **{n: (t, x.shape)})
+    return _Plan(name, prm, dev, x.dtype, state_dtype, tuple(x.shape), state=state, sizes=sizes)
+
+
 def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=True, seq_idx=None, nseq=None,
                    initial_state=None, state_dtype=None, save_for_backward=False, with_final_state=True,
                    final_state=None, out=None, workspace=None):
@@ -311,24 +409,22 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
     float32.  Returns (out [B, L, D], final_state [B or nseq, D, N]), and with ``save_for_backward`` a third
     tensor for selective_scan_backward.  ``state_dtype`` defaults to initial_state's, else float32."""
     import torch
-    lead = tuple(x.shape[:2])
-    S = _seq(seq_idx, nseq, lead, x.device)
-    if state_dtype is None:
-        state_dtype = initial_state.dtype if initial_state is not None else torch.float32
-    prm, dev = _scan_params(x, dt, A, B, C, D, dt_bias, z, dt_softplus, _state_code(state_dtype), S, lead)
-    shape = (S, prm.channels, prm.dstate)
-    _same(dev, state_dtype, initial_state=(initial_state, shape), final_state=(final_state, shape))
-    _same(dev, x.dtype, out=(out, x.shape))
+    key = ("scan", _mr(x), _mr(dt), _m(A), _mr(B), _mr(C), _m(D), _m(dt_bias), _mr(z), _m(seq_idx), _m(initial_state),
+           _m(final_state), _m(out), dt_softplus, nseq, state_dtype)
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _keep(key, _scan_plan("ssd_selective_scan", ("ssd_selective_scan_workspace_size",
+                                                            "ssd_selective_scan_saved_size"),
+                                     x, dt, A, B, C, D, dt_bias, z, dt_softplus, seq_idx, nseq, state_dtype,
+                                     dict(initial_state=initial_state, final_state=final_state), dict(out=out)))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = _new(plan.shape, plan.dtype, plan.dev)
     if final_state is None and with_final_state:
-        final_state = (torch.empty if seq_idx is None else torch.zeros)(shape, dtype=state_dtype, device=dev)
-    workspace = _workspace(workspace, _size("ssd_selective_scan_workspace_size", prm), dev)
-    saved = None
-    if save_for_backward:
-        saved = torch.empty(_size("ssd_selective_scan_saved_size", prm), dtype=torch.uint8, device=dev)
-    _call("ssd_selective_scan", prm, dev, _p(x), _p(dt), _p(A), _p(B), _p(C), _p(D), _p(dt_bias), _p(z), _p(seq_idx),
-          _p(initial_state), _p(out), _p(final_state), _p(saved), _p(workspace), workspace.numel())
+        final_state = _states(seq_idx is not None, plan.state, plan.state_dtype, plan.dev)
+    workspace = _space(workspace, plan.sizes[0], plan.dev)
+    saved = _new((plan.sizes[1],), torch.uint8, plan.dev) if save_for_backward else None
+    plan.call(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(dt_bias), _p(z), _p(seq_idx),
+              _p(initial_state), out.data_ptr(), _p(final_state), _p(saved), workspace.data_ptr(), workspace.numel())
     return (out, final_state, saved) if save_for_backward else (out, final_state)
 
 
@@ -338,31 +434,28 @@ def selective_scan_backward(dout, x, dt, A, B, C, D=None, dt_bias=None, z=None, 
     forward's inputs and the ``saved`` tensor it returned.  ddt is the gradient of the raw dt.  dD, ddt_bias,
     dz and dinitial_state are None where the input is."""
     import torch
-    lead = tuple(x.shape[:2])
-    S = _seq(seq_idx, nseq, lead, x.device)
-    if state_dtype is None:
-        given = [t for t in (initial_state, dfinal_state) if t is not None]
-        state_dtype = given[0].dtype if given else torch.float32
-    prm, dev = _scan_params(x, dt, A, B, C, D, dt_bias, z, dt_softplus, _state_code(state_dtype), S, lead)
-    shape = (S, prm.channels, prm.dstate)
-    _same(dev, state_dtype, initial_state=(initial_state, shape), dfinal_state=(dfinal_state, shape))
-    _same(dev, x.dtype, dout=(dout, x.shape))
-    _same(dev, torch.uint8, saved=(saved, (_size("ssd_selective_scan_saved_size", prm),)))
-    like = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)  # noqa: E731
+    key = ("scan backward", _mr(x), _mr(dt), _m(A), _mr(B), _mr(C), _m(D), _m(dt_bias), _mr(z), _m(seq_idx),
+           _m(initial_state), _m(dfinal_state), _m(dout), _m(saved), dt_softplus, nseq, state_dtype)
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _scan_plan("ssd_selective_scan_backward", ("ssd_selective_scan_backward_workspace_size",
+                                                          "ssd_selective_scan_saved_size"),
+                          x, dt, A, B, C, D, dt_bias, z, dt_softplus, seq_idx, nseq, state_dtype,
+                          dict(initial_state=initial_state, dfinal_state=dfinal_state), dict(dout=dout))
+        _same(plan.dev, torch.uint8, saved=(saved, (plan.sizes[1],)))
+        _keep(key, plan)
+    like = lambda t: None if t is None else _new(t.shape, t.dtype, plan.dev)  # noqa: E731
     g = ScanGrads(like(x), like(dt), like(A), like(B), like(C), like(D), like(dt_bias), like(z),
-                  None if initial_state is None else
-                  (torch.empty if seq_idx is None else torch.zeros)(shape, dtype=state_dtype, device=dev))
-    workspace = _workspace(workspace, _size("ssd_selective_scan_backward_workspace_size", prm), dev)
-    _call("ssd_selective_scan_backward", prm, dev, _p(dout), _p(dfinal_state), _p(x), _p(dt), _p(A), _p(B), _p(C), _p(D),
-          _p(dt_bias), _p(z), _p(seq_idx), _p(initial_state), _p(saved), _p(g.dx), _p(g.ddt), _p(g.dA), _p(g.dB),
-          _p(g.dC), _p(g.dD), _p(g.ddt_bias), _p(g.dz), _p(g.dinitial_state), _p(workspace), workspace.numel())
+                  None if initial_state is None else _states(seq_idx is not None, plan.state, plan.state_dtype, plan.dev))
+    workspace = _space(workspace, plan.sizes[0], plan.dev)
+    plan.call(dout.data_ptr(), _p(dfinal_state), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D),
+              _p(dt_bias), _p(z), _p(seq_idx), _p(initial_state), saved.data_ptr(), g.dx.data_ptr(), g.ddt.data_ptr(),
+              g.dA.data_ptr(), g.dB.data_ptr(), g.dC.data_ptr(), _p(g.dD), _p(g.ddt_bias), _p(g.dz), _p(g.dinitial_state),
+              workspace.data_ptr(), workspace.numel())
     return g
 
 
-def selective_scan_step(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, state, slots=None, dt_softplus=True, out=None):
-    """ssd_selective_scan_step: one token per row; x, dt, z [B, D], B, C [B, G, N].  ``state`` [nslots, D, N] is
-    updated in place; row b uses state ``slots[b]`` (int32; None: state b).  A row whose slot is not in
-    [0, nslots) touches no state and returns zeros.  Returns out [B, D]."""
+def _scan_step_plan(x, dt, A, B, C, D, dt_bias, z, state, slots, dt_softplus, out):
     import torch
     lead = tuple(x.shape[:1])
     if state.dim() != 3:
@@ -371,10 +464,22 @@ def selective_scan_step(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, state, 
     _same(dev, state.dtype, state=(state, (state.shape[0], prm.channels, prm.dstate)))
     _same(dev, torch.int32, slots=(slots, lead))
     _same(dev, x.dtype, out=(out, x.shape))
+    return _Plan("ssd_selective_scan_step", prm, dev, x.dtype, shape=tuple(x.shape))
+
+
+def selective_scan_step(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, state, slots=None, dt_softplus=True, out=None):
+    """ssd_selective_scan_step: one token per row; x, dt, z [B, D], B, C [B, G, N].  ``state`` [nslots, D, N] is
+    updated in place; row b uses state ``slots[b]`` (int32; None: state b).  A row whose slot is not in
+    [0, nslots) touches no state and returns zeros.  Returns out [B, D]."""
+    key = ("scan step", _mr(x), _mr(dt), _m(A), _mr(B), _mr(C), _m(D), _m(dt_bias), _mr(z), _m(state), _m(slots), _m(out),
+           dt_softplus)
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _keep(key, _scan_step_plan(x, dt, A, B, C, D, dt_bias, z, state, slots, dt_softplus, out))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _call("ssd_selective_scan_step", prm, dev, _p(x), _p(dt), _p(A), _p(B), _p(C), _p(D), _p(dt_bias), _p(z), _p(state),
-          _p(slots), _p(out))
+        out = _new(plan.shape, plan.dtype, plan.dev)
+    plan.call(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(dt_bias), _p(z),
+              state.data_ptr(), _p(slots), out.data_ptr())
     return out
 
 
@@ -395,7 +500,7 @@ def state_cache(nslots, shape, *, group=64, format="int8", device="cuda"):
     return codes, torch.zeros((nslots, n // group), dtype=torch.float32, device=device)
 
 
-def _cache_params(codes, scales, slots, batch, state_code):
+def _cache_plan(name, codes, scales, slots, batch, state_dtype, state):
     import torch
     dev = _on_gpu(codes, "the state cache")
     formats = {torch.int8: CACHE_INT8, torch.float8_e4m3fn: CACHE_E4M3}
@@ -404,32 +509,38 @@ def _cache_params(codes, scales, slots, batch, state_code):
     nslots, elems = codes.shape[0], codes[0].numel() if codes.shape[0] else 0
     if scales.dim() != 2 or scales.shape[0] != nslots or not scales.shape[1] or elems % scales.shape[1]:
         raise ValueError("scales must be [nslots, values / group]")
+    shape = (batch,) + tuple(codes.shape[1:])
     _same(dev, codes.dtype, codes=(codes, codes.shape))
     _same(dev, torch.float32, scales=(scales, scales.shape))
     _same(dev, torch.int32, slots=(slots, (batch,)))
-    return CacheParams(ctypes.sizeof(CacheParams), batch, nslots, elems, elems // scales.shape[1], formats[codes.dtype],
-                       state_code), dev
+    _same(dev, state_dtype, state=(state, shape))
+    prm = CacheParams(ctypes.sizeof(CacheParams), batch, nslots, elems, elems // scales.shape[1], formats[codes.dtype],
+                      _state_code(state_dtype))
+    return _Plan(name, prm, dev, state_dtype, shape=shape)
 
 
 def state_cache_write(state, codes, scales, slots=None):
     """ssd_state_cache_write: state [B, ...] (float32, float16 or bfloat16) into the slots ``slots[b]`` (int32;
     None: b) of a pool made by state_cache.  Rows whose slot is not in [0, nslots) are skipped."""
-    prm, dev = _cache_params(codes, scales, slots, state.shape[0], _state_code(state.dtype))
-    _same(dev, state.dtype, state=(state, (state.shape[0],) + tuple(codes.shape[1:])))
-    _call("ssd_state_cache_write", prm, dev, _p(state), _p(slots), _p(codes), _p(scales))
+    key = ("cache write", _m(state), _m(codes), _m(scales), _m(slots))
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _keep(key, _cache_plan("ssd_state_cache_write", codes, scales, slots, state.shape[0], state.dtype, state))
+    plan.call(state.data_ptr(), _p(slots), codes.data_ptr(), scales.data_ptr())
 
 
 def state_cache_read(codes, scales, slots=None, *, state_dtype=None, out=None):
     """ssd_state_cache_read: the states of ``slots`` (int32 [B]; None: every slot), in ``state_dtype`` (default
     float32) or into ``out`` [B, ...].  A row whose slot is not in [0, nslots) reads a zero state."""
     import torch
-    batch = codes.shape[0] if slots is None and out is None else (out if slots is None else slots).shape[0]
-    if state_dtype is None:
-        state_dtype = torch.float32 if out is None else out.dtype
-    prm, dev = _cache_params(codes, scales, slots, batch, _state_code(state_dtype))
-    shape = (batch,) + tuple(codes.shape[1:])
-    _same(dev, state_dtype, out=(out, shape))
+    key = ("cache read", _m(codes), _m(scales), _m(slots), _m(out), state_dtype)
+    plan = _PLANS.get(key)
+    if plan is None:
+        batch = codes.shape[0] if slots is None and out is None else (out if slots is None else slots).shape[0]
+        if state_dtype is None:
+            state_dtype = torch.float32 if out is None else out.dtype
+        plan = _keep(key, _cache_plan("ssd_state_cache_read", codes, scales, slots, batch, state_dtype, out))
     if out is None:
-        out = torch.empty(shape, dtype=state_dtype, device=dev)
-    _call("ssd_state_cache_read", prm, dev, _p(codes), _p(scales), _p(slots), _p(out))
+        out = _new(plan.shape, plan.dtype, plan.dev)
+    plan.call(codes.data_ptr(), scales.data_ptr(), _p(slots), out.data_ptr())
     return out
