@@ -224,46 +224,73 @@ __global__ __launch_bounds__(256) void k_scan_join(ScanArgs a) {
                 [&](int k) { return st + (k + 1) * per; });
 }
 
-// One token: N / 4 lanes hold a channel's states, four each, and share the sum over n.
-template <typename T, typename S, int N> __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a) {
-    constexpr int LPC = N / 4;  // lanes per channel
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = i / LPC;
-    const int n0 = (int)(i % LPC) * 4;
-    if (row >= (int64_t)a.batch * a.channels) return;  // whole channels: a channel's lanes stay together
-    const int b = (int)(row / a.channels), c = (int)(row % a.channels), g = c / a.dg;
-    const int slot = a.slots ? a.slots[b] : b;
-    T* out = (T*)a.out + (int64_t)b * a.channels + c;
-    if (slot < 0 || slot >= a.nseq) {
-        if (n0 == 0) *out = (T)0.f;
-        return;
-    }
-    S* st = (S*)a.pool + ((int64_t)slot * a.channels + c) * N + n0;
-    float h[4];
+// Four values of a row that starts on a multiple of four bytes.
+template <typename T> __device__ inline void load_four(const T* p, float (&v)[4]) {
+    typedef uint32_t words __attribute__((ext_vector_type(sizeof(T)), aligned(4)));
+    const words u = *(const words*)p;
+    typename TT<T>::v4 r;
+    __builtin_memcpy(&r, &u, 4 * sizeof(T));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = (float)st[j];
-    const float x = f32of(((const T*)a.x)[b * a.xs + c]);
-    const float v = f32of(((const T*)a.dt)[b * a.dts + c]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
-    const float d = a.softplus ? step_f(v) : v;
+    for (int j = 0; j < 4; ++j) v[j] = f32of(r[j]);
+}
+
+// One token: N / 4 lanes hold a channel's states, four each, and share the sum over n.  A lane takes its channel for R
+// batch rows, so that A and the channel's parameters are read once for them and their states are on their way
+// together.
+template <typename T, typename S, int N, int R> __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a) {
+    constexpr int LPC = N / 4, CPB = 256 / LPC;  // lanes per channel, channels per workgroup
+    constexpr int SD = sizeof(S) == 4 ? DT_F32 : __is_same(S, __bf16) ? DT_BF16 : DT_F16;
+    const uint32_t nb = (uint32_t)(a.channels + CPB - 1) / CPB;
+    const int b0 = (int)(blockIdx.x / nb) * R, c = (int)(blockIdx.x % nb) * CPB + (int)threadIdx.x / LPC;
+    const int n0 = (int)(threadIdx.x % LPC) * 4;
+    if (c >= a.channels) return;  // whole channels: a channel's lanes stay together
+    const int g = a.groups == 1 ? 0 : c / a.dg;
+    float h[R][4], x[R], dt[R], z[R], B[R][4], C[R][4];
+    int64_t at[R];
+    bool have[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int b = min(b0 + r, a.batch - 1);
+        const int slot = a.slots ? a.slots[b] : b;
+        have[r] = slot >= 0 && slot < a.nseq;
+        at[r] = ((int64_t)(have[r] ? slot : 0) * a.channels + c) * N + n0;
+        load_states<4>(a.pool, SD, at[r], h[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int b = min(b0 + r, a.batch - 1);
+        x[r] = f32of(((const T*)a.x)[b * a.xs + c]);
+        dt[r] = f32of(((const T*)a.dt)[b * a.dts + c]);
+        z[r] = a.z ? f32of(((const T*)a.z)[b * a.zs + c]) : 0.f;
+        load_four((const T*)a.B + b * a.Bs + g * N + n0, B[r]);
+        load_four((const T*)a.C + b * a.Cs + g * N + n0, C[r]);
+    }
     const f32x4 A = *(const f32x4*)(a.A + (int64_t)c * N + n0);
-    const T* Bp = (const T*)a.B + b * a.Bs + g * N + n0;
-    const T* Cp = (const T*)a.C + b * a.Cs + g * N + n0;
-    float y = 0.f;
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, Dc = a.D ? a.D[c] : 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        h[j] = __builtin_amdgcn_exp2f(d * (A[j] * kLog2e)) * h[j] + d * x * f32of(Bp[j]);
-        y += h[j] * f32of(Cp[j]);
-        st[j] = (S)h[j];
-    }
+    for (int r = 0; r < R; ++r) {
+        if (b0 + r >= a.batch) break;
+        const float v = dt[r] + bias, d = a.softplus ? step_f(v) : v, u = d * x[r];
+        float y = 0.f;
 #pragma unroll
-    for (int m = LPC / 2; m >= 1; m >>= 1) y += __shfl_xor(y, m, 64);
-    if (n0 == 0) {
-        if (a.D) y += a.D[c] * x;
-        if (a.z) y *= silu_f(f32of(((const T*)a.z)[b * a.zs + c]));
-        *out = (T)y;
+        for (int j = 0; j < 4; ++j) {
+            h[r][j] = __builtin_amdgcn_exp2f(d * (A[j] * kLog2e)) * h[r][j] + u * B[r][j];
+            y += h[r][j] * C[r][j];
+        }
+        if (have[r]) store_states<4>(a.pool, SD, at[r], h[r]);
+        y += dpp<0xb1>(y);  // lanes ^ 1
+        if (LPC >= 4) y += dpp<0x4e>(y);    // ^ 2
+        if (LPC >= 8) y += dpp<0x141>(y);   // the other half of 8
+        if (LPC >= 16) y += dpp<0x140>(y);  // the other half of 16
+        if (n0 == 0) {
+            y += Dc * x[r];
+            if (a.z) y *= silu_f(z[r]);
+            ((T*)a.out)[(int64_t)(b0 + r) * a.channels + c] = (T)(have[r] ? y : 0.f);
+        }
     }
 }
 
+constexpr int kStepRows = 2, kStepBlocks = 1024;
 constexpr int64_t kSplitBlocks = 2048;  // workgroups that fill the chip's 1024 SIMDs
 
 // Time splits.  A split costs a second pass over its tokens (without y) and a launch or two, so there
@@ -311,18 +338,24 @@ hipError_t launch_scan(ScanArgs& a, int in_dtype, hipStream_t st) {
     }
 }
 
+template <typename T, typename S, int N> hipError_t launch_scan_step_n(ScanArgs& a, hipStream_t st) {
+    const int64_t per_row = (a.channels + 1024 / N - 1) / (1024 / N);  // workgroups
+    // several rows a lane where that leaves enough workgroups to fill the chip
+    const bool many = per_row * (a.batch / kStepRows) >= kStepBlocks;
+    const int64_t blocks = per_row * (many ? (a.batch + kStepRows - 1) / kStepRows : a.batch);
+    void* args[] = {&a};
+    return hipLaunchKernel(many ? (const void*)&k_scan_step<T, S, N, kStepRows> : (const void*)&k_scan_step<T, S, N, 1>,
+                           dim3((unsigned)blocks), dim3(256), args, 0, st);
+}
+
 template <typename T, typename S> hipError_t launch_scan_step_ts(ScanArgs& a, hipStream_t st) {
-    const void* fn = nullptr;
     switch (a.dstate) {
-    case 8: fn = (const void*)&k_scan_step<T, S, 8>; break;
-    case 16: fn = (const void*)&k_scan_step<T, S, 16>; break;
-    case 32: fn = (const void*)&k_scan_step<T, S, 32>; break;
-    case 64: fn = (const void*)&k_scan_step<T, S, 64>; break;
+    case 8: return launch_scan_step_n<T, S, 8>(a, st);
+    case 16: return launch_scan_step_n<T, S, 16>(a, st);
+    case 32: return launch_scan_step_n<T, S, 32>(a, st);
+    case 64: return launch_scan_step_n<T, S, 64>(a, st);
     default: return hipErrorNotSupported;
     }
-    const int64_t lanes = (int64_t)a.batch * a.channels * (a.dstate / 4);
-    void* args[] = {&a};
-    return hipLaunchKernel(fn, dim3((unsigned)((lanes + 255) / 256)), dim3(256), args, 0, st);
 }
 
 template <typename T> hipError_t launch_scan_step_t(ScanArgs& a, hipStream_t st) {

@@ -21,9 +21,6 @@ namespace ssd {
 // most six sums wait for their partner.  Lane l ends with the value whose index is l's bits in the order
 // 3, 2, 1, 0, 5, 4 (the exchanges within 16 lanes ride on the addition, so they come first); of 32
 // values, lanes l and l ^ 16 hold the same.
-template <int CTRL> __device__ inline float dpp(float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
-}
 template <int V> struct WaveSum {
     static_assert(V == 32 || V == 64, "five or six exchanges");
     float wait[6];

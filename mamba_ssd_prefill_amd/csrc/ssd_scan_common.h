@@ -129,6 +129,11 @@ template <int NS> __device__ inline void store_states(void* base, int dtype, int
     }
 }
 
+// A lane exchange within 16 lanes that rides on the instruction using it.
+template <int CTRL> __device__ inline float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
 // softplus(v) = max(v, 0) + log1p(u), u = exp(-|v|).  log1p(u) = log(s) + (u - (s - 1)) / s to first order in
 // what rounding s = 1 + u loses; s - 1 is exact, and the division is left out: where s is not next to 1 the
 // term is below a step of the result.  The hardware logarithm is relative to its result near 1 too, so small

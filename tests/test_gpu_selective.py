@@ -485,6 +485,19 @@ def test_cache_special_values():
     assert bool((scales[5] == 2.0).all()) and not codes[5].any()
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_cache_quotients_below_the_fp32_range(fmt):
+    """Values so far below their group's largest that their quotient leaves fp32, of either sign, are code 0."""
+    v = torch.zeros(2, 32)
+    v[:, 0] = torch.tensor([1e30, 3e38])
+    v[:, 1:9] = torch.tensor([1e-45, -1e-45, 1e-38, -1e-38, 3e-39, -3e-39, 1e-20, -1e-20])
+    codes, scales = ssd.state_cache(2, (32,), group=16, format=fmt)
+    ssd.state_cache_write(v.cuda(), codes, scales)
+    back = ssd.state_cache_read(codes, scales).cpu()
+    torch.cuda.synchronize()
+    assert not back[:, 1:].any() and torch.equal(back, ref.cache(v, 16, fmt)[0].float())
+
+
 # ---- together ------------------------------------------------------------------------------------------------
 def layer(p, u, state=None, pos=None):
     """One selective layer's inner path on raw activations u = [x | z], as a model holds it: a joint projection's
