@@ -57,10 +57,15 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
     const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f, Dc = a.D ? a.D[p.c] : 0.f;
     const int64_t soff = (int64_t)p.c * N + n0, sstride = (int64_t)a.channels * N;
     const int tile0 = p.split * a.tiles_per_split, tile1 = min(tile0 + a.tiles_per_split, (a.seqlen + kTile - 1) / kTile);
-    if (p.split)
+    if (p.split && a.nsplit > kFoldSplits) {
         load_states<NS>(a.split_state, DT_F32, ((int64_t)p.b * a.nsplit + p.split) * sstride + soff, h);
-    else if (!VL && a.h0)
-        load_states<NS>(a.h0, a.state_dtype, p.b * sstride + soff, h);
+    } else {
+        if (!VL && a.h0) load_states<NS>(a.h0, a.state_dtype, p.b * sstride + soff, h);
+        const float* st = a.split_state + (int64_t)p.b * a.nsplit * sstride + soff;
+        const float* sum = a.split_sum + (int64_t)p.b * a.nsplit * a.channels + p.c;
+        fold_splits<NS>(A2, h, p.split, [&](int k) { return sum[(int64_t)k * a.channels]; },
+                        [&](int k) { return st + (k + 1) * sstride; });
+    }
     ScanTokens<T, TPW, true> next;
     next.load(a, p, tile0 * kTile, w, NW);
     for (int tile = tile0; tile < tile1; ++tile) {
@@ -203,7 +208,7 @@ __global__ __launch_bounds__(NW * 64) void k_scan_carry(ScanArgs a) {
     if (w == 0) a.split_sum[((int64_t)p.b * a.nsplit + p.split) * a.channels + p.c] = fresh ? __builtin_inff() : sum;
 }
 
-// Joins the splits: the state entering each, from the states that k_scan_carry left.  A lane owns one (channel, n).
+// Joins the splits where there are many: the state entering each, from the states that k_scan_carry left.  A lane owns one (channel, n).
 __global__ __launch_bounds__(256) void k_scan_join(ScanArgs a) {
     const int64_t per = (int64_t)a.channels * a.dstate, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= a.batch * per) return;
@@ -291,17 +296,47 @@ template <typename T, typename S, int N, int R> __global__ __launch_bounds__(256
 }
 
 constexpr int kStepRows = 2, kStepBlocks = 1024;
-constexpr int64_t kSplitBlocks = 2048;  // workgroups that fill the chip's 1024 SIMDs
-
-// Time splits.  A split costs a second pass over its tokens (without y) and a launch or two, so there
-// are only as many as it takes to give every SIMD of the chip work, and none shorter than 2 tiles.
+// Time splits.  A split gives the chip more waves and costs a second pass over its tokens, without the outputs.  A tile
+// takes a wave a time that its latency or, with many waves on a SIMD, their issue slots decide; the split that
+// takes the least time by that is chosen.  The constants (us, for w waves a SIMD of 4 states a lane) were fitted on
+// MI355X to 11 numbers of splits of 9 shapes from 1 x 131 x 1536 to 32 x 256 x 5120 (within 15% of the measured times
+// near the best split).  Measured, forward, no split / the split taken: 1 x 131 x 1536 23.8 / 12.2 us, 1 x 4096 x 5120
+// 711 / 143 us; 32 x 256 x 5120 151 us with none, 216 us with two.
+struct TileTime {
+    double latency, per_wave, issue;  // max(latency + per_wave * w, issue * w)
+    int resident;                     // waves a SIMD holds; more come in rounds, the last of them partly filled
+    double round(double w) const { return w > 0 ? std::max(latency + per_wave * w, issue * w) : 0; }
+    double at(double w) const {
+        if (w <= resident) return round(w);
+        const int full = (int)(w / resident);
+        const double even = round(resident) * w / resident, stepped = full * round(resident) + round(w - full * resident);
+        return even + 0.3 * (stepped - even);
+    }
+};
 int scan_splits(int64_t batch, int64_t seqlen, int64_t channels, int groups, int dstate, bool backward) {
+    const TileTime main_pass = backward ? TileTime{2.9, 0.95, 1.64, 3} : TileTime{2.4, 0.6, 0.94, 6};
+    const TileTime carry = backward ? TileTime{1.4, 0.25, 0.39, 8} : TileTime{1.9, 0.45, 0.65, 7};
+    const double launches = backward ? 7 : 5, each = 0.1;  // the passes' own launches, and each split's part in the join
     const int64_t dg = channels / groups, blocks = batch * groups * ((dg + 63) / 64);
     const int64_t tile = backward ? kScanPeriod : kTile, tiles = (seqlen + tile - 1) / tile;
-    int64_t s = std::min(kSplitBlocks / blocks, tiles / 2);
-    if (s < 2) return 1;
-    const int64_t per = (tiles + s - 1) / s;
-    return (int)((tiles + per - 1) / per);
+    const int waves = dstate == 8 ? 2 : dstate == 16 ? 4 : 8;  // of a workgroup
+    const double width = dstate == 64 ? 2 : 1;                 // quads of states a lane holds
+    const double w1 = (double)blocks * waves / 1024;
+    const int64_t most = std::min<int64_t>(tiles, 128);
+    int64_t best = 1;
+    double least = 0;
+    for (int64_t want = 1; want <= most; want += want < 4 ? 1 : want / 2) {  // 1, 2, 3, 4, 6, 9, 13, 19, 28, 42, 63, 94
+        const int64_t per = (tiles + want - 1) / want, s = (tiles + per - 1) / per;
+        const double w = w1 * (double)s, again = s > 1 ? (double)(s - 1) / (double)s : 0;
+        const double edges = 0.7 / std::max(1.0, w / main_pass.resident);  // a split's beginning and end, in tiles
+        const double t = ((double)per + edges) * width * (main_pass.at(w) + again * carry.at(w)) +
+                         (s > 1 ? launches + each * (double)s : 0);
+        if (want == 1 || t < least) {
+            least = t;
+            best = s;
+        }
+    }
+    return (int)best;
 }
 
 template <typename T, int NW, int NS> hipError_t launch_scan_n(ScanArgs& a, hipStream_t st) {
@@ -311,9 +346,11 @@ template <typename T, int NW, int NS> hipError_t launch_scan_n(ScanArgs& a, hipS
         const void* fn = a.seq ? (const void*)&k_scan_carry<T, NW, NS, true> : (const void*)&k_scan_carry<T, NW, NS, false>;
         hipError_t e = hipLaunchKernel(fn, dim3(blocks * (a.nsplit - 1)), dim3(NW * 64), args, 0, st);
         if (e != hipSuccess) return e;
-        const int64_t lanes = (int64_t)a.batch * a.channels * a.dstate;
-        e = hipLaunchKernel((const void*)&k_scan_join, dim3((unsigned)((lanes + 255) / 256)), dim3(256), args, 0, st);
-        if (e != hipSuccess) return e;
+        if (a.nsplit > kFoldSplits) {
+            const int64_t lanes = (int64_t)a.batch * a.channels * a.dstate;
+            e = hipLaunchKernel((const void*)&k_scan_join, dim3((unsigned)((lanes + 255) / 256)), dim3(256), args, 0, st);
+            if (e != hipSuccess) return e;
+        }
     }
     const void* fn = a.seq ? (const void*)&k_scan<T, NW, NS, true> : (const void*)&k_scan<T, NW, NS, false>;
     return hipLaunchKernel(fn, dim3(blocks * a.nsplit), dim3(NW * 64), args, 0, st);

@@ -111,10 +111,20 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
     float dD = 0.f, db = 0.f;
     const int64_t soff = (int64_t)p.c * N + n0, sstride = (int64_t)a.channels * N;
     const int tile0 = p.split * a.tiles_per_split, tile1 = min(tile0 + a.tiles_per_split, a.ntiles);
-    if (p.split + 1 < a.nsplit)
-        load_states<NS>(a.split_state, DT_F32, ((int64_t)p.b * a.nsplit + p.split) * sstride + soff, g);
-    else if (!VL && a.dfin)
+    if (p.split + 1 < a.nsplit) {
+        // (the last split's own pass began with the final state's gradient)
+        const float* st = a.split_state + (int64_t)p.b * a.nsplit * sstride + soff;
+        const float* sum = a.split_sum + (int64_t)p.b * a.nsplit * a.channels + p.c;
+        if (a.nsplit > kFoldSplits) {
+            load_states<NS>(st, DT_F32, p.split * sstride, g);
+        } else {
+            load_states<NS>(st, DT_F32, (a.nsplit - 2) * sstride, g);
+            fold_splits<NS>(A2, g, a.nsplit - 2 - p.split, [&](int k) { return sum[(int64_t)(a.nsplit - 2 - k) * a.channels]; },
+                            [&](int k) { return st + (a.nsplit - 3 - k) * sstride; });
+        }
+    } else if (!VL && a.dfin) {
         load_states<NS>(a.dfin, a.state_dtype, p.b * sstride + soff, g);
+    }
     // this wave's sums over the channels: lane l holds that of token `pk`, state `pi` of a tile
     typedef WaveSum<TB * NS> Sum;
     const int pidx = Sum::index(lane), pk = TB - 1 - pidx / NS, pi = pidx % NS;
@@ -382,7 +392,7 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward_carry(ScanArgs a) {
     if (w == 0) a.split_sum[((int64_t)p.b * a.nsplit + p.split) * a.channels + p.c] = fresh ? __builtin_inff() : sum;
 }
 
-// Joins the splits from the last to the first: the gradient entering each from behind.
+// Joins the splits where there are many, from the last to the first: the gradient entering each from behind.
 __global__ __launch_bounds__(256) void k_scan_backward_join(ScanArgs a) {
     const int64_t per = (int64_t)a.channels * a.dstate, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= a.batch * per) return;
@@ -447,9 +457,11 @@ hipError_t launch_scan_backward_n(ScanArgs& a, T* dB, T* dC, float* dA, float* d
                                : (const void*)&k_scan_backward_carry<T, NW, NS, false>;
         e = hipLaunchKernel(fn, dim3(blocks * (a.nsplit - 1)), dim3(NW * 64), args, 0, st);
         if (e != hipSuccess) return e;
-        const int64_t lanes = (int64_t)a.batch * a.channels * a.dstate;
-        e = hipLaunchKernel((const void*)&k_scan_backward_join, dim3((unsigned)((lanes + 255) / 256)), dim3(256), args, 0, st);
-        if (e != hipSuccess) return e;
+        if (a.nsplit > kFoldSplits) {
+            const int64_t lanes = (int64_t)a.batch * a.channels * a.dstate;
+            e = hipLaunchKernel((const void*)&k_scan_backward_join, dim3((unsigned)((lanes + 255) / 256)), dim3(256), args, 0, st);
+            if (e != hipSuccess) return e;
+        }
     }
     const void* fn = a.seq ? (const void*)&k_scan_backward<T, NW, NS, true> : (const void*)&k_scan_backward<T, NW, NS, false>;
     e = hipLaunchKernel(fn, dim3(blocks * a.nsplit), dim3(NW * 64), args, 0, st);

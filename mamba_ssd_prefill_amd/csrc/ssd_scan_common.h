@@ -216,6 +216,29 @@ __device__ inline void join_splits(float A2, float v, int n, Step step, Place pl
     }
 }
 
+// The same inside a pass over the splits, for a wave's own NS states of up to kFoldSplits splits: h after n splits,
+// without the join's launch.
+constexpr int kFoldSplits = 16;
+template <int NS, typename Step, typename Place>
+__device__ inline void fold_splits(const float (&A2)[NS], float (&h)[NS], int n, Step step, Place place) {
+    for (int k0 = 0; k0 < n; k0 += 4) {
+        float own[4][NS], d[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = min(k0 + j, n - 1);
+            load_states<NS>(place(k), DT_F32, 0, own[j]);
+            d[j] = step(k);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (k0 + j >= n) break;
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                h[i] = d[j] == __builtin_inff() ? own[j][i] : __builtin_amdgcn_exp2f(d[j] * A2[i]) * h[i] + own[j][i];
+        }
+    }
+}
+
 __device__ inline bool state_number(const ScanArgs& a, int q) { return q >= 0 && q < a.nseq; }
 
 }  // namespace ssd
