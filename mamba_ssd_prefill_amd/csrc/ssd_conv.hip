@@ -7,38 +7,64 @@
 // All three are HBM-bound streams.  A lane owns CW neighbouring channels of a run of tokens and slides a
 // window of W-1 inputs down them, so each input is read once a run plus a halo of W-1 rows;
 // consecutive lanes take consecutive channels.
+#include <type_traits>
+
 #include "ssd_device.h"
 #include "ssd_select.h"
 #include "ssd_sum_rows.h"
 
 namespace ssd {
 
-// CW elements at p, in one access.
+// CW elements in one access.  Rows are kept as loaded until they are used: converting a row that is still on its way
+// would wait for it.
+template <typename T, int CW> struct ConvPiece { typedef T type __attribute__((ext_vector_type(CW))); };
+template <typename T> struct ConvPiece<T, 1> { struct type { T v; __device__ T operator[](int) const { return v; } }; };
+template <typename T, int CW> __device__ inline typename ConvPiece<T, CW>::type load_raw(const T* p) {
+    return *(const typename ConvPiece<T, CW>::type*)p;
+}
 template <typename T, int CW> __device__ inline void load_cw(const T* p, float (&v)[CW]) {
-    if constexpr (CW == 4) {
-        const typename TT<T>::v4 r = *(const typename TT<T>::v4*)p;
+    const auto r = load_raw<T, CW>(p);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (float)r[e];
-    } else if constexpr (CW == 2) {
-        const typename TT<T>::v2 r = *(const typename TT<T>::v2*)p;
-        v[0] = (float)r[0];
-        v[1] = (float)r[1];
-    } else {
-        v[0] = (float)*p;
-    }
+    for (int e = 0; e < CW; ++e) v[e] = (float)r[e];
 }
 template <typename T, int CW> __device__ inline void store_cw(T* p, const float (&v)[CW]) {
-    if constexpr (CW == 4) {
-        typename TT<T>::v4 r;
+    if constexpr (CW > 1) {
+        typename ConvPiece<T, CW>::type r;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = (T)v[e];
-        *(typename TT<T>::v4*)p = r;
-    } else if constexpr (CW == 2) {
-        *(typename TT<T>::v2*)p = typename TT<T>::v2{(T)v[0], (T)v[1]};
+        for (int e = 0; e < CW; ++e) r[e] = (T)v[e];
+        *(typename ConvPiece<T, CW>::type*)p = r;
     } else {
         *p = (T)v[0];
     }
 }
+
+// A run of rows, loaded AHEAD rows before they are used.  The address moves on by a row a step and stays at the last
+// one: a product for each row's address took more slots than the convolution's own.
+template <typename T, int CW, int AHEAD> struct RowStream {
+    typename ConvPiece<T, CW>::type r[AHEAD];
+    const T* at;
+    int64_t stride;
+    int left;  // rows behind the one last asked for
+    __device__ inline RowStream(const T* first, int64_t stride_, int rows) : at(first), stride(stride_), left(rows - 1) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            r[i] = load_raw<T, CW>(at);
+            advance();
+        }
+    }
+    __device__ inline void advance() {
+        at += left > 0 ? stride : 0;
+        --left;
+    }
+    __device__ inline void take(float (&v)[CW]) {
+#pragma unroll
+        for (int e = 0; e < CW; ++e) v[e] = (float)r[0][e];
+#pragma unroll
+        for (int i = 0; i + 1 < AHEAD; ++i) r[i] = r[i + 1];
+        r[AHEAD - 1] = load_raw<T, CW>(at);
+        advance();
+    }
+};
 
 // Row `row` of channel c0 in a tensor split by channel ranges.
 template <typename T> __device__ inline T* split_ptr(void* const* base, int sa, int sb, int ch, int c0, int64_t row) {
@@ -47,18 +73,27 @@ template <typename T> __device__ inline T* split_ptr(void* const* base, int sa, 
     return (T*)base[2] + row * (ch - sb) + (c0 - sb);
 }
 
-// The lane's item: piece of CW channels (fastest), segment of a.rows tokens, batch row.
+// The lane's item: a piece of CW channels and a run of a.rows tokens.  A workgroup takes 64 pieces of 4 runs that follow
+// one another (of fewer channels, 2^k pieces of 256 / 2^k runs): the rows that two runs both read then come from
+// its own XCD's L2 (2 x 4096 x 5376 forward 47 us with 256 pieces of one run, 39 us so), and the indexes need no
+// long division.
 struct ConvItem {
     int b, c0, t0, t1;
 };
+__host__ __device__ inline int conv_piece_bits(int npc) {
+    int k = 0;
+    while (k < 6 && (1 << k) < npc) ++k;
+    return k;
+}
 template <int CW> __device__ inline bool conv_item(const CausalConvArgs& a, ConvItem* it) {
-    const int npc = a.channels / CW;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)a.batch * a.nseg * npc) return false;
-    it->c0 = (int)(i % npc) * CW;
-    const int64_t r = i / npc;
-    it->t0 = (int)(r % a.nseg) * a.rows;
-    it->b = (int)(r / a.nseg);
+    const int npc = a.channels / CW, bits = conv_piece_bits(npc);
+    const uint32_t pblocks = (uint32_t)(npc + (1 << bits) - 1) >> bits;
+    const int pc = (int)((blockIdx.x % pblocks) << bits) + (int)(threadIdx.x & ((1u << bits) - 1));
+    const uint32_t r = ((blockIdx.x / pblocks) << (8 - bits)) + (threadIdx.x >> bits);
+    if (pc >= npc || r >= (uint32_t)a.batch * (uint32_t)a.nseg) return false;
+    it->c0 = pc * CW;
+    it->t0 = (int)(r % (uint32_t)a.nseg) * a.rows;
+    it->b = (int)(r / (uint32_t)a.nseg);
     it->t1 = min(it->t0 + a.rows, a.seqlen);
     return true;
 }
@@ -68,8 +103,10 @@ template <int W, int CW> struct ConvW {
     __device__ inline void load(const CausalConvArgs& a, int c0) {
 #pragma unroll
         for (int e = 0; e < CW; ++e) {
+            struct __attribute__((packed, aligned(4))) Taps { float v[W]; };  // one access, on any multiple of 4 bytes
+            const Taps t = *(const Taps*)(a.w + (int64_t)(c0 + e) * W);
 #pragma unroll
-            for (int k = 0; k < W; ++k) w[k][e] = a.w[(int64_t)(c0 + e) * W + k];
+            for (int k = 0; k < W; ++k) w[k][e] = t.v[k];
             bias[e] = a.bias ? a.bias[c0 + e] : 0.f;
         }
     }
@@ -145,10 +182,19 @@ template <typename T, int W, int CW, bool VL> struct ConvWalk {
         for (int e = 0; e < CW; ++e) win[W - 2][e] = cur[e];
         if (place < W) ++place;
     }
+    // the window holds inputs (or the initial state) as they were, so this rounds nothing
+    __device__ inline void store_state() const {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < CW; ++e)
+                ((T*)a.fin)[((int64_t)q * a.channels + c0 + e) * (W - 1) + j] = (T)win[j][e];
+    }
     __device__ inline bool last(int t) const { return t == a.seqlen - 1 || (VL && qn != q); }
 };
 
-constexpr int kConvAhead = 4;
+// Rows on their way while one is used (2 and 4 measured alike forward, 1, 2 and 3 backward).
+constexpr int kConvAhead = 2, kConvAheadBackward = 1;
 
 template <typename T, int W, int CW, bool VL> __global__ __launch_bounds__(256) void k_causal_conv(CausalConvArgs a) {
     ConvItem it;
@@ -159,20 +205,11 @@ template <typename T, int W, int CW, bool VL> __global__ __launch_bounds__(256) 
     s.start(it.t0);
     T* out = split_ptr<T>(a.out, a.split_a, a.split_b, a.channels, it.c0, (int64_t)it.b * a.seqlen + it.t0);
     const int os = it.c0 < a.split_a ? a.split_a : it.c0 < a.split_b ? a.split_b - a.split_a : a.channels - a.split_b;
-    // kConvAhead rows on their way while one is used
-    float next[kConvAhead][CW];
-#pragma unroll
-    for (int i = 0; i < kConvAhead; ++i) load_cw<T, CW>(s.row(min(it.t0 + i, it.t1 - 1)), next[i]);
+    RowStream<T, CW, kConvAhead> rows(s.row(it.t0), a.xs, it.t1 - it.t0);
 #pragma unroll 4
     for (int t = it.t0; t < it.t1; ++t, out += os) {
         float cur[CW], pre[CW];
-#pragma unroll
-        for (int e = 0; e < CW; ++e) {
-            cur[e] = next[0][e];
-#pragma unroll
-            for (int i = 0; i + 1 < kConvAhead; ++i) next[i][e] = next[i + 1][e];
-        }
-        load_cw<T, CW>(s.row(min(t + kConvAhead, it.t1 - 1)), next[kConvAhead - 1]);
+        rows.take(cur);
         s.step_to(t);
         s.taps(k, cur, pre);
         if (a.silu) {
@@ -181,15 +218,11 @@ template <typename T, int W, int CW, bool VL> __global__ __launch_bounds__(256) 
         }
         store_cw<T, CW>(out, pre);
         s.push(cur);
-        if (a.fin && s.last(t) && s.has_state(s.q)) {
-            // the window holds inputs (or the initial state) as they were, so this rounds nothing
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                for (int e = 0; e < CW; ++e)
-                    ((T*)a.fin)[((int64_t)s.q * a.channels + it.c0 + e) * (W - 1) + j] = (T)s.win[j][e];
-        }
+        if (VL && a.fin && s.last(t) && s.has_state(s.q)) s.store_state();
     }
+    // (outside the loop where it can be: a store that may or may not have been made makes the next row's wait one
+    // for everything)
+    if (!VL && a.fin && it.t1 == a.seqlen) s.store_state();
 }
 
 // silu'(v) = p (1 + v (1 - p)), p the sigmoid of v
@@ -218,23 +251,70 @@ __global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) 
     // gradients of the initial state, at a sequence's first tokens
     float dh[W - 1][CW] = {};
     const int end = min(it.t1 + W - 1, a.seqlen);
-    float xnext[CW], gnext[CW];
-    load_cw<T, CW>(s.row(it.t0), xnext);
-    load_cw<T, CW>(dout, gnext);
-    for (int t = it.t0; t < it.t1 + W - 1; ++t) {
-        float here[CW] = {};
-        if (t < end) {
-            float cur[CW], pre[CW], g[CW];
+    // what the states add at token t, place `place` of its sequence
+    auto states = [&](int t, int place, const float (&g)[CW], float (&here)[CW]) {
+        const bool last = s.last(t);
+        // the initial state: tap j of the token at place p reads its column p + j while that is below W-1;
+        // the lane that holds the sequence's first token sums and stores it
+        const bool head = a.dh0 && place <= W - 2 && t - place >= it.t0 && t - place < it.t1 && s.has_state(s.q);
+        if (head) {
 #pragma unroll
-            for (int e = 0; e < CW; ++e) {
-                cur[e] = xnext[e];
-                g[e] = gnext[e];
+            for (int c = 0; c < W - 1; ++c) {
+#pragma unroll
+                for (int j = 0; j <= c; ++j) {
+                    if (place + j != c) continue;
+                    // the sequence's first token (place 0) begins every column
+#pragma unroll
+                    for (int e = 0; e < CW; ++e) dh[c][e] = (place ? dh[c][e] : 0.f) + k.w[j][e] * g[e];
+                }
             }
-            if (t + 1 < end) {  // a row ahead
-                dout += os;
-                load_cw<T, CW>(s.row(t + 1), xnext);
-                load_cw<T, CW>(dout, gnext);
+        }
+        if (a.dfin && last && s.has_state(s.q)) {
+            // column j of the final state is the input of token t - (W-2) + j, if it is in the sequence
+            const T* df = (const T*)a.dfin + ((int64_t)s.q * a.channels + it.c0) * (W - 1);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                if (W - 2 - j > place) continue;
+#pragma unroll
+                for (int e = 0; e < CW; ++e) {
+                    const float v = (float)df[e * (W - 1) + j];
+                    if (j == W - 2)
+                        here[e] += v;
+                    else
+                        acc[j + 1][e] += v;
+                }
             }
+            // a sequence shorter than the state keeps part of its initial state: column place + 1 + j
+            if (head) {
+#pragma unroll
+                for (int c = 1; c < W - 1; ++c)
+#pragma unroll
+                    for (int j = 0; j < c; ++j) {
+                        if (place + 1 + j != c) continue;
+#pragma unroll
+                        for (int e = 0; e < CW; ++e) dh[c][e] += (float)df[e * (W - 1) + j];
+                    }
+            }
+        }
+        if (head && (last || place == W - 2)) {
+#pragma unroll
+            for (int c = 0; c < W - 1; ++c)
+#pragma unroll
+                for (int e = 0; e < CW; ++e)
+                    ((T*)a.dh0)[((int64_t)s.q * a.channels + it.c0 + e) * (W - 1) + c] = (T)dh[c][e];
+        }
+    };
+    RowStream<T, CW, kConvAheadBackward> xrows(s.row(it.t0), a.xs, end - it.t0), grows(dout, os, end - it.t0);
+    T* dx = (T*)a.dx + (row0 + it.t0) * a.channels + it.c0;
+    // One token.  INNER: it is one of the run's own with W-1 of them before it, so that nothing here branches by lane
+    // (a load or store that may or may not have been made makes the next row's wait one for everything).
+    auto token = [&](auto inner, int t) {
+        constexpr bool INNER = decltype(inner)::value;
+        float here[CW] = {};
+        if (INNER || t < end) {
+            float cur[CW], pre[CW], g[CW];
+            xrows.take(cur);
+            grows.take(g);
             s.step_to(t);
             s.taps(k, cur, pre);
             if (a.silu) {
@@ -242,7 +322,7 @@ __global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) 
                 for (int e = 0; e < CW; ++e) g[e] *= dsilu_f(pre[e]);
             }
             const int place = s.place;  // of t in its sequence, up to W
-            if (t < it.t1) {
+            if (INNER || t < it.t1) {
 #pragma unroll
                 for (int e = 0; e < CW; ++e) {
                     db[e] += g[e];
@@ -261,66 +341,23 @@ __global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) 
                     for (int e = 0; e < CW; ++e) acc[j][e] += k.w[j][e] * g[e];
                 }
             s.push(cur);
-            const bool last = s.last(t);
-            // the initial state: tap j of the token at place p reads its column p + j while that is below W-1;
-            // the lane that holds the sequence's first token sums and stores it
-            const bool head = ST && a.dh0 && place <= W - 2 && t - place >= it.t0 && t - place < it.t1 && s.has_state(s.q);
-            if (head) {
-#pragma unroll
-                for (int c = 0; c < W - 1; ++c) {
-#pragma unroll
-                    for (int j = 0; j <= c; ++j) {
-                        if (place + j != c) continue;
-                        // the sequence's first token (place 0) begins every column
-#pragma unroll
-                        for (int e = 0; e < CW; ++e) dh[c][e] = (place ? dh[c][e] : 0.f) + k.w[j][e] * g[e];
-                    }
-                }
-            }
-            if (ST && a.dfin && last && s.has_state(s.q)) {
-                // column j of the final state is the input of token t - (W-2) + j, if it is in the sequence
-                const T* df = (const T*)a.dfin + ((int64_t)s.q * a.channels + it.c0) * (W - 1);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) {
-                    if (W - 2 - j > place) continue;
-#pragma unroll
-                    for (int e = 0; e < CW; ++e) {
-                        const float v = (float)df[e * (W - 1) + j];
-                        if (j == W - 2)
-                            here[e] += v;
-                        else
-                            acc[j + 1][e] += v;
-                    }
-                }
-                // a sequence shorter than the state keeps part of its initial state: column place + 1 + j
-                if (head) {
-#pragma unroll
-                    for (int c = 1; c < W - 1; ++c)
-#pragma unroll
-                        for (int j = 0; j < c; ++j) {
-                            if (place + 1 + j != c) continue;
-#pragma unroll
-                            for (int e = 0; e < CW; ++e) dh[c][e] += (float)df[e * (W - 1) + j];
-                        }
-                }
-            }
-            if (head && (last || place == W - 2)) {
-#pragma unroll
-                for (int c = 0; c < W - 1; ++c)
-#pragma unroll
-                    for (int e = 0; e < CW; ++e)
-                        ((T*)a.dh0)[((int64_t)s.q * a.channels + it.c0 + e) * (W - 1) + c] = (T)dh[c][e];
-            }
+            if constexpr (ST) states(t, place, g, here);
         }
-        const int sdone = t - (W - 1);
-        if (sdone >= it.t0) store_cw<T, CW>((T*)a.dx + (row0 + sdone) * a.channels + it.c0, acc[0]);
+        if (INNER || t - (W - 1) >= it.t0) {
+            store_cw<T, CW>(dx, acc[0]);
+            dx += a.channels;
+        }
 #pragma unroll
         for (int j = 0; j + 1 < W - 1; ++j)
 #pragma unroll
             for (int e = 0; e < CW; ++e) acc[j][e] = acc[j + 1][e];
 #pragma unroll
         for (int e = 0; e < CW; ++e) acc[W - 2][e] = here[e];
-    }
+    };
+    int t = it.t0;
+    for (; t < it.t0 + W - 1; ++t) token(std::false_type{}, t);
+    for (; t < it.t1; ++t) token(std::true_type{}, t);
+    for (; t < it.t1 + W - 1; ++t) token(std::false_type{}, t);
     float* part = a.part + (((int64_t)it.b * a.nseg + it.t0 / a.rows) * a.channels + it.c0) * (W + 1);
 #pragma unroll
     for (int e = 0; e < CW; ++e) {
@@ -372,9 +409,20 @@ template <typename T, int W> __global__ __launch_bounds__(256) void k_causal_con
     st[W - 2] = cur;
 }
 
-constexpr int kConvForwardRows = 16;  // tokens per lane of the forward
+// Tokens per lane: long runs read fewer rows twice (measured at 2 x 4096 x 5376, bf16: forward 43, 39.5, 37.7 us with 8, 16,
+// 32; backward 90, 77, 77 us with 16, 32, 64), short ones give a small problem more waves (1 x 4096 x 1792 packed:
+// 15.6, 12.7, 13.0 us with 4, 8, 16): the longest of 32, 16 and 8 that leaves 4 waves a SIMD.
+static int conv_rows(int64_t batch, int64_t seqlen, int64_t pieces) {
+    int rows = 32;
+    while (rows > 8 && batch * ((seqlen + rows - 1) / rows) * pieces < (int64_t)1 << 18) rows /= 2;
+    return rows;
+}
+constexpr int kConvWide = 4;          // channels a lane of the forward takes where rows allow it
+constexpr int kConvBackwardWide = 2;  // and of the backward (4: 84 us against 77 with 2 at 2 x 4096 x 5376)
 
-int conv_backward_rows(int64_t batch, int64_t seqlen, int64_t channels) { return 32; }
+int conv_backward_rows(int64_t batch, int64_t seqlen, int64_t channels) {
+    return conv_rows(batch, seqlen, channels / kConvBackwardWide);
+}
 
 // Whether lanes can take four channels with one access: every row they touch starts on a
 // multiple of four elements.
@@ -386,19 +434,21 @@ static bool conv_vec4(const CausalConvArgs& a, size_t es, const void* const* ten
     return true;
 }
 
-template <typename T, int W> hipError_t launch_conv_tw(CausalConvArgs& a, hipStream_t st) {
-    a.rows = kConvForwardRows;
-    a.nseg = (a.seqlen + a.rows - 1) / a.rows;
-    const bool v4 = conv_vec4(a, sizeof(T), a.out, 3);
-    const int64_t items = (int64_t)a.batch * a.nseg * (a.channels / (v4 ? 4 : 1));
-    void* args[] = {&a};
-    const void* fn = a.seq ? (v4 ? (const void*)&k_causal_conv<T, W, 4, true> : (const void*)&k_causal_conv<T, W, 1, true>)
-                           : (v4 ? (const void*)&k_causal_conv<T, W, 4, false> : (const void*)&k_causal_conv<T, W, 1, false>);
-    return hipLaunchKernel(fn, dim3((unsigned)((items + 255) / 256)), dim3(256), args, 0, st);
+static unsigned conv_blocks(const CausalConvArgs& a, int cw) {
+    const int npc = a.channels / cw, bits = conv_piece_bits(npc), per = 256 >> bits;
+    const int64_t pblocks = (npc + (1 << bits) - 1) >> bits, runs = (int64_t)a.batch * a.nseg;
+    return (unsigned)(pblocks * ((runs + per - 1) / per));
 }
 
-// Channels a lane of the backward takes where rows allow it.
-constexpr int kConvBackwardWide = 2;
+template <typename T, int W> hipError_t launch_conv_tw(CausalConvArgs& a, hipStream_t st) {
+    const bool v4 = conv_vec4(a, sizeof(T), a.out, 3);
+    a.rows = conv_rows(a.batch, a.seqlen, a.channels / (v4 ? kConvWide : 1));
+    a.nseg = (a.seqlen + a.rows - 1) / a.rows;
+    void* args[] = {&a};
+    const void* fn = a.seq ? (v4 ? (const void*)&k_causal_conv<T, W, kConvWide, true> : (const void*)&k_causal_conv<T, W, 1, true>)
+                           : (v4 ? (const void*)&k_causal_conv<T, W, kConvWide, false> : (const void*)&k_causal_conv<T, W, 1, false>);
+    return hipLaunchKernel(fn, dim3(conv_blocks(a, v4 ? kConvWide : 1)), dim3(256), args, 0, st);
+}
 
 template <typename T, int W, int CW> const void* conv_backward_kernel(bool packed, bool states) {
     if (packed) return (const void*)&k_causal_conv_backward<T, W, CW, true, true>;
@@ -411,12 +461,11 @@ template <typename T, int W> hipError_t launch_conv_back_tw(CausalConvArgs& a, f
     a.nseg = (a.seqlen + a.rows - 1) / a.rows;
     const void* tens[4] = {a.dout[0], a.dout[1], a.dout[2], a.dx};
     const bool v4 = conv_vec4(a, sizeof(T), tens, 4);
-    const int64_t items = (int64_t)a.batch * a.nseg * (a.channels / (v4 ? kConvBackwardWide : 1));
     void* args[] = {&a};
     const bool states = a.dh0 || a.dfin;
     const void* fn = v4 ? conv_backward_kernel<T, W, kConvBackwardWide>(a.seq, states)
                         : conv_backward_kernel<T, W, 1>(a.seq, states);
-    hipError_t e = hipLaunchKernel(fn, dim3((unsigned)((items + 255) / 256)), dim3(256), args, 0, st);
+    hipError_t e = hipLaunchKernel(fn, dim3(conv_blocks(a, v4 ? kConvBackwardWide : 1)), dim3(256), args, 0, st);
     if (e != hipSuccess) return e;
     int nrows = a.batch * a.nseg;
     const int64_t n = (int64_t)a.channels * (W + 1);
