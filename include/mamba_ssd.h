@@ -432,6 +432,9 @@ ssd_status_t ssd_prefill_block(const ssd_params_t* p, const void* xbc, const flo
  * The single-token forms work in place on a pool of nseq states: row b uses the state
  * slots[b] (int32; NULL: slot b, with nseq = batch).  Each slot in use appears once.  A row
  * whose slot lies outside [0, nseq) (a padded batch) touches no state and gets a zero output row.
+ *
+ * Outputs overlap no input, but for the states of the single-token forms.  A pass over a prompt may be
+ * split in time into runs of tokens that are joined by their states, as a function of the sizes alone.
  * ==================================================================================== */
 
 /* ---- causal depthwise convolution -----------------------------------------------------
@@ -508,7 +511,9 @@ typedef struct {
 } ssd_scan_params_t;
 
 /*   x, dt         [B, L, D]     in_dtype    required, rows
- *   A             [D, N]        fp32        required, 16-byte aligned; A <= 0 is a precondition (not checked)
+ *   A             [D, N]        fp32        required, 16-byte aligned; A <= 0 is a precondition (not checked);
+ *                                           steps may be negative (dt_softplus = 0) while the products of the
+ *                                           decays over a run of tokens stay in the fp32 range
  *   B, C          [B, L, G, N]  in_dtype    required, rows, 4-byte aligned
  *   D, dt_bias    [D]           fp32        NULL means 0
  *   z             [B, L, D]     in_dtype    rows; NULL: no gate

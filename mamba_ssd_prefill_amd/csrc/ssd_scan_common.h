@@ -194,6 +194,12 @@ template <int T> __device__ inline SeqMasks seq_masks(const ScanArgs& a, int64_t
     return SeqMasks{(uint32_t)__ballot(s), (uint32_t)__ballot(e)};
 }
 
+// The state v behind a split whose steps sum to d (infinite: nothing passes), `own` its state from a zero start.  (A
+// zero state passes nothing either, also where negative steps make the decay's product infinite.)
+__device__ inline float join_one(float A2, float v, float d, float own) {
+    return d == __builtin_inff() || v == 0.f ? own : __builtin_amdgcn_exp2f(d * A2) * v + own;
+}
+
 // Carries v through `n` time splits in order, v = decay(k) v + *place(k), and leaves it in their places.  step(k) is
 // the sum of steps that v decays by on the way (infinite: nothing passes).  Eight splits' values are
 // loaded together, so that the chain waits for one load in eight.
@@ -210,7 +216,7 @@ __device__ inline void join_splits(float A2, float v, int n, Step step, Place pl
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if (k0 + j >= n) break;
-            v = d[j] == __builtin_inff() ? own[j] : __builtin_amdgcn_exp2f(d[j] * A2) * v + own[j];
+            v = join_one(A2, v, d[j], own[j]);
             *place(k0 + j) = v;
         }
     }
@@ -234,7 +240,7 @@ __device__ inline void fold_splits(const float (&A2)[NS], float (&h)[NS], int n,
             if (k0 + j >= n) break;
 #pragma unroll
             for (int i = 0; i < NS; ++i)
-                h[i] = d[j] == __builtin_inff() ? own[j][i] : __builtin_amdgcn_exp2f(d[j] * A2[i]) * h[i] + own[j][i];
+                h[i] = join_one(A2[i], h[i], d[j], own[j][i]);
         }
     }
 }

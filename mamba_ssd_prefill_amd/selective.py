@@ -88,40 +88,68 @@ _MAX_PLANS = 512
 
 
 class _Plan:
-    __slots__ = ("prm", "ref", "fn", "name", "dev", "index", "dtype", "state_dtype", "shape", "parts", "state", "sizes")
+    __slots__ = ("prm", "ref", "fn", "name", "dev", "index", "out", "parts", "state", "spaces", "new")
 
-    def __init__(self, name, prm, dev, dtype, state_dtype=None, shape=None, parts=None, state=None, sizes=()):
+    def __init__(self, name, prm, dev, out=None, parts=None, state=None, spaces=(), new=()):
+        import torch
         self.prm, self.ref, self.name, self.dev = prm, ctypes.byref(prm), name, dev
         self.fn, self.index = getattr(load_library(), name), dev.index
-        self.dtype, self.state_dtype, self.shape, self.parts, self.state = dtype, state_dtype, shape, parts, state
-        self.sizes = [_size(s, prm) for s in sizes]
+        # layouts of the output like x, of one output per split, of the states, and of other new tensors
+        self.out, self.parts, self.state, self.new = out, parts, state, new
+        self.spaces = []
+        for s in spaces:
+            n = getattr(load_library(), s)(self.ref)
+            if n == 0:  # parameters the library does not take: its own call says why, before it looks at a pointer
+                raise SSDError(self.fn(self.ref, *[0] * (len(self.fn.argtypes) - 1)), name)
+            self.spaces.append(_layout((n,), torch.uint8, dev))
 
     def call(self, *args):
         """One C call on the current stream of the tensors' device, with that device current."""
-        import torch
-        if self.index is None or self.index == torch.cuda.current_device():
-            rc = self.fn(self.ref, *args, _stream(self.dev))
+        if _raw is None:
+            _bind()
+        if self.index == _device():
+            rc = self.fn(self.ref, *args, _raw(self.index))
         else:
+            import torch
             with torch.cuda.device(self.dev):
-                rc = self.fn(self.ref, *args, _stream(self.dev))
+                rc = self.fn(self.ref, *args, _raw(self.index))
         if rc:
             raise SSDError(rc, self.name)
 
 
-def _stream(dev):
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same handle without a Stream object
-    return raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+# torch's calls for a tensor's memory, the current device and its current stream's handle (bound at the first call)
+_empty = _device = _raw = None
 
 
-def _new(shape, dtype, dev):
-    """A new contiguous tensor (torch.empty by the shorter way)."""
+def _bind():
     import torch
-    strides, n = [], 1
+    global _empty, _device, _raw
+    torch.cuda.init()
+    _empty = torch.empty_strided
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _strides(shape):
+    out, n = [], 1
     for d in reversed(shape):
-        strides.append(n)
+        out.append(n)
         n *= d
-    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=dev)
+    return tuple(out[::-1])
+
+
+def _layout(shape, dtype, dev):
+    """What _new takes for a contiguous tensor."""
+    shape = tuple(shape)
+    return shape, _strides(shape), dtype, dev
+
+
+def _new(layout):
+    """A new tensor (torch.empty by a shorter way)."""
+    if _empty is None:
+        _bind()
+    return _empty(layout[0], layout[1], dtype=layout[2], device=layout[3])
 
 
 def _keep(key, plan):
@@ -143,14 +171,6 @@ def _mr(t):
 
 def _p(t):
     return None if t is None else t.data_ptr()
-
-
-def _size(name, prm):
-    """A size the library asks for; its functions give 0 for parameters they do not take."""
-    n = getattr(load_library(), name)(ctypes.byref(prm))
-    if n == 0:
-        raise SSDError(3, name)
-    return n
 
 
 def _code(t, name):
@@ -233,20 +253,20 @@ def _seq(seq_idx, nseq, lead, dev):
     return int(nseq)
 
 
-def _space(workspace, n, dev):
-    """The workspace given (the library checks its size), or n new bytes."""
-    import torch
+def _space(workspace, layout):
+    """The workspace given (the library checks its size), or a new one."""
     if workspace is None:
-        return _new((n,), torch.uint8, dev)
+        return _new(layout)
+    import torch
+    dev = layout[3]
     if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on %s" % dev)
     return workspace
 
 
-def _states(packed, shape, dtype, dev):
+def _states(packed, layout):
     """A new state output; entries of numbers that no sequence uses stay zero."""
-    import torch
-    return torch.zeros(shape, dtype=dtype, device=dev) if packed else _new(shape, dtype, dev)
+    return _new(layout).zero_() if packed else _new(layout)
 
 
 # ---- causal convolution ----------------------------------------------------------------------------
@@ -277,7 +297,7 @@ def _three(ts):
     return [_p(t) for t in ts] + [None] * (3 - len(ts))
 
 
-def _conv_plan(name, sizes, x, weight, bias, activation, seq_idx, nseq, splits, states, douts=()):
+def _conv_plan(name, spaces, x, weight, bias, activation, seq_idx, nseq, splits, states, douts=()):
     lead = tuple(x.shape[:2])
     S = _seq(seq_idx, nseq, lead, x.device)
     prm, dev, parts = _conv_params(x, weight, bias, activation, splits, S, lead)
@@ -288,15 +308,17 @@ def _conv_plan(name, sizes, x, weight, bias, activation, seq_idx, nseq, splits, 
         raise ValueError("dout must have one tensor per split")
     for d, n in zip(douts, parts):
         _same(dev, x.dtype, dout=(d, lead + (n,)))
-    return _Plan(name, prm, dev, x.dtype, shape=tuple(x.shape), parts=[lead + (n,) for n in parts], state=state, sizes=sizes)
+    lay = lambda t: None if t is None else _layout(t.shape, t.dtype, dev)  # noqa: E731
+    return _Plan(name, prm, dev, lay(x), [_layout(lead + (n,), x.dtype, dev) for n in parts], _layout(state, x.dtype, dev),
+                 spaces, [lay(weight), lay(bias)])
 
 
 def _outs(plan):
     """New outputs, one per split, and the three pointers the library takes."""
     if len(plan.parts) == 1:
-        o = _new(plan.parts[0], plan.dtype, plan.dev)
+        o = _new(plan.parts[0])
         return (o,), (o.data_ptr(), None, None)
-    outs = tuple([_new(s, plan.dtype, plan.dev) for s in plan.parts])
+    outs = tuple([_new(s) for s in plan.parts])
     return outs, _three(outs)
 
 
@@ -314,7 +336,7 @@ def causal_conv(x, weight, bias=None, *, activation="silu", seq_idx=None, nseq=N
                                      dict(initial_state=initial_state, final_state=final_state)))
     outs, ptrs = _outs(plan)
     if final_state is None and with_final_state:
-        final_state = _states(seq_idx is not None, plan.state, plan.dtype, plan.dev)
+        final_state = _states(seq_idx is not None, plan.state)
     plan.call(x.data_ptr(), weight.data_ptr(), _p(bias), _p(seq_idx), _p(initial_state), *ptrs, _p(final_state))
     return (outs[0] if splits is None else outs), final_state
 
@@ -324,7 +346,6 @@ def causal_conv_backward(dout, x, weight, bias=None, *, activation="silu", seq_i
     """ssd_causal_conv_backward: ConvGrads(dx, dweight, dbias, dinitial_state) of causal_conv from the gradient of
     its output (a tuple with ``splits``) and, if given, of its final state.  dbias and dinitial_state are None
     where bias and initial_state are."""
-    import torch
     splits = splits if splits is None else tuple(splits)
     douts = (dout,) if splits is None else tuple(dout)
     key = ("conv backward", _mr(x), _m(weight), _m(bias), _m(seq_idx), _m(initial_state), _m(dfinal_state), activation,
@@ -334,11 +355,10 @@ def causal_conv_backward(dout, x, weight, bias=None, *, activation="silu", seq_i
         plan = _keep(key, _conv_plan("ssd_causal_conv_backward", ("ssd_causal_conv_backward_workspace_size",), x, weight,
                                      bias, activation, seq_idx, nseq, splits,
                                      dict(initial_state=initial_state, dfinal_state=dfinal_state), douts))
-    dx = _new(plan.shape, plan.dtype, plan.dev)
-    dw = torch.empty_like(weight)
-    db = None if bias is None else torch.empty_like(bias)
-    dh = None if initial_state is None else _states(seq_idx is not None, plan.state, plan.dtype, plan.dev)
-    workspace = _space(workspace, plan.sizes[0], plan.dev)
+    dx, dw = _new(plan.out), _new(plan.new[0])
+    db = None if bias is None else _new(plan.new[1])
+    dh = None if initial_state is None else _states(seq_idx is not None, plan.state)
+    workspace = _space(workspace, plan.spaces[0])
     plan.call(*_three(douts), _p(dfinal_state), x.data_ptr(), weight.data_ptr(), _p(bias), _p(seq_idx), _p(initial_state),
               dx.data_ptr(), dw.data_ptr(), _p(db), _p(dh), workspace.data_ptr(), workspace.numel())
     return ConvGrads(dx, dw, db, dh)
@@ -352,7 +372,7 @@ def _conv_step_plan(x, weight, bias, activation, splits, state, slots):
     prm, dev, parts = _conv_params(x, weight, bias, activation, splits, state.shape[0], lead)
     _same(dev, x.dtype, state=(state, (state.shape[0], prm.channels, prm.width - 1)))
     _same(dev, torch.int32, slots=(slots, lead))
-    return _Plan("ssd_causal_conv_step", prm, dev, x.dtype, parts=[lead + (n,) for n in parts])
+    return _Plan("ssd_causal_conv_step", prm, dev, parts=[_layout(lead + (n,), x.dtype, dev) for n in parts])
 
 
 def causal_conv_step(x, weight, bias=None, *, state, activation="silu", slots=None, splits=None):
@@ -386,7 +406,7 @@ def _scan_params(x, dt, A, B, C, D, dt_bias, z, dt_softplus, state_code, nseq, l
                       rows("B", B, (G, N)), rows("C", C, (G, N))), dev
 
 
-def _scan_plan(name, sizes, x, dt, A, B, C, D, dt_bias, z, dt_softplus, seq_idx, nseq, state_dtype, states, like_x):
+def _scan_plan(name, spaces, x, dt, A, B, C, D, dt_bias, z, dt_softplus, seq_idx, nseq, state_dtype, states, like_x):
     lead = tuple(x.shape[:2])
     S = _seq(seq_idx, nseq, lead, x.device)
     if state_dtype is None:
@@ -399,7 +419,9 @@ def _scan_plan(name, sizes, x, dt, A, B, C, D, dt_bias, z, dt_softplus, seq_idx,
         _same(dev, state_dtype, **{n: (t, state)})
     for n, t in like_x.items():
         _same(dev, x.dtype, **{n: (t, x.shape)})
-    return _Plan(name, prm, dev, x.dtype, state_dtype, tuple(x.shape), state=state, sizes=sizes)
+    lay = lambda t: None if t is None else _layout(t.shape, t.dtype, dev)  # noqa: E731
+    return _Plan(name, prm, dev, lay(x), state=_layout(state, state_dtype, dev), spaces=spaces,
+                 new=[lay(t) for t in (x, dt, A, B, C, D, dt_bias, z)])
 
 
 def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=True, seq_idx=None, nseq=None,
@@ -408,7 +430,6 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
     """ssd_selective_scan over a prompt: x, dt, z [B, L, D], A [D, N] float32, B, C [B, L, G, N], D and dt_bias [D]
     float32.  Returns (out [B, L, D], final_state [B or nseq, D, N]), and with ``save_for_backward`` a third
     tensor for selective_scan_backward.  ``state_dtype`` defaults to initial_state's, else float32."""
-    import torch
     key = ("scan", _mr(x), _mr(dt), _m(A), _mr(B), _mr(C), _m(D), _m(dt_bias), _mr(z), _m(seq_idx), _m(initial_state),
            _m(final_state), _m(out), dt_softplus, nseq, state_dtype)
     plan = _PLANS.get(key)
@@ -418,11 +439,11 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
                                      x, dt, A, B, C, D, dt_bias, z, dt_softplus, seq_idx, nseq, state_dtype,
                                      dict(initial_state=initial_state, final_state=final_state), dict(out=out)))
     if out is None:
-        out = _new(plan.shape, plan.dtype, plan.dev)
+        out = _new(plan.out)
     if final_state is None and with_final_state:
-        final_state = _states(seq_idx is not None, plan.state, plan.state_dtype, plan.dev)
-    workspace = _space(workspace, plan.sizes[0], plan.dev)
-    saved = _new((plan.sizes[1],), torch.uint8, plan.dev) if save_for_backward else None
+        final_state = _states(seq_idx is not None, plan.state)
+    workspace = _space(workspace, plan.spaces[0])
+    saved = _new(plan.spaces[1]) if save_for_backward else None
     plan.call(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(dt_bias), _p(z), _p(seq_idx),
               _p(initial_state), out.data_ptr(), _p(final_state), _p(saved), workspace.data_ptr(), workspace.numel())
     return (out, final_state, saved) if save_for_backward else (out, final_state)
@@ -442,12 +463,11 @@ def selective_scan_backward(dout, x, dt, A, B, C, D=None, dt_bias=None, z=None, 
                                                           "ssd_selective_scan_saved_size"),
                           x, dt, A, B, C, D, dt_bias, z, dt_softplus, seq_idx, nseq, state_dtype,
                           dict(initial_state=initial_state, dfinal_state=dfinal_state), dict(dout=dout))
-        _same(plan.dev, torch.uint8, saved=(saved, (plan.sizes[1],)))
+        _same(plan.dev, torch.uint8, saved=(saved, plan.spaces[1][0]))
         _keep(key, plan)
-    like = lambda t: None if t is None else _new(t.shape, t.dtype, plan.dev)  # noqa: E731
-    g = ScanGrads(like(x), like(dt), like(A), like(B), like(C), like(D), like(dt_bias), like(z),
-                  None if initial_state is None else _states(seq_idx is not None, plan.state, plan.state_dtype, plan.dev))
-    workspace = _space(workspace, plan.sizes[0], plan.dev)
+    g = ScanGrads(*[None if n is None else _new(n) for n in plan.new],
+                  None if initial_state is None else _states(seq_idx is not None, plan.state))
+    workspace = _space(workspace, plan.spaces[0])
     plan.call(dout.data_ptr(), _p(dfinal_state), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D),
               _p(dt_bias), _p(z), _p(seq_idx), _p(initial_state), saved.data_ptr(), g.dx.data_ptr(), g.ddt.data_ptr(),
               g.dA.data_ptr(), g.dB.data_ptr(), g.dC.data_ptr(), _p(g.dD), _p(g.ddt_bias), _p(g.dz), _p(g.dinitial_state),
@@ -464,7 +484,7 @@ def _scan_step_plan(x, dt, A, B, C, D, dt_bias, z, state, slots, dt_softplus, ou
     _same(dev, state.dtype, state=(state, (state.shape[0], prm.channels, prm.dstate)))
     _same(dev, torch.int32, slots=(slots, lead))
     _same(dev, x.dtype, out=(out, x.shape))
-    return _Plan("ssd_selective_scan_step", prm, dev, x.dtype, shape=tuple(x.shape))
+    return _Plan("ssd_selective_scan_step", prm, dev, _layout(x.shape, x.dtype, dev))
 
 
 def selective_scan_step(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, state, slots=None, dt_softplus=True, out=None):
@@ -477,7 +497,7 @@ def selective_scan_step(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, state, 
     if plan is None:
         plan = _keep(key, _scan_step_plan(x, dt, A, B, C, D, dt_bias, z, state, slots, dt_softplus, out))
     if out is None:
-        out = _new(plan.shape, plan.dtype, plan.dev)
+        out = _new(plan.out)
     plan.call(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(dt_bias), _p(z),
               state.data_ptr(), _p(slots), out.data_ptr())
     return out
@@ -516,7 +536,7 @@ def _cache_plan(name, codes, scales, slots, batch, state_dtype, state):
     _same(dev, state_dtype, state=(state, shape))
     prm = CacheParams(ctypes.sizeof(CacheParams), batch, nslots, elems, elems // scales.shape[1], formats[codes.dtype],
                       _state_code(state_dtype))
-    return _Plan(name, prm, dev, state_dtype, shape=shape)
+    return _Plan(name, prm, dev, _layout(shape, state_dtype, dev))
 
 
 def state_cache_write(state, codes, scales, slots=None):
@@ -541,6 +561,6 @@ def state_cache_read(codes, scales, slots=None, *, state_dtype=None, out=None):
             state_dtype = torch.float32 if out is None else out.dtype
         plan = _keep(key, _cache_plan("ssd_state_cache_read", codes, scales, slots, batch, state_dtype, out))
     if out is None:
-        out = _new(plan.shape, plan.dtype, plan.dev)
+        out = _new(plan.out)
     plan.call(codes.data_ptr(), scales.data_ptr(), _p(slots), out.data_ptr())
     return out

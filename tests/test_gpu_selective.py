@@ -635,3 +635,41 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for o, f in got:
         assert torch.equal(o, want[0]) and torch.equal(f, want[1])
+
+
+def test_refusals_on_the_gpu():
+    """Shapes the library does not take come back as errors and leave the device usable."""
+    z = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    for bad in (lambda: ssd.selective_scan(z(1, 4, 8), z(1, 4, 8), z(8, 24), z(1, 4, 1, 24), z(1, 4, 1, 24)),
+                lambda: ssd.selective_scan(z(1, 0, 8), z(1, 0, 8), z(8, 16), z(1, 0, 1, 16), z(1, 0, 1, 16)),
+                lambda: ssd.selective_scan(z(1, 4, 9), z(1, 4, 9), z(9, 16), z(1, 4, 2, 16), z(1, 4, 2, 16)),
+                lambda: ssd.causal_conv(z(1, 4, 8), z(8, 5)), lambda: ssd.causal_conv(z(0, 4, 8), z(8, 4))):
+        with pytest.raises(ssd.SSDError):
+            bad()
+    x = z(1, 4, 8)
+    st = z(1, 8, 16)
+    for bad in (lambda: ssd.selective_scan(x, x, z(8, 16), z(1, 4, 1, 16), z(1, 4, 1, 16), initial_state=st, final_state=st),
+                lambda: ssd.selective_scan(x, x, z(8, 16), z(1, 4, 1, 16), z(1, 4, 1, 16), workspace=z(1, t=torch.uint8))):
+        with pytest.raises(ssd.SSDError):
+            bad()
+    with pytest.raises(ValueError):
+        ssd.selective_scan(x, x.half(), z(8, 16), z(1, 4, 1, 16), z(1, 4, 1, 16))
+    with pytest.raises(ValueError):
+        ssd.selective_scan(x, x.cpu(), z(8, 16), z(1, 4, 1, 16), z(1, 4, 1, 16))
+    out, _ = ssd.causal_conv(x + 1, torch.ones(8, 4, device="cuda"), activation=None)
+    assert out[0, :, 0].tolist() == [1, 2, 3, 4]
+
+
+def test_growing_states_over_splits():
+    """Negative steps grow the state; a zero state stays zero over a split whose decays' product overflows."""
+    L, D, N = 4096, 64, 16
+    x = torch.zeros(1, L, D, device="cuda")
+    x[:, -1] = 1
+    dt = torch.full((1, L, D), -1.0, device="cuda")
+    A = -torch.ones(D, N, device="cuda")
+    B = torch.ones(1, L, 1, N, device="cuda")
+    out, fin, saved = ssd.selective_scan(x, dt, A, B, B, dt_softplus=False, save_for_backward=True)
+    g = ssd.selective_scan_backward(x, x, dt, A, B, B, saved=saved, dt_softplus=False)
+    torch.cuda.synchronize()
+    assert not out[:, :-1].any() and bool((out[:, -1] == -N).all()) and bool((fin == -1).all())
+    assert bool((g.dC[0, -1] == -D).all()) and bool((g.dx[0, -1] == -N).all())

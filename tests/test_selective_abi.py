@@ -227,3 +227,15 @@ def test_row_views():
                 torch.zeros(1, 1, 8).expand(3, 5, 8)):
         with pytest.raises(ValueError):
             rows(bad)
+
+
+def test_refused_parameters_keep_their_status():
+    """A plan that the library refuses raises with the library's own status (CPU: the checks come before any call)."""
+    prm = scan_prm(seqlen=0)
+    with pytest.raises(ssd.SSDError) as e:
+        selective._Plan("ssd_selective_scan", prm, torch.device("cpu"), spaces=("ssd_selective_scan_workspace_size",))
+    assert e.value.code == SHAPE
+    with pytest.raises(ssd.SSDError) as e:
+        selective._Plan("ssd_selective_scan", scan_prm(dstate=24), torch.device("cpu"),
+                        spaces=("ssd_selective_scan_workspace_size",))
+    assert e.value.code == UNSUP
