@@ -13,6 +13,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmamba_ssd.so")
+META = os.path.join(HERE, "_meta.so")  # Python module: tensors' metadata (host code against torch's headers)
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = (["ssd_api.cpp", "ssd_noalloc.hip", "ssd_common.hip", "ssd_decode.hip", "ssd_block.hip", "ssd_select_api.cpp",
@@ -30,10 +31,27 @@ CFLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-fvisibility=
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
 
+def _meta_command(out):
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+             "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+            + ["-isystem" + d for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]]
+            + [os.path.join(CSRC, "ssd_meta.cpp"), "-o", out, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"])
+
+
 def build(force=True, verbose=False):
-    """Compile every HIP translation unit and link the shared library; returns its path."""
+    """Compile every HIP translation unit and link the shared library; returns its path.  Compiles the _meta module
+    beside it."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs, procs = [], []
+    meta_src, meta_tmp = os.path.join(CSRC, "ssd_meta.cpp"), META + ".tmp%d" % os.getpid()
+    new_meta = force or not os.path.exists(META) or os.path.getmtime(META) < os.path.getmtime(meta_src)
+    if new_meta:
+        procs.append(("ssd_meta.cpp", subprocess.Popen(_meta_command(meta_tmp), stdout=subprocess.PIPE,
+                                                       stderr=subprocess.STDOUT)))
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src + ".o")
         objs.append(obj)
@@ -63,6 +81,8 @@ def build(force=True, verbose=False):
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     subprocess.run(cmd, check=True, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     os.replace(tmp, LIB)
+    if new_meta:
+        os.replace(meta_tmp, META)
     return LIB
 
 

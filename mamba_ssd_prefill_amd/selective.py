@@ -81,8 +81,8 @@ def declare(lib):
 
 # ---- helpers -------------------------------------------------------------------------------------
 # A call's checks depend on its arguments' shapes, strides, types and devices alone, so their outcome -- a plan: the
-# parameter block, the output shapes, the workspace size -- is kept under those and found again in a few
-# microseconds.  Nothing is kept about a tensor's identity or contents.
+# parameter block, the output layouts, the workspace size -- is kept under those and found again in a microsecond.
+# Nothing is kept about a tensor's identity, address or contents.
 _PLANS = {}
 _MAX_PLANS = 512
 
@@ -159,14 +159,19 @@ def _keep(key, plan):
     return plan
 
 
-def _m(t):
-    """What a plan depends on of a tensor that has to be contiguous."""
-    return None if t is None else (t.shape, t.dtype, t.device, t.is_contiguous())
-
-
-def _mr(t):
-    """What a plan depends on of a tensor whose rows may be views."""
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+def _meta(*tensors):
+    """(key, addresses) of the tensors of a call, None for those not given: the native module _meta, bound at the first
+    call (built with the library; like it, there is no fallback)."""
+    global _meta
+    load_library()
+    import torch  # noqa: F401  (its libraries have to be loaded first)
+    try:
+        from ._meta import meta
+    except ImportError as e:
+        raise RuntimeError("mamba_ssd_prefill_amd._meta is not built (%s); run `python -m mamba_ssd_prefill_amd.build`"
+                           % e) from e
+    _meta = meta
+    return meta(*tensors)
 
 
 def _p(t):
@@ -329,7 +334,8 @@ def causal_conv(x, weight, bias=None, *, activation="silu", seq_idx=None, nseq=N
     ``splits`` (up to three channel counts) makes ``out`` a tuple of contiguous tensors, e.g. the x, B and C
     of an SSD block.  States [B or nseq, Ch, W-1] hold the inputs before (after) a sequence, oldest first."""
     splits = splits if splits is None else tuple(splits)
-    key = ("conv", _mr(x), _m(weight), _m(bias), _m(seq_idx), _m(initial_state), _m(final_state), activation, nseq, splits)
+    meta, (px, pw, pb, ps, ph, pf) = _meta(x, weight, bias, seq_idx, initial_state, final_state)
+    key = ("conv", meta, activation, nseq, splits)
     plan = _PLANS.get(key)
     if plan is None:
         plan = _keep(key, _conv_plan("ssd_causal_conv", (), x, weight, bias, activation, seq_idx, nseq, splits,
@@ -337,7 +343,8 @@ def causal_conv(x, weight, bias=None, *, activation="silu", seq_idx=None, nseq=N
     outs, ptrs = _outs(plan)
     if final_state is None and with_final_state:
         final_state = _states(seq_idx is not None, plan.state)
-    plan.call(x.data_ptr(), weight.data_ptr(), _p(bias), _p(seq_idx), _p(initial_state), *ptrs, _p(final_state))
+        pf = final_state.data_ptr()
+    plan.call(px, pw, pb, ps, ph, *ptrs, pf)
     return (outs[0] if splits is None else outs), final_state
 
 
@@ -348,8 +355,8 @@ def causal_conv_backward(dout, x, weight, bias=None, *, activation="silu", seq_i
     where bias and initial_state are."""
     splits = splits if splits is None else tuple(splits)
     douts = (dout,) if splits is None else tuple(dout)
-    key = ("conv backward", _mr(x), _m(weight), _m(bias), _m(seq_idx), _m(initial_state), _m(dfinal_state), activation,
-           nseq, splits, *[_m(d) for d in douts])
+    meta, (px, pw, pb, ps, ph, pf, *pd) = _meta(x, weight, bias, seq_idx, initial_state, dfinal_state, *douts)
+    key = ("conv backward", meta, activation, nseq, splits)
     plan = _PLANS.get(key)
     if plan is None:
         plan = _keep(key, _conv_plan("ssd_causal_conv_backward", ("ssd_causal_conv_backward_workspace_size",), x, weight,
@@ -359,8 +366,8 @@ def causal_conv_backward(dout, x, weight, bias=None, *, activation="silu", seq_i
     db = None if bias is None else _new(plan.new[1])
     dh = None if initial_state is None else _states(seq_idx is not None, plan.state)
     workspace = _space(workspace, plan.spaces[0])
-    plan.call(*_three(douts), _p(dfinal_state), x.data_ptr(), weight.data_ptr(), _p(bias), _p(seq_idx), _p(initial_state),
-              dx.data_ptr(), dw.data_ptr(), _p(db), _p(dh), workspace.data_ptr(), workspace.numel())
+    plan.call(*pd, *[None] * (3 - len(pd)), pf, px, pw, pb, ps, ph, dx.data_ptr(), dw.data_ptr(), _p(db), _p(dh),
+              workspace.data_ptr(), workspace.numel())
     return ConvGrads(dx, dw, db, dh)
 
 
@@ -380,12 +387,13 @@ def causal_conv_step(x, weight, bias=None, *, state, activation="silu", slots=No
     uses state ``slots[b]`` (int32; None: state b).  A row whose slot is not in [0, nslots) touches no
     state and returns zeros.  Returns out (a tuple with ``splits``)."""
     splits = splits if splits is None else tuple(splits)
-    key = ("conv step", _mr(x), _m(weight), _m(bias), _m(state), _m(slots), activation, splits)
+    meta, (px, pw, pb, pst, psl) = _meta(x, weight, bias, state, slots)
+    key = ("conv step", meta, activation, splits)
     plan = _PLANS.get(key)
     if plan is None:
         plan = _keep(key, _conv_step_plan(x, weight, bias, activation, splits, state, slots))
     outs, ptrs = _outs(plan)
-    plan.call(x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(), _p(slots), *ptrs)
+    plan.call(px, pw, pb, pst, psl, *ptrs)
     return outs[0] if splits is None else outs
 
 
@@ -430,8 +438,9 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
     """ssd_selective_scan over a prompt: x, dt, z [B, L, D], A [D, N] float32, B, C [B, L, G, N], D and dt_bias [D]
     float32.  Returns (out [B, L, D], final_state [B or nseq, D, N]), and with ``save_for_backward`` a third
     tensor for selective_scan_backward.  ``state_dtype`` defaults to initial_state's, else float32."""
-    key = ("scan", _mr(x), _mr(dt), _m(A), _mr(B), _mr(C), _m(D), _m(dt_bias), _mr(z), _m(seq_idx), _m(initial_state),
-           _m(final_state), _m(out), dt_softplus, nseq, state_dtype)
+    meta, (px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, pf, po) = _meta(x, dt, A, B, C, D, dt_bias, z, seq_idx, initial_state,
+                                                                    final_state, out)
+    key = ("scan", meta, dt_softplus, nseq, state_dtype)
     plan = _PLANS.get(key)
     if plan is None:
         plan = _keep(key, _scan_plan("ssd_selective_scan", ("ssd_selective_scan_workspace_size",
@@ -440,12 +449,13 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
                                      dict(initial_state=initial_state, final_state=final_state), dict(out=out)))
     if out is None:
         out = _new(plan.out)
+        po = out.data_ptr()
     if final_state is None and with_final_state:
         final_state = _states(seq_idx is not None, plan.state)
+        pf = final_state.data_ptr()
     workspace = _space(workspace, plan.spaces[0])
     saved = _new(plan.spaces[1]) if save_for_backward else None
-    plan.call(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(dt_bias), _p(z), _p(seq_idx),
-              _p(initial_state), out.data_ptr(), _p(final_state), _p(saved), workspace.data_ptr(), workspace.numel())
+    plan.call(px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, po, pf, _p(saved), workspace.data_ptr(), workspace.numel())
     return (out, final_state, saved) if save_for_backward else (out, final_state)
 
 
@@ -455,8 +465,9 @@ def selective_scan_backward(dout, x, dt, A, B, C, D=None, dt_bias=None, z=None, 
     forward's inputs and the ``saved`` tensor it returned.  ddt is the gradient of the raw dt.  dD, ddt_bias,
     dz and dinitial_state are None where the input is."""
     import torch
-    key = ("scan backward", _mr(x), _mr(dt), _m(A), _mr(B), _mr(C), _m(D), _m(dt_bias), _mr(z), _m(seq_idx),
-           _m(initial_state), _m(dfinal_state), _m(dout), _m(saved), dt_softplus, nseq, state_dtype)
+    meta, (pg, px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, pf, psv) = _meta(dout, x, dt, A, B, C, D, dt_bias, z, seq_idx,
+                                                                         initial_state, dfinal_state, saved)
+    key = ("scan backward", meta, dt_softplus, nseq, state_dtype)
     plan = _PLANS.get(key)
     if plan is None:
         plan = _scan_plan("ssd_selective_scan_backward", ("ssd_selective_scan_backward_workspace_size",
@@ -468,9 +479,8 @@ def selective_scan_backward(dout, x, dt, A, B, C, D=None, dt_bias=None, z=None, 
     g = ScanGrads(*[None if n is None else _new(n) for n in plan.new],
                   None if initial_state is None else _states(seq_idx is not None, plan.state))
     workspace = _space(workspace, plan.spaces[0])
-    plan.call(dout.data_ptr(), _p(dfinal_state), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D),
-              _p(dt_bias), _p(z), _p(seq_idx), _p(initial_state), saved.data_ptr(), g.dx.data_ptr(), g.ddt.data_ptr(),
-              g.dA.data_ptr(), g.dB.data_ptr(), g.dC.data_ptr(), _p(g.dD), _p(g.ddt_bias), _p(g.dz), _p(g.dinitial_state),
+    plan.call(pg, pf, px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, psv, g.dx.data_ptr(), g.ddt.data_ptr(), g.dA.data_ptr(),
+              g.dB.data_ptr(), g.dC.data_ptr(), _p(g.dD), _p(g.ddt_bias), _p(g.dz), _p(g.dinitial_state),
               workspace.data_ptr(), workspace.numel())
     return g
 
@@ -491,15 +501,15 @@ def selective_scan_step(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, state, 
     """ssd_selective_scan_step: one token per row; x, dt, z [B, D], B, C [B, G, N].  ``state`` [nslots, D, N] is
     updated in place; row b uses state ``slots[b]`` (int32; None: state b).  A row whose slot is not in
     [0, nslots) touches no state and returns zeros.  Returns out [B, D]."""
-    key = ("scan step", _mr(x), _mr(dt), _m(A), _mr(B), _mr(C), _m(D), _m(dt_bias), _mr(z), _m(state), _m(slots), _m(out),
-           dt_softplus)
+    meta, (px, pdt, pA, pB, pC, pD, pb, pz, pst, psl, po) = _meta(x, dt, A, B, C, D, dt_bias, z, state, slots, out)
+    key = ("scan step", meta, dt_softplus)
     plan = _PLANS.get(key)
     if plan is None:
         plan = _keep(key, _scan_step_plan(x, dt, A, B, C, D, dt_bias, z, state, slots, dt_softplus, out))
     if out is None:
         out = _new(plan.out)
-    plan.call(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(dt_bias), _p(z),
-              state.data_ptr(), _p(slots), out.data_ptr())
+        po = out.data_ptr()
+    plan.call(px, pdt, pA, pB, pC, pD, pb, pz, pst, psl, po)
     return out
 
 
@@ -542,18 +552,20 @@ def _cache_plan(name, codes, scales, slots, batch, state_dtype, state):
 def state_cache_write(state, codes, scales, slots=None):
     """ssd_state_cache_write: state [B, ...] (float32, float16 or bfloat16) into the slots ``slots[b]`` (int32;
     None: b) of a pool made by state_cache.  Rows whose slot is not in [0, nslots) are skipped."""
-    key = ("cache write", _m(state), _m(codes), _m(scales), _m(slots))
+    meta, (ps, pc, psc, psl) = _meta(state, codes, scales, slots)
+    key = ("cache write", meta)
     plan = _PLANS.get(key)
     if plan is None:
         plan = _keep(key, _cache_plan("ssd_state_cache_write", codes, scales, slots, state.shape[0], state.dtype, state))
-    plan.call(state.data_ptr(), _p(slots), codes.data_ptr(), scales.data_ptr())
+    plan.call(ps, psl, pc, psc)
 
 
 def state_cache_read(codes, scales, slots=None, *, state_dtype=None, out=None):
     """ssd_state_cache_read: the states of ``slots`` (int32 [B]; None: every slot), in ``state_dtype`` (default
     float32) or into ``out`` [B, ...].  A row whose slot is not in [0, nslots) reads a zero state."""
     import torch
-    key = ("cache read", _m(codes), _m(scales), _m(slots), _m(out), state_dtype)
+    meta, (pc, psc, psl, po) = _meta(codes, scales, slots, out)
+    key = ("cache read", meta, state_dtype)
     plan = _PLANS.get(key)
     if plan is None:
         batch = codes.shape[0] if slots is None and out is None else (out if slots is None else slots).shape[0]
@@ -562,5 +574,6 @@ def state_cache_read(codes, scales, slots=None, *, state_dtype=None, out=None):
         plan = _keep(key, _cache_plan("ssd_state_cache_read", codes, scales, slots, batch, state_dtype, out))
     if out is None:
         out = _new(plan.out)
-    plan.call(codes.data_ptr(), scales.data_ptr(), _p(slots), out.data_ptr())
+        po = out.data_ptr()
+    plan.call(pc, psc, psl, po)
     return out

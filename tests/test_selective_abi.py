@@ -239,3 +239,21 @@ def test_refused_parameters_keep_their_status():
         selective._Plan("ssd_selective_scan", scan_prm(dstate=24), torch.device("cpu"),
                         spaces=("ssd_selective_scan_workspace_size",))
     assert e.value.code == UNSUP
+
+
+def test_meta_tells_calls_apart():
+    """Equal keys for tensors that pass the same checks, others for another size, stride, type or place; addresses as
+    they are; other things than tensors are refused."""
+    from mamba_ssd_prefill_amd._meta import meta
+    x, y = torch.zeros(2, 3), torch.ones(2, 3)
+    key, (px, none, pv) = meta(x, None, x[:, 1:])
+    assert (px, none, pv) == (x.data_ptr(), None, x.data_ptr() + 4)
+    assert key == meta(y, None, y[:, 1:])[0]
+    keys = [meta(*a)[0] for a in ((x,), (x.t(),), (x.half(),), (x.view(6),), (x, None), (None, x), (None, None), (),
+                                  (x[:, :2],), (x[:1],), (x.view(1, 2, 3),))]
+    assert len(set(keys)) == len(keys)
+    for bad in (3, "x", [x]):
+        with pytest.raises(TypeError):
+            meta(x, bad)
+    with pytest.raises(ValueError):
+        meta(x.to_sparse())
