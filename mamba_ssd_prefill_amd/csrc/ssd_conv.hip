@@ -73,23 +73,18 @@ template <typename T> __device__ inline T* split_ptr(void* const* base, int sa, 
     return (T*)base[2] + row * (ch - sb) + (c0 - sb);
 }
 
-// The lane's item: a piece of CW channels and a run of a.rows tokens.  A workgroup takes 64 pieces of 4 runs that follow
-// one another (of fewer channels, 2^k pieces of 256 / 2^k runs): the rows that two runs both read then come from
-// its own XCD's L2 (2 x 4096 x 5376 forward 47 us with 256 pieces of one run, 39 us so), and the indexes need no
-// long division.
+// The lane's item: a piece of CW channels and a run of a.rows tokens.  A wave takes 64 pieces of one run, so that
+// tokens, sequence numbers and the branches on them are scalar; a workgroup takes four runs that follow one another:
+// the rows that two runs both read then come from its own XCD's L2 (2 x 4096 x 5376 forward 47 us with 256
+// pieces of one run, 39 us so).
 struct ConvItem {
     int b, c0, t0, t1;
 };
-__host__ __device__ inline int conv_piece_bits(int npc) {
-    int k = 0;
-    while (k < 6 && (1 << k) < npc) ++k;
-    return k;
-}
 template <int CW> __device__ inline bool conv_item(const CausalConvArgs& a, ConvItem* it) {
-    const int npc = a.channels / CW, bits = conv_piece_bits(npc);
-    const uint32_t pblocks = (uint32_t)(npc + (1 << bits) - 1) >> bits;
-    const int pc = (int)((blockIdx.x % pblocks) << bits) + (int)(threadIdx.x & ((1u << bits) - 1));
-    const uint32_t r = ((blockIdx.x / pblocks) << (8 - bits)) + (threadIdx.x >> bits);
+    const int npc = a.channels / CW;
+    const uint32_t pblocks = (uint32_t)(npc + 63) / 64;
+    const int pc = (int)(blockIdx.x % pblocks) * 64 + (int)(threadIdx.x & 63);
+    const uint32_t r = (blockIdx.x / pblocks) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (pc >= npc || r >= (uint32_t)a.batch * (uint32_t)a.nseg) return false;
     it->c0 = pc * CW;
     it->t0 = (int)(r % (uint32_t)a.nseg) * a.rows;
@@ -117,12 +112,13 @@ template <int W, int CW> struct ConvW {
 template <typename T, int W, int CW, bool VL> struct ConvWalk {
     const CausalConvArgs& a;
     const int b, c0;
-    const int32_t* seq;
+    typedef const __attribute__((address_space(4))) int32_t* Numbers;  // read through the scalar cache
+    Numbers seq;
     int q, place, qn, qnn;  // qn, qnn: the numbers of the next token and of the one after it
     float win[W - 1][CW];
 
     __device__ inline ConvWalk(const CausalConvArgs& a_, int b_, int c0_) : a(a_), b(b_), c0(c0_) {
-        seq = VL ? a.seq + (int64_t)b * a.seqlen : nullptr;
+        seq = VL ? (Numbers)(uintptr_t)(a.seq + (int64_t)b * a.seqlen) : (Numbers)0;
     }
     __device__ inline const T* row(int t) const { return (const T*)a.x + ((int64_t)b * a.seqlen + t) * a.xs + c0; }
     __device__ inline bool has_state(int n) const { return n >= 0 && n < (VL ? a.nseq : a.batch); }
@@ -130,7 +126,7 @@ template <typename T, int W, int CW, bool VL> struct ConvWalk {
     __device__ inline void load_state(int done) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            if (j + done > W - 2) continue;
+            if (j + done > W - 2) continue;  // an input of the sequence itself
 #pragma unroll
             for (int e = 0; e < CW; ++e)
                 win[j][e] = a.h0 && has_state(q)
@@ -138,19 +134,29 @@ template <typename T, int W, int CW, bool VL> struct ConvWalk {
                                 : 0.f;
         }
     }
-    // stand before token t
+    // stand before token t: the loads first, all at once (rows before the batch row's first are its first)
     __device__ inline void start(int t) {
-        q = VL ? seq[t] : b;
-        if (VL) {
-            qn = q;
+        typename ConvPiece<T, CW>::type before[W - 1];
+        int number[W];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) before[j] = load_raw<T, CW>(row(max(t - (W - 1) + j, 0)));
+        if constexpr (VL) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) number[j] = seq[max(t - j, 0)];
             qnn = seq[min(t + 1, a.seqlen - 1)];
+            q = qn = number[0];
+        } else {
+            q = b;
         }
         place = 0;
-        while (place < W - 1 && t - place > 0 && (!VL || seq[t - place - 1] == q)) ++place;
-        load_state(place);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)  // the inputs of this sequence before t
-            if (W - 1 - j <= place) load_cw<T, CW>(row(t - (W - 1) + j), win[j]);
+        for (int j = 1; j < W; ++j)
+            if (place == j - 1 && t >= j && (!VL || number[j] == q)) place = j;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < CW; ++e) win[j][e] = (float)before[j][e];
+        if (place < W - 1) load_state(place);
     }
     // begin with token t, coming from t - 1 (or from start(t))
     __device__ inline void step_to(int t) {
@@ -435,9 +441,8 @@ static bool conv_vec4(const CausalConvArgs& a, size_t es, const void* const* ten
 }
 
 static unsigned conv_blocks(const CausalConvArgs& a, int cw) {
-    const int npc = a.channels / cw, bits = conv_piece_bits(npc), per = 256 >> bits;
-    const int64_t pblocks = (npc + (1 << bits) - 1) >> bits, runs = (int64_t)a.batch * a.nseg;
-    return (unsigned)(pblocks * ((runs + per - 1) / per));
+    const int64_t pblocks = (a.channels / cw + 63) / 64, runs = (int64_t)a.batch * a.nseg;
+    return (unsigned)(pblocks * ((runs + 3) / 4));
 }
 
 template <typename T, int W> hipError_t launch_conv_tw(CausalConvArgs& a, hipStream_t st) {
