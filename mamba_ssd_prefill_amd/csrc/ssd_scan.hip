@@ -71,6 +71,11 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
     for (int tile = tile0; tile < tile1; ++tile) {
         const int t0 = tile * kTile;
         const ScanTokens<T, TPW, true> cur = next;
+        const Rows rb((const T*)a.B + p.g * N + n0, a.Bs, p.row0, t0, a.seqlen);
+        const Rows rc((const T*)a.C + p.g * N + n0, a.Cs, p.row0, t0, a.seqlen);
+        typename Rows::Group gb[2], gc[2];
+        gb[0].load(rb, 0);
+        gc[0].load(rc, 0);
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             const int k = w + j * NW;
@@ -83,11 +88,6 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
         if (VL) m = seq_masks<kTile>(a, p.row0, t0);
         __syncthreads();
         next.load(a, p, t0 + kTile, w, NW);
-        const Rows rb((const T*)a.B + p.g * N + n0, a.Bs, p.row0, t0, a.seqlen);
-        const Rows rc((const T*)a.C + p.g * N + n0, a.Cs, p.row0, t0, a.seqlen);
-        typename Rows::Group gb[2], gc[2];
-        gb[0].load(rb, 0);
-        gc[0].load(rc, 0);
 #pragma unroll
         for (int k = 0; k < kTile; ++k) {
             if (k % GT == 0 && k + GT < kTile) {
@@ -175,13 +175,13 @@ __global__ __launch_bounds__(NW * 64) void k_scan_carry(ScanArgs a) {
     prepare(0);
     for (int tile = tile0; tile < tile1; ++tile) {
         const int t0 = tile * kTile, buf = (tile - tile0) & 1;
+        const Rows rb((const T*)a.B + p.g * N + n0, a.Bs, p.row0, t0, a.seqlen);
+        typename Rows::Group gb[2];
+        gb[0].load(rb, 0);
         next.load(a, p, t0 + kTile, w, NW);
         SeqMasks m{0, 0};
         if (VL) m = seq_masks<kTile>(a, p.row0, t0);
         __syncthreads();
-        const Rows rb((const T*)a.B + p.g * N + n0, a.Bs, p.row0, t0, a.seqlen);
-        typename Rows::Group gb[2];
-        gb[0].load(rb, 0);
         float part = 0.f;
 #pragma unroll
         for (int k = 0; k < kTile; ++k) {
@@ -316,7 +316,8 @@ struct TileTime {
 int scan_splits(int64_t batch, int64_t seqlen, int64_t channels, int groups, int dstate, bool backward) {
     const TileTime main_pass = backward ? TileTime{2.9, 0.95, 1.64, 3} : TileTime{2.4, 0.6, 0.94, 6};
     const TileTime carry = backward ? TileTime{1.4, 0.25, 0.39, 8} : TileTime{1.9, 0.45, 0.65, 7};
-    const double launches = backward ? 7 : 5, each = 0.1;  // the passes' own launches, and each split's part in the join
+    // the passes' own launches, and each split's part in the join (its states written and read twice at 5 MB a us)
+    const double launches = backward ? 7 : 5, each = 0.05 + (double)batch * channels * dstate * 8 / 5e6;
     const int64_t dg = channels / groups, blocks = batch * groups * ((dg + 63) / 64);
     const int64_t tile = backward ? kScanPeriod : kTile, tiles = (seqlen + tile - 1) / tile;
     const int waves = dstate == 8 ? 2 : dstate == 16 ? 4 : 8;  // of a workgroup

@@ -139,6 +139,11 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
         const ScanArgs& a = args_again();
         const int t0 = tile * TB;
         const BackTokens<T, TPW> cur = next;
+        const Rows rb((const T*)a.B + p.g * N + n0, a.Bs, p.row0, t0, a.seqlen);
+        const Rows rc((const T*)a.C + p.g * N + n0, a.Cs, p.row0, t0, a.seqlen);
+        typename Rows::Group gb[2], gc[2];
+        gb[0].load(rb, 0);
+        gc[0].load(rc, 0);
         float hin[NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) hin[i] = hnext[i];
@@ -157,11 +162,6 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
 
         // the tile's states and decays again
         float h[TB][NS], e[TB][NS];
-        const Rows rb((const T*)a.B + p.g * N + n0, a.Bs, p.row0, t0, a.seqlen);
-        const Rows rc((const T*)a.C + p.g * N + n0, a.Cs, p.row0, t0, a.seqlen);
-        typename Rows::Group gb[2], gc[2];
-        gb[0].load(rb, 0);
-        gc[0].load(rc, 0);
 #pragma unroll
         for (int k = 0; k < TB; ++k) {
             if (k % GT == 0 && k + GT < TB) {
@@ -195,8 +195,6 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
         float dAt[NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) dAt[i] = 0.f;
-        gb[(TB / GT - 1) & 1].load(rb, TB - GT);
-        gc[(TB / GT - 1) & 1].load(rc, TB - GT);
 #pragma unroll
         for (int k = TB - 1; k >= 0; --k) {
             if (k == TB / 2 - 1) {  // half of the tile's states and decays are used up: room for the next tile's inputs
@@ -204,7 +202,7 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
                 next.load(a, p, t0 - TB, w, NW);
                 load_states<NS>(a.saved, DT_F32, ((int64_t)p.b * a.ntiles + max(tile - 1, 0)) * sstride + soff, hnext);
             }
-            if (k % GT == GT - 1 && k >= GT) {
+            if (k % GT == GT - 1 && k >= GT && k / GT < TB / GT - 1) {  // (the last two groups are still there)
                 gb[(k / GT - 1) & 1].load(rb, k - 2 * GT + 1);
                 gc[(k / GT - 1) & 1].load(rc, k - 2 * GT + 1);
             }
@@ -359,13 +357,13 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward_carry(ScanArgs a) {
     prepare(0, (tile1 - 1) * TB);
     for (int tile = tile1 - 1; tile >= tile0; --tile) {
         const int t0 = tile * TB, buf = (tile1 - 1 - tile) & 1;
+        const Rows rc((const T*)a.C + p.g * N + n0, a.Cs, p.row0, t0, a.seqlen);
+        typename Rows::Group gc[2];
+        gc[(TB / GT - 1) & 1].load(rc, TB - GT);
         load(t0 - TB);
         SeqMasks m{0, 0};
         if (VL) m = seq_masks<TB>(a, p.row0, t0);
         __syncthreads();
-        const Rows rc((const T*)a.C + p.g * N + n0, a.Cs, p.row0, t0, a.seqlen);
-        typename Rows::Group gc[2];
-        gc[(TB / GT - 1) & 1].load(rc, TB - GT);
         float part = 0.f;
 #pragma unroll
         for (int k = TB - 1; k >= 0; --k) {
