@@ -1,68 +1,80 @@
-// ssd_meta.cpp -- Python module mamba_ssd_prefill_amd._meta: what a call of the selective binding depends on of its
-// tensors, read in one call.
+// ssd_meta.cpp -- Python module mamba_ssd_prefill_amd._meta: the selective binding's dealings with torch's tensors, each
+// in one call.
 //
 // meta(*tensors) -> (key, pointers): `key` holds every tensor's type, device, sizes and strides as bytes (None has an
-// entry of its own), so that two calls with equal keys pass the same checks; `pointers` their addresses (None
-// for None).  Reading these through the tensors' Python attributes took 0.5 us a tensor, longer than the
-// launch itself for the eleven of a scan step.
+// entry of its own), so that two calls with equal keys pass the same checks; `pointers` their addresses (None for
+// None).  Reading these through the tensors' Python attributes took 0.5 us a tensor, longer than the launch
+// itself for the eleven of a scan step.
+// new(*layouts) -> tensors: uninitialised tensors, each of a layout that `meta` gives as the key of one tensor.
 #include <Python.h>
+#include <ATen/ATen.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
-
-#include <exception>
+#include <torch/csrc/utils/object_ptr.h>
 
 static PyObject* meta(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    PyObject* ptrs = PyTuple_New(n);
+    HANDLE_TH_ERRORS
+    THPObjectPtr ptrs(PyTuple_New(n));
     if (!ptrs) return nullptr;
-    try {
-        c10::SmallVector<int64_t, 160> key;
-        for (Py_ssize_t i = 0; i < n; ++i) {
-            if (args[i] == Py_None) {
-                key.push_back(-1);
-                Py_INCREF(Py_None);
-                PyTuple_SET_ITEM(ptrs, i, Py_None);
-                continue;
-            }
-            if (!THPVariable_Check(args[i])) {
-                PyErr_Format(PyExc_TypeError, "expected a tensor or None, got %s", Py_TYPE(args[i])->tp_name);
-                Py_DECREF(ptrs);
-                return nullptr;
-            }
-            const at::Tensor& t = THPVariable_Unpack(args[i]);
-            if (t.layout() != at::kStrided) {
-                PyErr_SetString(PyExc_ValueError, "expected a strided tensor");
-                Py_DECREF(ptrs);
-                return nullptr;
-            }
-            const c10::Device d = t.device();
-            key.push_back((int64_t)t.dim() << 32 | (int64_t)(uint8_t)t.scalar_type() << 16 |
-                          (int64_t)(uint8_t)d.type() << 8 | (uint8_t)d.index());
-            for (int64_t s : t.sizes()) key.push_back(s);
-            for (int64_t s : t.strides()) key.push_back(s);
-            PyObject* p = PyLong_FromUnsignedLongLong((unsigned long long)(uintptr_t)t.data_ptr());
-            if (!p) {
-                Py_DECREF(ptrs);
-                return nullptr;
-            }
-            PyTuple_SET_ITEM(ptrs, i, p);
+    c10::SmallVector<int64_t, 160> key;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (args[i] == Py_None) {
+            key.push_back(-1);
+            Py_INCREF(Py_None);
+            PyTuple_SET_ITEM(ptrs.get(), i, Py_None);
+            continue;
         }
-        PyObject* bytes = PyBytes_FromStringAndSize((const char*)key.data(), (Py_ssize_t)(key.size() * sizeof(int64_t)));
-        PyObject* out = bytes ? PyTuple_Pack(2, bytes, ptrs) : nullptr;
-        Py_XDECREF(bytes);
-        Py_DECREF(ptrs);
-        return out;
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-    } catch (...) {
-        PyErr_SetString(PyExc_RuntimeError, "a tensor could not be read");
+        if (!THPVariable_Check(args[i])) {
+            PyErr_Format(PyExc_TypeError, "expected a tensor or None, got %s", Py_TYPE(args[i])->tp_name);
+            return nullptr;
+        }
+        const at::Tensor& t = THPVariable_Unpack(args[i]);
+        if (t.layout() != at::kStrided) {
+            PyErr_SetString(PyExc_ValueError, "expected a strided tensor");
+            return nullptr;
+        }
+        const c10::Device d = t.device();
+        key.push_back((int64_t)t.dim() << 32 | (int64_t)(uint8_t)t.scalar_type() << 16 | (int64_t)(uint8_t)d.type() << 8 |
+                      (uint8_t)d.index());
+        for (int64_t s : t.sizes()) key.push_back(s);
+        for (int64_t s : t.strides()) key.push_back(s);
+        PyObject* p = PyLong_FromUnsignedLongLong((unsigned long long)(uintptr_t)t.data_ptr());
+        if (!p) return nullptr;
+        PyTuple_SET_ITEM(ptrs.get(), i, p);
     }
-    Py_DECREF(ptrs);
-    return nullptr;
+    THPObjectPtr bytes(PyBytes_FromStringAndSize((const char*)key.data(), (Py_ssize_t)(key.size() * sizeof(int64_t))));
+    return bytes ? PyTuple_Pack(2, bytes.get(), ptrs.get()) : nullptr;
+    END_HANDLE_TH_ERRORS
+}
+
+static PyObject* new_tensors(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    THPObjectPtr out(PyTuple_New(n));
+    if (!out) return nullptr;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const int64_t* v = PyBytes_Check(args[i]) ? (const int64_t*)PyBytes_AS_STRING(args[i]) : nullptr;
+        const Py_ssize_t words = v ? PyBytes_GET_SIZE(args[i]) / (Py_ssize_t)sizeof(int64_t) : 0;
+        const int64_t dim = words ? v[0] >> 32 : -1;
+        if (dim < 0 || words != 1 + 2 * dim) {
+            PyErr_SetString(PyExc_ValueError, "expected the layout of one tensor");
+            return nullptr;
+        }
+        const c10::Device device((c10::DeviceType)(uint8_t)(v[0] >> 8), (c10::DeviceIndex)(int8_t)v[0]);
+        const auto options = at::TensorOptions().dtype((at::ScalarType)(uint8_t)(v[0] >> 16)).device(device);
+        PyObject* t = THPVariable_Wrap(
+            at::empty_strided(at::IntArrayRef(v + 1, (size_t)dim), at::IntArrayRef(v + 1 + dim, (size_t)dim), options));
+        if (!t) return nullptr;
+        PyTuple_SET_ITEM(out.get(), i, t);
+    }
+    return out.release();
+    END_HANDLE_TH_ERRORS
 }
 
 static PyMethodDef methods[] = {
     {"meta", (PyCFunction)(void (*)(void))meta, METH_FASTCALL, "meta(*tensors) -> (key, pointers)"},
+    {"new", (PyCFunction)(void (*)(void))new_tensors, METH_FASTCALL, "new(*layouts) -> uninitialised tensors"},
     {nullptr, nullptr, 0, nullptr},
 };
-static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_meta", "Tensors' metadata in one call.", -1, methods,
+static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_meta", "Tensors' metadata, and new tensors, in one call.", -1, methods,
                              nullptr, nullptr, nullptr, nullptr};
 PyMODINIT_FUNC PyInit__meta(void) { return PyModule_Create(&module); }

@@ -23,6 +23,7 @@ states then have one entry per number instead of one per batch row.
 """
 import collections
 import ctypes
+import struct
 
 from . import SSDError, _dtype_code, load_library
 
@@ -88,7 +89,7 @@ _MAX_PLANS = 512
 
 
 class _Plan:
-    __slots__ = ("prm", "ref", "fn", "name", "dev", "index", "out", "parts", "state", "spaces", "new")
+    __slots__ = ("prm", "ref", "fn", "name", "dev", "index", "out", "parts", "state", "sizes", "spaces", "new")
 
     def __init__(self, name, prm, dev, out=None, parts=None, state=None, spaces=(), new=()):
         import torch
@@ -96,12 +97,13 @@ class _Plan:
         self.fn, self.index = getattr(load_library(), name), dev.index
         # layouts of the output like x, of one output per split, of the states, and of other new tensors
         self.out, self.parts, self.state, self.new = out, parts, state, new
-        self.spaces = []
+        self.sizes = []
         for s in spaces:
             n = getattr(load_library(), s)(self.ref)
             if n == 0:  # parameters the library does not take: its own call says why, before it looks at a pointer
                 raise SSDError(self.fn(self.ref, *[0] * (len(self.fn.argtypes) - 1)), name)
-            self.spaces.append(_layout((n,), torch.uint8, dev))
+            self.sizes.append(n)
+        self.spaces = [_layout((n,), torch.uint8, dev) for n in self.sizes]
 
     def call(self, *args):
         """One C call on the current stream of the tensors' device, with that device current."""
@@ -117,39 +119,53 @@ class _Plan:
             raise SSDError(rc, self.name)
 
 
-# torch's calls for a tensor's memory, the current device and its current stream's handle (bound at the first call)
-_empty = _device = _raw = None
+# torch's calls for the current device and its current stream's handle (bound at the first call)
+_device = _raw = None
 
 
 def _bind():
     import torch
-    global _empty, _device, _raw
+    global _device, _raw
     torch.cuda.init()
-    _empty = torch.empty_strided
     _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _strides(shape):
-    out, n = [], 1
-    for d in reversed(shape):
-        out.append(n)
-        n *= d
-    return tuple(out[::-1])
+def _native():
+    """The native module _meta (built with the library; like it, there is no fallback), its functions put in place of the
+    two stand-ins below."""
+    global _meta, _new
+    load_library()
+    import torch  # noqa: F401  (its libraries have to be loaded first)
+    try:
+        from . import _meta as m
+    except ImportError as e:
+        raise RuntimeError("mamba_ssd_prefill_amd._meta is not built (%s); run `python -m mamba_ssd_prefill_amd.build`"
+                           % e) from e
+    _meta, _new = m.meta, m.new
+    return m
+
+
+def _meta(*tensors):
+    """(key, addresses) of the tensors of a call, None for those not given."""
+    return _native().meta(*tensors)
+
+
+def _new(*layouts):
+    """New tensors of the layouts."""
+    return _native().new(*layouts)
 
 
 def _layout(shape, dtype, dev):
-    """What _new takes for a contiguous tensor."""
-    shape = tuple(shape)
-    return shape, _strides(shape), dtype, dev
-
-
-def _new(layout):
-    """A new tensor (torch.empty by a shorter way)."""
-    if _empty is None:
-        _bind()
-    return _empty(layout[0], layout[1], dtype=layout[2], device=layout[3])
+    """What _new takes for a contiguous tensor: the key of such a one."""
+    import torch
+    strides, n = [], 1
+    for d in reversed(shape):
+        strides.append(n)
+        n *= d
+    head = struct.unpack("=q", _meta(torch.empty((), dtype=dtype, device=dev))[0])[0]
+    return struct.pack("=%dq" % (1 + 2 * len(shape)), head | len(shape) << 32, *shape, *strides[::-1])
 
 
 def _keep(key, plan):
@@ -157,21 +173,6 @@ def _keep(key, plan):
         _PLANS.clear()
     _PLANS[key] = plan
     return plan
-
-
-def _meta(*tensors):
-    """(key, addresses) of the tensors of a call, None for those not given: the native module _meta, bound at the first
-    call (built with the library; like it, there is no fallback)."""
-    global _meta
-    load_library()
-    import torch  # noqa: F401  (its libraries have to be loaded first)
-    try:
-        from ._meta import meta
-    except ImportError as e:
-        raise RuntimeError("mamba_ssd_prefill_amd._meta is not built (%s); run `python -m mamba_ssd_prefill_amd.build`"
-                           % e) from e
-    _meta = meta
-    return meta(*tensors)
 
 
 def _p(t):
@@ -258,12 +259,9 @@ def _seq(seq_idx, nseq, lead, dev):
     return int(nseq)
 
 
-def _space(workspace, layout):
-    """The workspace given (the library checks its size), or a new one."""
-    if workspace is None:
-        return _new(layout)
+def _space(workspace, dev):
+    """The workspace given (the library checks its size)."""
     import torch
-    dev = layout[3]
     if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on %s" % dev)
     return workspace
@@ -271,7 +269,8 @@ def _space(workspace, layout):
 
 def _states(packed, layout):
     """A new state output; entries of numbers that no sequence uses stay zero."""
-    return _new(layout).zero_() if packed else _new(layout)
+    t, = _new(layout)
+    return t.zero_() if packed else t
 
 
 # ---- causal convolution ----------------------------------------------------------------------------
@@ -315,15 +314,12 @@ def _conv_plan(name, spaces, x, weight, bias, activation, seq_idx, nseq, splits,
         _same(dev, x.dtype, dout=(d, lead + (n,)))
     lay = lambda t: None if t is None else _layout(t.shape, t.dtype, dev)  # noqa: E731
     return _Plan(name, prm, dev, lay(x), [_layout(lead + (n,), x.dtype, dev) for n in parts], _layout(state, x.dtype, dev),
-                 spaces, [lay(weight), lay(bias)])
+                 spaces, [lay(t) for t in (weight, bias) if t is not None])
 
 
 def _outs(plan):
     """New outputs, one per split, and the three pointers the library takes."""
-    if len(plan.parts) == 1:
-        o = _new(plan.parts[0])
-        return (o,), (o.data_ptr(), None, None)
-    outs = tuple([_new(s) for s in plan.parts])
+    outs = _new(*plan.parts)
     return outs, _three(outs)
 
 
@@ -362,10 +358,10 @@ def causal_conv_backward(dout, x, weight, bias=None, *, activation="silu", seq_i
         plan = _keep(key, _conv_plan("ssd_causal_conv_backward", ("ssd_causal_conv_backward_workspace_size",), x, weight,
                                      bias, activation, seq_idx, nseq, splits,
                                      dict(initial_state=initial_state, dfinal_state=dfinal_state), douts))
-    dx, dw = _new(plan.out), _new(plan.new[0])
-    db = None if bias is None else _new(plan.new[1])
+    dx, dw, space, *db = _new(plan.out, plan.new[0], plan.spaces[0], *plan.new[1:])
+    db = db[0] if db else None
     dh = None if initial_state is None else _states(seq_idx is not None, plan.state)
-    workspace = _space(workspace, plan.spaces[0])
+    workspace = space if workspace is None else _space(workspace, plan.dev)
     plan.call(*pd, *[None] * (3 - len(pd)), pf, px, pw, pb, ps, ph, dx.data_ptr(), dw.data_ptr(), _p(db), _p(dh),
               workspace.data_ptr(), workspace.numel())
     return ConvGrads(dx, dw, db, dh)
@@ -448,13 +444,13 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
                                      x, dt, A, B, C, D, dt_bias, z, dt_softplus, seq_idx, nseq, state_dtype,
                                      dict(initial_state=initial_state, final_state=final_state), dict(out=out)))
     if out is None:
-        out = _new(plan.out)
+        out, = _new(plan.out)
         po = out.data_ptr()
     if final_state is None and with_final_state:
         final_state = _states(seq_idx is not None, plan.state)
         pf = final_state.data_ptr()
-    workspace = _space(workspace, plan.spaces[0])
-    saved = _new(plan.spaces[1]) if save_for_backward else None
+    workspace = _new(plan.spaces[0])[0] if workspace is None else _space(workspace, plan.dev)
+    saved = _new(plan.spaces[1])[0] if save_for_backward else None
     plan.call(px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, po, pf, _p(saved), workspace.data_ptr(), workspace.numel())
     return (out, final_state, saved) if save_for_backward else (out, final_state)
 
@@ -474,11 +470,12 @@ def selective_scan_backward(dout, x, dt, A, B, C, D=None, dt_bias=None, z=None, 
                                                           "ssd_selective_scan_saved_size"),
                           x, dt, A, B, C, D, dt_bias, z, dt_softplus, seq_idx, nseq, state_dtype,
                           dict(initial_state=initial_state, dfinal_state=dfinal_state), dict(dout=dout))
-        _same(plan.dev, torch.uint8, saved=(saved, plan.spaces[1][0]))
+        _same(plan.dev, torch.uint8, saved=(saved, (plan.sizes[1],)))
         _keep(key, plan)
-    g = ScanGrads(*[None if n is None else _new(n) for n in plan.new],
+    made = iter(_new(*[n for n in plan.new if n is not None]))
+    g = ScanGrads(*[None if n is None else next(made) for n in plan.new],
                   None if initial_state is None else _states(seq_idx is not None, plan.state))
-    workspace = _space(workspace, plan.spaces[0])
+    workspace = _new(plan.spaces[0])[0] if workspace is None else _space(workspace, plan.dev)
     plan.call(pg, pf, px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, psv, g.dx.data_ptr(), g.ddt.data_ptr(), g.dA.data_ptr(),
               g.dB.data_ptr(), g.dC.data_ptr(), _p(g.dD), _p(g.ddt_bias), _p(g.dz), _p(g.dinitial_state),
               workspace.data_ptr(), workspace.numel())
@@ -507,7 +504,7 @@ def selective_scan_step(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, state, 
     if plan is None:
         plan = _keep(key, _scan_step_plan(x, dt, A, B, C, D, dt_bias, z, state, slots, dt_softplus, out))
     if out is None:
-        out = _new(plan.out)
+        out, = _new(plan.out)
         po = out.data_ptr()
     plan.call(px, pdt, pA, pB, pC, pD, pb, pz, pst, psl, po)
     return out
@@ -573,7 +570,7 @@ def state_cache_read(codes, scales, slots=None, *, state_dtype=None, out=None):
             state_dtype = torch.float32 if out is None else out.dtype
         plan = _keep(key, _cache_plan("ssd_state_cache_read", codes, scales, slots, batch, state_dtype, out))
     if out is None:
-        out = _new(plan.out)
+        out, = _new(plan.out)
         po = out.data_ptr()
     plan.call(pc, psc, psl, po)
     return out

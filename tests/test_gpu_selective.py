@@ -673,3 +673,77 @@ def test_growing_states_over_splits():
     torch.cuda.synchronize()
     assert not out[:, :-1].any() and bool((out[:, -1] == -N).all()) and bool((fin == -1).all())
     assert bool((g.dC[0, -1] == -D).all()) and bool((g.dx[0, -1] == -N).all())
+
+
+def test_given_outputs_and_workspaces():
+    """Outputs and workspaces handed in are used, and states of numbers that no sequence uses stay as they were."""
+    s, seq, S, g = scan_inputs(2, 30, 70, 16, 1, "bf16", "f32", "pad", True, True, True, True, seed=51)
+    args, h0 = call_args(s)
+    kw = dict(seq_idx=seq.cuda(), nseq=S, initial_state=h0)
+    want, wfin = ssd.selective_scan(*args, **kw)
+    out, fin = torch.full_like(want, 5.0), torch.full_like(wfin, 5.0)
+    space = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    o, f = ssd.selective_scan(*args, out=out, final_state=fin, workspace=space, **kw)
+    cfin = torch.full((S, 70, 3), 5.0, dtype=torch.bfloat16, device="cuda")
+    cw, cb = torch.randn(70, 4, generator=g).cuda(), torch.randn(70, generator=g).cuda()
+    _, cf = ssd.causal_conv(args[0], cw, cb, seq_idx=kw["seq_idx"], nseq=S, final_state=cfin)
+    gr = [ssd.causal_conv_backward(want, args[0], cw, cb, seq_idx=kw["seq_idx"], nseq=S, workspace=w) for w in (None, space)]
+    torch.cuda.synchronize()
+    assert o.data_ptr() == out.data_ptr() and f.data_ptr() == fin.data_ptr() and cf.data_ptr() == cfin.data_ptr()
+    assert torch.equal(o, want) and torch.equal(f[:-1], wfin[:-1]) and bool((f[-1] == 5.0).all())
+    assert bool((cf[-1] == 5.0).all()) and not bool((cf[:-1] == 5.0).all())
+    assert all(torch.equal(a, b) for a, b in zip(*gr) if a is not None)
+    with pytest.raises(ssd.SSDError):
+        ssd.selective_scan_backward(want, *args, saved=ssd.selective_scan(*args, save_for_backward=True, **kw)[2],
+                                    workspace=space[:256], **kw)
+
+
+def test_offsets_past_32_bits():
+    """Rows, pools and caches whose offsets pass 2^32 bytes (and 2^31 elements)."""
+    g = gen(52)
+    D, N, L = 64, 16, 300
+    row = 1 << 23                                                          # elements between rows: 5 GB in all
+    wide = torch.empty(L, row, dtype=torch.bfloat16, device="cuda")
+    x, dt, B, C = (torch.randn(1, L, n, generator=g).bfloat16().cuda() for n in (D, D, N, N))
+    far = []
+    for i, t in enumerate((x, dt, B, C)):
+        v = wide.unsqueeze(0)[..., 128 * i:128 * i + t.shape[-1]]
+        v.copy_(t)
+        far.append(v)
+    A, w = -torch.rand(D, N, generator=g).cuda() - 0.1, torch.randn(D, 4, generator=g).cuda()
+    near = ssd.selective_scan(x, dt, A, B.unsqueeze(2), C.unsqueeze(2), save_for_backward=True)
+    got = ssd.selective_scan(far[0], far[1], A, far[2].unsqueeze(2), far[3].unsqueeze(2), save_for_backward=True)
+    for a, b in zip(near, got):
+        assert torch.equal(a, b)
+    ga = ssd.selective_scan_backward(x, x, dt, A, B.unsqueeze(2), C.unsqueeze(2), saved=near[2])
+    gb = ssd.selective_scan_backward(x, far[0], far[1], A, far[2].unsqueeze(2), far[3].unsqueeze(2), saved=got[2])
+    assert all(torch.equal(a, b) for a, b in zip(ga, gb) if a is not None)
+    for a, b in zip(ssd.causal_conv(x, w), ssd.causal_conv(far[0], w)):
+        assert torch.equal(a, b)
+    for a, b in zip(ssd.causal_conv_backward(x, x, w), ssd.causal_conv_backward(x, far[0], w)):
+        assert a is None or torch.equal(a, b)
+    del wide, far, v
+    # pools: 2^31 elements and more
+    D, N = 4096, 64
+    slots = (1 << 31) // (D * N) + 3
+    pool = torch.zeros(slots, D, N, dtype=torch.bfloat16, device="cuda")
+    where = torch.tensor([slots - 1, 1], dtype=torch.int32, device="cuda")
+    x = torch.randn(2, D, generator=g).bfloat16().cuda()
+    B = torch.randn(2, 1, N, generator=g).bfloat16().cuda()
+    A = -torch.ones(D, N, device="cuda")
+    small = torch.zeros(2, D, N, dtype=torch.bfloat16, device="cuda")
+    a = ssd.selective_scan_step(x, x, A, B, B, state=pool, slots=where)
+    b = ssd.selective_scan_step(x, x, A, B, B, state=small)
+    assert torch.equal(a, b) and torch.equal(pool[where.long()], small) and not pool[2:slots - 1:997].any()
+    del pool
+    codes, scales = ssd.state_cache(2 * slots, (D, N), group=32)
+    where = torch.tensor([2 * slots - 1, 1], dtype=torch.int32, device="cuda")
+    ssd.state_cache_write(small, codes, scales, where)
+    back = ssd.state_cache_read(codes, scales, where, state_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    assert torch.equal(back.cpu(), ref.cache(small.cpu(), 32, "int8")[0].float().bfloat16())
+    cpool = torch.zeros((1 << 31) // (D * 3) + 2, D, 3, dtype=torch.bfloat16, device="cuda")
+    cw = torch.ones(D, 4, device="cuda")
+    last = torch.tensor([cpool.shape[0] - 1, 0], dtype=torch.int32, device="cuda")
+    ssd.causal_conv_step(x, cw, state=cpool, slots=last)
+    assert torch.equal(cpool[last.long()][..., 2], x) and not cpool[1:-1:99991].any()

@@ -257,3 +257,15 @@ def test_meta_tells_calls_apart():
             meta(x, bad)
     with pytest.raises(ValueError):
         meta(x.to_sparse())
+
+
+def test_new_tensors_of_layouts():
+    from mamba_ssd_prefill_amd._meta import meta, new
+    lay = selective._layout((2, 3, 5), torch.bfloat16, torch.device("cpu"))
+    a, b = new(lay, meta(torch.zeros(4, 6)[:, :3])[0])
+    assert a.shape == (2, 3, 5) and a.dtype == torch.bfloat16 and a.is_contiguous()
+    assert b.shape == (4, 3) and b.stride() == (6, 1) and b.dtype == torch.float32
+    assert lay == meta(a)[0] and new() == ()
+    for bad in (b"", lay[:-8], lay + b"x" * 8, "x", meta(a, a)[0], meta(None)[0]):
+        with pytest.raises(ValueError):
+            new(bad)
