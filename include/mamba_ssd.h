@@ -426,12 +426,16 @@ ssd_status_t ssd_prefill_block(const ssd_params_t* p, const void* xbc, const flo
  * starts at t = 0 of every row and wherever seq_idx changes, and seq_idx[b,t] is the number of
  * the sequence holding token t; states are indexed by that number, in [0, nseq), and each number
  * labels one run of tokens.  Tokens whose number lies outside [0, nseq) (padding) run from a
- * zero state and write none.  Entries of state outputs that no sequence uses are left as they
- * were.  Below, S is batch without seq_idx and nseq with it.
+ * zero state and write none; like any token's, their outputs' gradients enter those of the
+ * parameters, so a padding's dout is zero and its inputs finite.  Entries of state outputs that
+ * no sequence uses are left as they were.  Below, S is batch without seq_idx and nseq with it.
  *
  * The single-token forms work in place on a pool of nseq states: row b uses the state
  * slots[b] (int32; NULL: slot b, with nseq = batch).  Each slot in use appears once.  A row
  * whose slot lies outside [0, nseq) (a padded batch) touches no state and gets a zero output row.
+ *
+ * Sizes that 32-bit token numbers or one launch's 2^32 lanes do not reach give SSD_ERR_INVALID_SHAPE (a
+ * lane takes 4 states of a step, 32 tokens of a channel of a convolution, 8 values of a cache).
  *
  * Outputs overlap no input, but for the states of the single-token forms.  A pass over a prompt may be
  * split in time into runs of tokens that are joined by their states, as a function of the sizes alone.

@@ -427,7 +427,7 @@ constexpr int kConvWide = 4;          // channels a lane of the forward takes wh
 constexpr int kConvBackwardWide = 2;  // and of the backward (4: 84 us against 77 with 2 at 2 x 4096 x 5376)
 
 int conv_backward_rows(int64_t batch, int64_t seqlen, int64_t channels) {
-    return conv_rows(batch, seqlen, channels / kConvBackwardWide);
+    return conv_rows(batch, seqlen, (channels + kConvBackwardWide - 1) / kConvBackwardWide);
 }
 
 // Whether lanes can take four channels with one access: every row they touch starts on a

@@ -14,6 +14,7 @@ namespace {
 
 constexpr size_t kAlign = 256;  // workspace region alignment
 constexpr int64_t kMaxIndex = (int64_t)1 << 31;
+constexpr int64_t kMaxLanes = (int64_t)1 << 32;  // of a launch
 
 size_t elem_size(int dt) { return dt == SSD_F32 ? 4 : 2; }
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
@@ -44,10 +45,10 @@ ssd_status_t validate_conv(const ssd_conv_params_t* p, bool step) {
     if (p->split_a < 0 || p->split_b < p->split_a || p->channels < p->split_b) return SSD_ERR_INVALID_SHAPE;
     if (!stride_ok(p->x_stride, p->channels)) return SSD_ERR_INVALID_SHAPE;
     if (p->width < 2 || p->width > 4) return SSD_ERR_UNSUPPORTED;
-    // lanes and tokens have to fit the kernels' 32-bit grid and row indexes
+    // tokens have to fit 32-bit row indexes and lanes a grid (runs are of 32 tokens where there are that many)
     if ((int64_t)p->batch * p->seqlen >= kMaxIndex) return SSD_ERR_INVALID_SHAPE;
-    const int64_t segs = ((int64_t)p->seqlen + 15) / 16;
-    if ((int64_t)p->batch * segs * p->channels / 256 >= kMaxIndex / 2) return SSD_ERR_INVALID_SHAPE;
+    const int64_t runs = (int64_t)p->batch * (((int64_t)p->seqlen + 31) / 32) + 3;
+    if (((int64_t)p->channels + 63) / 64 * runs >= kMaxLanes / 64) return SSD_ERR_INVALID_SHAPE;
     return SSD_OK;
 }
 
@@ -198,8 +199,18 @@ ssd_status_t validate_scan(const ssd_scan_params_t* p, bool step) {
     if ((int64_t)p->batch * p->seqlen >= kMaxIndex || (int64_t)p->channels * N >= kMaxIndex)
         return SSD_ERR_INVALID_SHAPE;
     const int64_t blocks = (int64_t)p->batch * p->ngroups * ((p->channels / p->ngroups + 63) / 64);
-    if (blocks >= kMaxIndex / 256 || (int64_t)p->batch * p->channels * (N / 4) / 256 >= kMaxIndex / 2 ||
-        (int64_t)p->batch * p->seqlen * gn >= kMaxIndex * 64)
+    if (blocks >= kMaxLanes / 512) return SSD_ERR_INVALID_SHAPE;
+    if (step && p->batch * (((int64_t)p->channels * (N / 4) + 255) / 256) >= kMaxLanes / 256) return SSD_ERR_INVALID_SHAPE;
+    return SSD_OK;
+}
+
+// The backward's sums take a lane for four values of dB or dC and for one of the parameters' gradients, by four waves.
+ssd_status_t validate_scan_backward(const ssd_scan_params_t* p) {
+    const ssd_status_t s = validate_scan(p, false);
+    if (s != SSD_OK) return s;
+    const int64_t runs = ((int64_t)p->batch * p->seqlen * (p->dstate / 2) + 63) / 64;
+    if (runs >= kMaxLanes / 256 / p->ngroups) return SSD_ERR_INVALID_SHAPE;
+    if (runs * p->ngroups + ((int64_t)p->channels * (p->dstate + 2) + 63) / 64 >= kMaxLanes / 256)
         return SSD_ERR_INVALID_SHAPE;
     return SSD_OK;
 }
@@ -282,7 +293,7 @@ SSD_EXPORT size_t ssd_selective_scan_workspace_size(const ssd_scan_params_t* p) 
 }
 
 SSD_EXPORT size_t ssd_selective_scan_backward_workspace_size(const ssd_scan_params_t* p) {
-    if (validate_scan(p, false) != SSD_OK) return 0;
+    if (validate_scan_backward(p) != SSD_OK) return 0;
     return scan_layout(p, true).total;
 }
 
@@ -328,7 +339,7 @@ SSD_EXPORT ssd_status_t ssd_selective_scan_backward(const ssd_scan_params_t* p, 
                                                     float* dA, void* dB, void* dC, float* dD, float* ddt_bias, void* dz,
                                                     void* dinitial_state, void* workspace, size_t workspace_bytes,
                                                     void* stream) {
-    ssd_status_t s = validate_scan(p, false);
+    ssd_status_t s = validate_scan_backward(p);
     if (s == SSD_OK) s = check_scan_inputs(p, x, dt, A, B, C, D, dt_bias, z);
     if (s != SSD_OK) return s;
     if (!dout || !saved || !dx || !ddt || !dA || !dB || !dC || (z && !dz) || !workspace) return SSD_ERR_NULL_POINTER;
@@ -393,7 +404,7 @@ ssd_status_t check_cache(const ssd_cache_params_t* p, const void* state, const i
     if (p->batch < 1 || p->nslots < 1 || p->elems < 1 || p->group < 1) return SSD_ERR_INVALID_SHAPE;
     if (p->group != 16 && p->group != 32 && p->group != 64 && p->group != 128) return SSD_ERR_UNSUPPORTED;
     if (p->elems % p->group || p->elems >= (int64_t)1 << 40) return SSD_ERR_INVALID_SHAPE;
-    if (p->elems / 1024 + 1 >= kMaxIndex / p->batch) return SSD_ERR_INVALID_SHAPE;
+    if (p->batch * ((p->elems + 2047) / 2048) >= kMaxLanes / 256) return SSD_ERR_INVALID_SHAPE;  // 8 values a lane
     if (!slots && p->nslots < p->batch) return SSD_ERR_INVALID_SHAPE;
     if (!state || !codes || !scales) return SSD_ERR_NULL_POINTER;
     if (!aligned(state, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(slots, 4))

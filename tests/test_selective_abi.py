@@ -269,3 +269,25 @@ def test_new_tensors_of_layouts():
     for bad in (b"", lay[:-8], lay + b"x" * 8, "x", meta(a, a)[0], meta(None)[0]):
         with pytest.raises(ValueError):
             new(bad)
+
+
+@pytest.mark.parametrize("name,fits,over", [
+    # (a missing tensor is found after the sizes)
+    ("ssd_causal_conv", dict(batch=1, seqlen=(1 << 31) - 256), dict(batch=1, seqlen=(1 << 31) - 1)),
+    ("ssd_causal_conv", dict(batch=1 << 12, seqlen=1 << 16, channels=448, split_a=448, split_b=448),
+     dict(batch=1 << 12, seqlen=1 << 16, channels=449, split_a=449, split_b=449)),
+    ("ssd_causal_conv_backward", dict(batch=1, seqlen=(1 << 31) - 256, channels=1, split_a=1, split_b=1),
+     dict(batch=1 << 26, seqlen=1, channels=1, split_a=1, split_b=1)),
+    ("ssd_causal_conv_step", dict(batch=(1 << 26) - 4, nseq=(1 << 26) - 4), dict(batch=1 << 26, nseq=1 << 26)),
+    ("ssd_selective_scan", dict(batch=(1 << 23) - 1, seqlen=200), dict(batch=1 << 23, seqlen=200)),
+    ("ssd_selective_scan_backward", dict(batch=1 << 20, seqlen=120), dict(batch=1 << 20, seqlen=128)),
+    ("ssd_selective_scan_backward", dict(seqlen=1 << 20, dstate=64, ngroups=8), dict(seqlen=1 << 20, dstate=64, ngroups=16)),
+    ("ssd_selective_scan_step", dict(batch=(1 << 22) - 1, nseq=(1 << 22) - 1, dstate=64),
+     dict(batch=1 << 22, nseq=1 << 22, dstate=64)),
+    ("ssd_state_cache_write", dict(batch=1 << 13, nslots=1 << 13, elems=2047 * 2048), dict(batch=1 << 13, nslots=1 << 13, elems=2047 * 2048 + 2048)),
+    ("ssd_state_cache_read", dict(elems=(1 << 34) - 4096), dict(elems=1 << 34)),
+])
+def test_a_launch_s_lanes_are_bounded(lib, name, fits, over):
+    first = ARGS[name][0].split()[0]
+    assert call(lib, name, params_for(name, **fits), **{first: None}) == NULLP
+    assert call(lib, name, params_for(name, **over), **{first: None}) == SHAPE
