@@ -76,12 +76,12 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
         typename Rows::Group gb[2], gc[2];
         gb[0].load(rb, 0);
         gc[0].load(rc, 0);
+        float step[TPW];
+        steps(a, cur.dt, bias, step);
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             const int k = w + j * NW;
-            const float v = f32of(cur.dt[j]) + bias;
-            // tokens past the end take no step: d = 0 leaves the state as it is
-            const float d = t0 + k < a.seqlen ? (a.softplus ? step_f(v) : v) : 0.f;
+            const float d = t0 + k < a.seqlen ? step[j] : 0.f;  // (no step past the end: the state stays as it is)
             s_d[k][lane] = f32x2{d, d * f32of(cur.x[j])};
         }
         SeqMasks m{0, 0};
@@ -123,15 +123,19 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
         __syncthreads();
         const TileRows<T, kTile> ro(a.out, a.channels, p.row0, t0, a.seqlen);
         const uint32_t lo = p.live ? (uint32_t)p.c * (uint32_t)sizeof(T) : kNoLane;
+        float y[TPW];
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-            const int k = w + j * NW;
-            float y = Dc * f32of(cur.x[j]);
+            y[j] = Dc * f32of(cur.x[j]);
 #pragma unroll
-            for (int i = 0; i < NW; ++i) y += s_y[i][k][lane];
-            if (a.z) y *= silu_f(f32of(cur.z[j]));
-            ro.store(k, lo, y);
+            for (int i = 0; i < NW; ++i) y[j] += s_y[i][w + j * NW][lane];
         }
+        if (a.z) {
+#pragma unroll
+            for (int j = 0; j < TPW; ++j) y[j] *= silu_f(f32of(cur.z[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) ro.store(w + j * NW, lo, y[j]);
     }
     if (!VL && a.fin && tile1 * kTile >= a.seqlen && p.live)
         store_states<NS>(a.fin, a.state_dtype, p.b * sstride + soff, h);
@@ -164,12 +168,10 @@ __global__ __launch_bounds__(NW * 64) void k_scan_carry(ScanArgs a) {
     bool fresh = false;
     ScanTokens<T, TPW, false> next;
     auto prepare = [&](int buf) {
+        float step[TPW];
+        steps(a, next.dt, bias, step);
 #pragma unroll
-        for (int j = 0; j < TPW; ++j) {
-            const float v = f32of(next.dt[j]) + bias;
-            const float d = a.softplus ? step_f(v) : v;
-            s_d[buf][w + j * NW][lane] = f32x2{d, d * f32of(next.x[j])};
-        }
+        for (int j = 0; j < TPW; ++j) s_d[buf][w + j * NW][lane] = f32x2{step[j], step[j] * f32of(next.x[j])};
     };
     next.load(a, p, tile0 * kTile, w, NW);
     prepare(0);

@@ -147,14 +147,21 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
         float hin[NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) hin[i] = hnext[i];
+        float step[TPW], dyj[TPW];
+        steps(a, cur.dt, bias, step);
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) dyj[j] = f32of(cur.g[j]);
+        if (a.z) {
+#pragma unroll
+            for (int j = 0; j < TPW; ++j) dyj[j] *= silu_f(f32of(cur.z[j]));
+        }
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             const int k = w + j * NW;
             const bool in = t0 + k < a.seqlen && p.live;
-            const float v = f32of(cur.dt[j]) + bias;
-            const float d = in ? (a.softplus ? step_f(v) : v) : 0.f, go = in ? f32of(cur.g[j]) : 0.f;
+            const float d = in ? step[j] : 0.f;
             s_d[k][lane] = f32x2{d, d * f32of(cur.x[j])};
-            s_g[k][lane] = a.z ? go * silu_f(f32of(cur.z[j])) : go;
+            s_g[k][lane] = in ? dyj[j] : 0.f;
         }
         SeqMasks m{0, 0};
         if (VL) m = seq_masks<TB>(a, p.row0, t0);
@@ -259,27 +266,41 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
         const TileRows<T, kScanPeriod> rd(a2.ddt, a2.channels, p.row0, t0, a2.seqlen);
         const TileRows<T, kScanPeriod> rz(a2.dz, a2.channels, p.row0, t0, a2.seqlen);
         const uint32_t lo = p.live ? (uint32_t)p.c * (uint32_t)sizeof(T) : kNoLane;
+        float y[TPW], u[TPW], ddt[TPW];
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             const int k = w + j * NW;
-            const float x = f32of(cur.x[j]), d = s_d[k][lane][0], dy = s_g[k][lane];
-            float y = Dc * x, u = 0.f, q = 0.f;
+            const float x = f32of(cur.x[j]);
+            float q = 0.f;
+            y[j] = Dc * x;
+            u[j] = 0.f;
 #pragma unroll
             for (int i = 0; i < NW; ++i) {
-                y += s_y[i][k][lane];
-                u += s_u[i][k][lane];
+                y[j] += s_y[i][k][lane];
+                u[j] += s_u[i][k][lane];
                 q += s_q[i][k][lane];
             }
-            float ddt = x * u + q * (1.f / kLog2e);
-            if (a2.softplus) ddt *= sigmoid_f(f32of(cur.dt[j]) + bias);
-            rx.store(k, lo, Dc * dy + d * u);
-            rd.store(k, lo, ddt);
-            if (a2.z) {
+            ddt[j] = x * u[j] + q * (1.f / kLog2e);
+        }
+        if (a2.softplus) {
+#pragma unroll
+            for (int j = 0; j < TPW; ++j) ddt[j] *= sigmoid_f(f32of(cur.dt[j]) + bias);
+        }
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            const int k = w + j * NW;
+            const float d = s_d[k][lane][0], dy = s_g[k][lane];
+            rx.store(k, lo, Dc * dy + d * u[j]);
+            rd.store(k, lo, ddt[j]);
+            dDt += dy * f32of(cur.x[j]);  // zero past the end, where x = dy = 0
+            dbt += t0 + k < a2.seqlen ? ddt[j] : 0.f;
+        }
+        if (a2.z) {
+#pragma unroll
+            for (int j = 0; j < TPW; ++j) {
                 const float z = f32of(cur.z[j]), sz = sigmoid_f(z);
-                rz.store(k, lo, f32of(cur.g[j]) * y * (sz * (1.f + z * (1.f - sz))));
+                rz.store(w + j * NW, lo, f32of(cur.g[j]) * y[j] * (sz * (1.f + z * (1.f - sz))));
             }
-            dDt += dy * x;  // zero past the end, where x = dy = 0
-            dbt += t0 + k < a2.seqlen ? ddt : 0.f;
         }
         dD += dDt;
         db += dbt;
@@ -346,11 +367,18 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward_carry(ScanArgs a) {
         }
     };
     auto prepare = [&](int buf, int t0) {
+        float step[TPW], dy[TPW];
+        steps(a, dt, bias, step);
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) dy[j] = f32of(go[j]);
+        if (a.z) {
+#pragma unroll
+            for (int j = 0; j < TPW; ++j) dy[j] *= silu_f(f32of(z[j]));
+        }
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             const bool in = t0 + w + j * NW < a.seqlen;
-            const float v = f32of(dt[j]) + bias, o = in ? f32of(go[j]) : 0.f;
-            s_d[buf][w + j * NW][lane] = f32x2{in ? (a.softplus ? step_f(v) : v) : 0.f, a.z ? o * silu_f(f32of(z[j])) : o};
+            s_d[buf][w + j * NW][lane] = f32x2{in ? step[j] : 0.f, in ? dy[j] : 0.f};
         }
     };
     load((tile1 - 1) * TB);

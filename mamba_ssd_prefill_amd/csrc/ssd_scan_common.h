@@ -74,7 +74,9 @@ template <typename T, int TOKENS> struct TileRows {
     // TOKENS rows from token t0 of a batch row (t0 < 0: none)
     __device__ inline TileRows(const void* base, int64_t row_stride, int64_t row0, int t0, int seqlen) {
         stride = (uint32_t)row_stride * (uint32_t)sizeof(T);
-        const int n = t0 < 0 ? 0 : max(0, min(seqlen - t0, TOKENS));
+        int n = min(seqlen - t0, TOKENS);
+        asm("" : "+s"(n));  // (else the two bounds become one vector instruction, with quarter-rate products behind it)
+        n = t0 < 0 ? 0 : max(n, 0);
         rsrc = make_rsrc((const char*)base + (uint64_t)(uint32_t)(row0 + max(t0, 0)) * stride, (uint32_t)n * stride);
     }
     __device__ inline T load(int k, uint32_t lane_off) const {
@@ -141,6 +143,17 @@ template <int CTRL> __device__ inline float dpp(float v) {
 __device__ inline float step_f(float v) {
     const float u = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e), s = 1.f + u;
     return fmaxf(v, 0.f) + (__builtin_amdgcn_logf(s) * 0.693147180559945309417f + (u - (s - 1.f)));
+}
+
+// The steps of a wave's tokens.  (All of them behind one branch: a branch for each token keeps their chains of dependent
+// instructions from running side by side.)
+template <typename T, int K> __device__ inline void steps(const ScanArgs& a, const T (&dt)[K], float bias, float (&d)[K]) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) d[j] = f32of(dt[j]) + bias;
+    if (a.softplus) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) d[j] = step_f(d[j]);
+    }
 }
 
 // softplus'(v)
