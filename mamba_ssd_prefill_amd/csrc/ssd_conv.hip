@@ -7,6 +7,8 @@
 // All three are HBM-bound streams.  A lane owns CW neighbouring channels of a run of tokens and slides a
 // window of W-1 inputs down them, so each input is read once a run plus a halo of W-1 rows;
 // consecutive lanes take consecutive channels.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "ssd_device.h"
@@ -199,8 +201,9 @@ template <typename T, int W, int CW, bool VL> struct ConvWalk {
     __device__ inline bool last(int t) const { return t == a.seqlen - 1 || (VL && qn != q); }
 };
 
-// Rows on their way while one is used (2 and 4 measured alike forward, 1, 2 and 3 backward).
-constexpr int kConvAhead = 2, kConvAheadBackward = 1;
+// Rows on their way while one is used (2 and 4 measured alike forward; backward 70.0, 68.2, 67.7 us with 1, 2, 3 in
+// runs of 32 tokens and 66.7, 71.4 with 2, 3 in runs of 16, at 2 x 4096 x 5376).
+constexpr int kConvAhead = 2, kConvAheadBackward = 2;
 
 template <typename T, int W, int CW, bool VL> __global__ __launch_bounds__(256) void k_causal_conv(CausalConvArgs a) {
     ConvItem it;
@@ -238,12 +241,9 @@ __device__ inline float dsilu_f(float v) {
 }
 
 // One pass over a run of tokens and the W-1 tokens behind it: dpre of a token completes dx of the token
-// W-1 before it.  A lane's sums of dw and dbias over its own tokens go to `part` (one row per
-// segment), summed by k_conv_sums in a fixed order.
+// W-1 before it.  dw and db: the lane's sums over its own tokens.
 template <typename T, int W, int CW, bool VL, bool ST>
-__global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) {
-    ConvItem it;
-    if (!conv_item<CW>(a, &it)) return;
+__device__ inline void conv_backward_run(const CausalConvArgs& a, const ConvItem& it, float (&dw)[W][CW], float (&db)[CW]) {
     ConvW<W, CW> k;
     k.load(a, it.c0);
     ConvWalk<T, W, CW, VL> s(a, it.b, it.c0);
@@ -251,7 +251,6 @@ __global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) 
     const int64_t row0 = (int64_t)it.b * a.seqlen;
     const T* dout = split_ptr<T>((void* const*)a.dout, a.split_a, a.split_b, a.channels, it.c0, row0 + it.t0);
     const int os = it.c0 < a.split_a ? a.split_a : it.c0 < a.split_b ? a.split_b - a.split_a : a.channels - a.split_b;
-    float dw[W][CW] = {}, db[CW] = {};
     // dx of the W-1 tokens before the current one, still short of later tokens' terms
     float acc[W - 1][CW] = {};
     // gradients of the initial state, at a sequence's first tokens
@@ -364,13 +363,33 @@ __global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) 
     for (; t < it.t0 + W - 1; ++t) token(std::false_type{}, t);
     for (; t < it.t1; ++t) token(std::true_type{}, t);
     for (; t < it.t1 + W - 1; ++t) token(std::false_type{}, t);
-    float* part = a.part + (((int64_t)it.b * a.nseg + it.t0 / a.rows) * a.channels + it.c0) * (W + 1);
+}
+
+// The sums of a workgroup's four runs meet in LDS and go to its row of `part` ([W + 1][channels], dw then dbias), summed
+// by k_conv_sums in a fixed order.  (A row for every run, 28 MB of them at 2 x 4096 x 5376, cost 78.6 us in all against 74.5.)
+template <typename T, int W, int CW, bool VL, bool ST>
+__global__ __launch_bounds__(256) void k_causal_conv_backward(CausalConvArgs a) {
+    __shared__ float s_part[4][W + 1][CW][64];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    float dw[W][CW] = {}, db[CW] = {};
+    ConvItem it;
+    const bool mine = conv_item<CW>(a, &it);
+    if (mine) conv_backward_run<T, W, CW, VL, ST>(a, it, dw, db);
 #pragma unroll
     for (int e = 0; e < CW; ++e) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) part[e * (W + 1) + j] = dw[j][e];
-        part[e * (W + 1) + W] = db[e];
+        for (int j = 0; j < W; ++j) s_part[w][j][e][lane] = dw[j][e];
+        s_part[w][W][e][lane] = db[e];
     }
+    __syncthreads();
+    const uint32_t pblocks = (uint32_t)(a.channels / CW + 63) / 64;
+    const int c0 = ((int)(blockIdx.x % pblocks) * 64 + lane) * CW;
+    if (c0 >= a.channels) return;
+    float* part = a.part + (int64_t)(blockIdx.x / pblocks) * (W + 1) * a.channels + c0;
+    for (int j = w; j <= W; j += 4)
+#pragma unroll
+        for (int e = 0; e < CW; ++e)
+            part[(int64_t)j * a.channels + e] = (s_part[0][j][e][lane] + s_part[1][j][e][lane]) + (s_part[2][j][e][lane] + s_part[3][j][e][lane]);
 }
 
 // dw [channels][W] and dbias [channels] from the rows of `part`, 64 values a workgroup.
@@ -380,7 +399,7 @@ template <int W> __global__ __launch_bounds__(256) void k_conv_sums(const float*
     const int64_t n = (int64_t)channels * (W + 1), i = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
     const float s = sum_rows<float>(part + i, n, nrows, lds, i < n);
     if (i >= n || threadIdx.x >= 64) return;
-    const int c = (int)(i / (W + 1)), j = (int)(i % (W + 1));
+    const int c = (int)(i % channels), j = (int)(i / channels);
     if (j < W)
         dw[(int64_t)c * W + j] = s;
     else if (db)
@@ -415,19 +434,32 @@ template <typename T, int W> __global__ __launch_bounds__(256) void k_causal_con
     st[W - 2] = cur;
 }
 
-// Tokens per lane: long runs read fewer rows twice (measured at 2 x 4096 x 5376, bf16: forward 43, 39.5, 37.7 us with 8, 16,
-// 32; backward 90, 77, 77 us with 16, 32, 64), short ones give a small problem more waves (1 x 4096 x 1792 packed:
-// 15.6, 12.7, 13.0 us with 4, 8, 16): the longest of 32, 16 and 8 that leaves 4 waves a SIMD.
-static int conv_rows(int64_t batch, int64_t seqlen, int64_t pieces) {
-    int rows = 32;
-    while (rows > 8 && batch * ((seqlen + rows - 1) / rows) * pieces < (int64_t)1 << 18) rows /= 2;
-    return rows;
+// Tokens of a run, up to `most`.  Long runs read fewer rows twice; and the workgroups, 2048 of which the chip holds at a
+// time, should come in full rounds, for in a round that is partly filled too few loads are on their way.  Both as a
+// cost relative to one pass over the rows, fitted to the times (us) of runs of 8, 16, 24, 32, 48 and 64 tokens:
+// 2 x 4096 x 5376 forward 37.6 35.0 34.2 36.6 34.1 36.6, backward 75 66 64 65 61 66;
+// 8 x 2048 x 5376 forward 74 73 73 73 78 79 (so 32 at most forward), backward 146 131 127 123 123 132;
+// 1 x 4096 x 1792 forward 7.8 8.5 8.8 10.2 12.9 15.7, backward 15.0 15.6 16.5 18.6 22.5 27.1.
+static int conv_rows(int64_t batch, int64_t seqlen, int64_t pieces, int most) {
+    const int64_t pblocks = (pieces + 63) / 64;
+    int best = 8;
+    double least = 0;
+    for (int rows = 8; rows <= most; rows += 4) {
+        const int64_t runs = batch * ((seqlen + rows - 1) / rows), rounds = pblocks * ((runs + 3) / 4);
+        const double full = (double)rounds / 2048, cost = (1 + 3.0 / rows) * std::cbrt(std::ceil(full) / full);
+        if (rows == 8 || cost < least) {
+            least = cost;
+            best = rows;
+        }
+    }
+    return best;
 }
 constexpr int kConvWide = 4;          // channels a lane of the forward takes where rows allow it
-constexpr int kConvBackwardWide = 2;  // and of the backward (4: 84 us against 77 with 2 at 2 x 4096 x 5376)
+constexpr int kConvBackwardWide = 2;  // and of the backward (4: 79 us against 70 with 2 at 2 x 4096 x 5376)
+constexpr int kConvMost = 32, kConvBackwardMost = 64;
 
 int conv_backward_rows(int64_t batch, int64_t seqlen, int64_t channels) {
-    return conv_rows(batch, seqlen, (channels + kConvBackwardWide - 1) / kConvBackwardWide);
+    return conv_rows(batch, seqlen, (channels + kConvBackwardWide - 1) / kConvBackwardWide, kConvBackwardMost);
 }
 
 // Whether lanes can take four channels with one access: every row they touch starts on a
@@ -447,7 +479,7 @@ static unsigned conv_blocks(const CausalConvArgs& a, int cw) {
 
 template <typename T, int W> hipError_t launch_conv_tw(CausalConvArgs& a, hipStream_t st) {
     const bool v4 = conv_vec4(a, sizeof(T), a.out, 3);
-    a.rows = conv_rows(a.batch, a.seqlen, a.channels / (v4 ? kConvWide : 1));
+    a.rows = conv_rows(a.batch, a.seqlen, a.channels / (v4 ? kConvWide : 1), kConvMost);
     a.nseg = (a.seqlen + a.rows - 1) / a.rows;
     void* args[] = {&a};
     const void* fn = a.seq ? (v4 ? (const void*)&k_causal_conv<T, W, kConvWide, true> : (const void*)&k_causal_conv<T, W, 1, true>)
@@ -472,7 +504,7 @@ template <typename T, int W> hipError_t launch_conv_back_tw(CausalConvArgs& a, f
                         : conv_backward_kernel<T, W, 1>(a.seq, states);
     hipError_t e = hipLaunchKernel(fn, dim3(conv_blocks(a, v4 ? kConvBackwardWide : 1)), dim3(256), args, 0, st);
     if (e != hipSuccess) return e;
-    int nrows = a.batch * a.nseg;
+    int nrows = (int)(((int64_t)a.batch * a.nseg + 3) / 4);
     const int64_t n = (int64_t)a.channels * (W + 1);
     void* sargs[] = {&a.part, &nrows, &a.channels, &dw, &db};
     return hipLaunchKernel((const void*)&k_conv_sums<W>, dim3((unsigned)((n + 63) / 64)), dim3(256), sargs, 0, st);

@@ -83,7 +83,7 @@ ssd_status_t check_ranges(const ssd_conv_params_t* p, const void* t0, const void
 size_t conv_part_bytes(const ssd_conv_params_t* p) {
     const int64_t rows = ssd::conv_backward_rows(p->batch, p->seqlen, p->channels);
     const int64_t nseg = (p->seqlen + rows - 1) / rows;
-    return align_up((size_t)p->batch * nseg * p->channels * (p->width + 1) * 4);
+    return align_up((size_t)((p->batch * nseg + 3) / 4) * p->channels * (p->width + 1) * 4);  // four runs a workgroup
 }
 
 }  // namespace
