@@ -4,7 +4,9 @@
 //     pre[t] = bias + sum_k w[k] in[t - (W-1) + k],     out = silu(pre) or pre
 //     dpre[t] = dout[t] silu'(pre[t]),   dx[s] = sum_i w[W-1-i] dpre[s+i],   dw[k] = sum_t dpre[t] in[t-(W-1)+k]
 //
-// All three are HBM-bound streams.  A lane owns CW neighbouring channels of a run of tokens and slides a
+// All three are HBM-bound streams: at 2 x 4096 x 5376, W = 4, bf16 the forward moves 176 MB in 36.5 us (4.8 TB/s, where a
+// large copy reaches 5.0), the backward 264 MB in 60 us (4.4) and 5 us for its sums; a step of one row takes the 2.8 us of
+// a launch.  A lane owns CW neighbouring channels of a run of tokens and slides a
 // window of W-1 inputs down them, so each input is read once a run plus a halo of W-1 rows;
 // consecutive lanes take consecutive channels.
 #include <algorithm>
