@@ -747,3 +747,69 @@ def test_offsets_past_32_bits():
     last = torch.tensor([cpool.shape[0] - 1, 0], dtype=torch.int32, device="cuda")
     ssd.causal_conv_step(x, cw, state=cpool, slots=last)
     assert torch.equal(cpool[last.long()][..., 2], x) and not cpool[1:-1:99991].any()
+
+
+def test_threads_at_once():
+    """Calls from several threads, each on its own stream, of sizes that are new to all of them."""
+    import threading
+    jobs = []
+    for i in range(6):
+        s, seq, S, _ = scan_inputs(2, 40 + 7 * (i // 2), 70, 16, 1, "bf16", "f32", "pad", True, True, True, True, seed=60 + i)
+        args, h0 = call_args(s)
+        w = torch.randn(70, 4, generator=gen(i)).cuda()
+        jobs.append((args, h0, w, dict(seq_idx=seq.cuda(), nseq=S)))
+    torch.cuda.synchronize()
+
+    def work(args, h0, w, kw):
+        out, fin, saved = ssd.selective_scan(*args, initial_state=h0, save_for_backward=True, **kw)
+        g = ssd.selective_scan_backward(out, *args, saved=saved, initial_state=h0, **kw)
+        c, cs = ssd.causal_conv(args[0], w, **kw)
+        return [out, fin, *g, c, cs]
+
+    got = [None] * len(jobs)
+
+    def run(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(5):
+                got[i] = work(*jobs[i])
+        st.synchronize()
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i, j in enumerate(jobs):
+        for a, b in zip(got[i], work(*j)):
+            assert (a is None and b is None) or torch.equal(a, b), i
+
+
+def test_first_call_inside_a_capture():
+    """Sizes not seen before, packed, in many time splits, captured at their first call and replayed."""
+    L, D, N = 1537, 66, 32
+    s, seq, S, g = scan_inputs(1, L, D, N, 1, "f16", "bf16", "pad", True, True, True, True, seed=71)
+    args, h0 = call_args(s)
+    kw = dict(seq_idx=seq.cuda(), nseq=S, initial_state=h0)
+    dout = torch.randn(1, L, D, generator=g).half().cuda()
+    w = torch.randn(D, 3, generator=g).cuda()
+    torch.cuda.synchronize()
+
+    def work():
+        out, fin, saved = ssd.selective_scan(*args, save_for_backward=True, **kw)
+        gr = ssd.selective_scan_backward(dout, *args, saved=saved, **kw)
+        c, cs = ssd.causal_conv(args[0], w, seq_idx=kw["seq_idx"], nseq=S)
+        cg = ssd.causal_conv_backward(dout, args[0], w, seq_idx=kw["seq_idx"], nseq=S)
+        return [out, fin, *gr, c, cs, *cg]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = work()
+    for k in range(3):
+        dout.copy_(torch.randn(1, L, D, generator=g).half())
+        args[0].copy_(torch.randn(1, L, D, generator=g).half())
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [None if t is None else t.clone() for t in held]
+        want = work()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert (a is None and b is None) or torch.equal(a, b), k
