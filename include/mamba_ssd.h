@@ -426,9 +426,9 @@ ssd_status_t ssd_prefill_block(const ssd_params_t* p, const void* xbc, const flo
  * starts at t = 0 of every row and wherever seq_idx changes, and seq_idx[b,t] is the number of
  * the sequence holding token t; states are indexed by that number, in [0, nseq), and each number
  * labels one run of tokens.  Tokens whose number lies outside [0, nseq) (padding) run from a
- * zero state and write none; like any token's, their outputs' gradients enter those of the
- * parameters, so a padding's dout is zero and its inputs finite.  Entries of state outputs that
- * no sequence uses are left as they were.  Below, S is batch without seq_idx and nseq with it.
+ * zero state and write none.  In the backward passes they count as nothing, whatever their inputs
+ * and dout hold: their own gradients are zero and they add nothing to the others.  Entries of
+ * state outputs that no sequence uses are left as they were.  Below, S is batch without seq_idx and nseq with it.
  *
  * The single-token forms work in place on a pool of nseq states: row b uses the state
  * slots[b] (int32; NULL: slot b, with nseq = batch).  Each slot in use appears once.  A row

@@ -323,6 +323,14 @@ __device__ inline void conv_backward_run(const CausalConvArgs& a, const ConvItem
             xrows.take(cur);
             grows.take(g);
             s.step_to(t);
+            if (VL && !s.has_state(s.q)) {  // padding counts as nothing, whatever it holds
+#pragma unroll
+                for (int e = 0; e < CW; ++e) {
+                    cur[e] = g[e] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) s.win[j][e] = 0.f;
+                }
+            }
             s.taps(k, cur, pre);
             if (a.silu) {
 #pragma unroll

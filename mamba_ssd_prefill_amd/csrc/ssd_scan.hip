@@ -86,7 +86,7 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
             const float d = t0 + k < a.seqlen ? step[j] : 0.f;  // (no step past the end: the state stays as it is)
             s_d[k][lane] = f32x2{d, d * f32of(cur.x[j])};
         }
-        SeqMasks m{0, 0};
+        SeqMasks m{0, 0, 0};
         if (VL) m = seq_masks<kTile>(a, p.row0, t0);
         __syncthreads();
         next.load(a, p, t0 + kTile, w, NW);
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(NW * 64) void k_scan_carry(ScanArgs a) {
         typename Rows::Group gb[2];
         gb[0].load(rb, 0);
         next.load(a, p, t0 + kTile, w, NW);
-        SeqMasks m{0, 0};
+        SeqMasks m{0, 0, 0};
         if (VL) m = seq_masks<kTile>(a, p.row0, t0);
         __syncthreads();
         float part = 0.f;

@@ -140,7 +140,15 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
     for (int tile = tile1 - 1; tile >= tile0; --tile) {
         const ScanArgs& a = args_again();
         const int t0 = tile * TB;
-        const BackTokens<T, TPW> cur = next;
+        BackTokens<T, TPW> cur = next;
+        SeqMasks m{0, 0, 0};
+        if (VL) {
+            // padding counts as nothing, whatever it holds: no step, no inputs, no gradient of its outputs
+            m = seq_masks<TB>(a, p.row0, t0);
+#pragma unroll
+            for (int j = 0; j < TPW; ++j)
+                if (m.pad >> (w + j * NW) & 1) cur.x[j] = cur.dt[j] = cur.z[j] = cur.g[j] = (T)0.f;
+        }
         const Rows rb((const T*)a.B + p.g * N + n0, a.Bs, p.row0, t0, a.seqlen);
         const Rows rc((const T*)a.C + p.g * N + n0, a.Cs, p.row0, t0, a.seqlen);
         typename Rows::Group gb[2], gc[2];
@@ -160,13 +168,11 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
             const int k = w + j * NW;
-            const bool in = t0 + k < a.seqlen && p.live;
+            const bool in = t0 + k < a.seqlen && p.live && !(VL && (m.pad >> k & 1));
             const float d = in ? step[j] : 0.f;
             s_d[k][lane] = f32x2{d, d * f32of(cur.x[j])};
             s_g[k][lane] = in ? dyj[j] : 0.f;
         }
-        SeqMasks m{0, 0};
-        if (VL) m = seq_masks<TB>(a, p.row0, t0);
         __syncthreads();
 
         // the tile's states and decays again
@@ -176,6 +182,10 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
             if (k % GT == 0 && k + GT < TB) {
                 gb[(k / GT + 1) & 1].load(rb, k + GT);
                 gc[(k / GT + 1) & 1].load(rc, k + GT);
+            }
+            if (VL && (m.pad >> k & 1)) {
+                gb[(k / GT) & 1].clear(k % GT);
+                gc[(k / GT) & 1].clear(k % GT);
             }
             float Bv[NS], Cv[NS];
             gb[(k / GT) & 1].values(k % GT, Bv);
@@ -188,6 +198,10 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
 #pragma unroll
                 for (int i = 0; i < NS; ++i) prev[i] = 0.f;
                 if (a.h0 && state_number(a, q)) load_states<NS>(a.h0, a.state_dtype, q * sstride + soff, prev);
+            }
+            if (VL && (m.pad >> k & 1)) {
+#pragma unroll
+                for (int i = 0; i < NS; ++i) prev[i] = 0.f;
             }
             const f32x2 dv = s_d[k][lane];
             float y = 0.f;
@@ -215,6 +229,10 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
                 gb[(k / GT - 1) & 1].load(rb, k - 2 * GT + 1);
                 gc[(k / GT - 1) & 1].load(rc, k - 2 * GT + 1);
             }
+            if (VL && (m.pad >> k & 1)) {
+                gb[(k / GT) & 1].clear(k % GT);
+                gc[(k / GT) & 1].clear(k % GT);
+            }
             float Bv[NS], Cv[NS], prev[NS];
             gb[(k / GT) & 1].values(k % GT, Bv);
             gc[(k / GT) & 1].values(k % GT, Cv);
@@ -231,6 +249,10 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
 #pragma unroll
                 for (int i = 0; i < NS; ++i) g[i] = 0.f;
                 if (a.dfin && state_number(a, q)) load_states<NS>(a.dfin, a.state_dtype, q * sstride + soff, g);
+            }
+            if (VL && (m.pad >> k & 1)) {
+#pragma unroll
+                for (int i = 0; i < NS; ++i) prev[i] = g[i] = 0.f;
             }
             const f32x2 dv = s_d[k][lane];
             const float dy = s_g[k][lane];
@@ -391,7 +413,7 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward_carry(ScanArgs a) {
         typename Rows::Group gc[2];
         gc[(TB / GT - 1) & 1].load(rc, TB - GT);
         load(t0 - TB);
-        SeqMasks m{0, 0};
+        SeqMasks m{0, 0, 0};
         if (VL) m = seq_masks<TB>(a, p.row0, t0);
         __syncthreads();
         float part = 0.f;

@@ -41,6 +41,10 @@ template <typename T, int NS> struct ScalarRows {
                 for (int i = 0; i < WORDS; ++i) w[j][i] = ((Words)(r.base + off))[i];
             }
         }
+        __device__ inline void clear(int j) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) w[j][i] = 0;
+        }
         // token k0 + j as fp32
         __device__ inline void values(int j, float (&v)[NS]) const {
             if constexpr (sizeof(T) == 4) {
@@ -192,19 +196,22 @@ __device__ inline ScanPlace scan_place(const ScanArgs& a) {
     return p;
 }
 
-// Sequence starts and ends among the T tokens from t0: bit k for token t0 + k.
+__device__ inline bool state_number(const ScanArgs& a, int q) { return q >= 0 && q < a.nseq; }
+
+// Sequence starts and ends and padding among the T tokens from t0 (those past the end are padding): bit k for token t0 + k.
 struct SeqMasks {
-    uint32_t start, end;
+    uint32_t start, end, pad;
 };
 template <int T> __device__ inline SeqMasks seq_masks(const ScanArgs& a, int64_t row0, int t0) {
     const int k = threadIdx.x & 63, t = t0 + k;
-    bool s = false, e = false;
+    bool s = false, e = false, p = true;
     if (k < T && t < a.seqlen) {
         const int32_t q = a.seq[row0 + t];
+        p = !state_number(a, q);
         s = t == 0 || a.seq[row0 + t - 1] != q;
         e = t == a.seqlen - 1 || a.seq[row0 + t + 1] != q;
     }
-    return SeqMasks{(uint32_t)__ballot(s), (uint32_t)__ballot(e)};
+    return SeqMasks{(uint32_t)__ballot(s), (uint32_t)__ballot(e), (uint32_t)__ballot(p)};
 }
 
 // The state v behind a split whose steps sum to d (infinite: nothing passes), `own` its state from a zero start.  (A
@@ -258,7 +265,5 @@ __device__ inline void fold_splits(const float (&A2)[NS], float (&h)[NS], int n,
         }
     }
 }
-
-__device__ inline bool state_number(const ScanArgs& a, int q) { return q >= 0 && q < a.nseq; }
 
 }  // namespace ssd

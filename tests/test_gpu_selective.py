@@ -116,6 +116,7 @@ def test_conv_backward(case):
     for p, q in zip(*runs):
         assert (p is None and q is None) or torch.equal(p, q)  # a fixed order of summation
     rr = ref.runs(B, L, seq)
+    dout = used(dout, seq, S)
     want = ref.conv_grads(dout, dfin, x, w, b, h0, S, act, rr)
     scale = ref.conv_grads(dout, dfin, x, w, b, h0, S, act, rr, absolute=True)
     names, tokens = ("dx", "dw", "dbias", "dh0"), B * L
@@ -235,7 +236,12 @@ def test_scan_backward(case):
     torch.cuda.synchronize()
     for p, q in zip(*two):
         assert (p is None and q is None) or torch.equal(p, q)  # a fixed order of summation
-    check_grads(two[0], dout, dfin, s, S, softplus, ref.runs(B, L, seq), case)
+    check_grads(two[0], used(dout, seq, S), dfin, s, S, softplus, ref.runs(B, L, seq), case)
+
+
+def used(dout, seq, S):
+    """The output gradients that count: none at padded tokens."""
+    return dout if seq is None else dout * ((seq >= 0) & (seq < S))[..., None]
 
 
 def check_grads(got, dout, dfin, s, S, softplus, rr, case):
@@ -277,7 +283,7 @@ def test_scan_long(case):
     # memories end after a few hundred tokens (decays of at least exp(-0.5 * 0.02) a token, sums of positive
     # scales), so a path has no more roundings that matter than one of 400 tokens; dA's sums run over all
     check_scan((out, fin), s, S, softplus, rr, min(L, 400), N, sdtype, "long")
-    check_grads(grads, dout, dfin, s, S, softplus, rr, (B, L) + case[2:])
+    check_grads(grads, used(dout, seq, S), dfin, s, S, softplus, rr, (B, L) + case[2:])
 
 
 def test_scan_of_a_prompt_in_two_calls_and_steps():
@@ -331,7 +337,7 @@ def test_scan_gradients_against_differences():
     rr = ref.runs(B, L, seq)
     args, h0 = call_args(s)
     kw = dict(seq_idx=seq.cuda(), nseq=S, initial_state=h0)
-    w, v = torch.randn(B, L, D, generator=g), torch.randn(S, D, N, generator=g)
+    w, v = used(torch.randn(B, L, D, generator=g), seq, S), torch.randn(S, D, N, generator=g)
     _, _, saved = ssd.selective_scan(*args, save_for_backward=True, **kw)
     grads = ssd.selective_scan_backward(w.cuda(), *args, saved=saved, dfinal_state=v.cuda(), **kw)
     by = dict(x=grads.dx, dt=grads.ddt, A=grads.dA, B=grads.dB, C=grads.dC, D=grads.dD, bias=grads.ddt_bias, z=grads.dz,
@@ -813,3 +819,36 @@ def test_first_call_inside_a_capture():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert (a is None and b is None) or torch.equal(a, b), k
+
+
+@pytest.mark.parametrize("L,D,N", [(60, 70, 16), (1700, 20, 8), (300, 40, 64)])
+def test_padding_adds_nothing_to_gradients(L, D, N):
+    """NaN and infinities in padded tokens, in every input and in dout: the gradients are those of clean padding, to the
+    bit, and zero at the padding."""
+    s, _, _, g = scan_inputs(2, L, D, N, 1, "bf16", "f32", None, False, True, True, True, seed=81)
+    seq = torch.full((2, L), -1, dtype=torch.int32)
+    seq[0, 5:L // 3], seq[0, L // 3:L // 3 + 9], seq[1, :2], seq[1, L - 20:] = 0, 1, 2, 3
+    pad = seq < 0
+    dout = torch.randn(2, L, D, generator=g).bfloat16()
+    w, b = torch.randn(D, 4, generator=g).cuda(), torch.randn(D, generator=g).cuda()
+    h0, c0 = torch.randn(4, D, N, generator=g).cuda(), torch.randn(4, D, 3, generator=g).bfloat16().cuda()
+    dfin, dcfin = torch.randn(4, D, N, generator=g).cuda(), torch.randn(4, D, 3, generator=g).bfloat16().cuda()
+    kw = dict(seq_idx=seq.cuda(), nseq=4)
+    res = []
+    for value in (0.0, float("nan"), float("inf"), float("-inf")):
+        inp = {k: (None if t is None else t.clone()) for k, t in s.items()}
+        do = dout.clone()
+        do[pad] = value
+        for k in ("x", "dt", "B", "C", "z"):
+            inp[k][pad] = value
+        args, _ = call_args(inp)
+        saved = ssd.selective_scan(*args, initial_state=h0, save_for_backward=True, **kw)[2]
+        gr = ssd.selective_scan_backward(do.cuda(), *args, saved=saved, initial_state=h0, dfinal_state=dfin, **kw)
+        cg = ssd.causal_conv_backward(do.cuda(), args[0], w, b, initial_state=c0, dfinal_state=dcfin, **kw)
+        torch.cuda.synchronize()
+        res.append([*gr, *cg])
+        for t in (gr.dx, gr.ddt, gr.dB, gr.dC, gr.dz, cg.dx):
+            assert not t[pad.cuda()].any()
+    for value, got in enumerate(res):
+        for name, a, c in zip(gr._fields + cg._fields, got, res[0]):
+            assert torch.isfinite(a.float()).all() and torch.equal(a, c), (value, name)
