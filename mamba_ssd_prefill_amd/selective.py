@@ -90,19 +90,21 @@ _MAX_PLANS = 512
 
 
 class _Plan:
-    __slots__ = ("prm", "ref", "fn", "name", "dev", "index", "out", "parts", "state", "sizes", "spaces", "new")
+    __slots__ = ("prm", "where", "address", "name", "dev", "index", "out", "parts", "state", "sizes", "spaces", "new")
 
     def __init__(self, name, prm, dev, out=None, parts=None, state=None, spaces=(), new=()):
         import torch
-        self.prm, self.ref, self.name, self.dev = prm, ctypes.byref(prm), name, dev
-        self.fn, self.index = getattr(load_library(), name), dev.index
+        self.prm, self.where, self.name, self.dev, self.index = prm, ctypes.addressof(prm), name, dev, dev.index
+        lib, ref = load_library(), ctypes.byref(prm)
+        fn = getattr(lib, name)
+        self.address = ctypes.cast(fn, ctypes.c_void_p).value
         # layouts of the output like x, of one output per split, of the states, and of other new tensors
         self.out, self.parts, self.state, self.new = out, parts, state, new
         self.sizes = []
         for s in spaces:
-            n = getattr(load_library(), s)(self.ref)
+            n = getattr(lib, s)(ref)
             if n == 0:  # parameters the library does not take: its own call says why, before it looks at a pointer
-                raise SSDError(self.fn(self.ref, *[0] * (len(self.fn.argtypes) - 1)), name)
+                raise SSDError(fn(ref, *[0] * (len(fn.argtypes) - 1)), name)
             self.sizes.append(n)
         self.spaces = [_layout((n,), torch.uint8, dev) for n in self.sizes]
 
@@ -111,11 +113,11 @@ class _Plan:
         if _raw is None:
             _bind()
         if self.index == _device():
-            rc = self.fn(self.ref, *args, _raw(self.index))
+            rc = _call(self.address, self.where, *args, _raw(self.index))
         else:
             import torch
             with torch.cuda.device(self.dev):
-                rc = self.fn(self.ref, *args, _raw(self.index))
+                rc = _call(self.address, self.where, *args, _raw(self.index))
         if rc:
             raise SSDError(rc, self.name)
 
@@ -135,8 +137,8 @@ def _bind():
 
 def _native():
     """The native module _meta (built with the library; like it, there is no fallback), its functions put in place of the
-    two stand-ins below."""
-    global _meta, _new
+    stand-ins below."""
+    global _meta, _new, _call
     load_library()
     import torch  # noqa: F401  (its libraries have to be loaded first)
     try:
@@ -144,7 +146,7 @@ def _native():
     except ImportError as e:
         raise RuntimeError("mamba_ssd_prefill_amd._meta is not built (%s); run `python -m mamba_ssd_prefill_amd.build`"
                            % e) from e
-    _meta, _new = m.meta, m.new
+    _meta, _new, _call = m.meta, m.new, m.call
     return m
 
 
@@ -156,6 +158,11 @@ def _meta(*tensors):
 def _new(*layouts):
     """New tensors of the layouts."""
     return _native().new(*layouts)
+
+
+def _call(function, *args):
+    """A function of the library by its address."""
+    return _native().call(function, *args)
 
 
 def _layout(shape, dtype, dev):

@@ -291,3 +291,22 @@ def test_a_launch_s_lanes_are_bounded(lib, name, fits, over):
     first = ARGS[name][0].split()[0]
     assert call(lib, name, params_for(name, **fits), **{first: None}) == NULLP
     assert call(lib, name, params_for(name, **over), **{first: None}) == SHAPE
+
+
+def test_library_calls_by_address():
+    from mamba_ssd_prefill_amd._meta import call
+    for n in (0, 1, 5, 6, 7, 17, 26, 32):
+        seen = []
+        f = ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_size_t] * n)(lambda *a: seen.append(a) or -n)
+        where = ctypes.cast(f, ctypes.c_void_p).value
+        args = [(1 << 63) + 7 * i if i % 3 else None for i in range(n)]
+        assert call(where, *args) == -n
+        assert seen == [tuple(a or 0 for a in args)]
+    for bad in ((), (where,) + (0,) * 33):
+        with pytest.raises(TypeError):
+            call(*bad)
+    with pytest.raises(ValueError):
+        call(0, 1)
+    for bad in ("x", -1, 1 << 64, 1.5):
+        with pytest.raises((TypeError, OverflowError)):
+            call(where, bad)
