@@ -243,8 +243,9 @@ __device__ inline void join_splits(float A2, float v, int n, Step step, Place pl
 }
 
 // The same inside a pass over the splits, for a wave's own NS states of up to kFoldSplits splits: h after n splits,
-// without the join's launch (1 x 131 x 1536 in 9 splits: 16.4 us so, 19.1 with the launch; with more splits every
-// workgroup's own walk takes longer than the launch).
+// without the join's launch.  With more splits every workgroup's own walk takes longer than that launch: 1 x 131 x 1536 in 9
+// splits takes 16.4 us a call so and 19.1 with the launch, but the main pass of 2 x 2048 x 5120 in 19 splits 119.8 us
+// against 109.5 + 7.5, the backward of 2 x 500 x 1536 in some 30 splits 38.6 against 28.0 + 6.1.
 constexpr int kFoldSplits = 16;
 template <int NS, typename Step, typename Place>
 __device__ inline void fold_splits(const float (&A2)[NS], float (&h)[NS], int n, Step step, Place place) {
