@@ -37,7 +37,8 @@ template <typename T, int TPW, bool Z> struct ScanTokens {
 // A workgroup runs its split's tokens a tile at a time: every wave prepares its tokens' (d, d x) in LDS, runs the
 // recurrence of its NS states through the tile, leaves its share of y in LDS, and finishes its tokens.  Four states a
 // lane (N = 64: eight) is what leaves a wave's part of the sums over n small and the waves many.  At 2 x 8192 x 5120, N = 16,
-// bf16: 339 us, the vector ALU busy for 81% of it with 8.0 slots a (token, channel, n), 6 of them the recurrence's.
+// bf16: 339 us, the vector ALU issuing in 96% of the cycles (some 2.0 GHz under this load) with 8.1 slots a (token,
+// channel, n), 6 of them the recurrence's.
 template <typename T, int NW, int NS, bool VL>
 __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
     constexpr int TPW = kTile / NW;    // tokens a wave prepares and finishes
@@ -146,7 +147,8 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
 // First pass over the time splits: the state at the end of each split but the last, from a zero state at
 // its start (into the next split's place), and the sum of its steps, by which the state entering it decays
 // (infinite where a sequence starts inside: nothing passes).  One barrier a tile: the next tile's (d, d x) go to the other
-// buffer.  At 2 x 8192 x 5120, N = 16, bf16: 244 us, the vector ALU busy for 84% of it with 6.1 slots a (token, channel, n).
+// buffer.  At 2 x 8192 x 5120, N = 16, bf16: 244 us, the vector ALU issuing in all cycles with 6.1 slots a (token,
+// channel, n), 5 of them the recurrence's.
 template <typename T, int NW, int NS, bool VL>
 __global__ __launch_bounds__(NW * 64) void k_scan_carry(ScanArgs a) {
     constexpr int TPW = kTile / NW, N = NW * NS;

@@ -10,8 +10,9 @@
 // from the saved state that enters it and kept in registers with their decays, and then the gradients run
 // back through them.  Tiles of 16 tokens (half the saved states) needed twice the registers and LDS, and with
 // two waves a SIMD instead of three the vector ALU waited: 360 us against 278 us at 2 x 2048 x 5120, N = 16, bf16.
-// Bound by the vector ALU: some 25 slots a (token, channel, n), 6 for the states and y again, 8 for the gradients, 6 for
-// the two sums over the channels (dB and dC), the rest what a (token, channel) needs once.
+// Bound by the vector ALU, which issues in 95% of the cycles there: 26 slots a (token, channel, n), 6 for the states and y
+// again, 8 for the gradients, 6 for the two sums over the channels (dB and dC), the rest what a (token, channel)
+// needs once.
 #include "ssd_scan_common.h"
 #include "ssd_sum_rows.h"
 
