@@ -447,9 +447,9 @@ template <typename T, int W> __global__ __launch_bounds__(256) void k_causal_con
 // Tokens of a run, up to `most`.  Long runs read fewer rows twice; and the workgroups, 2048 of which the chip holds at a
 // time, should come in full rounds, for in a round that is partly filled too few loads are on their way.  Both as a
 // cost relative to one pass over the rows, fitted to the times (us) of runs of 8, 16, 24, 32, 48 and 64 tokens:
-// 2 x 4096 x 5376 forward 37.6 35.0 34.2 36.6 34.1 36.6, backward 75 66 64 65 61 66;
-// 8 x 2048 x 5376 forward 74 73 73 73 78 79 (so 32 at most forward), backward 146 131 127 123 123 132;
-// 1 x 4096 x 1792 forward 7.8 8.5 8.8 10.2 12.9 15.7, backward 15.0 15.6 16.5 18.6 22.5 27.1.
+// 2 x 4096 x 5376 forward 35.3 34.0 33.0 35.2 33.1 35.8, backward 75 66 64 65 61 66;
+// 8 x 2048 x 5376 forward 73 73 72 72 74 77 (so 32 at most forward), backward 146 131 127 123 123 132;
+// 1 x 4096 x 1792 forward 8.1 8.2 9.0 10.1 12.5 14.4, backward 17.3 16.8 18.8 19.0 25.1 28.3.
 static int conv_rows(int64_t batch, int64_t seqlen, int64_t pieces, int most) {
     const int64_t pblocks = (pieces + 63) / 64;
     int best = 8;
@@ -464,21 +464,21 @@ static int conv_rows(int64_t batch, int64_t seqlen, int64_t pieces, int most) {
     }
     return best;
 }
-constexpr int kConvWide = 4;          // channels a lane of the forward takes where rows allow it
-constexpr int kConvBackwardWide = 2;  // and of the backward (4: 79 us against 70 with 2 at 2 x 4096 x 5376)
+// Channels a lane takes where rows allow it (4: forward 36.7 us against 36.8 with 2 at 2 x 4096 x 5376 and 11.3 against 9.6 at
+// 1 x 4096 x 1792, packed; backward 79 against 70 at 2 x 4096 x 5376).
+constexpr int kConvWide = 2;
 constexpr int kConvMost = 32, kConvBackwardMost = 64;
 
 int conv_backward_rows(int64_t batch, int64_t seqlen, int64_t channels) {
-    return conv_rows(batch, seqlen, (channels + kConvBackwardWide - 1) / kConvBackwardWide, kConvBackwardMost);
+    return conv_rows(batch, seqlen, (channels + kConvWide - 1) / kConvWide, kConvBackwardMost);
 }
 
-// Whether lanes can take four channels with one access: every row they touch starts on a
-// multiple of four elements.
-static bool conv_vec4(const CausalConvArgs& a, size_t es, const void* const* tens, int ntens) {
-    if (a.channels % 4 || a.split_a % 4 || a.split_b % 4 || a.xs % 4) return false;
-    if ((uintptr_t)a.x % (4 * es)) return false;
+// Whether lanes can take kConvWide channels with one access: every row they touch starts on a multiple of as many elements.
+static bool conv_wide(const CausalConvArgs& a, size_t es, const void* const* tens, int ntens) {
+    if (a.channels % kConvWide || a.split_a % kConvWide || a.split_b % kConvWide || a.xs % kConvWide) return false;
+    if ((uintptr_t)a.x % (kConvWide * es)) return false;
     for (int i = 0; i < ntens; ++i)
-        if ((uintptr_t)tens[i] % (4 * es)) return false;
+        if ((uintptr_t)tens[i] % (kConvWide * es)) return false;
     return true;
 }
 
@@ -488,13 +488,13 @@ static unsigned conv_blocks(const CausalConvArgs& a, int cw) {
 }
 
 template <typename T, int W> hipError_t launch_conv_tw(CausalConvArgs& a, hipStream_t st) {
-    const bool v4 = conv_vec4(a, sizeof(T), a.out, 3);
-    a.rows = conv_rows(a.batch, a.seqlen, a.channels / (v4 ? kConvWide : 1), kConvMost);
+    const bool wide = conv_wide(a, sizeof(T), a.out, 3);
+    a.rows = conv_rows(a.batch, a.seqlen, a.channels / (wide ? kConvWide : 1), kConvMost);
     a.nseg = (a.seqlen + a.rows - 1) / a.rows;
     void* args[] = {&a};
-    const void* fn = a.seq ? (v4 ? (const void*)&k_causal_conv<T, W, kConvWide, true> : (const void*)&k_causal_conv<T, W, 1, true>)
-                           : (v4 ? (const void*)&k_causal_conv<T, W, kConvWide, false> : (const void*)&k_causal_conv<T, W, 1, false>);
-    return hipLaunchKernel(fn, dim3(conv_blocks(a, v4 ? kConvWide : 1)), dim3(256), args, 0, st);
+    const void* fn = a.seq ? (wide ? (const void*)&k_causal_conv<T, W, kConvWide, true> : (const void*)&k_causal_conv<T, W, 1, true>)
+                           : (wide ? (const void*)&k_causal_conv<T, W, kConvWide, false> : (const void*)&k_causal_conv<T, W, 1, false>);
+    return hipLaunchKernel(fn, dim3(conv_blocks(a, wide ? kConvWide : 1)), dim3(256), args, 0, st);
 }
 
 template <typename T, int W, int CW> const void* conv_backward_kernel(bool packed, bool states) {
@@ -507,12 +507,12 @@ template <typename T, int W> hipError_t launch_conv_back_tw(CausalConvArgs& a, f
     a.rows = conv_backward_rows(a.batch, a.seqlen, a.channels);
     a.nseg = (a.seqlen + a.rows - 1) / a.rows;
     const void* tens[4] = {a.dout[0], a.dout[1], a.dout[2], a.dx};
-    const bool v4 = conv_vec4(a, sizeof(T), tens, 4);
+    const bool wide = conv_wide(a, sizeof(T), tens, 4);
     void* args[] = {&a};
     const bool states = a.dh0 || a.dfin;
-    const void* fn = v4 ? conv_backward_kernel<T, W, kConvBackwardWide>(a.seq, states)
+    const void* fn = wide ? conv_backward_kernel<T, W, kConvWide>(a.seq, states)
                         : conv_backward_kernel<T, W, 1>(a.seq, states);
-    hipError_t e = hipLaunchKernel(fn, dim3(conv_blocks(a, v4 ? kConvBackwardWide : 1)), dim3(256), args, 0, st);
+    hipError_t e = hipLaunchKernel(fn, dim3(conv_blocks(a, wide ? kConvWide : 1)), dim3(256), args, 0, st);
     if (e != hipSuccess) return e;
     int nrows = (int)(((int64_t)a.batch * a.nseg + 3) / 4);
     const int64_t n = (int64_t)a.channels * (W + 1);
