@@ -440,7 +440,7 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
                    initial_state=None, state_dtype=None, save_for_backward=False, with_final_state=True,
                    final_state=None, out=None, workspace=None):
     """ssd_selective_scan over a prompt: x, dt, z [B, L, D], A [D, N] float32, B, C [B, L, G, N], D and dt_bias [D]
-    float32.  Returns (out [B, L, D], final_state [B or nseq, D, N]), and with ``save_for_backward`` a third
+    float32; the rows of B and C start on multiples of 4 bytes.  Returns (out [B, L, D], final_state [B or nseq, D, N]), and with ``save_for_backward`` a third
     tensor for selective_scan_backward.  ``state_dtype`` defaults to initial_state's, else float32."""
     meta, (px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, pf, po) = _meta(x, dt, A, B, C, D, dt_bias, z, seq_idx, initial_state,
                                                                     final_state, out)
