@@ -19,8 +19,8 @@ the current stream of the tensors' device.  The names are re-exported by the pac
 Inputs with one row per token (x, dt, z, B, C) may be views whose rows lie a constant distance apart,
 such as the halves of a joint projection; everything else is contiguous.  Sequences packed into a
 batch row are told apart by ``seq_idx`` (int32 [B, L], numbers in [0, nseq), each for one run of tokens;
--1: padding, which gets and adds zero gradients), and states then have one entry per number instead of one per batch row.  ``slots`` name each
-state that a call writes once.
+-1: padding, which gets and adds zero gradients), and states then have one entry per number instead
+of one per batch row.  ``slots`` name each state that a call writes once.
 """
 import collections
 import ctypes
@@ -440,8 +440,9 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
                    initial_state=None, state_dtype=None, save_for_backward=False, with_final_state=True,
                    final_state=None, out=None, workspace=None):
     """ssd_selective_scan over a prompt: x, dt, z [B, L, D], A [D, N] float32, B, C [B, L, G, N], D and dt_bias [D]
-    float32; the rows of B and C start on multiples of 4 bytes.  Returns (out [B, L, D], final_state [B or nseq, D, N]), and with ``save_for_backward`` a third
-    tensor for selective_scan_backward.  ``state_dtype`` defaults to initial_state's, else float32."""
+    float32; the rows of B and C start on multiples of 4 bytes.  Returns (out [B, L, D], final_state
+    [B or nseq, D, N]), and with ``save_for_backward`` a third tensor for selective_scan_backward.
+    ``state_dtype`` defaults to initial_state's, else float32."""
     meta, (px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, pf, po) = _meta(x, dt, A, B, C, D, dt_bias, z, seq_idx, initial_state,
                                                                     final_state, out)
     key = ("scan", meta, dt_softplus, nseq, state_dtype)
