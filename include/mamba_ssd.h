@@ -502,7 +502,7 @@ ssd_status_t ssd_causal_conv_step(const ssd_conv_params_t* p, const void* x, con
 typedef struct {
     size_t struct_size; /* sizeof(ssd_scan_params_t) */
     int batch;          /* B >= 1 */
-    int seqlen;         /* L >= 1 (1 for ssd_selective_scan_step) */
+    int seqlen;         /* L >= 1, up to 2^31 - 64 (1 for ssd_selective_scan_step) */
     int channels;       /* D >= 1 */
     int dstate;         /* N in {8, 16, 32, 64} */
     int ngroups;        /* G >= 1, D % G == 0 */

@@ -174,6 +174,7 @@ SSD_EXPORT ssd_status_t ssd_causal_conv_step(const ssd_conv_params_t* p, const v
 namespace {
 
 constexpr int kScanTile = 16;  // tokens of a forward tile
+constexpr int64_t kMaxSeqlen = kMaxIndex - 64;  // a tile, and the 64 tokens whose numbers it looks at, end below 2^31
 constexpr int64_t kMaxRow = (int64_t)1 << 24;  // elements between rows
 
 ssd_status_t validate_scan(const ssd_scan_params_t* p, bool step) {
@@ -195,7 +196,8 @@ ssd_status_t validate_scan(const ssd_scan_params_t* p, bool step) {
         p->C_stride >= kMaxRow || p->channels >= kMaxRow || gn >= kMaxRow)
         return SSD_ERR_INVALID_SHAPE;
     if (p->in_dtype != SSD_F32 && (p->B_stride % 2 || p->C_stride % 2)) return SSD_ERR_MISALIGNED;
-    // rows, channels and workgroups have to fit 32-bit indexes
+    // rows, tokens behind a row's end, channels and workgroups have to fit 32-bit indexes
+    if (p->seqlen > kMaxSeqlen) return SSD_ERR_INVALID_SHAPE;
     if ((int64_t)p->batch * p->seqlen >= kMaxIndex || (int64_t)p->channels * N >= kMaxIndex)
         return SSD_ERR_INVALID_SHAPE;
     const int64_t blocks = (int64_t)p->batch * p->ngroups * ((p->channels / p->ngroups + 63) / 64);
@@ -203,6 +205,8 @@ ssd_status_t validate_scan(const ssd_scan_params_t* p, bool step) {
     if (step && p->batch * (((int64_t)p->channels * (N / 4) + 255) / 256) >= kMaxLanes / 256) return SSD_ERR_INVALID_SHAPE;
     return SSD_OK;
 }
+
+int64_t scan_tiles(const ssd_scan_params_t* p, int tile) { return ((int64_t)p->seqlen + tile - 1) / tile; }
 
 // The backward's sums take a lane for four values of dB or dC and for one of the parameters' gradients, by four waves.
 ssd_status_t validate_scan_backward(const ssd_scan_params_t* p) {
@@ -242,7 +246,7 @@ ssd::ScanArgs scan_args(const ssd_scan_params_t* p, const void* x, const void* d
     a.zs = p->z_stride ? p->z_stride : D_;
     a.Bs = p->B_stride ? p->B_stride : gn;
     a.Cs = p->C_stride ? p->C_stride : gn;
-    a.ntiles = (p->seqlen + ssd::kScanPeriod - 1) / ssd::kScanPeriod;
+    a.ntiles = (int)scan_tiles(p, ssd::kScanPeriod);
     return a;
 }
 
@@ -299,7 +303,7 @@ SSD_EXPORT size_t ssd_selective_scan_backward_workspace_size(const ssd_scan_para
 
 SSD_EXPORT size_t ssd_selective_scan_saved_size(const ssd_scan_params_t* p) {
     if (validate_scan(p, false) != SSD_OK) return 0;
-    return (size_t)p->batch * ((p->seqlen + ssd::kScanPeriod - 1) / ssd::kScanPeriod) * p->channels * p->dstate * 4;
+    return (size_t)p->batch * scan_tiles(p, ssd::kScanPeriod) * p->channels * p->dstate * 4;
 }
 
 SSD_EXPORT ssd_status_t ssd_selective_scan(const ssd_scan_params_t* p, const void* x, const void* dt, const float* A,
@@ -325,7 +329,7 @@ SSD_EXPORT ssd_status_t ssd_selective_scan(const ssd_scan_params_t* p, const voi
     a.fin = final_state;
     a.saved = (float*)saved;
     a.nsplit = l.nsplit;
-    a.tiles_per_split = ((p->seqlen + kScanTile - 1) / kScanTile + l.nsplit - 1) / l.nsplit;
+    a.tiles_per_split = (int)((scan_tiles(p, kScanTile) + l.nsplit - 1) / l.nsplit);
     a.split_state = (float*)((char*)workspace + l.state_off);
     a.split_sum = (float*)((char*)workspace + l.sum_off);
     return hip_status(ssd::launch_scan(a, p->in_dtype, (hipStream_t)stream));

@@ -310,3 +310,16 @@ def test_library_calls_by_address():
     for bad in ("x", -1, 1 << 64, 1.5):
         with pytest.raises((TypeError, OverflowError)):
             call(where, bad)
+
+
+@pytest.mark.parametrize("over", [0, 1, 47, 55, 62])
+def test_scan_tiles_of_the_longest_rows_stay_in_range(lib, over):
+    """A row's tiles and the tokens a tile reaches behind it are 32-bit numbers: the last 63 lengths are refused (the
+    backward's sums stop earlier)."""
+    one = dict(batch=1, channels=1, dstate=8)
+    assert call(lib, "ssd_selective_scan", scan_prm(seqlen=(1 << 31) - 64, **one), x=None) == NULLP
+    assert call(lib, "ssd_selective_scan", scan_prm(seqlen=(1 << 31) - 1 - over, **one), x=None) == SHAPE
+    assert lib.ssd_selective_scan_saved_size(ctypes.byref(scan_prm(seqlen=(1 << 31) - 64, **one))) == ((1 << 28) - 8) * 8 * 4
+    for size in (lib.ssd_selective_scan_saved_size, lib.ssd_selective_scan_workspace_size,
+                 lib.ssd_selective_scan_backward_workspace_size):
+        assert size(ctypes.byref(scan_prm(seqlen=(1 << 31) - 1 - over, **one))) == 0
