@@ -52,6 +52,14 @@ ssd_status_t validate_conv(const ssd_conv_params_t* p, bool step) {
     return SSD_OK;
 }
 
+// The backward's sums take four lanes for each value of dw and dbias.
+ssd_status_t validate_conv_backward(const ssd_conv_params_t* p) {
+    const ssd_status_t s = validate_conv(p, false);
+    if (s != SSD_OK) return s;
+    if (((int64_t)p->channels * (p->width + 1) + 63) / 64 >= kMaxLanes / 256) return SSD_ERR_INVALID_SHAPE;
+    return SSD_OK;
+}
+
 ssd::CausalConvArgs conv_args(const ssd_conv_params_t* p, const void* x, const float* w, const float* bias) {
     ssd::CausalConvArgs a{};
     a.x = x;
@@ -113,7 +121,7 @@ SSD_EXPORT ssd_status_t ssd_causal_conv(const ssd_conv_params_t* p, const void* 
 }
 
 SSD_EXPORT size_t ssd_causal_conv_backward_workspace_size(const ssd_conv_params_t* p) {
-    if (validate_conv(p, false) != SSD_OK) return 0;
+    if (validate_conv_backward(p) != SSD_OK) return 0;
     return conv_part_bytes(p);
 }
 
@@ -123,7 +131,7 @@ SSD_EXPORT ssd_status_t ssd_causal_conv_backward(const ssd_conv_params_t* p, con
                                                  const void* initial_state, void* dx, float* dw, float* dbias,
                                                  void* dinitial_state, void* workspace, size_t workspace_bytes,
                                                  void* stream) {
-    ssd_status_t s = validate_conv(p, false);
+    ssd_status_t s = validate_conv_backward(p);
     if (s != SSD_OK) return s;
     if (!x || !w || !dx || !dw || !workspace) return SSD_ERR_NULL_POINTER;
     const size_t es = elem_size(p->in_dtype);

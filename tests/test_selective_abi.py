@@ -323,3 +323,16 @@ def test_scan_tiles_of_the_longest_rows_stay_in_range(lib, over):
     for size in (lib.ssd_selective_scan_saved_size, lib.ssd_selective_scan_workspace_size,
                  lib.ssd_selective_scan_backward_workspace_size):
         assert size(ctypes.byref(scan_prm(seqlen=(1 << 31) - 1 - over, **one))) == 0
+
+
+@pytest.mark.parametrize("width,most", [(2, (1 << 30) // 3), (3, (1 << 30) // 4 - 1), (4, (1 << 30) // 5)])
+def test_lanes_of_the_convolution_backward_s_sums_are_bounded(lib, width, most):
+    """k_conv_sums takes four lanes a value of dw and dbias: (width + 1) * channels of them stay below 2^30."""
+    name = "ssd_causal_conv_backward"
+    at = lambda n: conv_prm(batch=1, seqlen=1, channels=n, split_a=n, split_b=n, width=width)  # noqa: E731
+    most = most // 64 * 64
+    assert call(lib, name, at(most), x=None) == NULLP
+    assert call(lib, name, at(most + 64), x=None) == SHAPE
+    assert lib.ssd_causal_conv_backward_workspace_size(ctypes.byref(at(most))) > 0
+    assert lib.ssd_causal_conv_backward_workspace_size(ctypes.byref(at(most + 64))) == 0
+    assert call(lib, "ssd_causal_conv", at(most + 64), x=None) == NULLP
