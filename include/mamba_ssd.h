@@ -456,7 +456,7 @@ typedef struct {
     int split_a;        /* 0 <= split_a <= split_b <= Ch: channels [0, split_a) go to out0, */
     int split_b;        /* [split_a, split_b) to out1, the rest to out2 (each [B, L, its channels]); */
                         /* split_a = Ch: everything to out0 */
-    int64_t x_stride;   /* elements between rows of x; 0: Ch */
+    int64_t x_stride;   /* elements between rows of x, below 2^31; 0: Ch */
 } ssd_conv_params_t;
 
 /*   x             [B, L, Ch]   in_dtype  required, rows
@@ -510,8 +510,8 @@ typedef struct {
     int state_dtype;    /* ssd_dtype_t of the states and their gradients (the scan itself runs in fp32) */
     int dt_softplus;    /* 1: d = softplus(dt_raw + dt_bias); 0: d = dt_raw + dt_bias */
     int nseq;           /* with seq_idx (or for the step): the number of states; else ignored */
-    int64_t x_stride, dt_stride, z_stride; /* elements between rows, below 2^24; 0: D (below 2^24) */
-    int64_t B_stride, C_stride;            /* elements between rows, below 2^24; 0: G*N (even for 16-bit types) */
+    int64_t x_stride, dt_stride, z_stride; /* elements between rows, below 2^24 (the step: 2^31); 0: D (below 2^24) */
+    int64_t B_stride, C_stride;            /* the same; 0: G*N (below 2^24); even for 16-bit types */
 } ssd_scan_params_t;
 
 /*   x, dt         [B, L, D]     in_dtype    required, rows

@@ -199,9 +199,10 @@ ssd_status_t validate_scan(const ssd_scan_params_t* p, bool step) {
     if (!stride_ok(p->x_stride, p->channels) || !stride_ok(p->dt_stride, p->channels) ||
         !stride_ok(p->z_stride, p->channels) || !stride_ok(p->B_stride, gn) || !stride_ok(p->C_stride, gn))
         return SSD_ERR_INVALID_SHAPE;
-    // a tile's rows are accessed at 32-bit offsets, those of B and C four bytes at a time
-    if (p->x_stride >= kMaxRow || p->dt_stride >= kMaxRow || p->z_stride >= kMaxRow || p->B_stride >= kMaxRow ||
-        p->C_stride >= kMaxRow || p->channels >= kMaxRow || gn >= kMaxRow)
+    // a tile's rows are accessed at 32-bit offsets (a step's at 64-bit ones), those of B and C four bytes at a time
+    if (p->channels >= kMaxRow || gn >= kMaxRow) return SSD_ERR_INVALID_SHAPE;
+    if (!step && (p->x_stride >= kMaxRow || p->dt_stride >= kMaxRow || p->z_stride >= kMaxRow ||
+                  p->B_stride >= kMaxRow || p->C_stride >= kMaxRow))
         return SSD_ERR_INVALID_SHAPE;
     if (p->in_dtype != SSD_F32 && (p->B_stride % 2 || p->C_stride % 2)) return SSD_ERR_MISALIGNED;
     // rows, tokens behind a row's end, channels and workgroups have to fit 32-bit indexes

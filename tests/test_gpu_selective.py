@@ -852,3 +852,26 @@ def test_padding_adds_nothing_to_gradients(L, D, N):
     for value, got in enumerate(res):
         for name, a, c in zip(gr._fields + cg._fields, got, res[0]):
             assert torch.isfinite(a.float()).all() and torch.equal(a, c), (value, name)
+
+
+def test_steps_on_views_far_apart():
+    """A token of every row of long tensors, both steps of a layer: views whose rows lie more than 2^24 elements apart."""
+    B, D, N, row = 3, 64, 16, (1 << 24) + 128
+    s, _, _, g = scan_inputs(B, 1, D, N, 1, "bf16", "f32", None, True, True, True, True, seed=91)
+    (x, dt, A, Bm, C, Dp, bias, z), h0 = call_args(s)
+    wide = torch.zeros(B, row, dtype=torch.bfloat16, device="cuda")
+    near = [x[:, 0], dt[:, 0], Bm[:, 0], C[:, 0], z[:, 0]]
+    far = [wide[:, 64 * i:64 * i + t[0].numel()].unflatten(1, t.shape[1:]) for i, t in enumerate(near)]
+    for f, t in zip(far, near):
+        f.copy_(t)
+    pools, outs = [h0.clone(), h0.clone()], []
+    for st, (x_, dt_, B_, C_, z_) in zip(pools, (near, far)):
+        outs.append(ssd.selective_scan_step(x_, dt_, A, B_, C_, Dp, bias, z_, state=st))
+    w, convs = torch.randn(D, 4, generator=g).cuda(), []
+    for x_ in (near[0], far[0]):
+        st = torch.zeros(B, D, 3, dtype=torch.bfloat16, device="cuda")
+        convs += [ssd.causal_conv_step(x_, w, state=st), st]
+    torch.cuda.synchronize()
+    assert far[0].stride(0) == row and torch.equal(*outs) and torch.equal(*pools)
+    assert torch.equal(convs[0], convs[2]) and torch.equal(convs[1], convs[3])
+    check_scan((outs[1][:, None], pools[1]), s, B, True, ref.runs(B, 1), 1, N, "f32", "far step")

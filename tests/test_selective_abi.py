@@ -336,3 +336,17 @@ def test_lanes_of_the_convolution_backward_s_sums_are_bounded(lib, width, most):
     assert lib.ssd_causal_conv_backward_workspace_size(ctypes.byref(at(most))) > 0
     assert lib.ssd_causal_conv_backward_workspace_size(ctypes.byref(at(most + 64))) == 0
     assert call(lib, "ssd_causal_conv", at(most + 64), x=None) == NULLP
+
+
+@pytest.mark.parametrize("field", ["x_stride", "dt_stride", "z_stride", "B_stride", "C_stride"])
+def test_rows_of_a_step_may_lie_far_apart(lib, field):
+    """One token of every row of a long joint projection (x = u[:, t, :D]): rows 2^24 elements and more apart, which the
+    prompt's tiles do not reach."""
+    name = "ssd_selective_scan_step"
+    for far in (1 << 24, 200000 * 10240, (1 << 31) - 2):
+        assert call(lib, name, params_for(name, **{field: far}), x=None) == NULLP
+    assert call(lib, name, params_for(name, **{field: 1 << 31}), x=None) == SHAPE
+    if field[0] in "BC":
+        assert call(lib, name, params_for(name, **{field: (1 << 24) + 1}), x=None) == MISAL
+    for name in ("ssd_selective_scan", "ssd_selective_scan_backward"):
+        assert call(lib, name, params_for(name, **{field: 1 << 24}), **{ARGS[name][0].split()[0]: None}) == SHAPE
