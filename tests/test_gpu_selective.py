@@ -875,3 +875,38 @@ def test_steps_on_views_far_apart():
     assert far[0].stride(0) == row and torch.equal(*outs) and torch.equal(*pools)
     assert torch.equal(convs[0], convs[2]) and torch.equal(convs[1], convs[3])
     check_scan((outs[1][:, None], pools[1]), s, B, True, ref.runs(B, 1), 1, N, "f32", "far step")
+
+
+# Lanes take two batch rows once that leaves 1024 workgroups: ceil(D / (1024 / N)) * (B // 2) of them.
+@pytest.mark.parametrize("N,D,G,B", [(16, 2048, 1, 65), (8, 4100, 2, 63), (32, 1028, 4, 65), (64, 520, 1, 64), (16, 2048, 2, 63),
+                                     (8, 4100, 1, 64)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("sdtype", ["f32", "f16", "bf16"])
+def test_scan_step_of_large_batches(N, D, G, B, dtype, sdtype):
+    """Batches at and below the edge (32 * 32, 33 * 31, 33 * 32, 33 * 32, 32 * 31, 33 * 32 workgroups), odd and even, on
+    shuffled slots of a larger pool; rows without a slot, each with a live one beside it; other slots keep their bits."""
+    say("scan step of a large batch", N, D, G, B, dtype, sdtype)
+    gate = sdtype != "f16"
+    s, _, _, g = scan_inputs(B, 1, D, N, G, dtype, sdtype, None, True, gate, gate, gate, seed=101)
+    (x, dt, A, Bm, C, Dp, bias, z), h0 = call_args(s)
+    nslots = B + 9
+    pool = torch.randn(nslots, D, N, generator=g).to(DT[sdtype]).cuda()
+    where = torch.randperm(nslots, generator=g)[:B]
+    slots = where.to(torch.int32)
+    none = {4: -1, 9: nslots, 20: -2 ** 31, 31: 2 ** 31 - 1, B - 1: -7}
+    for b, v in none.items():
+        slots[b] = v
+    live = torch.tensor([b not in none for b in range(B)])
+    pool[where[live].cuda()] = h0[live.cuda()]
+    before = pool.clone()
+    out = ssd.selective_scan_step(x[:, 0], dt[:, 0], A, Bm[:, 0], C[:, 0], Dp, bias, None if z is None else z[:, 0],
+                                  state=pool, slots=slots.cuda(), dt_softplus=gate)
+    torch.cuda.synchronize()
+    out, pool, before = out.cpu(), pool.cpu(), before.cpu()
+    assert not out[~live].any()
+    rest = torch.ones(nslots, dtype=torch.bool)
+    rest[where[live]] = False
+    assert torch.equal(pool[rest], before[rest])
+    part = {k: v[live] if v is not None and k in ("x", "dt", "B", "C", "z", "h0") else v for k, v in s.items()}
+    n = int(live.sum())
+    check_scan((out[live][:, None], pool[where[live]]), part, n, gate, ref.runs(n, 1), 1, N, sdtype, "step")
