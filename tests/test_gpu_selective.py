@@ -910,3 +910,48 @@ def test_scan_step_of_large_batches(N, D, G, B, dtype, sdtype):
     part = {k: v[live] if v is not None and k in ("x", "dt", "B", "C", "z", "h0") else v for k, v in s.items()}
     n = int(live.sum())
     check_scan((out[live][:, None], pool[where[live]]), part, n, gate, ref.runs(n, 1), 1, N, sdtype, "step")
+
+
+def time_splits(B, L, D, N, G, backward):
+    """The number of time splits, from the workspace: a split holds its state and the sum of its steps, backward also its
+    part of dA, dD and ddt_bias beside dB and dC of every channel block."""
+    import ctypes
+    lib = ssd.load_library()
+    p = ssd.ScanParams(ctypes.sizeof(ssd.ScanParams), B, L, D, N, G, 0, 0, 1, 0, 0, 0, 0, 0, 0)
+    if not backward:
+        return max(1, round(lib.ssd_selective_scan_workspace_size(ctypes.byref(p)) / (B * D * (N + 1) * 4)))
+    bc = 2 * B * G * ((D // G + 63) // 64) * L * N * 4
+    n = lib.ssd_selective_scan_backward_workspace_size(ctypes.byref(p)) - bc
+    one = B * D * (N + 2) * 4
+    return 1 if n < 1.5 * one else round(n / (one + B * D * (N + 1) * 4))
+
+
+@pytest.mark.parametrize("want,backward,B,D,N,G,dtype,sdtype", [
+    (2, False, 1, 70, 64, 1, "f32", "f32"), (4, True, 1, 64, 8, 1, "f32", "f32"), (6, False, 2, 130, 8, 2, "f32", "f32"),
+    (9, False, 1, 70, 16, 1, "f16", "f32"), (9, True, 2, 70, 16, 1, "bf16", "f32"), (13, False, 1, 40, 32, 1, "f32", "bf16"),
+    (13, True, 2, 33, 64, 1, "bf16", "f32"), (16, True, 2, 20, 16, 1, "f32", "f32"), (17, True, 1, 20, 16, 1, "f32", "f32"),
+    (16, False, 1, 20, 16, 1, "f32", "f32"), (17, False, 2, 20, 32, 1, "f32", "f32")])
+def test_states_cross_time_splits(want, backward, B, D, N, G, dtype, sdtype):
+    """Unpacked prompts in few splits (joined within the passes up to 16, by a launch of their own from 17), their states
+    going in and the gradients of those coming out across all of them.  The length is the first whose number of splits
+    is nearest to the one wanted.
+
+    The steps' sum times |A| stays below 0.0125 L over a row, so what enters at one end is there at the other.  A split's
+    decay, from a sum of steps with at most (16 + 34 tiles) roundings, adds 0.0125 L * 50 u < L u to the 8 L u of the
+    bound's exponentials, which count 8 roundings a token where two products, a sum and an exponential round 5 times."""
+    L = min(range(33, 530), key=lambda n: (abs(time_splits(B, n, D, N, G, backward) - want), n))
+    took = [time_splits(B, L, D, N, G, b) for b in (False, True)]
+    say("states cross splits", want, backward, B, L, D, N, G, dtype, sdtype, "splits", took)
+    assert took[backward] >= 2
+    s, _, _, g = scan_inputs(B, L, D, N, G, dtype, sdtype, None, True, True, True, True, seed=111)
+    s["A"] = -0.02 * torch.rand(D, N, generator=g)
+    assert float(0.02 * ref.steps(s["dt"], s["bias"], True)[1].sum(1).max()) <= 0.0125 * L
+    args, h0 = call_args(s)
+    kw = dict(initial_state=h0, state_dtype=DT[sdtype])
+    out, fin, saved = ssd.selective_scan(*args, save_for_backward=True, **kw)
+    dout, dfin = torch.randn(B, L, D, generator=g).to(s["x"].dtype), torch.randn(B, D, N, generator=g).to(DT[sdtype])
+    grads = ssd.selective_scan_backward(dout.cuda(), *args, saved=saved, dfinal_state=dfin.cuda(), **kw)
+    torch.cuda.synchronize()
+    rr = ref.runs(B, L)
+    check_scan((out, fin), s, B, True, rr, L, N, sdtype, "splits")
+    check_grads(grads, dout, dfin, s, B, True, rr, (B, L, D, N, G, dtype, sdtype))
