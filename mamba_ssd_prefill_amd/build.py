@@ -2,7 +2,8 @@
 
     python -m mamba_ssd_prefill_amd.build
 
-Each translation unit is compiled in its own hipcc process (in parallel), then linked.
+Each translation unit is compiled in its own hipcc process (in parallel), then linked.  The library needs no torch; the
+binding's native module _meta.so, host code against torch's headers, is built beside it where torch is installed.
 """
 import hashlib
 import os
@@ -42,16 +43,40 @@ def _meta_command(out):
             + [os.path.join(CSRC, "ssd_meta.cpp"), "-o", out, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"])
 
 
+def _meta_made_from(command):
+    """What _meta.so depends on besides its source: the command (paths, ABI) and the versions whose headers it reads."""
+    import platform
+    import torch
+    return "\n".join(command + ["torch " + torch.__version__, "python " + platform.python_version()])
+
+
+def _build_meta(force):
+    """Compile _meta.so unless it is up to date; with a note where there is no torch to build it for."""
+    src, stamp = os.path.join(CSRC, "ssd_meta.cpp"), os.path.join(BUILD_DIR, "_meta.made_from")
+    try:
+        made_from = _meta_made_from(_meta_command(META))
+    except ImportError as e:
+        print("the C library needs no torch, the binding's module _meta does: not built (%s)" % e, file=sys.stderr)
+        return
+    if not force and os.path.exists(META) and os.path.getmtime(META) >= os.path.getmtime(src) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == made_from:
+                return
+    tmp = META + ".tmp%d" % os.getpid()
+    done = subprocess.run(_meta_command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if done.returncode != 0:
+        raise RuntimeError("%s is built, the binding's module is not:\n== ssd_meta.cpp ==\n%s"
+                           % (os.path.basename(LIB), done.stdout.decode(errors="replace")))
+    os.replace(tmp, META)
+    with open(stamp, "w") as f:
+        f.write(made_from)
+
+
 def build(force=True, verbose=False):
-    """Compile every HIP translation unit and link the shared library; returns its path.  Compiles the _meta module
-    beside it."""
+    """Compile every HIP translation unit and link the shared library; returns its path.  Then compiles the _meta
+    module beside it."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs, procs = [], []
-    meta_src, meta_tmp = os.path.join(CSRC, "ssd_meta.cpp"), META + ".tmp%d" % os.getpid()
-    new_meta = force or not os.path.exists(META) or os.path.getmtime(META) < os.path.getmtime(meta_src)
-    if new_meta:
-        procs.append(("ssd_meta.cpp", subprocess.Popen(_meta_command(meta_tmp), stdout=subprocess.PIPE,
-                                                       stderr=subprocess.STDOUT)))
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src + ".o")
         objs.append(obj)
@@ -81,8 +106,7 @@ def build(force=True, verbose=False):
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     subprocess.run(cmd, check=True, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     os.replace(tmp, LIB)
-    if new_meta:
-        os.replace(meta_tmp, META)
+    _build_meta(force)
     return LIB
 
 
