@@ -24,6 +24,7 @@ of one per batch row.  ``slots`` name each state that a call writes once.
 """
 import collections
 import ctypes
+import numbers
 import struct
 
 from . import SSDError, _dtype_code, load_library
@@ -84,8 +85,9 @@ def declare(lib):
 # ---- helpers -------------------------------------------------------------------------------------
 # A call's checks depend on its arguments' shapes, strides, types and devices alone, so their outcome -- a plan: the
 # parameter block, the output layouts, the workspace size -- is kept under those and found again in a microsecond.
-# Nothing is kept about a tensor's identity, address or contents.
-_PLANS = {}
+# Nothing is kept about a tensor's identity, address or contents.  Plans come in two generations: when the newer one is
+# full the older one goes, and a plan found in the older one moves on, so that those in use stay.
+_PLANS, _BEFORE = {}, {}
 _MAX_PLANS = 512
 
 
@@ -176,11 +178,28 @@ def _layout(shape, dtype, dev):
     return struct.pack("=%dq" % (1 + 2 * len(shape)), head | len(shape) << 32, *shape, *strides[::-1])
 
 
+def _by_value(v):
+    """Whether equal keys mean equal arguments: not so for a tensor, which is told apart by its identity."""
+    import torch
+    if isinstance(v, tuple):
+        return all(_by_value(e) for e in v)
+    return v is None or isinstance(v, (str, bytes, numbers.Integral, torch.dtype))
+
+
 def _keep(key, plan):
-    if len(_PLANS) >= _MAX_PLANS:
-        _PLANS.clear()
+    global _PLANS, _BEFORE
+    if not _by_value(key):
+        return plan
+    if len(_PLANS) >= _MAX_PLANS // 2:
+        _PLANS, _BEFORE = {}, _PLANS
     _PLANS[key] = plan
     return plan
+
+
+def _older(key):
+    """The plan of the older generation, if it is there."""
+    plan = _BEFORE.pop(key, None)
+    return plan and _keep(key, plan)
 
 
 def _p(t):
@@ -340,7 +359,7 @@ def causal_conv(x, weight, bias=None, *, activation="silu", seq_idx=None, nseq=N
     splits = splits if splits is None else tuple(splits)
     meta, (px, pw, pb, ps, ph, pf) = _meta(x, weight, bias, seq_idx, initial_state, final_state)
     key = ("conv", meta, activation, nseq, splits)
-    plan = _PLANS.get(key)
+    plan = _PLANS.get(key) or _older(key)
     if plan is None:
         plan = _keep(key, _conv_plan("ssd_causal_conv", (), x, weight, bias, activation, seq_idx, nseq, splits,
                                      dict(initial_state=initial_state, final_state=final_state)))
@@ -361,7 +380,7 @@ def causal_conv_backward(dout, x, weight, bias=None, *, activation="silu", seq_i
     douts = (dout,) if splits is None else tuple(dout)
     meta, (px, pw, pb, ps, ph, pf, *pd) = _meta(x, weight, bias, seq_idx, initial_state, dfinal_state, *douts)
     key = ("conv backward", meta, activation, nseq, splits)
-    plan = _PLANS.get(key)
+    plan = _PLANS.get(key) or _older(key)
     if plan is None:
         plan = _keep(key, _conv_plan("ssd_causal_conv_backward", ("ssd_causal_conv_backward_workspace_size",), x, weight,
                                      bias, activation, seq_idx, nseq, splits,
@@ -393,7 +412,7 @@ def causal_conv_step(x, weight, bias=None, *, state, activation="silu", slots=No
     splits = splits if splits is None else tuple(splits)
     meta, (px, pw, pb, pst, psl) = _meta(x, weight, bias, state, slots)
     key = ("conv step", meta, activation, splits)
-    plan = _PLANS.get(key)
+    plan = _PLANS.get(key) or _older(key)
     if plan is None:
         plan = _keep(key, _conv_step_plan(x, weight, bias, activation, splits, state, slots))
     outs, ptrs = _outs(plan)
@@ -446,7 +465,7 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
     meta, (px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, pf, po) = _meta(x, dt, A, B, C, D, dt_bias, z, seq_idx, initial_state,
                                                                     final_state, out)
     key = ("scan", meta, dt_softplus, nseq, state_dtype)
-    plan = _PLANS.get(key)
+    plan = _PLANS.get(key) or _older(key)
     if plan is None:
         plan = _keep(key, _scan_plan("ssd_selective_scan", ("ssd_selective_scan_workspace_size",
                                                             "ssd_selective_scan_saved_size"),
@@ -473,7 +492,7 @@ def selective_scan_backward(dout, x, dt, A, B, C, D=None, dt_bias=None, z=None, 
     meta, (pg, px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, pf, psv) = _meta(dout, x, dt, A, B, C, D, dt_bias, z, seq_idx,
                                                                          initial_state, dfinal_state, saved)
     key = ("scan backward", meta, dt_softplus, nseq, state_dtype)
-    plan = _PLANS.get(key)
+    plan = _PLANS.get(key) or _older(key)
     if plan is None:
         plan = _scan_plan("ssd_selective_scan_backward", ("ssd_selective_scan_backward_workspace_size",
                                                           "ssd_selective_scan_saved_size"),
@@ -509,7 +528,7 @@ def selective_scan_step(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, state, 
     [0, nslots) touches no state and returns zeros.  Returns out [B, D]."""
     meta, (px, pdt, pA, pB, pC, pD, pb, pz, pst, psl, po) = _meta(x, dt, A, B, C, D, dt_bias, z, state, slots, out)
     key = ("scan step", meta, dt_softplus)
-    plan = _PLANS.get(key)
+    plan = _PLANS.get(key) or _older(key)
     if plan is None:
         plan = _keep(key, _scan_step_plan(x, dt, A, B, C, D, dt_bias, z, state, slots, dt_softplus, out))
     if out is None:
@@ -560,7 +579,7 @@ def state_cache_write(state, codes, scales, slots=None):
     None: b) of a pool made by state_cache.  Rows whose slot is not in [0, nslots) are skipped."""
     meta, (ps, pc, psc, psl) = _meta(state, codes, scales, slots)
     key = ("cache write", meta)
-    plan = _PLANS.get(key)
+    plan = _PLANS.get(key) or _older(key)
     if plan is None:
         plan = _keep(key, _cache_plan("ssd_state_cache_write", codes, scales, slots, state.shape[0], state.dtype, state))
     plan.call(ps, psl, pc, psc)
@@ -572,7 +591,7 @@ def state_cache_read(codes, scales, slots=None, *, state_dtype=None, out=None):
     import torch
     meta, (pc, psc, psl, po) = _meta(codes, scales, slots, out)
     key = ("cache read", meta, state_dtype)
-    plan = _PLANS.get(key)
+    plan = _PLANS.get(key) or _older(key)
     if plan is None:
         batch = codes.shape[0] if slots is None and out is None else (out if slots is None else slots).shape[0]
         if state_dtype is None:

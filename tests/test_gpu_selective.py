@@ -955,3 +955,18 @@ def test_states_cross_time_splits(want, backward, B, D, N, G, dtype, sdtype):
     rr = ref.runs(B, L)
     check_scan((out, fin), s, B, True, rr, L, N, sdtype, "splits")
     check_grads(grads, dout, dfin, s, B, True, rr, (B, L, D, N, G, dtype, sdtype))
+
+
+def test_arguments_that_change_in_place():
+    """A flag and a count held as tensors: a call reads their values of its own time."""
+    s, seq, S, _ = scan_inputs(1, 20, 64, 16, 1, "f32", "f32", "pad", False, True, True, True, seed=121)
+    args, _ = call_args(s)
+    flag, n = torch.tensor(True), torch.tensor(S)
+    plain = ssd.selective_scan(*args)
+    for value, more in ((True, 0), (False, 2)):
+        flag.fill_(value)
+        n.fill_(S + more)
+        a, b = (ssd.selective_scan(*args, dt_softplus=f, seq_idx=seq.cuda(), nseq=k) for f, k in ((flag, n), (value, S + more)))
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and len(a[1]) == S + more
+    assert torch.isfinite(plain[0]).all()

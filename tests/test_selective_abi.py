@@ -350,3 +350,36 @@ def test_rows_of_a_step_may_lie_far_apart(lib, field):
         assert call(lib, name, params_for(name, **{field: (1 << 24) + 1}), x=None) == MISAL
     for name in ("ssd_selective_scan", "ssd_selective_scan_backward"):
         assert call(lib, name, params_for(name, **{field: 1 << 24}), **{ARGS[name][0].split()[0]: None}) == SHAPE
+
+
+@pytest.fixture
+def plans(monkeypatch):
+    """The binding's store of plans, empty, and as it was afterwards."""
+    for name in ("_PLANS", "_BEFORE"):
+        monkeypatch.setattr(selective, name, {}, raising=False)
+    return lambda key: selective._PLANS.get(key) or selective._older(key)
+
+
+def test_plans_in_use_outlive_new_sizes(plans):
+    """A server's step keeps its plan while prompts of thousands of lengths come by."""
+    step = object()
+    selective._keep(("scan step", b"sizes", True), step)
+    for i in range(5 * selective._MAX_PLANS):
+        selective._keep(("scan", b"%d" % i, None), object())
+        if i % 7 == 0:
+            assert plans(("scan step", b"sizes", True)) is step, i
+    assert len(selective._PLANS) + len(selective._BEFORE) <= selective._MAX_PLANS
+    assert plans(("scan", b"0", None)) is None
+
+
+def test_plans_are_kept_under_values_alone(plans):
+    """An argument that is told apart by its identity (a tensor as a flag or a count) is never looked up again: its value
+    may be another by then."""
+    import numpy as np
+    plan = object()
+    for kept in (("conv", b"", "silu", 3, (4, 5)), ("scan", b"", True, None, torch.float16), ("scan", b"", np.int64(1), None)):
+        assert selective._keep(kept, plan) is plan and plans(kept) is plan
+    for flag in (torch.tensor(True), (2, torch.tensor(3)), [1]):
+        key = ("scan", b"", flag, None, None)
+        assert selective._keep(key, plan) is plan
+        assert not any(k[2] is flag for k in [*selective._PLANS, *selective._BEFORE])
