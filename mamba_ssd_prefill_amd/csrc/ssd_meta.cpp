@@ -7,7 +7,9 @@
 // itself for the eleven of a scan step.
 // new(*layouts) -> tensors: uninitialised tensors, each of a layout that `meta` gives as the key of one tensor.
 // call(function, *arguments) -> status: a function of the library by its address, with pointers and sizes as integers
-// (None: a null pointer), without the interpreter's lock.  ctypes took 0.6 us more for the twelve of a scan step.
+// (None: a null pointer), without the interpreter's lock.  A tensor stands for its address and is taken to be written by the
+// call: its version goes up, so that autograd refuses a backward pass that needs what it held before.  ctypes took 0.6 us
+// more for the twelve of a scan step.
 #include <Python.h>
 #include <ATen/ATen.h>
 #include <torch/csrc/Exceptions.h>
@@ -89,6 +91,7 @@ template <size_t... N> static constexpr std::array<Call, sizeof...(N)> call_tabl
 constexpr auto kCalls = call_table(std::make_index_sequence<kMaxArgs + 1>());
 
 static PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
     uintptr_t v[kMaxArgs + 1];
     if (n < 1 || n > (Py_ssize_t)kMaxArgs + 1) {
         PyErr_SetString(PyExc_TypeError, "expected a function and up to 32 arguments");
@@ -97,6 +100,12 @@ static PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     for (Py_ssize_t i = 0; i < n; ++i) {
         v[i] = 0;
         if (i && args[i] == Py_None) continue;
+        if (i && !PyLong_CheckExact(args[i]) && THPVariable_Check(args[i])) {
+            const at::Tensor& t = THPVariable_Unpack(args[i]);
+            v[i] = (uintptr_t)t.data_ptr();
+            if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+            continue;
+        }
         const unsigned long long u = PyLong_AsUnsignedLongLong(args[i]);
         if (u == (unsigned long long)-1 && PyErr_Occurred()) return nullptr;
         v[i] = (uintptr_t)u;
@@ -110,6 +119,7 @@ static PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     rc = kCalls[(size_t)n - 1]((void*)v[0], v + 1);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
+    END_HANDLE_TH_ERRORS
 }
 
 static PyMethodDef methods[] = {

@@ -111,7 +111,8 @@ class _Plan:
         self.spaces = [_layout((n,), torch.uint8, dev) for n in self.sizes]
 
     def call(self, *args):
-        """One C call on the current stream of the tensors' device, with that device current."""
+        """One C call on the current stream of the tensors' device, with that device current.  Tensors that it writes come
+        as they are, others as their addresses."""
         if _raw is None:
             _bind()
         if self.index == _device():
@@ -200,10 +201,6 @@ def _older(key):
     """The plan of the older generation, if it is there."""
     plan = _BEFORE.pop(key, None)
     return plan and _keep(key, plan)
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
 
 
 def _code(t, name):
@@ -324,10 +321,6 @@ def _conv_params(x, weight, bias, activation, splits, nseq, lead):
     return prm, dev, parts
 
 
-def _three(ts):
-    return [_p(t) for t in ts] + [None] * (3 - len(ts))
-
-
 def _conv_plan(name, spaces, x, weight, bias, activation, seq_idx, nseq, splits, states, douts=()):
     lead = tuple(x.shape[:2])
     S = _seq(seq_idx, nseq, lead, x.device)
@@ -345,9 +338,9 @@ def _conv_plan(name, spaces, x, weight, bias, activation, seq_idx, nseq, splits,
 
 
 def _outs(plan):
-    """New outputs, one per split, and the three pointers the library takes."""
+    """New outputs, one per split, and the three that the library takes."""
     outs = _new(*plan.parts)
-    return outs, _three(outs)
+    return outs, (*outs, None, None)[:3]
 
 
 def causal_conv(x, weight, bias=None, *, activation="silu", seq_idx=None, nseq=None, initial_state=None, splits=None,
@@ -357,17 +350,16 @@ def causal_conv(x, weight, bias=None, *, activation="silu", seq_idx=None, nseq=N
     ``splits`` (up to three channel counts) makes ``out`` a tuple of contiguous tensors, e.g. the x, B and C
     of an SSD block.  States [B or nseq, Ch, W-1] hold the inputs before (after) a sequence, oldest first."""
     splits = splits if splits is None else tuple(splits)
-    meta, (px, pw, pb, ps, ph, pf) = _meta(x, weight, bias, seq_idx, initial_state, final_state)
+    meta, (px, pw, pb, ps, ph, _) = _meta(x, weight, bias, seq_idx, initial_state, final_state)
     key = ("conv", meta, activation, nseq, splits)
     plan = _PLANS.get(key) or _older(key)
     if plan is None:
         plan = _keep(key, _conv_plan("ssd_causal_conv", (), x, weight, bias, activation, seq_idx, nseq, splits,
                                      dict(initial_state=initial_state, final_state=final_state)))
-    outs, ptrs = _outs(plan)
+    outs, three = _outs(plan)
     if final_state is None and with_final_state:
         final_state = _states(seq_idx is not None, plan.state)
-        pf = final_state.data_ptr()
-    plan.call(px, pw, pb, ps, ph, *ptrs, pf)
+    plan.call(px, pw, pb, ps, ph, *three, final_state)
     return (outs[0] if splits is None else outs), final_state
 
 
@@ -389,8 +381,7 @@ def causal_conv_backward(dout, x, weight, bias=None, *, activation="silu", seq_i
     db = db[0] if db else None
     dh = None if initial_state is None else _states(seq_idx is not None, plan.state)
     workspace = space if workspace is None else _space(workspace, plan.dev)
-    plan.call(*pd, *[None] * (3 - len(pd)), pf, px, pw, pb, ps, ph, dx.data_ptr(), dw.data_ptr(), _p(db), _p(dh),
-              workspace.data_ptr(), workspace.numel())
+    plan.call(*pd, *[None] * (3 - len(pd)), pf, px, pw, pb, ps, ph, dx, dw, db, dh, workspace, workspace.numel())
     return ConvGrads(dx, dw, db, dh)
 
 
@@ -410,13 +401,13 @@ def causal_conv_step(x, weight, bias=None, *, state, activation="silu", slots=No
     uses state ``slots[b]`` (int32; None: state b).  A row whose slot is not in [0, nslots) touches no
     state and returns zeros.  Returns out (a tuple with ``splits``)."""
     splits = splits if splits is None else tuple(splits)
-    meta, (px, pw, pb, pst, psl) = _meta(x, weight, bias, state, slots)
+    meta, (px, pw, pb, _, psl) = _meta(x, weight, bias, state, slots)
     key = ("conv step", meta, activation, splits)
     plan = _PLANS.get(key) or _older(key)
     if plan is None:
         plan = _keep(key, _conv_step_plan(x, weight, bias, activation, splits, state, slots))
-    outs, ptrs = _outs(plan)
-    plan.call(px, pw, pb, pst, psl, *ptrs)
+    outs, three = _outs(plan)
+    plan.call(px, pw, pb, state, psl, *three)
     return outs[0] if splits is None else outs
 
 
@@ -462,8 +453,8 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
     float32; the rows of B and C start on multiples of 4 bytes.  Returns (out [B, L, D], final_state
     [B or nseq, D, N]), and with ``save_for_backward`` a third tensor for selective_scan_backward.
     ``state_dtype`` defaults to initial_state's, else float32."""
-    meta, (px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, pf, po) = _meta(x, dt, A, B, C, D, dt_bias, z, seq_idx, initial_state,
-                                                                    final_state, out)
+    meta, (px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, _, _) = _meta(x, dt, A, B, C, D, dt_bias, z, seq_idx, initial_state,
+                                                                  final_state, out)
     key = ("scan", meta, dt_softplus, nseq, state_dtype)
     plan = _PLANS.get(key) or _older(key)
     if plan is None:
@@ -473,13 +464,11 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
                                      dict(initial_state=initial_state, final_state=final_state), dict(out=out)))
     if out is None:
         out, = _new(plan.out)
-        po = out.data_ptr()
     if final_state is None and with_final_state:
         final_state = _states(seq_idx is not None, plan.state)
-        pf = final_state.data_ptr()
     workspace = _new(plan.spaces[0])[0] if workspace is None else _space(workspace, plan.dev)
     saved = _new(plan.spaces[1])[0] if save_for_backward else None
-    plan.call(px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, po, pf, _p(saved), workspace.data_ptr(), workspace.numel())
+    plan.call(px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, out, final_state, saved, workspace, workspace.numel())
     return (out, final_state, saved) if save_for_backward else (out, final_state)
 
 
@@ -504,9 +493,7 @@ def selective_scan_backward(dout, x, dt, A, B, C, D=None, dt_bias=None, z=None, 
     g = ScanGrads(*[None if n is None else next(made) for n in plan.new],
                   None if initial_state is None else _states(seq_idx is not None, plan.state))
     workspace = _new(plan.spaces[0])[0] if workspace is None else _space(workspace, plan.dev)
-    plan.call(pg, pf, px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, psv, g.dx.data_ptr(), g.ddt.data_ptr(), g.dA.data_ptr(),
-              g.dB.data_ptr(), g.dC.data_ptr(), _p(g.dD), _p(g.ddt_bias), _p(g.dz), _p(g.dinitial_state),
-              workspace.data_ptr(), workspace.numel())
+    plan.call(pg, pf, px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, psv, *g, workspace, workspace.numel())
     return g
 
 
@@ -526,15 +513,14 @@ def selective_scan_step(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, state, 
     """ssd_selective_scan_step: one token per row; x, dt, z [B, D], B, C [B, G, N].  ``state`` [nslots, D, N] is
     updated in place; row b uses state ``slots[b]`` (int32; None: state b).  A row whose slot is not in
     [0, nslots) touches no state and returns zeros.  Returns out [B, D]."""
-    meta, (px, pdt, pA, pB, pC, pD, pb, pz, pst, psl, po) = _meta(x, dt, A, B, C, D, dt_bias, z, state, slots, out)
+    meta, (px, pdt, pA, pB, pC, pD, pb, pz, _, psl, _) = _meta(x, dt, A, B, C, D, dt_bias, z, state, slots, out)
     key = ("scan step", meta, dt_softplus)
     plan = _PLANS.get(key) or _older(key)
     if plan is None:
         plan = _keep(key, _scan_step_plan(x, dt, A, B, C, D, dt_bias, z, state, slots, dt_softplus, out))
     if out is None:
         out, = _new(plan.out)
-        po = out.data_ptr()
-    plan.call(px, pdt, pA, pB, pC, pD, pb, pz, pst, psl, po)
+    plan.call(px, pdt, pA, pB, pC, pD, pb, pz, state, psl, out)
     return out
 
 
@@ -577,19 +563,19 @@ def _cache_plan(name, codes, scales, slots, batch, state_dtype, state):
 def state_cache_write(state, codes, scales, slots=None):
     """ssd_state_cache_write: state [B, ...] (float32, float16 or bfloat16) into the slots ``slots[b]`` (int32;
     None: b) of a pool made by state_cache.  Rows whose slot is not in [0, nslots) are skipped."""
-    meta, (ps, pc, psc, psl) = _meta(state, codes, scales, slots)
+    meta, (ps, _, _, psl) = _meta(state, codes, scales, slots)
     key = ("cache write", meta)
     plan = _PLANS.get(key) or _older(key)
     if plan is None:
         plan = _keep(key, _cache_plan("ssd_state_cache_write", codes, scales, slots, state.shape[0], state.dtype, state))
-    plan.call(ps, psl, pc, psc)
+    plan.call(ps, psl, codes, scales)
 
 
 def state_cache_read(codes, scales, slots=None, *, state_dtype=None, out=None):
     """ssd_state_cache_read: the states of ``slots`` (int32 [B]; None: every slot), in ``state_dtype`` (default
     float32) or into ``out`` [B, ...].  A row whose slot is not in [0, nslots) reads a zero state."""
     import torch
-    meta, (pc, psc, psl, po) = _meta(codes, scales, slots, out)
+    meta, (pc, psc, psl, _) = _meta(codes, scales, slots, out)
     key = ("cache read", meta, state_dtype)
     plan = _PLANS.get(key) or _older(key)
     if plan is None:
@@ -599,6 +585,5 @@ def state_cache_read(codes, scales, slots=None, *, state_dtype=None, out=None):
         plan = _keep(key, _cache_plan("ssd_state_cache_read", codes, scales, slots, batch, state_dtype, out))
     if out is None:
         out, = _new(plan.out)
-        po = out.data_ptr()
-    plan.call(pc, psc, psl, po)
+    plan.call(pc, psc, psl, out)
     return out

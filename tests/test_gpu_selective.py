@@ -970,3 +970,38 @@ def test_arguments_that_change_in_place():
         torch.cuda.synchronize()
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and len(a[1]) == S + more
     assert torch.isfinite(plain[0]).all()
+
+
+def test_autograd_sees_what_is_written_in_place():
+    """A state that torch's autograd holds for a backward pass and that a step then moves on: the backward refuses, as
+    after a write by torch, and so for every tensor that a call writes into."""
+    B, D, N = 2, 64, 16
+    s, _, _, _ = scan_inputs(B, 1, D, N, 1, "f32", "f32", None, True, True, True, True, seed=131)
+    (x, dt, A, Bm, C, Dp, bias, z), h0 = call_args(s)
+    token = (x[:, 0], dt[:, 0], A, Bm[:, 0], C[:, 0], Dp, bias, z[:, 0])
+    w = torch.ones(D, 4, device="cuda")
+    new = lambda *shape: torch.zeros(*shape, device="cuda")  # noqa: E731
+    codes, scales = ssd.state_cache(B, (D, N), group=16)
+    state, conv, out, tok, fin, cfin, back = h0.clone(), new(B, D, 3), new(B, 1, D), new(B, D), new(B, D, N), new(B, D, 3), new(B, D, N)
+
+    def calls():
+        ssd.selective_scan_step(*token, state=state, out=tok)
+        ssd.causal_conv_step(x[:, 0], w, state=conv)
+        ssd.selective_scan(x, dt, A, Bm, C, Dp, bias, z, out=out, final_state=fin)
+        ssd.causal_conv(x, w, final_state=cfin)
+        ssd.state_cache_write(fin, codes, scales)
+        ssd.state_cache_read(codes, scales, out=back)
+    written = [state, conv, out, tok, fin, cfin, codes, scales, back]
+    read = [x, dt, A, Bm, C, Dp, bias, z, w]
+    before = [t._version for t in written], [t._version for t in read]
+    calls()
+    assert all(t._version > v for t, v in zip(written, before[0])) and [t._version for t in read] == before[1]
+    p = torch.ones(B, D, N, device="cuda", requires_grad=True)
+    loss = (p * state).sum()
+    ssd.selective_scan_step(*token, state=state)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    with torch.inference_mode():
+        state, out, tok, fin = state.clone(), new(B, 1, D), new(B, D), new(B, D, N)
+        calls()
+    torch.cuda.synchronize()

@@ -383,3 +383,23 @@ def test_plans_are_kept_under_values_alone(plans):
         key = ("scan", b"", flag, None, None)
         assert selective._keep(key, plan) is plan
         assert not any(k[2] is flag for k in [*selective._PLANS, *selective._BEFORE])
+
+
+def test_library_calls_raise_the_versions_of_written_tensors():
+    """A tensor among a call's arguments stands for its address and is taken to be written: its version goes up, as with
+    torch's own writes in place (a view's base's too; tensors of the inference mode have none)."""
+    from mamba_ssd_prefill_amd._meta import call
+    seen = []
+    f = ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_size_t] * 4)(lambda *a: seen.append(a) or 0)
+    where = ctypes.cast(f, ctypes.c_void_p).value
+    base = torch.zeros(4, 6)
+    with torch.inference_mode():
+        inf = torch.zeros(3)
+    other = torch.zeros(2)
+    assert call(where, base[1:], other.data_ptr(), None, inf) == 0
+    assert seen == [(base.data_ptr() + 24, other.data_ptr(), 0, inf.data_ptr())]
+    assert base._version == 1 and other._version == 0
+    with pytest.raises(TypeError):
+        call(base, 1)
+    with pytest.raises((RuntimeError, ValueError, NotImplementedError)):
+        call(where, base.to_sparse(), 0, 0, 0)
