@@ -515,7 +515,8 @@ typedef struct {
 } ssd_scan_params_t;
 
 /*   x, dt         [B, L, D]     in_dtype    required, rows
- *   A             [D, N]        fp32        required, 16-byte aligned; A <= 0 is a precondition (not checked);
+ *   A             [D, N]        fp32        required, 16-byte aligned; A <= 0 is a precondition (not checked; -inf
+ *                                           forgets the state at every step above 0);
  *                                           steps may be negative (dt_softplus = 0) while the products of the
  *                                           decays over a run of tokens stay in the fp32 range
  *   B, C          [B, L, G, N]  in_dtype    required, rows, 4-byte aligned

@@ -54,7 +54,7 @@ __global__ __launch_bounds__(NW * 64) void k_scan(ScanArgs a) {
     float A2[NS], h[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        A2[i] = a.A[(int64_t)p.c * N + n0 + i] * kLog2e;
+        A2[i] = decay_rate(a.A[(int64_t)p.c * N + n0 + i]);
         h[i] = 0.f;
     }
     const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f, Dc = a.D ? a.D[p.c] : 0.f;
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(NW * 64) void k_scan_carry(ScanArgs a) {
     float A2[NS], h[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        A2[i] = a.A[(int64_t)p.c * N + n0 + i] * kLog2e;
+        A2[i] = decay_rate(a.A[(int64_t)p.c * N + n0 + i]);
         h[i] = 0.f;
     }
     const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(256) void k_scan_join(ScanArgs a) {
     const int b = (int)(i / per);
     const int64_t cn = i % per;
     const int c = (int)(cn / a.dstate);
-    const float A2 = a.A[cn] * kLog2e;
+    const float A2 = decay_rate(a.A[cn]);
     float h = 0.f;
     if (!a.seq && a.h0) {
         const int64_t o = b * per + cn;
@@ -287,7 +287,7 @@ template <typename T, typename S, int N, int R> __global__ __launch_bounds__(256
         float y = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            h[r][j] = __builtin_amdgcn_exp2f(d * (A[j] * kLog2e)) * h[r][j] + u * B[r][j];
+            h[r][j] = __builtin_amdgcn_exp2f(d * decay_rate(A[j])) * h[r][j] + u * B[r][j];
             y += h[r][j] * C[r][j];
         }
         if (have[r]) store_states<4>(a.pool, SD, at[r], h[r]);

@@ -107,7 +107,7 @@ __global__ __launch_bounds__(NW * 64, NS == 4 ? 3 : 2) void k_scan_backward(Scan
     float A2[NS], g[NS], dA[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        A2[i] = a.A[(int64_t)p.c * N + n0 + i] * kLog2e;
+        A2[i] = decay_rate(a.A[(int64_t)p.c * N + n0 + i]);
         g[i] = dA[i] = 0.f;
     }
     const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f, Dc = a.D ? a.D[p.c] : 0.f;
@@ -366,7 +366,7 @@ __global__ __launch_bounds__(NW * 64) void k_scan_backward_carry(ScanArgs a) {
     float A2[NS], g[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        A2[i] = a.A[(int64_t)p.c * N + n0 + i] * kLog2e;
+        A2[i] = decay_rate(a.A[(int64_t)p.c * N + n0 + i]);
         g[i] = 0.f;
     }
     const float bias = a.dt_bias ? a.dt_bias[p.c] : 0.f;
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(256) void k_scan_backward_join(ScanArgs a) {
     float* st = a.split_state + (int64_t)b * a.nsplit * per + cn;
     const float* sum = a.split_sum + (int64_t)b * a.nsplit * a.channels + c;
     // the last split's own pass began with the final state's gradient
-    join_splits(a.A[cn] * kLog2e, st[(a.nsplit - 2) * per], a.nsplit - 2,
+    join_splits(decay_rate(a.A[cn]), st[(a.nsplit - 2) * per], a.nsplit - 2,
                 [&](int k) { return sum[(int64_t)(a.nsplit - 2 - k) * a.channels]; },
                 [&](int k) { return st + (a.nsplit - 3 - k) * per; });
 }

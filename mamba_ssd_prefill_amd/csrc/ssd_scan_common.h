@@ -14,6 +14,13 @@ namespace ssd {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// A log2(e), the decay's exponent for a step of 1, kept finite: no step (a token behind the end, padding) times an infinite A
+// would be NaN, where the state has to stay as it is.  (A NaN stays one.)
+__device__ inline float decay_rate(float A) {
+    const float r = A * kLog2e;
+    return r < -__FLT_MAX__ ? -__FLT_MAX__ : r;
+}
+
 // The rows of B (or C) of a tile for one wave, NS values each, read through the scalar cache (the data is written
 // before the launch) a group of GROUP tokens at a time, so that a group can be on its way while the one
 // before is used.  One base address a tile and 32-bit offsets: scalar instructions issue at the rate of vector

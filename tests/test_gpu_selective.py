@@ -1005,3 +1005,23 @@ def test_autograd_sees_what_is_written_in_place():
         state, out, tok, fin = state.clone(), new(B, 1, D), new(B, D), new(B, D, N)
         calls()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("L,pack", [(21, None), (21, "pad"), (131, None), (700, "full")])
+def test_infinite_decays(L, pack):
+    """A of -inf (and one whose product with log2(e) overflows) forgets the state at every step: outputs, states and gradients
+    are those of the limit, which the 64-bit loops reach with A = -1e30, also in rows that end inside a tile."""
+    B, D, N = 2, 66, 16
+    s, seq, S, g = scan_inputs(B, L, D, N, 1, "f32", "f32", pack, True, True, True, True, seed=141)
+    far = dict(s, A=s["A"].clone())
+    for t, v in ((s["A"], -1e30), (far["A"], float("-inf"))):
+        t[3, 5], t[65], t[7, 2] = v, v, -3.4e38
+    args, h0 = call_args(far)
+    kw = dict(seq_idx=cuda(seq), nseq=S if pack else None, initial_state=h0)
+    out, fin, saved = ssd.selective_scan(*args, save_for_backward=True, **kw)
+    dout, dfin = torch.randn(B, L, D, generator=g), torch.randn(S, D, N, generator=g)
+    grads = ssd.selective_scan_backward(dout.cuda(), *args, saved=saved, dfinal_state=dfin.cuda(), **kw)
+    torch.cuda.synchronize()
+    rr = ref.runs(B, L, seq)
+    check_scan((out, fin), s, S, True, rr, min(L, 400), N, "f32", "infinite decays")
+    check_grads(grads, used(dout, seq, S), dfin, s, S, True, rr, (B, L, D, N, 1, "f32", "f32"))
