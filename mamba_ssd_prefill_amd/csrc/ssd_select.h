@@ -22,7 +22,7 @@ struct CausalConvArgs {
     const void* dout[3];
     const void* dfin;
     void* dx;
-    float* part;  // [batch * nseg][channels][width + 1]: sums of dw and dbias over a segment
+    float* part;  // [ceil(batch * nseg / 4)][width + 1][channels]: sums of dw, then dbias, over four segments
     void* dh0;
     // step
     void* pool;

@@ -1,8 +1,9 @@
 """The selective state space scan, its short causal convolution and the 8-bit state cache.
 
-A thin ctypes binding over the second half of include/mamba_ssd.h, in the manner of the package's
-other entry points: it checks arguments, allocates outputs and workspaces, and passes pointers and
-the current stream of the tensors' device.  The names are re-exported by the package:
+A binding over the second half of include/mamba_ssd.h, in the manner of the package's other entry
+points: it checks arguments, allocates outputs and workspaces, and passes pointers and the current
+stream of the tensors' device.  The calls themselves go through a small compiled module (_meta, built
+beside the library against torch's headers).  The names are re-exported by the package:
 
     xc, conv_state = causal_conv(x, conv_w, conv_b)                      # prompt
     out, state = selective_scan(xc, dt, A, B, C, D, dt_bias, z)
@@ -21,6 +22,14 @@ such as the halves of a joint projection; everything else is contiguous.  Sequen
 batch row are told apart by ``seq_idx`` (int32 [B, L], numbers in [0, nseq), each for one run of tokens;
 -1: padding, which gets and adds zero gradients), and states then have one entry per number instead
 of one per batch row.  ``slots`` name each state that a call writes once.
+
+These calls are outside torch's autograd: what they return carries no graph, whether or not the inputs require
+gradients; gradients come from the _backward calls (wrap a pair in a torch.autograd.Function to train through
+them).  Tensors that a call writes in place (states, ``out``, ``final_state``, codes and scales) raise their version
+counters as torch's own writes do.
+
+Training keeps ``saved``: a state in fp32 every 8 tokens, 4 * B * ceil(L / 8) * D * N bytes.  That is N / 4
+times a 16-bit x: 4 times at N = 16, 671 MB for one layer at 2 x 8192 x 5120.
 """
 import collections
 import ctypes
@@ -451,7 +460,8 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, z=None, *, dt_softplus=
                    final_state=None, out=None, workspace=None):
     """ssd_selective_scan over a prompt: x, dt, z [B, L, D], A [D, N] float32, B, C [B, L, G, N], D and dt_bias [D]
     float32; the rows of B and C start on multiples of 4 bytes.  Returns (out [B, L, D], final_state
-    [B or nseq, D, N]), and with ``save_for_backward`` a third tensor for selective_scan_backward.
+    [B or nseq, D, N]), and with ``save_for_backward`` a third tensor for selective_scan_backward, N / 4 times as large as a
+    16-bit x.
     ``state_dtype`` defaults to initial_state's, else float32."""
     meta, (px, pdt, pA, pB, pC, pD, pb, pz, ps, ph, _, _) = _meta(x, dt, A, B, C, D, dt_bias, z, seq_idx, initial_state,
                                                                   final_state, out)
