@@ -27,6 +27,12 @@ ssd_status_t hip_status(hipError_t e) {
     return e == hipErrorNotSupported ? SSD_ERR_UNSUPPORTED : SSD_ERR_HIP;
 }
 
+// Whether two arrays of states, `bytes` each, have bytes in common (NULL: not given).
+bool overlap(const void* a, const void* b, size_t bytes) {
+    const uintptr_t u = (uintptr_t)a, v = (uintptr_t)b;
+    return a && b && (u < v ? v - u : u - v) < bytes;
+}
+
 // A row stride field: 0 (contiguous) or at least the row's length.
 bool stride_ok(int64_t s, int64_t row) { return s == 0 || (s >= row && s < kMaxIndex); }
 
@@ -109,7 +115,8 @@ SSD_EXPORT ssd_status_t ssd_causal_conv(const ssd_conv_params_t* p, const void* 
     if (!aligned(x, es) || !aligned(w, 4) || !aligned(bias, 4) || !aligned(seq_idx, 4) ||
         !aligned(initial_state, es) || !aligned(final_state, es))
         return SSD_ERR_MISALIGNED;
-    if (initial_state && initial_state == final_state) return SSD_ERR_INVALID_ARGUMENT;
+    const int64_t states = seq_idx ? p->nseq : p->batch;
+    if (overlap(initial_state, final_state, states * p->channels * (p->width - 1) * es)) return SSD_ERR_INVALID_ARGUMENT;
     ssd::CausalConvArgs a = conv_args(p, x, w, bias);
     a.seq = seq_idx;
     a.h0 = initial_state;
@@ -328,7 +335,9 @@ SSD_EXPORT ssd_status_t ssd_selective_scan(const ssd_scan_params_t* p, const voi
     if (!aligned(out, elem_size(p->in_dtype)) || !aligned(seq_idx, 4) || !aligned(initial_state, 16) ||
         !aligned(final_state, 16) || !aligned(saved, 16) || !aligned(workspace, kAlign))
         return SSD_ERR_MISALIGNED;
-    if (initial_state && initial_state == final_state) return SSD_ERR_INVALID_ARGUMENT;
+    const int64_t states = seq_idx ? p->nseq : p->batch;
+    if (overlap(initial_state, final_state, states * p->channels * p->dstate * elem_size(p->state_dtype)))
+        return SSD_ERR_INVALID_ARGUMENT;
     const ScanLayout l = scan_layout(p, false);
     if (workspace_bytes < l.total) return SSD_ERR_WORKSPACE_TOO_SMALL;
     ssd::ScanArgs a = scan_args(p, x, dt, A, B, C, D, dt_bias, z);

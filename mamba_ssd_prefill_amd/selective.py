@@ -18,7 +18,8 @@ beside the library against torch's headers).  The names are re-exported by the p
     state = state_cache_read(codes, scales, slots)
 
 Inputs with one row per token (x, dt, z, B, C) may be views whose rows lie a constant distance apart,
-such as the halves of a joint projection; everything else is contiguous.  Sequences packed into a
+such as the halves of a joint projection; everything else is contiguous.  Outputs that are handed in
+(``out``, ``final_state``) overlap no input.  Sequences packed into a
 batch row are told apart by ``seq_idx`` (int32 [B, L], numbers in [0, nseq), each for one run of tokens;
 -1: padding, which gets and adds zero gradients), and states then have one entry per number instead
 of one per batch row.  ``slots`` name each state that a call writes once.

@@ -403,3 +403,17 @@ def test_library_calls_raise_the_versions_of_written_tensors():
         call(base, 1)
     with pytest.raises((RuntimeError, ValueError, NotImplementedError)):
         call(where, base.to_sparse(), 0, 0, 0)
+
+
+def test_states_that_overlap_are_refused_for_prompts(lib):
+    """A final state that lies partly over the initial one (shifted views of one pool): other workgroups still read that."""
+    for name, size in (("ssd_causal_conv", 64 * 3 * 2), ("ssd_selective_scan", 64 * 16 * 4)):
+        for S, kw, seq in ((2, {}, None), (5, dict(nseq=5), FAKE * 64)):
+            prm = params_for(name, **kw)
+            for d in (16, size, S * size - 16):
+                for h0, fin in ((FAKE, FAKE + d), (FAKE + d, FAKE)):
+                    assert call(lib, name, prm, seq=seq, h0=h0, fin=fin) == BADARG, (name, S, d)
+        n = S * size  # next to each other: on to the next check
+        if name == "ssd_selective_scan":
+            assert call(lib, name, prm, seq=seq, h0=FAKE, fin=FAKE + n, ws_bytes=0) == WS_SMALL
+            assert call(lib, name, prm, seq=seq, h0=FAKE + n, fin=FAKE, ws_bytes=0) == WS_SMALL
