@@ -591,6 +591,161 @@ ssd_status_t ssd_state_cache_write(const ssd_cache_params_t* p, const void* stat
 ssd_status_t ssd_state_cache_read(const ssd_cache_params_t* p, const void* codes, const float* scales,
                                   const int32_t* slots, void* state, void* stream);
 
+/* ====================================================================================
+ * What stands around a mixer in a layer, and a second mixer: the root-mean-square norm with
+ * the residual's addition, the matrix product with its epilogue, and the gated linear
+ * recurrence.  The conventions above hold (rows with a *_stride, host-only checks, fixed orders
+ * of summation, outputs that overlap no input but where it is said).
+ * ==================================================================================== */
+
+/* ---- residual norm ----------------------------------------------------------------------
+ * For every row:  s = x + residual (or x),  r = 1 / sqrt(mean(s^2) + eps),  y = s * r * w,
+ * in fp32 (squares of a row have to stay in its range: |s| below 1.8e19 / sqrt(D)); sum is s
+ * rounded to sum_dtype, and y is that of s before this rounding.
+ * In 8 bits (format): the row has one scale, y becomes codes as in the state cache above:
+ *     scale = max|y| / 127 (int8) or / 448 (e4m3),  code = y / scale rounded to the nearest code, ties to even
+ * A row that holds an infinity or a NaN gets a NaN scale, one whose scale would be below 2^-80 scale 0; both
+ * have codes 0. */
+typedef struct {
+    size_t struct_size; /* sizeof(ssd_norm_params_t) */
+    int64_t rows;       /* M >= 1, below 2^31 */
+    int width;          /* D in [1, 16384] */
+    int in_dtype;       /* ssd_dtype_t of x, out, dout, dx */
+    int sum_dtype;      /* ssd_dtype_t of residual, sum, dsum, dresidual: in_dtype or SSD_F32 */
+    int format;         /* -1: out holds values; else ssd_cache_format_t (not in the backward) */
+    float eps;          /* >= 0 and finite (with 0 a row of zeros is 0 / 0) */
+    int64_t x_stride;   /* elements between rows of x (the backward: of s), below 2^31; 0: D */
+    int64_t residual_stride;
+} ssd_norm_params_t;
+
+/*   x        [M, D]  in_dtype   required, rows
+ *   w        [D]     fp32       required
+ *   residual [M, D]  sum_dtype  rows; NULL: none
+ *   out      [M, D]  in_dtype, or bytes (codes)  required
+ *   scales   [M]     fp32       with format >= 0: required; else NULL
+ *   sum      [M, D]  sum_dtype  with a residual: required; else NULL.  May be the residual itself (the addition
+ *                               in place, residual_stride 0 or D); no other overlap.
+ * Every pointer has its element's alignment. */
+ssd_status_t ssd_rms_norm(const ssd_norm_params_t* p, const void* x, const float* w, const void* residual, void* out,
+                          float* scales, void* sum, void* stream);
+
+/* The gradients at s, the sum that the forward pass returned (without a residual: x, sum_dtype = in_dtype),
+ * from dout [M, D] in_dtype and dsum [M, D] sum_dtype, the gradient of the sum itself (NULL means 0), contiguous:
+ *     n = s r,  g = dout w,  ds = r (g - n mean(g n)) + dsum,  dw = sum over rows of dout n
+ *   s         [M, D]  sum_dtype  required, rows (x_stride)
+ *   dx        [M, D]  in_dtype   ds; NULL: not wanted
+ *   dresidual [M, D]  sum_dtype  ds; NULL: not wanted (one of the two is required).  May be dsum itself.
+ *   dw        [D]     fp32       NULL: not wanted
+ *   workspace         256-byte aligned, ssd_rms_norm_backward_workspace_size() bytes */
+size_t ssd_rms_norm_backward_workspace_size(const ssd_norm_params_t* p);
+ssd_status_t ssd_rms_norm_backward(const ssd_norm_params_t* p, const void* dout, const void* s, const float* w,
+                                   const void* dsum, void* dx, void* dresidual, float* dw, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* ---- matrix product ---------------------------------------------------------------------
+ *     pre[m,n] = (sum_k x[m,k] * weight[n,k]) * x_scale[m] * weight_scale[n] + bias[n]
+ *     out[m,n] = act(pre[m,n]) + residual[m,n],   act: identity, v sigmoid(v), or v (1 + erf(v / sqrt 2)) / 2
+ * Sums in fp32 (int8: exactly, in 32-bit integers, up to K = 131071), everything behind them in fp32 too, rounded once. */
+typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GELU = 2 } ssd_act_t;
+typedef enum { SSD_IN_INT8 = 3, SSD_IN_E4M3 = 4 } ssd_code_dtype_t; /* operands in 8 bits, besides ssd_dtype_t */
+
+typedef struct {
+    size_t struct_size; /* sizeof(ssd_linear_params_t) */
+    int rows;           /* M >= 1 */
+    int width;          /* K >= 1; a row of 16-byte pieces has to stay below 4 MiB */
+    int outs;           /* N >= 1 */
+    int in_dtype;       /* of x and weight: ssd_dtype_t or ssd_code_dtype_t */
+    int out_dtype;      /* ssd_dtype_t of out, residual and pre (the backward: in_dtype) */
+    int act;            /* ssd_act_t */
+    int64_t x_stride;   /* elements between rows of x, below 2^31; 0: K */
+    int64_t residual_stride;
+} ssd_linear_params_t;
+
+/*   x            [M, K]  in_dtype   required, rows
+ *   weight       [N, K]  in_dtype   required, 16-byte aligned
+ *   bias         [N]     fp32       NULL means 0
+ *   residual     [M, N]  out_dtype  rows; NULL: none
+ *   x_scale      [M]     fp32       NULL means 1; only with operands in 8 bits
+ *   weight_scale [N]     fp32       likewise
+ *   pre          [M, N]  out_dtype  NULL: not wanted (kept for the backward pass of an activation)
+ *   out          [M, N]  out_dtype  required, contiguous
+ *   workspace            256-byte aligned, ssd_linear_workspace_size() bytes
+ * x is 16-byte aligned where it is contiguous with rows of a multiple of 16 bytes; else it has its element's
+ * alignment.  (Rows that are no multiple of 16 bytes, or do not start on one, are copied to the workspace first.) */
+size_t ssd_linear_workspace_size(const ssd_linear_params_t* p);
+ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, const void* weight, const float* bias,
+                        const void* residual, const float* x_scale, const float* weight_scale, void* pre, void* out,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradients from dout [M, N] (contiguous, 16-byte aligned) and, with an activation, the `pre` that the forward pass
+ * kept.  The residual's gradient is dout.  in_dtype fp32, fp16 or bf16.
+ *     dpre = dout act'(pre),  dx = dpre weight,  dweight = dpre^T x,  dbias = sum over rows of dpre
+ * dpre is rounded to in_dtype for the two products (a matrix instruction takes no wider operand), not for dbias.
+ *   dx      [M, K]  in_dtype  NULL: not wanted
+ *   dweight [N, K]  in_dtype  NULL: not wanted
+ *   dbias   [N]     fp32      NULL: not wanted (one of the three is required) */
+size_t ssd_linear_backward_workspace_size(const ssd_linear_params_t* p);
+ssd_status_t ssd_linear_backward(const ssd_linear_params_t* p, const void* dout, const void* x, const void* weight,
+                                 const void* pre, void* dx, void* dweight, float* dbias, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* ---- gated linear recurrence -----------------------------------------------------------------
+ * One decay and one input gate per (token, channel).  For every batch row b and channel c, over t = 0 .. L-1:
+ *     r = sigmoid(gate[b,t,c] + gate_bias[c]),  i = sigmoid(in_gate[b,t,c] + in_bias[c])  (1 without in_gate)
+ *     a = exp(A[c] * r),  beta = sqrt(1 - a^2)  (normalize = 1; else 1)
+ *     h = a * h + beta * i * x[b,t,c],   out[b,t,c] = h
+ * Sequences, states, padding and the pool of the single-token form are those of the selective scan above. */
+typedef struct {
+    size_t struct_size; /* sizeof(ssd_recurrence_params_t) */
+    int batch;          /* B >= 1 */
+    int seqlen;         /* L >= 1, up to 2^31 - 1024 (1 for the step) */
+    int channels;       /* D >= 1, below 2^21 */
+    int in_dtype;       /* ssd_dtype_t of x, gate, in_gate, out and their gradients */
+    int state_dtype;    /* ssd_dtype_t of the states and their gradients (the recurrence runs in fp32) */
+    int normalize;      /* 1 or 0 */
+    int nseq;           /* with seq_idx (or for the step): the number of states; else ignored */
+    int64_t x_stride, gate_stride, in_stride; /* elements between rows, below 2^21 (the step: 2^31); 0: D */
+} ssd_recurrence_params_t;
+
+/*   x, gate       [B, L, D]  in_dtype     required, rows
+ *   A             [D]        fp32         required; A <= 0 is a precondition (not checked; -inf forgets the state at every
+ *                                         token with an open gate)
+ *   in_gate       [B, L, D]  in_dtype     rows; NULL: i = 1
+ *   gate_bias     [D]        fp32         NULL means 0
+ *   in_bias       [D]        fp32         NULL means 0; only with in_gate
+ *   seq_idx       [B, L]     int32        NULL: every batch row is one sequence
+ *   initial_state [S, D]     state_dtype  NULL means 0
+ *   out           [B, L, D]  in_dtype     required, contiguous
+ *   final_state   [S, D]     state_dtype  NULL: not wanted; overlaps initial_state nowhere
+ *   saved                    fp32         NULL, or ssd_gated_recurrence_saved_size() bytes: states kept for the backward
+ *                                         pass, one every 128 tokens
+ *   workspace                             256-byte aligned, ssd_gated_recurrence_workspace_size() bytes */
+size_t ssd_gated_recurrence_workspace_size(const ssd_recurrence_params_t* p);
+size_t ssd_gated_recurrence_saved_size(const ssd_recurrence_params_t* p);
+ssd_status_t ssd_gated_recurrence(const ssd_recurrence_params_t* p, const void* x, const void* gate, const float* A,
+                                  const void* in_gate, const float* gate_bias, const float* in_bias,
+                                  const int32_t* seq_idx, const void* initial_state, void* out, void* final_state,
+                                  void* saved, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradients from dout [B, L, D] (contiguous), dfinal_state [S, D] (NULL means 0), the same inputs and the
+ * forward call's `saved`:
+ *   dx, dgate, din_gate [B, L, D] in_dtype contiguous (din_gate required exactly when in_gate is given); dA [D] fp32
+ *   required; dgate_bias, din_bias [D] fp32 and dinitial_state [S, D] state_dtype, NULL: not wanted.
+ * Where beta is 0 (A = 0, or a gate that is closed in fp32) its gradient counts as 0. */
+size_t ssd_gated_recurrence_backward_workspace_size(const ssd_recurrence_params_t* p);
+ssd_status_t ssd_gated_recurrence_backward(const ssd_recurrence_params_t* p, const void* dout, const void* dfinal_state,
+                                           const void* x, const void* gate, const float* A, const void* in_gate,
+                                           const float* gate_bias, const float* in_bias, const int32_t* seq_idx,
+                                           const void* initial_state, const void* saved, void* dx, void* dgate,
+                                           float* dA, void* din_gate, float* dgate_bias, float* din_bias,
+                                           void* dinitial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token per batch row: x, gate, in_gate [B, D] (rows) -> out [B, D]; state [nseq, D] state_dtype is updated in
+ * place (fp32 arithmetic, rounded to state_dtype once). */
+ssd_status_t ssd_gated_recurrence_step(const ssd_recurrence_params_t* p, const void* x, const void* gate, const float* A,
+                                       const void* in_gate, const float* gate_bias, const float* in_bias, void* state,
+                                       const int32_t* slots, void* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

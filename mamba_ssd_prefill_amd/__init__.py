@@ -8,7 +8,8 @@ built, every call raises: there is no fallback path.
     y, final_state = ssd_prefill(x, dt, A, B, C, D, dt_bias, initial_state,
                                  chunk_size=128, impl="fused")
 
-The selective scan, its causal convolution and the 8-bit state cache are in selective.py.
+The selective scan, its causal convolution and the 8-bit state cache are in selective.py; the residual norm, the matrix
+product with its epilogue and the gated linear recurrence in layer.py.
 """
 import ctypes
 import os
@@ -119,8 +120,9 @@ def load_library():
     for f in ("ssd_step_chunk_cumsum", "ssd_step_bmm", "ssd_step_chunk_state", "ssd_step_state_passing",
               "ssd_step_chunk_scan", "ssd_decode_step", "ssd_conv_silu", "ssd_gated_norm", "ssd_prefill_block"):
         getattr(lib, f).restype = ctypes.c_int
-    from . import selective
+    from . import layer, selective
     selective.declare(lib)
+    layer.declare(lib)
     _lib = lib
     return lib
 
@@ -485,3 +487,10 @@ from .selective import *  # noqa: E402,F401,F403
 
 __all__ += selective.__all__
 EXPORTED_SYMBOLS += selective.EXPORTED_SYMBOLS
+
+# ---- residual norm, matrix product, gated recurrence (layer.py) ------------------------------------
+from . import layer  # noqa: E402
+from .layer import *  # noqa: E402,F401,F403
+
+__all__ += layer.__all__
+EXPORTED_SYMBOLS += layer.EXPORTED_SYMBOLS

@@ -1,0 +1,120 @@
+// ssd_layer.h -- argument blocks and launchers of the residual norm, the matrix product with its epilogue and the gated
+// recurrence (kernels in ssd_norm.hip, ssd_linear*.hip, ssd_recur.hip; checks in ssd_layer_api.cpp).  Layouts are
+// described in include/mamba_ssd.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ssd {
+
+// ---- residual norm ----------------------------------------------------------------------------
+struct RmsArgs {
+    const void* x;  // the backward's: the sum
+    const void* res;
+    const float* w;
+    void* out;  // values or codes
+    float* scales;
+    void* sum;
+    // backward
+    const void* dout;
+    const void* dsum;
+    void* dx;
+    void* dres;
+    float* part;  // [parts][width]: sums of dw over the rows of a workgroup
+    int64_t rows, xs, rs;
+    int width, res_dtype, format;  // format -1: values
+    int parts;
+    float eps;
+};
+constexpr int kNormMaxWidth = 16384;
+constexpr int kNormParts = 1024;  // workgroups of the backward at most
+int norm_parts(int64_t rows, int width, int in_dtype);
+
+hipError_t launch_rms_norm(RmsArgs& a, int in_dtype, hipStream_t st);
+hipError_t launch_rms_norm_backward(RmsArgs& a, int in_dtype, float* dw, hipStream_t st);
+
+// ---- matrix product ---------------------------------------------------------------------------
+// Operands of the product: rows with the contraction's values one behind the other.
+enum : int { LT_F32 = 0, LT_F16 = 1, LT_BF16 = 2, LT_I8 = 3, LT_E4M3 = 4 };
+struct LinearArgs {
+    const void* x;  // [M] rows of kbytes, xs bytes apart
+    const void* w;  // [N] rows of kbytes, ws bytes apart
+    const float* bias;
+    const void* res;  // [M][N] out type, rows rs elements apart
+    const float* sx;  // [M] or NULL
+    const float* sw;  // [N] or NULL
+    void* out;        // [M][N]
+    void* pre;        // [M][N] or NULL
+    float* part;      // [splits][M][N] fp32 where the contraction is split
+    int64_t xs, ws, rs;
+    int M, N, kbytes, act, out_dtype;
+    int splits, steps_per_split;
+};
+struct LinearPlan {
+    int tile;    // index of the tile shape
+    int splits;  // of the contraction
+};
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type);
+hipError_t launch_linear(LinearArgs& a, int type, const LinearPlan& p, hipStream_t st);
+
+// Rows copied into ones that the product takes: kp values a row, those behind the source's zero.
+struct PackArgs {
+    const void* src;  // [rows] of cols values, stride elements apart
+    void* dst;        // [rows][kp], or transposed: [cols][kp] with kp >= rows
+    int64_t rows, cols, stride, kp;
+};
+hipError_t launch_pack(PackArgs& a, int elem_bytes, bool transposed, hipStream_t st);
+
+// dpre = dout act'(pre), as rows of np >= N values and transposed with rows of mp >= M (either NULL: not wanted), and its
+// sums over stretches of 64 rows.
+struct DpreArgs {
+    const void* dout;
+    const void* pre;
+    void* rows;
+    void* cols;
+    float* part;  // [ceil(M / 64)][N]
+    int64_t M, N, np, mp;
+    int act;
+};
+hipError_t launch_dpre(DpreArgs& a, int dtype, float* dbias, hipStream_t st);
+
+// ---- gated recurrence -------------------------------------------------------------------------
+struct RecurArgs {
+    const void* x;
+    const void* gate;
+    const void* ig;
+    const float* A;
+    const float* gb;
+    const float* ib;
+    const int32_t* seq;
+    const void* h0;
+    void* out;
+    void* fin;
+    float* saved;  // [batch][tiles][channels]: the state entering each tile of kRecurTile tokens
+    // backward
+    const void* dout;
+    const void* dfin;
+    void* dx;
+    void* dgate;
+    void* dig;
+    void* dh0;
+    float* part;  // [batch * nsplit][3][channels]: dA, dgate_bias, din_bias
+    // time splits: what each adds to the state (or its gradient) and what it lets through
+    float* split_state;  // [batch][nsplit][channels]
+    float* split_decay;
+    // step
+    void* pool;
+    const int32_t* slots;
+    int batch, seqlen, channels, nseq, state_dtype, normalize;
+    int nsplit, tiles_per_split, ntiles;
+    int64_t xs, gs, is;
+};
+constexpr int kRecurTile = 128;
+int recur_splits(int64_t batch, int64_t seqlen, int64_t channels);
+
+hipError_t launch_recur(RecurArgs& a, int in_dtype, hipStream_t st);
+hipError_t launch_recur_backward(RecurArgs& a, int in_dtype, float* dA, float* dgb, float* dib, hipStream_t st);
+hipError_t launch_recur_step(RecurArgs& a, int in_dtype, hipStream_t st);
+
+}  // namespace ssd

@@ -1,0 +1,362 @@
+// ssd_linear.h -- the matrix product out[m][n] = act(sum_k x[m][k] w[n][k] sx[m] sw[n] + bias[n]) + res[m][n] in tiles.
+//
+// Both operands have the contraction's values one behind the other, so a tile of either is rows of 128 bytes (32 fp32,
+// 64 16-bit or 128 8-bit values), and everything up to the matrix instruction is the same for all types.  A
+// workgroup brings BM rows of x and BN of w into LDS a step of 128 bytes ahead of the step that it multiplies
+// (direct loads to LDS, 16 bytes a lane; pieces behind a row's end are read past the buffer, as zeros).
+//
+// w is the matrix instruction's first operand, so a lane's four accumulators are four consecutive n of one m; the rows
+// of w that the 16 lanes of a block take are chosen so that the NB blocks of a wave leave 4 NB consecutive n in a lane,
+// which the epilogue reads and writes 16 bytes at a time.
+//
+// LDS rows are 128 bytes, two to a line of 64 banks; piece c of row r lies at c ^ swz(r), chosen so that the 16
+// rows that a read takes at one c fall on 16 different places of a line.
+#pragma once
+
+#include "ssd_device.h"
+#include "ssd_layer.h"
+
+#define SSD_LDS_PTR(T, p) ((__attribute__((address_space(3))) T*)(p))
+
+namespace ssd {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// One 16-byte piece of each operand (two for e4m3) multiplied onto a 16 x 16 block.
+template <int TYPE> struct Mul;
+template <> struct Mul<LT_BF16> {
+    typedef f32x4 Acc;
+    static constexpr int PIECES = 1;
+    __device__ static inline void run(const u32x4 (&w)[1], const u32x4 (&x)[1], Acc& c) {
+        c = TT<__bf16>::mma(__builtin_bit_cast(bf16x8, w[0]), __builtin_bit_cast(bf16x8, x[0]), c);
+    }
+};
+template <> struct Mul<LT_F16> {
+    typedef f32x4 Acc;
+    static constexpr int PIECES = 1;
+    __device__ static inline void run(const u32x4 (&w)[1], const u32x4 (&x)[1], Acc& c) {
+        c = TT<_Float16>::mma(__builtin_bit_cast(f16x8, w[0]), __builtin_bit_cast(f16x8, x[0]), c);
+    }
+};
+template <> struct Mul<LT_F32> {
+    typedef f32x4 Acc;
+    static constexpr int PIECES = 1;
+    __device__ static inline void run(const u32x4 (&w)[1], const u32x4 (&x)[1], Acc& c) {
+        const f32x4 a = __builtin_bit_cast(f32x4, w[0]), b = __builtin_bit_cast(f32x4, x[0]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c = TT<float>::mma(a[e], b[e], c);
+    }
+};
+template <> struct Mul<LT_I8> {
+    typedef i32x4 Acc;
+    static constexpr int PIECES = 1;
+    __device__ static inline void run(const u32x4 (&w)[1], const u32x4 (&x)[1], Acc& c) {
+        c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[0]), __builtin_bit_cast(i32x4, x[0]), c, 0, 0, 0);
+    }
+};
+template <> struct Mul<LT_E4M3> {
+    typedef f32x4 Acc;
+    static constexpr int PIECES = 2;
+    __device__ static inline void run(const u32x4 (&w)[2], const u32x4 (&x)[2], Acc& c) {
+        const i32x8 a = __builtin_shufflevector(__builtin_bit_cast(i32x4, w[0]), __builtin_bit_cast(i32x4, w[1]), 0, 1, 2, 3, 4, 5, 6, 7);
+        const i32x8 b = __builtin_shufflevector(__builtin_bit_cast(i32x4, x[0]), __builtin_bit_cast(i32x4, x[1]), 0, 1, 2, 3, 4, 5, 6, 7);
+        // (both scales 2^0: the rows' own come in the epilogue)
+        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+    }
+};
+
+// ---- epilogue -----------------------------------------------------------------------------------
+// gelu(v) = v (1 + erf(v / sqrt(2))) / 2
+__device__ inline float gelu_f(float v) { return 0.5f * v * (1.f + erff(v * 0.70710678118654752440f)); }
+__device__ inline float gelu_d(float v) {
+    return 0.5f * (1.f + erff(v * 0.70710678118654752440f)) + v * __expf(-0.5f * v * v) * 0.39894228040143267794f;
+}
+__device__ inline float sigm_f(float v) { return __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
+__device__ inline float act_f(float v, int act) {
+    // (v times a sigmoid of 0: -infinity gives 0 in the limit)
+    return act == 1 ? (v == -__builtin_inff() ? 0.f : v * sigm_f(v)) : act == 2 ? (v == -__builtin_inff() ? 0.f : gelu_f(v)) : v;
+}
+__device__ inline float act_d(float v, int act) {
+    if (act == 1) {
+        const float s = sigm_f(v), c = 1.f - s;
+        return c == 0.f ? 1.f : s == 0.f ? 0.f : s * __builtin_fmaf(v, c, 1.f);
+    }
+    return act == 2 ? (fabsf(v) > 1e4f ? (v > 0.f ? 1.f : 0.f) : gelu_d(v)) : 1.f;
+}
+
+// C consecutive values of one row at element offset `off`, n of them existing; the type is a run-time one.
+template <int C, typename T> __device__ inline void row_load_t(const void* p, int64_t off, int n, float (&v)[C]) {
+    constexpr int ONE = 16 / (int)sizeof(T) < C ? 16 / (int)sizeof(T) : C;
+    typedef T Raw __attribute__((ext_vector_type(ONE), aligned(sizeof(T))));
+    const T* q = (const T*)p + off;
+#pragma unroll
+    for (int i = 0; i < C; i += ONE) {
+        if (i + ONE <= n) {
+            const Raw r = *(const Raw*)(q + i);
+#pragma unroll
+            for (int e = 0; e < ONE; ++e) v[i + e] = (float)r[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < ONE; ++e) v[i + e] = i + e < n ? (float)q[i + e] : 0.f;
+        }
+    }
+}
+template <int C, typename T> __device__ inline void row_store_t(void* p, int64_t off, int n, const float (&v)[C]) {
+    constexpr int ONE = 16 / (int)sizeof(T) < C ? 16 / (int)sizeof(T) : C;
+    typedef T Raw __attribute__((ext_vector_type(ONE), aligned(sizeof(T))));
+    T* q = (T*)p + off;
+#pragma unroll
+    for (int i = 0; i < C; i += ONE) {
+        if (i + ONE <= n) {
+            Raw r;
+#pragma unroll
+            for (int e = 0; e < ONE; ++e) r[e] = (T)v[i + e];
+            *(Raw*)(q + i) = r;
+        } else {
+#pragma unroll
+            for (int e = 0; e < ONE; ++e)
+                if (i + e < n) q[i + e] = (T)v[i + e];
+        }
+    }
+}
+template <int C> __device__ inline void row_load(const void* p, int dt, int64_t off, int n, float (&v)[C]) {
+    if (dt == DT_F32)
+        row_load_t<C, float>(p, off, n, v);
+    else if (dt == DT_F16)
+        row_load_t<C, _Float16>(p, off, n, v);
+    else
+        row_load_t<C, __bf16>(p, off, n, v);
+}
+template <int C> __device__ inline void row_store(void* p, int dt, int64_t off, int n, const float (&v)[C]) {
+    if (dt == DT_F32)
+        row_store_t<C, float>(p, off, n, v);
+    else if (dt == DT_F16)
+        row_store_t<C, _Float16>(p, off, n, v);
+    else
+        row_store_t<C, __bf16>(p, off, n, v);
+}
+
+// What C consecutive columns from n take besides the product.
+template <int C> struct Columns {
+    float bias[C], scale[C];
+    int n, live;
+    __device__ inline Columns(const LinearArgs& a, int n0) : n(n0), live(a.N - n0) {
+        if (a.bias) row_load_t<C, float>(a.bias, n, live, bias);
+        if (a.sw) row_load_t<C, float>(a.sw, n, live, scale);
+    }
+    // the outputs of row m from its sums
+    __device__ inline void finish(const LinearArgs& a, int m, float (&v)[C]) const {
+        if (live <= 0) return;
+        const int64_t o = (int64_t)m * a.N + n;
+        if (a.sx) {
+            const float s = a.sx[m];
+#pragma unroll
+            for (int e = 0; e < C; ++e) v[e] *= s;
+        }
+        if (a.sw) {
+#pragma unroll
+            for (int e = 0; e < C; ++e) v[e] *= scale[e];
+        }
+        if (a.bias) {
+#pragma unroll
+            for (int e = 0; e < C; ++e) v[e] += bias[e];
+        }
+        if (a.pre) row_store<C>(a.pre, a.out_dtype, o, live, v);
+        if (a.act) {
+#pragma unroll
+            for (int e = 0; e < C; ++e) v[e] = act_f(v[e], a.act);
+        }
+        if (a.res) {
+            float r[C];
+            row_load<C>(a.res, a.out_dtype, (int64_t)m * a.rs + n, live, r);
+#pragma unroll
+            for (int e = 0; e < C; ++e) v[e] += r[e];
+        }
+        row_store<C>(a.out, a.out_dtype, o, live, v);
+    }
+};
+
+// ---- tiles ----------------------------------------------------------------------------------------
+constexpr uint32_t kNoPiece = 0x80000000u;  // an offset past every operand's buffer: reads as zeros
+
+// BM x BN outputs a workgroup, WVM x WVN waves.
+template <int TYPE, int BM, int BN, int WVM, int WVN> struct LinearTile {
+    static constexpr int NW = WVM * WVN, THREADS = 64 * NW, MB = BM / WVM / 16, NB = BN / WVN / 16;
+    static constexpr int STEP = 128;  // bytes of a row
+    static constexpr int RPI = 8 * NW;  // rows that one load of every lane brings
+    static constexpr int IX = BM / RPI, IW = BN / RPI;
+    static constexpr int STAGE = (BM + BN) * STEP, LDS = 2 * STAGE;
+    static constexpr int SH = __builtin_ctz(4 * NB);
+    static_assert(BM % RPI == 0 && BN % RPI == 0, "rows of a load");
+    __device__ static inline int swz_x(int row) { return (row >> 1) & 7; }
+    __device__ static inline int swz_w(int row) { return (row >> 1 & 1) | (row >> SH & 3) << 1; }
+};
+
+// Where a lane's pieces come from and go to: rows behind the last one repeat it.
+template <typename G, int BM, int BN> struct Loads {
+    __amdgpu_buffer_rsrc_t rx, rw;
+    char* lds;
+    uint32_t kbytes, ox[G::IX], ow[G::IW], cx[G::IX], cw[G::IW];
+    __device__ inline Loads(const LinearArgs& a, char* to, int m0, int n0, int wave, int lane) {
+        rx = make_rsrc((const char*)a.x + (int64_t)m0 * a.xs, 0x7fffffffu);
+        rw = make_rsrc((const char*)a.w + (int64_t)n0 * a.ws, 0x7fffffffu);
+        lds = to + wave * 1024;
+        kbytes = (uint32_t)a.kbytes;
+#pragma unroll
+        for (int j = 0; j < G::IX; ++j) {
+            const int row = j * G::RPI + wave * 8 + (lane >> 3);
+            cx[j] = (uint32_t)((lane & 7) ^ G::swz_x(row)) * 16;
+            ox[j] = (uint32_t)min(row, a.M - 1 - m0) * (uint32_t)a.xs + cx[j];
+        }
+#pragma unroll
+        for (int j = 0; j < G::IW; ++j) {
+            const int row = j * G::RPI + wave * 8 + (lane >> 3);
+            cw[j] = (uint32_t)((lane & 7) ^ G::swz_w(row)) * 16;
+            ow[j] = (uint32_t)min(row, a.N - 1 - n0) * (uint32_t)a.ws + cw[j];
+        }
+    }
+    __device__ inline void issue(int step) const {
+        const uint32_t k = (uint32_t)step * G::STEP, left = kbytes - k;
+        char* to = lds + (step & 1) * G::STAGE;
+#pragma unroll
+        for (int j = 0; j < G::IX; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, SSD_LDS_PTR(void, to + j * G::RPI * G::STEP), 16,
+                                                     cx[j] < left ? ox[j] + k : kNoPiece, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < G::IW; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, SSD_LDS_PTR(void, to + (BM + j * G::RPI) * G::STEP), 16,
+                                                     cw[j] < left ? ow[j] + k : kNoPiece, 0, 0, 0);
+    }
+};
+
+template <int TYPE, int BM, int BN, int WVM, int WVN>
+__global__ __launch_bounds__(64 * WVM * WVN) void k_linear(LinearArgs a) {
+    typedef LinearTile<TYPE, BM, BN, WVM, WVN> G;
+    typedef Mul<TYPE> M;
+    extern __shared__ __align__(1024) char lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+    // Neighbouring tiles go to one XCD (workgroups are dealt to eight in turn), in groups of 8 rows of tiles, so that
+    // the rows they share come from its L2.
+    uint32_t id = blockIdx.x;
+    const uint32_t whole = gridDim.x / 8 * 8;
+    if (id < whole) id = (id & 7) * (whole / 8) + id / 8;
+    const int split = (int)(id % (uint32_t)a.splits);
+    id /= (uint32_t)a.splits;
+    const int grp = 8 * tn, g0 = (int)id / grp * 8, gm = min(8, tm - g0);
+    const int m0 = (g0 + (int)(id % (uint32_t)grp) % gm) * BM, n0 = (int)(id % (uint32_t)grp) / gm * BN;
+    const int steps = (a.kbytes + G::STEP - 1) / G::STEP;
+    const int s0 = split * a.steps_per_split, s1 = min(s0 + a.steps_per_split, steps);
+
+    const Loads<G, BM, BN> loads(a, lds, m0, n0, wave, lane);
+    typename M::Acc acc[G::NB][G::MB];
+#pragma unroll
+    for (int i = 0; i < G::NB; ++i)
+#pragma unroll
+        for (int j = 0; j < G::MB; ++j) acc[i][j] = vzero<typename M::Acc>();
+    const int wm = wave % WVM, wn = wave / WVM, l16 = lane & 15, q = lane >> 4;
+    // this lane's row of its wave's first block, and the piece it starts with
+    const int xrow = wm * G::MB * 16 + l16, wrow = wn * G::NB * 16 + (l16 >> 2) * 4 * G::NB + (l16 & 3);
+    if (s0 < s1) loads.issue(s0);
+    for (int step = s0; step < s1; ++step) {
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // this wave's loads are there; behind the barrier everyone's
+        __syncthreads();
+        if (step + 1 < s1) loads.issue(step + 1);
+        const char* tx = lds + (step & 1) * G::STAGE;
+        const char* tw = tx + BM * G::STEP;
+#pragma unroll
+        for (int kk = 0; kk < 2 / M::PIECES; ++kk) {
+            u32x4 fx[G::MB][M::PIECES], fw[G::NB][M::PIECES];
+#pragma unroll
+            for (int p = 0; p < M::PIECES; ++p) {
+                const int c = (M::PIECES == 2 ? p : kk) * 4 + q;
+#pragma unroll
+                for (int i = 0; i < G::NB; ++i) {
+                    const int row = wrow + i * 4;
+                    fw[i][p] = *(const u32x4*)(tw + row * G::STEP + (c ^ G::swz_w(row)) * 16);
+                }
+#pragma unroll
+                for (int j = 0; j < G::MB; ++j) {
+                    const int row = xrow + j * 16;
+                    fx[j][p] = *(const u32x4*)(tx + row * G::STEP + (c ^ G::swz_x(row)) * 16);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < G::NB; ++i)
+#pragma unroll
+                for (int j = 0; j < G::MB; ++j) M::run(fw[i], fx[j], acc[i][j]);
+        }
+    }
+    constexpr int C = 4 * G::NB;
+    const int n = n0 + wn * G::NB * 16 + q * C;
+    if (a.splits > 1) {
+#pragma unroll
+        for (int j = 0; j < G::MB; ++j) {
+            const int m = m0 + xrow + j * 16;
+            if (m >= a.M || n >= a.N) continue;
+            float v[C];
+#pragma unroll
+            for (int i = 0; i < G::NB; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const auto t = acc[i][j][e];
+                    v[i * 4 + e] = __builtin_bit_cast(float, t);
+                }
+            row_store_t<C, float>(a.part, ((int64_t)split * a.M + m) * a.N + n, a.N - n, v);
+        }
+        return;
+    }
+    const Columns<C> cols(a, n);
+#pragma unroll
+    for (int j = 0; j < G::MB; ++j) {
+        const int m = m0 + xrow + j * 16;
+        if (m >= a.M) continue;
+        float v[C];
+#pragma unroll
+        for (int i = 0; i < G::NB; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i * 4 + e] = (float)acc[i][j][e];
+        cols.finish(a, m, v);
+    }
+}
+
+// The sums over the splits of the contraction, and what stands behind the product: four outputs a lane.
+template <typename V> __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a) {
+    const int per = (a.N + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int m = (int)(i / per), n = (int)(i % per) * 4;
+    if (m >= a.M) return;
+    V s[4] = {0, 0, 0, 0};
+    const int64_t o = (int64_t)m * a.N + n;
+    for (int k = 0; k < a.splits; ++k) {
+        float v[4];
+        row_load_t<4, float>(a.part, (int64_t)k * a.M * a.N + o, a.N - n, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += __builtin_bit_cast(V, v[e]);
+    }
+    const Columns<4> cols(a, n);
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)s[e];
+    cols.finish(a, m, v);
+}
+
+template <int TYPE, int BM, int BN, int WVM, int WVN> hipError_t launch_tile(LinearArgs& a, hipStream_t st) {
+    typedef LinearTile<TYPE, BM, BN, WVM, WVN> G;
+    const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
+    void* args[] = {&a};
+    const void* fn = (const void*)&k_linear<TYPE, BM, BN, WVM, WVN>;
+    return hipLaunchKernel(fn, dim3((unsigned)(tiles * a.splits)), dim3(G::THREADS), args, G::LDS, st);
+}
+
+template <int TYPE> hipError_t launch_linear_type(LinearArgs& a, const LinearPlan& p, hipStream_t st) {
+    hipError_t e = launch_tile<TYPE, 128, 128, 2, 2>(a, st);
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t lanes = (int64_t)a.M * ((a.N + 3) / 4);
+    void* args[] = {&a};
+    const void* fn = TYPE == LT_I8 ? (const void*)&k_linear_join<int> : (const void*)&k_linear_join<float>;
+    return hipLaunchKernel(fn, dim3((unsigned)((lanes + 255) / 256)), dim3(256), args, 0, st);
+}
+
+}  // namespace ssd

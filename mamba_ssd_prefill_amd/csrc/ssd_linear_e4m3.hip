@@ -1,0 +1,8 @@
+// ssd_linear_e4m3.hip -- the matrix product's kernels for e4m3 operands (ssd_linear.h).
+#include "ssd_linear.h"
+
+namespace ssd {
+
+hipError_t launch_linear_e4m3(LinearArgs& a, const LinearPlan& p, hipStream_t st) { return launch_linear_type<LT_E4M3>(a, p, st); }
+
+}  // namespace ssd

@@ -1,0 +1,376 @@
+// ssd_norm.hip -- root-mean-square norm of a residual stream's rows with the addition before it, its output as values or
+// in 8 bits, and its gradients (ssd_rms_norm / _backward in include/mamba_ssd.h).
+//
+//     s = x + residual,  r = 1 / sqrt(mean(s^2) + eps),  y = s r w
+//     n = s r,  g = dout w,  ds = r (g - n mean(g n)) + dsum,  dw = sum_rows dout n
+//
+// Both are HBM-bound streams: a row is read once, stays in registers (fp32) over the sums of the row, and is written
+// once.  A lane takes pieces of 16 bytes (of 16-bit values; 16 of fp32), a row's lanes being one wave, four or sixteen
+// by its width.  Rows and pieces need no alignment beyond their elements': wide accesses take any address on this
+// chip, and only the last piece of an odd row goes value by value.
+#include "ssd_code8.h"
+#include "ssd_layer.h"
+#include "ssd_sum_rows.h"
+
+namespace ssd {
+
+// VEC values at p of which n exist (the others read as 0 and are not written), 16 bytes an access.
+template <typename T, int VEC> __device__ inline void load_piece(const T* p, int n, float (&v)[VEC]) {
+    constexpr int ONE = 16 / (int)sizeof(T) < VEC ? 16 / (int)sizeof(T) : VEC;
+    typedef T Raw __attribute__((ext_vector_type(ONE), aligned(sizeof(T))));
+    if (n >= VEC) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += ONE) {
+            const Raw r = *(const Raw*)(p + i);
+#pragma unroll
+            for (int e = 0; e < ONE; ++e) v[i + e] = (float)r[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = e < n ? (float)p[e] : 0.f;
+    }
+}
+template <typename T, int VEC> __device__ inline void store_piece(T* p, int n, const float (&v)[VEC]) {
+    constexpr int ONE = 16 / (int)sizeof(T) < VEC ? 16 / (int)sizeof(T) : VEC;
+    typedef T Raw __attribute__((ext_vector_type(ONE), aligned(sizeof(T))));
+    if (n >= VEC) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += ONE) {
+            Raw r;
+#pragma unroll
+            for (int e = 0; e < ONE; ++e) r[e] = (T)v[i + e];
+            *(Raw*)(p + i) = r;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (e < n) p[e] = (T)v[e];
+    }
+}
+// The same for a type known at run time: in_dtype T, or fp32.
+template <typename T, int VEC>
+__device__ inline void load_piece_as(const void* p, int64_t off, bool f32, int n, float (&v)[VEC]) {
+    if (f32)
+        load_piece<float, VEC>((const float*)p + off, n, v);
+    else
+        load_piece<T, VEC>((const T*)p + off, n, v);
+}
+template <typename T, int VEC>
+__device__ inline void store_piece_as(void* p, int64_t off, bool f32, int n, const float (&v)[VEC]) {
+    if (f32)
+        store_piece<float, VEC>((float*)p + off, n, v);
+    else
+        store_piece<T, VEC>((T*)p + off, n, v);
+}
+
+__device__ inline float wave_sum(float v) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+    return v;
+}
+__device__ inline uint32_t wave_max(uint32_t v) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m, 64));
+    return v;
+}
+
+// Sums (or the largest) over the W waves of a row, in one order for every lane.  `lds`: W values of its own.
+template <int W> __device__ inline float row_sum(float v, float* lds) {
+    v = wave_sum(v);
+    if constexpr (W > 1) {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) lds[wave] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) v += lds[i];
+    }
+    return v;
+}
+template <int W> __device__ inline void row_sums(float& v, float& u, float* lds) {
+    v = wave_sum(v);
+    u = wave_sum(u);
+    if constexpr (W > 1) {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+            lds[wave] = v;
+            lds[W + wave] = u;
+        }
+        __syncthreads();
+        v = u = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            v += lds[i];
+            u += lds[W + i];
+        }
+    }
+}
+template <int W> __device__ inline uint32_t row_max(uint32_t v, uint32_t* lds) {
+    v = wave_max(v);
+    if constexpr (W > 1) {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) lds[wave] = v;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < W; ++i) v = max(v, lds[i]);
+    }
+    return v;
+}
+
+// W waves a row (a workgroup is four rows of one wave, or one row), NP pieces a lane at most.
+template <typename T, int W, int NP> __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rms_norm(RmsArgs a) {
+    constexpr int VEC = 16 / (int)sizeof(T), LANES = 64 * W, ROWS = W == 1 ? 4 : 1;
+    __shared__ float lds[4 * W];
+    const int lane = W == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+    const int D = a.width;
+    const bool res32 = a.res_dtype == DT_F32;
+    int turn = 0;  // (places for the sums are used in turn: a wave may be a row ahead of another's reads, never two)
+    for (int64_t row = (int64_t)blockIdx.x * ROWS + (W == 1 ? (int)(threadIdx.x >> 6) : 0); row < a.rows;
+         row += (int64_t)gridDim.x * ROWS, ++turn) {
+        float v[NP][VEC], ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const int e0 = (lane + LANES * k) * VEC;
+            if (e0 < D) load_piece<T, VEC>((const T*)a.x + row * a.xs + e0, D - e0, v[k]);
+        }
+        if (a.res) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const int e0 = (lane + LANES * k) * VEC;
+                if (e0 < D) {
+                    float r[VEC];
+                    load_piece_as<T, VEC>(a.res, row * a.rs + e0, res32, D - e0, r);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) v[k][e] += r[e];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const int e0 = (lane + LANES * k) * VEC;
+                if (e0 < D) store_piece_as<T, VEC>(a.sum, row * D + e0, res32, D - e0, v[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const int e0 = (lane + LANES * k) * VEC;
+            if (e0 < D) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) ss = __builtin_fmaf(v[k][e], v[k][e], ss);
+            }
+        }
+        const float r = __builtin_amdgcn_rsqf(row_sum<W>(ss, lds + (turn & 1) * 2 * W) / (float)D + a.eps);
+        uint32_t mu = 0;
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const int e0 = (lane + LANES * k) * VEC;
+            if (e0 < D) {
+                float w[VEC];
+                load_piece<float, VEC>(a.w + e0, D - e0, w);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    v[k][e] = v[k][e] * r * w[e];
+                    // (values behind the row's end are 0, or 0 times an infinite r: not looked at)
+                    if (e0 + e < D) mu = max(mu, __builtin_bit_cast(uint32_t, v[k][e]) & 0x7fffffffu);
+                }
+                if (a.format < 0) store_piece<T, VEC>((T*)a.out + row * D + e0, D - e0, v[k]);
+            }
+        }
+        if (a.format < 0) continue;
+        // 8 bits: as integers the magnitudes keep their order, with the infinities and NaN above every number
+        mu = row_max<W>(mu, (uint32_t*)lds + (turn & 1) * 2 * W + W);
+        float s = __builtin_bit_cast(float, mu) / (a.format == 0 ? 127.f : 448.f);
+        const bool none = mu >= 0x7f800000u || s < kMinScale;
+        if (none) s = mu >= 0x7f800000u ? __builtin_nanf("") : 0.f;
+        const float inv = 1.f / s;
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const int e0 = (lane + LANES * k) * VEC;
+            if (e0 < D) {
+                uint8_t c[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float q = quotient_to_odd(v[k][e], s, inv);
+                    c[e] = none ? 0 : (uint8_t)(a.format == 0 ? code_int8(q) : code_e4m3(q));
+                }
+                uint8_t* p = (uint8_t*)a.out + row * D + e0;
+                if (e0 + VEC <= D) {
+                    __builtin_memcpy(p, c, VEC);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        if (e0 + e < D) p[e] = c[e];
+                }
+            }
+        }
+        if (lane == 0) a.scales[row] = s;
+    }
+}
+
+// Gradients.  A workgroup takes every parts-th row (W = 1: four rows at a time), and its lanes keep the sums over
+// these rows of their pieces of dw.
+template <typename T, int W, int NP>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rms_norm_backward(RmsArgs a) {
+    constexpr int VEC = 16 / (int)sizeof(T), LANES = 64 * W, ROWS = W == 1 ? 4 : 1;
+    __shared__ float lds[4 * W];
+    __shared__ float meet[W == 1 ? 4 * 64 * NP * VEC : 1];
+    const int lane = W == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x, sub = W == 1 ? (int)(threadIdx.x >> 6) : 0;
+    const int D = a.width;
+    const bool res32 = a.res_dtype == DT_F32;
+    float dw[NP][VEC];
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dw[k][e] = 0.f;
+    int turn = 0;
+    for (int64_t row = (int64_t)blockIdx.x * ROWS + sub; row < a.rows; row += (int64_t)gridDim.x * ROWS) {
+        float s[NP][VEC], g[NP][VEC], ss = 0.f, gs = 0.f;
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const int e0 = (lane + LANES * k) * VEC;
+            if (e0 < D) {
+                load_piece_as<T, VEC>(a.x, row * a.xs + e0, res32, D - e0, s[k]);
+                load_piece<T, VEC>((const T*)a.dout + row * D + e0, D - e0, g[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const int e0 = (lane + LANES * k) * VEC;
+            if (e0 < D) {
+                float w[VEC];
+                load_piece<float, VEC>(a.w + e0, D - e0, w);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    ss = __builtin_fmaf(s[k][e], s[k][e], ss);
+                    gs = __builtin_fmaf(g[k][e] * w[e], s[k][e], gs);
+                }
+            }
+        }
+        // (two places for the sums, used in turn: a wave may be a row ahead of another's reads, never two)
+        row_sums<W>(ss, gs, lds + (turn & 1) * 2 * W);
+        ++turn;
+        const float r = __builtin_amdgcn_rsqf(ss / (float)D + a.eps);
+        const float c = gs / (float)D * r * r;  // ds = r (g - s c) + dsum
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const int e0 = (lane + LANES * k) * VEC;
+            if (e0 < D) {
+                float w[VEC], d[VEC];
+                load_piece<float, VEC>(a.w + e0, D - e0, w);
+                if (a.dsum) load_piece_as<T, VEC>(a.dsum, row * D + e0, res32, D - e0, d);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    dw[k][e] = __builtin_fmaf(g[k][e], s[k][e] * r, dw[k][e]);
+                    const float v = r * __builtin_fmaf(-s[k][e], c, g[k][e] * w[e]);
+                    d[e] = a.dsum ? v + d[e] : v;
+                }
+                if (a.dx) store_piece<T, VEC>((T*)a.dx + row * D + e0, D - e0, d);
+                if (a.dres) store_piece_as<T, VEC>(a.dres, row * D + e0, res32, D - e0, d);
+            }
+        }
+    }
+    if constexpr (W == 1) {  // the four rows' sums meet in LDS
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) meet[((sub * NP + k) * VEC + e) * 64 + lane] = dw[k][e];
+        __syncthreads();
+        if (sub) return;
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int i = (k * VEC + e) * 64 + lane;
+                dw[k][e] = (meet[i] + meet[NP * VEC * 64 + i]) + (meet[2 * NP * VEC * 64 + i] + meet[3 * NP * VEC * 64 + i]);
+            }
+    }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const int e0 = (lane + LANES * k) * VEC;
+        if (e0 < D) store_piece<float, VEC>(a.part + (int64_t)blockIdx.x * D + e0, D - e0, dw[k]);
+    }
+}
+
+// dw from the workgroups' sums: 64 columns a workgroup.
+__global__ __launch_bounds__(256) void k_norm_dw(const float* part, float* dw, int parts, int width) {
+    __shared__ float lds[256];
+    const int c = blockIdx.x * 64 + (threadIdx.x & 63);
+    const bool live = c < width;
+    const float s = sum_rows<float>(part + (live ? c : 0), width, parts, lds, live);
+    if (live && threadIdx.x < 64) dw[c] = s;
+}
+
+namespace {
+template <typename T> const void* forward_kernel(int pieces, bool few, int& W) {
+    if (!few) {
+        W = 1;
+        if (pieces <= 64) return (const void*)&k_rms_norm<T, 1, 1>;
+        if (pieces <= 128) return (const void*)&k_rms_norm<T, 1, 2>;
+        if (pieces <= 320) return (const void*)&k_rms_norm<T, 1, 5>;
+    }
+    W = 4;
+    if (pieces <= 256) return (const void*)&k_rms_norm<T, 4, 1>;
+    if (pieces <= 512) return (const void*)&k_rms_norm<T, 4, 2>;
+    if (pieces <= 1024) return (const void*)&k_rms_norm<T, 4, 4>;
+    W = 16;
+    if (pieces <= 2048) return (const void*)&k_rms_norm<T, 16, 2>;
+    return (const void*)&k_rms_norm<T, 16, 4>;
+}
+template <typename T> const void* backward_kernel(int pieces, int& W) {
+    W = 1;
+    if (pieces <= 64) return (const void*)&k_rms_norm_backward<T, 1, 1>;
+    if (pieces <= 128) return (const void*)&k_rms_norm_backward<T, 1, 2>;
+    W = 4;
+    if (pieces <= 256) return (const void*)&k_rms_norm_backward<T, 4, 1>;
+    if (pieces <= 512) return (const void*)&k_rms_norm_backward<T, 4, 2>;
+    if (pieces <= 1024) return (const void*)&k_rms_norm_backward<T, 4, 4>;
+    W = 16;
+    if (pieces <= 2048) return (const void*)&k_rms_norm_backward<T, 16, 2>;
+    return (const void*)&k_rms_norm_backward<T, 16, 4>;
+}
+int pieces_of(int width, int in_dtype) {
+    const int vec = in_dtype == DT_F32 ? 4 : 8;
+    return (width + vec - 1) / vec;
+}
+template <typename F> hipError_t by_type(int in_dtype, F f) {
+    switch (in_dtype) {
+    case DT_F32: return f((float*)nullptr);
+    case DT_F16: return f((_Float16*)nullptr);
+    case DT_BF16: return f((__bf16*)nullptr);
+    default: return hipErrorNotSupported;
+    }
+}
+}  // namespace
+
+constexpr int64_t kNormBlocks = 1 << 20;  // more rows are taken in turns
+
+int norm_parts(int64_t rows, int width, int in_dtype) {
+    const int64_t groups = pieces_of(width, in_dtype) <= 128 ? (rows + 3) / 4 : rows;
+    return (int)(groups < kNormParts ? groups : kNormParts);
+}
+
+hipError_t launch_rms_norm(RmsArgs& a, int in_dtype, hipStream_t st) {
+    return by_type(in_dtype, [&](auto* t) {
+        typedef __remove_pointer(decltype(t)) T;
+        int W;
+        const void* fn = forward_kernel<T>(pieces_of(a.width, in_dtype), a.rows < 1024, W);
+        int64_t grid = W == 1 ? (a.rows + 3) / 4 : a.rows;
+        if (grid > kNormBlocks) grid = kNormBlocks;
+        void* args[] = {&a};
+        return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(W == 1 ? 256 : 64 * W), args, 0, st);
+    });
+}
+
+hipError_t launch_rms_norm_backward(RmsArgs& a, int in_dtype, float* dw, hipStream_t st) {
+    const hipError_t e = by_type(in_dtype, [&](auto* t) {
+        typedef __remove_pointer(decltype(t)) T;
+        int W;
+        const void* fn = backward_kernel<T>(pieces_of(a.width, in_dtype), W);
+        void* args[] = {&a};
+        return hipLaunchKernel(fn, dim3((unsigned)a.parts), dim3(W == 1 ? 256 : 64 * W), args, 0, st);
+    });
+    if (e != hipSuccess || !dw) return e;
+    void* args[] = {&a.part, &dw, &a.parts, &a.width};
+    return hipLaunchKernel((const void*)&k_norm_dw, dim3((unsigned)((a.width + 63) / 64)), dim3(256), args, 0, st);
+}
+
+}  // namespace ssd

@@ -29,6 +29,8 @@ REQUIRED = {
     "v_mfma_f32_16x16x32_bf16": 8,
     "v_mfma_f32_16x16x32_f16": 8,
     "v_mfma_f32_16x16x4_f32": 10,
+    "v_mfma_i32_16x16x64_i8": 8,
+    "v_mfma_scale_f32_16x16x128_f8f6f4": 12,
 }
 
 _RANGE = re.compile(r"\b([av])\[(\d+):(\d+)\]")

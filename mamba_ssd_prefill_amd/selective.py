@@ -80,14 +80,14 @@ _SIZES = {"ssd_causal_conv_backward_workspace_size": ConvParams, "ssd_selective_
 EXPORTED_SYMBOLS = sorted(_SIGNATURES) + sorted(_SIZES)
 
 
-def declare(lib):
+def declare(lib, signatures=_SIGNATURES, sizes=_SIZES):
     """Argument types of this module's entry points (called once, when the library is loaded)."""
     vp, sz = ctypes.c_void_p, ctypes.c_size_t
-    for name, (params, n, ws) in _SIGNATURES.items():
+    for name, (params, n, ws) in signatures.items():
         f = getattr(lib, name)
         f.argtypes = [ctypes.POINTER(params)] + [vp] * n + ([vp, sz] if ws else []) + [vp]
         f.restype = ctypes.c_int
-    for name, params in _SIZES.items():
+    for name, params in sizes.items():
         f = getattr(lib, name)
         f.argtypes, f.restype = [ctypes.POINTER(params)], sz
 
@@ -194,7 +194,7 @@ def _by_value(v):
     import torch
     if isinstance(v, tuple):
         return all(_by_value(e) for e in v)
-    return v is None or isinstance(v, (str, bytes, numbers.Integral, torch.dtype))
+    return v is None or isinstance(v, (str, bytes, numbers.Integral, float, torch.dtype))
 
 
 def _keep(key, plan):
