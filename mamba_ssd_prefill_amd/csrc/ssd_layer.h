@@ -99,19 +99,20 @@ struct RecurArgs {
     void* dgate;
     void* dig;
     void* dh0;
-    float* part;  // [batch * nsplit][3][channels]: dA, dgate_bias, din_bias
-    // time splits: what each adds to the state (or its gradient) and what it lets through
-    float* split_state;  // [batch][nsplit][channels]
-    float* split_decay;
+    float* part;  // [batch][tiles][3][channels]: dA, dgate_bias, din_bias
+    // with more than one tile: what each does to the state (or its gradient), and how many workgroups have started
+    uint64_t* hops;  // [batch][tiles][channels]
+    uint32_t* ticket;
     // step
     void* pool;
     const int32_t* slots;
     int batch, seqlen, channels, nseq, state_dtype, normalize;
-    int nsplit, tiles_per_split, ntiles;
+    int ntiles;
     int64_t xs, gs, is;
 };
-constexpr int kRecurTile = 128;
-int recur_splits(int64_t batch, int64_t seqlen, int64_t channels);
+constexpr int kRecurTile = 128;  // tokens of a tile
+int64_t recur_tiles(int64_t seqlen);
+int64_t recur_blocks(int64_t channels, int in_dtype);  // workgroups of a tile of one batch row
 
 hipError_t launch_recur(RecurArgs& a, int in_dtype, hipStream_t st);
 hipError_t launch_recur_backward(RecurArgs& a, int in_dtype, float* dA, float* dgb, float* dib, hipStream_t st);

@@ -378,30 +378,23 @@ ssd_status_t validate_recurrence(const ssd_recurrence_params_t* p, bool step) {
     if (!step && (p->x_stride >= kMaxRecRow || p->gate_stride >= kMaxRecRow || p->in_stride >= kMaxRecRow))
         return SSD_ERR_INVALID_SHAPE;
     if (step) return (int64_t)p->batch * D >= kMaxLanes ? SSD_ERR_INVALID_SHAPE : SSD_OK;
-    const int64_t groups = (D + 31) / 32 * p->batch * ssd::recur_splits(p->batch, p->seqlen, D);
+    const int64_t groups = ssd::recur_blocks(D, p->in_dtype) * p->batch * ssd::recur_tiles(p->seqlen);
     return groups >= kMaxLanes / 512 ? SSD_ERR_INVALID_SHAPE : SSD_OK;
 }
 
-int64_t recur_tiles(const ssd_recurrence_params_t* p) {
-    return ((int64_t)p->seqlen + ssd::kRecurTile - 1) / ssd::kRecurTile;
-}
-
 struct RecLayout {
-    int nsplit;
-    size_t state_off, decay_off, part_off, total;
+    size_t hops_off, ticket_off, part_off, total;
 };
 
 RecLayout rec_layout(const ssd_recurrence_params_t* p, bool backward) {
     RecLayout l{};
-    const size_t B = p->batch, D = p->channels;
-    l.nsplit = ssd::recur_splits(p->batch, p->seqlen, p->channels);
-    const size_t n = B * l.nsplit * D * 4;
+    const size_t tiles = ssd::recur_tiles(p->seqlen), n = p->batch * tiles * p->channels;
     Regions r;
-    if (l.nsplit > 1) {
-        l.state_off = r.add(n);
-        l.decay_off = r.add(n);
+    if (tiles > 1) {
+        l.hops_off = r.add(n * 8);
+        l.ticket_off = r.add(4);
     }
-    if (backward) l.part_off = r.add(3 * n);
+    if (backward) l.part_off = r.add(3 * n * 4);
     l.total = r.size();
     return l;
 }
@@ -427,12 +420,10 @@ ssd::RecurArgs rec_args(const ssd_recurrence_params_t* p, const void* x, const v
     return a;
 }
 
-void rec_splits(ssd::RecurArgs& a, const ssd_recurrence_params_t* p, const RecLayout& l, char* ws) {
-    a.ntiles = (int)recur_tiles(p);
-    a.nsplit = l.nsplit;
-    a.tiles_per_split = (a.ntiles + l.nsplit - 1) / l.nsplit;
-    a.split_state = (float*)(ws + l.state_off);
-    a.split_decay = (float*)(ws + l.decay_off);
+void rec_space(ssd::RecurArgs& a, const ssd_recurrence_params_t* p, const RecLayout& l, char* ws) {
+    a.ntiles = (int)ssd::recur_tiles(p->seqlen);
+    a.hops = (uint64_t*)(ws + l.hops_off);
+    a.ticket = (uint32_t*)(ws + l.ticket_off);
     a.part = (float*)(ws + l.part_off);
 }
 
@@ -461,7 +452,7 @@ SSD_EXPORT size_t ssd_gated_recurrence_backward_workspace_size(const ssd_recurre
 
 SSD_EXPORT size_t ssd_gated_recurrence_saved_size(const ssd_recurrence_params_t* p) {
     if (validate_recurrence(p, false) != SSD_OK) return 0;
-    return (size_t)p->batch * recur_tiles(p) * p->channels * 4;
+    return (size_t)p->batch * ssd::recur_tiles(p->seqlen) * p->channels * 4;
 }
 
 SSD_EXPORT ssd_status_t ssd_gated_recurrence(const ssd_recurrence_params_t* p, const void* x, const void* gate, const float* A,
@@ -483,7 +474,7 @@ SSD_EXPORT ssd_status_t ssd_gated_recurrence(const ssd_recurrence_params_t* p, c
     const RecLayout l = rec_layout(p, false);
     if (workspace_bytes < l.total) return SSD_ERR_WORKSPACE_TOO_SMALL;
     ssd::RecurArgs a = rec_args(p, x, gate, A, in_gate, gate_bias, in_bias);
-    rec_splits(a, p, l, (char*)workspace);
+    rec_space(a, p, l, (char*)workspace);
     a.seq = seq_idx;
     a.h0 = initial_state;
     a.out = out;
@@ -513,7 +504,7 @@ SSD_EXPORT ssd_status_t ssd_gated_recurrence_backward(
     const RecLayout l = rec_layout(p, true);
     if (workspace_bytes < l.total) return SSD_ERR_WORKSPACE_TOO_SMALL;
     ssd::RecurArgs a = rec_args(p, x, gate, A, in_gate, gate_bias, in_bias);
-    rec_splits(a, p, l, (char*)workspace);
+    rec_space(a, p, l, (char*)workspace);
     a.seq = seq_idx;
     a.h0 = initial_state;
     a.saved = (float*)const_cast<void*>(saved);

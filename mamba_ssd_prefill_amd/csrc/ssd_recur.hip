@@ -6,20 +6,27 @@
 //     g = dout + (a g of t+1),  dl = a g h of t-1 - (a^2 / beta) g i x     (l = A r)
 //     dx = g beta i,  din_gate = g beta x i (1 - i),  dgate = dl A r (1 - r),  dA = sum dl r
 //
-// Both passes are HBM-bound (8 and 14 bytes a token and channel of 16 bits), so each reads its inputs once: a workgroup
-// walks 32 channels of a batch row through time in tiles of kRecurTile tokens.  A lane holds two channels over a
-// run of T tokens; the runs of a tile are joined by what each lets through (the product of its decays) and what it
-// adds, over the four runs of a wave by lane exchanges and over waves through LDS.  The next tile's rows are on
-// their way meanwhile.  Prompts of few channels are cut in time: a first pass finds what each split lets
-// through and adds, and the main pass starts from the splits before it.
+// Both passes are HBM-bound (8 and 14 bytes a token and channel of 16 bits), and read each input once.  A workgroup takes
+// a tile of 128 bytes of channels and kRecurTile tokens, all tiles of a time before those of the next; a lane holds two
+// channels over a run of TOK tokens.  What a run of tokens does to the state is a hop h -> p h + q.  The runs of a wave are
+// joined by lane exchanges, the waves through LDS, and the tiles through memory: a tile publishes its hop as soon as it has
+// it, finds the state that enters it by looking back over the hops before it, and publishes the state that leaves it, so
+// that those behind need not look further.
+//
+// Rows of 128 bytes are what the memory wants: reading three tensors of 2 x 8192 x 5120 by walking 32-byte columns of them
+// reached 2.0 TB/s, 64 bytes 2.4, 128 bytes 3.8 on 160 CUs alone (one workgroup a column, a forward pass of 250 us).
 #include "ssd_layer.h"
 #include "ssd_scan_common.h"
+#include "ssd_sum_rows.h"
 
 namespace ssd {
 
-constexpr int kRecWaves = 8, kRecT = kRecurTile / (4 * kRecWaves), kRecThreads = 64 * kRecWaves;
-static_assert(kRecT * 4 * kRecWaves == kRecurTile, "runs of a tile");
-constexpr int kRecCh = 32;  // channels of a workgroup
+constexpr int kRecW = 8, kRecThreads = 64 * kRecW;  // waves of a workgroup
+// Lanes of a row of 128 bytes, runs of a wave, tokens of a run, by the element size.
+template <typename T> struct RecGeo {
+    static constexpr int LN = 64 / (int)sizeof(T), CH = 2 * LN, RUNS = 64 / LN, TOK = kRecurTile / (RUNS * kRecW);
+    static_assert(RUNS * kRecW * TOK == kRecurTile, "a tile");
+};
 
 // Two channels of a token.
 struct Two {
@@ -104,508 +111,617 @@ __device__ inline void state_to(void* p, int dtype, int64_t i, float v) {
         ((__bf16*)p)[i] = (__bf16)v;
 }
 
-// sigmoid(v) = 1 / (1 + e), e = exp(-v), and 1 - sigmoid(v) = e / (1 + e), each right relative to itself (a gate closed
-// so far that e is infinite is 0, and the other 1).
-struct Gate {
-    float s, c;
-};
-__device__ inline Gate gate_of(float v) {
-    const float t = -v * kLog2e, e = __builtin_amdgcn_exp2f(t), s = __builtin_amdgcn_rcpf(1.f + e);
-    return Gate{s, t > 126.f ? 1.f : e * s};
-}
-
-// sqrt(1 - exp(2 l)), l <= 0, a = exp(l).  Near 0 the difference loses what a was rounded by, so 1 - exp(y) comes
-// from its series there: 8 terms are right to 2^-26 down to y = -1/2.
-__device__ inline float beta_of(float l, float a) {
-    const float y = 2.f * l;
-    float p = __builtin_fmaf(y, 1.f / 40320.f, 1.f / 5040.f);
-    p = __builtin_fmaf(y, p, 1.f / 720.f);
-    p = __builtin_fmaf(y, p, 1.f / 120.f);
-    p = __builtin_fmaf(y, p, 1.f / 24.f);
-    p = __builtin_fmaf(y, p, 1.f / 6.f);
-    p = __builtin_fmaf(y, p, 0.5f);
-    p = __builtin_fmaf(y, p, 1.f);
-    const float b2 = y > -0.5f ? -y * p : __builtin_fmaf(-a, a, 1.f);
-    return __builtin_amdgcn_sqrtf(b2);
-}
-
-// A channel's parameters.  A is kept finite, so that a closed gate times an infinite A is not NaN.
+// A channel's parameters, scaled for the exponentials: A log2(e), -2 A, and the biases times -log2(e).  A is kept finite, so
+// that a closed gate times an infinite A is not NaN.
 struct RecParams {
-    float A, A2, gb, ib;
+    float A, A2, Am, gb, ib;
 };
 __device__ inline RecParams rec_params(const RecurArgs& a, int c, bool live) {
-    RecParams p{0.f, 0.f, 0.f, 0.f};
+    RecParams p{0.f, 0.f, 0.f, 0.f, 0.f};
     if (live) {
         const float A = a.A[c];
         p.A = A < -0x1p100f ? -0x1p100f : A;
         p.A2 = p.A * kLog2e;
-        p.gb = a.gb ? a.gb[c] : 0.f;
-        p.ib = a.ib ? a.ib[c] : 0.f;
+        p.Am = -2.f * p.A;
+        p.gb = a.gb ? -kLog2e * a.gb[c] : 0.f;
+        p.ib = a.ib ? -kLog2e * a.ib[c] : 0.f;
     }
     return p;
 }
 
-// What a run of tokens does to the state before it: h -> p h + q.  p = -1: nothing passes (a sequence starts in it).
+// sigmoid(v) = 1 / (1 + e), e = exp(-v - bias), and 1 - sigmoid = e / (1 + e), each right relative to itself (a gate closed
+// so far that e is infinite is 0, and the other 1).
+__device__ inline float gate_of(float v, float bias) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(__builtin_fmaf(v, -kLog2e, bias)));
+}
+struct Gate {
+    float s, c;
+};
+__device__ inline Gate gates_of(float v, float bias) {
+    const float t = __builtin_fmaf(v, -kLog2e, bias), e = __builtin_amdgcn_exp2f(t), s = __builtin_amdgcn_rcpf(1.f + e);
+    return Gate{s, t > 126.f ? 1.f : e * s};
+}
+
+// sqrt(1 - exp(-z)), z = -2 A r >= 0, a = exp(-z / 2).  Near 0 the difference loses what a was rounded by, so up to
+// z = 1/2 it is z times the minimax polynomial of (1 - exp(-z)) / z there (right to 0.12 * 2^-24).
+__device__ inline float beta_of(float z, float a) {
+    float p = __builtin_fmaf(z, -0.0011216349666938186f, 0.008187386207282543f);
+    p = __builtin_fmaf(z, p, -0.041629090905189514f);
+    p = __builtin_fmaf(z, p, 0.16666224598884583f);
+    p = __builtin_fmaf(z, p, -0.4999998211860657f);
+    p = __builtin_fmaf(z, p, 1.f) * z;
+    float q = __builtin_fmaf(-a, a, 1.f);
+    asm("" : "+v"(p), "+v"(q));  // (both at hand: else a branch for every value, which keeps them from running side by side)
+    return __builtin_amdgcn_sqrtf(z < 0.5f ? p : q);
+}
+
+// What a run of tokens does to the state before it: h -> p h + q.  PACKED: p = -1 lets nothing through (a sequence starts
+// in it), not even a NaN.
 struct Hop {
     float p, q;
 };
-__device__ inline Hop then(Hop f, Hop s) {  // f first
-    if (s.p < 0.f) return s;
-    return Hop{f.p < 0.f ? f.p : f.p * s.p, __builtin_fmaf(s.p, f.q, s.q)};
+template <bool PACKED> __device__ inline Hop then(Hop f, Hop s) {  // f first
+    if (PACKED && s.p < 0.f) return s;
+    return Hop{PACKED && f.p < 0.f ? f.p : f.p * s.p, __builtin_fmaf(s.p, f.q, s.q)};
 }
-__device__ inline float after(Hop s, float h) { return s.p < 0.f ? s.q : __builtin_fmaf(s.p, h, s.q); }
+template <bool PACKED> __device__ inline float after(Hop s, float h) { return PACKED && s.p < 0.f ? s.q : __builtin_fmaf(s.p, h, s.q); }
 
-__device__ inline Hop shift_hop(Hop v, int lanes) { return Hop{__shfl_up(v.p, lanes, 64), __shfl_up(v.q, lanes, 64)}; }
-__device__ inline Hop shift_hop_down(Hop v, int lanes) { return Hop{__shfl_down(v.p, lanes, 64), __shfl_down(v.q, lanes, 64)}; }
+__device__ inline uint32_t bits(float v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ inline float unbits(uint32_t v) { return __builtin_bit_cast(float, v); }
+// The runs of a wave (of LN lanes each) joined in pairs: rows of 16 lanes, then half waves.  At each level every lane gets
+// the hop of the pair's first in time (REV: time runs backwards), and `own` becomes that of the whole pair.
+template <int LN, bool REV, bool PACKED> struct WaveHops {
+    Hop first[2];
+    template <int LEVEL> __device__ inline void level(Hop& own) {
+        Hop lo, hi;
+        if constexpr (LEVEL == 0) {
+            const auto p = __builtin_amdgcn_permlane16_swap(bits(own.p), bits(own.p), false, false);
+            const auto q = __builtin_amdgcn_permlane16_swap(bits(own.q), bits(own.q), false, false);
+            lo = Hop{unbits(p[0]), unbits(q[0])};
+            hi = Hop{unbits(p[1]), unbits(q[1])};
+        } else {
+            const auto p = __builtin_amdgcn_permlane32_swap(bits(own.p), bits(own.p), false, false);
+            const auto q = __builtin_amdgcn_permlane32_swap(bits(own.q), bits(own.q), false, false);
+            lo = Hop{unbits(p[0]), unbits(q[0])};
+            hi = Hop{unbits(p[1]), unbits(q[1])};
+        }
+        first[LEVEL] = REV ? hi : lo;
+        own = then<PACKED>(first[LEVEL], REV ? lo : hi);
+    }
+    __device__ inline Hop join(Hop own) {
+        if constexpr (LN == 16) level<0>(own);
+        level<1>(own);
+        return own;
+    }
+    // the state entering this lane's run, from the one entering the wave
+    __device__ inline float enter(float h) const {
+        const bool late16 = ((threadIdx.x & 16) != 0) != REV, late32 = ((threadIdx.x & 32) != 0) != REV;
+        h = late32 ? after<PACKED>(first[1], h) : h;
+        if constexpr (LN == 16) h = late16 ? after<PACKED>(first[0], h) : h;
+        return h;
+    }
+};
 
-// The state entering each lane's run, from the runs' hops and the state `carry` entering the tile, which becomes the one
-// leaving it.  `lds` [waves][32]: a tile's own place (two used in turn).  REV: time runs backwards, from the
-// last run to the first.
-template <bool REV> __device__ inline float join_runs(Hop own, float& carry, Hop* lds, int slot) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), run = lane >> 4;
-    Hop inc = own;
-#pragma unroll
-    for (int d = 1; d < 4; d *= 2) {
-        const Hop o = REV ? shift_hop_down(inc, 16 * d) : shift_hop(inc, 16 * d);
-        if (REV ? run + d < 4 : run >= d) inc = then(o, inc);
+// (p, q) of two channels a lane.
+typedef f32x4 HopPair;
+
+// The runs of a tile: put() leaves the waves' hops in LDS ([kRecW][LN]); behind a barrier fold() gives the tile's, and
+// enter() the state entering a run from the one entering the tile.
+template <int LN, bool REV, bool PACKED> struct TileHops {
+    WaveHops<LN, REV, PACKED> waves[2];
+    Hop tile[2], before[2];  // of the whole tile, of the waves before this one
+    __device__ inline void put(const Hop (&own)[2], HopPair* lds) {
+        const Hop a = waves[0].join(own[0]), b = waves[1].join(own[1]);
+        const int lane = threadIdx.x & 63;
+        if (lane < LN) lds[(threadIdx.x >> 6) * LN + lane] = HopPair{a.p, a.q, b.p, b.q};
     }
-    if (run == (REV ? 0 : 3)) lds[wave * kRecCh + slot] = inc;
-    const Hop before = REV ? shift_hop_down(inc, 16) : shift_hop(inc, 16);  // of the wave's runs before this one
-    __syncthreads();
-    float h = carry, mine = 0.f;
+    __device__ inline void fold(const HopPair* lds) {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        tile[0] = tile[1] = before[0] = before[1] = Hop{1.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < kRecWaves; ++k) {
-        const int w = REV ? kRecWaves - 1 - k : k;
-        if (w == wave) mine = h;
-        h = after(lds[w * kRecCh + slot], h);
+        for (int i = 0; i < kRecW; ++i) {
+            const int w = REV ? kRecW - 1 - i : i;
+            const HopPair o = lds[w * LN + (threadIdx.x & (LN - 1))];
+            if (w == wave) {
+                before[0] = tile[0];
+                before[1] = tile[1];
+            }
+            tile[0] = then<PACKED>(tile[0], Hop{o[0], o[1]});
+            tile[1] = then<PACKED>(tile[1], Hop{o[2], o[3]});
+        }
     }
-    carry = h;
-    return run == (REV ? 3 : 0) ? mine : after(before, mine);
+    __device__ inline float enter(int k, float h) const { return waves[k].enter(after<PACKED>(before[k], h)); }
+};
+
+// ---- tiles through memory ---------------------------------------------------------------------------
+// A tile's word for a channel: its hop (p, q), or (-1, the state that leaves it), which lets nothing before it through.
+// A word is written and read whole, by atomics that the whole device sees, and says by itself whether it is there yet.
+constexpr uint64_t kNoHop = ~(uint64_t)0;
+// Looks at a word that is not there before a lane gives up (and its states become NaN).  Workgroups take the tiles in the
+// order of their start, so a tile that is waited for is always running: this ends only waits that a second call running on
+// the same workspace made endless.
+constexpr int kMaxLooks = 1 << 20;
+
+__device__ inline float no_nan(float v) { return v != v ? __builtin_nanf("") : v; }  // (all ones would be kNoHop)
+__device__ inline void publish(uint64_t* at, Hop h) {
+    const uint64_t v = (uint64_t)bits(no_nan(h.p)) << 32 | bits(no_nan(h.q));
+    __hip_atomic_store(at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Where a workgroup stands.  Neighbouring channel blocks go to one XCD (workgroups are dealt to eight in turn), whose L2
-// then holds the 128-byte lines that two of them share.
+__global__ __launch_bounds__(256) void k_recur_clear(uint64_t* hops, int64_t n, uint32_t* ticket) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) hops[i] = kNoHop;
+}
+
+// The state entering tile `tile` (REV: the gradient behind it) for this lane's two channels.  The words of kRecW tiles (or
+// twice as many) before it are read at a time, one a wave, again until one of them lets nothing through; from there
+// on the hops are applied one by one.  So the result is that of tiles one behind the other to the bit, whichever words
+// were there at which time.  c0: the workgroup's first channel; `init`: what enters the first tile.  `lds`: [64 * kRecW].
+template <int LN, bool REV> __device__ inline void look_back(const RecurArgs& a, int b, int tile, int c0, const void* init, Hop* lds, float (&h)[2]) {
+    constexpr int CH = 2 * LN, PER = 64 / CH, WIN = kRecW * PER;
+    const int lane = threadIdx.x & 63, place = (int)(threadIdx.x >> 6) * PER + lane / CH, c = c0 + lane % CH;
+    const int t = REV ? tile + 1 + place : tile - 1 - place;
+    const bool there = c < a.channels && t >= 0 && t < a.ntiles;
+    const uint64_t* at = a.hops + (there ? ((int64_t)b * a.ntiles + t) * a.channels + c : 0);
+    Hop r{-1.f, 0.f};
+    if (!there && c < a.channels && init) r.q = state_at(init, a.state_dtype, (int64_t)b * a.channels + c);
+    int looks = 0;
+    for (int round = 0;; ++round) {
+        if (there) {
+            uint64_t v = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            while (v == kNoHop && looks < kMaxLooks) {
+                __builtin_amdgcn_s_sleep(1);
+                v = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                ++looks;
+            }
+            r = v == kNoHop ? Hop{-1.f, __builtin_nanf("")} : Hop{unbits((uint32_t)(v >> 32)), unbits((uint32_t)v)};
+        }
+        lds[place * CH + lane % CH] = r;
+        __syncthreads();
+        const int i0 = 2 * (lane & (LN - 1));
+        bool found[2] = {false, false};
+        h[0] = h[1] = 0.f;
+#pragma unroll
+        for (int i = WIN - 1; i >= 0; --i) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const Hop o = lds[i * CH + i0 + k];
+                found[k] = found[k] || o.p < 0.f;
+                h[k] = after<true>(o, h[k]);
+            }
+        }
+        if (__all(found[0] && found[1])) break;  // (the same in every wave)
+        if (round == kMaxLooks) {
+            h[0] = h[1] = __builtin_nanf("");
+            break;
+        }
+        __syncthreads();
+    }
+}
+
+// A workgroup's tile: in the order that workgroups start, all tiles of a time (REV: from the last) before those of the next.
 struct RecPlace {
-    int b, split, c0, tok;     // first of this lane's channels, first token of its run in a tile
+    int b, tile, block0, c0, tok;  // first channel of the workgroup, of this lane; first token of its run in the tile
     bool live[2];
     int64_t row0;
 };
-__device__ inline RecPlace rec_place(const RecurArgs& a) {
-    RecPlace p;
-    const int nblk = (a.channels + kRecCh - 1) / kRecCh;
+template <typename T, bool REV> __device__ inline RecPlace rec_place(const RecurArgs& a) {
+    typedef RecGeo<T> G;
+    __shared__ uint32_t mine;
     uint32_t i = blockIdx.x;
-    const uint32_t n = gridDim.x, whole = n / 8 * 8;
-    if (i < whole) i = (i & 7) * (whole / 8) + i / 8;
-    const int blk = (int)(i % (uint32_t)nblk);
-    i /= (uint32_t)nblk;
-    p.split = (int)(i % (uint32_t)a.nsplit);
-    p.b = (int)(i / (uint32_t)a.nsplit);
+    if (a.ntiles > 1) {
+        if (threadIdx.x == 0) mine = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        i = __builtin_amdgcn_readfirstlane(mine);
+        i = i < gridDim.x ? i : gridDim.x - 1;  // (never, but for a second call on the same workspace)
+    }
+    RecPlace p;
+    const uint32_t nblk = ((uint32_t)a.channels + G::CH - 1) / G::CH;
+    p.block0 = (int)(i % nblk) * G::CH;
+    i /= nblk;
+    p.b = (int)(i % (uint32_t)a.batch);
+    p.tile = (int)(i / (uint32_t)a.batch);
+    if (REV) p.tile = a.ntiles - 1 - p.tile;
     const int lane = threadIdx.x & 63;
-    p.c0 = blk * kRecCh + (lane & 15) * 2;
+    p.c0 = p.block0 + (lane & (G::LN - 1)) * 2;
     p.live[0] = p.c0 < a.channels;
     p.live[1] = p.c0 + 1 < a.channels;
-    p.tok = ((int)(threadIdx.x >> 6) * 4 + (lane >> 4)) * kRecT;
+    p.tok = ((int)(threadIdx.x >> 6) * G::RUNS + lane / G::LN) * G::TOK;
     p.row0 = (int64_t)p.b * a.seqlen;
     return p;
 }
 
-// Of a lane's T tokens from t: which start a sequence, end one, and are padding (those behind the row's end are neither
-// start nor end); their numbers.
-struct RecSeq {
-    uint32_t start, end, pad;
-    int32_t q[kRecT];
-};
-__device__ inline RecSeq rec_seq(const RecurArgs& a, int64_t row0, int t) {
-    RecSeq s{0, 0, 0, {}};
-    const int32_t* seq = a.seq + row0;
-    int32_t before = 0;
-    if (t > 0 && t < a.seqlen) before = seq[t - 1];
-#pragma unroll
-    for (int j = 0; j < kRecT; ++j) {
-        s.q[j] = -1;
-        if (t + j < a.seqlen) {
-            const int32_t q = seq[t + j];
-            s.q[j] = q;
-            if (t + j == 0 || before != q) s.start |= 1u << j;
-            if (t + j == a.seqlen - 1 || seq[t + j + 1] != q) s.end |= 1u << j;
-            if (q < 0 || q >= a.nseq) s.pad |= 1u << j;
-            before = q;
-        }
-    }
-    return s;
-}
-
-// Decays and additions of a lane's tokens.  Tokens behind the row's end leave the state as it is.
-template <typename T, bool PAIRED, bool PACKED> struct RecTile {
+// A lane's inputs of a tile, as loaded.  seq: the sequence numbers of its tokens, and of the ones before and behind.
+template <typename T, bool PAIRED, bool PACKED, int TOK> struct RecTile {
     typedef RecRows<T, PAIRED> Rows;
-    typename Rows::Held x[kRecT], g[kRecT], i[kRecT];
+    typename Rows::Held x[TOK], g[TOK], i[TOK];
+    int32_t seq[PACKED ? TOK + 2 : 1];
     __device__ inline void load(const RecurArgs& a, const RecPlace& p, const uint32_t (&ch)[2], int t0) {
         const int n = min(a.seqlen - t0, kRecurTile);
-        const Rows rx(a.x, a.xs, p.row0 + min(t0, a.seqlen - 1), n), rg(a.gate, a.gs, p.row0 + min(t0, a.seqlen - 1), n);
+        const Rows rx(a.x, a.xs, p.row0 + t0, n), rg(a.gate, a.gs, p.row0 + t0, n);
 #pragma unroll
-        for (int j = 0; j < kRecT; ++j) {
+        for (int j = 0; j < TOK; ++j) {
             x[j] = rx.load(p.tok + j, ch);
             g[j] = rg.load(p.tok + j, ch);
         }
         if (a.ig) {
-            const Rows ri(a.ig, a.is, p.row0 + min(t0, a.seqlen - 1), n);
+            const Rows ri(a.ig, a.is, p.row0 + t0, n);
 #pragma unroll
-            for (int j = 0; j < kRecT; ++j) i[j] = ri.load(p.tok + j, ch);
+            for (int j = 0; j < TOK; ++j) i[j] = ri.load(p.tok + j, ch);
+        }
+        if constexpr (PACKED) {
+#pragma unroll
+            for (int j = 0; j < TOK + 2; ++j) {
+                const int t = min(max(t0 + p.tok + j - 1, 0), a.seqlen - 1);
+                seq[j] = a.seq[p.row0 + t];
+            }
         }
     }
 };
 
-// The tile's decay and addition of token j, channel k.
+// Of a lane's tokens from t: which start a sequence, end one, and are padding (those behind the row's end are neither
+// start nor end).
+struct RecSeq {
+    uint32_t start, end, pad;
+};
+template <int TOK> __device__ inline RecSeq rec_seq(const RecurArgs& a, const int32_t (&q)[TOK + 2], int t) {
+    RecSeq s{0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < TOK; ++j) {
+        if (t + j < a.seqlen) {
+            if (t + j == 0 || q[j] != q[j + 1]) s.start |= 1u << j;
+            if (t + j == a.seqlen - 1 || q[j + 2] != q[j + 1]) s.end |= 1u << j;
+            if (q[j + 1] < 0 || q[j + 1] >= a.nseq) s.pad |= 1u << j;
+        }
+    }
+    return s;
+}
+// The state (or its gradient) of sequence q for this lane's channel k, 0 where there is none.
+__device__ inline float seq_state(const RecurArgs& a, const RecPlace& p, const void* states, int32_t q, bool pad, int k) {
+    return pad || !states || !p.live[k] ? 0.f : state_at(states, a.state_dtype, (int64_t)q * a.channels + p.c0 + k);
+}
+
+// Decays and additions of a lane's tokens.  (All tokens behind one branch: one for each value keeps their chains of dependent
+// instructions from running side by side; training 2 x 4096 x 5120 took 420 us with them.)
 struct RecStep {
     float a, u;
 };
-__device__ inline RecStep rec_step_of(const RecurArgs& a, const RecParams& p, float x, float g, float i) {
-    const float r = gate_of(g + p.gb).s;
-    const float d = __builtin_amdgcn_exp2f(p.A2 * r);
-    float u = a.ig ? x * gate_of(i + p.ib).s : x;
-    if (a.normalize) u *= beta_of(p.A * r, d);
-    return RecStep{d, u};
+template <typename Rows, int TOK, typename Tile>
+__device__ inline void rec_steps(const RecurArgs& a, const RecParams (&prm)[2], const Tile& t, RecStep (&st)[TOK][2]) {
+    float r[TOK][2];
+#pragma unroll
+    for (int j = 0; j < TOK; ++j) {
+        const Two x = Rows::values(t.x[j]), g = Rows::values(t.g[j]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            r[j][k] = gate_of(g.c[k], prm[k].gb);
+            st[j][k] = RecStep{__builtin_amdgcn_exp2f(prm[k].A2 * r[j][k]), x.c[k]};
+        }
+    }
+    if (a.ig) {
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+            const Two i = Rows::values(t.i[j]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) st[j][k].u *= gate_of(i.c[k], prm[k].ib);
+        }
+    }
+    if (a.normalize) {
+#pragma unroll
+        for (int j = 0; j < TOK; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) st[j][k].u *= beta_of(prm[k].Am * r[j][k], st[j][k].a);
+    }
 }
 
-// MAIN: outputs; else only what the split lets through and adds.
-template <typename T, bool PAIRED, bool PACKED, bool MAIN> __global__ __launch_bounds__(kRecThreads) void k_recur(RecurArgs a) {
-    typedef RecTile<T, PAIRED, PACKED> Tile;
+template <typename T, bool PAIRED, bool PACKED> __global__ __launch_bounds__(kRecThreads) void k_recur(RecurArgs a) {
+    typedef RecGeo<T> G;
+    constexpr int TOK = G::TOK, LN = G::LN;
+    typedef RecTile<T, PAIRED, PACKED, TOK> Tile;
     typedef typename Tile::Rows Rows;
-    __shared__ Hop lds[2][2][kRecWaves * kRecCh];
-    const RecPlace p = rec_place(a);
-    const int slot = (threadIdx.x & 15) * 2;
+    __shared__ HopPair waves[kRecW * LN];
+    __shared__ Hop looked[kRecW * 64];
+    const RecPlace p = rec_place<T, false>(a);
+    const int t0 = p.tile * kRecurTile;
     uint32_t ch[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) ch[k] = p.live[k] ? (uint32_t)(p.c0 + k) * (uint32_t)sizeof(T) : kNoLane;
+    Tile now;
+    now.load(a, p, ch, t0);
     RecParams prm[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) prm[k] = rec_params(a, p.c0 + k, p.live[k]);
-    const int first = p.split * a.tiles_per_split, last = min(first + a.tiles_per_split, a.ntiles);
-    float carry[2] = {0.f, 0.f};
-    Hop whole[2] = {{1.f, 0.f}, {1.f, 0.f}};
-    if constexpr (MAIN) {
+    RecSeq sq{0, 0, 0};
+    if constexpr (PACKED) sq = rec_seq<TOK>(a, now.seq, t0 + p.tok);
+    RecStep st[TOK][2];
+    rec_steps<Rows, TOK>(a, prm, now, st);
+    if (t0 + kRecurTile > a.seqlen) {  // tokens behind the row's end leave the state as it is
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (!p.live[k]) continue;
-            if (!PACKED && a.h0) carry[k] = state_at(a.h0, a.state_dtype, (int64_t)p.b * a.channels + p.c0 + k);
-            for (int s = 0; s < p.split; ++s) {
-                const int64_t o = ((int64_t)p.b * a.nsplit + s) * a.channels + p.c0 + k;
-                carry[k] = after(Hop{a.split_decay[o], a.split_state[o]}, carry[k]);
-            }
-        }
-    }
-    Tile next;
-    if (first < last) next.load(a, p, ch, first * kRecurTile);
-    for (int tile = first; tile < last; ++tile) {
-        const int t0 = tile * kRecurTile;
-        Tile now = next;
-        if (tile + 1 < last) next.load(a, p, ch, t0 + kRecurTile);
-        RecSeq sq;
-        if constexpr (PACKED) sq = rec_seq(a, p.row0, t0 + p.tok);
-        if (MAIN && a.saved && threadIdx.x < 16) {
+        for (int j = 0; j < TOK; ++j)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                if (p.live[k]) a.saved[((int64_t)p.b * a.ntiles + tile) * a.channels + p.c0 + k] = carry[k];
-        }
-        float d[kRecT][2], u[kRecT][2];
-        Hop own[2] = {{1.f, 0.f}, {1.f, 0.f}};
+                if (t0 + p.tok + j >= a.seqlen) st[j][k] = RecStep{1.f, 0.f};
+    }
+    if constexpr (PACKED) {
+        if (sq.start) {
 #pragma unroll
-        for (int j = 0; j < kRecT; ++j) {
-            const Two x = Rows::values(now.x[j]), g = Rows::values(now.g[j]);
-            Two i{{0.f, 0.f}};
-            if (a.ig) i = Rows::values(now.i[j]);
-            const bool in = t0 + p.tok + j < a.seqlen;
+            for (int j = 0; j < TOK; ++j)
+                if (sq.start >> j & 1) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                RecStep s = rec_step_of(a, prm[k], x.c[k], g.c[k], i.c[k]);
-                if (!in) s = RecStep{1.f, 0.f};
-                if constexpr (PACKED) {
-                    if (sq.start >> j & 1) {
-                        const bool pad = sq.pad >> j & 1;
-                        const float h0 = pad || !a.h0 || !p.live[k] ? 0.f
-                            : state_at(a.h0, a.state_dtype, (int64_t)sq.q[j] * a.channels + p.c0 + k);
-                        s = RecStep{-1.f, __builtin_fmaf(s.a, h0, s.u)};
+                    for (int k = 0; k < 2; ++k) {
+                        const float h0 = seq_state(a, p, a.h0, now.seq[j + 1], sq.pad >> j & 1, k);
+                        st[j][k] = RecStep{-1.f, __builtin_fmaf(st[j][k].a, h0, st[j][k].u)};
                     }
                 }
-                d[j][k] = s.a;
-                u[j][k] = s.u;
-                own[k] = PACKED ? then(own[k], Hop{s.a, s.u}) : Hop{own[k].p * s.a, __builtin_fmaf(s.a, own[k].q, s.u)};
-            }
-        }
-        float h[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if constexpr (MAIN) {
-                h[k] = join_runs<false>(own[k], carry[k], lds[tile & 1][k], slot / 2);
-            } else {
-                // the split's hop: its runs' hops in order
-                const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, run = lane >> 4;
-                Hop inc = own[k];
-#pragma unroll
-                for (int e = 1; e < 4; e *= 2) {
-                    const Hop o = shift_hop(inc, 16 * e);
-                    if (run >= e) inc = then(o, inc);
-                }
-                if (run == 3) lds[tile & 1][k][wave * kRecCh + slot / 2] = inc;
-                __syncthreads();
-                for (int w = 0; w < kRecWaves; ++w) whole[k] = then(whole[k], lds[tile & 1][k][w * kRecCh + slot / 2]);
-            }
-        }
-        if constexpr (MAIN) {
-            const Rows ro(a.out, a.channels, p.row0 + t0, min(a.seqlen - t0, kRecurTile));
-#pragma unroll
-            for (int j = 0; j < kRecT; ++j) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) h[k] = after(Hop{d[j][k], u[j][k]}, h[k]);
-                ro.store(p.tok + j, ch, h[0], h[1]);
-                if constexpr (PACKED) {
-                    if (a.fin && (sq.end & ~sq.pad) >> j & 1) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (p.live[k]) state_to(a.fin, a.state_dtype, (int64_t)sq.q[j] * a.channels + p.c0 + k, h[k]);
-                    }
-                }
-            }
         }
     }
-    if (threadIdx.x < 16) {
+    Hop own[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (!p.live[k]) continue;
-            if constexpr (!MAIN) {
-                const int64_t o = ((int64_t)p.b * a.nsplit + p.split) * a.channels + p.c0 + k;
-                a.split_decay[o] = whole[k].p;
-                a.split_state[o] = whole[k].q;
-            } else if (!PACKED && a.fin && last == a.ntiles) {
-                state_to(a.fin, a.state_dtype, (int64_t)p.b * a.channels + p.c0 + k, carry[k]);
-            }
-        }
+    for (int k = 0; k < 2; ++k) {
+        own[k] = Hop{st[0][k].a, st[0][k].u};
+#pragma unroll
+        for (int j = 1; j < TOK; ++j) own[k] = then<PACKED>(own[k], Hop{st[j][k].a, st[j][k].u});
     }
-}
-
-// Gradients.  The tiles run from the last to the first.  MAIN false: what a split passes on to the tokens before it of
-// the gradient behind it, and what it adds.
-template <typename T, bool PAIRED, bool PACKED, bool MAIN>
-__global__ __launch_bounds__(kRecThreads) void k_recur_backward(RecurArgs a) {
-    typedef RecTile<T, PAIRED, PACKED> Tile;
-    typedef typename Tile::Rows Rows;
-    __shared__ Hop lds[2][2][2][kRecWaves * kRecCh];
-    const RecPlace p = rec_place(a);
-    const int slot = (threadIdx.x & 15) * 2;
-    uint32_t ch[2];
+    TileHops<LN, false, PACKED> hops;
+    hops.put(own, waves);
+    __syncthreads();
+    hops.fold(waves);
+    const bool writer = threadIdx.x < LN;
+    uint64_t* const word = a.hops + ((int64_t)p.b * a.ntiles + p.tile) * a.channels + p.c0;
+    if (writer && p.tile > 0 && p.tile + 1 < a.ntiles) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) ch[k] = p.live[k] ? (uint32_t)(p.c0 + k) * (uint32_t)sizeof(T) : kNoLane;
-    RecParams prm[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) prm[k] = rec_params(a, p.c0 + k, p.live[k]);
-    const int first = p.split * a.tiles_per_split, last = min(first + a.tiles_per_split, a.ntiles);
-    float carry[2] = {0.f, 0.f};
-    float sA[2] = {0.f, 0.f}, sg[2] = {0.f, 0.f}, si[2] = {0.f, 0.f};
-    Hop whole[2] = {{1.f, 0.f}, {1.f, 0.f}};
-    if constexpr (MAIN) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (!p.live[k]) continue;
-            if (!PACKED && a.dfin) carry[k] = state_at(a.dfin, a.state_dtype, (int64_t)p.b * a.channels + p.c0 + k);
-            for (int s = a.nsplit - 1; s > p.split; --s) {
-                const int64_t o = ((int64_t)p.b * a.nsplit + s) * a.channels + p.c0 + k;
-                carry[k] = after(Hop{a.split_decay[o], a.split_state[o]}, carry[k]);
-            }
-        }
+        for (int k = 0; k < 2; ++k)
+            if (p.live[k]) publish(word + k, hops.tile[k]);
     }
-    for (int tile = last - 1; tile >= first; --tile) {
-        const int t0 = tile * kRecurTile, n = min(a.seqlen - t0, kRecurTile);
-        Tile now;
-        now.load(a, p, ch, t0);
-        typename Rows::Held dout[kRecT];
-        const Rows rd(a.dout, a.channels, p.row0 + t0, n);
-#pragma unroll
-        for (int j = 0; j < kRecT; ++j) dout[j] = rd.load(p.tok + j, ch);
-        RecSeq sq;
-        if constexpr (PACKED) sq = rec_seq(a, p.row0, t0 + p.tok);
-        Gate r[kRecT][2], i[kRecT][2];
-        float d[kRecT][2], be[kRecT][2];
-        Hop own[2] = {{1.f, 0.f}, {1.f, 0.f}};
-#pragma unroll
-        for (int j = 0; j < kRecT; ++j) {
-            const Two x = Rows::values(now.x[j]), g = Rows::values(now.g[j]);
-            Two iv{{0.f, 0.f}};
-            if (a.ig) iv = Rows::values(now.i[j]);
-            const bool in = t0 + p.tok + j < a.seqlen;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                r[j][k] = gate_of(g.c[k] + prm[k].gb);
-                i[j][k] = a.ig ? gate_of(iv.c[k] + prm[k].ib) : Gate{1.f, 0.f};
-                d[j][k] = __builtin_amdgcn_exp2f(prm[k].A2 * r[j][k].s);
-                be[j][k] = a.normalize ? beta_of(prm[k].A * r[j][k].s, d[j][k]) : 1.f;
-                Hop s{d[j][k], x.c[k] * i[j][k].s * be[j][k]};
-                if (!in) s = Hop{1.f, 0.f};
-                if constexpr (PACKED) {
-                    if (sq.start >> j & 1) {
-                        const bool pad = sq.pad >> j & 1;
-                        const float h0 = pad || !a.h0 || !p.live[k] ? 0.f
-                            : state_at(a.h0, a.state_dtype, (int64_t)sq.q[j] * a.channels + p.c0 + k);
-                        s = Hop{-1.f, __builtin_fmaf(s.p, h0, s.q)};
-                    }
-                    own[k] = then(own[k], s);
-                } else {
-                    own[k] = Hop{own[k].p * s.p, __builtin_fmaf(s.p, own[k].q, s.q)};
-                }
-            }
-        }
-        // the state entering the run, and then what each token passes on of the gradient behind it
-        float before[kRecT][2];
-        Hop back[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if constexpr (MAIN) {
-                float c = p.live[k] ? a.saved[((int64_t)p.b * a.ntiles + tile) * a.channels + p.c0 + k] : 0.f;
-                float h = join_runs<false>(own[k], c, lds[tile & 1][0][k], slot / 2);
-#pragma unroll
-                for (int j = 0; j < kRecT; ++j) {
-                    if constexpr (PACKED) {
-                        if (sq.start >> j & 1)
-                            h = sq.pad >> j & 1 || !a.h0 || !p.live[k] ? 0.f
-                                : state_at(a.h0, a.state_dtype, (int64_t)sq.q[j] * a.channels + p.c0 + k);
-                    }
-                    before[j][k] = h;
-                    h = __builtin_fmaf(d[j][k], h, Rows::values(now.x[j]).c[k] * i[j][k].s * be[j][k]);
-                }
-            }
-            back[k] = Hop{1.f, 0.f};
-#pragma unroll
-            for (int j = kRecT - 1; j >= 0; --j) {
-                const bool in = t0 + p.tok + j < a.seqlen;
-                float o = Rows::values(dout[j]).c[k];
-                Hop s{d[j][k], d[j][k] * o};  // v -> a (dout + v)
-                if constexpr (PACKED) {
-                    const bool pad = sq.pad >> j & 1;
-                    if (sq.end >> j & 1) {  // behind a sequence's end: the gradient of its final state
-                        const float v = pad || !a.dfin || !p.live[k] ? 0.f
-                            : state_at(a.dfin, a.state_dtype, (int64_t)sq.q[j] * a.channels + p.c0 + k);
-                        s = Hop{-1.f, d[j][k] * (o + v)};
-                    }
-                    if (sq.start >> j & 1 || pad) s = Hop{-1.f, 0.f};
-                }
-                if (!in) s = Hop{1.f, 0.f};
-                back[k] = PACKED ? then(back[k], s) : Hop{back[k].p * s.p, __builtin_fmaf(s.p, back[k].q, s.q)};
-            }
-        }
-        if constexpr (!MAIN) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, run = lane >> 4;
-                Hop inc = back[k];
-#pragma unroll
-                for (int e = 1; e < 4; e *= 2) {
-                    const Hop o = shift_hop_down(inc, 16 * e);
-                    if (run + e < 4) inc = then(o, inc);
-                }
-                if (run == 0) lds[tile & 1][1][k][wave * kRecCh + slot / 2] = inc;
-                __syncthreads();
-                for (int w = kRecWaves - 1; w >= 0; --w) whole[k] = then(whole[k], lds[tile & 1][1][k][w * kRecCh + slot / 2]);
-            }
-        } else {
-            float v[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) v[k] = join_runs<true>(back[k], carry[k], lds[tile & 1][1][k], slot / 2);
-            const Rows rx(a.dx, a.channels, p.row0 + t0, n), rg(a.dgate, a.channels, p.row0 + t0, n);
-            const Rows ri(a.ig ? a.dig : a.dgate, a.channels, p.row0 + t0, a.ig ? n : 0);
-#pragma unroll
-            for (int j = kRecT - 1; j >= 0; --j) {
-                const bool in = t0 + p.tok + j < a.seqlen;
-                const Two x = Rows::values(now.x[j]), o = Rows::values(dout[j]);
-                float dx[2], dg[2], di[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    bool pad = !in;
-                    if constexpr (PACKED) {
-                        pad = pad || (sq.pad >> j & 1);
-                        if (sq.end >> j & 1)
-                            v[k] = pad || !a.dfin || !p.live[k] ? 0.f
-                                : state_at(a.dfin, a.state_dtype, (int64_t)sq.q[j] * a.channels + p.c0 + k);
-                    }
-                    const float g = o.c[k] + v[k];
-                    const float gx = g * x.c[k], gi = gx * i[j][k].s;
-                    float dl = d[j][k] * g * before[j][k];
-                    // (beta = 0, a closed gate: the product with r (1 - r) goes to 0)
-                    if (a.normalize && be[j][k] != 0.f) dl -= d[j][k] * d[j][k] / be[j][k] * gi;
-                    const float dr = dl * prm[k].A;
-                    dx[k] = pad ? 0.f : g * be[j][k] * i[j][k].s;
-                    dg[k] = pad ? 0.f : dr * r[j][k].s * r[j][k].c;
-                    di[k] = pad ? 0.f : gi * be[j][k] * i[j][k].c;
-                    sA[k] += pad ? 0.f : dl * r[j][k].s;
-                    sg[k] += dg[k];
-                    si[k] += di[k];
-                    if (in) v[k] = d[j][k] * g;
-                    if constexpr (PACKED) {
-                        if (sq.start >> j & 1) {
-                            if (a.dh0 && !pad && p.live[k])
-                                state_to(a.dh0, a.state_dtype, (int64_t)sq.q[j] * a.channels + p.c0 + k, v[k]);
-                        }
-                        if (pad) v[k] = 0.f;
-                    }
-                }
-                rx.store(p.tok + j, ch, dx[0], dx[1]);
-                rg.store(p.tok + j, ch, dg[0], dg[1]);
-                if (a.ig) ri.store(p.tok + j, ch, di[0], di[1]);
-            }
-        }
-    }
-    if constexpr (!MAIN) {
-        if (threadIdx.x < 16) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (!p.live[k]) continue;
-                const int64_t o = ((int64_t)p.b * a.nsplit + p.split) * a.channels + p.c0 + k;
-                a.split_decay[o] = whole[k].p;
-                a.split_state[o] = whole[k].q;
-            }
-        }
+    float h[2];
+    if (p.tile > 0) {
+        look_back<LN, false>(a, p.b, p.tile, p.block0, PACKED ? nullptr : a.h0, looked, h);
     } else {
-        if (!PACKED && a.dh0 && first == 0 && threadIdx.x < 16) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (p.live[k]) state_to(a.dh0, a.state_dtype, (int64_t)p.b * a.channels + p.c0 + k, carry[k]);
-        }
-        // the sums over the workgroup's tokens: over a wave's four runs, then over waves
-        __shared__ float sums[3][2][kRecWaves * kRecCh];
+        for (int k = 0; k < 2; ++k)
+            h[k] = !PACKED && a.h0 && p.live[k] ? state_at(a.h0, a.state_dtype, (int64_t)p.b * a.channels + p.c0 + k) : 0.f;
+    }
+    if (writer) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            float s[3] = {sA[k], sg[k], si[k]};
-#pragma unroll
-            for (int e = 0; e < 3; ++e) {
-                s[e] += __shfl_xor(s[e], 16, 64);
-                s[e] += __shfl_xor(s[e], 32, 64);
-                if ((threadIdx.x & 63) < 16) sums[e][k][(threadIdx.x >> 6) * kRecCh + slot / 2] = s[e];
-            }
+            if (!p.live[k]) continue;
+            const float end = after<PACKED>(hops.tile[k], h[k]);
+            if (p.tile + 1 < a.ntiles) publish(word + k, Hop{-1.f, end});
+            if (a.saved) a.saved[((int64_t)p.b * a.ntiles + p.tile) * a.channels + p.c0 + k] = h[k];
+            if (!PACKED && a.fin && p.tile + 1 == a.ntiles) state_to(a.fin, a.state_dtype, (int64_t)p.b * a.channels + p.c0 + k, end);
         }
-        __syncthreads();
-        if (threadIdx.x < 16) {
-            const int64_t part = (int64_t)p.b * a.nsplit + p.split;
+    }
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) h[k] = hops.enter(k, h[k]);
+    const Rows ro(a.out, a.channels, p.row0 + t0, min(a.seqlen - t0, kRecurTile));
 #pragma unroll
-                for (int e = 0; e < 3; ++e) {
-                    float s = 0.f;
-                    for (int w = 0; w < kRecWaves; ++w) s += sums[e][k][w * kRecCh + slot / 2];
-                    if (p.live[k]) a.part[(part * 3 + e) * a.channels + p.c0 + k] = s;
-                }
+    for (int j = 0; j < TOK; ++j) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) h[k] = after<PACKED>(Hop{st[j][k].a, st[j][k].u}, h[k]);
+        ro.store(p.tok + j, ch, h[0], h[1]);
+        if constexpr (PACKED) {
+            if (a.fin && (sq.end & ~sq.pad) >> j & 1) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (p.live[k]) state_to(a.fin, a.state_dtype, (int64_t)now.seq[j + 1] * a.channels + p.c0 + k, h[k]);
+            }
         }
     }
 }
 
-// dA, dgate_bias, din_bias from the workgroups' sums.
-__global__ __launch_bounds__(256) void k_recur_sums(const float* part, int parts, int channels, float* dA, float* dgb, float* dib) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= channels) return;
-    float s[3] = {0.f, 0.f, 0.f};
-    for (int k = 0; k < parts; ++k)
+// Gradients.  The state entering the tile is the one that the forward pass kept; the gradient behind it comes by looking
+// back over the tiles after it.
+template <typename T, bool PAIRED, bool PACKED> __global__ __launch_bounds__(kRecThreads) void k_recur_backward(RecurArgs a) {
+    typedef RecGeo<T> G;
+    constexpr int TOK = G::TOK, LN = G::LN;
+    typedef RecTile<T, PAIRED, PACKED, TOK> Tile;
+    typedef typename Tile::Rows Rows;
+    __shared__ HopPair waves[2][kRecW * LN];
+    __shared__ Hop looked[kRecW * 64];
+    const RecPlace p = rec_place<T, true>(a);
+    const int t0 = p.tile * kRecurTile, n = min(a.seqlen - t0, kRecurTile);
+    uint32_t ch[2];
 #pragma unroll
-        for (int e = 0; e < 3; ++e) s[e] += part[((int64_t)k * 3 + e) * channels + c];
-    if (dA) dA[c] = s[0];
-    if (dgb) dgb[c] = s[1];
-    if (dib) dib[c] = s[2];
+    for (int k = 0; k < 2; ++k) ch[k] = p.live[k] ? (uint32_t)(p.c0 + k) * (uint32_t)sizeof(T) : kNoLane;
+    Tile now;
+    typename Rows::Held dout[TOK];
+    now.load(a, p, ch, t0);
+    const Rows rd(a.dout, a.channels, p.row0 + t0, n);
+#pragma unroll
+    for (int j = 0; j < TOK; ++j) dout[j] = rd.load(p.tok + j, ch);
+    float start[2] = {0.f, 0.f};
+    RecParams prm[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (p.live[k]) start[k] = a.saved[((int64_t)p.b * a.ntiles + p.tile) * a.channels + p.c0 + k];
+        prm[k] = rec_params(a, p.c0 + k, p.live[k]);
+    }
+    RecSeq sq{0, 0, 0};
+    if constexpr (PACKED) sq = rec_seq<TOK>(a, now.seq, t0 + p.tok);
+    Gate r[TOK][2], i[TOK][2];
+    float d[TOK][2], be[TOK][2], u[TOK][2];
+#pragma unroll
+    for (int j = 0; j < TOK; ++j) {
+        const Two x = Rows::values(now.x[j]), g = Rows::values(now.g[j]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            r[j][k] = gates_of(g.c[k], prm[k].gb);
+            i[j][k] = Gate{1.f, 0.f};
+            d[j][k] = __builtin_amdgcn_exp2f(prm[k].A2 * r[j][k].s);
+            be[j][k] = 1.f;
+            u[j][k] = x.c[k];
+        }
+    }
+    if (a.ig) {
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+            const Two v = Rows::values(now.i[j]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                i[j][k] = gates_of(v.c[k], prm[k].ib);
+                u[j][k] *= i[j][k].s;
+            }
+        }
+    }
+    if (a.normalize) {
+#pragma unroll
+        for (int j = 0; j < TOK; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                be[j][k] = beta_of(prm[k].Am * r[j][k].s, d[j][k]);
+                u[j][k] *= be[j][k];
+            }
+    }
+    // The hops of the states (tokens behind the row's end come after all others here), and of the gradients: what each
+    // token passes on of the gradient v behind it, v -> a (dout + v).
+    Hop own[2], back[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+            Hop s{d[j][k], u[j][k]};
+            if constexpr (PACKED) {
+                if (sq.start >> j & 1)
+                    s = Hop{-1.f, __builtin_fmaf(s.p, seq_state(a, p, a.h0, now.seq[j + 1], sq.pad >> j & 1, k), s.q)};
+            }
+            own[k] = j ? then<PACKED>(own[k], s) : s;
+        }
+#pragma unroll
+        for (int j = TOK - 1; j >= 0; --j) {
+            const float o = Rows::values(dout[j]).c[k];
+            Hop s{d[j][k], d[j][k] * o};
+            if constexpr (PACKED) {
+                const bool pad = sq.pad >> j & 1;
+                // behind a sequence's end: the gradient of its final state
+                if (sq.end >> j & 1) s = Hop{-1.f, d[j][k] * (o + seq_state(a, p, a.dfin, now.seq[j + 1], pad, k))};
+                if (sq.start >> j & 1 || pad) s = Hop{-1.f, 0.f};
+            }
+            if (t0 + p.tok + j >= a.seqlen) s = Hop{1.f, 0.f};
+            back[k] = j == TOK - 1 ? s : then<PACKED>(back[k], s);
+        }
+    }
+    TileHops<LN, false, PACKED> fwd;
+    TileHops<LN, true, PACKED> rev;
+    fwd.put(own, waves[0]);
+    rev.put(back, waves[1]);
+    __syncthreads();
+    rev.fold(waves[1]);
+    const bool writer = threadIdx.x < LN;
+    uint64_t* const word = a.hops + ((int64_t)p.b * a.ntiles + p.tile) * a.channels + p.c0;
+    if (writer && p.tile > 0 && p.tile + 1 < a.ntiles) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (p.live[k]) publish(word + k, rev.tile[k]);
+    }
+    fwd.fold(waves[0]);
+    float before[TOK][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float h = fwd.enter(k, start[k]);
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+            if constexpr (PACKED) {
+                if (sq.start >> j & 1) h = seq_state(a, p, a.h0, now.seq[j + 1], sq.pad >> j & 1, k);
+            }
+            before[j][k] = h;
+            h = __builtin_fmaf(d[j][k], h, u[j][k]);
+        }
+    }
+    float v[2];
+    if (p.tile + 1 < a.ntiles) {
+        look_back<LN, true>(a, p.b, p.tile, p.block0, PACKED ? nullptr : a.dfin, looked, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            v[k] = !PACKED && a.dfin && p.live[k] ? state_at(a.dfin, a.state_dtype, (int64_t)p.b * a.channels + p.c0 + k) : 0.f;
+    }
+    if (writer) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (!p.live[k]) continue;
+            const float end = after<PACKED>(rev.tile[k], v[k]);
+            if (p.tile > 0) publish(word + k, Hop{-1.f, end});
+            if (!PACKED && a.dh0 && p.tile == 0) state_to(a.dh0, a.state_dtype, (int64_t)p.b * a.channels + p.c0 + k, end);
+        }
+    }
+    const float root = a.normalize ? 1.f : 0.f;
+    float sum[3][2] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};  // dA, dgate_bias, din_bias
+#pragma unroll
+    for (int k = 0; k < 2; ++k) v[k] = rev.enter(k, v[k]);
+    const Rows rx(a.dx, a.channels, p.row0 + t0, n), rg(a.dgate, a.channels, p.row0 + t0, n);
+    const Rows ri(a.ig ? a.dig : a.dgate, a.channels, p.row0 + t0, a.ig ? n : 0);
+#pragma unroll
+    for (int j = TOK - 1; j >= 0; --j) {
+        const bool in = t0 + p.tok + j < a.seqlen;
+        const Two x = Rows::values(now.x[j]), o = Rows::values(dout[j]);
+        float dx[2], dg[2], di[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            bool pad = !in;
+            if constexpr (PACKED) {
+                pad = pad || (sq.pad >> j & 1);
+                if (sq.end >> j & 1) v[k] = seq_state(a, p, a.dfin, now.seq[j + 1], pad, k);
+            }
+            const float g = o.c[k] + v[k];
+            const float gi = g * x.c[k] * i[j][k].s, ag = d[j][k] * g;
+            float dl = ag * before[j][k];
+            // (beta = 0, a closed gate: the product with r (1 - r) goes to 0; without beta root is 0)
+            dl -= be[j][k] != 0.f ? root * d[j][k] * d[j][k] * gi * __builtin_amdgcn_rcpf(be[j][k]) : 0.f;
+            dx[k] = g * be[j][k] * i[j][k].s;
+            float dA = dl * r[j][k].s;
+            dg[k] = prm[k].A * dA * r[j][k].c;
+            di[k] = gi * be[j][k] * i[j][k].c;
+            if (pad) dx[k] = dg[k] = di[k] = dA = 0.f;
+            sum[0][k] += dA;
+            sum[1][k] += dg[k];
+            sum[2][k] += di[k];
+            if (in) v[k] = ag;
+            if constexpr (PACKED) {
+                if (sq.start >> j & 1 && a.dh0 && !pad && p.live[k])
+                    state_to(a.dh0, a.state_dtype, (int64_t)now.seq[j + 1] * a.channels + p.c0 + k, ag);
+                if (pad) v[k] = 0.f;
+            }
+        }
+        rx.store(p.tok + j, ch, dx[0], dx[1]);
+        rg.store(p.tok + j, ch, dg[0], dg[1]);
+        if (a.ig) ri.store(p.tok + j, ch, di[0], di[1]);
+    }
+    // the sums over the tile's tokens: over a wave's runs, then over waves
+    __shared__ float sums[3][2][kRecW * LN];
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float s = sum[e][k];
+#pragma unroll
+            for (int m = LN; m < 64; m *= 2) s += __shfl_xor(s, m, 64);
+            if ((threadIdx.x & 63) < LN) sums[e][k][(threadIdx.x >> 6) * LN + (threadIdx.x & 63)] = s;
+        }
+    __syncthreads();
+    if (writer) {
+        const int64_t part = (int64_t)p.b * a.ntiles + p.tile;
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < kRecW; ++w) s += sums[e][k][w * LN + threadIdx.x];
+                if (p.live[k]) a.part[(part * 3 + e) * a.channels + p.c0 + k] = s;
+            }
+    }
+}
+
+// dA, dgate_bias, din_bias from the tiles' sums: 64 columns of [3][channels] a workgroup.
+__global__ __launch_bounds__(256) void k_recur_sums(const float* part, int parts, int channels, float* dA, float* dgb, float* dib) {
+    __shared__ float lds[256];
+    const int64_t n = 3 * (int64_t)channels, i = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    const bool live = i < n;
+    const float s = sum_rows<float>(part + (live ? i : 0), n, parts, lds, live);
+    if (!live || threadIdx.x >= 64) return;
+    const int e = (int)(i / channels), c = (int)(i % channels);
+    float* to = e == 0 ? dA : e == 1 ? dgb : dib;
+    if (to) to[c] = s;
 }
 
 // One token a row: a lane a (row, channel).
@@ -622,34 +738,34 @@ template <typename T> __global__ __launch_bounds__(256) void k_recur_step(RecurA
     const float x = (float)((const T*)a.x)[b * a.xs + c], g = (float)((const T*)a.gate)[b * a.gs + c];
     const float ig = a.ig ? (float)((const T*)a.ig)[b * a.is + c] : 0.f;
     const int64_t at = (int64_t)slot * a.channels + c;
-    const RecStep s = rec_step_of(a, rec_params(a, c, true), x, g, ig);
-    const float h = __builtin_fmaf(s.a, state_at(a.pool, a.state_dtype, at), s.u);
+    const RecParams p = rec_params(a, c, true);
+    const float r = gate_of(g, p.gb), d = __builtin_amdgcn_exp2f(p.A2 * r);
+    float u = a.ig ? x * gate_of(ig, p.ib) : x;
+    if (a.normalize) u *= beta_of(p.Am * r, d);
+    const float h = __builtin_fmaf(d, state_at(a.pool, a.state_dtype, at), u);
     state_to(a.pool, a.state_dtype, at, h);
     *out = (T)h;
 }
 
-int recur_splits(int64_t batch, int64_t seqlen, int64_t channels) {
-    const int64_t blocks = batch * ((channels + kRecCh - 1) / kRecCh), tiles = (seqlen + kRecurTile - 1) / kRecurTile;
-    int64_t s = blocks >= 256 ? 1 : (512 + blocks - 1) / blocks;
-    if (s > tiles) s = tiles;
-    if (s > 32) s = 32;
-    const int64_t per = (tiles + s - 1) / s;
-    return (int)((tiles + per - 1) / per);  // none without a tile
+int64_t recur_tiles(int64_t seqlen) { return (seqlen + kRecurTile - 1) / kRecurTile; }
+int64_t recur_blocks(int64_t channels, int in_dtype) {
+    const int64_t ch = in_dtype == DT_F32 ? RecGeo<float>::CH : RecGeo<_Float16>::CH;
+    return (channels + ch - 1) / ch;
 }
 
 namespace {
 template <typename T, bool PAIRED, bool PACKED> hipError_t launch_rec_t(RecurArgs& a, bool backward, hipStream_t st) {
-    const unsigned blocks = (unsigned)((a.channels + kRecCh - 1) / kRecCh) * (unsigned)a.nsplit * (unsigned)a.batch;
-    void* args[] = {&a};
-    if (a.nsplit > 1) {
-        const hipError_t e = hipLaunchKernel(backward ? (const void*)&k_recur_backward<T, PAIRED, PACKED, false>
-                                                      : (const void*)&k_recur<T, PAIRED, PACKED, false>,
-                                             dim3(blocks), dim3(kRecThreads), args, 0, st);
+    const int64_t blocks = (int64_t)((a.channels + RecGeo<T>::CH - 1) / RecGeo<T>::CH) * a.batch * a.ntiles;
+    if (a.ntiles > 1) {
+        int64_t n = (int64_t)a.batch * a.ntiles * a.channels;
+        void* args[] = {&a.hops, &n, &a.ticket};
+        const int64_t grid = (n + 1023) / 1024;
+        const hipError_t e = hipLaunchKernel((const void*)&k_recur_clear, dim3((unsigned)(grid < 2048 ? grid : 2048)), dim3(256), args, 0, st);
         if (e != hipSuccess) return e;
     }
-    return hipLaunchKernel(backward ? (const void*)&k_recur_backward<T, PAIRED, PACKED, true>
-                                    : (const void*)&k_recur<T, PAIRED, PACKED, true>,
-                           dim3(blocks), dim3(kRecThreads), args, 0, st);
+    void* args[] = {&a};
+    return hipLaunchKernel(backward ? (const void*)&k_recur_backward<T, PAIRED, PACKED> : (const void*)&k_recur<T, PAIRED, PACKED>,
+                           dim3((unsigned)blocks), dim3(kRecThreads), args, 0, st);
 }
 // Whether the two channels of a lane can be accessed together: every row starts on a multiple of that.
 template <typename T> bool paired(const RecurArgs& a) {
@@ -681,9 +797,9 @@ hipError_t launch_recur(RecurArgs& a, int in_dtype, hipStream_t st) { return lau
 hipError_t launch_recur_backward(RecurArgs& a, int in_dtype, float* dA, float* dgb, float* dib, hipStream_t st) {
     const hipError_t e = launch_rec_any(a, in_dtype, true, st);
     if (e != hipSuccess) return e;
-    int parts = a.batch * a.nsplit;
+    int parts = a.batch * a.ntiles;
     void* args[] = {&a.part, &parts, &a.channels, &dA, &dgb, &dib};
-    return hipLaunchKernel((const void*)&k_recur_sums, dim3((unsigned)((a.channels + 255) / 256)), dim3(256), args, 0, st);
+    return hipLaunchKernel((const void*)&k_recur_sums, dim3((unsigned)((3 * (int64_t)a.channels + 63) / 64)), dim3(256), args, 0, st);
 }
 
 hipError_t launch_recur_step(RecurArgs& a, int in_dtype, hipStream_t st) {
