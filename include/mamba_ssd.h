@@ -718,7 +718,7 @@ typedef struct {
  *   out           [B, L, D]  in_dtype     required, contiguous
  *   final_state   [S, D]     state_dtype  NULL: not wanted; overlaps initial_state nowhere
  *   saved                    fp32         NULL, or ssd_gated_recurrence_saved_size() bytes: states kept for the backward
- *                                         pass, one every 128 tokens
+ *                                         pass, one every 64 tokens
  *   workspace                             256-byte aligned, ssd_gated_recurrence_workspace_size() bytes */
 size_t ssd_gated_recurrence_workspace_size(const ssd_recurrence_params_t* p);
 size_t ssd_gated_recurrence_saved_size(const ssd_recurrence_params_t* p);

@@ -18,10 +18,11 @@ META = os.path.join(HERE, "_meta.so")  # Python module: tensors' metadata (host 
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = (["ssd_api.cpp", "ssd_noalloc.hip", "ssd_common.hip", "ssd_decode.hip", "ssd_block.hip", "ssd_select_api.cpp",
-            "ssd_conv.hip", "ssd_scan.hip", "ssd_scan_bwd.hip", "ssd_cache.hip", "ssd_layer_api.cpp", "ssd_norm.hip", "ssd_recur.hip",
-            "ssd_linear.hip", "ssd_linear_f32.hip", "ssd_linear_f16.hip", "ssd_linear_bf16.hip", "ssd_linear_i8.hip",
-            "ssd_linear_e4m3.hip", "ssd_kernels_f32.hip", "ssd_kernels_f32_vl.hip",
+            "ssd_conv.hip", "ssd_scan.hip", "ssd_scan_bwd.hip", "ssd_cache.hip", "ssd_layer_api.cpp", "ssd_norm.hip", "ssd_linear.hip",
+            "ssd_recur.hip", "ssd_kernels_f32.hip", "ssd_kernels_f32_vl.hip",
             "ssd_kernels_f16.hip", "ssd_kernels_bf16.hip", "ssd_kernels_f16_blk.hip", "ssd_kernels_bf16_blk.hip"]
+           + ["ssd_recur_%s.hip" % d for d in ("f32", "f16", "bf16")]
+           + ["ssd_linear_%s.hip" % d for d in ("f32", "f16", "bf16", "i8", "e4m3")]
            + ["ssd_kernels_%s_q%d%s.hip" % (d, q, v) for d in ("f16", "bf16") for q in (64, 128, 256)
               for v in ("", "_vl")])
 

@@ -91,7 +91,7 @@ struct RecurArgs {
     const void* h0;
     void* out;
     void* fin;
-    float* saved;  // [batch][tiles][channels]: the state entering each tile of kRecurTile tokens
+    float* saved;  // [batch][kept][channels]: the state entering every kRecurSaved tokens
     // backward
     const void* dout;
     const void* dfin;
@@ -100,9 +100,10 @@ struct RecurArgs {
     void* dig;
     void* dh0;
     float* part;  // [batch][tiles][3][channels]: dA, dgate_bias, din_bias
-    // with more than one tile: what each does to the state (or its gradient), and how many workgroups have started
-    uint64_t* hops;  // [batch][tiles][channels]
-    uint32_t* ticket;
+    // with more than one tile: what each does to the state (or its gradient), and how many workgroups of each chain of
+    // tiles have started
+    uint64_t* hops;     // [batch][tiles][channels]
+    uint32_t* tickets;  // [batch][blocks][kTicketWords]
     // step
     void* pool;
     const int32_t* slots;
@@ -110,8 +111,11 @@ struct RecurArgs {
     int ntiles;
     int64_t xs, gs, is;
 };
-constexpr int kRecurTile = 128;  // tokens of a tile
-int64_t recur_tiles(int64_t seqlen);
+constexpr int kTicketWords = 32;  // counters on lines of their own
+constexpr int kRecurTile = 128;  // tokens of a tile of the forward pass
+constexpr int kRecurSaved = 64;  // tokens between two kept states: a tile of the backward pass
+constexpr int64_t recur_kept(int64_t seqlen) { return (seqlen + kRecurSaved - 1) / kRecurSaved; }
+int64_t recur_tiles(int64_t seqlen, bool backward);
 int64_t recur_blocks(int64_t channels, int in_dtype);  // workgroups of a tile of one batch row
 
 hipError_t launch_recur(RecurArgs& a, int in_dtype, hipStream_t st);

@@ -378,7 +378,7 @@ ssd_status_t validate_recurrence(const ssd_recurrence_params_t* p, bool step) {
     if (!step && (p->x_stride >= kMaxRecRow || p->gate_stride >= kMaxRecRow || p->in_stride >= kMaxRecRow))
         return SSD_ERR_INVALID_SHAPE;
     if (step) return (int64_t)p->batch * D >= kMaxLanes ? SSD_ERR_INVALID_SHAPE : SSD_OK;
-    const int64_t groups = ssd::recur_blocks(D, p->in_dtype) * p->batch * ssd::recur_tiles(p->seqlen);
+    const int64_t groups = ssd::recur_blocks(D, p->in_dtype) * p->batch * ssd::recur_tiles(p->seqlen, true);
     return groups >= kMaxLanes / 512 ? SSD_ERR_INVALID_SHAPE : SSD_OK;
 }
 
@@ -388,11 +388,11 @@ struct RecLayout {
 
 RecLayout rec_layout(const ssd_recurrence_params_t* p, bool backward) {
     RecLayout l{};
-    const size_t tiles = ssd::recur_tiles(p->seqlen), n = p->batch * tiles * p->channels;
+    const size_t tiles = ssd::recur_tiles(p->seqlen, backward), n = p->batch * tiles * p->channels;
     Regions r;
     if (tiles > 1) {
         l.hops_off = r.add(n * 8);
-        l.ticket_off = r.add(4);
+        l.ticket_off = r.add((size_t)p->batch * ssd::recur_blocks(p->channels, p->in_dtype) * ssd::kTicketWords * 4);
     }
     if (backward) l.part_off = r.add(3 * n * 4);
     l.total = r.size();
@@ -420,10 +420,10 @@ ssd::RecurArgs rec_args(const ssd_recurrence_params_t* p, const void* x, const v
     return a;
 }
 
-void rec_space(ssd::RecurArgs& a, const ssd_recurrence_params_t* p, const RecLayout& l, char* ws) {
-    a.ntiles = (int)ssd::recur_tiles(p->seqlen);
+void rec_space(ssd::RecurArgs& a, const ssd_recurrence_params_t* p, const RecLayout& l, char* ws, bool backward) {
+    a.ntiles = (int)ssd::recur_tiles(p->seqlen, backward);
     a.hops = (uint64_t*)(ws + l.hops_off);
-    a.ticket = (uint32_t*)(ws + l.ticket_off);
+    a.tickets = (uint32_t*)(ws + l.ticket_off);
     a.part = (float*)(ws + l.part_off);
 }
 
@@ -452,7 +452,7 @@ SSD_EXPORT size_t ssd_gated_recurrence_backward_workspace_size(const ssd_recurre
 
 SSD_EXPORT size_t ssd_gated_recurrence_saved_size(const ssd_recurrence_params_t* p) {
     if (validate_recurrence(p, false) != SSD_OK) return 0;
-    return (size_t)p->batch * ssd::recur_tiles(p->seqlen) * p->channels * 4;
+    return (size_t)p->batch * ssd::recur_kept(p->seqlen) * p->channels * 4;
 }
 
 SSD_EXPORT ssd_status_t ssd_gated_recurrence(const ssd_recurrence_params_t* p, const void* x, const void* gate, const float* A,
@@ -474,7 +474,7 @@ SSD_EXPORT ssd_status_t ssd_gated_recurrence(const ssd_recurrence_params_t* p, c
     const RecLayout l = rec_layout(p, false);
     if (workspace_bytes < l.total) return SSD_ERR_WORKSPACE_TOO_SMALL;
     ssd::RecurArgs a = rec_args(p, x, gate, A, in_gate, gate_bias, in_bias);
-    rec_space(a, p, l, (char*)workspace);
+    rec_space(a, p, l, (char*)workspace, false);
     a.seq = seq_idx;
     a.h0 = initial_state;
     a.out = out;
@@ -504,7 +504,7 @@ SSD_EXPORT ssd_status_t ssd_gated_recurrence_backward(
     const RecLayout l = rec_layout(p, true);
     if (workspace_bytes < l.total) return SSD_ERR_WORKSPACE_TOO_SMALL;
     ssd::RecurArgs a = rec_args(p, x, gate, A, in_gate, gate_bias, in_bias);
-    rec_space(a, p, l, (char*)workspace);
+    rec_space(a, p, l, (char*)workspace, true);
     a.seq = seq_idx;
     a.h0 = initial_state;
     a.saved = (float*)const_cast<void*>(saved);

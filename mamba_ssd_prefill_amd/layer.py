@@ -22,7 +22,7 @@ tensors' device, no autograd graph, raised version counters.  The names are re-e
     g = linear_backward(dout, x, w, pre=pre, activation="silu", with_bias=True)         # g.dx, g.dweight, g.dbias
     g = rms_norm_backward(dout, s, norm_w, dresidual=ds)                 # g.dx, g.dresidual, g.dweight
 
-Training keeps for the recurrence a state in fp32 every 128 tokens, for a product with an activation ``pre``, for the norm
+Training keeps for the recurrence a state in fp32 every 64 tokens, for a product with an activation ``pre``, for the norm
 the sum that it returns.
 """
 import collections

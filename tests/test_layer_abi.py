@@ -244,7 +244,7 @@ def test_workspaces(lib, name, size, prm):
 
 def test_saved_states(lib):
     size = lib.ssd_gated_recurrence_saved_size
-    for L, tiles in ((1, 1), (128, 1), (129, 2), (1000, 8)):
+    for L, tiles in ((1, 1), (64, 1), (65, 2), (1000, 16)):
         assert size(ctypes.byref(rec_prm(seqlen=L))) == 2 * tiles * 64 * 4
 
 
