@@ -698,7 +698,7 @@ ssd_status_t ssd_linear_backward(const ssd_linear_params_t* p, const void* dout,
 typedef struct {
     size_t struct_size; /* sizeof(ssd_recurrence_params_t) */
     int batch;          /* B >= 1 */
-    int seqlen;         /* L >= 1, up to 2^31 - 1024 (1 for the step) */
+    int seqlen;         /* L >= 1 (1 for the step); B * ceil(L / 64) * ceil(D / 64) (fp32: D / 32) below 2^24 */
     int channels;       /* D >= 1, below 2^21 */
     int in_dtype;       /* ssd_dtype_t of x, gate, in_gate, out and their gradients */
     int state_dtype;    /* ssd_dtype_t of the states and their gradients (the recurrence runs in fp32) */

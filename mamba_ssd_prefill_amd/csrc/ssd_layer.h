@@ -112,6 +112,7 @@ struct RecurArgs {
     int64_t xs, gs, is;
 };
 constexpr int kTicketWords = 32;  // counters on lines of their own
+constexpr int kRecurWaves = 4;   // of a workgroup
 constexpr int kRecurTile = 128;  // tokens of a tile of the forward pass
 constexpr int kRecurSaved = 64;  // tokens between two kept states: a tile of the backward pass
 constexpr int64_t recur_kept(int64_t seqlen) { return (seqlen + kRecurSaved - 1) / kRecurSaved; }

@@ -363,7 +363,6 @@ SSD_EXPORT ssd_status_t ssd_linear_backward(const ssd_linear_params_t* p, const 
 namespace {
 
 constexpr int64_t kMaxRecRow = (int64_t)1 << 21;  // elements between rows: a tile's 128 rows have 31-bit offsets
-constexpr int64_t kMaxRecLen = kMaxIndex - 1024;  // tokens behind a row's end have numbers too
 
 ssd_status_t validate_recurrence(const ssd_recurrence_params_t* p, bool step) {
     if (!p) return SSD_ERR_NULL_POINTER;
@@ -372,14 +371,14 @@ ssd_status_t validate_recurrence(const ssd_recurrence_params_t* p, bool step) {
     if (p->batch < 1 || p->seqlen < 1 || p->channels < 1) return SSD_ERR_INVALID_SHAPE;
     if (step && (p->seqlen != 1 || p->nseq < 1)) return SSD_ERR_INVALID_SHAPE;
     const int64_t D = p->channels;
-    if (D >= kMaxRecRow || p->seqlen > kMaxRecLen || (int64_t)p->batch * p->seqlen >= kMaxIndex) return SSD_ERR_INVALID_SHAPE;
+    if (D >= kMaxRecRow || (int64_t)p->batch * p->seqlen >= kMaxIndex) return SSD_ERR_INVALID_SHAPE;
     if (!stride_ok(p->x_stride, D) || !stride_ok(p->gate_stride, D) || !stride_ok(p->in_stride, D))
         return SSD_ERR_INVALID_SHAPE;
     if (!step && (p->x_stride >= kMaxRecRow || p->gate_stride >= kMaxRecRow || p->in_stride >= kMaxRecRow))
         return SSD_ERR_INVALID_SHAPE;
     if (step) return (int64_t)p->batch * D >= kMaxLanes ? SSD_ERR_INVALID_SHAPE : SSD_OK;
     const int64_t groups = ssd::recur_blocks(D, p->in_dtype) * p->batch * ssd::recur_tiles(p->seqlen, true);
-    return groups >= kMaxLanes / 512 ? SSD_ERR_INVALID_SHAPE : SSD_OK;
+    return groups >= kMaxLanes / (64 * ssd::kRecurWaves) ? SSD_ERR_INVALID_SHAPE : SSD_OK;
 }
 
 struct RecLayout {

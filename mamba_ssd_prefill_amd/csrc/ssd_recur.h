@@ -24,10 +24,10 @@ namespace ssd {
 
 // Waves of a workgroup, tokens of a tile, waves that a SIMD is to hold (which bounds the registers).
 struct RecFwd {
-    static constexpr int W = 4, TILE = kRecurTile, EU = 3;
+    static constexpr int W = kRecurWaves, TILE = kRecurTile, EU = 3;
 };
 struct RecBwd {
-    static constexpr int W = 4, TILE = kRecurSaved, EU = 2;
+    static constexpr int W = kRecurWaves, TILE = kRecurSaved, EU = 2;
 };
 // Lanes of a row of 128 bytes, runs of a wave, tokens of a run, by the element size.
 template <typename T, typename D> struct RecGeo {

@@ -182,9 +182,11 @@ def test_recurrence_sizes_past_a_tile_s_offsets(lib, name):
         assert call(lib, name, rec_prm(**{f: 1 << 21})) == SHAPE
         assert call(lib, name, rec_prm(**{f: (1 << 21) - 1}), ws_bytes=0) == WS_SMALL
         assert call(lib, "ssd_gated_recurrence_step", params_for("ssd_gated_recurrence_step", **{f: 1 << 21}), slots=FAKE + 2) == MISAL
-    assert call(lib, name, rec_prm(batch=1, seqlen=2**31 - 1023, channels=1)) == SHAPE
-    assert call(lib, name, rec_prm(batch=1, seqlen=2**31 - 1024, channels=1), ws_bytes=0) == WS_SMALL
-    assert call(lib, name, rec_prm(batch=1 << 18, channels=(1 << 21) - 1)) == SHAPE  # workgroups
+    # workgroups of 256 lanes: one for 64 tokens and 128 bytes of channels
+    for t, ch in ((0, 32), (1, 64), (2, 64)):
+        assert call(lib, name, rec_prm(batch=1, seqlen=(1 << 30) - 64, channels=ch, in_dtype=t), ws_bytes=0) == WS_SMALL
+        assert call(lib, name, rec_prm(batch=1, seqlen=(1 << 30) - 63, channels=1, in_dtype=t)) == SHAPE
+        assert call(lib, name, rec_prm(batch=1, seqlen=1 << 29, channels=ch + 1, in_dtype=t)) == SHAPE
 
 
 def test_recurrence_step_lanes(lib):
