@@ -64,7 +64,8 @@ struct PackArgs {
     void* dst;        // [rows][kp], or transposed: [cols][kp] with kp >= rows
     int64_t rows, cols, stride, kp;
 };
-hipError_t launch_pack(PackArgs& a, int elem_bytes, bool transposed, hipStream_t st);
+// Two operands' in one launch (dst NULL: none).  Transposed: 2 or 4 bytes.
+hipError_t launch_pack(PackArgs& a, PackArgs& b, int elem_bytes, bool transposed, hipStream_t st);
 
 // dpre = dout act'(pre), as rows of np >= N values and transposed with rows of mp >= M (either NULL: not wanted), and its
 // sums over stretches of 64 rows.

@@ -156,9 +156,11 @@ ssd_status_t validate_linear(const ssd_linear_params_t* p, bool backward) {
     const int64_t M = p->rows, K = p->width, N = p->outs;
     if (padded(K, es) * (int64_t)es >= kMaxRowBytes) return SSD_ERR_INVALID_SHAPE;
     if (p->in_dtype == SSD_IN_INT8 && K > kMaxInt8Width) return SSD_ERR_UNSUPPORTED;
-    // lanes of the product (256 for 64 x 64 outputs at least) and of the copies (256 for 64 x 64 values)
+    // lanes of the product (512 for 256 x 256 outputs) and of the gradient behind the activation (256 for 64 x 64), of the
+    // operands' copies (one for 16 bytes of either, in one launch) and transposed copies (256 for 64 x 64 of either)
     const int64_t most = kMaxLanes / 256, mb = (M + 63) / 64, nb = (N + 63) / 64, kb = (K + 63) / 64 + 1;
-    if (mb * nb >= most || mb * kb >= most || nb * kb >= most) return SSD_ERR_INVALID_SHAPE;
+    if (mb * nb >= most || mb * kb >= most || nb * kb >= most || (mb + nb) * kb >= most) return SSD_ERR_INVALID_SHAPE;
+    if ((M + N) * (padded(K, es) * (int64_t)es / 16) >= kMaxLanes - 256) return SSD_ERR_INVALID_SHAPE;
     if (backward && (padded(N, es) * (int64_t)es >= kMaxRowBytes || padded(M, es) * (int64_t)es >= kMaxRowBytes))
         return SSD_ERR_INVALID_SHAPE;
     return SSD_OK;
@@ -191,12 +193,6 @@ LinearLayout linear_layout(const ssd_linear_params_t* p) {
     return l;
 }
 
-hipError_t pack(const void* src, void* dst, int64_t rows, int64_t cols, int64_t stride, int64_t kp, size_t es,
-                bool transposed, hipStream_t st) {
-    ssd::PackArgs a{src, dst, rows, cols, stride, kp};
-    return ssd::launch_pack(a, (int)es, transposed, st);
-}
-
 }  // namespace
 
 SSD_EXPORT size_t ssd_linear_workspace_size(const ssd_linear_params_t* p) {
@@ -221,17 +217,20 @@ SSD_EXPORT ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, 
     const hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
     int64_t xs = p->x_stride ? p->x_stride : p->width, wstr = p->width;
+    ssd::PackArgs px{}, pw{};
     if (l.pack_x || !aligned(x, 16)) {
-        const hipError_t e = pack(x, ws + l.x_off, p->rows, p->width, xs, l.kp, es, false, st);
-        if (e != hipSuccess) return hip_status(e);
-        x = ws + l.x_off;
+        px = ssd::PackArgs{x, ws + l.x_off, p->rows, p->width, xs, l.kp};
+        x = px.dst;
         xs = l.kp;
     }
     if (l.pack_w) {
-        const hipError_t e = pack(weight, ws + l.w_off, p->outs, p->width, p->width, l.kp, es, false, st);
-        if (e != hipSuccess) return hip_status(e);
-        weight = ws + l.w_off;
+        pw = ssd::PackArgs{weight, ws + l.w_off, p->outs, p->width, p->width, l.kp};
+        weight = pw.dst;
         wstr = l.kp;
+    }
+    if (px.dst || pw.dst) {
+        const hipError_t e = ssd::launch_pack(px, pw, (int)es, false, st);
+        if (e != hipSuccess) return hip_status(e);
     }
     ssd::LinearArgs a{};
     a.x = x;
@@ -326,33 +325,36 @@ SSD_EXPORT ssd_status_t ssd_linear_backward(const ssd_linear_params_t* p, const 
         const hipError_t e = ssd::launch_dpre(d, p->in_dtype, dbias, st);
         if (e != hipSuccess) return hip_status(e);
     }
+    ssd::PackArgs wt{}, xt{};
+    if (dx) wt = ssd::PackArgs{weight, ws + l.wt_off, N, K, K, l.np};
+    if (dweight) xt = ssd::PackArgs{x, ws + l.xt_off, M, K, p->x_stride ? p->x_stride : K, l.mp};
+    if (dx || dweight) {
+        const hipError_t e = ssd::launch_pack(wt, xt, (int)es, true, st);
+        if (e != hipSuccess) return hip_status(e);
+    }
     ssd::LinearArgs a{};
     a.part = (float*)(ws + l.part_off);
     a.out_dtype = p->in_dtype;
     a.N = p->width;
     a.rs = K;
     if (dx) {
-        hipError_t e = pack(weight, ws + l.wt_off, N, K, K, l.np, es, true, st);
-        if (e != hipSuccess) return hip_status(e);
         a.x = rows ? ws + l.rows_off : dout;
-        a.w = ws + l.wt_off;
+        a.w = wt.dst;
         a.xs = a.ws = l.np * es;
         a.kbytes = (int)(l.np * es);
         a.M = p->rows;
         a.out = dx;
-        e = ssd::launch_linear(a, p->in_dtype, l.dx_plan, st);
+        const hipError_t e = ssd::launch_linear(a, p->in_dtype, l.dx_plan, st);
         if (e != hipSuccess) return hip_status(e);
     }
     if (dweight) {
-        hipError_t e = pack(x, ws + l.xt_off, M, K, p->x_stride ? p->x_stride : K, l.mp, es, true, st);
-        if (e != hipSuccess) return hip_status(e);
         a.x = ws + l.cols_off;
-        a.w = ws + l.xt_off;
+        a.w = xt.dst;
         a.xs = a.ws = l.mp * es;
         a.kbytes = (int)(l.mp * es);
         a.M = p->outs;
         a.out = dweight;
-        e = ssd::launch_linear(a, p->in_dtype, l.dw_plan, st);
+        const hipError_t e = ssd::launch_linear(a, p->in_dtype, l.dw_plan, st);
         if (e != hipSuccess) return hip_status(e);
     }
     return SSD_OK;

@@ -27,21 +27,21 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 template <int TYPE> struct Mul;
 template <> struct Mul<LT_BF16> {
     typedef f32x4 Acc;
-    static constexpr int PIECES = 1;
+    static constexpr int PIECES = 1, ISSUES = 1;
     __device__ static inline void run(const u32x4 (&w)[1], const u32x4 (&x)[1], Acc& c) {
         c = TT<__bf16>::mma(__builtin_bit_cast(bf16x8, w[0]), __builtin_bit_cast(bf16x8, x[0]), c);
     }
 };
 template <> struct Mul<LT_F16> {
     typedef f32x4 Acc;
-    static constexpr int PIECES = 1;
+    static constexpr int PIECES = 1, ISSUES = 1;
     __device__ static inline void run(const u32x4 (&w)[1], const u32x4 (&x)[1], Acc& c) {
         c = TT<_Float16>::mma(__builtin_bit_cast(f16x8, w[0]), __builtin_bit_cast(f16x8, x[0]), c);
     }
 };
 template <> struct Mul<LT_F32> {
     typedef f32x4 Acc;
-    static constexpr int PIECES = 1;
+    static constexpr int PIECES = 1, ISSUES = 4;
     __device__ static inline void run(const u32x4 (&w)[1], const u32x4 (&x)[1], Acc& c) {
         const f32x4 a = __builtin_bit_cast(f32x4, w[0]), b = __builtin_bit_cast(f32x4, x[0]);
 #pragma unroll
@@ -50,14 +50,14 @@ template <> struct Mul<LT_F32> {
 };
 template <> struct Mul<LT_I8> {
     typedef i32x4 Acc;
-    static constexpr int PIECES = 1;
+    static constexpr int PIECES = 1, ISSUES = 1;
     __device__ static inline void run(const u32x4 (&w)[1], const u32x4 (&x)[1], Acc& c) {
         c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[0]), __builtin_bit_cast(i32x4, x[0]), c, 0, 0, 0);
     }
 };
 template <> struct Mul<LT_E4M3> {
     typedef f32x4 Acc;
-    static constexpr int PIECES = 2;
+    static constexpr int PIECES = 2, ISSUES = 1;
     __device__ static inline void run(const u32x4 (&w)[2], const u32x4 (&x)[2], Acc& c) {
         const i32x8 a = __builtin_shufflevector(__builtin_bit_cast(i32x4, w[0]), __builtin_bit_cast(i32x4, w[1]), 0, 1, 2, 3, 4, 5, 6, 7);
         const i32x8 b = __builtin_shufflevector(__builtin_bit_cast(i32x4, x[0]), __builtin_bit_cast(i32x4, x[1]), 0, 1, 2, 3, 4, 5, 6, 7);
@@ -86,8 +86,9 @@ __device__ inline float act_d(float v, int act) {
 }
 
 // C consecutive values of one row at element offset `off`, n of them existing; the type is a run-time one.
+template <int C, typename T> constexpr int piece_of() { return C % (16 / (int)sizeof(T)) == 0 ? 16 / (int)sizeof(T) : 4; }
 template <int C, typename T> __device__ inline void row_load_t(const void* p, int64_t off, int n, float (&v)[C]) {
-    constexpr int ONE = 16 / (int)sizeof(T) < C ? 16 / (int)sizeof(T) : C;
+    constexpr int ONE = piece_of<C, T>();
     typedef T Raw __attribute__((ext_vector_type(ONE), aligned(sizeof(T))));
     const T* q = (const T*)p + off;
 #pragma unroll
@@ -103,7 +104,7 @@ template <int C, typename T> __device__ inline void row_load_t(const void* p, in
     }
 }
 template <int C, typename T> __device__ inline void row_store_t(void* p, int64_t off, int n, const float (&v)[C]) {
-    constexpr int ONE = 16 / (int)sizeof(T) < C ? 16 / (int)sizeof(T) : C;
+    constexpr int ONE = piece_of<C, T>();
     typedef T Raw __attribute__((ext_vector_type(ONE), aligned(sizeof(T))));
     T* q = (T*)p + off;
 #pragma unroll
@@ -177,20 +178,40 @@ template <int C> struct Columns {
     }
 };
 
+// At most N of this wave's memory accesses on their way (bits 3:0 and 15:14 of the instruction's operand; the other counters
+// unwatched).
+template <int N> __device__ inline void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0f70);
+}
+
+// This wave's reads of LDS are done.
+__device__ inline void wait_reads() { __builtin_amdgcn_s_waitcnt(0xc07f); }
+// A barrier that waits for nothing else (__syncthreads waits for all loads).
+__device__ inline void barrier_only() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // ---- tiles ----------------------------------------------------------------------------------------
 constexpr uint32_t kNoPiece = 0x80000000u;  // an offset past every operand's buffer: reads as zeros
 
 // BM x BN outputs a workgroup, WVM x WVN waves.
-template <int TYPE, int BM, int BN, int WVM, int WVN> struct LinearTile {
+template <int TYPE, int BM, int BN, int WVM, int WVN, int S> struct LinearTile {
     static constexpr int NW = WVM * WVN, THREADS = 64 * NW, MB = BM / WVM / 16, NB = BN / WVN / 16;
     static constexpr int STEP = 128;  // bytes of a row
     static constexpr int RPI = 8 * NW;  // rows that one load of every lane brings
-    static constexpr int IX = BM / RPI, IW = BN / RPI;
-    static constexpr int STAGE = (BM + BN) * STEP, LDS = 2 * STAGE;
-    static constexpr int SH = __builtin_ctz(4 * NB);
-    static_assert(BM % RPI == 0 && BN % RPI == 0, "rows of a load");
+    static constexpr int IX = (BM + RPI - 1) / RPI, IW = (BN + RPI - 1) / RPI;  // (the last one by some waves, which others repeat)
+    static constexpr int LOADS = IX + IW;  // of a lane for a step
+    static constexpr int STAGE = (BM + BN) * STEP, LDS = S * STAGE;
+    static_assert((S - 2) * LOADS < 64, "loads on their way are counted in six bits");
+    static_assert(BM % (16 * WVM) == 0 && BN % (16 * WVN) == 0 && LDS <= 160 * 1024, "blocks of a wave");
+    // the first of the 8 rows that a wave brings with load j of a tile's ROWS
+    template <int ROWS> __device__ static inline int load_row(int j, int wave) {
+        return (j + 1) * RPI <= ROWS ? j * RPI + wave * 8 : j * RPI + wave % ((ROWS - j * RPI) / 8) * 8;
+    }
     __device__ static inline int swz_x(int row) { return (row >> 1) & 7; }
-    __device__ static inline int swz_w(int row) { return (row >> 1 & 1) | (row >> SH & 3) << 1; }
+    __device__ static inline int swz_w(int row) { return (row >> 1 & 1) | (row / (4 * NB) & 3) << 1; }
 };
 
 // Where a lane's pieces come from and go to: rows behind the last one repeat it.
@@ -198,41 +219,92 @@ template <typename G, int BM, int BN> struct Loads {
     __amdgpu_buffer_rsrc_t rx, rw;
     char* lds;
     uint32_t kbytes, ox[G::IX], ow[G::IW], cx[G::IX], cw[G::IW];
+    int tx[G::IX], tw[G::IW];  // where a wave's rows go
     __device__ inline Loads(const LinearArgs& a, char* to, int m0, int n0, int wave, int lane) {
         rx = make_rsrc((const char*)a.x + (int64_t)m0 * a.xs, 0x7fffffffu);
         rw = make_rsrc((const char*)a.w + (int64_t)n0 * a.ws, 0x7fffffffu);
-        lds = to + wave * 1024;
+        lds = to;
         kbytes = (uint32_t)a.kbytes;
 #pragma unroll
         for (int j = 0; j < G::IX; ++j) {
-            const int row = j * G::RPI + wave * 8 + (lane >> 3);
+            tx[j] = G::template load_row<BM>(j, wave) * G::STEP;
+            const int row = G::template load_row<BM>(j, wave) + (lane >> 3);
             cx[j] = (uint32_t)((lane & 7) ^ G::swz_x(row)) * 16;
             ox[j] = (uint32_t)min(row, a.M - 1 - m0) * (uint32_t)a.xs + cx[j];
         }
 #pragma unroll
         for (int j = 0; j < G::IW; ++j) {
-            const int row = j * G::RPI + wave * 8 + (lane >> 3);
+            tw[j] = (BM + G::template load_row<BN>(j, wave)) * G::STEP;
+            const int row = G::template load_row<BN>(j, wave) + (lane >> 3);
             cw[j] = (uint32_t)((lane & 7) ^ G::swz_w(row)) * 16;
             ow[j] = (uint32_t)min(row, a.N - 1 - n0) * (uint32_t)a.ws + cw[j];
         }
     }
-    __device__ inline void issue(int step) const {
+    __device__ inline void issue(int step, int place) const {
         const uint32_t k = (uint32_t)step * G::STEP, left = kbytes - k;
-        char* to = lds + (step & 1) * G::STAGE;
+        char* to = lds + place * G::STAGE;
 #pragma unroll
         for (int j = 0; j < G::IX; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, SSD_LDS_PTR(void, to + j * G::RPI * G::STEP), 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, SSD_LDS_PTR(void, to + tx[j]), 16,
                                                      cx[j] < left ? ox[j] + k : kNoPiece, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < G::IW; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, SSD_LDS_PTR(void, to + (BM + j * G::RPI) * G::STEP), 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, SSD_LDS_PTR(void, to + tw[j]), 16,
                                                      cw[j] < left ? ow[j] + k : kNoPiece, 0, 0, 0);
     }
 };
 
-template <int TYPE, int BM, int BN, int WVM, int WVN>
-__global__ __launch_bounds__(64 * WVM * WVN) void k_linear(LinearArgs a) {
-    typedef LinearTile<TYPE, BM, BN, WVM, WVN> G;
+// The order of a stretch of instructions: READS reads of LDS spread over the first MULS matrix instructions; the same with
+// LOADS loads to LDS before them.  (As written, all of them would be issued before the first matrix instruction, by every
+// wave of a SIMD at the same time.)
+template <int READS, int MULS> __device__ inline void reads_among() {
+    constexpr int PER = MULS / READS > 0 ? MULS / READS : 1;
+#pragma unroll
+    for (int i = 0; i < READS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, MULS, 0);
+}
+template <int LOADS, int READS, int MULS> __device__ inline void loads_among() {
+    constexpr int PER = MULS / (READS + LOADS) > 0 ? MULS / (READS + LOADS) : 1;
+#pragma unroll
+    for (int i = 0; i < READS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, MULS, 0);
+}
+
+// A half step's fragments of a wave's blocks, or a whole step's where an instruction takes two pieces.
+template <typename G, typename M> struct Frags {
+    u32x4 x[G::MB][M::PIECES], w[G::NB][M::PIECES];
+    __device__ inline void read(const char* px, const char* pw, int xrow, int wrow, int half, int q) {
+#pragma unroll
+        for (int p = 0; p < M::PIECES; ++p) {
+            const int c = (M::PIECES == 2 ? p : half) * 4 + q;
+#pragma unroll
+            for (int i = 0; i < G::NB; ++i) w[i][p] = *(const u32x4*)(pw + i * 4 * G::STEP + (c ^ G::swz_w(wrow + i * 4)) * 16);
+#pragma unroll
+            for (int j = 0; j < G::MB; ++j) x[j][p] = *(const u32x4*)(px + j * 16 * G::STEP + (c ^ G::swz_x(xrow + j * 16)) * 16);
+        }
+    }
+    __device__ inline void multiply(typename M::Acc (&acc)[G::NB][G::MB]) const {
+#pragma unroll
+        for (int i = 0; i < G::NB; ++i)
+#pragma unroll
+            for (int j = 0; j < G::MB; ++j) M::run(w[i], x[j], acc[i][j]);
+    }
+};
+
+template <int TYPE, int BM, int BN, int WVM, int WVN, int S>
+__global__ __launch_bounds__(64 * WVM * WVN, 2) void k_linear(LinearArgs a) {
+    typedef LinearTile<TYPE, BM, BN, WVM, WVN, S> G;
     typedef Mul<TYPE> M;
     extern __shared__ __align__(1024) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -258,34 +330,67 @@ __global__ __launch_bounds__(64 * WVM * WVN) void k_linear(LinearArgs a) {
     const int wm = wave % WVM, wn = wave / WVM, l16 = lane & 15, q = lane >> 4;
     // this lane's row of its wave's first block, and the piece it starts with
     const int xrow = wm * G::MB * 16 + l16, wrow = wn * G::NB * 16 + (l16 >> 2) * 4 * G::NB + (l16 & 3);
-    if (s0 < s1) loads.issue(s0);
-    for (int step = s0; step < s1; ++step) {
-        __builtin_amdgcn_s_waitcnt(0x0f70);  // this wave's loads are there; behind the barrier everyone's
-        __syncthreads();
-        if (step + 1 < s1) loads.issue(step + 1);
-        const char* tx = lds + (step & 1) * G::STAGE;
-        const char* tw = tx + BM * G::STEP;
+    const char* const px = lds + xrow * G::STEP;
+    const char* const pw = lds + (BM + wrow) * G::STEP;
+    if constexpr (M::PIECES == 2 || (S <= 3 && G::NW == 4)) {
+        // One set of fragments, waves that wait while others multiply.
 #pragma unroll
-        for (int kk = 0; kk < 2 / M::PIECES; ++kk) {
-            u32x4 fx[G::MB][M::PIECES], fw[G::NB][M::PIECES];
+        for (int i = 0; i < S - 1; ++i)
+            if (s0 + i < s1) loads.issue(s0 + i, i);
+        for (int step = s0, place = 0; step < s1; ++step) {
+            if (S > 2 && step + S - 2 < s1)
+                wait_loads<(S - 2) * G::LOADS>();
+            else
+                wait_loads<0>();
+            barrier_only();
+            if (step + S - 1 < s1) loads.issue(step + S - 1, place == 0 ? S - 1 : place - 1);
+            const char *tx = px + place * G::STAGE, *tw = pw + place * G::STAGE;
 #pragma unroll
-            for (int p = 0; p < M::PIECES; ++p) {
-                const int c = (M::PIECES == 2 ? p : kk) * 4 + q;
-#pragma unroll
-                for (int i = 0; i < G::NB; ++i) {
-                    const int row = wrow + i * 4;
-                    fw[i][p] = *(const u32x4*)(tw + row * G::STEP + (c ^ G::swz_w(row)) * 16);
-                }
-#pragma unroll
-                for (int j = 0; j < G::MB; ++j) {
-                    const int row = xrow + j * 16;
-                    fx[j][p] = *(const u32x4*)(tx + row * G::STEP + (c ^ G::swz_x(row)) * 16);
-                }
+            for (int h = 0; h < 2 / M::PIECES; ++h) {
+                Frags<G, M> f;
+                f.read(tx, tw, xrow, wrow, h, q);
+                f.multiply(acc);
             }
+            wait_reads();  // (the place is written again behind the next barrier)
+            place = place == S - 1 ? 0 : place + 1;
+        }
+    } else {
 #pragma unroll
-            for (int i = 0; i < G::NB; ++i)
-#pragma unroll
-                for (int j = 0; j < G::MB; ++j) M::run(fw[i], fx[j], acc[i][j]);
+        for (int i = 0; i < S; ++i)
+            if (s0 + i < s1) loads.issue(s0 + i, i);
+        Frags<G, M> f0, f1;
+        int step = s0, place = 0;
+        if (s0 + S <= s1) {
+            wait_loads<(S - 1) * G::LOADS>();
+            barrier_only();
+            f0.read(px, pw, xrow, wrow, 0, q);
+            for (; step + S < s1; ++step) {
+                const int at = place * G::STAGE, next = place == S - 1 ? 0 : place + 1;
+                f1.read(px + at, pw + at, xrow, wrow, 1, q);
+                f0.multiply(acc);
+                reads_among<G::MB + G::NB, G::MB * G::NB * M::ISSUES>();
+                // this wave has read all of the step, and its loads of the next one are there (those of the S - 2 behind it may be
+                // on their way): behind the barrier the same holds for every wave, and the step's place is free
+                wait_reads();
+                wait_loads<(S - 2) * G::LOADS>();
+                barrier_only();
+                loads.issue(step + S, place);
+                place = next;
+                f0.read(px + place * G::STAGE, pw + place * G::STAGE, xrow, wrow, 0, q);
+                f1.multiply(acc);
+                loads_among<G::LOADS, G::MB + G::NB, G::MB * G::NB * M::ISSUES>();
+            }
+        }
+        // the last S steps, or what there is
+        wait_loads<0>();
+        barrier_only();
+        for (; step < s1; ++step) {
+            const int at = place * G::STAGE;
+            f0.read(px + at, pw + at, xrow, wrow, 0, q);
+            f1.read(px + at, pw + at, xrow, wrow, 1, q);
+            f0.multiply(acc);
+            f1.multiply(acc);
+            place = place == S - 1 ? 0 : place + 1;
         }
     }
     constexpr int C = 4 * G::NB;
@@ -342,16 +447,26 @@ template <typename V> __global__ __launch_bounds__(256) void k_linear_join(Linea
     cols.finish(a, m, v);
 }
 
-template <int TYPE, int BM, int BN, int WVM, int WVN> hipError_t launch_tile(LinearArgs& a, hipStream_t st) {
-    typedef LinearTile<TYPE, BM, BN, WVM, WVN> G;
+template <int TYPE, int BM, int BN, int WVM, int WVN, int S = 2> hipError_t launch_tile(LinearArgs& a, hipStream_t st) {
+    typedef LinearTile<TYPE, BM, BN, WVM, WVN, S> G;
     const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
     void* args[] = {&a};
-    const void* fn = (const void*)&k_linear<TYPE, BM, BN, WVM, WVN>;
+    const void* fn = (const void*)&k_linear<TYPE, BM, BN, WVM, WVN, S>;
     return hipLaunchKernel(fn, dim3((unsigned)(tiles * a.splits)), dim3(G::THREADS), args, G::LDS, st);
 }
 
 template <int TYPE> hipError_t launch_linear_type(LinearArgs& a, const LinearPlan& p, hipStream_t st) {
-    hipError_t e = launch_tile<TYPE, 128, 128, 2, 2>(a, st);
+    hipError_t e;
+    switch (p.tile) {
+    case 0: e = launch_tile<TYPE, 128, 128, 2, 2>(a, st); break;
+    case 1: e = launch_tile<TYPE, 256, 256, 2, 4>(a, st); break;
+    case 2: e = launch_tile<TYPE, 128, 192, 2, 2>(a, st); break;
+    case 3: e = launch_tile<TYPE, 256, 160, 4, 2, TYPE == LT_E4M3 ? 2 : 3>(a, st); break;
+    case 4: e = launch_tile<TYPE, 256, 128, 4, 2, TYPE == LT_E4M3 ? 2 : 3>(a, st); break;
+    case 5: e = launch_tile<TYPE, 64, 128, 1, 4, 3>(a, st); break;
+    case 6: e = launch_tile<TYPE, 32, 64, 1, 4, 6>(a, st); break;
+    default: e = launch_tile<TYPE, 16, 64, 1, 4, 8>(a, st); break;
+    }
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t lanes = (int64_t)a.M * ((a.N + 3) / 4);
     void* args[] = {&a};

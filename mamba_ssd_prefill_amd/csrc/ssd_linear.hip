@@ -1,5 +1,7 @@
 // ssd_linear.hip -- what stands around the matrix product: the choice of tiles, rows that it cannot take as they are
 // copied into ones that it can, and dout act'(pre) for its gradients (ssd_linear / _backward in include/mamba_ssd.h).
+#include <math.h>
+
 #include "ssd_linear.h"
 #include "ssd_sum_rows.h"
 
@@ -11,14 +13,51 @@ hipError_t launch_linear_bf16(LinearArgs&, const LinearPlan&, hipStream_t);
 hipError_t launch_linear_i8(LinearArgs&, const LinearPlan&, hipStream_t);
 hipError_t launch_linear_e4m3(LinearArgs&, const LinearPlan&, hipStream_t);
 
+// The tile and the splits of the contraction by a model of the time, fitted to sweeps over 1 to 8192 rows at 2560 x
+// 10576, 5120 x 2560, 1024 x 4096, 4096 x 1024 and 8192 x 8192 (16-bit operands; it picks the fastest pair of the sweep or one
+// within 8 % of it):
+//   2.5 us + rounds (steps c + e),  and 4 us + 8 bytes a partial sum at 4 TB/s where the contraction is split,
+// c being the time of a step with 1, 2, .. workgroups a CU and e that of a tile's start and epilogue.  8192 x 5120 x 2560
+// takes 206 us in tiles of 256 x 160 (two full rounds of 256 CUs), 271 us in 256 x 256 and 248 us in 128 x 128; 16 x
+// 5120 x 2560 11.2 us in 16 x 64 split by 4, 19 us unsplit.  fp32 is bound by its matrix instructions, 16 times slower: c
+// goes by the area.
+namespace {
+struct TileModel {
+    int bm, bn, most;  // workgroups a CU
+    float c[2], e;
+};
+constexpr TileModel kTiles[] = {
+    {128, 128, 2, {0.75f, 0.90f}, 4.f}, {256, 256, 1, {1.67f, 0.f}, 6.f},    {128, 192, 2, {0.85f, 1.28f}, 5.f},
+    {256, 160, 1, {1.15f, 0.f}, 5.f},   {256, 128, 1, {0.88f, 0.f}, 5.f},    {64, 128, 2, {0.55f, 0.62f}, 3.f},
+    {32, 64, 2, {0.17f, 0.30f}, 2.f},   {16, 64, 2, {0.165f, 0.28f}, 2.f},
+};
+constexpr float kCUs = 256.f;
+}  // namespace
+
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type) {
-    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128), steps = (kbytes + 127) / 128;
-    int64_t s = tiles >= 256 ? 1 : 512 / tiles;
-    if (s > steps / 4) s = steps / 4;
-    if (s > 32) s = 32;
-    if (s < 1) s = 1;
-    const int64_t per = (steps + s - 1) / s;
-    return LinearPlan{0, (int)((steps + per - 1) / per)};  // none without a step
+    const int64_t steps = (kbytes + 127) / 128;
+    LinearPlan best{0, 1};
+    float least = 3.4e38f;
+    for (int t = 0; t < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
+        const TileModel& m = kTiles[t];
+        const int64_t tiles = ((M + m.bm - 1) / m.bm) * ((N + m.bn - 1) / m.bn);
+        for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            const int64_t per = (steps + splits - 1) / splits;
+            if (splits > 1 && (per < 4 || (steps + per - 1) / per != splits)) break;  // (none without a step)
+            if (tiles * splits >= ((int64_t)1 << 32) / 512) continue;  // (lanes of a launch; 256 x 256 always fits)
+            const float work = (float)(tiles * splits);
+            int o = 1;
+            while (o < m.most && work > kCUs * (float)o) ++o;
+            const float c = type == LT_F32 ? 1.95f * (float)o * (float)(m.bm * m.bn) / 16384.f : m.c[o - 1];
+            float us = ceilf(work / (kCUs * (float)o)) * ((float)per * c + m.e);
+            if (splits > 1) us += 4.f + (float)splits * (float)M * (float)N * 2e-6f;
+            if (us < least) {
+                least = us;
+                best = LinearPlan{t, splits};
+            }
+        }
+    }
+    return best;
 }
 
 hipError_t launch_linear(LinearArgs& a, int type, const LinearPlan& p, hipStream_t st) {
@@ -36,75 +75,152 @@ hipError_t launch_linear(LinearArgs& a, int type, const LinearPlan& p, hipStream
 }
 
 // ---- rows of another pitch, or transposed --------------------------------------------------------------
-// 64 x 64 values a workgroup.
-template <typename T, bool TRANSPOSED> __global__ __launch_bounds__(256) void k_pack(PackArgs a) {
-    __shared__ T tile[TRANSPOSED ? 64 : 1][TRANSPOSED ? 64 + 4 / (int)sizeof(T) : 1];
-    const int64_t cb = TRANSPOSED ? (a.cols + 63) / 64 : (a.kp + 63) / 64;
-    const int64_t r0 = (int64_t)(blockIdx.x / (uint32_t)cb) * 64, c0 = (int64_t)(blockIdx.x % (uint32_t)cb) * 64;
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-    if constexpr (!TRANSPOSED) {
+// V values of T as loaded (as integers of its size: nothing is computed with them).
+template <typename T> struct Piece {
+    static constexpr int V = 16 / (int)sizeof(T);
+    T v[V];
+    // n of them exist at p, the others are 0
+    __device__ inline void load(const T* p, int64_t n) {
+        typedef T Raw __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+        if (n >= V) {
+            const Raw r = *(const Raw*)p;
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-            const int64_t r = r0 + y + i, c = c0 + x;
-            if (r < a.rows && c < a.kp) ((T*)a.dst)[r * a.kp + c] = c < a.cols ? ((const T*)a.src)[r * a.stride + c] : (T)0;
-        }
-    } else {
+            for (int e = 0; e < V; ++e) v[e] = r[e];
+        } else {
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-            const int64_t r = r0 + y + i, c = c0 + x;
-            tile[y + i][x] = r < a.rows && c < a.cols ? ((const T*)a.src)[r * a.stride + c] : (T)0;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-            const int64_t c = c0 + y + i, r = r0 + x;
-            if (c < a.cols && r < a.kp) ((T*)a.dst)[c * a.kp + r] = tile[x][y + i];
+            for (int e = 0; e < V; ++e) v[e] = e < n ? p[e] : (T)0;
         }
     }
+    __device__ inline void store(T* p) const {  // 16-byte aligned
+        typedef T Raw __attribute__((ext_vector_type(V)));
+        Raw r;
+#pragma unroll
+        for (int e = 0; e < V; ++e) r[e] = v[e];
+        *(Raw*)p = r;
+    }
+};
+
+// Both operands' rows in one launch, a piece a lane.
+template <typename T> __global__ __launch_bounds__(256) void k_pack_rows(PackArgs a, PackArgs b, int64_t na) {
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const bool second = i >= na;
+    if (second) i -= na;
+    const PackArgs& p = second ? b : a;
+    const uint32_t per = (uint32_t)(p.kp / Piece<T>::V);
+    const int64_t r = i / per, c = i % per * Piece<T>::V;
+    if (r >= p.rows) return;
+    Piece<T> v;
+    v.load((const T*)p.src + r * p.stride + c, p.cols - c);
+    v.store((T*)p.dst + r * p.kp + c);
 }
 
-hipError_t launch_pack(PackArgs& a, int elem_bytes, bool transposed, hipStream_t st) {
-    const int64_t blocks = transposed ? ((a.kp + 63) / 64) * ((a.cols + 63) / 64) : ((a.rows + 63) / 64) * ((a.kp + 63) / 64);
-    const void* fn = elem_bytes == 4 ? (transposed ? (const void*)&k_pack<uint32_t, true> : (const void*)&k_pack<uint32_t, false>)
-                   : elem_bytes == 2 ? (transposed ? (const void*)&k_pack<uint16_t, true> : (const void*)&k_pack<uint16_t, false>)
-                                     : (transposed ? (const void*)&k_pack<uint8_t, true> : (const void*)&k_pack<uint8_t, false>);
-    void* args[] = {&a};
-    return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, st);
+// 64 x 64 values a workgroup, through LDS, both operands in one launch.
+template <typename T> struct Square {
+    static constexpr int V = Piece<T>::V, LPR = 64 / V, RPP = 256 / LPR, PASSES = 64 / RPP, PITCH = 64 + 4 / (int)sizeof(T);
+    T t[64][PITCH];
+    // rows r0.. of the transposed: this lane's pieces of columns c0.. of `rows` rows of kp values
+    __device__ inline void store_columns(T* dst, int64_t kp, int64_t c0, int64_t cols, int64_t r0) const {
+        const int x = (int)(threadIdx.x % LPR) * V, y = threadIdx.x / LPR;
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            const int64_t c = c0 + y + i * RPP;
+            if (c >= cols || r0 + x >= kp) continue;
+            Piece<T> p;
+#pragma unroll
+            for (int e = 0; e < V; ++e) p.v[e] = t[x + e][y + i * RPP];
+            p.store(dst + c * kp + r0 + x);
+        }
+    }
+};
+
+template <typename T> __global__ __launch_bounds__(256) void k_transpose(PackArgs a, PackArgs b, uint32_t na) {
+    typedef Square<T> S;
+    __shared__ S sq;
+    const bool second = blockIdx.x >= na;
+    const PackArgs& p = second ? b : a;
+    const uint32_t i = second ? blockIdx.x - na : blockIdx.x, cb = (uint32_t)((p.cols + 63) / 64);
+    const int64_t r0 = (int64_t)(i / cb) * 64, c0 = (int64_t)(i % cb) * 64;
+    const int x = (int)(threadIdx.x % S::LPR) * S::V, y = threadIdx.x / S::LPR;
+#pragma unroll
+    for (int k = 0; k < S::PASSES; ++k) {
+        const int64_t r = r0 + y + k * S::RPP, c = c0 + x;
+        Piece<T> v{};
+        if (r < p.rows && c < p.cols) v.load((const T*)p.src + r * p.stride + c, p.cols - c);
+#pragma unroll
+        for (int e = 0; e < S::V; ++e) sq.t[y + k * S::RPP][x + e] = v.v[e];
+    }
+    __syncthreads();
+    sq.store_columns((T*)p.dst, p.kp, c0, p.cols, r0);
+}
+
+hipError_t launch_pack(PackArgs& a, PackArgs& b, int elem_bytes, bool transposed, hipStream_t st) {
+    if (transposed) {
+        auto blocks = [](const PackArgs& p) { return p.dst ? (p.kp + 63) / 64 * ((p.cols + 63) / 64) : 0; };
+        uint32_t na = (uint32_t)blocks(a);
+        const void* fn = elem_bytes == 4 ? (const void*)&k_transpose<uint32_t> : (const void*)&k_transpose<uint16_t>;
+        void* args[] = {&a, &b, &na};
+        return hipLaunchKernel(fn, dim3((unsigned)(na + blocks(b))), dim3(256), args, 0, st);
+    }
+    auto lanes = [&](const PackArgs& p) { return p.dst ? p.rows * (p.kp / (16 / elem_bytes)) : 0; };
+    int64_t na = lanes(a);
+    const void* fn = elem_bytes == 4 ? (const void*)&k_pack_rows<uint32_t>
+                   : elem_bytes == 2 ? (const void*)&k_pack_rows<uint16_t> : (const void*)&k_pack_rows<uint8_t>;
+    void* args[] = {&a, &b, &na};
+    return hipLaunchKernel(fn, dim3((unsigned)((na + lanes(b) + 255) / 256)), dim3(256), args, 0, st);
 }
 
 // ---- dout act'(pre) -------------------------------------------------------------------------------------
 // 64 x 64 values a workgroup; the column sums come from the values before they are rounded.
 template <typename T> __global__ __launch_bounds__(256) void k_dpre(DpreArgs a) {
-    __shared__ T tile[64][64 + 4 / (int)sizeof(T)];
-    __shared__ float sums[256];
-    const int64_t cb = (a.N + 63) / 64;
-    const int64_t r0 = (int64_t)(blockIdx.x / (uint32_t)cb) * 64, c0 = (int64_t)(blockIdx.x % (uint32_t)cb) * 64;
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    typedef Square<T> S;
+    constexpr int V = S::V;
+    __shared__ S sq;
+    __shared__ float sums[S::RPP][64], quarters[256];
+    const uint32_t cb = (uint32_t)((a.N + 63) / 64);
+    const int64_t r0 = (int64_t)(blockIdx.x / cb) * 64, c0 = (int64_t)(blockIdx.x % cb) * 64;
+    const int x = (int)(threadIdx.x % S::LPR) * V, y = threadIdx.x / S::LPR;
     const int64_t c = c0 + x;
-    float s = 0.f;
+    float s[V];
 #pragma unroll
-    for (int i = 0; i < 64; i += 4) {
-        const int64_t r = r0 + y + i;
-        float v = 0.f;
+    for (int e = 0; e < V; ++e) s[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < S::PASSES; ++k) {
+        const int64_t r = r0 + y + k * S::RPP;
+        float v[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = 0.f;
         if (r < a.M && c < a.N) {
-            v = (float)((const T*)a.dout)[r * a.N + c];
-            if (a.act) v *= act_d((float)((const T*)a.pre)[r * a.N + c], a.act);
-        }
-        s += v;
-        const T o = (T)v;
-        if (a.rows && r < a.M && c < a.np) ((T*)a.rows)[r * a.np + c] = o;
-        if (a.cols) tile[y + i][x] = o;
-    }
-    sums[threadIdx.x] = s;
-    __syncthreads();
-    if (a.part && threadIdx.x < 64 && c < a.N)
-        a.part[(r0 / 64) * a.N + c] = (sums[x] + sums[64 + x]) + (sums[128 + x] + sums[192 + x]);
-    if (a.cols) {
+            const int n = (int)min(a.N - c, (int64_t)V);
+            row_load_t<V, T>(a.dout, r * a.N + c, n, v);
+            if (a.act) {
+                float p[V];
+                row_load_t<V, T>(a.pre, r * a.N + c, n, p);
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-            const int64_t n = c0 + y + i, m = r0 + x;
-            if (n < a.N && m < a.mp) ((T*)a.cols)[n * a.mp + m] = tile[x][y + i];
+                for (int e = 0; e < V; ++e)
+                    if (e < n) v[e] *= act_d(p[e], a.act);
+            }
         }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            s[e] += v[e];
+            if (a.cols) sq.t[y + k * S::RPP][x + e] = (T)v[e];
+        }
+        // (a padded pitch is the next multiple of a piece)
+        if (a.rows && r < a.M && c < a.np) row_store_t<V, T>(a.rows, r * a.np + c, V, v);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) sums[y][x + e] = s[e];
+    __syncthreads();
+    if (a.cols) sq.store_columns((T*)a.cols, a.mp, c0, a.N, r0);
+    if (a.part) {
+        const int col = threadIdx.x & 63, part = threadIdx.x >> 6;
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < S::RPP / 4; ++i) t += sums[part * (S::RPP / 4) + i][col];
+        quarters[threadIdx.x] = t;
+        __syncthreads();
+        if (threadIdx.x < 64 && c0 + col < a.N)
+            a.part[(r0 / 64) * a.N + c0 + col] = (quarters[col] + quarters[64 + col]) + (quarters[128 + col] + quarters[192 + col]);
     }
 }
 
@@ -117,8 +233,7 @@ __global__ __launch_bounds__(256) void k_dbias(const float* part, float* db, int
 }
 
 hipError_t launch_dpre(DpreArgs& a, int dtype, float* dbias, hipStream_t st) {
-    // (a padded column behind N lies in the last block of 64, a padded row behind M likewise: both pitches are the next
-    // multiple of at most 8)
+    // (padded columns behind N and padded rows behind M lie in the last blocks of 64)
     const int64_t blocks = ((a.M + 63) / 64) * ((a.N + 63) / 64);
     const void* fn = dtype == DT_F32 ? (const void*)&k_dpre<float>
                    : dtype == DT_F16 ? (const void*)&k_dpre<_Float16> : (const void*)&k_dpre<__bf16>;
