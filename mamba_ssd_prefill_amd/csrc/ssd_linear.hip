@@ -224,11 +224,11 @@ template <typename T> __global__ __launch_bounds__(256) void k_dpre(DpreArgs a) 
     }
 }
 
-__global__ __launch_bounds__(256) void k_dbias(const float* part, float* db, int parts, int64_t N) {
-    __shared__ float lds[256];
+__global__ __launch_bounds__(1024) void k_dbias(const float* part, float* db, int parts, int64_t N) {
+    __shared__ float lds[1024];
     const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
     const bool live = c < N;
-    const float s = sum_rows<float>(part + (live ? c : 0), N, parts, lds, live);
+    const float s = sum_many_rows<float>(part + (live ? c : 0), N, parts, lds, live);
     if (live && threadIdx.x < 64) db[c] = s;
 }
 
@@ -242,7 +242,7 @@ hipError_t launch_dpre(DpreArgs& a, int dtype, float* dbias, hipStream_t st) {
     if (e != hipSuccess || !dbias) return e;
     int parts = (int)((a.M + 63) / 64);
     void* sum_args[] = {&a.part, &dbias, &parts, &a.N};
-    return hipLaunchKernel((const void*)&k_dbias, dim3((unsigned)((a.N + 63) / 64)), dim3(256), sum_args, 0, st);
+    return hipLaunchKernel((const void*)&k_dbias, dim3((unsigned)((a.N + 63) / 64)), dim3(1024), sum_args, 0, st);
 }
 
 }  // namespace ssd

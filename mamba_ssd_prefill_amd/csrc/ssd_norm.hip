@@ -290,12 +290,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rms_norm_backward(Rms
     }
 }
 
-// dw from the workgroups' sums: 64 columns a workgroup.
-__global__ __launch_bounds__(256) void k_norm_dw(const float* part, float* dw, int parts, int width) {
-    __shared__ float lds[256];
+// dw from the workgroups' sums: 64 columns a workgroup.  (With 4 waves instead of 16, 1024 x 2560 sums took 14 us.)
+__global__ __launch_bounds__(1024) void k_norm_dw(const float* part, float* dw, int parts, int width) {
+    __shared__ float lds[1024];
     const int c = blockIdx.x * 64 + (threadIdx.x & 63);
     const bool live = c < width;
-    const float s = sum_rows<float>(part + (live ? c : 0), width, parts, lds, live);
+    const float s = sum_many_rows<float>(part + (live ? c : 0), width, parts, lds, live);
     if (live && threadIdx.x < 64) dw[c] = s;
 }
 
@@ -341,6 +341,7 @@ template <typename F> hipError_t by_type(int in_dtype, F f) {
 }
 }  // namespace
 
+constexpr int64_t kFewRows = 4096;
 constexpr int64_t kNormBlocks = 1 << 20;  // more rows are taken in turns
 
 int norm_parts(int64_t rows, int width, int in_dtype) {
@@ -352,7 +353,7 @@ hipError_t launch_rms_norm(RmsArgs& a, int in_dtype, hipStream_t st) {
     return by_type(in_dtype, [&](auto* t) {
         typedef __remove_pointer(decltype(t)) T;
         int W;
-        const void* fn = forward_kernel<T>(pieces_of(a.width, in_dtype), a.rows < 1024, W);
+        const void* fn = forward_kernel<T>(pieces_of(a.width, in_dtype), a.rows < kFewRows, W);
         int64_t grid = W == 1 ? (a.rows + 3) / 4 : a.rows;
         if (grid > kNormBlocks) grid = kNormBlocks;
         void* args[] = {&a};
@@ -370,7 +371,7 @@ hipError_t launch_rms_norm_backward(RmsArgs& a, int in_dtype, float* dw, hipStre
     });
     if (e != hipSuccess || !dw) return e;
     void* args[] = {&a.part, &dw, &a.parts, &a.width};
-    return hipLaunchKernel((const void*)&k_norm_dw, dim3((unsigned)((a.width + 63) / 64)), dim3(256), args, 0, st);
+    return hipLaunchKernel((const void*)&k_norm_dw, dim3((unsigned)((a.width + 63) / 64)), dim3(1024), args, 0, st);
 }
 
 }  // namespace ssd

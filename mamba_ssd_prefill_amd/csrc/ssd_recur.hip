@@ -27,27 +27,97 @@ __global__ __launch_bounds__(256) void k_recur_sums(const float* part, int parts
     if (to) to[c] = s;
 }
 
-// One token a row: a lane a (row, channel).
-template <typename T> __global__ __launch_bounds__(256) void k_recur_step(RecurArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)a.batch * a.channels) return;
-    const int b = (int)(i / a.channels), c = (int)(i % a.channels);
-    const int slot = a.slots ? a.slots[b] : b;
-    T* out = (T*)a.out + i;
-    if (slot < 0 || slot >= a.nseq) {
-        *out = (T)0.f;
-        return;
+// One token a row: a lane takes V channels of up to ROWS rows, whose parameters it reads once.
+template <typename T, int V> __device__ inline void step_load(const T* p, float (&v)[V]) {
+    typedef T Raw __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+    if constexpr (V == 1) {
+        v[0] = (float)*p;
+    } else {
+        const Raw r = *(const Raw*)p;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = (float)r[e];
     }
-    const float x = (float)((const T*)a.x)[b * a.xs + c], g = (float)((const T*)a.gate)[b * a.gs + c];
-    const float ig = a.ig ? (float)((const T*)a.ig)[b * a.is + c] : 0.f;
-    const int64_t at = (int64_t)slot * a.channels + c;
-    const RecParams p = rec_params(a, c, true);
-    const float r = gate_of(g, p.gb), d = __builtin_amdgcn_exp2f(p.A2 * r);
-    float u = a.ig ? x * gate_of(ig, p.ib) : x;
-    if (a.normalize) u *= beta_of(p.Am * r, d);
-    const float h = __builtin_fmaf(d, state_at(a.pool, a.state_dtype, at), u);
-    state_to(a.pool, a.state_dtype, at, h);
-    *out = (T)h;
+}
+template <typename T, int V> __device__ inline void step_store(T* p, const float (&v)[V]) {
+    typedef T Raw __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+    if constexpr (V == 1) {
+        *p = (T)v[0];
+    } else {
+        Raw r;
+#pragma unroll
+        for (int e = 0; e < V; ++e) r[e] = (T)v[e];
+        *(Raw*)p = r;
+    }
+}
+template <int V> __device__ inline void state_load(const void* p, int dtype, int64_t i, float (&v)[V]) {
+    if (dtype == DT_F32)
+        step_load<float, V>((const float*)p + i, v);
+    else if (dtype == DT_F16)
+        step_load<_Float16, V>((const _Float16*)p + i, v);
+    else
+        step_load<__bf16, V>((const __bf16*)p + i, v);
+}
+template <int V> __device__ inline void state_store(void* p, int dtype, int64_t i, const float (&v)[V]) {
+    if (dtype == DT_F32)
+        step_store<float, V>((float*)p + i, v);
+    else if (dtype == DT_F16)
+        step_store<_Float16, V>((_Float16*)p + i, v);
+    else
+        step_store<__bf16, V>((__bf16*)p + i, v);
+}
+template <typename T, int V, int ROWS> __global__ __launch_bounds__(256) void k_recur_step(RecurArgs a) {
+    const uint32_t per = (uint32_t)a.channels / V;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int c = (int)(i % per) * V, b0 = (int)(i / per) * ROWS;
+    if (b0 >= a.batch) return;
+    float x[ROWS][V], g[ROWS][V], ig[ROWS][V], h[ROWS][V];
+    int slot[ROWS];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        const int b = min(b0 + k, a.batch - 1);
+        slot[k] = a.slots ? a.slots[b] : b;
+    }
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        const int64_t b = min(b0 + k, a.batch - 1);
+        step_load<T, V>((const T*)a.x + b * a.xs + c, x[k]);
+        step_load<T, V>((const T*)a.gate + b * a.gs + c, g[k]);
+        if (a.ig) step_load<T, V>((const T*)a.ig + b * a.is + c, ig[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k)
+        if (slot[k] >= 0 && slot[k] < a.nseq) state_load<V>(a.pool, a.state_dtype, (int64_t)slot[k] * a.channels + c, h[k]);
+    RecParams p[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) p[e] = rec_params(a, c + e, true);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        if (b0 + k >= a.batch) break;
+        T* out = (T*)a.out + (int64_t)(b0 + k) * a.channels + c;
+        if (slot[k] < 0 || slot[k] >= a.nseq) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) out[e] = (T)0.f;
+            continue;
+        }
+        float r[V], u[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            r[e] = gate_of(g[k][e], p[e].gb);
+            u[e] = x[k][e];
+        }
+        if (a.ig) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) u[e] *= gate_of(ig[k][e], p[e].ib);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float d = __builtin_amdgcn_exp2f(p[e].A2 * r[e]);
+            if (a.normalize) u[e] *= beta_of(p[e].Am * r[e], d);
+            h[k][e] = __builtin_fmaf(d, h[k][e], u[e]);
+        }
+        state_store<V>(a.pool, a.state_dtype, (int64_t)slot[k] * a.channels + c, h[k]);
+        step_store<T, V>(out, h[k]);
+    }
 }
 
 int64_t recur_tiles(int64_t seqlen, bool backward) {
@@ -84,12 +154,25 @@ hipError_t launch_recur_backward(RecurArgs& a, int in_dtype, float* dA, float* d
     return hipLaunchKernel((const void*)&k_recur_sums, dim3((unsigned)((3 * (int64_t)a.channels + 63) / 64)), dim3(256), args, 0, st);
 }
 
-hipError_t launch_recur_step(RecurArgs& a, int in_dtype, hipStream_t st) {
-    const int64_t n = (int64_t)a.batch * a.channels;
-    const void* fn = in_dtype == DT_F32 ? (const void*)&k_recur_step<float>
-                   : in_dtype == DT_F16 ? (const void*)&k_recur_step<_Float16> : (const void*)&k_recur_step<__bf16>;
+// Two channels a lane where their number is even, and four rows where that leaves 512 workgroups (256 x 5120, bf16: 7.9 us, one row
+// 8.2, four channels 9.2 us).
+template <typename T> static hipError_t launch_step_t(RecurArgs& a, hipStream_t st) {
+    const int v = a.channels % 2 ? 1 : 2;
+    const int64_t lanes = (int64_t)a.batch * (a.channels / v);
+    const bool four = lanes / 4 >= 512 * 256;
+    const void* fn = v == 2 ? (four ? (const void*)&k_recur_step<T, 2, 4> : (const void*)&k_recur_step<T, 2, 1>)
+                            : (four ? (const void*)&k_recur_step<T, 1, 4> : (const void*)&k_recur_step<T, 1, 1>);
+    const int64_t n = (four ? ((int64_t)a.batch + 3) / 4 : a.batch) * (int64_t)(a.channels / v);
     void* args[] = {&a};
     return hipLaunchKernel(fn, dim3((unsigned)((n + 255) / 256)), dim3(256), args, 0, st);
+}
+hipError_t launch_recur_step(RecurArgs& a, int in_dtype, hipStream_t st) {
+    switch (in_dtype) {
+    case DT_F32: return launch_step_t<float>(a, st);
+    case DT_F16: return launch_step_t<_Float16>(a, st);
+    case DT_BF16: return launch_step_t<__bf16>(a, st);
+    default: return hipErrorNotSupported;
+    }
 }
 
 }  // namespace ssd
