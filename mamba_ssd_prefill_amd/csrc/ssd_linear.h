@@ -465,7 +465,8 @@ template <int TYPE> hipError_t launch_linear_type(LinearArgs& a, const LinearPla
     case 4: e = launch_tile<TYPE, 256, 128, 4, 2, TYPE == LT_E4M3 ? 2 : 3>(a, st); break;
     case 5: e = launch_tile<TYPE, 64, 128, 1, 4, 3>(a, st); break;
     case 6: e = launch_tile<TYPE, 32, 64, 1, 4, 6>(a, st); break;
-    default: e = launch_tile<TYPE, 16, 64, 1, 4, 8>(a, st); break;
+    case 7: e = launch_tile<TYPE, 16, 64, 1, 4, 8>(a, st); break;
+    default: e = launch_tile<TYPE, 128, 128, 4, 2, TYPE == LT_E4M3 ? 2 : 4>(a, st); break;
     }
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t lanes = (int64_t)a.M * ((a.N + 3) / 4);

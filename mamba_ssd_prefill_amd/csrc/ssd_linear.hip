@@ -29,7 +29,7 @@ struct TileModel {
 constexpr TileModel kTiles[] = {
     {128, 128, 2, {0.75f, 0.90f}, 4.f}, {256, 256, 1, {1.67f, 0.f}, 6.f},    {128, 192, 2, {0.85f, 1.28f}, 5.f},
     {256, 160, 1, {1.15f, 0.f}, 5.f},   {256, 128, 1, {0.88f, 0.f}, 5.f},    {64, 128, 2, {0.55f, 0.62f}, 3.f},
-    {32, 64, 2, {0.17f, 0.30f}, 2.f},   {16, 64, 2, {0.165f, 0.28f}, 2.f},
+    {32, 64, 2, {0.17f, 0.30f}, 2.f},   {16, 64, 2, {0.165f, 0.28f}, 2.f},   {128, 128, 1, {0.50f, 0.f}, 4.f},
 };
 constexpr float kCUs = 256.f;
 }  // namespace

@@ -22,12 +22,14 @@
 
 namespace ssd {
 
-// Waves of a workgroup, tokens of a tile, waves that a SIMD is to hold (which bounds the registers).
+// Waves of a workgroup, tokens of a tile, waves that a SIMD is to hold (which bounds the registers; the backward's forms
+// for packed rows and odd channels need more of them).  Measured at 2 x 4096 x 5120, bf16: tiles of 64, 128, 256 tokens
+// forward 270, 183, 177 us at 2 x 8192; backward with 2 and 3 waves a SIMD 210 and 172 us.
 struct RecFwd {
     static constexpr int W = kRecurWaves, TILE = kRecurTile, EU = 3;
 };
 struct RecBwd {
-    static constexpr int W = kRecurWaves, TILE = kRecurSaved, EU = 2;
+    static constexpr int W = kRecurWaves, TILE = kRecurSaved, EU = 3;
 };
 // Lanes of a row of 128 bytes, runs of a wave, tokens of a run, by the element size.
 template <typename T, typename D> struct RecGeo {
@@ -75,6 +77,11 @@ template <typename T, bool PAIRED> struct RecRows {
             h.w[0] = (lo & 0xffffu) | hi << 16;
         }
         return h;
+    }
+    // keeps the compiler from holding on to what it unpacked before
+    __device__ static inline void pin(Held& h) {
+        asm volatile("" : "+v"(h.w[0]));
+        if constexpr (sizeof(T) == 4) asm volatile("" : "+v"(h.w[1]));
     }
     __device__ static inline Two values(const Held& h) {
         if constexpr (sizeof(T) == 4) {
@@ -517,13 +524,14 @@ __global__ __launch_bounds__(64 * RecFwd::W, RecFwd::EU) void k_recur(RecurArgs 
 // Gradients.  The state entering the tile is the one that the forward pass kept; the gradient behind it comes by looking
 // back over the tiles after it.
 template <typename T, bool PAIRED, bool PACKED, typename F>
-__global__ __launch_bounds__(64 * RecBwd::W, RecBwd::EU) void k_recur_backward(RecurArgs a) {
+__global__ __launch_bounds__(64 * RecBwd::W, PAIRED && !PACKED ? RecBwd::EU : 2) void k_recur_backward(RecurArgs a) {
     typedef RecGeo<T, RecBwd> G;
     constexpr int TOK = G::TOK, LN = G::LN, W = G::W;
     typedef RecTile<T, PAIRED, PACKED, G, F> Tile;
     typedef typename Tile::Rows Rows;
     __shared__ HopPair waves[2][W * LN];
     __shared__ HopPair looked[W * 32];
+    __shared__ f32x4 parked[TOK][64 * W];  // r and A (1 - r) of a lane's tokens, which are not needed before the gradients
     const RecPlace p = rec_place<G, true>(a);
     const int t0 = p.tile * G::TILE, n = min(a.seqlen - t0, G::TILE);
     uint32_t ch[2];
@@ -544,19 +552,20 @@ __global__ __launch_bounds__(64 * RecBwd::W, RecBwd::EU) void k_recur_backward(R
     }
     RecSeq sq{0, 0, 0};
     if constexpr (PACKED) sq = rec_seq<TOK>(a, now.seq, t0 + p.tok);
-    // of each token: the decay, r and A (1 - r), beta i and 1 - i, the addition, and the part of the decay's gradient
-    // that goes by beta: dl = a g (h - a i x / beta), h the state before it
-    float d[TOK][2], rs[TOK][2], rc[TOK][2], bi[TOK][2], ic[TOK][2], u[TOK][2], w[TOK][2];
+    // of each token: the decay, r and A (1 - r), beta i and 1 - i, and the part of the decay's gradient that goes by
+    // beta: dl = a g (h - a i x / beta), h the state before it
+    float d[TOK][2], bi[TOK][2], ic[TOK][2], w[TOK][2];
 #pragma unroll
     for (int j = 0; j < TOK; ++j) {
         const Two x = Rows::values(now.x[j]), g = Rows::values(now.g[j]);
         Two iv{};
         if constexpr (F::ig) iv = Rows::values(now.i[j]);
+        f32x4 park;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const Gate r = gates_of(g.c[k], prm[k].gb);
-            rs[j][k] = r.s;
-            rc[j][k] = prm[k].A * r.c;
+            park[k] = r.s;
+            park[2 + k] = prm[k].A * r.c;
             d[j][k] = __builtin_amdgcn_exp2f(prm[k].A2 * r.s);
             float xi = x.c[k];
             bi[j][k] = 1.f;
@@ -566,16 +575,18 @@ __global__ __launch_bounds__(64 * RecBwd::W, RecBwd::EU) void k_recur_backward(R
                 ic[j][k] = i.c;
                 xi *= i.s;
             }
-            u[j][k] = xi;
             if constexpr (F::norm) {
                 const float be = beta_of(prm[k].Am * r.s, d[j][k]);
                 bi[j][k] *= be;
-                u[j][k] *= be;
                 // (beta = 0, a closed gate: the product with r (1 - r) goes to 0)
                 w[j][k] = be != 0.f ? d[j][k] * xi * __builtin_amdgcn_rcpf(be) : 0.f;
             }
         }
+        parked[j][threadIdx.x] = park;
     }
+    // (x and dout stay packed between their uses: unpacked ones of all tokens cost 32 registers)
+#pragma unroll
+    for (int j = 0; j < TOK; ++j) Rows::pin(now.x[j]);
     // The hops of the states (tokens behind the row's end come after all others here), and of the gradients: what each
     // token passes on of the gradient v behind it, v -> a (dout + v).
     Hop own[2], back[2];
@@ -583,7 +594,7 @@ __global__ __launch_bounds__(64 * RecBwd::W, RecBwd::EU) void k_recur_backward(R
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int j = 0; j < TOK; ++j) {
-            Hop s{d[j][k], u[j][k]};
+            Hop s{d[j][k], Rows::values(now.x[j]).c[k] * bi[j][k]};
             if constexpr (PACKED) {
                 if (sq.start >> j & 1)
                     s = Hop{-1.f, __builtin_fmaf(s.p, seq_state(a, p, a.h0, now.seq[j + 1], sq.pad >> j & 1, k), s.q)};
@@ -619,6 +630,8 @@ __global__ __launch_bounds__(64 * RecBwd::W, RecBwd::EU) void k_recur_backward(R
     }
     fwd.fold(waves[0]);
 #pragma unroll
+    for (int j = 0; j < TOK; ++j) Rows::pin(now.x[j]);
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
         float h = fwd.enter(k, start[k]);
 #pragma unroll
@@ -627,7 +640,7 @@ __global__ __launch_bounds__(64 * RecBwd::W, RecBwd::EU) void k_recur_backward(R
                 if (sq.start >> j & 1) h = seq_state(a, p, a.h0, now.seq[j + 1], sq.pad >> j & 1, k);
             }
             w[j][k] = F::norm ? h - w[j][k] : h;
-            h = __builtin_fmaf(d[j][k], h, u[j][k]);
+            h = __builtin_fmaf(d[j][k], h, Rows::values(now.x[j]).c[k] * bi[j][k]);
         }
     }
     float v[2];
@@ -649,6 +662,11 @@ __global__ __launch_bounds__(64 * RecBwd::W, RecBwd::EU) void k_recur_backward(R
     }
     float sum[3][2] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};  // dA, dgate_bias, din_bias
 #pragma unroll
+    for (int j = 0; j < TOK; ++j) {
+        Rows::pin(now.x[j]);
+        Rows::pin(dout[j]);
+    }
+#pragma unroll
     for (int k = 0; k < 2; ++k) v[k] = rev.enter(k, v[k]);
     const Rows rx(a.dx, a.channels, p.row0 + t0, n), rg(a.dgate, a.channels, p.row0 + t0, n);
     const Rows ri(F::ig ? a.dig : a.dgate, a.channels, p.row0 + t0, F::ig ? n : 0);
@@ -656,6 +674,7 @@ __global__ __launch_bounds__(64 * RecBwd::W, RecBwd::EU) void k_recur_backward(R
     for (int j = TOK - 1; j >= 0; --j) {
         const bool in = t0 + p.tok + j < a.seqlen;
         const Two x = Rows::values(now.x[j]), o = Rows::values(dout[j]);
+        const f32x4 park = parked[j][threadIdx.x];
         float dx[2], dg[2], di[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -665,9 +684,9 @@ __global__ __launch_bounds__(64 * RecBwd::W, RecBwd::EU) void k_recur_backward(R
                 if (sq.end >> j & 1) v[k] = seq_state(a, p, a.dfin, now.seq[j + 1], pad, k);
             }
             const float g = o.c[k] + v[k], ag = d[j][k] * g;
-            float dA = ag * w[j][k] * rs[j][k];
+            float dA = ag * w[j][k] * park[k];
             dx[k] = g * bi[j][k];
-            dg[k] = dA * rc[j][k];
+            dg[k] = dA * park[2 + k];
             di[k] = 0.f;
             if constexpr (F::ig) di[k] = dx[k] * x.c[k] * ic[j][k];
             if (pad) dx[k] = dg[k] = di[k] = dA = 0.f;
