@@ -584,6 +584,23 @@ __global__ __launch_bounds__(64 * RecBwd::W, PAIRED && !PACKED ? RecBwd::EU : 2)
         }
         parked[j][threadIdx.x] = park;
     }
+    // Tokens that count as nothing, so that no mask is needed behind this: those behind the row's end pass on what they get,
+    // and padding (whatever it holds) nothing.
+    if (t0 + G::TILE > a.seqlen || (PACKED && sq.pad)) {
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+            const bool out = t0 + p.tok + j >= a.seqlen, pad = PACKED && (sq.pad >> j & 1);
+            if (out || pad) {
+                now.x[j] = dout[j] = typename Rows::Held{};
+                parked[j][threadIdx.x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    d[j][k] = out ? 1.f : 0.f;
+                    bi[j][k] = w[j][k] = ic[j][k] = 0.f;
+                }
+            }
+        }
+    }
     // (x and dout stay packed between their uses: unpacked ones of all tokens cost 32 registers)
 #pragma unroll
     for (int j = 0; j < TOK; ++j) Rows::pin(now.x[j]);
@@ -598,6 +615,7 @@ __global__ __launch_bounds__(64 * RecBwd::W, PAIRED && !PACKED ? RecBwd::EU : 2)
             if constexpr (PACKED) {
                 if (sq.start >> j & 1)
                     s = Hop{-1.f, __builtin_fmaf(s.p, seq_state(a, p, a.h0, now.seq[j + 1], sq.pad >> j & 1, k), s.q)};
+                if (sq.pad >> j & 1) s = Hop{-1.f, 0.f};  // (the forward pass may have carried a NaN here)
             }
             own[k] = j ? then<PACKED>(own[k], s) : s;
         }
@@ -611,7 +629,6 @@ __global__ __launch_bounds__(64 * RecBwd::W, PAIRED && !PACKED ? RecBwd::EU : 2)
                 if (sq.end >> j & 1) s = Hop{-1.f, d[j][k] * (o + seq_state(a, p, a.dfin, now.seq[j + 1], pad, k))};
                 if (sq.start >> j & 1 || pad) s = Hop{-1.f, 0.f};
             }
-            if (t0 + p.tok + j >= a.seqlen) s = Hop{1.f, 0.f};
             back[k] = j == TOK - 1 ? s : then<PACKED>(back[k], s);
         }
     }
@@ -638,6 +655,7 @@ __global__ __launch_bounds__(64 * RecBwd::W, PAIRED && !PACKED ? RecBwd::EU : 2)
         for (int j = 0; j < TOK; ++j) {
             if constexpr (PACKED) {
                 if (sq.start >> j & 1) h = seq_state(a, p, a.h0, now.seq[j + 1], sq.pad >> j & 1, k);
+                if (sq.pad >> j & 1) h = 0.f;
             }
             w[j][k] = F::norm ? h - w[j][k] : h;
             h = __builtin_fmaf(d[j][k], h, Rows::values(now.x[j]).c[k] * bi[j][k]);
@@ -672,28 +690,25 @@ __global__ __launch_bounds__(64 * RecBwd::W, PAIRED && !PACKED ? RecBwd::EU : 2)
     const Rows ri(F::ig ? a.dig : a.dgate, a.channels, p.row0 + t0, F::ig ? n : 0);
 #pragma unroll
     for (int j = TOK - 1; j >= 0; --j) {
-        const bool in = t0 + p.tok + j < a.seqlen;
         const Two x = Rows::values(now.x[j]), o = Rows::values(dout[j]);
         const f32x4 park = parked[j][threadIdx.x];
         float dx[2], dg[2], di[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            bool pad = !in;
+            const bool pad = PACKED && (sq.pad >> j & 1);
             if constexpr (PACKED) {
-                pad = pad || (sq.pad >> j & 1);
                 if (sq.end >> j & 1) v[k] = seq_state(a, p, a.dfin, now.seq[j + 1], pad, k);
             }
             const float g = o.c[k] + v[k], ag = d[j][k] * g;
-            float dA = ag * w[j][k] * park[k];
+            const float dA = ag * w[j][k] * park[k];
             dx[k] = g * bi[j][k];
             dg[k] = dA * park[2 + k];
             di[k] = 0.f;
             if constexpr (F::ig) di[k] = dx[k] * x.c[k] * ic[j][k];
-            if (pad) dx[k] = dg[k] = di[k] = dA = 0.f;
             sum[0][k] += dA;
             sum[1][k] += dg[k];
             if constexpr (F::ig) sum[2][k] += di[k];
-            if (in) v[k] = ag;
+            v[k] = ag;
             if constexpr (PACKED) {
                 if (sq.start >> j & 1 && a.dh0 && !pad && p.live[k])
                     state_to(a.dh0, a.state_dtype, (int64_t)now.seq[j + 1] * a.channels + p.c0 + k, ag);
