@@ -668,7 +668,8 @@ typedef struct {
  *   x_scale      [M]     fp32       NULL means 1; only with operands in 8 bits
  *   weight_scale [N]     fp32       likewise
  *   pre          [M, N]  out_dtype  NULL: not wanted (kept for the backward pass of an activation)
- *   out          [M, N]  out_dtype  required, contiguous
+ *   out          [M, N]  out_dtype  required, contiguous.  May be the residual itself (residual_stride 0 or N); overlaps it
+ *                                   nowhere else
  *   workspace            256-byte aligned, ssd_linear_workspace_size() bytes
  * x is 16-byte aligned where it is contiguous with rows of a multiple of 16 bytes; else it has its element's
  * alignment.  (Rows that are no multiple of 16 bytes, or do not start on one, are copied to the workspace first.) */
@@ -677,7 +678,8 @@ ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, const void*
                         const void* residual, const float* x_scale, const float* weight_scale, void* pre, void* out,
                         void* workspace, size_t workspace_bytes, void* stream);
 
-/* The gradients from dout [M, N] (contiguous, 16-byte aligned) and, with an activation, the `pre` that the forward pass
+/* The gradients from dout [M, N] (contiguous; 16-byte aligned where dx is wanted, there is no activation and N values are a
+ * multiple of 16 bytes) and, with an activation, the `pre` that the forward pass
  * kept.  The residual's gradient is dout.  in_dtype fp32, fp16 or bf16.
  *     dpre = dout act'(pre),  dx = dpre weight,  dweight = dpre^T x,  dbias = sum over rows of dpre
  * dpre is rounded to in_dtype for the two products (a matrix instruction takes no wider operand), not for dbias.

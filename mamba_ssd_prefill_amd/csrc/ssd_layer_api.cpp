@@ -213,6 +213,11 @@ SSD_EXPORT ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, 
         !aligned(x_scale, 4) || !aligned(weight_scale, 4) || !aligned(pre, os) || !aligned(out, os) ||
         !aligned(workspace, kAlign))
         return SSD_ERR_MISALIGNED;
+    // in place, each value is read by the lane that writes it; anywhere else another lane may still read
+    const int64_t rs = p->residual_stride ? p->residual_stride : p->outs;
+    if (residual && !(out == residual && rs == p->outs) &&
+        overlap(residual, (size_t)((p->rows - 1) * rs + p->outs) * os, out, (size_t)p->rows * p->outs * os))
+        return SSD_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < l.total) return SSD_ERR_WORKSPACE_TOO_SMALL;
     const hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
@@ -244,7 +249,7 @@ SSD_EXPORT ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, 
     a.part = (float*)(ws + l.part_off);
     a.xs = xs * es;
     a.ws = wstr * es;
-    a.rs = p->residual_stride ? p->residual_stride : p->outs;
+    a.rs = rs;
     a.M = p->rows;
     a.N = p->outs;
     a.kbytes = (int)(l.kp * es);
@@ -302,14 +307,14 @@ SSD_EXPORT ssd_status_t ssd_linear_backward(const ssd_linear_params_t* p, const 
     if (!p->act && pre) return SSD_ERR_INVALID_ARGUMENT;
     const size_t es = elem_size(p->in_dtype);
     const LinearBackLayout l = linear_back_layout(p);
-    if (!aligned(dout, 16) || !aligned(x, es) || !aligned(weight, es) || !aligned(pre, es) || !aligned(dx, es) ||
+    const bool rows = l.rows && dx;  // (else dx comes from dout itself)
+    if (!aligned(dout, dx && !rows ? 16 : es) || !aligned(x, es) || !aligned(weight, es) || !aligned(pre, es) || !aligned(dx, es) ||
         !aligned(dweight, es) || !aligned(dbias, 4) || !aligned(workspace, kAlign))
         return SSD_ERR_MISALIGNED;
     if (workspace_bytes < l.total) return SSD_ERR_WORKSPACE_TOO_SMALL;
     const hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
     const int64_t M = p->rows, K = p->width, N = p->outs;
-    const bool rows = l.rows && dx;
     if (rows || dweight || dbias) {
         ssd::DpreArgs d{};
         d.dout = dout;

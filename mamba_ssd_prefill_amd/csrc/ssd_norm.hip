@@ -117,6 +117,29 @@ template <int W> __device__ inline uint32_t row_max(uint32_t v, uint32_t* lds) {
     return v;
 }
 
+// The codes of VEC values at scale s.  (The conversion instruction rounds to the nearest e4m3 value, ties to even, from the
+// quotient rounded to odd as well as code_e4m3 does in a dozen instructions: 2048 x 2560 values 15.8 -> 14.5 us.)
+template <int VEC> __device__ inline void codes_of(const float (&v)[VEC], float s, float inv, int format, uint8_t (&c)[VEC]) {
+    float q[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) q[e] = quotient_to_odd(v[e], s, inv);
+    if (format == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) c[e] = (uint8_t)code_int8(q[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+            float t[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = fminf(fmaxf(q[e + i], -448.f), 448.f);
+            int w = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
+            w = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w, true);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[e + i] = (uint8_t)((uint32_t)w >> 8 * i);
+        }
+    }
+}
+
 // W waves a row (a workgroup is four rows of one wave, or one row), NP pieces a lane at most.
 template <typename T, int W, int NP> __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rms_norm(RmsArgs a) {
     constexpr int VEC = 16 / (int)sizeof(T), LANES = 64 * W, ROWS = W == 1 ? 4 : 1;
@@ -187,11 +210,8 @@ template <typename T, int W, int NP> __global__ __launch_bounds__(W == 1 ? 256 :
             const int e0 = (lane + LANES * k) * VEC;
             if (e0 < D) {
                 uint8_t c[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float q = quotient_to_odd(v[k][e], s, inv);
-                    c[e] = none ? 0 : (uint8_t)(a.format == 0 ? code_int8(q) : code_e4m3(q));
-                }
+                codes_of<VEC>(v[k], s, inv, a.format, c);
+                if (none) __builtin_memset(c, 0, VEC);
                 uint8_t* p = (uint8_t*)a.out + row * D + e0;
                 if (e0 + VEC <= D) {
                     __builtin_memcpy(p, c, VEC);

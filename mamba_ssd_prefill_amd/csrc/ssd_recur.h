@@ -253,10 +253,10 @@ template <int W, int LN, bool REV, bool PACKED> struct TileHops {
 // A tile's word for a channel: its hop (p, q), or (-1, the state that leaves it), which lets nothing before it through.
 // A word is written and read whole, by atomics that the whole device sees, and says by itself whether it is there yet.
 constexpr uint64_t kNoHop = ~(uint64_t)0;
-// Looks at a word that is not there before a lane gives up (and its states become NaN).  Workgroups take a chain's
-// tiles in the order of their start, so a tile that is waited for is always running: this ends only waits that a second
-// call running on the same workspace made endless.
-constexpr int kMaxLooks = 1 << 20;
+// Looks (of a microsecond or so) at a word that is not there before a lane gives up, and its states become NaN.  Workgroups
+// take a chain's tiles in the order of their start, so a tile that is waited for is always running and its word microseconds
+// away: this ends only waits that a second call running on the same workspace made endless.
+constexpr int kMaxLooks = 1 << 16;
 
 __device__ inline float no_nan(float v) { return v != v ? __builtin_nanf("") : v; }  // (all ones would be kNoHop)
 __device__ inline void publish(uint64_t* at, Hop h) {

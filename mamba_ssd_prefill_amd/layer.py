@@ -137,11 +137,13 @@ def rms_norm(x, weight, residual=None, *, eps=1e-5, format=None, out=None, resid
     plan = _s._PLANS.get(key) or _s._older(key)
     if plan is None:
         plan = _s._keep(key, _norm_plan(x, weight, residual, eps, format, out, residual_out))
-    if out is None:
+    if out is None and residual is not None and residual_out is None:
+        out, residual_out = _s._new(plan.out, plan.state)
+    elif out is None:
         out, = _s._new(plan.out)
-    scales = None if format is None else _s._new(plan.new)[0]
-    if residual is not None and residual_out is None:
+    elif residual is not None and residual_out is None:
         residual_out, = _s._new(plan.state)
+    scales = None if format is None else _s._new(plan.new)[0]
     plan.call(px, pw, pr, out, scales, residual_out)
     got = (out,) if format is None else (out, scales)
     if residual is not None:
@@ -218,16 +220,19 @@ def linear(x, weight, bias=None, residual=None, *, activation=None, x_scale=None
     """ssd_linear: act(x weight^T + bias) + residual, x [..., K], weight [N, K], bias [N] float32, residual [..., N];
     ``activation`` None, "silu" or "gelu".  x and weight are float32, float16 or bfloat16, or 8-bit codes (torch.int8,
     torch.float8_e4m3fn) with ``x_scale`` [...] and ``weight_scale`` [N] float32 (None: 1).  Returns out [..., N] in
-    ``out_dtype`` (default: out's, the residual's, or x's), and with ``save_pre`` (out, pre) for linear_backward."""
+    ``out_dtype`` (default: out's, the residual's, or x's), and with ``save_pre`` (out, pre) for linear_backward.  ``out`` may
+    be the (contiguous) residual itself."""
     meta, (px, pw, pb, pr, psx, psw, _) = _s._meta(x, weight, bias, residual, x_scale, weight_scale, out)
     key = ("linear", meta, activation, out_dtype)
     plan = _s._PLANS.get(key) or _s._older(key)
     if plan is None:
         plan = _s._keep(key, _linear_plan(x, weight, bias, residual, activation, x_scale, weight_scale, out_dtype, out))
-    if out is None:
-        out, = _s._new(plan.out)
+    if out is None and workspace is None:
+        out, workspace = _s._new(plan.out, plan.spaces[0])
+    else:
+        out = _s._new(plan.out)[0] if out is None else out
+        workspace = _workspace(plan, workspace)
     pre = _s._new(plan.out)[0] if save_pre else None
-    workspace = _workspace(plan, workspace)
     plan.call(px, pw, pb, pr, psx, psw, pre, out, workspace, workspace.numel())
     return (out, pre) if save_pre else out
 

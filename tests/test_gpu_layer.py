@@ -305,6 +305,28 @@ def test_linear_rows_keep_to_themselves(M, K, N, dtype):
     assert torch.equal(got[:-1, :-1], clean[:-1, :-1]) and got[-1].isnan().all() and not got[:-1, -1].isfinite().any()
 
 
+@pytest.mark.parametrize("M,N", [(3, 40), (200, 333), (300, 1024)])
+def test_linear_onto_the_residual_in_place(M, N):
+    g = gen(10)
+    x, w, r = rn(g, M, 512).bfloat16().cuda(), rn(g, N, 512).bfloat16().cuda(), rn(g, M, N).bfloat16().cuda()
+    want = ssd.linear(x, w, residual=r, activation="silu")
+    v = r._version
+    got = ssd.linear(x, w, residual=r, activation="silu", out=r)
+    assert got is r and r._version > v and torch.equal(got, want)
+
+
+def test_nan_codes_and_scales_stay_in_their_rows():
+    x = torch.ones(5, 256, device="cuda").to(torch.float8_e4m3fn)
+    w = torch.ones(70, 256, device="cuda").to(torch.float8_e4m3fn)
+    s = torch.ones(5, device="cuda")
+    x.view(torch.uint8)[1, 200], s[3] = 0x7f, NAN
+    w.view(torch.uint8)[7, 0] = 0xff
+    got = ssd.linear(x, w, x_scale=s, out_dtype=torch.float32)
+    bad = torch.zeros(5, 70, dtype=torch.bool, device="cuda")
+    bad[[1, 3]], bad[:, 7] = True, True
+    assert torch.equal(got.isnan(), bad) and (got[~bad] == 256).all()
+
+
 @pytest.mark.parametrize("act,want", [("silu", [0.0, INF, 0.0]), ("gelu", [0.0, INF, 0.0])])
 def test_activations_of_infinities(act, want):
     x, w = torch.ones(1, 1, device="cuda"), torch.tensor([[-INF], [INF], [0.0]], device="cuda")
@@ -329,6 +351,7 @@ REC = [
     (1, 4500, 40, "f16", "f32", None, True, True, True, True, False),
     (1, 2100, 34, "bf16", "f32", "pad", True, True, True, True, True),
     (40, 150, 250, "bf16", "f32", None, True, True, True, True, False),
+    (1, 5000, 200, "f32", "f32", "pad", True, True, True, True, False),
 ]
 
 
@@ -512,6 +535,83 @@ def test_recurrence_prompt_in_two_pieces():
     K = 2 * (700 * per_token(A) + 100)  # both sides are off by that at most
     ref.close(torch.cat([a, b], 1), whole, S[0], K, torch.float32, "out")
     ref.close(end, fin, S[1], K, torch.float32, "state")
+
+
+# ---- sizes past 32 bits -----------------------------------------------------------------------------
+def test_norm_past_32_bits():
+    """More than 2^32 bytes and 2^31 values: the last rows are those of a call on them alone."""
+    M, D = 140000, 16001
+    x = torch.empty(M, D, dtype=torch.float16, device="cuda").normal_()
+    w = torch.rand(D, device="cuda")
+    y, s = ssd.rms_norm(x, w, x)
+    rows = slice(M - 3, M)
+    want = ssd.rms_norm(x[rows], w, x[rows])
+    assert torch.equal(y[rows], want[0]) and torch.equal(s[rows], want[1])
+    codes, scales = ssd.rms_norm(x, w, format="int8")
+    want = ssd.rms_norm(x[rows], w, format="int8")
+    assert torch.equal(codes[rows], want[0]) and torch.equal(scales[rows], want[1])
+    del codes, s
+    g = ssd.rms_norm_backward(y, x, w)
+    want = ssd.rms_norm_backward(y[rows], x[rows], w)
+    assert torch.equal(g.dx[rows], want.dx)
+
+
+def test_linear_past_32_bits():
+    """More than 2^32 bytes of x, of a view of x, and of out."""
+    M, K = 600000, 4096
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_()
+    w = torch.empty(70, K, dtype=torch.bfloat16, device="cuda").normal_()
+    rows = [0, 1, 262143, 262144, 524287, 524288, M - 1]
+    ref64 = x[rows].cpu().double() @ w.cpu().double().t()
+    S = x[rows].cpu().double().abs() @ w.cpu().double().abs().t()
+    ref.close(ssd.linear(x, w)[rows], ref64, S, 2 * K + 20, torch.bfloat16, "out")
+    part = x[:, 3:2003]
+    ref64 = part[rows].cpu().double() @ w[:, :2000].cpu().double().t()
+    ref.close(ssd.linear(part, w[:, :2000].contiguous())[rows], ref64, S, 2 * K + 20, torch.bfloat16, "out of a view")
+    del part
+    u, v = x[:, :8].contiguous(), torch.empty(4000, 8, dtype=torch.bfloat16, device="cuda").normal_()
+    del x
+    out = ssd.linear(u, v)
+    ref64, S = u[rows].cpu().double() @ v.cpu().double().t(), u[rows].cpu().double().abs() @ v.cpu().double().abs().t()
+    ref.close(out[rows], ref64, S, 36, torch.bfloat16, "wide out")
+
+
+def test_recurrence_past_32_bits():
+    """More than 2^31 values: the last tokens are those of a call that starts from the state before them."""
+    L, D, n = 270000, 8100, 301
+    x, gate = (torch.empty(1, L, D, device="cuda").normal_() for _ in range(2))
+    A = -torch.exp(torch.empty(D, device="cuda").normal_() - 2)
+    out, fin, saved = ssd.gated_recurrence(x, gate, A, save_for_backward=True)
+    tail = lambda t: t[:, L - n:].contiguous()  # noqa: E731
+    want, wfin = ssd.gated_recurrence(tail(x), tail(gate), A, initial_state=out[:, L - n - 1].clone())
+    S = ref.recurrence(tail(x), tail(gate), A, None, None, None, True, out[:, L - n - 1], 1, [(0, 0, 0, n)], absolute=True)
+    K = 2 * (n * per_token(A) + 100)
+    ref.close(tail(out), want, S[0], K, torch.float32, "out")
+    ref.close(fin, wfin, S[1], K, torch.float32, "state")
+    assert out.isfinite().all()
+    del want, gate, saved
+    gate = out  # (any values do)
+    h = ssd.gated_recurrence(x, gate, A, save_for_backward=True)
+    g = ssd.gated_recurrence_backward(x, x, gate, A, saved=h[2])
+    w, _, ws = ssd.gated_recurrence(tail(x), tail(gate), A, initial_state=h[0][:, L - n - 1].clone(), save_for_backward=True)
+    b = ssd.gated_recurrence_backward(tail(x), tail(x), tail(gate), A, initial_state=h[0][:, L - n - 1].clone(), saved=ws)
+    S = ref.recurrence_grads(tail(x), None, tail(x), tail(gate), A, None, None, None, True, h[0][:, L - n - 1], 1, [(0, 0, 0, n)],
+                             absolute=True)
+    K = 2 * (2 * n * per_token(A) + 200)
+    ref.close(tail(g.dx), b.dx, S[0], K, torch.float32, "dx")
+    ref.close(tail(g.dgate), b.dgate, S[1], K, torch.float32, "dgate")
+
+
+def test_recurrence_step_of_far_rows():
+    wide = torch.empty(3, 700_000_000, dtype=torch.float16, device="cuda")
+    x, gate = wide[:, :70], wide[:, 699_999_900:699_999_970]
+    x.normal_()
+    gate.normal_()
+    A, pool = -torch.ones(70, device="cuda"), torch.ones(3, 70, device="cuda")
+    other = pool.clone()
+    got = ssd.gated_recurrence_step(x, gate, A, state=pool)
+    assert torch.equal(got, ssd.gated_recurrence_step(x.contiguous(), gate.contiguous(), A, state=other))
+    assert torch.equal(pool, other)
 
 
 # ---- together ---------------------------------------------------------------------------------------

@@ -123,6 +123,10 @@ def test_misaligned(lib, name):
             continue
         kw[f] = FAKE + (i << 41) + a // 2
         assert call(lib, name, params_for(name, **p), **kw) == MISAL, (f, a)
+    if name == "ssd_linear_backward":  # dout itself is an operand only without an activation, of whole pieces, for dx
+        for prm, kw in ((linear_prm(act=1), dict(pre=FAKE)), (linear_prm(outs=97), {}), (linear_prm(), dict(dx=None))):
+            assert call(lib, name, prm, dout=FAKE + 2, ws_bytes=0, **kw) == WS_SMALL
+            assert call(lib, name, prm, dout=FAKE + 1, ws_bytes=0, **kw) == MISAL
     if name == "ssd_linear":  # the rows of a view may start anywhere, by their elements
         assert call(lib, name, linear_prm(x_stride=70), x=FAKE + 2, ws_bytes=0) == WS_SMALL
         assert call(lib, name, linear_prm(x_stride=70), x=FAKE + 1) == MISAL
@@ -148,7 +152,7 @@ def test_norm_backward_has_no_codes(lib):
     (dict(out_dtype=3), BADARG), (dict(act=3), BADARG), (dict(act=-1), BADARG), (dict(x_stride=63), SHAPE),
     (dict(x_stride=1 << 31), SHAPE), (dict(residual_stride=95), SHAPE), (dict(width=1 << 21), SHAPE),
     (dict(rows=2**31 - 1, outs=2**31 - 1), SHAPE), (dict(rows=2**31 - 1, width=1 << 18), SHAPE),
-    (dict(outs=2**31 - 1, width=1 << 18), SHAPE)])
+    (dict(outs=2**31 - 1, width=1 << 18), SHAPE), (dict(rows=1 << 19, outs=1 << 19, width=1 << 16), SHAPE)])
 def test_linear_parameters(lib, name, kw, code):
     assert call(lib, name, linear_prm(**kw)) == code
 
@@ -219,6 +223,12 @@ def test_overlaps_are_refused(lib):
     assert norm(norm_prm(residual_stride=70), residual=FAKE, sum=FAKE) == BADARG
     # (refused behind these checks only by another one: nothing is launched)
     assert norm(norm_prm(residual_stride=64), residual=FAKE, sum=FAKE, x=FAKE + 1) == MISAL
+    m = 30 * 96 * 2
+    for shift in (2, -2, m - 2, 2 - m):
+        assert call(lib, "ssd_linear", linear_prm(), res=FAKE, out=FAKE + shift, ws_bytes=0) == BADARG
+    assert call(lib, "ssd_linear", linear_prm(residual_stride=97), res=FAKE, out=FAKE, ws_bytes=0) == BADARG
+    for stride in (0, 96):
+        assert call(lib, "ssd_linear", linear_prm(residual_stride=stride), res=FAKE, out=FAKE, ws_bytes=0) == WS_SMALL
     b = dict(dsum=FAKE, ws_bytes=0)
     assert call(lib, "ssd_rms_norm_backward", norm_prm(), dres=FAKE + 2, **b) == BADARG
     assert call(lib, "ssd_rms_norm_backward", norm_prm(), dres=FAKE, **b) == WS_SMALL
