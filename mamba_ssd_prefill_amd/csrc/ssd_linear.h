@@ -2,15 +2,22 @@
 //
 // Both operands have the contraction's values one behind the other, so a tile of either is rows of 128 bytes (32 fp32,
 // 64 16-bit or 128 8-bit values), and everything up to the matrix instruction is the same for all types.  A
-// workgroup brings BM rows of x and BN of w into LDS a step of 128 bytes ahead of the step that it multiplies
-// (direct loads to LDS, 16 bytes a lane; pieces behind a row's end are read past the buffer, as zeros).
+// workgroup brings BM rows of x and BN of w into LDS by steps of 128 bytes, S of them in LDS or on their way
+// (direct loads to LDS, 16 bytes a lane; pieces behind a row's end are read past the buffer, as zeros).  Two steps are
+// enough where one takes a microsecond; short ones, of small tiles, are loads' latency, and take 6 or 8.
 //
 // w is the matrix instruction's first operand, so a lane's four accumulators are four consecutive n of one m; the rows
 // of w that the 16 lanes of a block take are chosen so that the NB blocks of a wave leave 4 NB consecutive n in a lane,
 // which the epilogue reads and writes 16 bytes at a time.
 //
 // LDS rows are 128 bytes, two to a line of 64 banks; piece c of row r lies at c ^ swz(r), chosen so that the 16
-// rows that a read takes at one c fall on 16 different places of a line.
+// rows that a read takes at one c fall on 16 different places of a line (no bank conflicts by the counter).
+//
+// Large products are bound by the matrix instructions and how well they are fed, smaller ones by their number of workgroups
+// and a step's latency, single rows by the weights' bytes.  Measured, bf16: 8192 x 8192 x 8192 869 us, 1.27 PFLOP/s (a
+// library's product 1.41); 4096 x 4096 x 1024 36 us (library 40), 4096 x 1024 x 4096 34 us (35); one row of 2560 x
+// 10576, 54 MB of weights, 10 us.  e4m3: 8192 x 8192 x 8192 444 us, 2.48 PFLOP/s (library 2.97); 2048 x 2560 x 10576 61 us (75).
+// fp32: 2048 x 2048 x 2048 132 us, 130 TFLOP/s (library, at 4096^3, 136).
 #pragma once
 
 #include "ssd_device.h"
@@ -42,10 +49,9 @@ template <> struct Mul<LT_F16> {
 template <> struct Mul<LT_F32> {
     typedef f32x4 Acc;
     static constexpr int PIECES = 1, ISSUES = 4;
-    __device__ static inline void run(const u32x4 (&w)[1], const u32x4 (&x)[1], Acc& c) {
-        const f32x4 a = __builtin_bit_cast(f32x4, w[0]), b = __builtin_bit_cast(f32x4, x[0]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c = TT<float>::mma(a[e], b[e], c);
+    // one of a piece's four values
+    __device__ static inline void run_one(const u32x4 (&w)[1], const u32x4 (&x)[1], Acc& c, int e) {
+        c = TT<float>::mma(__builtin_bit_cast(f32x4, w[0])[e], __builtin_bit_cast(f32x4, x[0])[e], c);
     }
 };
 template <> struct Mul<LT_I8> {
@@ -295,10 +301,19 @@ template <typename G, typename M> struct Frags {
         }
     }
     __device__ inline void multiply(typename M::Acc (&acc)[G::NB][G::MB]) const {
+        if constexpr (M::ISSUES == 4) {  // (fp32: the four instructions of a block depend on each other)
 #pragma unroll
-        for (int i = 0; i < G::NB; ++i)
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int j = 0; j < G::MB; ++j) M::run(w[i], x[j], acc[i][j]);
+                for (int i = 0; i < G::NB; ++i)
+#pragma unroll
+                    for (int j = 0; j < G::MB; ++j) M::run_one(w[i], x[j], acc[i][j], e);
+        } else {
+#pragma unroll
+            for (int i = 0; i < G::NB; ++i)
+#pragma unroll
+                for (int j = 0; j < G::MB; ++j) M::run(w[i], x[j], acc[i][j]);
+        }
     }
 };
 
@@ -332,8 +347,10 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_linear(LinearArgs a) {
     const int xrow = wm * G::MB * 16 + l16, wrow = wn * G::NB * 16 + (l16 >> 2) * 4 * G::NB + (l16 & 3);
     const char* const px = lds + xrow * G::STEP;
     const char* const pw = lds + (BM + wrow) * G::STEP;
-    if constexpr (M::PIECES == 2 || (S <= 3 && G::NW == 4)) {
-        // One set of fragments, waves that wait while others multiply.
+    if constexpr (M::PIECES == 2 || S == 2) {
+        // One set of fragments: e4m3, whose step is one instruction a block, and large tiles in two places, whose waves
+        // multiply for long enough to cover another's waits (8192^3 bf16, 256 x 256: 865 us so, 887 with the loop below; 128 x
+        // 128 by four waves 1000 and 1020; but 256 x 160 in three places 1093 and 972, 256 x 128 1041 and 932).
 #pragma unroll
         for (int i = 0; i < S - 1; ++i)
             if (s0 + i < s1) loads.issue(s0 + i, i);
@@ -358,6 +375,8 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_linear(LinearArgs a) {
 #pragma unroll
         for (int i = 0; i < S; ++i)
             if (s0 + i < s1) loads.issue(s0 + i, i);
+        // Two sets: half a step is read while the one before is multiplied (16 x 5120 x 2560 in tiles of 16 x 64: 13.5 us
+        // so, 19.5 with the loop above).
         Frags<G, M> f0, f1;
         int step = s0, place = 0;
         if (s0 + S <= s1) {
@@ -379,6 +398,11 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_linear(LinearArgs a) {
                 f0.read(px + place * G::STAGE, pw + place * G::STAGE, xrow, wrow, 0, q);
                 f1.multiply(acc);
                 loads_among<G::LOADS, G::MB + G::NB, G::MB * G::NB * M::ISSUES>();
+                // (fp32: the compiler reuses a block's registers one wait state early across the loop's end)
+                if constexpr (M::ISSUES == 4) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    asm volatile("s_nop 1");
+                }
             }
         }
         // the last S steps, or what there is
@@ -457,7 +481,7 @@ template <int TYPE, int BM, int BN, int WVM, int WVN, int S = 2> hipError_t laun
 
 template <int TYPE> hipError_t launch_linear_type(LinearArgs& a, const LinearPlan& p, hipStream_t st) {
     hipError_t e;
-    switch (p.tile) {
+    switch (p.tile) {  // (kTiles in ssd_linear.hip; what each takes of the 160 KB of LDS decides how many share a CU)
     case 0: e = launch_tile<TYPE, 128, 128, 2, 2>(a, st); break;
     case 1: e = launch_tile<TYPE, 256, 256, 2, 4>(a, st); break;
     case 2: e = launch_tile<TYPE, 128, 192, 2, 2>(a, st); break;

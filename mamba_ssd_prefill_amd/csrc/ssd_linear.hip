@@ -14,13 +14,13 @@ hipError_t launch_linear_i8(LinearArgs&, const LinearPlan&, hipStream_t);
 hipError_t launch_linear_e4m3(LinearArgs&, const LinearPlan&, hipStream_t);
 
 // The tile and the splits of the contraction by a model of the time, fitted to sweeps over 1 to 8192 rows at 2560 x
-// 10576, 5120 x 2560, 1024 x 4096, 4096 x 1024 and 8192 x 8192 (16-bit operands; it picks the fastest pair of the sweep or one
-// within 8 % of it):
+// 10576, 5120 x 2560, 1024 x 4096, 4096 x 1024 and 8192 x 8192 (bf16: of 19 such products it takes the fastest pair of the
+// sweep or one within 11 %, but for 64 x 2560 x 10576, 24 us against 19):
 //   2.5 us + rounds (steps c + e),  and 4 us + 8 bytes a partial sum at 4 TB/s where the contraction is split,
 // c being the time of a step with 1, 2, .. workgroups a CU and e that of a tile's start and epilogue.  8192 x 5120 x 2560
 // takes 206 us in tiles of 256 x 160 (two full rounds of 256 CUs), 271 us in 256 x 256 and 248 us in 128 x 128; 16 x
-// 5120 x 2560 11.2 us in 16 x 64 split by 4, 19 us unsplit.  fp32 is bound by its matrix instructions, 16 times slower: c
-// goes by the area.
+// 5120 x 2560 10.9 us in 16 x 64 split by 4, 13.5 us unsplit.  fp32 is bound by its matrix instructions, 16 times slower: c
+// goes by the area, down to what a step's latency takes.
 namespace {
 struct TileModel {
     int bm, bn, most;  // workgroups a CU
@@ -28,7 +28,7 @@ struct TileModel {
 };
 constexpr TileModel kTiles[] = {
     {128, 128, 2, {0.75f, 0.90f}, 4.f}, {256, 256, 1, {1.67f, 0.f}, 6.f},    {128, 192, 2, {0.85f, 1.28f}, 5.f},
-    {256, 160, 1, {1.15f, 0.f}, 5.f},   {256, 128, 1, {0.88f, 0.f}, 5.f},    {64, 128, 2, {0.55f, 0.62f}, 3.f},
+    {256, 160, 1, {1.15f, 0.f}, 5.f},   {256, 128, 1, {0.88f, 0.f}, 5.f},    {64, 128, 2, {0.45f, 0.60f}, 2.5f},
     {32, 64, 2, {0.17f, 0.30f}, 2.f},   {16, 64, 2, {0.165f, 0.28f}, 2.f},   {128, 128, 1, {0.50f, 0.f}, 4.f},
 };
 constexpr float kCUs = 256.f;
@@ -48,7 +48,7 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type) {
             const float work = (float)(tiles * splits);
             int o = 1;
             while (o < m.most && work > kCUs * (float)o) ++o;
-            const float c = type == LT_F32 ? 1.95f * (float)o * (float)(m.bm * m.bn) / 16384.f : m.c[o - 1];
+            const float c = type == LT_F32 ? fmaxf(0.2f, 1.95f * (float)o * (float)(m.bm * m.bn) / 16384.f) : m.c[o - 1];
             float us = ceilf(work / (kCUs * (float)o)) * ((float)per * c + m.e);
             if (splits > 1) us += 4.f + (float)splits * (float)M * (float)N * 2e-6f;
             if (us < least) {
@@ -100,9 +100,10 @@ template <typename T> struct Piece {
     }
 };
 
-// Both operands' rows in one launch, a piece a lane.
-template <typename T> __global__ __launch_bounds__(256) void k_pack_rows(PackArgs a, PackArgs b, int64_t na) {
-    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// Both operands' rows in one launch, a piece a lane.  (fp32, 333 and 771 rows of 1110: 7 us, of which a launch takes 3; the
+// product after it 18.)
+template <typename T> __global__ __launch_bounds__(256) void k_pack_rows(PackArgs a, PackArgs b, uint32_t na) {
+    uint32_t i = blockIdx.x * 256 + threadIdx.x;  // (a launch's lanes fit)
     const bool second = i >= na;
     if (second) i -= na;
     const PackArgs& p = second ? b : a;
@@ -114,7 +115,7 @@ template <typename T> __global__ __launch_bounds__(256) void k_pack_rows(PackArg
     v.store((T*)p.dst + r * p.kp + c);
 }
 
-// 64 x 64 values a workgroup, through LDS, both operands in one launch.
+// 64 x 64 values a workgroup, through LDS, both operands in one launch: 4096 x 1024 twice, f16, 7.8 us, 4.3 TB/s.
 template <typename T> struct Square {
     static constexpr int V = Piece<T>::V, LPR = 64 / V, RPP = 256 / LPR, PASSES = 64 / RPP, PITCH = 64 + 4 / (int)sizeof(T);
     T t[64][PITCH];
@@ -162,7 +163,7 @@ hipError_t launch_pack(PackArgs& a, PackArgs& b, int elem_bytes, bool transposed
         return hipLaunchKernel(fn, dim3((unsigned)(na + blocks(b))), dim3(256), args, 0, st);
     }
     auto lanes = [&](const PackArgs& p) { return p.dst ? p.rows * (p.kp / (16 / elem_bytes)) : 0; };
-    int64_t na = lanes(a);
+    uint32_t na = (uint32_t)lanes(a);
     const void* fn = elem_bytes == 4 ? (const void*)&k_pack_rows<uint32_t>
                    : elem_bytes == 2 ? (const void*)&k_pack_rows<uint16_t> : (const void*)&k_pack_rows<uint8_t>;
     void* args[] = {&a, &b, &na};
@@ -170,7 +171,9 @@ hipError_t launch_pack(PackArgs& a, PackArgs& b, int elem_bytes, bool transposed
 }
 
 // ---- dout act'(pre) -------------------------------------------------------------------------------------
-// 64 x 64 values a workgroup; the column sums come from the values before they are rounded.
+// 64 x 64 values a workgroup, written as rows and as columns, since the two products take their contraction's values one
+// behind the other; the column sums come from the values before they are rounded.  HBM-bound: 4096 x 4096
+// f16, 134 MB, 29 us, 4.6 TB/s.
 template <typename T> __global__ __launch_bounds__(256) void k_dpre(DpreArgs a) {
     typedef Square<T> S;
     constexpr int V = S::V;

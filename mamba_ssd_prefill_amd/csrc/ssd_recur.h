@@ -6,7 +6,7 @@
 //     g = dout + (a g of t+1),  dl = a g h of t-1 - (a^2 / beta) g i x     (l = A r)
 //     dx = g beta i,  din_gate = g beta x i (1 - i),  dgate = dl A r (1 - r),  dA = sum dl r
 //
-// Both passes are HBM-bound (8 and 14 bytes a token and channel of 16 bits), and read each input once.  A workgroup takes
+// Both passes read each input once and write each output once: 8 and 14 bytes a token and channel of 16 bits.  A workgroup takes
 // a tile of 128 bytes of channels and kRecurTile tokens, all tiles of a time before those of the next; a lane holds two
 // channels over a run of TOK tokens.  What a run of tokens does to the state is a hop h -> p h + q.  The runs of a wave are
 // joined by lane exchanges, the waves through LDS, and the tiles through memory: a tile publishes its hop as soon as it has
@@ -15,6 +15,10 @@
 //
 // Rows of 128 bytes are what the memory wants: reading three tensors of 2 x 8192 x 5120 by walking 32-byte columns of them
 // reached 2.0 TB/s, 64 bytes 2.4, 128 bytes 3.8 on 160 CUs alone (one workgroup a column, a forward pass of 250 us).
+//
+// Measured, bf16 with both gates: forward 174 us at 2 x 8192 x 5120 (671 MB: 3.9 TB/s, a large copy reaches 5.1), 94 us at 2 x
+// 4096 x 5120, whose backward pass takes 162 us.  The vector ALU issues for some 100 of the 174 us, HBM would need 133: what
+// holds the time is a tile's chain of ticket, loads, hop and look-back, which three waves a SIMD do not cover wholly.
 #pragma once
 
 #include "ssd_layer.h"
@@ -53,7 +57,6 @@ template <typename T, bool PAIRED> struct RecRows {
         stride = (uint32_t)row_stride * (uint32_t)sizeof(T);
         rsrc = make_rsrc((const char*)base + row * (int64_t)stride, (uint32_t)max(ntok, 0) * stride);
     }
-    typedef uint32_t Raw __attribute__((ext_vector_type(sizeof(T) == 4 ? 2 : 1)));
     struct Held {
         uint32_t w[sizeof(T) == 4 ? 2 : 1];
     };
@@ -180,7 +183,9 @@ template <bool PACKED> __device__ inline Hop then(Hop f, Hop s) {  // f first
     if (PACKED && s.p < 0.f) return s;
     return Hop{PACKED && f.p < 0.f ? f.p : f.p * s.p, __builtin_fmaf(s.p, f.q, s.q)};
 }
-template <bool PACKED> __device__ inline float after(Hop s, float h) { return PACKED && s.p < 0.f ? s.q : __builtin_fmaf(s.p, h, s.q); }
+template <bool PACKED> __device__ inline float after(Hop s, float h) {
+    return PACKED && s.p < 0.f ? s.q : __builtin_fmaf(s.p, h, s.q);
+}
 
 __device__ inline uint32_t bits(float v) { return __builtin_bit_cast(uint32_t, v); }
 __device__ inline float unbits(uint32_t v) { return __builtin_bit_cast(float, v); }
@@ -267,7 +272,8 @@ __device__ inline void publish(uint64_t* at, Hop h) {
 // The state entering tile `tile` (REV: the gradient behind it) for this lane's two channels.  The words of W tiles (or
 // twice as many) before it are read at a time, one a wave, again until one of them lets nothing through; from there
 // on the hops are applied one by one.  So the result is that of tiles one behind the other to the bit, whichever words
-// were there at which time.  c0: the workgroup's first channel; `init`: what enters the first tile.  `lds`: [32 * W].
+// were there at which time.  (Windows two and four times as wide: 174 -> 177 and 180 us at 2 x 8192 x 5120.)
+// c0: the workgroup's first channel; `init`: what enters the first tile.  `lds`: [32 * W].
 template <int W, int LN, bool REV>
 __device__ inline void look_back(const RecurArgs& a, int b, int tile, int c0, const void* init, HopPair* lds, float (&h)[2]) {
     constexpr int CH = 2 * LN, PER = 64 / CH, WIN = W * PER;
@@ -494,7 +500,8 @@ __global__ __launch_bounds__(64 * RecFwd::W, RecFwd::EU) void k_recur(RecurArgs 
             if (!p.live[k]) continue;
             const float end = after<PACKED>(hops.tile[k], h[k]);
             if (p.tile + 1 < a.ntiles) publish(word + k, Hop{-1.f, end});
-            if (!PACKED && a.fin && p.tile + 1 == a.ntiles) state_to(a.fin, a.state_dtype, (int64_t)p.b * a.channels + p.c0 + k, end);
+            if (!PACKED && a.fin && p.tile + 1 == a.ntiles)
+                state_to(a.fin, a.state_dtype, (int64_t)p.b * a.channels + p.c0 + k, end);
         }
     }
 #pragma unroll

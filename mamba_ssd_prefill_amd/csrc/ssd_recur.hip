@@ -135,7 +135,8 @@ static hipError_t launch_rec_any(RecurArgs& a, int in_dtype, bool backward, hipS
         int64_t n = (int64_t)a.batch * a.ntiles * a.channels, c = chains;
         void* args[] = {&a.hops, &n, &a.tickets, &c};
         const int64_t grid = (n + 1023) / 1024;
-        const hipError_t e = hipLaunchKernel((const void*)&k_recur_clear, dim3((unsigned)(grid < 2048 ? grid : 2048)), dim3(256), args, 0, st);
+        const hipError_t e =
+            hipLaunchKernel((const void*)&k_recur_clear, dim3((unsigned)(grid < 2048 ? grid : 2048)), dim3(256), args, 0, st);
         if (e != hipSuccess) return e;
     }
     const void* fn = in_dtype == DT_F32 ? rec_kernel_f32(a, backward)
@@ -151,11 +152,12 @@ hipError_t launch_recur_backward(RecurArgs& a, int in_dtype, float* dA, float* d
     if (e != hipSuccess) return e;
     int parts = a.batch * a.ntiles;
     void* args[] = {&a.part, &parts, &a.channels, &dA, &dgb, &dib};
-    return hipLaunchKernel((const void*)&k_recur_sums, dim3((unsigned)((3 * (int64_t)a.channels + 63) / 64)), dim3(256), args, 0, st);
+    return hipLaunchKernel((const void*)&k_recur_sums, dim3((unsigned)((3 * (int64_t)a.channels + 63) / 64)), dim3(256), args, 0,
+                           st);
 }
 
-// Two channels a lane where their number is even, and four rows where that leaves 512 workgroups (256 x 5120, bf16: 7.9 us, one row
-// 8.2, four channels 9.2 us).
+// HBM-bound: 256 x 5120, bf16 with fp32 states, 21 MB, 7.9 us with the launch.  Two channels a lane where their number is even, and
+// four rows where that leaves 512 workgroups (one row 8.2 us, four channels 9.2 us).
 template <typename T> static hipError_t launch_step_t(RecurArgs& a, hipStream_t st) {
     const int v = a.channels % 2 ? 1 : 2;
     const int64_t lanes = (int64_t)a.batch * (a.channels / v);
