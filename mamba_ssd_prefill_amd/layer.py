@@ -91,6 +91,13 @@ def _lead(x, what):
     return tuple(x.shape[:-1]), n
 
 
+def _counts(**sizes):
+    """Sizes that a parameter block holds in 32 bits (ctypes would cut them)."""
+    for name, n in sizes.items():
+        if n >= 2**31:
+            raise ValueError("%s must be below 2^31 (got %d)" % (name, n))
+
+
 def _workspace(plan, given, i=0):
     return _s._new(plan.spaces[i])[0] if given is None else _s._space(given, plan.dev)
 
@@ -101,6 +108,7 @@ def _norm_params(x, weight, residual, sum_dtype, eps, fmt):
     lead, rows = _lead(x, "x")
     D = x.shape[-1]
     import torch
+    _counts(width=D)
     _s._same(dev, torch.float32, weight=(weight, (D,)))
     xs = _s._rows("x", x, dev, x.dtype, x.shape, len(lead))
     rs = 0 if residual is None else _s._rows("residual", residual, dev, sum_dtype, x.shape, len(lead))
@@ -193,6 +201,7 @@ def _linear_params(x, weight, act, out_dtype, what):
     if weight.dim() != 2:
         raise ValueError("weight must be [outs, width]")
     K, N = x.shape[-1], weight.shape[0]
+    _counts(rows=rows, width=K, outs=N)
     _s._same(dev, x.dtype, weight=(weight, (N, K)))
     xs = _s._rows("x", x, dev, x.dtype, x.shape, len(lead))
     return LinearParams(ctypes.sizeof(LinearParams), rows, K, N, codes[x.dtype], _s._state_code(out_dtype), _ACTS[act], xs,
@@ -274,6 +283,7 @@ def _recurrence_params(x, gate, A, in_gate, gate_bias, in_bias, normalize, state
     if x.dim() != len(lead) + 1:
         raise ValueError("x must have %d dimensions (got %d)" % (len(lead) + 1, x.dim()))
     code, ch = _s._code(x, "x"), x.shape[-1]
+    _counts(batch=lead[0], seqlen=lead[-1] if len(lead) > 1 else 1, channels=ch, nseq=nseq)
     _s._same(dev, torch.float32, A=(A, (ch,)), gate_bias=(gate_bias, (ch,)), in_bias=(in_bias, (ch,)))
     if in_bias is not None and in_gate is None:
         raise ValueError("in_bias goes with in_gate")

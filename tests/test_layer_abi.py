@@ -344,3 +344,23 @@ def test_refused_parameters_keep_their_status(monkeypatch):
     with pytest.raises(ssd.SSDError) as e:
         ssd.rms_norm_backward(torch.zeros(2, 20000), torch.zeros(2, 20000), torch.zeros(20000))
     assert e.value.code == UNSUP
+
+
+def test_counts_that_the_parameter_blocks_cannot_hold(monkeypatch):
+    """Sizes from 2^31 are refused, not cut to 32 bits (tensors without data, so that they take no memory)."""
+    monkeypatch.setattr(layer._s, "_on_gpu", lambda t, what: t.device)
+    n = 2**31 + 5
+    new = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device="meta")  # noqa: E731
+    w = new(8)
+    cases = [(lambda: ssd.rms_norm(new(1, n), new(n)), "width"), (lambda: ssd.linear(new(n, 8), new(3, 8)), "rows"),
+             (lambda: ssd.linear(new(2, n), new(3, n)), "width"), (lambda: ssd.linear(new(2, 8), new(n, 8)), "outs"),
+             (lambda: ssd.linear_backward(new(n, 3), new(n, 8), new(3, 8)), "rows"),
+             (lambda: ssd.gated_recurrence(new(n, 1, 8), new(n, 1, 8), w), "batch"),
+             (lambda: ssd.gated_recurrence(new(1, n, 8), new(1, n, 8), w), "seqlen"),
+             (lambda: ssd.gated_recurrence(new(1, 1, n), new(1, 1, n), new(n)), "channels"),
+             (lambda: ssd.gated_recurrence(new(1, 1, 8), new(1, 1, 8), w, seq_idx=new(1, 1, dtype=torch.int32), nseq=n), "nseq"),
+             (lambda: ssd.gated_recurrence_step(new(n, 8), new(n, 8), w, state=new(4, 8)), "batch"),
+             (lambda: ssd.gated_recurrence_step(new(2, 8), new(2, 8), w, state=new(n, 8)), "nseq")]
+    for f, name in cases:
+        with pytest.raises(ValueError, match=name + " must be below"):
+            f()
