@@ -54,9 +54,16 @@ struct LinearArgs {
 struct LinearPlan {
     int tile;    // index of the tile shape
     int splits;  // of the contraction
+    float us;    // by the model that chose them
 };
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type);
-hipError_t launch_linear(LinearArgs& a, int type, const LinearPlan& p, hipStream_t st);
+struct LinearSize {
+    int64_t M, N, kbytes;
+    LinearPlan plan;
+};
+LinearPlan linear_plan_two(const LinearSize& a, const LinearSize& b, int type);
+// b: a second product in the same launch (by linear_plan_two), or NULL
+hipError_t launch_linear(LinearArgs& a, LinearArgs* b, int type, const LinearPlan& p, hipStream_t st);
 
 // Rows copied into ones that the product takes: kp values a row, those behind the source's zero.
 struct PackArgs {

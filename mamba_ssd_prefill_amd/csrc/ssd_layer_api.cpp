@@ -255,14 +255,14 @@ SSD_EXPORT ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, 
     a.kbytes = (int)(l.kp * es);
     a.act = p->act;
     a.out_dtype = p->out_dtype;
-    return hip_status(ssd::launch_linear(a, p->in_dtype, l.plan, st));
+    return hip_status(ssd::launch_linear(a, nullptr, p->in_dtype, l.plan, st));
 }
 
 namespace {
 
 // The backward's workspace.
 struct LinearBackLayout {
-    ssd::LinearPlan dx_plan, dw_plan;
+    ssd::LinearPlan dx_plan, dw_plan, both_plan;  // (both: splits 0 where they are launched one by one)
     bool rows;  // dpre as rows of its own (else dout serves)
     int64_t mp, np;
     size_t rows_off, cols_off, wt_off, xt_off, part_off, bias_off, total;
@@ -277,6 +277,8 @@ LinearBackLayout linear_back_layout(const ssd_linear_params_t* p) {
     l.rows = p->act || l.np != (int64_t)N;
     l.dx_plan = ssd::linear_plan(M, K, l.np * es, p->in_dtype);
     l.dw_plan = ssd::linear_plan(N, K, l.mp * es, p->in_dtype);
+    const int64_t m = M, k = K, n = N, eb = es;
+    l.both_plan = ssd::linear_plan_two({m, k, l.np * eb, l.dx_plan}, {n, k, l.mp * eb, l.dw_plan}, p->in_dtype);
     Regions r;
     l.rows_off = l.rows ? r.add(M * l.np * es) : 0;
     l.cols_off = r.add(N * l.mp * es);
@@ -337,29 +339,29 @@ SSD_EXPORT ssd_status_t ssd_linear_backward(const ssd_linear_params_t* p, const 
         const hipError_t e = ssd::launch_pack(wt, xt, (int)es, true, st);
         if (e != hipSuccess) return hip_status(e);
     }
-    ssd::LinearArgs a{};
-    a.part = (float*)(ws + l.part_off);
-    a.out_dtype = p->in_dtype;
-    a.N = p->width;
-    a.rs = K;
+    const auto product = [&](const void* xr, const void* wr, int64_t rows, int64_t row_bytes, void* out) {
+        ssd::LinearArgs a{};
+        a.x = xr;
+        a.w = wr;
+        a.xs = a.ws = row_bytes;
+        a.kbytes = (int)row_bytes;
+        a.M = (int)rows;
+        a.N = p->width;
+        a.rs = K;
+        a.out = out;
+        a.out_dtype = p->in_dtype;
+        a.part = (float*)(ws + l.part_off);
+        return a;
+    };
+    ssd::LinearArgs x_args = product(rows ? ws + l.rows_off : dout, wt.dst, M, l.np * es, dx);
+    ssd::LinearArgs w_args = product(ws + l.cols_off, xt.dst, N, l.mp * es, dweight);
+    if (dx && dweight && l.both_plan.splits) return hip_status(ssd::launch_linear(x_args, &w_args, p->in_dtype, l.both_plan, st));
     if (dx) {
-        a.x = rows ? ws + l.rows_off : dout;
-        a.w = wt.dst;
-        a.xs = a.ws = l.np * es;
-        a.kbytes = (int)(l.np * es);
-        a.M = p->rows;
-        a.out = dx;
-        const hipError_t e = ssd::launch_linear(a, p->in_dtype, l.dx_plan, st);
+        const hipError_t e = ssd::launch_linear(x_args, nullptr, p->in_dtype, l.dx_plan, st);
         if (e != hipSuccess) return hip_status(e);
     }
     if (dweight) {
-        a.x = ws + l.cols_off;
-        a.w = xt.dst;
-        a.xs = a.ws = l.mp * es;
-        a.kbytes = (int)(l.mp * es);
-        a.M = p->outs;
-        a.out = dweight;
-        const hipError_t e = ssd::launch_linear(a, p->in_dtype, l.dw_plan, st);
+        const hipError_t e = ssd::launch_linear(w_args, nullptr, p->in_dtype, l.dw_plan, st);
         if (e != hipSuccess) return hip_status(e);
     }
     return SSD_OK;

@@ -317,17 +317,20 @@ template <typename G, typename M> struct Frags {
     }
 };
 
+// One product, or two of like size in one launch (`other`'s workgroups from `count` on).
 template <int TYPE, int BM, int BN, int WVM, int WVN, int S>
-__global__ __launch_bounds__(64 * WVM * WVN, 2) void k_linear(LinearArgs a) {
+__global__ __launch_bounds__(64 * WVM * WVN, 2) void k_linear(LinearArgs one, LinearArgs other, uint32_t count) {
     typedef LinearTile<TYPE, BM, BN, WVM, WVN, S> G;
     typedef Mul<TYPE> M;
     extern __shared__ __align__(1024) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const bool second = blockIdx.x >= count;
+    const LinearArgs& a = second ? other : one;
     const int tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
     // Neighbouring tiles go to one XCD (workgroups are dealt to eight in turn), in groups of 8 rows of tiles, so that
     // the rows they share come from its L2.
-    uint32_t id = blockIdx.x;
-    const uint32_t whole = gridDim.x / 8 * 8;
+    uint32_t id = second ? blockIdx.x - count : blockIdx.x;
+    const uint32_t whole = (second ? gridDim.x - count : count) / 8 * 8;
     if (id < whole) id = (id & 7) * (whole / 8) + id / 8;
     const int split = (int)(id % (uint32_t)a.splits);
     id /= (uint32_t)a.splits;
@@ -471,26 +474,31 @@ template <typename V> __global__ __launch_bounds__(256) void k_linear_join(Linea
     cols.finish(a, m, v);
 }
 
-template <int TYPE, int BM, int BN, int WVM, int WVN, int S = 2> hipError_t launch_tile(LinearArgs& a, hipStream_t st) {
+template <int TYPE, int BM, int BN, int WVM, int WVN, int S = 2>
+hipError_t launch_tile(LinearArgs& a, LinearArgs* b, hipStream_t st) {
     typedef LinearTile<TYPE, BM, BN, WVM, WVN, S> G;
-    const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
-    void* args[] = {&a};
+    const auto groups = [](const LinearArgs& l) {
+        return (uint32_t)((int64_t)((l.M + BM - 1) / BM) * ((l.N + BN - 1) / BN) * l.splits);
+    };
+    uint32_t count = groups(a);
+    void* args[] = {&a, b ? b : &a, &count};
     const void* fn = (const void*)&k_linear<TYPE, BM, BN, WVM, WVN, S>;
-    return hipLaunchKernel(fn, dim3((unsigned)(tiles * a.splits)), dim3(G::THREADS), args, G::LDS, st);
+    return hipLaunchKernel(fn, dim3(b ? count + groups(*b) : count), dim3(G::THREADS), args, G::LDS, st);
 }
 
-template <int TYPE> hipError_t launch_linear_type(LinearArgs& a, const LinearPlan& p, hipStream_t st) {
+// (b: a second product in the same launch, neither being split, or NULL)
+template <int TYPE> hipError_t launch_linear_type(LinearArgs& a, LinearArgs* b, const LinearPlan& p, hipStream_t st) {
     hipError_t e;
     switch (p.tile) {  // (kTiles in ssd_linear.hip; what each takes of the 160 KB of LDS decides how many share a CU)
-    case 0: e = launch_tile<TYPE, 128, 128, 2, 2>(a, st); break;
-    case 1: e = launch_tile<TYPE, 256, 256, 2, 4>(a, st); break;
-    case 2: e = launch_tile<TYPE, 128, 192, 2, 2>(a, st); break;
-    case 3: e = launch_tile<TYPE, 256, 160, 4, 2, TYPE == LT_E4M3 ? 2 : 3>(a, st); break;
-    case 4: e = launch_tile<TYPE, 256, 128, 4, 2, TYPE == LT_E4M3 ? 2 : 3>(a, st); break;
-    case 5: e = launch_tile<TYPE, 64, 128, 1, 4, 3>(a, st); break;
-    case 6: e = launch_tile<TYPE, 32, 64, 1, 4, 6>(a, st); break;
-    case 7: e = launch_tile<TYPE, 16, 64, 1, 4, 8>(a, st); break;
-    default: e = launch_tile<TYPE, 128, 128, 4, 2, TYPE == LT_E4M3 ? 2 : 4>(a, st); break;
+    case 0: e = launch_tile<TYPE, 128, 128, 2, 2>(a, b, st); break;
+    case 1: e = launch_tile<TYPE, 256, 256, 2, 4>(a, b, st); break;
+    case 2: e = launch_tile<TYPE, 128, 192, 2, 2>(a, b, st); break;
+    case 3: e = launch_tile<TYPE, 256, 160, 4, 2, TYPE == LT_E4M3 ? 2 : 3>(a, b, st); break;
+    case 4: e = launch_tile<TYPE, 256, 128, 4, 2, TYPE == LT_E4M3 ? 2 : 3>(a, b, st); break;
+    case 5: e = launch_tile<TYPE, 64, 128, 1, 4, 3>(a, b, st); break;
+    case 6: e = launch_tile<TYPE, 32, 64, 1, 4, 6>(a, b, st); break;
+    case 7: e = launch_tile<TYPE, 16, 64, 1, 4, 8>(a, b, st); break;
+    default: e = launch_tile<TYPE, 128, 128, 4, 2, TYPE == LT_E4M3 ? 2 : 4>(a, b, st); break;
     }
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t lanes = (int64_t)a.M * ((a.N + 3) / 4);

@@ -3,6 +3,8 @@
 
 namespace ssd {
 
-hipError_t launch_linear_e4m3(LinearArgs& a, const LinearPlan& p, hipStream_t st) { return launch_linear_type<LT_E4M3>(a, p, st); }
+hipError_t launch_linear_e4m3(LinearArgs& a, LinearArgs* b, const LinearPlan& p, hipStream_t st) {
+    return launch_linear_type<LT_E4M3>(a, b, p, st);
+}
 
 }  // namespace ssd

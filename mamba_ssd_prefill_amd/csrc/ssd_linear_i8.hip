@@ -3,6 +3,8 @@
 
 namespace ssd {
 
-hipError_t launch_linear_i8(LinearArgs& a, const LinearPlan& p, hipStream_t st) { return launch_linear_type<LT_I8>(a, p, st); }
+hipError_t launch_linear_i8(LinearArgs& a, LinearArgs* b, const LinearPlan& p, hipStream_t st) {
+    return launch_linear_type<LT_I8>(a, b, p, st);
+}
 
 }  // namespace ssd
