@@ -71,8 +71,8 @@ struct PackArgs {
     void* dst;        // [rows][kp], or transposed: [cols][kp] with kp >= rows
     int64_t rows, cols, stride, kp;
 };
-// Two operands' in one launch (dst NULL: none).  Transposed: 2 or 4 bytes.
-hipError_t launch_pack(PackArgs& a, PackArgs& b, int elem_bytes, bool transposed, hipStream_t st);
+// Two operands' in one launch (dst NULL: none).
+hipError_t launch_pack(PackArgs& a, PackArgs& b, int elem_bytes, hipStream_t st);
 
 // dpre = dout act'(pre), as rows of np >= N values and transposed with rows of mp >= M (either NULL: not wanted), and its
 // sums over stretches of 64 rows.
@@ -85,7 +85,9 @@ struct DpreArgs {
     int64_t M, N, np, mp;
     int act;
 };
-hipError_t launch_dpre(DpreArgs& a, int dtype, float* dbias, hipStream_t st);
+// That (where one of rows, cols and part is wanted), two operands transposed (dst NULL: none), and the sums of `part` (dbias NULL:
+// not wanted).
+hipError_t launch_linear_before(DpreArgs& a, PackArgs& p, PackArgs& q, int dtype, float* dbias, hipStream_t st);
 
 // ---- gated recurrence -------------------------------------------------------------------------
 struct RecurArgs {

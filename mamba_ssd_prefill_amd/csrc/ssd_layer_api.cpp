@@ -156,11 +156,12 @@ ssd_status_t validate_linear(const ssd_linear_params_t* p, bool backward) {
     const int64_t M = p->rows, K = p->width, N = p->outs;
     if (padded(K, es) * (int64_t)es >= kMaxRowBytes) return SSD_ERR_INVALID_SHAPE;
     if (p->in_dtype == SSD_IN_INT8 && K > kMaxInt8Width) return SSD_ERR_UNSUPPORTED;
-    // lanes of the product (512 for 256 x 256 outputs) and of the gradient behind the activation (256 for 64 x 64), of the
-    // operands' copies (one for 16 bytes of either, in one launch) and transposed copies (256 for 64 x 64 of either)
+    // lanes of the product (512 for 256 x 256 outputs) and of the operands' copies (one for 16 bytes of either, in one launch); of
+    // the gradient behind the activation with the transposed copies (256 for 64 x 64 of any)
     const int64_t most = kMaxLanes / 256, mb = (M + 63) / 64, nb = (N + 63) / 64, kb = (K + 63) / 64 + 1;
     if (mb * nb >= most || mb * kb >= most || nb * kb >= most || (mb + nb) * kb >= most) return SSD_ERR_INVALID_SHAPE;
     if ((M + N) * (padded(K, es) * (int64_t)es / 16) >= kMaxLanes - 256) return SSD_ERR_INVALID_SHAPE;
+    if (backward && mb * nb + (mb + nb) * kb >= most) return SSD_ERR_INVALID_SHAPE;
     if (backward && (padded(N, es) * (int64_t)es >= kMaxRowBytes || padded(M, es) * (int64_t)es >= kMaxRowBytes))
         return SSD_ERR_INVALID_SHAPE;
     return SSD_OK;
@@ -234,7 +235,7 @@ SSD_EXPORT ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, 
         wstr = l.kp;
     }
     if (px.dst || pw.dst) {
-        const hipError_t e = ssd::launch_pack(px, pw, (int)es, false, st);
+        const hipError_t e = ssd::launch_pack(px, pw, (int)es, st);
         if (e != hipSuccess) return hip_status(e);
     }
     ssd::LinearArgs a{};
@@ -317,28 +318,22 @@ SSD_EXPORT ssd_status_t ssd_linear_backward(const ssd_linear_params_t* p, const 
     const hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
     const int64_t M = p->rows, K = p->width, N = p->outs;
-    if (rows || dweight || dbias) {
-        ssd::DpreArgs d{};
-        d.dout = dout;
-        d.pre = pre;
-        d.rows = rows ? ws + l.rows_off : nullptr;
-        d.cols = dweight ? ws + l.cols_off : nullptr;
-        d.part = dbias ? (float*)(ws + l.bias_off) : nullptr;
-        d.M = M;
-        d.N = N;
-        d.np = l.np;
-        d.mp = l.mp;
-        d.act = p->act;
-        const hipError_t e = ssd::launch_dpre(d, p->in_dtype, dbias, st);
-        if (e != hipSuccess) return hip_status(e);
-    }
+    ssd::DpreArgs d{};
+    d.dout = dout;
+    d.pre = pre;
+    d.rows = rows ? ws + l.rows_off : nullptr;
+    d.cols = dweight ? ws + l.cols_off : nullptr;
+    d.part = dbias ? (float*)(ws + l.bias_off) : nullptr;
+    d.M = M;
+    d.N = N;
+    d.np = l.np;
+    d.mp = l.mp;
+    d.act = p->act;
     ssd::PackArgs wt{}, xt{};
     if (dx) wt = ssd::PackArgs{weight, ws + l.wt_off, N, K, K, l.np};
     if (dweight) xt = ssd::PackArgs{x, ws + l.xt_off, M, K, p->x_stride ? p->x_stride : K, l.mp};
-    if (dx || dweight) {
-        const hipError_t e = ssd::launch_pack(wt, xt, (int)es, true, st);
-        if (e != hipSuccess) return hip_status(e);
-    }
+    const hipError_t before = ssd::launch_linear_before(d, wt, xt, p->in_dtype, dbias, st);
+    if (before != hipSuccess) return hip_status(before);
     const auto product = [&](const void* xr, const void* wr, int64_t rows, int64_t row_bytes, void* out) {
         ssd::LinearArgs a{};
         a.x = xr;

@@ -135,7 +135,7 @@ template <typename T> __global__ __launch_bounds__(256) void k_pack_rows(PackArg
     v.store((T*)p.dst + r * p.kp + c);
 }
 
-// 64 x 64 values a workgroup, through LDS, both operands in one launch: 4096 x 1024 twice, f16, 7.8 us, 4.3 TB/s.
+// 64 x 64 values on their way to rows of the transposed.
 template <typename T> struct Square {
     static constexpr int V = Piece<T>::V, LPR = 64 / V, RPP = 256 / LPR, PASSES = 64 / RPP, PITCH = 64 + 4 / (int)sizeof(T);
     T t[64][PITCH];
@@ -154,34 +154,7 @@ template <typename T> struct Square {
     }
 };
 
-template <typename T> __global__ __launch_bounds__(256) void k_transpose(PackArgs a, PackArgs b, uint32_t na) {
-    typedef Square<T> S;
-    __shared__ S sq;
-    const bool second = blockIdx.x >= na;
-    const PackArgs& p = second ? b : a;
-    const uint32_t i = second ? blockIdx.x - na : blockIdx.x, cb = (uint32_t)((p.cols + 63) / 64);
-    const int64_t r0 = (int64_t)(i / cb) * 64, c0 = (int64_t)(i % cb) * 64;
-    const int x = (int)(threadIdx.x % S::LPR) * S::V, y = threadIdx.x / S::LPR;
-#pragma unroll
-    for (int k = 0; k < S::PASSES; ++k) {
-        const int64_t r = r0 + y + k * S::RPP, c = c0 + x;
-        Piece<T> v{};
-        if (r < p.rows && c < p.cols) v.load((const T*)p.src + r * p.stride + c, p.cols - c);
-#pragma unroll
-        for (int e = 0; e < S::V; ++e) sq.t[y + k * S::RPP][x + e] = v.v[e];
-    }
-    __syncthreads();
-    sq.store_columns((T*)p.dst, p.kp, c0, p.cols, r0);
-}
-
-hipError_t launch_pack(PackArgs& a, PackArgs& b, int elem_bytes, bool transposed, hipStream_t st) {
-    if (transposed) {
-        auto blocks = [](const PackArgs& p) { return p.dst ? (p.kp + 63) / 64 * ((p.cols + 63) / 64) : 0; };
-        uint32_t na = (uint32_t)blocks(a);
-        const void* fn = elem_bytes == 4 ? (const void*)&k_transpose<uint32_t> : (const void*)&k_transpose<uint16_t>;
-        void* args[] = {&a, &b, &na};
-        return hipLaunchKernel(fn, dim3((unsigned)(na + blocks(b))), dim3(256), args, 0, st);
-    }
+hipError_t launch_pack(PackArgs& a, PackArgs& b, int elem_bytes, hipStream_t st) {
     auto lanes = [&](const PackArgs& p) { return p.dst ? p.rows * (p.kp / (16 / elem_bytes)) : 0; };
     uint32_t na = (uint32_t)lanes(a);
     const void* fn = elem_bytes == 4 ? (const void*)&k_pack_rows<uint32_t>
@@ -190,60 +163,91 @@ hipError_t launch_pack(PackArgs& a, PackArgs& b, int elem_bytes, bool transposed
     return hipLaunchKernel(fn, dim3((unsigned)((na + lanes(b) + 255) / 256)), dim3(256), args, 0, st);
 }
 
-// ---- dout act'(pre) -------------------------------------------------------------------------------------
-// 64 x 64 values a workgroup, written as rows and as columns, since the two products take their contraction's values one
-// behind the other; the column sums come from the values before they are rounded.  HBM-bound: 4096 x 4096
-// f16, 134 MB, 29 us, 4.6 TB/s.
-template <typename T> __global__ __launch_bounds__(256) void k_dpre(DpreArgs a) {
-    typedef Square<T> S;
-    constexpr int V = S::V;
-    __shared__ S sq;
-    __shared__ float sums[S::RPP][64], quarters[256];
-    const uint32_t cb = (uint32_t)((a.N + 63) / 64);
-    const int64_t r0 = (int64_t)(blockIdx.x / cb) * 64, c0 = (int64_t)(blockIdx.x % cb) * 64;
-    const int x = (int)(threadIdx.x % S::LPR) * V, y = threadIdx.x / S::LPR;
-    const int64_t c = c0 + x;
-    float s[V];
+// ---- before the gradients' products -----------------------------------------------------------------------
+// 64 x 64 values a workgroup, through LDS: dout act'(pre), written as rows and as columns, since the two products take their
+// contraction's values one behind the other, with its column sums, from the values before they are rounded; and the
+// transposed weight and input.  HBM-bound: dout and pre of 4096 x 4096 f16, a weight and an input of
+// 4096 x 1024, 168 MB, 31.6 us, 5.3 TB/s (in two launches 29.4 and 7.8).
+template <typename T> struct Dpre {
+    static constexpr int V = Square<T>::V;
+    Square<T> sq;
+    float sums[Square<T>::RPP][64], quarters[256];
+    __device__ inline void run(const DpreArgs& a, uint32_t block) {
+        typedef Square<T> S;
+        const uint32_t cb = (uint32_t)((a.N + 63) / 64);
+        const int64_t r0 = (int64_t)(block / cb) * 64, c0 = (int64_t)(block % cb) * 64;
+        const int x = (int)(threadIdx.x % S::LPR) * V, y = threadIdx.x / S::LPR;
+        const int64_t c = c0 + x;
+        float s[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) s[e] = 0.f;
+        for (int e = 0; e < V; ++e) s[e] = 0.f;
 #pragma unroll
-    for (int k = 0; k < S::PASSES; ++k) {
-        const int64_t r = r0 + y + k * S::RPP;
-        float v[V];
+        for (int k = 0; k < S::PASSES; ++k) {
+            const int64_t r = r0 + y + k * S::RPP;
+            float v[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = 0.f;
-        if (r < a.M && c < a.N) {
-            const int n = (int)min(a.N - c, (int64_t)V);
-            row_load_t<V, T>(a.dout, r * a.N + c, n, v);
-            if (a.act) {
-                float p[V];
-                row_load_t<V, T>(a.pre, r * a.N + c, n, p);
+            for (int e = 0; e < V; ++e) v[e] = 0.f;
+            if (r < a.M && c < a.N) {
+                const int n = (int)min(a.N - c, (int64_t)V);
+                row_load_t<V, T>(a.dout, r * a.N + c, n, v);
+                if (a.act) {
+                    float p[V];
+                    row_load_t<V, T>(a.pre, r * a.N + c, n, p);
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if (e < n) v[e] *= act_d(p[e], a.act);
+                    for (int e = 0; e < V; ++e)
+                        if (e < n) v[e] *= act_d(p[e], a.act);
+                }
             }
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                s[e] += v[e];
+                if (a.cols) sq.t[y + k * S::RPP][x + e] = (T)v[e];
+            }
+            // (a padded pitch is the next multiple of a piece)
+            if (a.rows && r < a.M && c < a.np) row_store_t<V, T>(a.rows, r * a.np + c, V, v);
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            s[e] += v[e];
-            if (a.cols) sq.t[y + k * S::RPP][x + e] = (T)v[e];
-        }
-        // (a padded pitch is the next multiple of a piece)
-        if (a.rows && r < a.M && c < a.np) row_store_t<V, T>(a.rows, r * a.np + c, V, v);
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) sums[y][x + e] = s[e];
-    __syncthreads();
-    if (a.cols) sq.store_columns((T*)a.cols, a.mp, c0, a.N, r0);
-    if (a.part) {
-        const int col = threadIdx.x & 63, part = threadIdx.x >> 6;
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < S::RPP / 4; ++i) t += sums[part * (S::RPP / 4) + i][col];
-        quarters[threadIdx.x] = t;
+        for (int e = 0; e < V; ++e) sums[y][x + e] = s[e];
         __syncthreads();
-        if (threadIdx.x < 64 && c0 + col < a.N)
-            a.part[(r0 / 64) * a.N + c0 + col] = (quarters[col] + quarters[64 + col]) + (quarters[128 + col] + quarters[192 + col]);
+        if (a.cols) sq.store_columns((T*)a.cols, a.mp, c0, a.N, r0);
+        if (a.part) {
+            const int col = threadIdx.x & 63, part = threadIdx.x >> 6;
+            float t = 0.f;
+#pragma unroll
+            for (int i = 0; i < S::RPP / 4; ++i) t += sums[part * (S::RPP / 4) + i][col];
+            quarters[threadIdx.x] = t;
+            __syncthreads();
+            if (threadIdx.x < 64 && c0 + col < a.N)
+                a.part[(r0 / 64) * a.N + c0 + col] = (quarters[col] + quarters[64 + col]) + (quarters[128 + col] + quarters[192 + col]);
+        }
+    }
+    __device__ inline void transpose(const PackArgs& p, uint32_t block) {
+        typedef Square<T> S;
+        const uint32_t cb = (uint32_t)((p.cols + 63) / 64);
+        const int64_t r0 = (int64_t)(block / cb) * 64, c0 = (int64_t)(block % cb) * 64;
+        const int x = (int)(threadIdx.x % S::LPR) * V, y = threadIdx.x / S::LPR;
+#pragma unroll
+        for (int k = 0; k < S::PASSES; ++k) {
+            const int64_t r = r0 + y + k * S::RPP, c = c0 + x;
+            Piece<T> v{};
+            if (r < p.rows && c < p.cols) v.load((const T*)p.src + r * p.stride + c, p.cols - c);
+#pragma unroll
+            for (int e = 0; e < V; ++e) sq.t[y + k * S::RPP][x + e] = v.v[e];
+        }
+        __syncthreads();
+        sq.store_columns((T*)p.dst, p.kp, c0, p.cols, r0);
+    }
+};
+// The first `nd` workgroups dout act'(pre), then `np` transposing p, the others q.
+template <typename T>
+__global__ __launch_bounds__(256) void k_linear_before(DpreArgs a, PackArgs p, PackArgs q, uint32_t nd, uint32_t np) {
+    __shared__ Dpre<T> d;
+    if (blockIdx.x < nd) {
+        d.run(a, blockIdx.x);
+    } else {
+        const uint32_t i = blockIdx.x - nd;
+        const bool second = i >= np;
+        d.transpose(second ? q : p, second ? i - np : i);
     }
 }
 
@@ -255,13 +259,14 @@ __global__ __launch_bounds__(1024) void k_dbias(const float* part, float* db, in
     if (live && threadIdx.x < 64) db[c] = s;
 }
 
-hipError_t launch_dpre(DpreArgs& a, int dtype, float* dbias, hipStream_t st) {
+hipError_t launch_linear_before(DpreArgs& a, PackArgs& p, PackArgs& q, int dtype, float* dbias, hipStream_t st) {
     // (padded columns behind N and padded rows behind M lie in the last blocks of 64)
-    const int64_t blocks = ((a.M + 63) / 64) * ((a.N + 63) / 64);
-    const void* fn = dtype == DT_F32 ? (const void*)&k_dpre<float>
-                   : dtype == DT_F16 ? (const void*)&k_dpre<_Float16> : (const void*)&k_dpre<__bf16>;
-    void* args[] = {&a};
-    const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, st);
+    auto blocks = [](const PackArgs& t) { return t.dst ? (t.kp + 63) / 64 * ((t.cols + 63) / 64) : 0; };
+    uint32_t nd = a.rows || a.cols || a.part ? (uint32_t)(((a.M + 63) / 64) * ((a.N + 63) / 64)) : 0, np = (uint32_t)blocks(p);
+    const void* fn = dtype == DT_F32 ? (const void*)&k_linear_before<float>
+                   : dtype == DT_F16 ? (const void*)&k_linear_before<_Float16> : (const void*)&k_linear_before<__bf16>;
+    void* args[] = {&a, &p, &q, &nd, &np};
+    const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)(nd + np + blocks(q))), dim3(256), args, 0, st);
     if (e != hipSuccess || !dbias) return e;
     int parts = (int)((a.M + 63) / 64);
     void* sum_args[] = {&a.part, &dbias, &parts, &a.N};

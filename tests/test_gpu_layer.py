@@ -246,6 +246,27 @@ def test_linear_backward(case):
     assert only.dx is None and torch.equal(only.dweight, a.dweight)
 
 
+@pytest.mark.parametrize("M,K,N,dtype", [(2100, 520, 1300, "f16"), (300, 1030, 4100, "bf16"), (4099, 257, 130, "bf16"),
+                                         (1030, 390, 771, "f32")], ids=str)
+def test_linear_backward_of_unlike_contractions(M, K, N, dtype):
+    """Both products in one launch or two, their contractions (N and M) of other lengths, alone and together."""
+    say("linear backward", M, K, N, dtype)
+    g, t = gen(44), DT[dtype]
+    x, w, dout = rn(g, M, K).to(t), (rn(g, N, K) / K**0.5).to(t), rn(g, M, N).to(t)
+    pre = rn(g, M, N).to(t)
+    a = ssd.linear_backward(dout.cuda(), x.cuda(), w.cuda(), with_bias=True, pre=pre.cuda(), activation="silu")
+    torch.cuda.synchronize()
+    want = ref.product_grads(dout, x, w, pre, "silu")
+    S = ref.product_grads(dout, x, w, pre, "silu", absolute=True)
+    half = torch.finfo(t).eps / 2 / ref.U  # dpre's own rounding
+    for got, exact, size, n, out, name in zip(a, want, S, (2 * N + 80 + half, 2 * M + 80 + half, M + 80), (t, t, torch.float32),
+                                              ("dx", "dweight", "dbias")):
+        ref.close(got, exact, size, n, out, name)
+        alone = ssd.linear_backward(dout.cuda(), x.cuda(), w.cuda(), pre=pre.cuda(), activation="silu", with_dx=name == "dx",
+                                    with_dweight=name == "dweight", with_bias=name == "dbias")
+        ref.close(getattr(alone, name), exact, size, n, out, name)
+
+
 CODES = [
     # (lead, K, N, type, out type, bias, residual, activation, strided, scales)
     ((1,), 16, 8, "int8", "f32", False, False, None, False, True),
