@@ -672,7 +672,8 @@ typedef struct {
  *                                   nowhere else
  *   workspace            256-byte aligned, ssd_linear_workspace_size() bytes
  * x is 16-byte aligned where it is contiguous with rows of a multiple of 16 bytes; else it has its element's
- * alignment.  (Rows that are no multiple of 16 bytes, or do not start on one, are copied to the workspace first.) */
+ * alignment.  (Rows that are no multiple of 16 bytes, or do not start on one, are loaded by 4 bytes or copied to the workspace first;
+ * the sums are the same to the bit.) */
 size_t ssd_linear_workspace_size(const ssd_linear_params_t* p);
 ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, const void* weight, const float* bias,
                         const void* residual, const float* x_scale, const float* weight_scale, void* pre, void* out,
@@ -685,7 +686,8 @@ ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, const void*
  * dpre is rounded to in_dtype for the two products (a matrix instruction takes no wider operand), not for dbias.
  *   dx      [M, K]  in_dtype  NULL: not wanted
  *   dweight [N, K]  in_dtype  NULL: not wanted
- *   dbias   [N]     fp32      NULL: not wanted (one of the three is required) */
+ *   dbias   [N]     fp32      NULL: not wanted (one of the three is required)
+ * dx and dweight wanted together may be summed in another order than each alone. */
 size_t ssd_linear_backward_workspace_size(const ssd_linear_params_t* p);
 ssd_status_t ssd_linear_backward(const ssd_linear_params_t* p, const void* dout, const void* x, const void* weight,
                                  const void* pre, void* dx, void* dweight, float* dbias, void* workspace,

@@ -55,8 +55,11 @@ struct LinearPlan {
     int tile;    // index of the tile shape
     int splits;  // of the contraction
     float us;    // by the model that chose them
+    bool narrow; // loads of 4 bytes a lane: rows of a multiple of 4 bytes
 };
-LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type);
+// copied: the bytes of rows that 16-byte loads do not take as they are, to be copied first (plan not narrow) or loaded by 4
+// bytes; may_narrow: whether these can be
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type, int64_t copied = 0, bool may_narrow = false);
 struct LinearSize {
     int64_t M, N, kbytes;
     LinearPlan plan;

@@ -167,7 +167,9 @@ ssd_status_t validate_linear(const ssd_linear_params_t* p, bool backward) {
     return SSD_OK;
 }
 
-bool rows_fit(int64_t stride, size_t es) { return stride * es % 16 == 0 && stride * (int64_t)es < kMaxRowBytes; }
+bool rows_fit(int64_t stride, size_t es, size_t piece) {
+    return stride * es % piece == 0 && stride * (int64_t)es < kMaxRowBytes;
+}
 
 // The workspace of a product: copies of the operands where their rows do not fit, and the sums of the splits.
 struct LinearLayout {
@@ -181,11 +183,17 @@ LinearLayout linear_layout(const ssd_linear_params_t* p) {
     LinearLayout l{};
     const size_t es = elem_size(p->in_dtype);
     const int64_t K = p->width;
+    const int64_t xs = p->x_stride ? p->x_stride : K;
     l.kp = padded(K, es);
     l.pack_w = l.kp != K;
-    l.pack_x = l.kp != K || !rows_fit(p->x_stride ? p->x_stride : K, es);
-    l.may_pack_x = l.pack_x || (p->x_stride && p->x_stride != K);  // a view's rows may start anywhere
-    l.plan = ssd::linear_plan(p->rows, p->outs, l.kp * es, p->in_dtype);
+    l.pack_x = l.kp != K || !rows_fit(xs, es, 16);
+    l.may_pack_x = l.pack_x || xs != K;  // a view's rows may start anywhere
+    const int64_t copied = ((l.pack_x ? p->rows : 0) + (l.pack_w ? (int64_t)p->outs : 0)) * K * (int64_t)es;
+    l.plan = ssd::linear_plan(p->rows, p->outs, l.kp * es, p->in_dtype, copied, copied && K * es % 4 == 0);
+    if (l.plan.narrow) {
+        l.pack_w = false;
+        l.pack_x = !rows_fit(xs, es, 4);
+    }
     Regions r;
     l.x_off = l.may_pack_x ? r.add((size_t)p->rows * l.kp * es) : 0;
     l.w_off = l.pack_w ? r.add((size_t)p->outs * l.kp * es) : 0;
@@ -222,9 +230,10 @@ SSD_EXPORT ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, 
     if (workspace_bytes < l.total) return SSD_ERR_WORKSPACE_TOO_SMALL;
     const hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
-    int64_t xs = p->x_stride ? p->x_stride : p->width, wstr = p->width;
+    const int64_t K = p->width;
+    int64_t xs = p->x_stride ? p->x_stride : K, wstr = K;
     ssd::PackArgs px{}, pw{};
-    if (l.pack_x || !aligned(x, 16)) {
+    if (l.pack_x || !aligned(x, l.plan.narrow ? 4 : 16)) {
         px = ssd::PackArgs{x, ws + l.x_off, p->rows, p->width, xs, l.kp};
         x = px.dst;
         xs = l.kp;
@@ -253,7 +262,7 @@ SSD_EXPORT ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, 
     a.rs = rs;
     a.M = p->rows;
     a.N = p->outs;
-    a.kbytes = (int)(l.kp * es);
+    a.kbytes = (int)((l.plan.narrow ? K : l.kp) * es);
     a.act = p->act;
     a.out_dtype = p->out_dtype;
     return hip_status(ssd::launch_linear(a, nullptr, p->in_dtype, l.plan, st));

@@ -202,19 +202,26 @@ __device__ inline void barrier_only() {
 // ---- tiles ----------------------------------------------------------------------------------------
 constexpr uint32_t kNoPiece = 0x80000000u;  // an offset past every operand's buffer: reads as zeros
 
-// BM x BN outputs a workgroup, WVM x WVN waves.
-template <int TYPE, int BM, int BN, int WVM, int WVN, int S> struct LinearTile {
+// BM x BN outputs a workgroup, WVM x WVN waves, S steps in LDS, W bytes a lane and load: 16, or 4 for rows that start
+// anywhere on 4 bytes.
+template <int TYPE, int BM, int BN, int WVM, int WVN, int S, int W> struct LinearTile {
     static constexpr int NW = WVM * WVN, THREADS = 64 * NW, MB = BM / WVM / 16, NB = BN / WVN / 16;
-    static constexpr int STEP = 128;  // bytes of a row
-    static constexpr int RPI = 8 * NW;  // rows that one load of every lane brings
+    static constexpr int STEP = 128, WIDE = W;  // bytes of a row, of a load
+    static constexpr int LPR = STEP / W, RPL = 64 / LPR;  // lanes of a row, rows of a wave's load
+    static constexpr int RPI = RPL * NW;                  // rows that one load of every lane brings
     static constexpr int IX = (BM + RPI - 1) / RPI, IW = (BN + RPI - 1) / RPI;  // (the last one by some waves, which others repeat)
     static constexpr int LOADS = IX + IW;  // of a lane for a step
     static constexpr int STAGE = (BM + BN) * STEP, LDS = S * STAGE;
-    static_assert((S - 2) * LOADS < 64, "loads on their way are counted in six bits");
+    static_assert((S - 1) * LOADS < 64, "loads on their way are counted in six bits");
     static_assert(BM % (16 * WVM) == 0 && BN % (16 * WVN) == 0 && LDS <= 160 * 1024, "blocks of a wave");
-    // the first of the 8 rows that a wave brings with load j of a tile's ROWS
+    // the first of the RPL rows that a wave brings with load j of a tile's ROWS
     template <int ROWS> __device__ static inline int load_row(int j, int wave) {
-        return (j + 1) * RPI <= ROWS ? j * RPI + wave * 8 : j * RPI + wave % ((ROWS - j * RPI) / 8) * 8;
+        return (j + 1) * RPI <= ROWS ? j * RPI + wave * RPL : j * RPI + wave % ((ROWS - j * RPI) / RPL) * RPL;
+    }
+    // where in its row the W bytes are that a lane brings to its place
+    __device__ static inline uint32_t bytes_at(int lane, int swz) {
+        const int at = lane % LPR * W;
+        return (uint32_t)((at >> 4 ^ swz) << 4 | (at & 15));
     }
     __device__ static inline int swz_x(int row) { return (row >> 1) & 7; }
     __device__ static inline int swz_w(int row) { return (row >> 1 & 1) | (row / (4 * NB) & 3) << 1; }
@@ -234,15 +241,15 @@ template <typename G, int BM, int BN> struct Loads {
 #pragma unroll
         for (int j = 0; j < G::IX; ++j) {
             tx[j] = G::template load_row<BM>(j, wave) * G::STEP;
-            const int row = G::template load_row<BM>(j, wave) + (lane >> 3);
-            cx[j] = (uint32_t)((lane & 7) ^ G::swz_x(row)) * 16;
+            const int row = G::template load_row<BM>(j, wave) + lane / G::LPR;
+            cx[j] = G::bytes_at(lane, G::swz_x(row));
             ox[j] = (uint32_t)min(row, a.M - 1 - m0) * (uint32_t)a.xs + cx[j];
         }
 #pragma unroll
         for (int j = 0; j < G::IW; ++j) {
             tw[j] = (BM + G::template load_row<BN>(j, wave)) * G::STEP;
-            const int row = G::template load_row<BN>(j, wave) + (lane >> 3);
-            cw[j] = (uint32_t)((lane & 7) ^ G::swz_w(row)) * 16;
+            const int row = G::template load_row<BN>(j, wave) + lane / G::LPR;
+            cw[j] = G::bytes_at(lane, G::swz_w(row));
             ow[j] = (uint32_t)min(row, a.N - 1 - n0) * (uint32_t)a.ws + cw[j];
         }
     }
@@ -251,11 +258,11 @@ template <typename G, int BM, int BN> struct Loads {
         char* to = lds + place * G::STAGE;
 #pragma unroll
         for (int j = 0; j < G::IX; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, SSD_LDS_PTR(void, to + tx[j]), 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, SSD_LDS_PTR(void, to + tx[j]), G::WIDE,
                                                      cx[j] < left ? ox[j] + k : kNoPiece, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < G::IW; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, SSD_LDS_PTR(void, to + tw[j]), 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, SSD_LDS_PTR(void, to + tw[j]), G::WIDE,
                                                      cw[j] < left ? ow[j] + k : kNoPiece, 0, 0, 0);
     }
 };
@@ -318,9 +325,9 @@ template <typename G, typename M> struct Frags {
 };
 
 // One product, or two of like size in one launch (`other`'s workgroups from `count` on).
-template <int TYPE, int BM, int BN, int WVM, int WVN, int S>
+template <int TYPE, int BM, int BN, int WVM, int WVN, int S, int W>
 __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_linear(LinearArgs one, LinearArgs other, uint32_t count) {
-    typedef LinearTile<TYPE, BM, BN, WVM, WVN, S> G;
+    typedef LinearTile<TYPE, BM, BN, WVM, WVN, S, W> G;
     typedef Mul<TYPE> M;
     extern __shared__ __align__(1024) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -474,22 +481,24 @@ template <typename V> __global__ __launch_bounds__(256) void k_linear_join(Linea
     cols.finish(a, m, v);
 }
 
-template <int TYPE, int BM, int BN, int WVM, int WVN, int S = 2>
+template <int TYPE, int BM, int BN, int WVM, int WVN, int S = 2, int W = 16>
 hipError_t launch_tile(LinearArgs& a, LinearArgs* b, hipStream_t st) {
-    typedef LinearTile<TYPE, BM, BN, WVM, WVN, S> G;
+    typedef LinearTile<TYPE, BM, BN, WVM, WVN, S, W> G;
     const auto groups = [](const LinearArgs& l) {
         return (uint32_t)((int64_t)((l.M + BM - 1) / BM) * ((l.N + BN - 1) / BN) * l.splits);
     };
     uint32_t count = groups(a);
     void* args[] = {&a, b ? b : &a, &count};
-    const void* fn = (const void*)&k_linear<TYPE, BM, BN, WVM, WVN, S>;
+    const void* fn = (const void*)&k_linear<TYPE, BM, BN, WVM, WVN, S, W>;
     return hipLaunchKernel(fn, dim3(b ? count + groups(*b) : count), dim3(G::THREADS), args, G::LDS, st);
 }
 
+constexpr int kNarrowTiles = 16;
 // (b: a second product in the same launch, neither being split, or NULL)
 template <int TYPE> hipError_t launch_linear_type(LinearArgs& a, LinearArgs* b, const LinearPlan& p, hipStream_t st) {
     hipError_t e;
-    switch (p.tile) {  // (kTiles in ssd_linear.hip; what each takes of the 160 KB of LDS decides how many share a CU)
+    // (kTiles in ssd_linear.hip; what each takes of the 160 KB of LDS decides how many share a CU)
+    switch (p.narrow ? kNarrowTiles + p.tile : p.tile) {
     case 0: e = launch_tile<TYPE, 128, 128, 2, 2>(a, b, st); break;
     case 1: e = launch_tile<TYPE, 256, 256, 2, 4>(a, b, st); break;
     case 2: e = launch_tile<TYPE, 128, 192, 2, 2>(a, b, st); break;
@@ -498,6 +507,9 @@ template <int TYPE> hipError_t launch_linear_type(LinearArgs& a, LinearArgs* b, 
     case 5: e = launch_tile<TYPE, 64, 128, 1, 4, 3>(a, b, st); break;
     case 6: e = launch_tile<TYPE, 32, 64, 1, 4, 6>(a, b, st); break;
     case 7: e = launch_tile<TYPE, 16, 64, 1, 4, 8>(a, b, st); break;
+    case kNarrowTiles + 5: e = launch_tile<TYPE, 64, 128, 1, 4, 3, 4>(a, b, st); break;
+    case kNarrowTiles + 6: e = launch_tile<TYPE, 32, 64, 1, 4, 6, 4>(a, b, st); break;
+    case kNarrowTiles + 7: e = launch_tile<TYPE, 16, 64, 1, 4, 7, 4>(a, b, st); break;
     default: e = launch_tile<TYPE, 128, 128, 4, 2, TYPE == LT_E4M3 ? 2 : 4>(a, b, st); break;
     }
     if (e != hipSuccess || a.splits == 1) return e;

@@ -21,6 +21,9 @@ hipError_t launch_linear_e4m3(LinearArgs&, LinearArgs*, const LinearPlan&, hipSt
 // takes 206 us in tiles of 256 x 160 (two full rounds of 256 CUs), 271 us in 256 x 256 and 248 us in 128 x 128; 16 x
 // 5120 x 2560 10.9 us in 16 x 64 split by 4, 13.5 us unsplit.  fp32 is bound by its matrix instructions, 16 times slower: c
 // goes by the area, down to what a step's latency takes.
+// Rows that are no multiple of 16 bytes are copied to ones that are (3 us and their bytes twice at 4 TB/s), or, of a multiple
+// of 4 bytes and in the three smaller tiles, loaded by 4 bytes a lane, whose steps take 1.35 times as long: one row of 2562
+// x 10576 bf16 15.5 us against 35.6 copied, 16 rows 18.7 and 36.4, 128 rows 37 and 47; but fp32 1500 x 1110 x 2000 88 and 77.
 namespace {
 struct TileModel {
     int bm, bn, most;  // workgroups a CU
@@ -44,19 +47,31 @@ static float tiles_us(const TileModel& m, int type, float groups, float steps) {
 static int64_t tiles_of(const TileModel& m, int64_t M, int64_t N) { return ((M + m.bm - 1) / m.bm) * ((N + m.bn - 1) / m.bn); }
 constexpr int64_t kMostGroups = ((int64_t)1 << 32) / 512;  // (lanes of a launch; 256 x 256 always fits)
 
-LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type) {
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type, int64_t copied, bool may_narrow) {
     const int64_t steps = (kbytes + 127) / 128;
-    LinearPlan best{0, 1, 3.4e38f};
+    LinearPlan best{0, 1, 3.4e38f, false};
+    const auto splitting = [&](int splits) { return splits > 1 ? 4.f + (float)splits * (float)M * (float)N * 2e-6f : 0.f; };
     for (int t = 0; t < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
         const int64_t tiles = tiles_of(kTiles[t], M, N);
         for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
             const int64_t per = (steps + splits - 1) / splits;
             if (splits > 1 && (per < 4 || (steps + per - 1) / per != splits)) break;  // (none without a step)
             if (tiles * splits >= kMostGroups) continue;
-            float us = 2.5f + tiles_us(kTiles[t], type, (float)(tiles * splits), (float)per);
-            if (splits > 1) us += 4.f + (float)splits * (float)M * (float)N * 2e-6f;
-            if (us < best.us) best = LinearPlan{t, splits, us};
+            const float us = 2.5f + tiles_us(kTiles[t], type, (float)(tiles * splits), (float)per) + splitting(splits);
+            if (us < best.us) best = LinearPlan{t, splits, us, false};
         }
+    }
+    if (!copied) return best;
+    best.us += 3.f + (float)copied * 0.5e-6f;
+    if (!may_narrow) return best;
+    // (the same splits, so that the same values give the same sums to the bit in rows of any alignment)
+    const int splits = best.splits;
+    const int64_t per = (steps + splits - 1) / splits;
+    for (int t = 5; t <= 7; ++t) {
+        const int64_t groups = tiles_of(kTiles[t], M, N) * splits;
+        if (groups >= kMostGroups) continue;
+        const float us = 2.5f + tiles_us(kTiles[t], type, (float)groups, (float)per * 1.35f) + splitting(splits);
+        if (us < best.us) best = LinearPlan{t, splits, us, true};
     }
     return best;
 }
@@ -65,14 +80,14 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type) {
 // 256 tiles of 256 x 128, 2 x 39 us in 128 x 128): the tile, by the same model, workgroups of a round counted with the
 // longer one's steps where there is but one round, else with the average.  Splits 0: one by one is as fast.
 LinearPlan linear_plan_two(const LinearSize& a, const LinearSize& b, int type) {
-    LinearPlan best{0, 0, a.plan.us + b.plan.us};
+    LinearPlan best{0, 0, a.plan.us + b.plan.us, false};
     const float sa = (float)((a.kbytes + 127) / 128), sb = (float)((b.kbytes + 127) / 128);
     for (int t = 0; t < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
         const int64_t ta = tiles_of(kTiles[t], a.M, a.N), tb = tiles_of(kTiles[t], b.M, b.N);
         if (ta + tb >= kMostGroups) continue;
         const float groups = (float)(ta + tb), mean = ((float)ta * sa + (float)tb * sb) / groups;
         const float us = 2.5f + tiles_us(kTiles[t], type, groups, groups > kCUs * (float)kTiles[t].most ? mean : fmaxf(sa, sb));
-        if (us < best.us) best = LinearPlan{t, 1, us};
+        if (us < best.us) best = LinearPlan{t, 1, us, false};
     }
     return best;
 }

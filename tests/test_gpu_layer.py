@@ -267,6 +267,37 @@ def test_linear_backward_of_unlike_contractions(M, K, N, dtype):
         ref.close(getattr(alone, name), exact, size, n, out, name)
 
 
+@pytest.mark.parametrize("shift,gap", [(4, 8), (16, 4), (2, 2), (0, 16)], ids=str)
+@pytest.mark.parametrize("M,K,N,dtype", [(1, 2562, 300, "bf16"), (16, 1110, 771, "f32"), (70, 302, 130, "f16"), (1, 1, 1, "f32"),
+                                         (33, 1540, 771, "int8"), (5, 260, 64, "e4m3"), (129, 2, 33, "bf16"),
+                                         (600, 1002, 700, "bf16")], ids=str)
+def test_linear_of_rows_between_16_bytes(M, K, N, dtype, shift, gap):
+    """Rows of a multiple of 4 bytes (and ones that are not, by their stride or first byte), among values that would show."""
+    g = gen(45)
+    if dtype in DT:
+        t = DT[dtype]
+        x, w = rn(g, M, K).to(t), (rn(g, N, K) / K**0.5).to(t)
+    elif dtype == "int8":
+        t = torch.int8
+        x, w = (torch.randint(-128, 128, s, generator=g, dtype=t) for s in ((M, K), (N, K)))
+    else:
+        t = torch.float8_e4m3fn
+        x, w = ((100 * rn(g, *s)).clamp(-448, 448).to(t) for s in ((M, K), (N, K)))
+    shift, gap = -(-shift // t.itemsize), -(-gap // t.itemsize)
+    flat = torch.full((M * (K + gap) * t.itemsize + 64,), 0x7f, dtype=torch.uint8, device="cuda")  # (fp16, e4m3: NaN)
+    if dtype in ("bf16", "f32"):
+        flat.fill_(0xff)  # NaN
+    rows = flat.view(t)[shift:shift + M * (K + gap)].view(M, K + gap)[:, :K]
+    rows.view(torch.uint8).copy_(x.cuda().view(torch.uint8))
+    tail = torch.full((N * K * t.itemsize + 64,), 0xff if dtype in ("bf16", "f32") else 0x7f, dtype=torch.uint8, device="cuda")
+    wg = tail.view(t)[:N * K].view(N, K)
+    wg.view(torch.uint8).copy_(w.cuda().view(torch.uint8))
+    got = ssd.linear(rows, wg, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    want, S = (ref.product(x, w, None, None, None, absolute=k) for k in (False, True))
+    ref.close(got, want, S, (0 if dtype == "int8" else 2 * K) + 20, torch.float32, "linear")
+
+
 CODES = [
     # (lead, K, N, type, out type, bias, residual, activation, strided, scales)
     ((1,), 16, 8, "int8", "f32", False, False, None, False, True),
