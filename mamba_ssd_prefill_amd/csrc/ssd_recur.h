@@ -16,8 +16,8 @@
 // Rows of 128 bytes are what the memory wants: reading three tensors of 2 x 8192 x 5120 by walking 32-byte columns of them
 // reached 2.0 TB/s, 64 bytes 2.4, 128 bytes 3.8 on 160 CUs alone (one workgroup a column, a forward pass of 250 us).
 //
-// Measured, bf16 with both gates: forward 174 us at 2 x 8192 x 5120 (671 MB: 3.9 TB/s, a large copy reaches 5.1), 94 us at 2 x
-// 4096 x 5120, whose backward pass takes 162 us.  The vector ALU issues for some 100 of the 174 us, HBM would need 133: what
+// Measured, bf16 with both gates: forward 169 us at 2 x 8192 x 5120 (671 MB: 4.0 TB/s, a large copy reaches 5.1), 92 us at 2 x
+// 4096 x 5120, whose backward pass takes 162 us.  The vector ALU issues for some 100 of the 169 us, HBM would need 133: what
 // holds the time is a tile's chain of ticket, loads, hop and look-back, which three waves a SIMD do not cover wholly.
 #pragma once
 
@@ -30,15 +30,15 @@ namespace ssd {
 // for packed rows and odd channels need more of them).  Measured at 2 x 4096 x 5120, bf16: tiles of 64, 128, 256 tokens
 // forward 270, 183, 177 us at 2 x 8192; backward with 2 and 3 waves a SIMD 210 and 172 us.
 struct RecFwd {
-    static constexpr int W = kRecurWaves, TILE = kRecurTile, EU = 3;
+    static constexpr int W = kRecurWaves, TILE = kRecurTile, EU = 3, FAR = 8;
 };
 struct RecBwd {
-    static constexpr int W = kRecurWaves, TILE = kRecurSaved, EU = 3;
+    static constexpr int W = kRecurWaves, TILE = kRecurSaved, EU = 3, FAR = 4;
 };
 // Lanes of a row of 128 bytes, runs of a wave, tokens of a run, by the element size.
 template <typename T, typename D> struct RecGeo {
     static constexpr int LN = 64 / (int)sizeof(T), CH = 2 * LN, RUNS = 64 / LN, W = D::W, TILE = D::TILE;
-    static constexpr int TOK = TILE / (RUNS * W), THREADS = 64 * W;
+    static constexpr int TOK = TILE / (RUNS * W), THREADS = 64 * W, FAR = sizeof(T) == 4 ? 1 : D::FAR;
     static_assert(RUNS * W * TOK == TILE, "a tile");
     static_assert(kRecurSaved % TOK == 0, "states are kept where a run starts");
 };
@@ -269,51 +269,76 @@ __device__ inline void publish(uint64_t* at, Hop h) {
     __hip_atomic_store(at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The state entering tile `tile` (REV: the gradient behind it) for this lane's two channels.  The words of W tiles (or
-// twice as many) before it are read at a time, one a wave, again until one of them lets nothing through; from there
-// on the hops are applied one by one.  So the result is that of tiles one behind the other to the bit, whichever words
-// were there at which time.  (Windows two and four times as wide: 174 -> 177 and 180 us at 2 x 8192 x 5120.)
-// c0: the workgroup's first channel; `init`: what enters the first tile.  `lds`: [32 * W].
-template <int W, int LN, bool REV>
-__device__ inline void look_back(const RecurArgs& a, int b, int tile, int c0, const void* init, HopPair* lds, float (&h)[2]) {
-    constexpr int CH = 2 * LN, PER = 64 / CH, WIN = W * PER;
-    const int lane = threadIdx.x & 63, place = (int)(threadIdx.x >> 6) * PER + lane / CH, c = c0 + lane % CH;
-    const int t = REV ? tile + 1 + place : tile - 1 - place;
-    const bool there = c < a.channels && t >= 0 && t < a.ntiles;
-    const uint64_t* at = a.hops + (there ? ((int64_t)b * a.ntiles + t) * a.channels + c : 0);
-    Hop r{-1.f, 0.f};
-    if (!there && c < a.channels && init) r.q = state_at(init, a.state_dtype, (int64_t)b * a.channels + c);
-    int looks = 0;
-    for (int round = 0;; ++round) {
-        if (there) {
-            uint64_t v = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            while (v == kNoHop && looks < kMaxLooks) {
-                __builtin_amdgcn_s_sleep(1);
-                v = __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                ++looks;
-            }
-            r = v == kNoHop ? Hop{-1.f, __builtin_nanf("")} : Hop{unbits((uint32_t)(v >> 32)), unbits((uint32_t)v)};
+// The state entering tile `tile` (REV: the gradient behind it) for this lane's two channels.  The words of W tiles (fp32:
+// twice as many) before it are read at a time, one a wave; if none of them lets nothing through, those of FAR times as many
+// are, again until one does.  From there on the hops are applied one by one.  So the result is that of tiles one behind the
+// other to the bit, whichever words were there at which time.  (2 x 8192 x 5120 bf16: the near windows alone 174 us, eight times as
+// many where they do not do 169, 16 and 32 tiles at every look 177 and 180; training at 2 x 4096 x 5120 262 and 258 us.
+// fp32, 1 x 3001 x 1110: 24.5 us, 25.7 with a far window of 32 tiles.)
+// c0: the workgroup's first channel; `init`: what enters the first tile.  `lds`: [32 * W * FAR].
+template <int W, int LN, bool REV, int FAR> struct LookBack {
+    static constexpr int CH = 2 * LN, PER = 64 / CH, WIN = W * PER;
+    const uint64_t* base;
+    HopPair* lds;
+    Hop init;
+    int tile, tiles, stride, c, place, looks;
+    bool live;
+    __device__ inline LookBack(const RecurArgs& a, int b, int tile_, int c0, const void* first, HopPair* lds_)
+        : lds(lds_), init{-1.f, 0.f}, tile(tile_), tiles(a.ntiles), stride(a.channels), looks(0) {
+        const int lane = threadIdx.x & 63;
+        place = (int)(threadIdx.x >> 6) * PER + lane / CH;
+        c = c0 + lane % CH;
+        live = c < a.channels;
+        base = a.hops + (int64_t)b * a.ntiles * a.channels + (live ? c : 0);
+        if (live && first) init.q = state_at(first, a.state_dtype, (int64_t)b * a.channels + c);
+    }
+    // Whether the words of N windows tell it all, and the state if so.
+    template <int N> __device__ inline bool look(float (&h)[2]) {
+        const int lane = threadIdx.x & 63;
+        uint64_t v[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int t = REV ? tile + 1 + place + n * WIN : tile - 1 - place - n * WIN;
+            v[n] = 0;
+            if (live && t >= 0 && t < tiles)
+                v[n] = __hip_atomic_load(base + (int64_t)t * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        ((f32x2*)lds)[place * CH + lane % CH] = f32x2{r.p, r.q};
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int t = REV ? tile + 1 + place + n * WIN : tile - 1 - place - n * WIN;
+            Hop r = init;
+            if (live && t >= 0 && t < tiles) {
+                while (v[n] == kNoHop && looks < kMaxLooks) {
+                    __builtin_amdgcn_s_sleep(1);
+                    v[n] = __hip_atomic_load(base + (int64_t)t * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    ++looks;
+                }
+                r = v[n] == kNoHop ? Hop{-1.f, __builtin_nanf("")} : Hop{unbits((uint32_t)(v[n] >> 32)), unbits((uint32_t)v[n])};
+            }
+            ((f32x2*)lds)[(n * WIN + place) * CH + lane % CH] = f32x2{r.p, r.q};
+        }
         __syncthreads();
         bool found[2] = {false, false};
         h[0] = h[1] = 0.f;
 #pragma unroll 2
-        for (int i = WIN - 1; i >= 0; --i) {
+        for (int i = N * WIN - 1; i >= 0; --i) {
             const HopPair o = lds[i * LN + (lane & (LN - 1))];
             found[0] = found[0] || o[0] < 0.f;
             found[1] = found[1] || o[2] < 0.f;
             h[0] = after<true>(Hop{o[0], o[1]}, h[0]);
             h[1] = after<true>(Hop{o[2], o[3]}, h[1]);
         }
-        if (__all(found[0] && found[1])) break;  // (the same in every wave)
-        if (round == kMaxLooks) {
-            h[0] = h[1] = __builtin_nanf("");
-            break;
-        }
-        __syncthreads();
+        return __all(found[0] && found[1]);  // (the same in every wave)
     }
-}
+    __device__ inline void run(float (&h)[2]) {
+        if (look<1>(h)) return;
+        for (int round = 0; round < kMaxLooks; ++round) {
+            __syncthreads();
+            if (look<FAR>(h)) return;
+        }
+        h[0] = h[1] = __builtin_nanf("");
+    }
+};
 
 // A workgroup's tile.  The workgroups are dealt to the chains (a block of channels of a batch row) in turn, and a chain's
 // take its tiles in the order that they start (REV: from the last), by a counter a chain.  (Neighbouring chains
@@ -420,7 +445,7 @@ __global__ __launch_bounds__(64 * RecFwd::W, RecFwd::EU) void k_recur(RecurArgs 
     typedef RecTile<T, PAIRED, PACKED, G, F> Tile;
     typedef typename Tile::Rows Rows;
     __shared__ HopPair waves[W * LN];
-    __shared__ HopPair looked[W * 32];
+    __shared__ HopPair looked[W * 32 * G::FAR];
     const RecPlace p = rec_place<G, false>(a);
     const int t0 = p.tile * G::TILE;
     uint32_t ch[2];
@@ -488,7 +513,7 @@ __global__ __launch_bounds__(64 * RecFwd::W, RecFwd::EU) void k_recur(RecurArgs 
     }
     float h[2];
     if (p.tile > 0) {
-        look_back<W, LN, false>(a, p.b, p.tile, p.block0, PACKED ? nullptr : a.h0, looked, h);
+        LookBack<W, LN, false, G::FAR>(a, p.b, p.tile, p.block0, PACKED ? nullptr : a.h0, looked).run(h);
     } else {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -537,7 +562,7 @@ __global__ __launch_bounds__(64 * RecBwd::W, PAIRED && !PACKED ? RecBwd::EU : 2)
     typedef RecTile<T, PAIRED, PACKED, G, F> Tile;
     typedef typename Tile::Rows Rows;
     __shared__ HopPair waves[2][W * LN];
-    __shared__ HopPair looked[W * 32];
+    __shared__ HopPair looked[W * 32 * G::FAR];
     __shared__ f32x4 parked[TOK][64 * W];  // r and A (1 - r) of a lane's tokens, which are not needed before the gradients
     const RecPlace p = rec_place<G, true>(a);
     const int t0 = p.tile * G::TILE, n = min(a.seqlen - t0, G::TILE);
@@ -670,7 +695,7 @@ __global__ __launch_bounds__(64 * RecBwd::W, PAIRED && !PACKED ? RecBwd::EU : 2)
     }
     float v[2];
     if (p.tile + 1 < a.ntiles) {
-        look_back<W, LN, true>(a, p.b, p.tile, p.block0, PACKED ? nullptr : a.dfin, looked, v);
+        LookBack<W, LN, true, G::FAR>(a, p.b, p.tile, p.block0, PACKED ? nullptr : a.dfin, looked).run(v);
     } else {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
