@@ -189,11 +189,8 @@ LinearLayout linear_layout(const ssd_linear_params_t* p) {
     l.pack_x = l.kp != K || !rows_fit(xs, es, 16);
     l.may_pack_x = l.pack_x || xs != K;  // a view's rows may start anywhere
     const int64_t copied = ((l.pack_x ? p->rows : 0) + (l.pack_w ? (int64_t)p->outs : 0)) * K * (int64_t)es;
-    l.plan = ssd::linear_plan(p->rows, p->outs, l.kp * es, p->in_dtype, copied, copied && K * es % 4 == 0);
-    if (l.plan.narrow) {
-        l.pack_w = false;
-        l.pack_x = !rows_fit(xs, es, 4);
-    }
+    l.plan = ssd::linear_plan(p->rows, p->outs, l.kp * es, p->in_dtype, copied, rows_fit(K, es, 4) && rows_fit(xs, es, 4));
+    if (l.plan.narrow) l.pack_w = l.pack_x = false;
     Regions r;
     l.x_off = l.may_pack_x ? r.add((size_t)p->rows * l.kp * es) : 0;
     l.w_off = l.pack_w ? r.add((size_t)p->outs * l.kp * es) : 0;
