@@ -356,7 +356,10 @@ SSD_EXPORT ssd_status_t ssd_linear_backward(const ssd_linear_params_t* p, const 
     };
     ssd::LinearArgs x_args = product(rows ? ws + l.rows_off : dout, wt.dst, M, l.np * es, dx);
     ssd::LinearArgs w_args = product(ws + l.cols_off, xt.dst, N, l.mp * es, dweight);
-    if (dx && dweight && l.both_plan.splits) return hip_status(ssd::launch_linear(x_args, &w_args, p->in_dtype, l.both_plan, st));
+    if (dx && dweight && l.both_plan.splits) {  // (the longer contraction's workgroups first)
+        ssd::LinearArgs &first = N > M ? x_args : w_args, &then = N > M ? w_args : x_args;
+        return hip_status(ssd::launch_linear(first, &then, p->in_dtype, l.both_plan, st));
+    }
     if (dx) {
         const hipError_t e = ssd::launch_linear(x_args, nullptr, p->in_dtype, l.dx_plan, st);
         if (e != hipSuccess) return hip_status(e);

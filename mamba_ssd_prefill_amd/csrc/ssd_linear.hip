@@ -37,12 +37,12 @@ constexpr TileModel kTiles[] = {
 constexpr float kCUs = 256.f;
 }  // namespace
 
-// The time of `groups` workgroups of so many steps.
-static float tiles_us(const TileModel& m, int type, float groups, float steps) {
+// The time of `groups` workgroups of so many steps, `longest` of one of them.
+static float tiles_us(const TileModel& m, int type, float groups, float steps, float longest = 0.f) {
     int o = 1;
     while (o < m.most && groups > kCUs * (float)o) ++o;
     const float c = type == LT_F32 ? fmaxf(0.2f, 1.95f * (float)o * (float)(m.bm * m.bn) / 16384.f) : m.c[o - 1];
-    return ceilf(groups / (kCUs * (float)o)) * (steps * c + m.e);
+    return fmaxf(ceilf(groups / (kCUs * (float)o)) * (steps * c + m.e), longest * c + m.e);
 }
 static int64_t tiles_of(const TileModel& m, int64_t M, int64_t N) { return ((M + m.bm - 1) / m.bm) * ((N + m.bn - 1) / m.bn); }
 constexpr int64_t kMostGroups = ((int64_t)1 << 32) / 512;  // (lanes of a launch; 256 x 256 always fits)
@@ -76,9 +76,10 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type, int64_t c
     return best;
 }
 
-// Two products in one launch, where their tiles fill the chip better than each product's alone (4096 x 4096 x 1024 twice, f16: 65 us in
-// 256 tiles of 256 x 128, 2 x 39 us in 128 x 128): the tile, by the same model, workgroups of a round counted with the
-// longer one's steps where there is but one round, else with the average.  Splits 0: one by one is as fast.
+// Two products in one launch, where their tiles fill the chip better than each product's alone (4096 x 4096 x 1024 twice,
+// f16: 65 us in 256 tiles of 256 x 128, 2 x 39 us in 128 x 128): the tile, by the same model, with the average of the
+// workgroups' steps, and no less than the longest takes.  (Products of unlike contractions go one by one: 512 x 2560 x 10576,
+// f16, takes 90 us so, 260 in one launch of 256 x 256.)  Splits 0: one by one is as fast.
 LinearPlan linear_plan_two(const LinearSize& a, const LinearSize& b, int type) {
     LinearPlan best{0, 0, a.plan.us + b.plan.us, false};
     const float sa = (float)((a.kbytes + 127) / 128), sb = (float)((b.kbytes + 127) / 128);
@@ -86,7 +87,7 @@ LinearPlan linear_plan_two(const LinearSize& a, const LinearSize& b, int type) {
         const int64_t ta = tiles_of(kTiles[t], a.M, a.N), tb = tiles_of(kTiles[t], b.M, b.N);
         if (ta + tb >= kMostGroups) continue;
         const float groups = (float)(ta + tb), mean = ((float)ta * sa + (float)tb * sb) / groups;
-        const float us = 2.5f + tiles_us(kTiles[t], type, groups, groups > kCUs * (float)kTiles[t].most ? mean : fmaxf(sa, sb));
+        const float us = 2.5f + tiles_us(kTiles[t], type, groups, mean, fmaxf(sa, sb));
         if (us < best.us) best = LinearPlan{t, 1, us, false};
     }
     return best;

@@ -247,7 +247,7 @@ def test_linear_backward(case):
 
 
 @pytest.mark.parametrize("M,K,N,dtype", [(2100, 520, 1300, "f16"), (300, 1030, 4100, "bf16"), (4099, 257, 130, "bf16"),
-                                         (1030, 390, 771, "f32")], ids=str)
+                                         (1030, 390, 771, "f32"), (3, 1044, 2514, "f16"), (2514, 1044, 3, "bf16")], ids=str)
 def test_linear_backward_of_unlike_contractions(M, K, N, dtype):
     """Both products in one launch or two, their contractions (N and M) of other lengths, alone and together."""
     say("linear backward", M, K, N, dtype)
