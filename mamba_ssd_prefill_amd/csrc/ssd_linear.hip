@@ -26,7 +26,8 @@ hipError_t launch_linear_e4m3(LinearArgs&, LinearArgs*, const LinearPlan&, hipSt
 // x 10576 bf16 15.5 us against 35.6 copied, 16 rows 18.7 and 36.4, 128 rows 37 and 47; but fp32 1500 x 1110 x 2000 88 and 77.
 namespace {
 struct TileModel {
-    int bm, bn, most;  // workgroups a CU
+    uint32_t bm, bn;
+    int most;  // workgroups a CU
     float c[2], e;
 };
 constexpr TileModel kTiles[] = {
@@ -34,30 +35,36 @@ constexpr TileModel kTiles[] = {
     {256, 160, 1, {1.15f, 0.f}, 5.f},   {256, 128, 1, {0.88f, 0.f}, 5.f},    {64, 128, 2, {0.45f, 0.60f}, 2.5f},
     {32, 64, 2, {0.17f, 0.30f}, 2.f},   {16, 64, 2, {0.165f, 0.28f}, 2.f},   {128, 128, 1, {0.50f, 0.f}, 4.f},
 };
-constexpr float kCUs = 256.f;
+constexpr int kTileCount = sizeof(kTiles) / sizeof(kTiles[0]);
+constexpr uint32_t kCUs = 256;
 }  // namespace
 
 // The time of `groups` workgroups of so many steps, `longest` of one of them.
-static float tiles_us(const TileModel& m, int type, float groups, float steps, float longest = 0.f) {
-    int o = 1;
-    while (o < m.most && groups > kCUs * (float)o) ++o;
-    const float c = type == LT_F32 ? fmaxf(0.2f, 1.95f * (float)o * (float)(m.bm * m.bn) / 16384.f) : m.c[o - 1];
-    return fmaxf(ceilf(groups / (kCUs * (float)o)) * (steps * c + m.e), longest * c + m.e);
+static inline float tiles_us(const TileModel& m, int type, int64_t groups, float steps, float longest = 0.f) {
+    const int o = m.most > 1 && groups > kCUs ? 2 : 1;
+    const float f32 = 1.95f / 16384.f * (float)(o * m.bm * m.bn), c = type != LT_F32 ? m.c[o - 1] : f32 > 0.2f ? f32 : 0.2f;
+    const float all = (float)((groups + kCUs * o - 1) / (kCUs * o)) * (steps * c + m.e), one = longest * c + m.e;
+    return all > one ? all : one;
 }
-static int64_t tiles_of(const TileModel& m, int64_t M, int64_t N) { return ((M + m.bm - 1) / m.bm) * ((N + m.bn - 1) / m.bn); }
+static inline int64_t tiles_of(const TileModel& m, int64_t M, int64_t N) {
+    return (int64_t)(((uint32_t)M + m.bm - 1) / m.bm) * (((uint32_t)N + m.bn - 1) / m.bn);
+}
 constexpr int64_t kMostGroups = ((int64_t)1 << 32) / 512;  // (lanes of a launch; 256 x 256 always fits)
 
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type, int64_t copied, bool may_narrow) {
     const int64_t steps = (kbytes + 127) / 128;
     LinearPlan best{0, 1, 3.4e38f, false};
     const auto splitting = [&](int splits) { return splits > 1 ? 4.f + (float)splits * (float)M * (float)N * 2e-6f : 0.f; };
-    for (int t = 0; t < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
-        const int64_t tiles = tiles_of(kTiles[t], M, N);
-        for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
-            const int64_t per = (steps + splits - 1) / splits;
-            if (splits > 1 && (per < 4 || (steps + per - 1) / per != splits)) break;  // (none without a step)
-            if (tiles * splits >= kMostGroups) continue;
-            const float us = 2.5f + tiles_us(kTiles[t], type, (float)(tiles * splits), (float)per) + splitting(splits);
+    int64_t tiles[kTileCount];
+    for (int t = 0; t < kTileCount; ++t) tiles[t] = tiles_of(kTiles[t], M, N);
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        const uint32_t per = ((uint32_t)steps + splits - 1) / splits;
+        if (splits > 1 && (per < 4 || ((uint32_t)steps + per - 1) / per != (uint32_t)splits)) break;  // (none without a step)
+        const float rest = 2.5f + splitting(splits);
+        if (rest >= best.us) break;
+        for (int t = 0; t < kTileCount; ++t) {
+            if (tiles[t] * splits >= kMostGroups) continue;
+            const float us = rest + tiles_us(kTiles[t], type, tiles[t] * splits, (float)per);
             if (us < best.us) best = LinearPlan{t, splits, us, false};
         }
     }
@@ -68,9 +75,9 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type, int64_t c
     const int splits = best.splits;
     const int64_t per = (steps + splits - 1) / splits;
     for (int t = 5; t <= 7; ++t) {
-        const int64_t groups = tiles_of(kTiles[t], M, N) * splits;
+        const int64_t groups = tiles[t] * splits;
         if (groups >= kMostGroups) continue;
-        const float us = 2.5f + tiles_us(kTiles[t], type, (float)groups, (float)per * 1.35f) + splitting(splits);
+        const float us = 2.5f + tiles_us(kTiles[t], type, groups, (float)per * 1.35f) + splitting(splits);
         if (us < best.us) best = LinearPlan{t, splits, us, true};
     }
     return best;
@@ -83,11 +90,11 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type, int64_t c
 LinearPlan linear_plan_two(const LinearSize& a, const LinearSize& b, int type) {
     LinearPlan best{0, 0, a.plan.us + b.plan.us, false};
     const float sa = (float)((a.kbytes + 127) / 128), sb = (float)((b.kbytes + 127) / 128);
-    for (int t = 0; t < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
+    for (int t = 0; t < kTileCount; ++t) {
         const int64_t ta = tiles_of(kTiles[t], a.M, a.N), tb = tiles_of(kTiles[t], b.M, b.N);
         if (ta + tb >= kMostGroups) continue;
-        const float groups = (float)(ta + tb), mean = ((float)ta * sa + (float)tb * sb) / groups;
-        const float us = 2.5f + tiles_us(kTiles[t], type, groups, mean, fmaxf(sa, sb));
+        const float mean = ((float)ta * sa + (float)tb * sb) / (float)(ta + tb);
+        const float us = 2.5f + tiles_us(kTiles[t], type, ta + tb, mean, sa > sb ? sa : sb);
         if (us < best.us) best = LinearPlan{t, 1, us, false};
     }
     return best;
