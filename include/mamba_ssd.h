@@ -671,9 +671,9 @@ typedef struct {
  *   out          [M, N]  out_dtype  required, contiguous.  May be the residual itself (residual_stride 0 or N); overlaps it
  *                                   nowhere else
  *   workspace            256-byte aligned, ssd_linear_workspace_size() bytes
- * x is 16-byte aligned where it is contiguous with rows of a multiple of 16 bytes; else it has its element's
- * alignment.  (Rows that are no multiple of 16 bytes, or do not start on one, are loaded by 4 bytes or copied to the workspace first;
- * the sums are the same to the bit.) */
+ * x is 16-byte aligned where x_stride is 0 and its rows are a multiple of 16 bytes; else it has its element's alignment (so
+ * x_stride = K takes contiguous rows that start anywhere, for a workspace with room to copy them).  (Rows that are no multiple of
+ * 16 bytes, or do not start on one, are loaded by 4 bytes or copied to the workspace first; the sums are the same to the bit.) */
 size_t ssd_linear_workspace_size(const ssd_linear_params_t* p);
 ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, const void* weight, const float* bias,
                         const void* residual, const float* x_scale, const float* weight_scale, void* pre, void* out,

@@ -187,7 +187,7 @@ LinearLayout linear_layout(const ssd_linear_params_t* p) {
     l.kp = padded(K, es);
     l.pack_w = l.kp != K;
     l.pack_x = l.kp != K || !rows_fit(xs, es, 16);
-    l.may_pack_x = l.pack_x || xs != K;  // a view's rows may start anywhere
+    l.may_pack_x = l.pack_x || p->x_stride;  // a view's rows, also of one row, may start anywhere
     const int64_t copied = ((l.pack_x ? p->rows : 0) + (l.pack_w ? (int64_t)p->outs : 0)) * K * (int64_t)es;
     l.plan = ssd::linear_plan(p->rows, p->outs, l.kp * es, p->in_dtype, copied, rows_fit(K, es, 4) && rows_fit(xs, es, 4));
     if (l.plan.narrow) l.pack_w = l.pack_x = false;

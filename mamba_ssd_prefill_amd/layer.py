@@ -208,7 +208,7 @@ def _linear_params(x, weight, act, out_dtype, what):
                         0), dev, lead
 
 
-def _linear_plan(x, weight, bias, residual, act, x_scale, weight_scale, out_dtype, out):
+def _linear_plan(x, weight, bias, residual, act, x_scale, weight_scale, out_dtype, out, off):
     import torch
     if out_dtype is None:
         given = [t for t in (out, residual) if t is not None]
@@ -217,6 +217,8 @@ def _linear_plan(x, weight, bias, residual, act, x_scale, weight_scale, out_dtyp
         out_dtype = given[0].dtype if given else x.dtype
     prm, dev, lead = _linear_params(x, weight, act, out_dtype, "linear")
     N = prm.outs
+    if off and not prm.x_stride:  # rows of a view, as the library sees it: they may start anywhere
+        prm.x_stride = prm.width
     _s._same(dev, torch.float32, bias=(bias, (N,)), x_scale=(x_scale, lead), weight_scale=(weight_scale, (N,)))
     if residual is not None:
         prm.residual_stride = _s._rows("residual", residual, dev, out_dtype, lead + (N,), len(lead))
@@ -232,10 +234,11 @@ def linear(x, weight, bias=None, residual=None, *, activation=None, x_scale=None
     ``out_dtype`` (default: out's, the residual's, or x's), and with ``save_pre`` (out, pre) for linear_backward.  ``out`` may
     be the (contiguous) residual itself."""
     meta, (px, pw, pb, pr, psx, psw, _) = _s._meta(x, weight, bias, residual, x_scale, weight_scale, out)
-    key = ("linear", meta, activation, out_dtype)
+    off = px & 15 != 0  # contiguous rows of a view: one row of a batch, or ones behind an odd offset
+    key = ("linear", meta, activation, out_dtype, off)
     plan = _s._PLANS.get(key) or _s._older(key)
     if plan is None:
-        plan = _s._keep(key, _linear_plan(x, weight, bias, residual, activation, x_scale, weight_scale, out_dtype, out))
+        plan = _s._keep(key, _linear_plan(x, weight, bias, residual, activation, x_scale, weight_scale, out_dtype, out, off))
     if out is None and workspace is None:
         out, workspace = _s._new(plan.out, plan.spaces[0])
     else:

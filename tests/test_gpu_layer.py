@@ -298,6 +298,30 @@ def test_linear_of_rows_between_16_bytes(M, K, N, dtype, shift, gap):
     ref.close(got, want, S, (0 if dtype == "int8" else 2 * K) + 20, torch.float32, "linear")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("M,K,N,shift", [(1, 64, 70, 1), (1, 64, 70, 3), (1, 2560, 300, 5), (2, 64, 70, 1), (200, 192, 130, 7),
+                                         (1, 64, 70, 16)], ids=str)
+def test_linear_of_contiguous_rows_that_start_anywhere(M, K, N, shift, dtype):
+    """A slice of one row, and rows behind an odd offset, both contiguous: the bits of the same values on a border."""
+    say("contiguous rows", M, K, N, shift, dtype)
+    g = gen(46)
+    if dtype in DT:
+        wide, w = rn(g, M * K + 16).to(DT[dtype]).cuda(), (rn(g, N, K) / K**0.5).to(DT[dtype]).cuda()
+    else:
+        wide, w = (torch.randint(-100, 100, s, generator=g, dtype=torch.int8).cuda() for s in ((M * K + 16,), (N, K)))
+        if dtype == "e4m3":
+            wide, w = wide.float().to(torch.float8_e4m3fn), w.float().to(torch.float8_e4m3fn)
+    x = wide[None, shift:shift + K] if M == 1 else wide[shift:shift + M * K].view(M, K)
+    assert x.is_contiguous() and x.data_ptr() % 16 == shift * x.element_size() % 16
+    aligned = torch.empty_like(x).copy_(x)
+    want = ssd.linear(aligned, w, out_dtype=torch.float32)
+    for _ in range(2):
+        assert torch.equal(ssd.linear(x, w, out_dtype=torch.float32), want)
+        assert torch.equal(ssd.linear(aligned, w, out_dtype=torch.float32), want)
+    pre, S = (ref.product(aligned.cpu(), w.cpu(), absolute=k) for k in (False, True))
+    ref.close(want, pre, S, 2 * K + 20, torch.float32, "linear")
+
+
 CODES = [
     # (lead, K, N, type, out type, bias, residual, activation, strided, scales)
     ((1,), 16, 8, "int8", "f32", False, False, None, False, True),

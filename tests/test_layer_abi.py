@@ -132,6 +132,19 @@ def test_misaligned(lib, name):
         assert call(lib, name, linear_prm(x_stride=70), x=FAKE + 1) == MISAL
 
 
+@pytest.mark.parametrize("dtype,es", [(0, 4), (1, 2), (2, 2), (3, 1), (4, 1)])
+@pytest.mark.parametrize("rows", [1, 30])
+def test_contiguous_rows_that_start_anywhere(lib, dtype, es, rows):
+    """One row of a view counts as contiguous, and so do rows behind an odd offset: with their stride given they are taken as a
+    view's are, and the workspace has room to copy them."""
+    prm, size = linear_prm(in_dtype=dtype, rows=rows, x_stride=64), lib.ssd_linear_workspace_size
+    assert call(lib, "ssd_linear", prm, x=FAKE + es, ws_bytes=0) == WS_SMALL
+    if es > 1:
+        assert call(lib, "ssd_linear", prm, x=FAKE + es // 2) == MISAL
+    room = size(ctypes.byref(prm)) - size(ctypes.byref(linear_prm(in_dtype=dtype, rows=rows)))
+    assert room >= rows * 64 * es - 256  # (a product without copies has one region of 256 bytes)
+
+
 @pytest.mark.parametrize("name", ["ssd_rms_norm", "ssd_rms_norm_backward"])
 @pytest.mark.parametrize("kw,code", [
     (dict(rows=0), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=1 << 31), SHAPE), (dict(width=0), SHAPE), (dict(width=16385), UNSUP),
