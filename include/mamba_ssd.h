@@ -662,7 +662,8 @@ typedef struct {
 } ssd_linear_params_t;
 
 /*   x            [M, K]  in_dtype   required, rows
- *   weight       [N, K]  in_dtype   required, 16-byte aligned
+ *   weight       [N, K]  in_dtype   required; 16-byte aligned where its rows are a multiple of 16 bytes, else 4-byte aligned where
+ *                                   they are a multiple of 4, else with its element's alignment
  *   bias         [N]     fp32       NULL means 0
  *   residual     [M, N]  out_dtype  rows; NULL: none
  *   x_scale      [M]     fp32       NULL means 1; only with operands in 8 bits

@@ -167,6 +167,9 @@ ssd_status_t validate_linear(const ssd_linear_params_t* p, bool backward) {
     return SSD_OK;
 }
 
+// Where weight has to start so that rows cut out of one that starts on 16 bytes are taken: loaded as they are, or copied.
+size_t weight_align(int64_t row_bytes, size_t es) { return row_bytes % 16 == 0 ? 16 : row_bytes % 4 == 0 ? 4 : es; }
+
 bool rows_fit(int64_t stride, size_t es, size_t piece) {
     return stride * es % piece == 0 && stride * (int64_t)es < kMaxRowBytes;
 }
@@ -215,7 +218,7 @@ SSD_EXPORT ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, 
     if ((x_scale || weight_scale) && p->in_dtype < SSD_IN_INT8) return SSD_ERR_INVALID_ARGUMENT;
     const size_t es = elem_size(p->in_dtype), os = elem_size(p->out_dtype);
     LinearLayout l = linear_layout(p);
-    if (!aligned(x, l.may_pack_x ? es : 16) || !aligned(weight, 16) || !aligned(bias, 4) || !aligned(residual, os) ||
+    if (!aligned(x, l.may_pack_x ? es : 16) || !aligned(weight, weight_align(p->width * (int64_t)es, es)) || !aligned(bias, 4) || !aligned(residual, os) ||
         !aligned(x_scale, 4) || !aligned(weight_scale, 4) || !aligned(pre, os) || !aligned(out, os) ||
         !aligned(workspace, kAlign))
         return SSD_ERR_MISALIGNED;

@@ -322,6 +322,27 @@ def test_linear_of_contiguous_rows_that_start_anywhere(M, K, N, shift, dtype):
     ref.close(want, pre, S, 2 * K + 20, torch.float32, "linear")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("M,K,N,first", [(1, 77, 70, 1), (3, 1541, 130, 3), (200, 259, 300, 5), (1, 1542, 70, 3), (5, 70, 64, 1),
+                                         (300, 1002, 520, 7)], ids=str)
+def test_linear_with_rows_cut_out_of_a_joint_weight(M, K, N, first, dtype):
+    """Part of a weight whose rows are no multiple of 16 bytes: the bits of a weight of its own."""
+    say("part of a weight", M, K, N, first, dtype)
+    g = gen(47)
+    if dtype in DT:
+        x, joint = rn(g, M, K).to(DT[dtype]).cuda(), (rn(g, N + first + 2, K) / K**0.5).to(DT[dtype]).cuda()
+    else:
+        x, joint = (torch.randint(-100, 100, s, generator=g, dtype=torch.int8).cuda() for s in ((M, K), (N + first + 2, K)))
+        if dtype == "e4m3":
+            x, joint = x.float().to(torch.float8_e4m3fn), joint.float().to(torch.float8_e4m3fn)
+    joint[:first], joint[first + N:] = (NAN, NAN) if dtype != "int8" else (127, 127)
+    w = joint[first:first + N]
+    got = ssd.linear(x, w, out_dtype=torch.float32)
+    assert torch.equal(got, ssd.linear(x, torch.empty_like(w).copy_(w), out_dtype=torch.float32))
+    pre, S = (ref.product(x.cpu(), w.cpu(), absolute=k) for k in (False, True))
+    ref.close(got, pre, S, 2 * K + 20, torch.float32, "linear")
+
+
 CODES = [
     # (lead, K, N, type, out type, bias, residual, activation, strided, scales)
     ((1,), 16, 8, "int8", "f32", False, False, None, False, True),

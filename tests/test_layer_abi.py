@@ -133,6 +133,20 @@ def test_misaligned(lib, name):
 
 
 @pytest.mark.parametrize("dtype,es", [(0, 4), (1, 2), (2, 2), (3, 1), (4, 1)])
+@pytest.mark.parametrize("rows", [1, 30, 4000])
+def test_rows_cut_out_of_a_joint_weight(lib, dtype, es, rows):
+    """A weight that starts k rows behind an aligned one's first row is taken, whatever the rows' length."""
+    for width in (64, 63, 65, 66, 68, 72, 1, 2, 2561, 2562):
+        row = width * es
+        prm = linear_prm(in_dtype=dtype, rows=rows, width=width)
+        for k in (1, 2, 3, 7):
+            assert call(lib, "ssd_linear", prm, w=FAKE + k * row, ws_bytes=0) == WS_SMALL, (width, k)
+        need = 16 if row % 16 == 0 else 4 if row % 4 == 0 else es
+        if need > 1:
+            assert call(lib, "ssd_linear", prm, w=FAKE + need // 2) == MISAL, width
+
+
+@pytest.mark.parametrize("dtype,es", [(0, 4), (1, 2), (2, 2), (3, 1), (4, 1)])
 @pytest.mark.parametrize("rows", [1, 30])
 def test_contiguous_rows_that_start_anywhere(lib, dtype, es, rows):
     """One row of a view counts as contiguous, and so do rows behind an odd offset: with their stride given they are taken as a
