@@ -604,6 +604,7 @@ ssd_status_t ssd_state_cache_read(const ssd_cache_params_t* p, const void* codes
  * rounded to sum_dtype, and y is that of s before this rounding.
  * In 8 bits (format): the row has one scale, y becomes codes as in the state cache above:
  *     scale = max|y| / 127 (int8) or / 448 (e4m3),  code = y / scale rounded to the nearest code, ties to even
+ * with everything behind s in fp64 (the scale is rounded to fp32, the quotient is by the rounded one).
  * A row that holds an infinity or a NaN gets a NaN scale, one whose scale would be below 2^-80 scale 0; both
  * have codes 0. */
 typedef struct {

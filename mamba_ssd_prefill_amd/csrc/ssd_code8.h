@@ -1,5 +1,5 @@
 // ssd_code8.h -- values in 8 bits with one fp32 scale for a run of them: v / scale rounded to a code of int8 or e4m3
-// (the state cache's groups, the norm's rows).
+// (the state cache's groups; the norm's rows, whose quotients are of 64 bits).
 #pragma once
 
 #include "ssd_device.h"

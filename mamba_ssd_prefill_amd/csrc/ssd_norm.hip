@@ -69,13 +69,8 @@ __device__ inline float wave_sum(float v) {
     for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
     return v;
 }
-__device__ inline uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m, 64));
-    return v;
-}
 
-// Sums (or the largest) over the W waves of a row, in one order for every lane.  `lds`: W values of its own.
+// Sums over the W waves of a row, in one order for every lane.  `lds`: W values of its own.
 template <int W> __device__ inline float row_sum(float v, float* lds) {
     v = wave_sum(v);
     if constexpr (W > 1) {
@@ -106,52 +101,85 @@ template <int W> __device__ inline void row_sums(float& v, float& u, float* lds)
         }
     }
 }
-template <int W> __device__ inline uint32_t row_max(uint32_t v, uint32_t* lds) {
-    v = wave_max(v);
+// In 64 bits: the sum of v, and the largest of u (neither negative).
+template <int W> __device__ inline void row_sum_max(double& v, double& u, double* lds) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) {
+        v += __shfl_xor(v, m, 64);
+        u = __builtin_fmax(u, __shfl_xor(u, m, 64));
+    }
     if constexpr (W > 1) {
         const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) lds[wave] = v;
+        if ((threadIdx.x & 63) == 0) {
+            lds[wave] = v;
+            lds[W + wave] = u;
+        }
         __syncthreads();
+        v = u = 0;
 #pragma unroll
-        for (int i = 0; i < W; ++i) v = max(v, lds[i]);
+        for (int i = 0; i < W; ++i) {
+            v += lds[i];
+            u = __builtin_fmax(u, lds[W + i]);
+        }
     }
-    return v;
 }
 
-// The codes of VEC values at scale s.  (The conversion instruction rounds to the nearest e4m3 value, ties to even, from the
-// quotient rounded to odd as well as code_e4m3 does in a dozen instructions: 2048 x 2560 values 15.8 -> 14.5 us.)
-template <int VEC> __device__ inline void codes_of(const float (&v)[VEC], float s, float inv, int format, uint8_t (&c)[VEC]) {
+// 1 / v and 1 / sqrt(v) by Newton's steps from the instructions' 23 bits or so, some 2^-45 and 2^-52 off (NaN for 0 and the
+// infinities, whose rows have no codes).
+__device__ inline double inverse(double v) {
+    const double q = __builtin_amdgcn_rcp(v);
+    return __builtin_fma(__builtin_fma(-v, q, 1.0), q, q);
+}
+__device__ inline double inverse_root(double v) {
+    double q = __builtin_amdgcn_rsq(v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) q = __builtin_fma(__builtin_fma(-v * q, q, 1.0), 0.5 * q, q);
+    return q;
+}
+
+// The codes of the quotients t scale, right to two steps of 64 bits: cut to 21 bits with the last one set where something was cut
+// ("rounded to odd"), a quotient rounds to the code that all of it does, which the conversion instruction does for e4m3,
+// ties to even.
+template <int VEC> __device__ inline void codes_of(const double (&t)[VEC], double scale, int format, uint8_t (&c)[VEC]) {
     float q[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) q[e] = quotient_to_odd(v[e], s, inv);
+    for (int e = 0; e < VEC; ++e) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, t[e] * scale);
+        const uint32_t high = (uint32_t)(u >> 32) | min((uint32_t)u, 1u);
+        q[e] = (float)__builtin_bit_cast(double, (uint64_t)high << 32);
+    }
     if (format == 0) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) c[e] = (uint8_t)code_int8(q[e]);
     } else {
 #pragma unroll
         for (int e = 0; e < VEC; e += 4) {
-            float t[4];
+            float v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) t[i] = fminf(fmaxf(q[e + i], -448.f), 448.f);
-            int w = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
-            w = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w, true);
+            for (int i = 0; i < 4; ++i) v[i] = fminf(fmaxf(q[e + i], -448.f), 448.f);
+            int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+            w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[e + i] = (uint8_t)((uint32_t)w >> 8 * i);
         }
     }
 }
 
-// W waves a row (a workgroup is four rows of one wave, or one row), NP pieces a lane at most.
-template <typename T, int W, int NP> __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rms_norm(RmsArgs a) {
+// W waves a row (a workgroup is four rows of one wave, or one row), NP pieces a lane at most.  CODES: behind s everything is in
+// 64 bits, since a value next to a border of two codes has to fall on its own side: with y and the scale in 32 bits some ten
+// of 2048 x 2560 values took their neighbour's code.  (Such values of bf16 onto bf16 to e4m3, from the caches: 11.9 us, 12.5
+// in 32 bits with a second exchange for the largest |y|; 8192 x 2560 onto fp32 48.4 and 45.8, by the 96 registers.)
+template <typename T, int W, int NP, bool CODES>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rms_norm(RmsArgs a) {
     constexpr int VEC = 16 / (int)sizeof(T), LANES = 64 * W, ROWS = W == 1 ? 4 : 1;
-    __shared__ float lds[4 * W];
+    __shared__ double lds[4 * W];
     const int lane = W == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
     const int D = a.width;
     const bool res32 = a.res_dtype == DT_F32;
     int turn = 0;  // (places for the sums are used in turn: a wave may be a row ahead of another's reads, never two)
     for (int64_t row = (int64_t)blockIdx.x * ROWS + (W == 1 ? (int)(threadIdx.x >> 6) : 0); row < a.rows;
          row += (int64_t)gridDim.x * ROWS, ++turn) {
-        float v[NP][VEC], ss = 0.f;
+        float v[NP][VEC];
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
             const int e0 = (lane + LANES * k) * VEC;
@@ -174,56 +202,77 @@ template <typename T, int W, int NP> __global__ __launch_bounds__(W == 1 ? 256 :
                 if (e0 < D) store_piece_as<T, VEC>(a.sum, row * D + e0, res32, D - e0, v[k]);
             }
         }
+        double* const sums = lds + (turn & 1) * 2 * W;
+        if constexpr (!CODES) {
+            float ss = 0.f;
 #pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            const int e0 = (lane + LANES * k) * VEC;
-            if (e0 < D) {
+            for (int k = 0; k < NP; ++k) {
+                const int e0 = (lane + LANES * k) * VEC;
+                if (e0 < D) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) ss = __builtin_fmaf(v[k][e], v[k][e], ss);
-            }
-        }
-        const float r = __builtin_amdgcn_rsqf(row_sum<W>(ss, lds + (turn & 1) * 2 * W) / (float)D + a.eps);
-        uint32_t mu = 0;
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            const int e0 = (lane + LANES * k) * VEC;
-            if (e0 < D) {
-                float w[VEC];
-                load_piece<float, VEC>(a.w + e0, D - e0, w);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    v[k][e] = v[k][e] * r * w[e];
-                    // (values behind the row's end are 0, or 0 times an infinite r: not looked at)
-                    if (e0 + e < D) mu = max(mu, __builtin_bit_cast(uint32_t, v[k][e]) & 0x7fffffffu);
-                }
-                if (a.format < 0) store_piece<T, VEC>((T*)a.out + row * D + e0, D - e0, v[k]);
-            }
-        }
-        if (a.format < 0) continue;
-        // 8 bits: as integers the magnitudes keep their order, with the infinities and NaN above every number
-        mu = row_max<W>(mu, (uint32_t*)lds + (turn & 1) * 2 * W + W);
-        float s = __builtin_bit_cast(float, mu) / (a.format == 0 ? 127.f : 448.f);
-        const bool none = mu >= 0x7f800000u || s < kMinScale;
-        if (none) s = mu >= 0x7f800000u ? __builtin_nanf("") : 0.f;
-        const float inv = 1.f / s;
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            const int e0 = (lane + LANES * k) * VEC;
-            if (e0 < D) {
-                uint8_t c[VEC];
-                codes_of<VEC>(v[k], s, inv, a.format, c);
-                if (none) __builtin_memset(c, 0, VEC);
-                uint8_t* p = (uint8_t*)a.out + row * D + e0;
-                if (e0 + VEC <= D) {
-                    __builtin_memcpy(p, c, VEC);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (e0 + e < D) p[e] = c[e];
+                    for (int e = 0; e < VEC; ++e) ss = __builtin_fmaf(v[k][e], v[k][e], ss);
                 }
             }
+            const float r = __builtin_amdgcn_rsqf(row_sum<W>(ss, (float*)sums) / (float)D + a.eps);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const int e0 = (lane + LANES * k) * VEC;
+                if (e0 < D) {
+                    float w[VEC];
+                    load_piece<float, VEC>(a.w + e0, D - e0, w);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) v[k][e] = v[k][e] * r * w[e];
+                    store_piece<T, VEC>((T*)a.out + row * D + e0, D - e0, v[k]);
+                }
+            }
+        } else {
+            // y = t r, t = s w (exact in 64 bits), so the largest |y| is r times the largest |t|, and both come by one exchange;
+            // `odd` is NaN where a weight is none or infinite, as is r where a value of the row is
+            double ss = 0, t[NP][VEC], most = 0;
+            float odd = 0.f;
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const int e0 = (lane + LANES * k) * VEC;
+                if (e0 < D) {
+                    float w[VEC];
+                    load_piece<float, VEC>(a.w + e0, D - e0, w);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const double d = v[k][e];
+                        ss = __builtin_fma(d, d, ss);
+                        t[k][e] = d * (double)w[e];
+                        most = __builtin_fmax(most, __builtin_fabs(t[k][e]));
+                        odd = __builtin_fmaf(w[e], 0.f, odd);
+                    }
+                }
+            }
+            if (odd != odd) most = (double)__builtin_inff();
+            row_sum_max<W>(ss, most, sums);
+            const double r = inverse_root(ss / (double)D + (double)a.eps);
+            float s = (float)(most * r * (a.format == 0 ? 1.0 / 127.0 : 1.0 / 448.0));
+            const bool out = !(s < __builtin_inff());  // (an infinity or NaN in the row, or a scale past fp32)
+            const bool none = out || s < kMinScale;
+            if (none) s = out ? __builtin_nanf("") : 0.f;
+            const double c0 = r * inverse((double)s);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const int e0 = (lane + LANES * k) * VEC;
+                if (e0 < D) {
+                    uint8_t c[VEC];
+                    codes_of<VEC>(t[k], c0, a.format, c);
+                    if (none) __builtin_memset(c, 0, VEC);
+                    uint8_t* p = (uint8_t*)a.out + row * D + e0;
+                    if (e0 + VEC <= D) {
+                        __builtin_memcpy(p, c, VEC);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e)
+                            if (e0 + e < D) p[e] = c[e];
+                    }
+                }
+            }
+            if (lane == 0) a.scales[row] = s;
         }
-        if (lane == 0) a.scales[row] = s;
     }
 }
 
@@ -321,19 +370,19 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const float* part, float* dw, 
 }
 
 namespace {
-template <typename T> const void* forward_kernel(int pieces, bool few, int& W) {
+template <typename T, bool CODES> const void* forward_kernel(int pieces, bool few, int& W) {
     if (!few) {
         W = 1;
-        if (pieces <= 64) return (const void*)&k_rms_norm<T, 1, 1>;
-        if (pieces <= 128) return (const void*)&k_rms_norm<T, 1, 2>;
+        if (pieces <= 64) return (const void*)&k_rms_norm<T, 1, 1, CODES>;
+        if (pieces <= 128) return (const void*)&k_rms_norm<T, 1, 2, CODES>;
     }
     W = 4;
-    if (pieces <= 256) return (const void*)&k_rms_norm<T, 4, 1>;
-    if (pieces <= 512) return (const void*)&k_rms_norm<T, 4, 2>;
-    if (pieces <= 1024) return (const void*)&k_rms_norm<T, 4, 4>;
+    if (pieces <= 256) return (const void*)&k_rms_norm<T, 4, 1, CODES>;
+    if (pieces <= 512) return (const void*)&k_rms_norm<T, 4, 2, CODES>;
+    if (pieces <= 1024) return (const void*)&k_rms_norm<T, 4, 4, CODES>;
     W = 16;
-    if (pieces <= 2048) return (const void*)&k_rms_norm<T, 16, 2>;
-    return (const void*)&k_rms_norm<T, 16, 4>;
+    if (pieces <= 2048) return (const void*)&k_rms_norm<T, 16, 2, CODES>;
+    return (const void*)&k_rms_norm<T, 16, 4, CODES>;
 }
 template <typename T> const void* backward_kernel(int pieces, int& W) {
     W = 1;
@@ -376,7 +425,8 @@ hipError_t launch_rms_norm(RmsArgs& a, int in_dtype, hipStream_t st) {
     return by_type(in_dtype, [&](auto* t) {
         typedef __remove_pointer(decltype(t)) T;
         int W;
-        const void* fn = forward_kernel<T>(pieces_of(a.width, in_dtype), a.rows < kFewRows, W);
+        const void* fn = a.format < 0 ? forward_kernel<T, false>(pieces_of(a.width, in_dtype), a.rows < kFewRows, W)
+                                        : forward_kernel<T, true>(pieces_of(a.width, in_dtype), a.rows < kFewRows, W);
         int64_t grid = W == 1 ? (a.rows + 3) / 4 : a.rows;
         if (grid > kNormBlocks) grid = kNormBlocks;
         void* args[] = {&a};

@@ -90,6 +90,27 @@ def test_norm(case):
     assert len(got) == 1 + (fmt is not None) + (res is not None)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("M,D,dtype,res", [(1500, 2560, "bf16", "f32"), (1500, 2560, "f16", "same"), (4000, 1000, "bf16", "same"),
+                                           (2500, 1111, "f32", "f32"), (400, 8191, "f16", None), (300, 12000, "f32", "same")], ids=str)
+def test_norm_codes_next_to_borders(M, D, dtype, res, fmt):
+    """Millions of values, of which some come within fp32's steps of a border of two codes: each takes the code of the 64-bit
+    definition.  The sum with the residual is in fp32; behind it a value is right to the roundings of 64 bits, D of them and
+    10: far below 2^-36.  The scale is right to half a step of fp32, and the quotient is by the scale as returned."""
+    say("codes next to borders", M, D, dtype, res, fmt)
+    g, t, eps = gen(34), DT[dtype], 2.0**-17
+    x, w = rn(g, M, D).to(t), 1 + 0.2 * rn(g, D)
+    r = None if res is None else (3 * rn(g, M, D)).to(t if res == "same" else torch.float32)
+    codes, scales, *_ = ssd.rms_norm(x.cuda(), w.cuda(), cuda(r), eps=eps, format=fmt)
+    torch.cuda.synchronize()
+    _, y = ref.norm(x.float() if r is None else x.float() + r.float(), None, w, eps)
+    want, scales = y.abs().amax(-1) / (127 if fmt == "int8" else 448), scales.cpu().double()
+    assert ((scales - want).abs() <= (ref.U + 2.0**-36) * want).all()
+    q = y / scales[..., None]
+    off = (codes.float().cpu().double() - q).abs() - ref.code_step(q, fmt) / 2
+    assert (off <= 2.0**-36 * q.abs()).all(), "%d codes" % int((off > 2.0**-36 * q.abs()).sum())
+
+
 @pytest.mark.parametrize("case", NORM, ids=str)
 def test_norm_backward(case):
     say("norm backward", case)
@@ -150,6 +171,19 @@ def test_norm_rows_keep_to_themselves(fmt):
     else:
         assert torch.equal(got[0].float()[rows], clean[0].float()[rows]) and torch.equal(got[1][rows], clean[1][rows])
         assert got[1][[1, 3]].isnan().all() and got[1][5] == 0 and (got[0].float()[[1, 3, 5]] == 0).all()
+
+
+@pytest.mark.parametrize("D", [300, 1000, 2560, 12001])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_norm_codes_of_weights_that_are_no_numbers(fmt, bad, D):
+    """Such a weight is in every row, also against a value of 0; a zero row's scale is 0 without one."""
+    x, w = rn(gen(7), 5, D).cuda(), torch.ones(D, device="cuda")
+    x[2], x[3, D - 1] = 0, 0
+    assert ssd.rms_norm(x, w, format=fmt)[1].isfinite().all()
+    w[D - 1] = bad
+    codes, scales = ssd.rms_norm(x, w, format=fmt)
+    assert scales.isnan().all() and (codes.float() == 0).all()
 
 
 def test_norm_backward_padding_bits():
