@@ -510,7 +510,14 @@ template <int TYPE> hipError_t launch_linear_type(LinearArgs& a, LinearArgs* b, 
     case kNarrowTiles + 5: e = launch_tile<TYPE, 64, 128, 1, 4, 3, 4>(a, b, st); break;
     case kNarrowTiles + 6: e = launch_tile<TYPE, 32, 64, 1, 4, 6, 4>(a, b, st); break;
     case kNarrowTiles + 7: e = launch_tile<TYPE, 16, 64, 1, 4, 7, 4>(a, b, st); break;
-    default: e = launch_tile<TYPE, 128, 128, 4, 2, TYPE == LT_E4M3 ? 2 : 4>(a, b, st); break;
+    case 8:
+        // (fp32 has none: its tiles go by their area, by which 128 x 128 with two workgroups a CU is never behind)
+        if constexpr (TYPE != LT_F32) {
+            e = launch_tile<TYPE, 128, 128, 4, 2, TYPE == LT_E4M3 ? 2 : 4>(a, b, st);
+            break;
+        }
+        [[fallthrough]];
+    default: return hipErrorNotSupported;
     }
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t lanes = (int64_t)a.M * ((a.N + 3) / 4);

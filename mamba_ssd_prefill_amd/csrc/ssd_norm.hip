@@ -381,8 +381,9 @@ template <typename T, bool CODES> const void* forward_kernel(int pieces, bool fe
     if (pieces <= 512) return (const void*)&k_rms_norm<T, 4, 2, CODES>;
     if (pieces <= 1024) return (const void*)&k_rms_norm<T, 4, 4, CODES>;
     W = 16;
-    if (pieces <= 2048) return (const void*)&k_rms_norm<T, 16, 2, CODES>;
-    return (const void*)&k_rms_norm<T, 16, 4, CODES>;
+    if constexpr (sizeof(T) == 4)  // (16384 values are 2048 pieces of 16 bits)
+        if (pieces > 2048) return (const void*)&k_rms_norm<T, 16, 4, CODES>;
+    return (const void*)&k_rms_norm<T, 16, 2, CODES>;
 }
 template <typename T> const void* backward_kernel(int pieces, int& W) {
     W = 1;
@@ -393,8 +394,9 @@ template <typename T> const void* backward_kernel(int pieces, int& W) {
     if (pieces <= 512) return (const void*)&k_rms_norm_backward<T, 4, 2>;
     if (pieces <= 1024) return (const void*)&k_rms_norm_backward<T, 4, 4>;
     W = 16;
-    if (pieces <= 2048) return (const void*)&k_rms_norm_backward<T, 16, 2>;
-    return (const void*)&k_rms_norm_backward<T, 16, 4>;
+    if constexpr (sizeof(T) == 4)  // (16384 values are 2048 pieces of 16 bits)
+        if (pieces > 2048) return (const void*)&k_rms_norm_backward<T, 16, 4>;
+    return (const void*)&k_rms_norm_backward<T, 16, 2>;
 }
 int pieces_of(int width, int in_dtype) {
     const int vec = in_dtype == DT_F32 ? 4 : 8;
