@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "ssd_linear_plan.h"
+
 namespace ssd {
 
 // ---- residual norm ----------------------------------------------------------------------------
@@ -35,8 +37,6 @@ hipError_t launch_rms_norm(RmsArgs& a, int in_dtype, hipStream_t st);
 hipError_t launch_rms_norm_backward(RmsArgs& a, int in_dtype, float* dw, hipStream_t st);
 
 // ---- matrix product ---------------------------------------------------------------------------
-// Operands of the product: rows with the contraction's values one behind the other.
-enum : int { LT_F32 = 0, LT_F16 = 1, LT_BF16 = 2, LT_I8 = 3, LT_E4M3 = 4 };
 struct LinearArgs {
     const void* x;  // [M] rows of kbytes, xs bytes apart
     const void* w;  // [N] rows of kbytes, ws bytes apart
@@ -51,20 +51,6 @@ struct LinearArgs {
     int M, N, kbytes, act, out_dtype;
     int splits, steps_per_split;
 };
-struct LinearPlan {
-    int tile;    // index of the tile shape
-    int splits;  // of the contraction
-    float us;    // by the model that chose them
-    bool narrow; // loads of 4 bytes a lane: rows of a multiple of 4 bytes
-};
-// copied: the bytes of rows that 16-byte loads do not take as they are, to be copied first (plan not narrow) or loaded by 4
-// bytes; may_narrow: whether these can be
-LinearPlan linear_plan(int64_t M, int64_t N, int64_t kbytes, int type, int64_t copied = 0, bool may_narrow = false);
-struct LinearSize {
-    int64_t M, N, kbytes;
-    LinearPlan plan;
-};
-LinearPlan linear_plan_two(const LinearSize& a, const LinearSize& b, int type);
 // b: a second product in the same launch (by linear_plan_two), or NULL
 hipError_t launch_linear(LinearArgs& a, LinearArgs* b, int type, const LinearPlan& p, hipStream_t st);
 

@@ -135,14 +135,7 @@ SSD_EXPORT ssd_status_t ssd_rms_norm_backward(const ssd_norm_params_t* p, const 
 
 namespace {
 
-constexpr int64_t kMaxRowBytes = (int64_t)1 << 22;  // of an operand: 256 rows of a tile have 31-bit offsets
 constexpr int kMaxInt8Width = 131071;               // 128 * 128 * K stays below 2^31
-
-// K values as rows of 16-byte pieces.
-int64_t padded(int64_t k, size_t es) {
-    const int64_t per = 16 / (int64_t)es;
-    return (k + per - 1) / per * per;
-}
 
 ssd_status_t validate_linear(const ssd_linear_params_t* p, bool backward) {
     if (!p) return SSD_ERR_NULL_POINTER;
@@ -154,15 +147,15 @@ ssd_status_t validate_linear(const ssd_linear_params_t* p, bool backward) {
     if (!stride_ok(p->x_stride, p->width) || !stride_ok(p->residual_stride, p->outs)) return SSD_ERR_INVALID_SHAPE;
     const size_t es = elem_size(p->in_dtype);
     const int64_t M = p->rows, K = p->width, N = p->outs;
-    if (padded(K, es) * (int64_t)es >= kMaxRowBytes) return SSD_ERR_INVALID_SHAPE;
+    if (ssd::padded(K, es) * (int64_t)es >= ssd::kMaxRowBytes) return SSD_ERR_INVALID_SHAPE;
     if (p->in_dtype == SSD_IN_INT8 && K > kMaxInt8Width) return SSD_ERR_UNSUPPORTED;
     // lanes of the product (512 for 256 x 256 outputs) and of the operands' copies (one for 16 bytes of either, in one launch); of
     // the gradient behind the activation with the transposed copies (256 for 64 x 64 of any)
     const int64_t most = kMaxLanes / 256, mb = (M + 63) / 64, nb = (N + 63) / 64, kb = (K + 63) / 64 + 1;
     if (mb * nb >= most || mb * kb >= most || nb * kb >= most || (mb + nb) * kb >= most) return SSD_ERR_INVALID_SHAPE;
-    if ((M + N) * (padded(K, es) * (int64_t)es / 16) >= kMaxLanes - 256) return SSD_ERR_INVALID_SHAPE;
+    if ((M + N) * (ssd::padded(K, es) * (int64_t)es / 16) >= kMaxLanes - 256) return SSD_ERR_INVALID_SHAPE;
     if (backward && mb * nb + (mb + nb) * kb >= most) return SSD_ERR_INVALID_SHAPE;
-    if (backward && (padded(N, es) * (int64_t)es >= kMaxRowBytes || padded(M, es) * (int64_t)es >= kMaxRowBytes))
+    if (backward && (ssd::padded(N, es) * (int64_t)es >= ssd::kMaxRowBytes || ssd::padded(M, es) * (int64_t)es >= ssd::kMaxRowBytes))
         return SSD_ERR_INVALID_SHAPE;
     return SSD_OK;
 }
@@ -170,30 +163,14 @@ ssd_status_t validate_linear(const ssd_linear_params_t* p, bool backward) {
 // Where weight has to start so that rows cut out of one that starts on 16 bytes are taken: loaded as they are, or copied.
 size_t weight_align(int64_t row_bytes, size_t es) { return row_bytes % 16 == 0 ? 16 : row_bytes % 4 == 0 ? 4 : es; }
 
-bool rows_fit(int64_t stride, size_t es, size_t piece) {
-    return stride * es % piece == 0 && stride * (int64_t)es < kMaxRowBytes;
-}
-
 // The workspace of a product: copies of the operands where their rows do not fit, and the sums of the splits.
-struct LinearLayout {
-    ssd::LinearPlan plan;
-    bool pack_x, pack_w, may_pack_x;
-    int64_t kp;
+struct LinearLayout : ssd::LinearForm {
     size_t x_off, w_off, part_off, total;
 };
 
 LinearLayout linear_layout(const ssd_linear_params_t* p) {
-    LinearLayout l{};
     const size_t es = elem_size(p->in_dtype);
-    const int64_t K = p->width;
-    const int64_t xs = p->x_stride ? p->x_stride : K;
-    l.kp = padded(K, es);
-    l.pack_w = l.kp != K;
-    l.pack_x = l.kp != K || !rows_fit(xs, es, 16);
-    l.may_pack_x = l.pack_x || p->x_stride;  // a view's rows, also of one row, may start anywhere
-    const int64_t copied = ((l.pack_x ? p->rows : 0) + (l.pack_w ? (int64_t)p->outs : 0)) * K * (int64_t)es;
-    l.plan = ssd::linear_plan(p->rows, p->outs, l.kp * es, p->in_dtype, copied, rows_fit(K, es, 4) && rows_fit(xs, es, 4));
-    if (l.plan.narrow) l.pack_w = l.pack_x = false;
+    LinearLayout l{ssd::linear_form(p->rows, p->width, p->outs, p->x_stride, p->in_dtype, es)};
     Regions r;
     l.x_off = l.may_pack_x ? r.add((size_t)p->rows * l.kp * es) : 0;
     l.w_off = l.pack_w ? r.add((size_t)p->outs * l.kp * es) : 0;
@@ -271,24 +248,16 @@ SSD_EXPORT ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, 
 namespace {
 
 // The backward's workspace.
-struct LinearBackLayout {
-    ssd::LinearPlan dx_plan, dw_plan, both_plan;  // (both: splits 0 where they are launched one by one)
+struct LinearBackLayout : ssd::LinearBackForm {
     bool rows;  // dpre as rows of its own (else dout serves)
-    int64_t mp, np;
     size_t rows_off, cols_off, wt_off, xt_off, part_off, bias_off, total;
 };
 
 LinearBackLayout linear_back_layout(const ssd_linear_params_t* p) {
-    LinearBackLayout l{};
     const size_t es = elem_size(p->in_dtype);
     const size_t M = p->rows, K = p->width, N = p->outs;
-    l.mp = padded(M, es);
-    l.np = padded(N, es);
-    l.rows = p->act || l.np != (int64_t)N;
-    l.dx_plan = ssd::linear_plan(M, K, l.np * es, p->in_dtype);
-    l.dw_plan = ssd::linear_plan(N, K, l.mp * es, p->in_dtype);
-    const int64_t m = M, k = K, n = N, eb = es;
-    l.both_plan = ssd::linear_plan_two({m, k, l.np * eb, l.dx_plan}, {n, k, l.mp * eb, l.dw_plan}, p->in_dtype);
+    LinearBackLayout l{ssd::linear_back_form(p->rows, p->width, p->outs, p->in_dtype, es)};
+    l.rows = p->act || l.np != p->outs;
     Regions r;
     l.rows_off = l.rows ? r.add(M * l.np * es) : 0;
     l.cols_off = r.add(N * l.mp * es);
