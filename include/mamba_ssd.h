@@ -646,7 +646,10 @@ ssd_status_t ssd_rms_norm_backward(const ssd_norm_params_t* p, const void* dout,
 /* ---- matrix product ---------------------------------------------------------------------
  *     pre[m,n] = (sum_k x[m,k] * weight[n,k]) * x_scale[m] * weight_scale[n] + bias[n]
  *     out[m,n] = act(pre[m,n]) + residual[m,n],   act: identity, v sigmoid(v), or v (1 + erf(v / sqrt 2)) / 2
- * Sums in fp32 (int8: exactly, in 32-bit integers, up to K = 131071), everything behind them in fp32 too, rounded once. */
+ * Sums in fp32 (int8: exactly, in 32-bit integers, up to K = 131071), everything behind them in fp32 too, rounded once.  e4m3 with
+ * out_dtype fp16 or bf16 is multiplied by the matrix instruction for codes, which cuts each of eight products that it adds at a
+ * time to 13 bits below the largest one's leading bit (some 1.5e-5 of the result for operands of like size, below those types' half
+ * steps); with out_dtype fp32 its sums are fp32 ones. */
 typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GELU = 2 } ssd_act_t;
 typedef enum { SSD_IN_INT8 = 3, SSD_IN_E4M3 = 4 } ssd_code_dtype_t; /* operands in 8 bits, besides ssd_dtype_t */
 

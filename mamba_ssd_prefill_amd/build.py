@@ -22,7 +22,7 @@ SOURCES = (["ssd_api.cpp", "ssd_noalloc.hip", "ssd_common.hip", "ssd_decode.hip"
             "ssd_recur.hip", "ssd_kernels_f32.hip", "ssd_kernels_f32_vl.hip",
             "ssd_kernels_f16.hip", "ssd_kernels_bf16.hip", "ssd_kernels_f16_blk.hip", "ssd_kernels_bf16_blk.hip"]
            + ["ssd_recur_%s.hip" % d for d in ("f32", "f16", "bf16")]
-           + ["ssd_linear_%s.hip" % d for d in ("f32", "f16", "bf16", "i8", "e4m3")]
+           + ["ssd_linear_%s.hip" % d for d in ("f32", "f16", "bf16", "i8", "e4m3", "e4m3_f32")]
            + ["ssd_kernels_%s_q%d%s.hip" % (d, q, v) for d in ("f16", "bf16") for q in (64, 128, 256)
               for v in ("", "_vl")])
 

@@ -11,6 +11,7 @@ hipError_t launch_linear_f16(LinearArgs&, LinearArgs*, const LinearPlan&, hipStr
 hipError_t launch_linear_bf16(LinearArgs&, LinearArgs*, const LinearPlan&, hipStream_t);
 hipError_t launch_linear_i8(LinearArgs&, LinearArgs*, const LinearPlan&, hipStream_t);
 hipError_t launch_linear_e4m3(LinearArgs&, LinearArgs*, const LinearPlan&, hipStream_t);
+hipError_t launch_linear_e4m3_f32(LinearArgs&, LinearArgs*, const LinearPlan&, hipStream_t);
 
 hipError_t launch_linear(LinearArgs& a, LinearArgs* b, int type, const LinearPlan& p, hipStream_t st) {
     for (LinearArgs* l : {&a, b}) {
@@ -24,7 +25,7 @@ hipError_t launch_linear(LinearArgs& a, LinearArgs* b, int type, const LinearPla
     case LT_F16: return launch_linear_f16(a, b, p, st);
     case LT_BF16: return launch_linear_bf16(a, b, p, st);
     case LT_I8: return launch_linear_i8(a, b, p, st);
-    case LT_E4M3: return launch_linear_e4m3(a, b, p, st);
+    case LT_E4M3: return a.out_dtype == DT_F32 ? launch_linear_e4m3_f32(a, b, p, st) : launch_linear_e4m3(a, b, p, st);
     default: return hipErrorNotSupported;
     }
 }

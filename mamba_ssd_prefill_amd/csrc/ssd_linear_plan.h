@@ -10,7 +10,8 @@
 namespace ssd {
 
 // Operands of the product: rows with the contraction's values one behind the other.
-enum : int { LT_F32 = 0, LT_F16 = 1, LT_BF16 = 2, LT_I8 = 3, LT_E4M3 = 4 };
+// LT_E4M3_F32: e4m3 for outputs in fp32 (a kernel's type; everywhere else LT_E4M3).
+enum : int { LT_F32 = 0, LT_F16 = 1, LT_BF16 = 2, LT_I8 = 3, LT_E4M3 = 4, LT_E4M3_F32 = 5 };
 struct LinearPlan {
     int tile;    // index of the tile shape
     int splits;  // of the contraction

@@ -414,6 +414,32 @@ def test_linear_of_codes(case):
     check_product(got, pre, K, S, case, r, exact_sums=fmt == "int8")
 
 
+@pytest.mark.parametrize("M,K,N", [(64, 8, 64), (64, 32, 64), (16, 64, 64), (5, 129, 70), (300, 2560, 1000), (2048, 256, 10576)])
+def test_e4m3_sums_in_fp32(M, K, N):
+    """Outputs in fp32 are within two roundings a product, also where there are few and of unlike size."""
+    g = torch.Generator(device="cuda").manual_seed(48)
+    x, w = ((100 * torch.randn(*s, generator=g, device="cuda")).clamp(-448, 448).to(torch.float8_e4m3fn) for s in ((M, K), (N, K)))
+    got = ssd.linear(x, w, out_dtype=torch.float32).double()
+    a, b = x.float().double(), w.float().double()
+    want, S = a @ b.t(), a.abs() @ b.t().abs()
+    assert ((got - want).abs() <= (2 * K + 20) * ref.U * S).all()
+
+
+def test_e4m3_products_of_unlike_size():
+    """Codes times one beside 2^16, in each of 16 places: sums of 24 bits, exact in fp32."""
+    values = torch.arange(256, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).float()
+    values = values[values.isfinite() & (values.abs() >= 2.0**-4)]  # multiples of 2^-7: 2^16 and that have 24 bits
+    one = torch.zeros(len(values), 40, device="cuda")
+    one[:, 3] = 256
+    for k in range(16):
+        x = one.clone()
+        x[:, 4 + k] = values
+        w = torch.zeros(1, 40, device="cuda")
+        w[0, 3], w[0, 4 + k] = 256, 1
+        got = ssd.linear(x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn), out_dtype=torch.float32)[:, 0]
+        assert torch.equal(got.double(), 65536 + values.double()), k
+
+
 def test_int8_sums_are_exact():
     """The widest contraction of the largest codes: 2^31 less 2^14."""
     K = 131071
