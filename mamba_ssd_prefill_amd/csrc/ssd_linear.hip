@@ -104,6 +104,10 @@ hipError_t launch_pack(PackArgs& a, PackArgs& b, int elem_bytes, hipStream_t st)
 // contraction's values one behind the other, with its column sums, from the values before they are rounded; and the
 // transposed weight and input.  HBM-bound: dout and pre of 4096 x 4096 f16, a weight and an input of
 // 4096 x 1024, 168 MB, 31.6 us, 5.3 TB/s (in two launches 29.4 and 7.8).
+// dpre is rounded to the operands' type for the products, which take no wider one (fp16: values below 2^-14 lose bits, as
+// those of dout have).  Of 4096 x 1024 x 4096 normal values in fp16 the gradients are 2.9e-4 off in the 2-norm, 2.1e-4 of it by
+// their own rounding; in two parts, the rounded value and the rest, they would be 2.1e-4 off, and the products, of
+// twice the contraction, take 140 us instead of 76 (one by one).  Without an activation dpre is dout, and nothing is rounded.
 template <typename T> struct Dpre {
     static constexpr int V = Square<T>::V;
     Square<T> sq;

@@ -51,3 +51,28 @@ def test_recurrence_token_by_token(case, slow):
 def test_recurrence_across_many_tiles(dtype, gated):
     """70 tiles forward and 140 backward, states that last: those passed between tiles decide the outputs behind them."""
     check((1, 8900, 40, dtype, "f32", None, True, gated, True, True, False), True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,extra,shift", [(66, 1, 1), (64, 3, 0), (66, 2, 1), (65, 1, 1)])
+def test_recurrence_rows_that_start_anywhere(D, extra, shift, dtype):
+    """Rows on their elements' alignment alone: the bits of aligned ones, forward, backward and for one token."""
+    say("rows that start anywhere", D, extra, shift, dtype)
+    B, L, g = 2, 200, torch.Generator().manual_seed(92)
+    whole = [rn(g, B, L, D).to(DT[dtype]).cuda() for _ in range(3)]
+
+    def moved(t):
+        flat = torch.full((t[..., 0].numel() * (D + extra) + 8,), float("nan"), dtype=t.dtype, device="cuda")
+        lead = t.shape[:-1]
+        rows = flat[shift:shift + t[..., 0].numel() * (D + extra)].view(*lead, D + extra)[..., :D]
+        rows.copy_(t)
+        return rows
+    A, dout = -torch.exp(rn(g, D) - 2).cuda(), rn(g, B, L, D).to(DT[dtype]).cuda()
+    results = []
+    for x, gate, ig in (whole, [moved(t) for t in whole]):
+        out, fin, saved = ssd.gated_recurrence(x, gate, A, ig, save_for_backward=True)
+        grads = ssd.gated_recurrence_backward(dout, x, gate, A, ig, saved=saved)
+        pool = fin.clone()
+        one = ssd.gated_recurrence_step(x[:, 3], gate[:, 3], A, ig[:, 3], state=pool)
+        results.append([out, fin, one, pool] + [v for v in grads if v is not None])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
