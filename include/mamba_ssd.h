@@ -600,7 +600,7 @@ ssd_status_t ssd_state_cache_read(const ssd_cache_params_t* p, const void* codes
 
 /* ---- residual norm ----------------------------------------------------------------------
  * For every row:  s = x + residual (or x),  r = 1 / sqrt(mean(s^2) + eps),  y = s * r * w,
- * in fp32 (squares of a row have to stay in its range: |s| below 1.8e19 / sqrt(D)); sum is s
+ * in fp32 (squares of a row have to stay in its range: |s| below 1.8e19 / sqrt(D); those below 1.4e-45 are 0); sum is s
  * rounded to sum_dtype, and y is that of s before this rounding.
  * In 8 bits (format): the row has one scale, y becomes codes as in the state cache above:
  *     scale = max|y| / 127 (int8) or / 448 (e4m3),  code = y / scale rounded to the nearest code, ties to even

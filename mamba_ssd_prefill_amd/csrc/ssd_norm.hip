@@ -101,6 +101,12 @@ template <int W> __device__ inline void row_sums(float& v, float& u, float* lds)
         }
     }
 }
+// 1 / sqrt(v).  (The instruction takes a subnormal v for 0: rows of tiny values, or of zeros, with a subnormal eps.)
+__device__ inline float inverse_root(float v) {
+    const bool tiny = v < 0x1p-100f;
+    return __builtin_amdgcn_rsqf(tiny ? v * 0x1p60f : v) * (tiny ? 0x1p30f : 1.f);
+}
+
 // In 64 bits: the sum of v, and the largest of u (neither negative).
 template <int W> __device__ inline void row_sum_max(double& v, double& u, double* lds) {
 #pragma unroll
@@ -213,7 +219,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rms_norm(RmsArgs a) {
                     for (int e = 0; e < VEC; ++e) ss = __builtin_fmaf(v[k][e], v[k][e], ss);
                 }
             }
-            const float r = __builtin_amdgcn_rsqf(row_sum<W>(ss, (float*)sums) / (float)D + a.eps);
+            const float r = inverse_root(row_sum<W>(ss, (float*)sums) / (float)D + a.eps);
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
                 const int e0 = (lane + LANES * k) * VEC;
@@ -318,7 +324,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rms_norm_backward(Rms
         // (two places for the sums, used in turn: a wave may be a row ahead of another's reads, never two)
         row_sums<W>(ss, gs, lds + (turn & 1) * 2 * W);
         ++turn;
-        const float r = __builtin_amdgcn_rsqf(ss / (float)D + a.eps);
+        const float r = inverse_root(ss / (float)D + a.eps);
         const float c = gs / (float)D * r * r;  // ds = r (g - s c) + dsum
 #pragma unroll
         for (int k = 0; k < NP; ++k) {

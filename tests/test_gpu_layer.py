@@ -146,6 +146,25 @@ def test_norm_of_more_rows_than_workgroups():
     ref.close(got.dweight, dw, Sw, 70 + M, torch.float32, "dweight")
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-39, 2.0**-130])
+@pytest.mark.parametrize("D", [64, 1500])
+def test_norm_of_subnormal_squares(D, eps):
+    """Rows of 2^-66 and the like (their squares are exact), and of zeros where eps alone stands under the root."""
+    g = gen(6)
+    sign = torch.where(rn(g, 4, D) > 0, 1.0, -1.0)
+    x, w, dout = sign * 2.0 ** torch.tensor([[-66.0], [-62.0], [-70.0], [-64.0]]), rn(g, D), rn(g, 4, D)
+    if eps:
+        x[3] = 0
+    eps = float(torch.tensor(eps))
+    y = ssd.rms_norm(x.cuda(), w.cuda(), eps=eps)
+    _, want = ref.norm(x, None, w, eps)
+    ref.close(y, want, want.abs(), 60, torch.float32, "norm")
+    got = ssd.rms_norm_backward(dout.cuda(), x.cuda(), w.cuda(), eps=eps)
+    (ds, dw), (Sd, Sw) = (ref.norm_grads(dout, x, w, None, eps, absolute=k) for k in (False, True))
+    ref.close(got.dx, ds, Sd, 200, torch.float32, "dx")
+    ref.close(got.dweight, dw, Sw, 74, torch.float32, "dweight")
+
+
 def test_norm_in_place_and_given_outputs():
     g = gen(5)
     x, r, w = rn(g, 2, 9, 300).bfloat16().cuda(), rn(g, 2, 9, 300).cuda(), rn(g, 300).cuda()
