@@ -728,7 +728,8 @@ typedef struct {
  *   final_state   [S, D]     state_dtype  NULL: not wanted; overlaps initial_state nowhere
  *   saved                    fp32         NULL, or ssd_gated_recurrence_saved_size() bytes: states kept for the backward
  *                                         pass, one every 64 tokens
- *   workspace                             256-byte aligned, ssd_gated_recurrence_workspace_size() bytes */
+ *   workspace                             256-byte aligned, ssd_gated_recurrence_workspace_size() bytes (a second call at
+ *                                         work on it at the same time can make states NaN in both) */
 size_t ssd_gated_recurrence_workspace_size(const ssd_recurrence_params_t* p);
 size_t ssd_gated_recurrence_saved_size(const ssd_recurrence_params_t* p);
 ssd_status_t ssd_gated_recurrence(const ssd_recurrence_params_t* p, const void* x, const void* gate, const float* A,

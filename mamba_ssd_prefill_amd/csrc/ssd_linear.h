@@ -14,9 +14,10 @@
 // rows that a read takes at one c fall on 16 different places of a line (no bank conflicts by the counter).
 //
 // Large products are bound by the matrix instructions and how well they are fed, smaller ones by their number of workgroups
-// and a step's latency, single rows by the weights' bytes.  Measured, bf16: 8192 x 8192 x 8192 869 us, 1.27 PFLOP/s (a
-// library's product 1.41); 4096 x 4096 x 1024 36 us (library 40), 4096 x 1024 x 4096 34 us (35); one row of 2560 x
-// 10576, 54 MB of weights, 10 us.  e4m3: 8192 x 8192 x 8192 444 us, 2.48 PFLOP/s (library 2.97); 2048 x 2560 x 10576 61 us (75).
+// and a step's latency, single rows by the weights' bytes.  Measured, bf16: 8192 x 8192 x 8192 865 us, 1.27 PFLOP/s (a
+// library's product 1.42); 4096 x 4096 x 1024 36 us (library 40), 4096 x 1024 x 4096 34 us (35); one row of 2560 x
+// 10576, 54 MB of weights, 10 us.  e4m3 to bf16: 8192 x 8192 x 8192 426 to 444 us, 2.5 PFLOP/s (library 2.8 to 3.0);
+// 2048 x 2560 x 10576 61 to 67 us (74).  int8: 69 us there, 8192 x 5120 x 2560 115 us.
 // fp32: 2048 x 2048 x 2048 132 us, 130 TFLOP/s (library, at 4096^3, 136).
 #pragma once
 

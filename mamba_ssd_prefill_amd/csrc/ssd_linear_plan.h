@@ -25,7 +25,9 @@ struct LinearSize {
 
 // The tile and the splits of the contraction by a model of the time, fitted to sweeps over 1 to 8192 rows at 2560 x
 // 10576, 5120 x 2560, 1024 x 4096, 4096 x 1024 and 8192 x 8192 (bf16: of 19 such products it takes the fastest pair of the
-// sweep or one within 11 %, but for 64 x 2560 x 10576, 24 us against 19):
+// sweep or one within 11 %, but for 64 x 2560 x 10576, 24 us against 19; the other types have the same constants: of ten products
+// of 1 to 8192 rows fp16, int8 and e4m3 take the fastest or one within 9 %, but for these 64 rows in fp16, fp32 one within
+// 15 %, but for 128 x 2560 x 10576 and 512 x 5120 x 2560, 93 and 155 us against 74 and 123):
 //   2.5 us + rounds (steps c + e),  and 4 us + 8 bytes a partial sum at 4 TB/s where the contraction is split,
 // c being the time of a step with 1, 2, .. workgroups a CU and e that of a tile's start and epilogue.  8192 x 5120 x 2560
 // takes 206 us in tiles of 256 x 160 (two full rounds of 256 CUs), 271 us in 256 x 256 and 248 us in 128 x 128; 16 x
@@ -33,7 +35,7 @@ struct LinearSize {
 // goes by the area, down to what a step's latency takes.
 // Rows that are no multiple of 16 bytes are copied to ones that are (3 us and their bytes twice at 4 TB/s), or, of a multiple
 // of 4 bytes and in the three smaller tiles, loaded by 4 bytes a lane, whose steps take 1.35 times as long: one row of 2562
-// x 10576 bf16 15.5 us against 35.6 copied, 16 rows 18.7 and 36.4, 128 rows 37 and 47; but fp32 1500 x 1110 x 2000 88 and 77.
+// x 10576 bf16 14.2 us against 35.6 copied, 16 rows 18.7 and 36.4, 128 rows 37 and 47; but fp32 1500 x 1110 x 2000 88 and 77.
 struct TileModel {
     uint32_t bm, bn;
     int most;  // workgroups a CU
