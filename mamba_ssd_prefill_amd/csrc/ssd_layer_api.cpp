@@ -155,7 +155,7 @@ ssd_status_t validate_linear(const ssd_linear_params_t* p, bool backward) {
     if (mb * nb >= most || mb * kb >= most || nb * kb >= most || (mb + nb) * kb >= most) return SSD_ERR_INVALID_SHAPE;
     if ((M + N) * (ssd::padded(K, es) * (int64_t)es / 16) >= kMaxLanes - 256) return SSD_ERR_INVALID_SHAPE;
     if (backward && mb * nb + (mb + nb) * kb >= most) return SSD_ERR_INVALID_SHAPE;
-    if (backward && (ssd::padded(N, es) * (int64_t)es >= ssd::kMaxRowBytes || ssd::padded(M, es) * (int64_t)es >= ssd::kMaxRowBytes))
+    if (backward && ssd::padded(M > N ? M : N, es) * (int64_t)es >= ssd::kMaxRowBytes)
         return SSD_ERR_INVALID_SHAPE;
     return SSD_OK;
 }
@@ -195,9 +195,9 @@ SSD_EXPORT ssd_status_t ssd_linear(const ssd_linear_params_t* p, const void* x, 
     if ((x_scale || weight_scale) && p->in_dtype < SSD_IN_INT8) return SSD_ERR_INVALID_ARGUMENT;
     const size_t es = elem_size(p->in_dtype), os = elem_size(p->out_dtype);
     LinearLayout l = linear_layout(p);
-    if (!aligned(x, l.may_pack_x ? es : 16) || !aligned(weight, weight_align(p->width * (int64_t)es, es)) || !aligned(bias, 4) || !aligned(residual, os) ||
-        !aligned(x_scale, 4) || !aligned(weight_scale, 4) || !aligned(pre, os) || !aligned(out, os) ||
-        !aligned(workspace, kAlign))
+    if (!aligned(x, l.may_pack_x ? es : 16) || !aligned(weight, weight_align(p->width * (int64_t)es, es)) ||
+        !aligned(bias, 4) || !aligned(residual, os) || !aligned(x_scale, 4) || !aligned(weight_scale, 4) ||
+        !aligned(pre, os) || !aligned(out, os) || !aligned(workspace, kAlign))
         return SSD_ERR_MISALIGNED;
     // in place, each value is read by the lane that writes it; anywhere else another lane may still read
     const int64_t rs = p->residual_stride ? p->residual_stride : p->outs;

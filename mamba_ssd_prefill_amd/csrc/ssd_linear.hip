@@ -1,4 +1,5 @@
-// ssd_linear.hip -- what stands around the matrix product: rows that it cannot take as they are copied into ones that it can, and dout act'(pre) for its gradients (ssd_linear / _backward in include/mamba_ssd.h).
+// ssd_linear.hip -- what stands around the matrix product: rows that it cannot take as they are copied into ones that it can,
+// and dout act'(pre) for its gradients (ssd_linear / _backward in include/mamba_ssd.h).
 #include <math.h>
 
 #include "ssd_linear.h"

@@ -230,7 +230,8 @@ def linear(x, weight, bias=None, residual=None, *, activation=None, x_scale=None
            save_pre=False, out=None, workspace=None):
     """ssd_linear: act(x weight^T + bias) + residual, x [..., K], weight [N, K], bias [N] float32, residual [..., N];
     ``activation`` None, "silu" or "gelu".  x and weight are float32, float16 or bfloat16, or 8-bit codes (torch.int8,
-    torch.float8_e4m3fn) with ``x_scale`` [...] and ``weight_scale`` [N] float32 (None: 1).  Returns out [..., N] in
+    torch.float8_e4m3fn) with ``x_scale`` [...] and ``weight_scale`` [N] float32 (None: 1); e4m3 has sums of full fp32
+    precision where ``out_dtype`` is float32.  Returns out [..., N] in
     ``out_dtype`` (default: out's, the residual's, or x's), and with ``save_pre`` (out, pre) for linear_backward.  ``out`` may
     be the (contiguous) residual itself."""
     meta, (px, pw, pb, pr, psx, psw, _) = _s._meta(x, weight, bias, residual, x_scale, weight_scale, out)

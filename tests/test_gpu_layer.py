@@ -92,7 +92,8 @@ def test_norm(case):
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("M,D,dtype,res", [(1500, 2560, "bf16", "f32"), (1500, 2560, "f16", "same"), (4000, 1000, "bf16", "same"),
-                                           (2500, 1111, "f32", "f32"), (400, 8191, "f16", None), (300, 12000, "f32", "same")], ids=str)
+                                           (2500, 1111, "f32", "f32"), (400, 8191, "f16", None),
+                                           (300, 12000, "f32", "same")], ids=str)
 def test_norm_codes_next_to_borders(M, D, dtype, res, fmt):
     """Millions of values, of which some come within fp32's steps of a border of two codes: each takes the code of the 64-bit
     definition.  The sum with the residual is in fp32; behind it a value is right to the roundings of 64 bits, D of them and

@@ -26,7 +26,8 @@ def close(got, want, scale, roundings, name):
     bad = ~((got.double() - want).abs() <= tol)
     if bad.any():
         at = bad.nonzero()
-        raise AssertionError("%s: %d of %d values off, from %s to %s" % (name, len(at), bad.numel(), at[0].tolist(), at[-1].tolist()))
+        raise AssertionError("%s: %d of %d values off, from %s to %s"
+                             % (name, len(at), bad.numel(), at[0].tolist(), at[-1].tolist()))
 
 
 def wide(t):
